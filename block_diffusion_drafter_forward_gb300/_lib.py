@@ -27,6 +27,7 @@ DFLASH_DEV_BAD_CTX = 0x2
 DFLASH_DEV_BAD_TOKEN = 0x4
 DFLASH_DEV_TIMEOUT = 0x8
 DFLASH_DEV_BAD_WIDTH = 0x10
+DFLASH_DEV_NO_ROOM = 0x20
 
 STATUS_NAMES = {0: "OK", -1: "EINVAL", -2: "ENOMEM", -3: "ECUDA", -4: "ECAPACITY", -5: "EUNSUPPORTED",
                 -6: "EDEVICE"}
@@ -67,11 +68,18 @@ class dflash_weights(ctypes.Structure):
                 ("markov_w1", ctypes.c_void_p), ("markov_w2", ctypes.c_void_p)]
 
 
+class dflash_kv_pages(ctypes.Structure):
+    _fields_ = [("pool", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("status", ctypes.c_void_p),
+                ("dtype", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32)]
+
+
 EXPORTS = ("dflash_create", "dflash_destroy", "dflash_write_ctx_kv", "dflash_propose", "dflash_kv_layout",
            "dflash_device_status", "dflash_last_error", "dflash_fp8_lm_head", "dflash_profile",
            "dflash_profile_kinds", "dflash_profile_read", "dflash_gemm_bf16",
            "dflash_attention_check", "dflash_gemm_bf16_noalloc", "dflash_set_persistent", "dflash_persistent",
-           "dflash_propose_ex", "dflash_write_ctx_kv_batch", "dflash_fp8_layer")
+           "dflash_propose_ex", "dflash_write_ctx_kv_batch", "dflash_fp8_layer", "dflash_extend_tables",
+           "dflash_append_kv", "dflash_attend", "dflash_attend_workspace", "dflash_sample")
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -122,6 +130,18 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dflash_set_persistent.restype = c.c_int
     lib.dflash_persistent.argtypes = [vp]
     lib.dflash_persistent.restype = c.c_int
+    i64, kv = c.c_int64, c.POINTER(dflash_kv_pages)
+    lib.dflash_extend_tables.argtypes = [vp, vp, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp]
+    lib.dflash_extend_tables.restype = c.c_int
+    lib.dflash_append_kv.argtypes = [kv, vp, i64, vp, i64, vp, i32, vp]
+    lib.dflash_append_kv.restype = c.c_int
+    lib.dflash_attend.argtypes = [kv, vp, i64, vp, i32, vp, vp, i32, i32, i32, i32, c.c_float, i32, i32, vp, i64, vp, vp,
+                                  i64, vp]
+    lib.dflash_attend.restype = c.c_int
+    lib.dflash_attend_workspace.argtypes = [kv]
+    lib.dflash_attend_workspace.restype = i64
+    lib.dflash_sample.argtypes = [vp, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.dflash_sample.restype = c.c_int
     lib.dflash_last_error.argtypes = [vp]
     lib.dflash_last_error.restype = c.c_char_p
     _lib = lib
@@ -266,3 +286,47 @@ def dflash_gemm_bf16_noalloc(W: int, N: int, K: int, X: int, M: int, out: int, n
                                          nsplit, ctypes.c_void_p(stream))
     if rc != DFLASH_OK:
         raise DflashError(rc, "dflash_gemm_bf16_noalloc failed")
+
+
+# The serving operators take no handle: their message is the thread's (dflash_last_error(NULL)).
+# Addresses go as plain ints, 0 for NULL.
+def dflash_extend_tables(ctx_lens: int, new_rows: int, nb: int, page_tables: int, max_pages_per_seq: int, free_pages: int,
+                         n_free: int, free_begin: int, free_end: int, kv_lens: int, row_starts: int, row_seq: int,
+                         row_index: int, slots: int, max_rows: int, status: int = 0, stream: int = 0) -> None:
+    rc = load().dflash_extend_tables(ctx_lens, new_rows, nb, page_tables, max_pages_per_seq, free_pages, n_free, free_begin,
+                                     free_end, kv_lens, row_starts, row_seq, row_index, slots, max_rows, status, stream)
+    if rc:
+        _check(rc, None)
+
+
+def dflash_append_kv(kv: dflash_kv_pages, k: int, k_stride: int, v: int, v_stride: int, slots: int, n: int,
+                     stream: int = 0) -> None:
+    rc = load().dflash_append_kv(ctypes.byref(kv), k, k_stride, v, v_stride, slots, n, stream)
+    if rc:
+        _check(rc, None)
+
+
+def dflash_attend_workspace(kv: dflash_kv_pages) -> int:
+    n = load().dflash_attend_workspace(ctypes.byref(kv))
+    if n < 0:
+        _check(int(n), None)
+    return n
+
+
+def dflash_attend(kv: dflash_kv_pages, q: int, q_stride: int, page_tables: int, max_pages_per_seq: int, kv_lens: int,
+                  row_starts: int, nb: int, n_rows: int, max_new: int, n_q_heads: int, scale: float, window: int,
+                  causal: int, out: int, out_stride: int, lse: int, workspace: int, workspace_bytes: int,
+                  stream: int = 0) -> None:
+    rc = load().dflash_attend(ctypes.byref(kv), q, q_stride, page_tables, max_pages_per_seq, kv_lens, row_starts, nb,
+                              n_rows, max_new, n_q_heads, scale, window, causal, out, out_stride, lse, workspace,
+                              workspace_bytes, stream)
+    if rc:
+        _check(rc, None)
+
+
+def dflash_sample(logits: int, row_stride: int, dtype: int, rows: int, vocab: int, u: int, temperature: int, top_k: int,
+                  top_p: int, min_p: int, tokens: int, probs: int, stream: int = 0) -> None:
+    rc = load().dflash_sample(logits, row_stride, dtype, rows, vocab, u, temperature, top_k, top_p, min_p, tokens, probs,
+                              stream)
+    if rc:
+        _check(rc, None)

@@ -15,6 +15,7 @@
 #include "gemm_tc.cuh"
 #include "markov.cuh"
 #include "persist_tc.cuh"
+#include "serve.cuh"
 
 using namespace dflash;
 
@@ -484,6 +485,15 @@ static bool persist_every_cta_has_work(int64_t H, int64_t F, int64_t nh, int64_t
   for (const auto& sh : shapes)
     if (((sh[0] + 127) / 128) * (sh[1] / 64) < (int64_t)G) return false;
   return true;
+}
+
+int dflash::call_error(int code, const char* msg, cudaError_t e) noexcept {
+  try {
+    g_create_error = msg;
+    if (e != cudaSuccess) g_create_error.append(": ").append(cudaGetErrorString(e));
+  } catch (...) {  // out of host memory: the status alone
+  }
+  return code;
 }
 
 extern "C" {

@@ -1,0 +1,156 @@
+// Attention of a chunk of new tokens per sequence over its paged K/V rows (dflash_attend).
+#include <float.h>
+
+#include "launch_util.cuh"
+#include "serve.cuh"
+
+namespace dflash {
+namespace {
+
+struct AttendParams {
+  const void* q;
+  void* out;
+  float* lse;
+  const void* pool;
+  const int32_t *page_tables, *kv_lens, *row_starts;
+  uint32_t* status;
+  int64_t q_stride, out_stride, page_stride;  // elements
+  int nb, n_rows, mpps, num_pages, nh, nkv, window, causal;
+  float scale_log2;  // scale * log2(e): scores are exponents of 2
+};
+
+// Sequence s: its rows [*r0, *r0 + *n), key rows *kv.  false: no rows, or out of range (*bad).
+__device__ __forceinline__ bool seq_of(const AttendParams& p, int s, int* r0, int* n, int* kv, bool* bad) {
+  const int a = __ldg(p.row_starts + s), b = __ldg(p.row_starts + s + 1), k = __ldg(p.kv_lens + s);
+  *bad = a < 0 || b < a || b > p.n_rows || k < 0 || (long long)k > (long long)p.mpps * kPage;
+  *r0 = a;
+  *n = b - a;
+  *kv = k;
+  return !*bad && b > a;
+}
+
+__device__ __forceinline__ int page_id(const AttendParams& p, int s, int lp) {
+  const int page = __ldg(p.page_tables + (int64_t)s * p.mpps + lp);
+  if (page >= 0 && page < p.num_pages) return page;
+  if (p.status) atomicOr(p.status, DFLASH_DEV_BAD_PAGE);
+  return 0;
+}
+
+// CUDA-core form: one warp per (row, query head), online softmax over pages of 16 keys.  Lane l
+// takes key l % 16 and one half of the dims of q . k, and dims l, l + 32, ... of the output.
+template <typename T, int HD>
+__global__ void __launch_bounds__(128) attend_simple_kernel(const AttendParams p) {
+  __shared__ float s_q[4][HD];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t x = (int64_t)blockIdx.x * 4 + warp;
+  const int i = (int)(x / p.nh), h = (int)(x % p.nh), g = h / (p.nh / p.nkv);
+  if (i >= p.n_rows) return;
+  int lo = 0, hi = p.nb;  // the last sequence that starts at or before row i
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(p.row_starts + mid) <= i) lo = mid; else hi = mid;
+  }
+  const int s = lo;
+  int r0, n, kv;
+  bool bad;
+  const bool rows = seq_of(p, s, &r0, &n, &kv, &bad);
+  if (bad && p.status && lane == 0) atomicOr(p.status, DFLASH_DEV_BAD_CTX);
+  if (!rows || i < r0 || i >= r0 + n) return;
+  const T* q = static_cast<const T*>(p.q) + i * p.q_stride + h * HD;
+#pragma unroll
+  for (int e = 0; e < HD / 32; ++e) s_q[warp][lane + 32 * e] = Elem<T>::to_f(q[lane + 32 * e]) * p.scale_log2;
+  __syncwarp();
+  const int pos = kv - n + (i - r0);
+  const int k_end = p.causal ? min(kv, pos + 1) : kv;
+  const int k_begin = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+  float m = -INFINITY, l = 0.f, acc[HD / 32];
+#pragma unroll
+  for (int e = 0; e < HD / 32; ++e) acc[e] = 0.f;
+  const int half = lane >> 4, j = lane & 15;
+  for (int lp = k_begin / kPage; lp * kPage < k_end; ++lp) {
+    const T* tile = static_cast<const T*>(p.pool) + page_id(p, s, lp) * p.page_stride + (int64_t)g * 2 * kPage * HD;
+    float sc = 0.f;
+#pragma unroll
+    for (int c = 0; c < HD / 16; ++c) {
+      const int d8 = half * (HD / 16) + c;
+      const T* k = tile + k_in_tile(j, d8 * 8, HD);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sc = fmaf(s_q[warp][d8 * 8 + e], Elem<T>::to_f(k[e]), sc);
+    }
+    sc += __shfl_xor_sync(0xffffffffu, sc, 16);
+    const int key = lp * kPage + j;
+    const bool see = key >= k_begin && key < k_end;
+    sc = see ? sc : -INFINITY;
+    float mx = sc;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float m_new = fmaxf(m, mx);
+    const float base = m_new == -INFINITY ? 0.f : m_new;
+    const float alpha = exp2f(m - base), pr = see ? exp2f(sc - base) : 0.f;
+    float sum = pr;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    l = l * alpha + sum;
+    m = m_new;
+#pragma unroll
+    for (int e = 0; e < HD / 32; ++e) acc[e] *= alpha;
+    const T* v = tile + kPage * HD;
+    for (int jj = max(0, k_begin - lp * kPage); jj < min(kPage, k_end - lp * kPage); ++jj) {  // seen keys only
+      const float w = __shfl_sync(0xffffffffu, pr, jj);
+#pragma unroll
+      for (int e = 0; e < HD / 32; ++e) acc[e] = fmaf(w, Elem<T>::to_f(v[v_in_tile(jj, lane + 32 * e, HD)]), acc[e]);
+    }
+  }
+  T* out = static_cast<T*>(p.out) + i * p.out_stride + h * HD;
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+#pragma unroll
+  for (int e = 0; e < HD / 32; ++e) out[lane + 32 * e] = Elem<T>::from_f(acc[e] * inv);
+  if (p.lse && lane == 0) p.lse[(int64_t)i * p.nh + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+}  // namespace
+}  // namespace dflash
+
+using namespace dflash;
+
+extern "C" int64_t dflash_attend_workspace(const dflash_kv_pages* kv) {
+  if (int rc = check_pages(kv)) return rc;
+  return 0;
+}
+
+extern "C" int dflash_attend(const dflash_kv_pages* kv, const void* q, int64_t q_stride, const int32_t* page_tables,
+                             int32_t max_pages_per_seq, const int32_t* kv_lens, const int32_t* row_starts, int32_t nb,
+                             int32_t n_rows, int32_t max_new, int32_t n_q_heads, float scale, int32_t window,
+                             int32_t causal, void* out, int64_t out_stride, float* lse, void* workspace,
+                             int64_t workspace_bytes, dflash_stream stream) {
+  if (int rc = check_pages(kv)) return rc;
+  if (nb < 1 || n_rows < 0 || max_new < 0) return call_error(DFLASH_EINVAL, "attend: nb >= 1, n_rows >= 0 and max_new >= 0");
+  if (max_pages_per_seq < 1 || max_pages_per_seq >= 1 << 27)
+    return call_error(DFLASH_EINVAL, "attend: max_pages_per_seq must be in [1, 2^27)");
+  if (n_q_heads < 1 || n_q_heads % kv->n_kv_heads || n_q_heads / kv->n_kv_heads > 128)
+    return call_error(DFLASH_EINVAL, "attend: n_q_heads must be a multiple of n_kv_heads, at most 128 times it");
+  if (window < 0) return call_error(DFLASH_EINVAL, "attend: window must be >= 0");
+  if (!(scale > 0.f) || !(scale <= FLT_MAX)) return call_error(DFLASH_EINVAL, "attend: scale must be positive and finite");
+  if (n_rows == 0) return DFLASH_OK;
+  if (!q || !out || !page_tables || !kv_lens || !row_starts) return call_error(DFLASH_EINVAL, "attend: null pointer");
+  const int64_t need = dflash_attend_workspace(kv);
+  if (need < 0) return (int)need;
+  if (workspace_bytes < need || (need > 0 && (!workspace || !aligned16(workspace))))
+    return call_error(DFLASH_EINVAL, "attend: workspace below dflash_attend_workspace() bytes, or not 16-byte aligned");
+  const int es = kv->dtype == DFLASH_F32 ? 4 : 2;
+  const int64_t row = (int64_t)n_q_heads * kv->head_dim;
+  if (q_stride < row || out_stride < row || (q_stride * es) % 16 || (out_stride * es) % 16 || !aligned16(q) || !aligned16(out))
+    return call_error(DFLASH_EINVAL, "attend: rows below n_q_heads * head_dim, or q, out or a stride not whole 16 bytes");
+  AttendParams p{q, out, lse, kv->pool, page_tables, kv_lens, row_starts, kv->status, q_stride, out_stride, kv->page_stride,
+                 nb, n_rows, max_pages_per_seq, kv->num_pages, n_q_heads, kv->n_kv_heads, window, causal != 0,
+                 scale * 1.4426950408889634f};
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t blocks = ((int64_t)n_rows * n_q_heads + 3) / 4;
+  if (blocks > 0x7fffffff) return call_error(DFLASH_ECAPACITY, "attend: too many rows for one call");
+  const bool f32 = kv->dtype == DFLASH_F32, w = kv->head_dim == 128;
+  auto kern = f32 ? (w ? attend_simple_kernel<float, 128> : attend_simple_kernel<float, 64>)
+                  : (w ? attend_simple_kernel<__nv_bfloat16, 128> : attend_simple_kernel<__nv_bfloat16, 64>);
+  kern<<<(unsigned)blocks, 128, 0, st>>>(p);
+  if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return call_error(DFLASH_ECUDA, "attend", e);
+  return DFLASH_OK;
+}

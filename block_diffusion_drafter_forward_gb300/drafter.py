@@ -197,5 +197,23 @@ class Drafter:
     def kv_layout(self) -> Tuple[int, int, Tuple[int, ...]]:
         return L.dflash_kv_layout(self.handle)
 
+    def kv_pages(self, layer: int) -> "PagedKV":
+        """One layer of the drafter's own pool as a PagedKV: a view, which keeps the drafter alive."""
+        from .serve import PagedKV
+        if not 0 <= layer < self.cfg.n_layers:
+            raise ValueError(f"layer: expected one of {self.cfg.n_layers}, got {layer}")
+        ptr, nbytes, st = self.kv_layout()
+
+        class _View:  # the library owns the memory, the tensor keeps the view and so the handle
+            owner = self
+            __cuda_array_interface__ = {"shape": (nbytes // st[5],), "typestr": "<f4" if st[5] == 4 else "<u2",
+                                        "data": (ptr, False), "version": 3}
+
+        pool = torch.as_tensor(_View(), device=self.tensors["norm"].device)
+        if st[5] == 2:
+            pool = pool.view(torch.bfloat16)
+        nkv, pages = self.cfg.n_kv_heads, self.ccfg.num_pages
+        return PagedKV(pool[layer * st[0]:layer * st[0] + pages * st[1]].view(pages, nkv, 2, st[4]))
+
     def device_status(self, stream=None) -> int:
         return L.dflash_device_status(self.handle, _stream(stream))

@@ -1,0 +1,262 @@
+"""Serving operators around the drafter, over torch device tensors: page tables and row maps built
+on the device (`extend_tables`), K/V rows appended to a paged cache and attended over (`PagedKV`),
+and tokens drawn from logits (`sample`).  Thin calls of dflash_extend_tables, dflash_append_kv,
+dflash_attend and dflash_sample: include/dflash.h states what each computes and refuses.
+
+Every call is asynchronous on `stream` (default: the current stream of the tensors' device), copies
+nothing to the host and keeps nothing for the next call.  Outputs and workspaces that a call
+allocates itself belong to that stream.  The kernels report bad page ids, lengths and full pools in
+one status word per device, read and cleared by `serve_status`."""
+from __future__ import annotations
+
+import ctypes
+import math
+import threading
+from typing import Dict, NamedTuple, Optional, Tuple
+
+import torch
+
+from . import _lib as L
+
+_I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
+_status: Dict[int, torch.Tensor] = {}  # device index -> its status word
+_status_lock = threading.Lock()
+
+
+class RowPlan(NamedTuple):
+    """What `extend_tables` returns: rows of a step and where they go (int32 device tensors)."""
+    kv_lens: torch.Tensor     # [nb] rows of each sequence, the new ones included
+    row_starts: torch.Tensor  # [nb + 1] first new row of each sequence in the step; the last: total
+    row_seq: torch.Tensor     # [max_rows] sequence of each new row, -1 past the total
+    row_index: torch.Tensor   # [max_rows] its row (and position) in the sequence, -1 past the total
+    slots: torch.Tensor       # [max_rows] its slot in the cache, -1 past the total
+    free_end: torch.Tensor    # [1] position in the stack of free pages after this step
+
+
+def _status_word(device: torch.device) -> torch.Tensor:
+    w = _status.get(device.index)
+    if w is None:
+        with _status_lock:
+            w = _status.get(device.index)
+            if w is None:
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("the first serving call of a device (or serve_status()) must come before a capture")
+                w = torch.zeros(1, dtype=_I32, device=device)
+                torch.cuda.current_stream(device).synchronize()  # zeroed for every stream
+                _status[device.index] = w
+    return w
+
+
+def serve_status(device=None, stream: Optional[torch.cuda.Stream] = None) -> int:
+    """Synchronise `stream` (default: the current one), read the device's DFLASH_DEV_* bits of the
+    serving calls since the last read, and clear them."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    with torch.cuda.stream(stream or torch.cuda.current_stream(device)):
+        w = _status_word(device)
+        bits = int(w.item())
+        if bits:
+            w.bitwise_and_(~bits)  # those read, no others
+            torch.cuda.current_stream(device).synchronize()
+    return bits
+
+
+def _want(t, name: str, dtype: torch.dtype, shape: Tuple[int, ...], device: torch.device) -> int:
+    """The address of a contiguous `dtype` tensor of exactly `shape` on `device`; raises otherwise."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        if t.device != device:
+            raise ValueError(f"{name}: expected a tensor on {device}, got one on {t.device}")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _first(t, name: str, dim: int, dtypes=(_I32,)) -> torch.Tensor:
+    """The tensor whose device and sizes the others of a call are held to."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name}: expected a cuda tensor, got one on {t.device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.dim() != dim:
+        raise ValueError(f"{name}: expected {dim} dimensions, got {t.dim()}")
+    return t
+
+
+def _rows_of(t, name: str, dtype: torch.dtype, shape: Tuple[int, ...], device: torch.device) -> Tuple[int, int]:
+    """(address, elements between rows) of a [rows, heads, dim] tensor whose heads are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}, got one on {t.device}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    st = t.stride()
+    row = shape[1] * shape[2]
+    if t.numel() and ((shape[2] > 1 and st[2] != 1) or (shape[1] > 1 and st[1] != shape[2]) or (shape[0] > 1 and st[0] < row)):
+        raise ValueError(f"{name}: the heads of a row must be contiguous and rows must not overlap, got strides {st}")
+    return t.data_ptr(), (st[0] if shape[0] > 1 else row)
+
+
+class _On:
+    """The call's device made current, and the raw stream to launch on."""
+    __slots__ = ("device", "stream", "ctx")
+
+    def __init__(self, device: torch.device, stream: Optional[torch.cuda.Stream]):
+        self.device, self.stream, self.ctx = device, stream, None
+
+    def __enter__(self) -> int:
+        if self.stream is not None:
+            if self.stream.device != self.device:
+                raise ValueError(f"stream: expected a stream of {self.device}, got one of {self.stream.device}")
+            self.ctx = torch.cuda.stream(self.stream)  # also makes its device current
+            self.ctx.__enter__()
+            return self.stream.cuda_stream
+        if torch.cuda.current_device() != self.device.index:
+            self.ctx = torch.cuda.device(self.device)
+            self.ctx.__enter__()
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def __exit__(self, *a) -> None:
+        if self.ctx is not None:
+            self.ctx.__exit__(*a)
+
+
+def extend_tables(ctx_lens: torch.Tensor, new_rows: torch.Tensor, page_tables: torch.Tensor, free_pages: torch.Tensor,
+                  free_begin: torch.Tensor, max_rows: int, out: Optional[RowPlan] = None, stream=None) -> RowPlan:
+    """Pages for the new rows of a batch and every new row's place.  ctx_lens, new_rows [nb];
+    page_tables [nb, max_pages_per_seq], extended in place; free_pages [n] a stack of page ids taken
+    from position free_begin [1] on.  Sequences are served in order while pages and max_rows last.
+    `out`: a RowPlan to write into; its kv_lens may be ctx_lens and its free_end free_begin."""
+    dev = _first(ctx_lens, "ctx_lens", 1).device
+    nb = ctx_lens.shape[0]
+    a_ctx = _want(ctx_lens, "ctx_lens", _I32, (nb,), dev)
+    a_new = _want(new_rows, "new_rows", _I32, (nb,), dev)
+    mpps = _first(page_tables, "page_tables", 2).shape[1]
+    a_pt = _want(page_tables, "page_tables", _I32, (nb, mpps), dev)
+    n_free = _first(free_pages, "free_pages", 1).shape[0]
+    a_free = _want(free_pages, "free_pages", _I32, (n_free,), dev)
+    a_begin = _want(free_begin, "free_begin", _I32, (1,), dev)
+    max_rows = int(max_rows)
+    if max_rows < 0:
+        raise ValueError("max_rows must be >= 0")
+    with _On(dev, stream) as st:
+        if out is None:
+            def e(n):
+                return torch.empty(n, dtype=_I32, device=dev)
+            out = RowPlan(e(nb), e(nb + 1), e(max_rows), e(max_rows), e(max_rows), e(1))
+        rows = (max_rows,)
+        L.dflash_extend_tables(
+            a_ctx, a_new, nb, a_pt, mpps, a_free or a_pt, n_free, a_begin, _want(out.free_end, "out.free_end", _I32, (1,), dev),
+            _want(out.kv_lens, "out.kv_lens", _I32, (nb,), dev), _want(out.row_starts, "out.row_starts", _I32, (nb + 1,), dev),
+            _want(out.row_seq, "out.row_seq", _I32, rows, dev) or a_pt, _want(out.row_index, "out.row_index", _I32, rows, dev) or a_pt,
+            _want(out.slots, "out.slots", _I32, rows, dev) or a_pt, max_rows, _status_word(dev).data_ptr(), st)
+    return out
+
+
+class PagedKV:
+    """K/V pages of one layer: a tensor [pages, kv_heads, 2, 16 * head_dim] (bfloat16 or float32,
+    contiguous but for the stride between pages), whose last dimension is a tile in the layout of
+    dflash_kv_layout.  One layer of a larger tensor, or of a drafter's own pool
+    (`Drafter.kv_pages`), is a view of it."""
+
+    def __init__(self, pool: torch.Tensor):
+        _first(pool, "pool", 4, (_BF16, _F32))
+        P, nkv, two, tile = pool.shape
+        if two != 2 or tile not in (1024, 2048):
+            raise ValueError(f"pool: expected shape [pages, kv_heads, 2, 16 * 64 or 16 * 128], got {tuple(pool.shape)}")
+        st = pool.stride()
+        if st[3] != 1 or st[2] != tile or (nkv > 1 and st[1] != 2 * tile):
+            raise ValueError("pool: heads and tiles of a page must be contiguous")
+        self.pool = pool
+        self.head_dim = tile // 16
+        self._stride = st[0] if P > 1 else 2 * nkv * tile
+        k = L.dflash_kv_pages()
+        k.pool, k.page_stride = pool.data_ptr(), self._stride
+        k.status = _status_word(pool.device).data_ptr()
+        k.dtype = L.DFLASH_BF16 if pool.dtype is _BF16 else L.DFLASH_F32
+        k.n_kv_heads, k.head_dim, k.num_pages = nkv, self.head_dim, P
+        self._c = k
+
+    @classmethod
+    def empty(cls, num_pages: int, n_kv_heads: int, head_dim: int, dtype: torch.dtype = _BF16, device="cuda") -> "PagedKV":
+        """A cache of its own (pages uninitialised: rows are defined once appended)."""
+        return cls(torch.empty((num_pages, n_kv_heads, 2, 16 * head_dim), dtype=dtype, device=device))
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> torch.Tensor:
+        """Rows k, v [n, kv_heads, head_dim] (any stride between rows) into slots [n] (negative: skipped)
+        of the pages.  Returns the pages' tensor."""
+        pool = self.pool
+        dev = pool.device
+        n = _first(slots, "slots", 1).shape[0]
+        a_s = _want(slots, "slots", _I32, (n,), dev)
+        shape = (n, pool.shape[1], self.head_dim)
+        a_k, ks = _rows_of(k, "k", pool.dtype, shape, dev)
+        a_v, vs = _rows_of(v, "v", pool.dtype, shape, dev)
+        with _On(dev, stream) as st:
+            L.dflash_append_kv(self._c, a_k, ks, a_v, vs, a_s, n, st)
+        return pool
+
+    def attend(self, q: torch.Tensor, page_tables: torch.Tensor, kv_lens: torch.Tensor, row_starts: torch.Tensor,
+               max_new: int, causal: bool = True, window: int = 0, scale: Optional[float] = None,
+               out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, stream=None):
+        """Attention of each sequence's newest rows over its pages.  q [rows, heads, head_dim]; rows
+        row_starts[s] .. row_starts[s + 1] - 1 are the last rows of sequence s, which has kv_lens[s].
+        max_new: the longest chunk, or an upper bound (it picks the kernel).  scale: 1 / sqrt(head_dim)
+        by default.  Returns out [rows, heads, head_dim] (a new one is zeroed, so that rows behind the
+        last sequence hold zeros), or (out, lse) when `lse` [rows, heads] float32 is given."""
+        pool = self.pool
+        dev = pool.device
+        hd = self.head_dim
+        n, nh = _first(q, "q", 3, (pool.dtype,)).shape[:2]
+        shape = (n, nh, hd)
+        a_q, qs = _rows_of(q, "q", pool.dtype, shape, dev)
+        nb, mpps = _first(page_tables, "page_tables", 2).shape
+        a_pt = _want(page_tables, "page_tables", _I32, (nb, mpps), dev)
+        a_kv = _want(kv_lens, "kv_lens", _I32, (nb,), dev)
+        a_rs = _want(row_starts, "row_starts", _I32, (nb + 1,), dev)
+        a_lse = 0 if lse is None else _want(lse, "lse", _F32, (n, nh), dev)
+        with _On(dev, stream) as st:
+            if out is None:
+                out = torch.zeros(shape, dtype=pool.dtype, device=dev)
+            a_out, os_ = _rows_of(out, "out", pool.dtype, shape, dev)
+            need = L.dflash_attend_workspace(self._c)
+            ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+            L.dflash_attend(self._c, a_q, qs, a_pt, mpps, a_kv, a_rs, nb, n, int(max_new), nh,
+                            1.0 / math.sqrt(hd) if scale is None else float(scale), int(window), 1 if causal else 0,
+                            a_out, os_, a_lse, ws.data_ptr() if need else 0, need, st)
+        return out if lse is None else (out, lse)
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Tensor] = None,
+           top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+           min_p: Optional[torch.Tensor] = None, tokens: Optional[torch.Tensor] = None,
+           probs: Optional[torch.Tensor] = None, stream=None):
+    """One token per row of logits [rows, vocab] (bfloat16 or float32, any stride between rows) from
+    uniform numbers u [rows] float32.  temperature, top_p, min_p float32 and top_k int32 [rows], each
+    optional.  Returns tokens [rows] int32, or (tokens, probs) when `probs` [rows] float32 is given."""
+    dev = _first(logits, "logits", 2, (_BF16, _F32)).device
+    rows, V = logits.shape
+    st0, st1 = logits.stride()
+    if (V > 1 and st1 != 1) or (rows > 1 and st0 < V):
+        raise ValueError(f"logits: a row must be contiguous and rows must not overlap, got strides {(st0, st1)}")
+    a_u = _want(u, "u", _F32, (rows,), dev)
+    opt = [0 if t is None else _want(t, name, dt, (rows,), dev)
+           for t, name, dt in ((temperature, "temperature", _F32), (top_k, "top_k", _I32), (top_p, "top_p", _F32),
+                               (min_p, "min_p", _F32), (probs, "probs", _F32))]
+    with _On(dev, stream) as st:
+        if tokens is None:
+            tokens = torch.empty(rows, dtype=_I32, device=dev)
+        a_t = _want(tokens, "tokens", _I32, (rows,), dev)
+        L.dflash_sample(logits.data_ptr(), st0 if rows > 1 else V, L.DFLASH_BF16 if logits.dtype is _BF16 else L.DFLASH_F32,
+                        rows, V, a_u, opt[0], opt[1], opt[2], opt[3], a_t, opt[4], st)
+    return tokens if probs is None else (tokens, probs)

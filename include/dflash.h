@@ -65,6 +65,7 @@ typedef enum {
 #define DFLASH_DEV_BAD_TOKEN 0x4u   /* a bonus token outside [0, vocab) (row embedded as zeros) */
 #define DFLASH_DEV_TIMEOUT 0x8u     /* a kernel's bounded wait gave up (its outputs are invalid) */
 #define DFLASH_DEV_BAD_WIDTH 0x10u  /* dflash_propose_ex: a block width outside [2, gamma] (clamped) */
+#define DFLASH_DEV_NO_ROOM 0x20u    /* dflash_extend_tables: free pages or row slots ran out */
 
 /* Drafter configuration.  Names follow the drafter config.json of the pages
  * (hidden_size, num_attention_heads, num_key_value_heads, head_dim, intermediate_size,
@@ -313,6 +314,110 @@ int dflash_attention_check(dflash_handle* h, int32_t layer, const int32_t* ctx_l
                            const int32_t* page_tables, int32_t nb, int32_t max_ctx_len,
                            void* out_cuda_core, void* out_tensor_core, dflash_stream stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Serving operators: what a step of the target model over a paged K/V cache needs beside the
+ * drafter.  They take no handle: the caller owns every buffer.  All are asynchronous on
+ * `stream` (with the buffers' device current), allocate nothing, keep nothing between calls and
+ * may be captured into CUDA graphs.  On an error status nothing was launched and
+ * dflash_last_error(NULL) gives the message on this thread.  `status` pointers are one uint32
+ * word on the device or NULL; the kernels OR DFLASH_DEV_* bits into it and never clear it.
+ * ------------------------------------------------------------------------------------- */
+
+/* Pages of one layer's K/V cache: the tile layout of dflash_kv_layout with a head's V tile
+ * directly after its K tile, i.e. element offset page * page_stride + head * 32 * head_dim
+ * (+ 16 * head_dim for V) + the offset inside a tile given there.  A layer of a drafter's own
+ * pool is one such (pool + layer * strides[0], page_stride = strides[1]). */
+typedef struct {
+  void* pool;            /* device base of page 0, 16-byte aligned */
+  int64_t page_stride;   /* elements between pages: >= 32 * n_kv_heads * head_dim, whole 16 bytes */
+  uint32_t* status;      /* device status word or NULL */
+  int32_t dtype;         /* DFLASH_BF16 or DFLASH_F32 */
+  int32_t n_kv_heads;    /* 1..1024 */
+  int32_t head_dim;      /* 64 or 128 */
+  int32_t num_pages;
+} dflash_kv_pages;
+
+/* Gives the new rows of a batch their pages and maps every row to its place, on the device.
+ * Sequence s holds ctx_lens[s] rows and gets new_rows[s] more.  It needs
+ * ceil((ctx + new) / 16) - ceil(ctx / 16) pages, taken in order of s from
+ * free_pages[*free_begin ...] (a stack of n_free page ids) and entered in its row of
+ * page_tables [nb, max_pages_per_seq] (entries of pages it holds already, and those past its new
+ * end, are left as they are).  Outputs:
+ *   kv_lens    [nb]     ctx_lens[s] + rows granted (may be ctx_lens itself)
+ *   row_starts [nb+1]   first row of each sequence in the step's rows; row_starts[nb] = total
+ *   row_seq, row_index, slots [max_rows]  of row i: its sequence, its row index in the sequence
+ *                       (and RoPE position) and its slot page * 16 + row_index % 16; -1, -1, -1
+ *                       for rows from the total on.  row_seq and row_index are what
+ *                       dflash_write_ctx_kv_batch takes, slots what dflash_append_kv takes.
+ *   free_end   [1]      *free_begin + pages taken (may be free_begin itself)
+ * Sequences are served in order: from the first whose pages or rows do not fit in n_free or
+ * max_rows on, none gets rows (DFLASH_DEV_NO_ROOM).  A sequence with a negative length or more
+ * than 16 * max_pages_per_seq rows gets none (DFLASH_DEV_BAD_CTX), the others are served.
+ * 1 <= nb <= 16384 (ECAPACITY).  No other outputs may overlap inputs or each other. */
+int dflash_extend_tables(const int32_t* ctx_lens, const int32_t* new_rows, int32_t nb, int32_t* page_tables,
+                         int32_t max_pages_per_seq, const int32_t* free_pages, int32_t n_free,
+                         const int32_t* free_begin, int32_t* free_end, int32_t* kv_lens, int32_t* row_starts,
+                         int32_t* row_seq, int32_t* row_index, int32_t* slots, int32_t max_rows, uint32_t* status,
+                         dflash_stream stream);
+
+/* Copies K and V rows into the pages: row i of k and v [n, n_kv_heads, head_dim] (pages' dtype,
+ * heads contiguous, `k_stride` / `v_stride` elements between rows) goes to slot slots[i].
+ * Negative slots are skipped; a slot >= 16 * num_pages is skipped and sets DFLASH_DEV_BAD_PAGE.
+ * Two rows aimed at the same slot race: every element ends as one of the two rows'.  k, v and the
+ * strides are whole 16 bytes (EINVAL).  n == 0 is a no-op. */
+int dflash_append_kv(const dflash_kv_pages* kv, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                     const int32_t* slots, int32_t n, dflash_stream stream);
+
+/* Attention of each sequence's new rows over its paged rows.  Rows row_starts[s] ..
+ * row_starts[s+1]-1 of q [n_rows, n_q_heads, head_dim] belong to sequence s and are its last rows:
+ * with n of them, row i sits at position p = kv_lens[s] - n + i.  Query head h reads kv head
+ * h / (n_q_heads / n_kv_heads).  Key j < kv_lens[s] is seen iff (j <= p or not causal) and
+ * (p - j < window or window == 0):
+ *   out = sum_j softmax_j(scale q . k_j) v_j,   lse = ln sum_j exp(scale q . k_j)   (fp32)
+ * A row that sees no key gets out = 0 and lse = -inf.  Rows of q and out are `q_stride` and
+ * `out_stride` elements apart (heads contiguous, whole 16 bytes); lse [n_rows, n_q_heads] or NULL.
+ * Rows of out and lse outside every sequence's range are left as they are.  row_starts never
+ * falls and stays in [0, n_rows], kv_lens in [0, 16 * max_pages_per_seq]: a sequence that breaks
+ * this is skipped (its rows are left as they are) and sets DFLASH_DEV_BAD_CTX.  A page id outside
+ * [0, num_pages) is read as page 0 and sets DFLASH_DEV_BAD_PAGE.  Page rows from kv_lens on are
+ * not used, whatever they hold; a key that is masked for some rows only (by the causal mask or
+ * the window) must hold finite values.  max_new is a host hint of the longest chunk (it picks the kernel,
+ * any value gives the same results up to summation order).  n_q_heads is a multiple of
+ * n_kv_heads, at most 128 times it.  `workspace` of dflash_attend_workspace() bytes (16-byte
+ * aligned) is scratch of this call: calls that may overlap on the GPU, replayed graphs among
+ * them, need one each. */
+int dflash_attend(const dflash_kv_pages* kv, const void* q, int64_t q_stride, const int32_t* page_tables,
+                  int32_t max_pages_per_seq, const int32_t* kv_lens, const int32_t* row_starts, int32_t nb,
+                  int32_t n_rows, int32_t max_new, int32_t n_q_heads, float scale, int32_t window, int32_t causal,
+                  void* out, int64_t out_stride, float* lse, void* workspace, int64_t workspace_bytes,
+                  dflash_stream stream);
+
+/* Bytes of workspace that dflash_attend needs on the current device for these pages (its size
+ * does not depend on the batch); negative: a dflash_status. */
+int64_t dflash_attend_workspace(const dflash_kv_pages* kv);
+
+/* One token per row of logits [rows, vocab] (`row_stride` elements between rows; dtype
+ * DFLASH_BF16 or DFLASH_F32), drawn from the uniform numbers u [rows] in [0, 1).  temperature,
+ * top_k, top_p, min_p: device arrays [rows] or NULL (1, off, off, off).  Row r with logits x_i,
+ * largest m, T = temperature:
+ *   w_i = exp((x_i - m) / T), taken as 0 where it is below 2^-40;
+ *   top-k (k > 0): the k largest x stay, equal ones by lowest index;
+ *   top-p (p < 1): in falling order (equal ones by index) those stay before which less than p of
+ *     the mass left by top-k lies; the first always stays;
+ *   min-p: those with w_i < min_p go (the largest has w = 1);
+ *   token = the first kept index, in index order, at which the running sum of kept w exceeds
+ *     u times their total (the last kept one if rounding leaves none).
+ * T == 0 gives the lowest index of the largest logit.  NaN logits count as -inf, which is never
+ * drawn; +inf logits share the draw alone.  A row without a candidate, or whose temperature is
+ * negative or not finite, gets token -1 and probability 0.  u outside [0, 1) or NaN is clamped.
+ * Weights and sums carry about 40 bits, so the token is that of exact arithmetic unless u or p
+ * falls within about 1e-12 of a border.
+ *   tokens [rows] int32;  probs [rows] fp32 or NULL: kept weight of the token / their total.
+ * 1 <= vocab <= 400000 (fp32) or 800000 (bf16) (EUNSUPPORTED above).  rows == 0 is a no-op. */
+int dflash_sample(const void* logits, int64_t row_stride, int32_t dtype, int32_t rows, int32_t vocab, const float* u,
+                  const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                  int32_t* tokens, float* probs, dflash_stream stream);
+
 /* Synchronise `stream`, read the device status word into *flags (may be NULL) and clear
  * it.  When DFLASH_DEV_TIMEOUT was set it also re-arms the handle's internal tile counters
  * (a kernel that gave up a wait may have left them part-counted), so the next call starts
@@ -320,7 +425,7 @@ int dflash_attention_check(dflash_handle* h, int32_t layer, const int32_t* ctx_l
 int dflash_device_status(dflash_handle* h, dflash_stream stream, uint32_t* flags);
 
 /* Last error message of the handle ("" if none); with h == NULL the message of the last
- * failed dflash_create on this thread. */
+ * failed call without a handle (dflash_create, the serving operators) on this thread. */
 const char* dflash_last_error(const dflash_handle* h);
 
 #ifdef __cplusplus
