@@ -23,4 +23,11 @@ inline cudaError_t smem_attr_once(K kern, int bytes, std::atomic<unsigned long l
   return e;
 }
 
+// SMs of the current device.
+inline cudaError_t sm_count(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+}
+
 }  // namespace dflash

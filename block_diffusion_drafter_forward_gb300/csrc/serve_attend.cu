@@ -1,33 +1,13 @@
-// Attention of a chunk of new tokens per sequence over its paged K/V rows (dflash_attend).
+// Attention of a chunk of new tokens per sequence over its paged K/V rows (dflash_attend): the C
+// entries, and the fp32 form on the CUDA cores (as the fp32 drafter's path).  The bf16 form is
+// serve_attend_tc.cu.
 #include <float.h>
 
 #include "launch_util.cuh"
-#include "serve.cuh"
+#include "serve_attend.cuh"
 
 namespace dflash {
 namespace {
-
-struct AttendParams {
-  const void* q;
-  void* out;
-  float* lse;
-  const void* pool;
-  const int32_t *page_tables, *kv_lens, *row_starts;
-  uint32_t* status;
-  int64_t q_stride, out_stride, page_stride;  // elements
-  int nb, n_rows, mpps, num_pages, nh, nkv, window, causal;
-  float scale_log2;  // scale * log2(e): scores are exponents of 2
-};
-
-// Sequence s: its rows [*r0, *r0 + *n), key rows *kv.  false: no rows, or out of range (*bad).
-__device__ __forceinline__ bool seq_of(const AttendParams& p, int s, int* r0, int* n, int* kv, bool* bad) {
-  const int a = __ldg(p.row_starts + s), b = __ldg(p.row_starts + s + 1), k = __ldg(p.kv_lens + s);
-  *bad = a < 0 || b < a || b > p.n_rows || k < 0 || (long long)k > (long long)p.mpps * kPage;
-  *r0 = a;
-  *n = b - a;
-  *kv = k;
-  return !*bad && b > a;
-}
 
 __device__ __forceinline__ int page_id(const AttendParams& p, int s, int lp) {
   const int page = __ldg(p.page_tables + (int64_t)s * p.mpps + lp);
@@ -38,7 +18,7 @@ __device__ __forceinline__ int page_id(const AttendParams& p, int s, int lp) {
 
 // CUDA-core form: one warp per (row, query head), online softmax over pages of 16 keys.  Lane l
 // takes key l % 16 and one half of the dims of q . k, and dims l, l + 32, ... of the output.
-template <typename T, int HD>
+template <int HD>
 __global__ void __launch_bounds__(128) attend_simple_kernel(const AttendParams p) {
   __shared__ float s_q[4][HD];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -56,9 +36,9 @@ __global__ void __launch_bounds__(128) attend_simple_kernel(const AttendParams p
   const bool rows = seq_of(p, s, &r0, &n, &kv, &bad);
   if (bad && p.status && lane == 0) atomicOr(p.status, DFLASH_DEV_BAD_CTX);
   if (!rows || i < r0 || i >= r0 + n) return;
-  const T* q = static_cast<const T*>(p.q) + i * p.q_stride + h * HD;
+  const float* q = static_cast<const float*>(p.q) + i * p.q_stride + h * HD;
 #pragma unroll
-  for (int e = 0; e < HD / 32; ++e) s_q[warp][lane + 32 * e] = Elem<T>::to_f(q[lane + 32 * e]) * p.scale_log2;
+  for (int e = 0; e < HD / 32; ++e) s_q[warp][lane + 32 * e] = q[lane + 32 * e] * p.scale_log2;
   __syncwarp();
   const int pos = kv - n + (i - r0);
   const int k_end = p.causal ? min(kv, pos + 1) : kv;
@@ -68,14 +48,14 @@ __global__ void __launch_bounds__(128) attend_simple_kernel(const AttendParams p
   for (int e = 0; e < HD / 32; ++e) acc[e] = 0.f;
   const int half = lane >> 4, j = lane & 15;
   for (int lp = k_begin / kPage; lp * kPage < k_end; ++lp) {
-    const T* tile = static_cast<const T*>(p.pool) + page_id(p, s, lp) * p.page_stride + (int64_t)g * 2 * kPage * HD;
+    const float* tile = static_cast<const float*>(p.pool) + page_id(p, s, lp) * p.page_stride + (int64_t)g * 2 * kPage * HD;
     float sc = 0.f;
 #pragma unroll
     for (int c = 0; c < HD / 16; ++c) {
       const int d8 = half * (HD / 16) + c;
-      const T* k = tile + k_in_tile(j, d8 * 8, HD);
+      const float* k = tile + k_in_tile(j, d8 * 8, HD);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sc = fmaf(s_q[warp][d8 * 8 + e], Elem<T>::to_f(k[e]), sc);
+      for (int e = 0; e < 8; ++e) sc = fmaf(s_q[warp][d8 * 8 + e], k[e], sc);
     }
     sc += __shfl_xor_sync(0xffffffffu, sc, 16);
     const int key = lp * kPage + j;
@@ -94,18 +74,18 @@ __global__ void __launch_bounds__(128) attend_simple_kernel(const AttendParams p
     m = m_new;
 #pragma unroll
     for (int e = 0; e < HD / 32; ++e) acc[e] *= alpha;
-    const T* v = tile + kPage * HD;
+    const float* v = tile + kPage * HD;
     for (int jj = max(0, k_begin - lp * kPage); jj < min(kPage, k_end - lp * kPage); ++jj) {  // seen keys only
       const float w = __shfl_sync(0xffffffffu, pr, jj);
 #pragma unroll
-      for (int e = 0; e < HD / 32; ++e) acc[e] = fmaf(w, Elem<T>::to_f(v[v_in_tile(jj, lane + 32 * e, HD)]), acc[e]);
+      for (int e = 0; e < HD / 32; ++e) acc[e] = fmaf(w, v[v_in_tile(jj, lane + 32 * e, HD)], acc[e]);
     }
   }
-  T* out = static_cast<T*>(p.out) + i * p.out_stride + h * HD;
+  float* out = static_cast<float*>(p.out) + i * p.out_stride + h * HD;
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
 #pragma unroll
-  for (int e = 0; e < HD / 32; ++e) out[lane + 32 * e] = Elem<T>::from_f(acc[e] * inv);
-  if (p.lse && lane == 0) p.lse[(int64_t)i * p.nh + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  for (int e = 0; e < HD / 32; ++e) out[lane + 32 * e] = acc[e] * inv;
+  if (p.lse && lane == 0) p.lse[(int64_t)i * p.nh + h] = lse_of(m, l);
 }
 
 }  // namespace
@@ -115,7 +95,10 @@ using namespace dflash;
 
 extern "C" int64_t dflash_attend_workspace(const dflash_kv_pages* kv) {
   if (int rc = check_pages(kv)) return rc;
-  return 0;
+  if (kv->dtype == DFLASH_F32) return 0;
+  int sms = 0;
+  if (cudaError_t e = sm_count(&sms); e != cudaSuccess) return call_error(DFLASH_ECUDA, "attend_workspace", e);
+  return attend_tc_workspace(kv->head_dim, sms);
 }
 
 extern "C" int dflash_attend(const dflash_kv_pages* kv, const void* q, int64_t q_stride, const int32_t* page_tables,
@@ -125,8 +108,9 @@ extern "C" int dflash_attend(const dflash_kv_pages* kv, const void* q, int64_t q
                              int64_t workspace_bytes, dflash_stream stream) {
   if (int rc = check_pages(kv)) return rc;
   if (nb < 1 || n_rows < 0 || max_new < 0) return call_error(DFLASH_EINVAL, "attend: nb >= 1, n_rows >= 0 and max_new >= 0");
-  if (max_pages_per_seq < 1 || max_pages_per_seq >= 1 << 27)
-    return call_error(DFLASH_EINVAL, "attend: max_pages_per_seq must be in [1, 2^27)");
+  if (nb > 16384) return call_error(DFLASH_ECAPACITY, "attend: nb above 16384");
+  if (max_pages_per_seq < 1 || max_pages_per_seq >= 1 << 26)  // key indices stay below 2^30
+    return call_error(DFLASH_EINVAL, "attend: max_pages_per_seq must be in [1, 2^26)");
   if (n_q_heads < 1 || n_q_heads % kv->n_kv_heads || n_q_heads / kv->n_kv_heads > 128)
     return call_error(DFLASH_EINVAL, "attend: n_q_heads must be a multiple of n_kv_heads, at most 128 times it");
   if (window < 0) return call_error(DFLASH_EINVAL, "attend: window must be >= 0");
@@ -145,12 +129,18 @@ extern "C" int dflash_attend(const dflash_kv_pages* kv, const void* q, int64_t q
                  nb, n_rows, max_pages_per_seq, kv->num_pages, n_q_heads, kv->n_kv_heads, window, causal != 0,
                  scale * 1.4426950408889634f};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (kv->dtype == DFLASH_BF16) {
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e == cudaSuccess) e = launch_attend_tc(p, kv->head_dim, max_new, workspace, sms, st);
+    return e == cudaSuccess ? DFLASH_OK : call_error(DFLASH_ECUDA, "attend", e);
+  }
   const int64_t blocks = ((int64_t)n_rows * n_q_heads + 3) / 4;
   if (blocks > 0x7fffffff) return call_error(DFLASH_ECAPACITY, "attend: too many rows for one call");
-  const bool f32 = kv->dtype == DFLASH_F32, w = kv->head_dim == 128;
-  auto kern = f32 ? (w ? attend_simple_kernel<float, 128> : attend_simple_kernel<float, 64>)
-                  : (w ? attend_simple_kernel<__nv_bfloat16, 128> : attend_simple_kernel<__nv_bfloat16, 64>);
-  kern<<<(unsigned)blocks, 128, 0, st>>>(p);
+  if (kv->head_dim == 128)
+    attend_simple_kernel<128><<<(unsigned)blocks, 128, 0, st>>>(p);
+  else
+    attend_simple_kernel<64><<<(unsigned)blocks, 128, 0, st>>>(p);
   if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return call_error(DFLASH_ECUDA, "attend", e);
   return DFLASH_OK;
 }

@@ -1,0 +1,778 @@
+// Tensor-core form of dflash_attend (bf16): paged attention of ragged chunks, stream-K.
+//
+// Work unit = (sequence, query tile, kv head): with G = query heads per kv head, the G heads of
+// T = floor(128 / G) tokens are the rows of one 128-row UMMA tile (row = token * G + head), so a
+// K/V byte feeds every query head that shares it.  Keys go in chunks of 128 (8 pages).  The
+// chunks of all units, in (sequence, tile, head) order, form one index space; CTA b of a
+// one-CTA-per-SM grid takes slots [b W / n, (b + 1) W / n) of it, sized on the device from the
+// lengths, so prompts, blocks and single tokens share the SMs evenly and a graph replayed with
+// other lengths stays balanced.  A unit cut between CTAs leaves fp32 partials (O, m, l) in the
+// workspace (at most two per CTA) that attend_combine_kernel merges in key order.
+//
+// Two softmax streams of 128 threads (one query row each) keep the tensor cores fed, in two forms:
+//   two tiles (long chunks): stream x owns query tile x of a 256-row unit, both read the same
+//     K/V slots: 4 x 128 x 128 x head_dim products per 64 KB of K/V, tensor-bound;
+//   one tile (short chunks): stream x takes the chunks of parity x of the same queries, and the
+//     two (O, m, l) meet at the segment's end: HBM-bound, two chunks' softmax in flight.
+// Per stream the order is S = Q K^T -> softmax -> O += P V -> next S; while one stream's softmax
+// runs, the tensor cores work for the other.  P goes back as bf16 over its own S columns and is
+// read from TMEM; O stays in TMEM and is rescaled only when a row's maximum grew by more than
+// 2^8 (P <= 2^8 stays exact in range, the normalised result is the same).
+//
+// Rounding: P is bf16 (the MMA's operand type), sums and O fp32, the normaliser sums the fp32 P.
+// Warp roles: 0-3 stream 0, 4-7 stream 1, 8 K pages, 9 MMA issue, 10 V pages, 11 zeroes the key
+// rows behind a sequence's end in its last V page (never-written rows may hold NaN, and 0 * NaN
+// would reach O; their scores are masked by select).
+#include <float.h>
+
+#include <atomic>
+
+#include "launch_util.cuh"
+#include "serve_attend.cuh"
+#include "tc_common.cuh"
+
+namespace dflash {
+namespace {
+
+using namespace tc;
+
+constexpr int kKeys = 128;                      // keys per chunk
+constexpr int kPages = kKeys / kPage;           // 8
+constexpr int kThreads = 384;
+constexpr int kWarps = kThreads / 32;
+constexpr int kCtl = 2944;                      // barriers, plan, row exchange
+
+// Slots of the index space a unit occupies beside its chunks: the cost of opening a segment
+// (queries, pipeline restart, output) in chunks.
+constexpr int kUnitCost = 3;
+
+template <int HD, int NT>
+struct Cfg {
+  static constexpr int kTile = kPage * HD * 2;         // a page of one head: bytes of K (or V)
+  static constexpr int kQ = 128 * HD * 2;              // a query tile
+  static constexpr int kSlot = kPages * kTile;         // a chunk's K (or V)
+  static constexpr int kNK = HD == 128 ? 3 : 6;        // K and V slots in flight
+  static constexpr int kNV = HD == 128 ? (NT == 2 ? 2 : 3) : 6;
+  static constexpr int kSmem = NT * kQ + (kNK + kNV) * kSlot + kCtl + 128;
+};
+
+struct Seg {
+  int s, r0, n, kv;     // sequence, its first row, rows, key rows
+  int tile, g, t0;      // query tile, kv head, its first token
+  int k0, nch;          // first key (page aligned), chunks of the unit
+  int c_lo, c_hi;       // this CTA's chunks of it
+};
+
+// Tokens of a unit's tile and the chunks it visits.
+struct Shape {
+  int group, T, TT;     // query heads per kv head, tokens of a 128-row tile, of a unit
+};
+__device__ __forceinline__ Shape shape_of(const AttendParams& p, int NT) {
+  Shape h;
+  h.group = p.nh / p.nkv;
+  h.T = 128 / h.group;
+  h.TT = h.T * NT;
+  return h;
+}
+__device__ __forceinline__ int unit_chunks(const AttendParams& p, const Shape& h, int n, int kv, int tile, int* k0) {
+  const int t0 = tile * h.TT, t1 = min(n, t0 + h.TT);
+  const int end = p.causal ? min(kv, max(0, kv - n + t1)) : kv;
+  int lo = p.window > 0 ? max(0, kv - n + t0 - p.window + 1) : 0;
+  lo &= ~(kPage - 1);
+  *k0 = lo;
+  return max(1, (end - lo + kKeys - 1) / kKeys);  // a unit without keys still writes its zeros
+}
+
+// The segments of index range [lo, hi), from unit (s, tile, g) whose first slot is pu.
+struct Walk {
+  long long lo, hi, pu;
+  int s, tile, g;
+
+  __device__ bool next(const AttendParams& p, const Shape& h, Seg& q) {
+    while (pu < hi && s < p.nb) {
+      bool bad;
+      if (!seq_of(p, s, &q.r0, &q.n, &q.kv, &bad)) {
+        ++s;
+        tile = g = 0;
+        continue;
+      }
+      q.nch = unit_chunks(p, h, q.n, q.kv, tile, &q.k0);
+      q.s = s, q.tile = tile, q.g = g, q.t0 = tile * h.TT;
+      const long long first = pu + kUnitCost;
+      pu = first + q.nch;
+      if (++g == p.nkv) {
+        g = 0;
+        if (++tile * h.TT >= q.n) tile = 0, ++s;
+      }
+      if (hi <= first || lo >= pu) continue;  // only cost slots of it are in range
+      q.c_lo = (int)(lo > first ? lo - first : 0);
+      q.c_hi = (int)(hi < pu ? hi - first : q.nch);
+      return true;
+    }
+    return false;
+  }
+};
+
+struct Ctl {
+  uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6], v_raw[6];
+  uint64_t s_full[2], p_full[2], o_done[2], o_free[2], q_full[2], q_empty;
+  uint32_t tmem_slot;
+  int flags[2];
+  int s0, tile0, found;
+  long long red[kWarps], W, base;
+  float2 ml[2][128];  // one tile: the streams' (m, l) of every row
+};
+static_assert(sizeof(Ctl) <= kCtl, "control block overflows its slot");
+
+// Slots of tiles [a, b) of a sequence for one kv head, by this thread.
+__device__ __forceinline__ long long tile_slots(const AttendParams& p, const Shape& h, int n, int kv, int a, int b, int step) {
+  long long r = 0;
+  int k0;
+  for (int t = a; t < b; t += step) r += unit_chunks(p, h, n, kv, t, &k0) + kUnitCost;
+  return r;
+}
+
+// This CTA's walk.  `scratch`: nb long longs of shared memory.  All threads.
+__device__ Walk plan(const AttendParams& p, const Shape& h, Ctl& c, long long* scratch, bool wide, long long* W_out) {
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  // slots of each sequence (all kv heads): a thread per sequence, or a warp where chunks are long
+  for (int s = wide ? warp : t; s < p.nb; s += wide ? kWarps : kThreads) {
+    int r0, n, kv;
+    bool bad;
+    long long m = 0;
+    if (seq_of(p, s, &r0, &n, &kv, &bad)) {
+      const int tiles = (n + h.TT - 1) / h.TT;
+      m = wide ? tile_slots(p, h, n, kv, lane, tiles, 32) : tile_slots(p, h, n, kv, 0, tiles, 1);
+    } else if (bad && blockIdx.x == 0 && p.status && (!wide || lane == 0)) {
+      atomicOr(p.status, DFLASH_DEV_BAD_CTX);
+    }
+    if (wide) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+    }
+    if (!wide || lane == 0) scratch[s] = m * p.nkv;
+  }
+  if (t == 0) c.found = 0;
+  __syncthreads();
+  // thread t sums sequences [t per, (t + 1) per)
+  const int per = (p.nb + kThreads - 1) / kThreads, s_lo = min(p.nb, t * per), s_hi = min(p.nb, s_lo + per);
+  auto scan = [&](long long v, long long* all) {  // exclusive sum over the threads before this one
+    long long inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) c.red[warp] = inc;
+    __syncthreads();
+    long long b = inc - v, a = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) b += c.red[w];
+      a += c.red[w];
+    }
+    __syncthreads();
+    *all = a;
+    return b;
+  };
+  long long mine = 0, W;
+  for (int s = s_lo; s < s_hi; ++s) mine += scratch[s];
+  long long at = scan(mine, &W);
+  const int G = (int)min((long long)gridDim.x, W), b = blockIdx.x;
+  Walk w;
+  w.lo = b < G ? (long long)b * W / G : 0;
+  w.hi = b < G ? (long long)(b + 1) * W / G : 0;
+  w.s = p.nb, w.tile = w.g = 0, w.pu = w.hi;
+  *W_out = W;
+  if (w.lo >= w.hi) return w;
+  if (at <= w.lo && w.lo < at + mine) {
+    for (int s = s_lo; s < s_hi; ++s) {
+      if (w.lo < at + scratch[s]) {
+        c.s0 = s, c.base = at;
+        break;
+      }
+      at += scratch[s];
+    }
+  }
+  __syncthreads();
+  const int s0 = c.s0;
+  long long base = c.base;
+  int r0, n, kv, k0;
+  bool bad;
+  seq_of(p, s0, &r0, &n, &kv, &bad);
+  const int tiles = (n + h.TT - 1) / h.TT;
+  for (int b0 = 0; b0 < tiles; b0 += kThreads) {  // the tile that holds slot lo
+    const int tile = b0 + t;
+    const long long v = tile < tiles ? (long long)(unit_chunks(p, h, n, kv, tile, &k0) + kUnitCost) * p.nkv : 0;
+    long long all;
+    const long long x = base + scan(v, &all);
+    if (v > 0 && x <= w.lo && w.lo < x + v) c.tile0 = tile, c.base = x, c.found = 1;
+    base += all;
+    __syncthreads();
+    if (c.found) break;
+  }
+  w.s = s0, w.tile = c.tile0;
+  const int slots = unit_chunks(p, h, n, kv, w.tile, &k0) + kUnitCost;
+  w.g = (int)((w.lo - c.base) / slots);
+  w.pu = c.base + (long long)w.g * slots;
+  return w;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The chunks of stream x, in order, as every role counts them.
+template <int NT>
+struct It {
+  Walk w;
+  Seg sg;
+  int j, n;        // chunk within the segment, chunks of it
+  int kc0;         // chunks of the segments before it
+  int it;          // chunks this stream did before
+  int seg, act;    // segments before this one: all, and those this stream works in
+  bool valid;
+
+  // does stream x work in the segment?
+  __device__ static bool active(const Shape& h, const Seg& q, int x) {
+    return x == 0 || (NT == 2 ? q.t0 + h.T < q.n : q.c_hi - q.c_lo > 1);
+  }
+  __device__ bool enter(const AttendParams& p, const Shape& h, int x) {
+    while (w.next(p, h, sg)) {
+      ++seg;
+      n = sg.c_hi - sg.c_lo;
+      if (active(h, sg, x)) {
+        ++act;
+        j = NT == 2 ? 0 : x;
+        return true;
+      }
+      kc0 += n;
+    }
+    return false;
+  }
+  __device__ void start(const AttendParams& p, const Shape& h, const Walk& w0, int x) {
+    w = w0;
+    kc0 = it = 0;
+    seg = act = -1;
+    valid = enter(p, h, x);
+  }
+  __device__ bool first(int x) const { return j == (NT == 2 ? 0 : x); }
+  __device__ void step(const AttendParams& p, const Shape& h, int x) {
+    ++it;
+    j += NT == 2 ? 1 : 2;
+    if (j < n) return;
+    kc0 += n;
+    valid = enter(p, h, x);
+  }
+  // pages of the chunk that hold keys of the sequence
+  __device__ int pages() const {
+    const int k = sg.k0 + (sg.c_lo + j) * kKeys;
+    return max(0, min(kPages, (sg.kv - k + kPage - 1) / kPage));
+  }
+};
+
+template <int HD, int NT>
+__global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendParams p, const AttendWork wk) {
+  using C = Cfg<HD, NT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  uint8_t* sQ = smem;
+  uint8_t* sK = sQ + NT * C::kQ;
+  uint8_t* sV = sK + C::kNK * C::kSlot;
+  Ctl& c = *reinterpret_cast<Ctl*>(sV + C::kNV * C::kSlot);
+  volatile int* flags = c.flags;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const Shape h = shape_of(p, NT);
+
+  if (t == 0) wk.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+  long long W;
+  const Walk walk = plan(p, h, c, reinterpret_cast<long long*>(sK), wk.long_chunks, &W);
+  if (walk.lo >= walk.hi) {  // nothing for this CTA
+    pdl_trigger();
+    return;
+  }
+  if (t == 0) {
+    for (int i = 0; i < 6; ++i) {
+      mbar_init(&c.k_full[i], 1);
+      mbar_init(&c.k_empty[i], NT);
+      mbar_init(&c.v_full[i], 1);
+      mbar_init(&c.v_empty[i], NT);
+      mbar_init(&c.v_raw[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c.s_full[i], 1);
+      mbar_init(&c.p_full[i], 128);
+      mbar_init(&c.o_done[i], 1);
+      mbar_init(&c.o_free[i], NT == 2 ? 128 : 256);
+      mbar_init(&c.q_full[i], 128);
+    }
+    mbar_init(&c.q_empty, 1);
+    flags[0] = 0;
+    fence_barrier_init();
+  }
+  fence_proxy_async_smem();  // the plan's scratch is overwritten by copies
+  if (warp == 0) tmem_alloc(&c.tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = c.tmem_slot;
+  pdl_trigger();
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (warp == 8 || warp == 10) {
+      // ---- page producers: lane l copies page l of a chunk.  The page ids of the next chunk are
+      // fetched while the warp waits for a slot.
+      const int kv = warp == 10;
+      uint64_t* full = kv ? c.v_full : c.k_full;
+      uint64_t* empty = kv ? c.v_empty : c.k_empty;
+      uint8_t* ring = kv ? sV : sK;
+      const int slots = kv ? C::kNV : C::kNK;
+      Walk w = walk;
+      Seg q;
+      int i = 0;
+      bool stop = false;
+      while (!stop && w.next(p, h, q)) {
+        const int pages = (q.kv + kPage - 1) / kPage;
+        auto fetch = [&](int ch) {
+          const int lp = (q.k0 + ch * kKeys) / kPage + lane;
+          return lane < kPages && lp < pages && ch < q.c_hi ? __ldg(p.page_tables + (int64_t)q.s * p.mpps + lp) : 0;
+        };
+        int page = fetch(q.c_lo);
+        for (int ch = q.c_lo; ch < q.c_hi; ++ch, ++i) {
+          const int b = i % slots;
+          if (i >= slots && !mbar_wait_ab(&empty[b], (i / slots - 1) & 1, flags)) {
+            stop = true;
+            break;
+          }
+          const int key = q.k0 + ch * kKeys;
+          const int np = max(0, min(kPages, pages - key / kPage));
+          // V of a chunk whose last page is part full (or that has no page) goes by the zeroing warp
+          const bool tail = kv && (np == 0 || key + np * kPage > q.kv);
+          uint64_t* bar = tail ? &c.v_raw[b] : &full[b];
+          if (lane == 0) mbar_arrive_expect_tx(bar, np * C::kTile);
+          __syncwarp();
+          if (lane < np) {
+            if (page < 0 || page >= p.num_pages) {
+              if (p.status) atomicOr(p.status, DFLASH_DEV_BAD_PAGE);
+              page = 0;
+            }
+            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.pool) + page * p.page_stride +
+                                       ((int64_t)q.g * 2 + kv) * (kPage * HD);
+            bulk_load(ring + b * C::kSlot + lane * C::kTile, src, C::kTile, bar);
+          }
+          page = fetch(ch + 1);
+        }
+      }
+    } else if (warp == 9) {
+      // ---- MMA issue (lane 0): each stream alternates S and P V; whichever is ready goes out
+      if (lane == 0) {
+        constexpr uint32_t id_s = idesc_bf16(128, kKeys), id_o = idesc_bf16(128, HD);
+        It<NT> its[2];
+        bool pv[2] = {false, false};
+        its[0].start(p, h, walk, 0);
+        its[1].start(p, h, walk, 1);
+        long long idle = 0;
+        int s_out = 0;  // one tile: S of the segment issued so far
+        while (its[0].valid || its[1].valid) {
+          bool did = false;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            It<NT>& a = its[x];
+            const uint32_t tS = tmem + x * 128, tO = tmem + 256 + x * 128;
+            const bool give_up = flags[0];  // after a timeout: commits only, no MMAs
+            if (a.valid && pv[x]) {
+              const int kc = a.kc0 + a.j, vb = kc % C::kNV;
+              const int segs = NT == 2 ? a.act : a.seg;
+              if (give_up || (mbar_test_wait(&c.p_full[x], a.it & 1) && mbar_test_wait(&c.v_full[vb], (kc / C::kNV) & 1) &&
+                              (!a.first(x) || segs == 0 || mbar_test_wait(&c.o_free[NT == 2 ? x : 0], (segs - 1) & 1)))) {
+                tc_fence_after();
+                if (!give_up) {
+                  const int np = max(1, a.pages());
+                  for (int k = 0; k < np; ++k)  // 16 keys = 8 TMEM columns of P each
+                    mma_bf16_tmem_a(tO, tS + k * 8, desc_noswz(sV + vb * C::kSlot + k * C::kTile, 128, 256), id_o,
+                                    (!a.first(x) || k > 0) ? 1u : 0u);
+                }
+                mma_commit(&c.o_done[x]);
+                mma_commit(&c.v_empty[vb]);
+                if (NT == 2 && x == 0 && !It<NT>::active(h, a.sg, 1)) mma_commit(&c.v_empty[vb]);
+                pv[x] = false;
+                a.step(p, h, x);
+                did = true;
+              }
+            }
+            if (a.valid && !pv[x]) {
+              const int kc = a.kc0 + a.j, kb = kc % C::kNK;
+              if (give_up || (mbar_test_wait(&c.k_full[kb], (kc / C::kNK) & 1) &&
+                              (!a.first(x) || mbar_test_wait(&c.q_full[NT == 2 ? x : 0], (NT == 2 ? a.act : a.seg) & 1)))) {
+                tc_fence_after();
+                if (!give_up) {
+                  const uint8_t* q = sQ + (NT == 2 ? x : 0) * C::kQ;
+                  const uint8_t* k = sK + kb * C::kSlot;
+#pragma unroll
+                  for (int d = 0; d < HD / 16; ++d)
+                    mma_bf16(tS, desc_noswz(q + d * 256, 128, HD * 16), desc_noswz(k + d * 256, 128, HD * 16), id_s,
+                             d > 0 ? 1u : 0u);
+                }
+                mma_commit(&c.s_full[x]);
+                mma_commit(&c.k_empty[kb]);
+                if (NT == 2 && x == 0 && !It<NT>::active(h, a.sg, 1)) mma_commit(&c.k_empty[kb]);
+                if (NT == 1 && ++s_out == a.n) {  // both streams' S read the same queries
+                  mma_commit(&c.q_empty);
+                  s_out = 0;
+                }
+                pv[x] = true;
+                did = true;
+              }
+            }
+          }
+          idle = did ? 0 : idle + 1;
+          if (idle > kSpinLimit) flags[0] = 1;
+        }
+      }
+      __syncwarp();
+    } else {
+      // ---- zero the rows behind the sequence's end in its last V page (keys >= kv)
+      Walk w = walk;
+      Seg q;
+      int i = 0;
+      uint32_t used = 0;  // parity of each slot's v_raw
+      bool stop = false;
+      while (!stop && w.next(p, h, q)) {
+        const int pages = (q.kv + kPage - 1) / kPage;
+        const int n = q.c_hi - q.c_lo;
+        const int key = q.k0 + (q.c_hi - 1) * kKeys;  // only a unit's last chunk can reach past the end
+        const int np = max(0, min(kPages, pages - key / kPage));
+        i += n;
+        if (np > 0 && key + np * kPage <= q.kv) continue;
+        const int b = (i - 1) % C::kNV;
+        if (!mbar_wait_ab(&c.v_raw[b], (used >> b) & 1, flags)) {
+          stop = true;
+          break;
+        }
+        used ^= 1u << b;
+        const int lp = max(0, np - 1), live = np == 0 ? 0 : q.kv - key - lp * kPage;  // rows of the page to keep
+        uint4* v = reinterpret_cast<uint4*>(sV + b * C::kSlot + lp * C::kTile);
+        for (int e = lane; e < HD * 2; e += 32) {  // 16 bytes: 8 keys of one dim, (d / 8, key / 8, d % 8)
+          const int j0 = (e >> 3 & 1) * 8;
+          if (j0 >= live) {
+            v[e] = make_uint4(0, 0, 0, 0);
+          } else if (j0 + 8 > live) {
+            __nv_bfloat16* x = reinterpret_cast<__nv_bfloat16*>(v + e);
+            for (int k = live - j0; k < 8; ++k) x[k] = __float2bfloat16(0.f);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c.v_full[b]);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    // ---- softmax streams: thread = query row `row` of its tile
+    const int x = warp >> 2, row = t & 127;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + x * 128 + lane_off;
+    const int tok = row / h.group, head = row - tok * h.group;
+    // queries of a segment's tile (16-byte pieces; a warp copies 8 rows x 64 bytes at a time: whole
+    // sectors of q, conflict-free rows of the operand layout)
+    auto load_q = [&](const Seg& q) {
+      const int tb = q.t0 + (NT == 2 ? x * h.T : 0);
+      uint8_t* dst = sQ + (NT == 2 ? x : 0) * C::kQ;
+#pragma unroll
+      for (int k = 0; k < HD / 8; ++k) {
+        const int idx = k * 4 + (warp & 3);
+        const int r = idx / (HD / 32) * 8 + (lane & 7), d8 = idx % (HD / 32) * 4 + (lane >> 3);
+        const int tk = r / h.group, hd = r - tk * h.group;
+        uint8_t* d = dst + ((r >> 3) * (HD / 8) + d8) * 128 + (r & 7) * 16;
+        if (tk < h.T && tb + tk < q.n)
+          cp_async16(d, static_cast<const __nv_bfloat16*>(p.q) + (int64_t)(q.r0 + tb + tk) * p.q_stride +
+                            ((int64_t)q.g * h.group + hd) * HD + d8 * 8);
+        else
+          *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto q_ready = [&] {
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+      mbar_arrive(&c.q_full[NT == 2 ? x : 0]);
+    };
+    // one tile: the stream that does a segment's last chunk loads the next one's queries
+    auto loads_after = [&](const Seg& q) { return NT == 2 || ((q.c_hi - q.c_lo - 1) & 1) == x; };
+
+    Walk w = walk;
+    Seg q, nq;
+    bool have = w.next(p, h, q);
+    while (NT == 2 && have && !It<NT>::active(h, q, x)) have = w.next(p, h, q);
+    if (have && (NT == 2 || x == 0)) {
+      load_q(q);
+      q_ready();
+    }
+    int it = 0, seg = 0;  // chunks and segments done by this stream
+    while (have) {
+      bool more = w.next(p, h, nq);
+      while (NT == 2 && more && !It<NT>::active(h, nq, x)) more = w.next(p, h, nq);
+      const int n = q.c_hi - q.c_lo;
+      const int tk = q.t0 + (NT == 2 ? x * h.T : 0) + tok;
+      const bool valid = tok < h.T && tk < q.n;
+      const bool warp_valid = __any_sync(0xffffffffu, valid);
+      // keys [lo, hi) are seen by this row (rows without a token: anything, they are not written)
+      const int pos = q.kv - q.n + tk;
+      const int hi = !valid ? INT_MAX : p.causal ? min(q.kv, pos + 1) : q.kv;
+      const int lo = valid && p.window > 0 ? max(0, pos - p.window + 1) : 0;
+      float m = -INFINITY, l = 0.f;
+      int done = 0;
+#pragma unroll 1
+      for (int j = NT == 2 ? 0 : x; j < n; j += NT == 2 ? 1 : 2, ++it, ++done) {
+        if (!mbar_wait_ab(&c.s_full[x], it & 1, flags)) flags[0] = 1;
+        tc_fence_after();
+        const bool load_next = j == n - 1 && more && loads_after(q);
+        if (load_next) {  // once every S that reads this segment's queries is done
+          if (NT == 1 && !mbar_wait_ab(&c.q_empty, seg & 1, flags)) flags[0] = 1;
+          load_q(nq);
+        }
+        if (warp_valid) {
+          const int kb = q.k0 + (q.c_lo + j) * kKeys;
+          float a[64], b[64];
+          tmem_ld64(tS, a);
+          tmem_ld64(tS + 64, b);
+          if (__any_sync(0xffffffffu, kb < lo || kb + kKeys > hi)) {
+            const unsigned span = hi > lo ? (unsigned)(hi - lo) : 0u;
+#pragma unroll
+            for (int e = 0; e < 64; ++e) {
+              if ((unsigned)(kb + e - lo) >= span) a[e] = -INFINITY;
+              if ((unsigned)(kb + 64 + e - lo) >= span) b[e] = -INFINITY;
+            }
+          }
+          float m0 = a[0], m1 = b[0], m2 = a[1], m3 = b[1];
+#pragma unroll
+          for (int e = 2; e < 64; e += 2) {
+            m0 = fmaxf(m0, a[e]), m1 = fmaxf(m1, b[e]);
+            m2 = fmaxf(m2, a[e + 1]), m3 = fmaxf(m3, b[e + 1]);
+          }
+          const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * p.scale_log2;
+          const bool grow = top > m + 8.f;  // (m = -inf: any finite score)
+          const float m_new = grow ? top : m;
+          const float alpha = grow && m != -INFINITY ? ex2(m - m_new) : 1.f;
+          if (done > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            if (!mbar_wait_ab(&c.o_done[x], (it - 1) & 1, flags)) flags[0] = 1;
+            tc_fence_after();
+#pragma unroll 1
+            for (int d = 0; d < HD; d += 32) {
+              float v[32];
+              tmem_ld32(tmem + 256 + x * 128 + lane_off + d, v);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] *= alpha;
+              tmem_st32(tmem + 256 + x * 128 + lane_off + d, v);
+            }
+          }
+          const float off = m_new == -INFINITY ? 0.f : -m_new;
+          float l0 = 0.f, l1 = 0.f;
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float u = ex2(fmaf(a[2 * e], p.scale_log2, off)), v = ex2(fmaf(a[2 * e + 1], p.scale_log2, off));
+            l0 += u, l1 += v;
+            pk[e] = pack_bf16(u, v);
+          }
+          tmem_st32u(tS, pk);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float u = ex2(fmaf(b[2 * e], p.scale_log2, off)), v = ex2(fmaf(b[2 * e + 1], p.scale_log2, off));
+            l0 += u, l1 += v;
+            pk[e] = pack_bf16(u, v);
+          }
+          tmem_st32u(tS + 32, pk);
+          l = l * alpha + (l0 + l1);
+          m = m_new;
+        }
+        tc_fence_before();
+        mbar_arrive(&c.p_full[x]);
+        if (load_next) q_ready();
+      }
+      // ---- the segment's rows
+      const bool whole = q.c_lo == 0 && q.c_hi == q.nch;
+      const int slot = 2 * blockIdx.x + (q.c_lo == 0 ? 1 : 0);  // partials: the unit's start, or a later part
+      float w0 = 1.f, w1 = 0.f;  // weights of O 0 and O 1 in this row
+      bool use1 = false;
+      // this stream's O: its last P V done, hence every earlier one
+      if (done > 0 && !mbar_wait_ab(&c.o_done[x], (it - 1) & 1, flags)) flags[0] = 1;
+      if (NT == 1) {  // and the other's, with its (m, l)
+        c.ml[x][row] = make_float2(m, l);
+        named_barrier(1 + (warp & 3), 64);
+        const float2 o = c.ml[x ^ 1][row];
+        named_barrier(1 + (warp & 3), 64);  // read before the next segment's write
+        const float M = fmaxf(m, o.x), base = M == -INFINITY ? 0.f : M;
+        const float f = ex2(m - base), fo = ex2(o.x - base);
+        l = l * f + o.y * fo;
+        m = M;
+        w0 = x == 0 ? f : fo;
+        w1 = x == 0 ? fo : f;
+        use1 = n > 1;
+      }
+      tc_fence_after();
+      if (__all_sync(0xffffffffu, !flags[0]) && warp_valid) {
+        // one tile: stream x writes dims [x HD / 2, + HD / 2) of both; two: its own row
+        constexpr int kD = NT == 2 ? HD : HD / 2;
+        const int d_lo = NT == 2 ? 0 : x * kD;
+        const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;
+        const int64_t gr = q.r0 + tk;
+        const int gh = q.g * h.group + head;
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + gr * p.out_stride + (int64_t)gh * HD + d_lo;
+        const int prow = (NT == 2 ? x * 128 : 0) + row;
+        if (NT == 1) w0 *= inv, w1 *= inv;
+#pragma unroll 1
+        for (int d = 0; d < kD; d += 32) {
+          float v[32];
+          if (NT == 2) {
+            tmem_ld32(tmem + 256 + x * 128 + lane_off + d, v);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] *= inv;
+          } else {
+            tmem_ld32(tmem + 256 + lane_off + d_lo + d, v);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] *= w0;
+            if (use1) {
+              float v1[32];
+              tmem_ld32(tmem + 384 + lane_off + d_lo + d, v1);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = fmaf(v1[e], w1, v[e]);
+            }
+          }
+          if (!valid) continue;
+          if (whole) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              *reinterpret_cast<uint4*>(dst + d + e) = make_uint4(pack_bf16(v[e], v[e + 1]), pack_bf16(v[e + 2], v[e + 3]),
+                                                                  pack_bf16(v[e + 4], v[e + 5]), pack_bf16(v[e + 6], v[e + 7]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              __stcg(part_at(wk, slot, prow, (d_lo + d + e) >> 2, NT * 128, HD), make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
+          }
+        }
+        if (valid && (NT == 2 || x == 0)) {
+          if (!whole)
+            __stcg(wk.ml + (int64_t)slot * (NT * 128) + prow, make_float2(m, l));
+          else if (p.lse)
+            p.lse[gr * p.nh + gh] = lse_of(m, l);
+        }
+      }
+      if (t == 0 && q.c_lo == 0 && !whole) {  // the unit starts here and goes on in the next CTAs
+        const long long end = walk.hi - (q.c_hi - 1) + q.nch - 1;  // past its last slot: slot hi - 1 is chunk c_hi - 1
+        const int G = (int)min((long long)gridDim.x, W);
+        const int last = (int)((end * G + W - 1) / W) - 1;
+        wk.meta[blockIdx.x] = make_int4(last - (int)blockIdx.x + 1, q.s, q.tile, q.g);
+      }
+      tc_fence_before();
+      mbar_arrive(&c.o_free[NT == 2 ? x : 0]);
+      q = nq;
+      have = more;
+      ++seg;
+    }
+    if (flags[0]) {
+      if (t == 0 && p.status) atomicOr(p.status, DFLASH_DEV_TIMEOUT);
+      for (int k = 0; k < 2000; ++k) __nanosleep(1000);  // copies still in flight land first
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// Merges the partials of the unit that starts in CTA b = blockIdx.x and ends in a later one, in
+// key order.  Threads: dims 4 db .. of rows in turn; blockIdx.y strides over the row groups.
+template <int HD, int NT>
+__global__ void __launch_bounds__(128) attend_combine_kernel(const AttendParams p, const AttendWork wk) {
+  pdl_wait();
+  const int4 meta = wk.meta[blockIdx.x];
+  const int nsplit = meta.x;
+  if (nsplit == 0) return;
+  const Shape h = shape_of(p, NT);
+  int r0, n, kv;
+  bool bad;
+  seq_of(p, meta.y, &r0, &n, &kv, &bad);
+  const int t0 = meta.z * h.TT, g = meta.w;
+  constexpr int kDb = HD / 4, kR = 128 / kDb;  // dim blocks of a row, rows of a block
+  const int t = threadIdx.x, rr = t % kR, db = t / kR;
+  const int tiles = min(NT, (n - t0 + h.T - 1) / h.T);  // query tiles with tokens
+  for (int row = blockIdx.y * kR + rr; row < tiles * 128; row += gridDim.y * kR) {
+    const int x = row >> 7, tok = (row & 127) / h.group, head = (row & 127) - tok * h.group;
+    const int tk = t0 + x * h.T + tok;
+    if (tok >= h.T || tk >= n) continue;
+    float M = -INFINITY, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int q0 = 0; q0 < nsplit; q0 += 8) {
+      float2 ml[8];
+      float4 o[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int q = q0 + u, slot = 2 * (blockIdx.x + q) + (q == 0 ? 1 : 0);
+        const bool v = q < nsplit;
+        ml[u] = v ? __ldcg(wk.ml + (int64_t)slot * (NT * 128) + row) : make_float2(-INFINITY, 0.f);
+        o[u] = v ? __ldcg(part_at(wk, slot, row, db, NT * 128, HD)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float Mn = fmaxf(M, ml[u].x), base = Mn == -INFINITY ? 0.f : Mn;
+        const float f = exp2f(M - base), fu = exp2f(ml[u].x - base);
+        acc.x = acc.x * f + o[u].x * fu;
+        acc.y = acc.y * f + o[u].y * fu;
+        acc.z = acc.z * f + o[u].z * fu;
+        acc.w = acc.w * f + o[u].w * fu;
+        L = L * f + ml[u].y * fu;
+        M = Mn;
+      }
+    }
+    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+    const int64_t gr = r0 + tk;
+    const int gh = g * h.group + head;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + gr * p.out_stride + (int64_t)gh * HD + db * 4;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    if (p.lse && db == 0) p.lse[gr * p.nh + gh] = lse_of(M, L);
+  }
+}
+
+template <int HD, int NT>
+cudaError_t launch(const AttendParams& p, const AttendWork& w, int sms, cudaStream_t st) {
+  static std::atomic<unsigned long long> attr{0};
+  if (cudaError_t e = smem_attr_once(attend_tc_kernel<HD, NT>, Cfg<HD, NT>::kSmem, attr); e != cudaSuccess) return e;
+  attend_tc_kernel<HD, NT><<<sms, kThreads, Cfg<HD, NT>::kSmem, st>>>(p, w);
+  if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(sms, 8);
+  c.blockDim = dim3(128);
+  c.stream = st;
+  c.attrs = a;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, attend_combine_kernel<HD, NT>, p, w);
+}
+
+}  // namespace
+
+int64_t attend_tc_workspace(int head_dim, int sms) {
+  // per CTA two partial slots of 256 rows: O, (m, l); and the split unit's place
+  return (int64_t)sms * (2 * 256 * (head_dim * 4 + 8) + 16);
+}
+
+cudaError_t launch_attend_tc(const AttendParams& p, int head_dim, int max_new, void* workspace, int sms, cudaStream_t st) {
+  AttendWork w;
+  w.o = static_cast<float4*>(workspace);
+  w.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + (int64_t)sms * 2 * 256 * head_dim * 4);
+  w.meta = reinterpret_cast<int4*>(w.ml + (int64_t)sms * 2 * 256);
+  const int T = 128 / (p.nh / p.nkv);
+  const bool two = max_new > T;  // chunks longer than one tile: two tiles share every K/V slot
+  w.long_chunks = max_new > 4 * (two ? 2 * T : T);
+  if (head_dim == 128) return two ? launch<128, 2>(p, w, sms, st) : launch<128, 1>(p, w, sms, st);
+  return two ? launch<64, 2>(p, w, sms, st) : launch<64, 1>(p, w, sms, st);
+}
+
+}  // namespace dflash
