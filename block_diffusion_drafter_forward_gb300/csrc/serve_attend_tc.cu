@@ -379,6 +379,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         its[1].start(p, h, walk, 1);
         long long idle = 0;
         int s_out = 0;  // one tile: S of the segment issued so far
+        // A wait by parity is exact only while the phase before the awaited one is known complete, so
+        // a stream may not run ahead of the other by a ring.  One tile: S and P V go out in chunk
+        // order over both streams.  Two tiles: stream 1, which can skip segments, keeps within a
+        // ring of stream 0, which works in all of them.
+        int s_next = 0, pv_next = 0;  // chunks whose S / P V is out (two tiles: stream 0's)
+        auto s_turn = [&](int x, int kc) { return NT == 1 ? kc == s_next : x == 0 || s_next > kc - C::kNK; };
+        auto pv_turn = [&](int x, int kc) { return NT == 1 ? kc == pv_next : x == 0 || pv_next > kc - C::kNV; };
         while (its[0].valid || its[1].valid) {
           bool did = false;
 #pragma unroll
@@ -389,7 +396,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
             if (a.valid && pv[x]) {
               const int kc = a.kc0 + a.j, vb = kc % C::kNV;
               const int segs = NT == 2 ? a.act : a.seg;
-              if (give_up || (mbar_test_wait(&c.p_full[x], a.it & 1) && mbar_test_wait(&c.v_full[vb], (kc / C::kNV) & 1) &&
+              if (give_up || (pv_turn(x, kc) && mbar_test_wait(&c.p_full[x], a.it & 1) &&
+                              mbar_test_wait(&c.v_full[vb], (kc / C::kNV) & 1) &&
                               (!a.first(x) || segs == 0 || mbar_test_wait(&c.o_free[NT == 2 ? x : 0], (segs - 1) & 1)))) {
                 tc_fence_after();
                 if (!give_up) {
@@ -401,6 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
                 mma_commit(&c.o_done[x]);
                 mma_commit(&c.v_empty[vb]);
                 if (NT == 2 && x == 0 && !It<NT>::active(h, a.sg, 1)) mma_commit(&c.v_empty[vb]);
+                if (NT == 1 || x == 0) ++pv_next;
                 pv[x] = false;
                 a.step(p, h, x);
                 did = true;
@@ -408,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
             }
             if (a.valid && !pv[x]) {
               const int kc = a.kc0 + a.j, kb = kc % C::kNK;
-              if (give_up || (mbar_test_wait(&c.k_full[kb], (kc / C::kNK) & 1) &&
+              if (give_up || (s_turn(x, kc) && mbar_test_wait(&c.k_full[kb], (kc / C::kNK) & 1) &&
                               (!a.first(x) || mbar_test_wait(&c.q_full[NT == 2 ? x : 0], (NT == 2 ? a.act : a.seg) & 1)))) {
                 tc_fence_after();
                 if (!give_up) {
@@ -426,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
                   mma_commit(&c.q_empty);
                   s_out = 0;
                 }
+                if (NT == 1 || x == 0) ++s_next;
                 pv[x] = true;
                 did = true;
               }

@@ -203,6 +203,12 @@ ATTEND = [
     ([5000, 4000], [1, 1], 8, 1, 64, 1000, True),
     ([0], [1500], 16, 2, 128, 0, True),
     ([0], [1500], 16, 2, 64, 333, False),
+    # many chunks per CTA, so that both softmax streams go round the page rings many times
+    ([30000, 28001, 31977, 25000, 29999, 27000], [1, 1, 2, 1, 1, 3], 32, 4, 128, 0, True),
+    ([20000, 28001, 21977], [1, 30, 2], 32, 4, 64, 0, True),
+    # single tokens among prompts: units whose second query tile is empty, long and short
+    ([9000, 0, 7000, 20, 12000, 3, 8000], [1, 400, 1, 16, 1, 1, 90], 32, 4, 128, 0, True),
+    ([3000] * 40, [1, 40, 2, 1, 1, 300, 1, 17] * 5, 32, 4, 128, 0, True),
 ]
 
 
