@@ -23,11 +23,16 @@ inline cudaError_t smem_attr_once(K kern, int bytes, std::atomic<unsigned long l
   return e;
 }
 
-// SMs of the current device.
+// SMs of the current device (asked once per device).
 inline cudaError_t sm_count(int* sms) {
+  static std::atomic<int> known[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
+  return e;
 }
 
 }  // namespace dflash

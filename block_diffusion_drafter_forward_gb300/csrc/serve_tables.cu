@@ -147,29 +147,116 @@ struct AppendParams {
   const int32_t* slots;
   uint32_t* status;
   int n, nkv, num_pages;
+  bool wide;  // tiles start on 32 bytes
 };
 
-// Row r, head h, dims 8 c .. 8 c + 7 of K and V: one thread each.
+// A block takes kRows consecutive rows and kHeads heads; a warp one entry of one head at a time.
+// An entry is a run of eight rows whose slots fill one half page in order (the usual case: a
+// step's rows of a sequence follow one another), or a single row.  In the tile eight keys of a
+// half page lie side by side, so a run is written in whole sectors: K by lanes of 8 rows x 4
+// pieces (64 contiguous bytes read per row, 128 written), V transposed in registers (a lane
+// reads two dims of the eight rows and writes both dims' eight keys).  A single row writes V
+// element by element.  Bound by HBM, both ways once.
+constexpr int kRows = 16, kHeads = 4;
+
+template <typename T>
+__device__ __forceinline__ void copy16(T* d, const T* s) {
+  *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>(s);
+}
+// 32 bytes; one store where they are aligned (the pages' base and stride decide, `wide`)
+__device__ __forceinline__ void put32(void* d, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(d)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(d)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+__device__ __forceinline__ void put_keys(__nv_bfloat16* d, const uint32_t (&r)[8], bool wide) {  // dims x, x + 1 of 8 keys
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] = __byte_perm(r[2 * i], r[2 * i + 1], 0x5410);
+    w[4 + i] = __byte_perm(r[2 * i], r[2 * i + 1], 0x7632);
+  }
+  put32(d, w, wide);
+}
+__device__ __forceinline__ void put_keys(float* d, const uint2 (&r)[8], bool wide) {
+  const uint32_t x[8] = {r[0].x, r[1].x, r[2].x, r[3].x, r[4].x, r[5].x, r[6].x, r[7].x};
+  const uint32_t y[8] = {r[0].y, r[1].y, r[2].y, r[3].y, r[4].y, r[5].y, r[6].y, r[7].y};
+  put32(d, x, wide);
+  put32(d + 8, y, wide);
+}
+template <typename T> struct Two;  // two dims of a row
+template <> struct Two<__nv_bfloat16> { using type = uint32_t; };
+template <> struct Two<float> { using type = uint2; };
+
 template <typename T, int HD>
 __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
-  constexpr int kC = HD / 8;
-  const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int c = (int)(x % kC), h = (int)(x / kC % p.nkv);
-  const int64_t r = x / kC / p.nkv;
-  if (r >= p.n) return;
-  const int slot = p.slots[r];
-  if (slot < 0) return;
-  const int page = slot / kPage, j = slot % kPage;
-  if (page >= p.num_pages) {
-    if (p.status && c == 0 && h == 0) atomicOr(p.status, DFLASH_DEV_BAD_PAGE);
-    return;
+  using T2 = typename Two<T>::type;
+  __shared__ int s_slot[kRows + 14], s_entry[kRows], s_n;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int r0 = blockIdx.x * kRows;
+  if (t < kRows + 14) {  // the rows here, and seven on either side that a run may reach
+    const int r = r0 - 7 + t;
+    s_slot[t] = r >= 0 && r < p.n ? p.slots[r] : -1;
   }
-  T* tile = reinterpret_cast<T*>(p.pool + page * p.page_bytes) + (int64_t)h * 2 * kPage * HD;
-  const T* k = reinterpret_cast<const T*>(p.k + r * p.ks) + h * HD + c * 8;
-  const T* v = reinterpret_cast<const T*>(p.v + r * p.vs) + h * HD + c * 8;
-  for (int e = 0; e < 8; ++e) {
-    tile[k_in_tile(j, c * 8 + e, HD)] = k[e];
-    tile[kPage * HD + v_in_tile(j, c * 8 + e, HD)] = v[e];
+  if (t == 0) s_n = 0;
+  __syncthreads();
+  if (t < 32) {
+    bool take = false, run = false;
+    if (t < kRows) {
+      const int slot = s_slot[7 + t];
+      if (slot >= 0 && slot / kPage >= p.num_pages) {
+        if (p.status && blockIdx.y == 0) atomicOr(p.status, DFLASH_DEV_BAD_PAGE);
+      } else if (slot >= 0) {
+        const int o = slot & 7, first = 7 + t - o;  // a row's run is decided alike in every block that sees it
+        run = true;
+        for (int k = 0; k < 8; ++k) run = run && s_slot[first + k] == slot - o + k;
+        take = !run || o == 0;  // a run belongs to the block of its first row
+      }
+    }
+    const unsigned m = __ballot_sync(0xffffffffu, take);
+    if (take) s_entry[__popc(m & ((1u << t) - 1))] = t | (run ? 64 : 0);
+    if (t == 0) s_n = __popc(m);
+  }
+  __syncthreads();
+  const int h = blockIdx.y * kHeads + (warp & (kHeads - 1));
+  if (h >= p.nkv) return;
+  constexpr int kPer = 16 / sizeof(T);  // dims of a 16-byte piece
+  for (int e = warp / kHeads; e < s_n; e += 8 / kHeads) {
+    const int i = s_entry[e] & 63, slot = s_slot[7 + i];
+    const int64_t row = r0 + i;
+    T* tile = reinterpret_cast<T*>(p.pool + (slot / kPage) * p.page_bytes) + (int64_t)h * 2 * kPage * HD;
+    const int j = slot % kPage;
+    const T* k = reinterpret_cast<const T*>(p.k + row * p.ks) + h * HD;
+    const T* v = reinterpret_cast<const T*>(p.v + row * p.vs) + h * HD;
+    if (s_entry[e] & 64) {
+      const T* kr = reinterpret_cast<const T*>(reinterpret_cast<const uint8_t*>(k) + (lane & 7) * p.ks);
+      uint4 kk[HD / kPer / 4];
+      T2 vv[HD / 64][8];
+#pragma unroll
+      for (int c = 0; c < HD / kPer / 4; ++c) kk[c] = *reinterpret_cast<const uint4*>(kr + (c * 4 + (lane >> 3)) * kPer);
+#pragma unroll
+      for (int c = 0; c < HD / 64; ++c) {
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          vv[c][x] = *reinterpret_cast<const T2*>(
+              reinterpret_cast<const T*>(reinterpret_cast<const uint8_t*>(v) + x * p.vs) + c * 64 + 2 * lane);
+      }
+#pragma unroll
+      for (int c = 0; c < HD / kPer / 4; ++c)
+        *reinterpret_cast<uint4*>(tile + k_in_tile(j + (lane & 7), (c * 4 + (lane >> 3)) * kPer, HD)) = kk[c];
+#pragma unroll
+      for (int c = 0; c < HD / 64; ++c) put_keys(tile + kPage * HD + v_in_tile(j, c * 64 + 2 * lane, HD), vv[c], p.wide);
+    } else {
+#pragma unroll
+      for (int c = lane; c < HD / kPer; c += 32) copy16(tile + k_in_tile(j, c * kPer, HD), k + c * kPer);
+#pragma unroll
+      for (int d = lane; d < HD; d += 32) tile[kPage * HD + v_in_tile(j, d, HD)] = v[d];
+    }
   }
 }
 
@@ -224,14 +311,14 @@ extern "C" int dflash_append_kv(const dflash_kv_pages* kv, const void* k, int64_
   if (k_stride < row || v_stride < row || (k_stride * es) % 16 || (v_stride * es) % 16 || !aligned16(k) || !aligned16(v))
     return call_error(DFLASH_EINVAL, "append_kv: rows below n_kv_heads * head_dim, or k, v or a stride not whole 16 bytes");
   AppendParams p{static_cast<const uint8_t*>(k), static_cast<const uint8_t*>(v), k_stride * es, v_stride * es,
-                 static_cast<uint8_t*>(kv->pool), kv->page_stride * es, slots, kv->status, n, kv->n_kv_heads, kv->num_pages};
-  const int64_t items = (int64_t)n * row / 8, blocks = (items + 255) / 256;
-  if (blocks > 0x7fffffff) return call_error(DFLASH_ECAPACITY, "append_kv: too many rows for one call");
+                 static_cast<uint8_t*>(kv->pool), kv->page_stride * es, slots, kv->status, n, kv->n_kv_heads, kv->num_pages,
+                 reinterpret_cast<uintptr_t>(kv->pool) % 32 == 0 && (kv->page_stride * es) % 32 == 0};
+  const dim3 grid((unsigned)((n + (int64_t)kRows - 1) / kRows), (unsigned)((kv->n_kv_heads + kHeads - 1) / kHeads));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool f32 = kv->dtype == DFLASH_F32, w = kv->head_dim == 128;
   auto kern = f32 ? (w ? append_kernel<float, 128> : append_kernel<float, 64>)
                   : (w ? append_kernel<__nv_bfloat16, 128> : append_kernel<__nv_bfloat16, 64>);
-  kern<<<(unsigned)blocks, 256, 0, st>>>(p);
+  kern<<<grid, 256, 0, st>>>(p);
   if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return call_error(DFLASH_ECUDA, "append_kv", e);
   return DFLASH_OK;
 }

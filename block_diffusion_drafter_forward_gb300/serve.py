@@ -62,21 +62,6 @@ def serve_status(device=None, stream: Optional[torch.cuda.Stream] = None) -> int
     return bits
 
 
-def _want(t, name: str, dtype: torch.dtype, shape: Tuple[int, ...], device: torch.device) -> int:
-    """The address of a contiguous `dtype` tensor of exactly `shape` on `device`; raises otherwise."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        if t.device != device:
-            raise ValueError(f"{name}: expected a tensor on {device}, got one on {t.device}")
-        if t.dtype is not dtype:
-            raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-        raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr()
-
-
 def _first(t, name: str, dim: int, dtypes=(_I32,)) -> torch.Tensor:
     """The tensor whose device and sizes the others of a call are held to."""
     if not isinstance(t, torch.Tensor):
@@ -90,8 +75,8 @@ def _first(t, name: str, dim: int, dtypes=(_I32,)) -> torch.Tensor:
     return t
 
 
-def _rows_of(t, name: str, dtype: torch.dtype, shape: Tuple[int, ...], device: torch.device) -> Tuple[int, int]:
-    """(address, elements between rows) of a [rows, heads, dim] tensor whose heads are contiguous."""
+def _refuse(t, name: str, dtype: torch.dtype, shape: Tuple[int, ...], device: torch.device) -> None:
+    """Raises for what keeps `t` from being a `dtype` tensor of `shape` on `device` with its rows contiguous."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.device != device:
@@ -100,35 +85,87 @@ def _rows_of(t, name: str, dtype: torch.dtype, shape: Tuple[int, ...], device: t
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    st = t.stride()
-    row = shape[1] * shape[2]
-    if t.numel() and ((shape[2] > 1 and st[2] != 1) or (shape[1] > 1 and st[1] != shape[2]) or (shape[0] > 1 and st[0] < row)):
-        raise ValueError(f"{name}: the heads of a row must be contiguous and rows must not overlap, got strides {st}")
-    return t.data_ptr(), (st[0] if shape[0] > 1 else row)
+    raise ValueError(f"{name}: must be contiguous")
+
+
+def _addresses(device: torch.device, *wanted) -> list:
+    """The addresses of contiguous tensors on `device`, given as (tensor, name, dtype, shape); raises for
+    the first that is something else.  (A loop of plain comparisons: the smallest calls cost little more.)"""
+    i = device.index if device.type == "cuda" else -1  # get_device() of a host tensor is -1
+    out = []
+    for t, name, dtype, shape in wanted:
+        try:
+            ok = t.dtype is dtype and t.get_device() == i and t.shape == shape and t.is_contiguous()
+        except AttributeError:
+            ok = False
+        if not ok:
+            _refuse(t, name, dtype, shape, device)
+        out.append(t.data_ptr())
+    return out
+
+
+def _rows_of(t, name: str, dtype: torch.dtype, shape: Tuple[int, ...], device: torch.device) -> Tuple[int, int]:
+    """(address, elements between rows) of a [rows, heads, dim] tensor whose heads are contiguous."""
+    i = device.index if device.type == "cuda" else -1
+    try:
+        ok = t.dtype is dtype and t.get_device() == i and t.shape == shape
+    except AttributeError:
+        ok = False
+    if not ok:
+        _refuse(t, name, dtype, shape, device)
+    rows, heads, dim = shape
+    s0, s1, s2 = t.stride()
+    if s2 == 1 and s1 == dim and (s0 >= heads * dim or rows <= 1):
+        return t.data_ptr(), (s0 if rows > 1 else heads * dim)
+    # sizes of one leave a stride without meaning
+    if t.numel() and ((dim > 1 and s2 != 1) or (heads > 1 and s1 != dim) or (rows > 1 and s0 < heads * dim)):
+        raise ValueError(f"{name}: the heads of a row must be contiguous and rows must not overlap, got strides {(s0, s1, s2)}")
+    return t.data_ptr(), (s0 if rows > 1 else heads * dim)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 class _On:
-    """The call's device made current, and the raw stream to launch on."""
+    """Makes `device` and `stream` (None: the device's current one) current for the calls inside."""
     __slots__ = ("device", "stream", "ctx")
 
     def __init__(self, device: torch.device, stream: Optional[torch.cuda.Stream]):
-        self.device, self.stream, self.ctx = device, stream, None
+        self.device, self.stream = device, stream
 
     def __enter__(self) -> int:
         if self.stream is not None:
             if self.stream.device != self.device:
                 raise ValueError(f"stream: expected a stream of {self.device}, got one of {self.stream.device}")
             self.ctx = torch.cuda.stream(self.stream)  # also makes its device current
-            self.ctx.__enter__()
-            return self.stream.cuda_stream
-        if torch.cuda.current_device() != self.device.index:
+        else:
             self.ctx = torch.cuda.device(self.device)
-            self.ctx.__enter__()
+        self.ctx.__enter__()
         return torch.cuda.current_stream(self.device).cuda_stream
 
     def __exit__(self, *a) -> None:
-        if self.ctx is not None:
-            self.ctx.__exit__(*a)
+        self.ctx.__exit__(*a)
+
+
+class _Here:
+    """The same where the device is current and no stream is given: nothing to change."""
+    __slots__ = ("raw",)
+
+    def __init__(self, raw: int):
+        self.raw = raw
+
+    def __enter__(self) -> int:
+        return self.raw
+
+    def __exit__(self, *a) -> None:
+        pass
+
+
+def _on(device: torch.device, stream: Optional[torch.cuda.Stream]):
+    i = device.index
+    if stream is None and torch.cuda.current_device() == i:
+        return _Here(_raw_stream(i) if _raw_stream else torch.cuda.current_stream(device).cuda_stream)
+    return _On(device, stream)
 
 
 def extend_tables(ctx_lens: torch.Tensor, new_rows: torch.Tensor, page_tables: torch.Tensor, free_pages: torch.Tensor,
@@ -138,28 +175,27 @@ def extend_tables(ctx_lens: torch.Tensor, new_rows: torch.Tensor, page_tables: t
     from position free_begin [1] on.  Sequences are served in order while pages and max_rows last.
     `out`: a RowPlan to write into; its kv_lens may be ctx_lens and its free_end free_begin."""
     dev = _first(ctx_lens, "ctx_lens", 1).device
-    nb = ctx_lens.shape[0]
-    a_ctx = _want(ctx_lens, "ctx_lens", _I32, (nb,), dev)
-    a_new = _want(new_rows, "new_rows", _I32, (nb,), dev)
+    nb, max_rows = ctx_lens.shape[0], int(max_rows)
     mpps = _first(page_tables, "page_tables", 2).shape[1]
-    a_pt = _want(page_tables, "page_tables", _I32, (nb, mpps), dev)
     n_free = _first(free_pages, "free_pages", 1).shape[0]
-    a_free = _want(free_pages, "free_pages", _I32, (n_free,), dev)
-    a_begin = _want(free_begin, "free_begin", _I32, (1,), dev)
-    max_rows = int(max_rows)
     if max_rows < 0:
         raise ValueError("max_rows must be >= 0")
-    with _On(dev, stream) as st:
+    one, seqs, rows = (1,), (nb,), (max_rows,)
+    with _on(dev, stream) as st:
         if out is None:
             def e(n):
                 return torch.empty(n, dtype=_I32, device=dev)
             out = RowPlan(e(nb), e(nb + 1), e(max_rows), e(max_rows), e(max_rows), e(1))
-        rows = (max_rows,)
-        L.dflash_extend_tables(
-            a_ctx, a_new, nb, a_pt, mpps, a_free or a_pt, n_free, a_begin, _want(out.free_end, "out.free_end", _I32, (1,), dev),
-            _want(out.kv_lens, "out.kv_lens", _I32, (nb,), dev), _want(out.row_starts, "out.row_starts", _I32, (nb + 1,), dev),
-            _want(out.row_seq, "out.row_seq", _I32, rows, dev) or a_pt, _want(out.row_index, "out.row_index", _I32, rows, dev) or a_pt,
-            _want(out.slots, "out.slots", _I32, rows, dev) or a_pt, max_rows, _status_word(dev).data_ptr(), st)
+        kv_lens, row_starts, row_seq, row_index, slots, free_end = out
+        a_ctx, a_new, a_pt, a_free, a_begin, a_end, a_kv, a_rs, a_seq, a_idx, a_slots = _addresses(
+            dev, (ctx_lens, "ctx_lens", _I32, seqs), (new_rows, "new_rows", _I32, seqs),
+            (page_tables, "page_tables", _I32, (nb, mpps)), (free_pages, "free_pages", _I32, (n_free,)),
+            (free_begin, "free_begin", _I32, one), (free_end, "out.free_end", _I32, one),
+            (kv_lens, "out.kv_lens", _I32, seqs), (row_starts, "out.row_starts", _I32, (nb + 1,)),
+            (row_seq, "out.row_seq", _I32, rows), (row_index, "out.row_index", _I32, rows), (slots, "out.slots", _I32, rows))
+        # an empty tensor has no address, and the entry takes none that is null
+        L.dflash_extend_tables(a_ctx, a_new, nb, a_pt, mpps, a_free or a_pt, n_free, a_begin, a_end, a_kv, a_rs, a_seq or a_pt,
+                               a_idx or a_pt, a_slots or a_pt, max_rows, _status_word(dev).data_ptr(), st)
     return out
 
 
@@ -198,11 +234,11 @@ class PagedKV:
         pool = self.pool
         dev = pool.device
         n = _first(slots, "slots", 1).shape[0]
-        a_s = _want(slots, "slots", _I32, (n,), dev)
+        a_s, = _addresses(dev, (slots, "slots", _I32, (n,)))
         shape = (n, pool.shape[1], self.head_dim)
         a_k, ks = _rows_of(k, "k", pool.dtype, shape, dev)
         a_v, vs = _rows_of(v, "v", pool.dtype, shape, dev)
-        with _On(dev, stream) as st:
+        with _on(dev, stream) as st:
             L.dflash_append_kv(self._c, a_k, ks, a_v, vs, a_s, n, st)
         return pool
 
@@ -221,11 +257,10 @@ class PagedKV:
         shape = (n, nh, hd)
         a_q, qs = _rows_of(q, "q", pool.dtype, shape, dev)
         nb, mpps = _first(page_tables, "page_tables", 2).shape
-        a_pt = _want(page_tables, "page_tables", _I32, (nb, mpps), dev)
-        a_kv = _want(kv_lens, "kv_lens", _I32, (nb,), dev)
-        a_rs = _want(row_starts, "row_starts", _I32, (nb + 1,), dev)
-        a_lse = 0 if lse is None else _want(lse, "lse", _F32, (n, nh), dev)
-        with _On(dev, stream) as st:
+        a_pt, a_kv, a_rs = _addresses(dev, (page_tables, "page_tables", _I32, (nb, mpps)), (kv_lens, "kv_lens", _I32, (nb,)),
+                                      (row_starts, "row_starts", _I32, (nb + 1,)))
+        a_lse = 0 if lse is None else _addresses(dev, (lse, "lse", _F32, (n, nh)))[0]
+        with _on(dev, stream) as st:
             if out is None:
                 out = torch.zeros(shape, dtype=pool.dtype, device=dev)
             a_out, os_ = _rows_of(out, "out", pool.dtype, shape, dev)
@@ -249,14 +284,16 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Te
     st0, st1 = logits.stride()
     if (V > 1 and st1 != 1) or (rows > 1 and st0 < V):
         raise ValueError(f"logits: a row must be contiguous and rows must not overlap, got strides {(st0, st1)}")
-    a_u = _want(u, "u", _F32, (rows,), dev)
-    opt = [0 if t is None else _want(t, name, dt, (rows,), dev)
-           for t, name, dt in ((temperature, "temperature", _F32), (top_k, "top_k", _I32), (top_p, "top_p", _F32),
-                               (min_p, "min_p", _F32), (probs, "probs", _F32))]
-    with _On(dev, stream) as st:
+    col = (rows,)
+    a_u, = _addresses(dev, (u, "u", _F32, col))
+    a_temp, a_k, a_p, a_min, a_probs = [
+        0 if w[0] is None else _addresses(dev, w)[0]
+        for w in ((temperature, "temperature", _F32, col), (top_k, "top_k", _I32, col), (top_p, "top_p", _F32, col),
+                  (min_p, "min_p", _F32, col), (probs, "probs", _F32, col))]
+    with _on(dev, stream) as st:
         if tokens is None:
             tokens = torch.empty(rows, dtype=_I32, device=dev)
-        a_t = _want(tokens, "tokens", _I32, (rows,), dev)
+        a_t, = _addresses(dev, (tokens, "tokens", _I32, col))
         L.dflash_sample(logits.data_ptr(), st0 if rows > 1 else V, L.DFLASH_BF16 if logits.dtype is _BF16 else L.DFLASH_F32,
-                        rows, V, a_u, opt[0], opt[1], opt[2], opt[3], a_t, opt[4], st)
+                        rows, V, a_u, a_temp, a_k, a_p, a_min, a_t, a_probs, st)
     return tokens if probs is None else (tokens, probs)

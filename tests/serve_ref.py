@@ -10,7 +10,7 @@ PAGE = 16
 
 def tables(ctx, new, table, free, begin, max_rows):
     """(table, kv_lens, row_starts, row_seq, row_index, slots, free_end) as int lists/arrays."""
-    table = np.array(table, dtype=np.int64)
+    table = np.array(table.tolist() if isinstance(table, torch.Tensor) else table, dtype=np.int64)
     nb, mpps = table.shape
     seq, idx, slot, kv, starts = [], [], [], [], [0]
     at, rows, room = begin, 0, True

@@ -125,6 +125,26 @@ def test_append(dtype, nkv, hd, slots):
     assert bool((wide[:, nkv] == 0).all()) and status() == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_pages_on_16_bytes_only(dtype):
+    """A pool whose base and page stride are multiples of 16 bytes, not of 32: append, then attention."""
+    from block_diffusion_drafter_forward_gb300 import PagedKV
+    nkv, hd, P = 2, 128, 5
+    off = 128 // torch.finfo(dtype).bits
+    flat = torch.zeros(P * (32 * nkv * hd + off) + off, dtype=dtype, device="cuda")
+    pool = flat[off:].as_strided((P, nkv, 2, 16 * hd), (32 * nkv * hd + off, 32 * hd, 16 * hd, 1), flat[off:].storage_offset())
+    assert pool.data_ptr() % 32 == 16
+    k, v = torch.randn(2, 70, nkv, hd, device="cuda").to(dtype)
+    table = torch.tensor([[3, 1, 4, 0, 2]], dtype=torch.int32)
+    slots = [int(table[0, i // 16]) * 16 + i % 16 for i in range(70)]
+    kv = PagedKV(pool)
+    kv.append(k, v, i32(slots))
+    assert torch.equal(pool.cpu(), R.put(torch.zeros(P, nkv, 2, 16 * hd, dtype=dtype), k.cpu(), v.cpu(), slots))
+    q = torch.randn(7, 8, hd, device="cuda").to(dtype)
+    out, lse = kv.attend(q, table.cuda(), i32([70]), i32([0, 7]), 7, lse=torch.empty(7, 8, device="cuda"))
+    check_attend(out, lse, R.attend(q, pool, table.cuda(), [70], [0, 7], True, 0, 1 / math.sqrt(hd)), slice(0, 7), hd)
+
+
 def test_append_reports_slots_past_the_pages():
     from block_diffusion_drafter_forward_gb300 import PagedKV, _lib
     status()

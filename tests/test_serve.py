@@ -123,7 +123,7 @@ def test_pages_struct_matches_the_c_compiler(tmp_path):
 
 def test_python_calls_refuse_host_tensors_and_wrong_shapes():
     from block_diffusion_drafter_forward_gb300 import PagedKV, extend_tables, sample
-    from block_diffusion_drafter_forward_gb300.serve import _rows_of, _want
+    from block_diffusion_drafter_forward_gb300.serve import _addresses, _rows_of
     z = torch.zeros(2, dtype=torch.int32)
     with pytest.raises(ValueError, match="ctx_lens: expected a cuda tensor"):
         extend_tables(z, z, z.view(2, 1), z, z[:1], 4)
@@ -134,9 +134,12 @@ def test_python_calls_refuse_host_tensors_and_wrong_shapes():
     with pytest.raises(TypeError, match="logits"):
         sample([1.0], torch.zeros(2))
     cpu = torch.device("cpu")
+    assert _addresses(cpu, (z, "z", torch.int32, (2,))) == [z.data_ptr()]
+    with pytest.raises(TypeError, match="t: expected"):
+        _addresses(cpu, ([1, 2], "t", torch.int32, (2,)))
     for t, msg in ((z.float(), "expected torch.int32"), (z[:1], "expected shape"), (torch.zeros(4, dtype=torch.int32)[::2], "contiguous")):
         with pytest.raises(ValueError, match=msg):
-            _want(t, "t", torch.int32, (2,), cpu)
+            _addresses(cpu, (t, "t", torch.int32, (2,)))
     x = torch.zeros(6, 4, 8)
     assert _rows_of(x[:, 1:3], "x", torch.float32, (6, 2, 8), cpu)[1] == 32
     assert _rows_of(x[:1], "x", torch.float32, (1, 4, 8), cpu)[1] == 32
