@@ -1,45 +1,47 @@
 // One token per row of logits by temperature, top-k, top-p and min-p (dflash_sample).
 //
-// A cluster of C CTAs owns a row: each keeps its slice of the row in shared memory, so the logits
-// are read from HBM once whatever the number of passes.  In falling order of the logits every
-// filter keeps a prefix, and the prefix is short in most rows:
-//   1. largest logit m (and its lowest index: the answer where T == 0);
-//   2. a histogram of t = (m - x) log2(e) / T in 1024 equal bins of [0, 20) (of [0, 40) if that
-//      does not reach far enough) and, for top-p alone, the row's mass: the counts give the bin in
-//      which top-k ends, the bounds on a bin's mass (2 %) the last bin that top-p can reach;
-//   3. the logits up to that bin, usually a few dozen, go to the first CTA, which sorts them, sums
-//      their weights in fixed point and finds the kept prefix and the token.
-// Rows whose prefix does not fit in the list (flat ones) find the border by bisection on the
-// logits' order-preserving keys; those, and rows without top-k and top-p, then sum the kept mass of
-// every warp's segment in index order, and the warp whose segment holds u * total walks it.  Passes
-// skip vectors whose largest logit is below what the pass looks at.
+// In falling order of the logits every filter keeps a prefix, and the prefix is short in most
+// rows: so the row is read once, and only the logits near its maximum are held.
+//   stream_kernel: a CTA (or a cluster of 8, when rows are few) streams a row through a ring in
+//     shared memory, with the running maximum m.  Logits from a floor on, which a look at the row's
+//     first blocks sets, go to a list; top-p alone also sums the mass of the others.  At the end a
+//     histogram of the list (counts, masses) over t = (m - x) log2(e) / T says how far the prefix
+//     reaches; that part, usually a few dozen logits, is sorted, and its weights' running sums give
+//     the kept prefix and the token.  Rows without a short prefix by right (temperature alone)
+//     sum every warp's stretches of the row in index order, rescaled as m grows; the stretch that
+//     holds u * total is read again.  Vectors whose logits are all far below m (t > 12) go in fp32,
+//     with a bound on their error: where the token could depend on it, or the probability's last
+//     bit (flat rows; a few in a hundred others), the row is streamed once more with exact weights.
+//   select_kernel: rows whose prefix did not fit in the list (flat ones) have their slice in the
+//     shared memory of a cluster of 8 and find (tau, n) - the lowest kept logit, and how many of
+//     those equal to it stay - by histograms over the logits' order-preserving keys, 10 bits a
+//     round, with exact counts (top-k) and masses (top-p); then sum stretches as above.
+// Bound by HBM: one read of the logits (the finishing phases of some CTAs overlap the streaming of
+// others; three CTAs per SM with 32 KB of copies in flight each).
+//
 // The token is a whole number that a sum's last bit can change, so weights are pairs of floats
 // (exp2 by a 128-entry table and a short polynomial on the compensated argument, about 2^-41)
-// and sums are compensated: in plain fp32 one row in a few hundred would differ.  Weights below
-// 2^-20 enter top-p's total mass in plain fp32 (they hold a small part of it).
+// and masses are compensated or whole numbers: in plain fp32 one row in a few hundred would
+// differ.  Only the mass past the list's range enters top-p's total in plain fp32 (a small part of it).
 #include <cooperative_groups.h>
 #include <float.h>
 #include <string.h>
 
-#include <cmath>
-
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "launch_util.cuh"
 #include "serve.cuh"
+#include "tc_common.cuh"
 
 namespace dflash {
 namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 1024;
-constexpr int kMaxC = 8;
-constexpr int kList = 2048;                  // logits that the sorted list holds
 constexpr float kCut = 40.f;                 // weights below 2^-40 are 0
-constexpr float kNear = 20.f;                // the histogram's first range of t
-constexpr int kSliceBytes = 184 * 1024;      // shared memory for a CTA's slice
+constexpr int kRetry = -2;                   // a row that stream_kernel leaves to select_kernel
 
 struct SampleParams {
   const void* logits;
@@ -49,7 +51,7 @@ struct SampleParams {
   const int32_t* top_k;
   int32_t* tokens;
   float* probs;
-  int per;  // elements of a slice (a multiple of 8)
+  int per;  // positions of a CTA's slice (a multiple of 8)
   float2 table[128];  // 2^(j / 128) as pairs
 };
 
@@ -63,6 +65,11 @@ __device__ __forceinline__ F2 add(F2 a, F2 b) {
   const float e = (a.h - (s - bb)) + (b.h - bb) + (a.l + b.l);
   const float h = s + e;
   return {h, e - (h - s)};
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  const float p = a.h * b.h, e = fmaf(a.h, b.h, -p) + fmaf(a.h, b.l, a.l * b.h);
+  const float h = p + e;
+  return {h, e - (h - p)};
 }
 __device__ __forceinline__ bool below(F2 a, float b) { return a.h < b || (a.h == b && a.l < 0.f); }
 // Masses as whole numbers of 2^-B: sums and comparisons are exact and cost integer operations
@@ -144,29 +151,6 @@ __device__ __forceinline__ F2 weight(const Scale& s, float x) {
   return {hh * sc, (lo - (hh - h)) * sc};
 }
 
-// ------------------------------------------------------------------ shared state
-struct Slot {  // what a CTA tells the others, double-buffered by exchange
-  unsigned long long d[2];
-  float f;
-  unsigned u[4];
-};
-struct Shared {
-  float2 table[128];
-  unsigned hist[kBins];      // the slice's histogram
-  Slot slot[2];
-  unsigned long long wsum[kWarps];  // kept mass of each warp's segment
-  unsigned wties[kWarps];    // logits equal to tau in it
-  unsigned long long all_sum[kMaxC * kWarps];
-  unsigned all_ties[kMaxC * kWarps];
-  float red_f[2][kWarps];
-  unsigned red_u[4][kWarps];
-  unsigned long long red_l[2][kWarps];
-  int pick[4];
-  unsigned n_list;
-  unsigned index[kList];               // of the sorted list: vocabulary index
-  unsigned long long list[kList];      // (~key, index), then fixed-point weights
-};
-
 // 16 bytes of logits: their largest (NaN counts as nothing), and the values.
 template <typename T>
 struct Vec;
@@ -201,719 +185,990 @@ struct Vec<float> {
   }
 };
 
+
+__device__ __forceinline__ Scale scale_of(float m, float T, const float2* table) {
+  // log2(e) / T: the quotient, and the exact remainder's quotient
+  constexpr float kE = 1.44269502162933349609375f, kEl = 1.92596299e-8f;  // log2(e)
+  Scale s;
+  s.m = m;
+  s.c_hi = kE / T;
+  s.c_lo = isinf(s.c_hi) ? 0.f : (fmaf(-s.c_hi, T, kE) + kEl) / T;
+  s.table = table;
+  return s;
+}
+// a logit from which on t can be below r (rounding allowed for)
+__device__ __forceinline__ float reach(const Scale& s, float r) {
+  return isinf(s.c_hi) || isinf(s.m) ? s.m : s.m - r / s.c_hi * 1.00001f - fabsf(s.m) * 1e-6f;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float clean(float x) { return x == x ? x + 0.f : -INFINITY; }  // NaN: -inf, -0: +0
+
+struct Row {  // a row's settings
+  float T, p, lo, u;
+  int k;
+  bool use_k, use_p;
+};
+__device__ __forceinline__ Row row_of(const SampleParams& q, int row) {
+  Row r;
+  r.T = q.temperature ? q.temperature[row] : 1.f;
+  r.k = q.top_k ? q.top_k[row] : 0;
+  r.p = q.top_p ? q.top_p[row] : 1.f;
+  r.lo = q.min_p ? q.min_p[row] : 0.f;
+  const float u = q.u[row];
+  r.u = u > 0.f ? u : 0.f;
+  r.use_k = r.k > 0 && r.k < q.vocab;
+  r.use_p = r.p < 1.f;
+  r.p = fmaxf(r.p, 0.f);
+  return r;
+}
+
+// A CTA's part of a row.  Positions count from the 16-byte boundary at or before the row's first
+// logit, so that vectors are aligned whatever the row's address; position i of the slice is logit
+// first + i, and those outside [begin, count) hold -inf.
+template <typename T>
+struct Slice {
+  const T* src;
+  int first, begin, count;
+  __device__ Slice(const SampleParams& q, int row, int rank) {
+    src = static_cast<const T*>(q.logits) + (int64_t)row * q.stride;
+    const int skip = (int)(reinterpret_cast<uintptr_t>(src) & 15) / (int)sizeof(T);
+    first = rank * q.per - skip;
+    begin = max(0, -first);
+    count = max(0, min(q.per, q.vocab - first));
+  }
+  __device__ bool whole(int i) const { return i >= begin && i + Vec<T>::N <= count; }
+  __device__ const T* at(int i) const { return src + (first + i); }
+  __device__ uint4 edge(int i) const {  // a vector at the row's ends
+    uint4 r = make_uint4(Vec<T>::kPad, Vec<T>::kPad, Vec<T>::kPad, Vec<T>::kPad);
+#pragma unroll
+    for (int e = 0; e < Vec<T>::N; ++e)
+      if (i + e >= begin && i + e < count) reinterpret_cast<T*>(&r)[e] = src[first + i + e];
+    return r;
+  }
+};
+
+// Walks a stretch of a row in order for the first position whose running mass exceeds `target`
+// (else the last with any mass).  One warp; step(i, w) gives the kept weights w of positions
+// i + lane * N ..; `before`: the mass ahead of the stretch; *passed: whether the target was.
+template <int N, typename F>
+__device__ __forceinline__ void walk(int n, unsigned long long before, unsigned long long target, F&& step, int* token,
+                                     F2* weight_out, bool* passed = nullptr) {
+  const int lane = threadIdx.x & 31;
+  *token = -1;
+  *weight_out = F2{0.f, 0.f};
+  if (passed) *passed = true;
+  for (int i0 = 0; i0 < n; i0 += 32 * N) {
+    F2 w[N];
+    step(i0, w);
+    unsigned long long f[N], mine = 0;
+#pragma unroll
+    for (int e = 0; e < N; ++e) f[e] = fix<43>(w[e]), mine += f[e];
+    unsigned long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    unsigned long long cum = before + (inc - mine);
+    F2 my_w = {0.f, 0.f};
+    int my = -1;
+    bool hit = false;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      cum += f[e];
+      if (f[e] > 0 && !hit) {
+        my = i0 + lane * N + e;
+        my_w = w[e];
+        hit = cum > target;
+      }
+    }
+    const unsigned hits = __ballot_sync(0xffffffffu, hit), any = __ballot_sync(0xffffffffu, my >= 0);
+    if (any) {
+      const int from = hits ? __ffs(hits) - 1 : 31 - __clz(any);
+      *token = __shfl_sync(0xffffffffu, my, from);
+      *weight_out = F2{__shfl_sync(0xffffffffu, my_w.h, from), __shfl_sync(0xffffffffu, my_w.l, from)};
+    }
+    if (hits) return;
+    before += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  if (passed) *passed = false;
+}
+
+__device__ __forceinline__ float prob_of(F2 w, unsigned long long total) {  // total in units of 2^-43
+  return (float)(((double)w.h + (double)w.l) / ((double)total * 0x1p-43));
+}
+__device__ __forceinline__ void put(const SampleParams& q, int row, int token, float prob) {
+  q.tokens[row] = token;
+  if (q.probs) q.probs[row] = prob;
+}
+
+// ------------------------------------------------------------------ stream_kernel
+constexpr int kST = 256, kSW = kST / 32;     // threads, warps
+constexpr int kStages = 3, kVec = 4;         // ring: blocks in flight; vectors of a thread in a block
+constexpr int kStageBytes = kST * kVec * 16; // 16 KB
+constexpr int kList = 2048;                  // logits that a list holds
+constexpr int kAim = 1536;                   // and that the floor may aim at
+constexpr int kBins = 256;                   // histogram of the list
+constexpr int kLook = 64;                    // bins of the look at the first blocks
+constexpr float kFar = 32.f;                 // their range of t, below the maximum found there
+// Far masses in fp32: a bound on their relative error (x - m rounded: t 2^-25 ln 2 < 8.3e-7; ex2
+// 2^-22; the correction's and the tree's roundings 5 2^-24), and the error a probability may carry
+constexpr float kNear = 12.f;
+constexpr float kFastError = 1.4e-6f, kProbError = 8e-8f;
+constexpr int kStreamSmem = kStages * kStageBytes + kList * 8;
+
+struct Stretch {  // mass of a warp's part of a block, relative to ref; `far`: what of it came in fp32
+  float h, l, far, ref;
+};
+
+struct StreamShared {
+  float2 table[128];
+  unsigned count[kBins];
+  unsigned long long mass[kBins];
+  unsigned long long red_l[kSW], rest, best, before, part, far, far_part;
+  unsigned red_u[kSW];
+  unsigned m_key, n_list, n_final, bad;
+  float floor;
+  int pick[2];
+};
+
 template <typename T, int C>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) {
-  constexpr int N = Vec<T>::N;
+__global__ void __launch_bounds__(kST, 3) stream_kernel(const SampleParams q) {
+  constexpr int N = Vec<T>::N, kBlock = kST * kVec * N, kWarpPart = kVec * 32 * N;
   extern __shared__ __align__(16) uint8_t smem[];
-  T* xs = reinterpret_cast<T*>(smem);
-  __shared__ Shared sh;
+  uint4* ring = reinterpret_cast<uint4*>(smem);
+  unsigned long long* list = reinterpret_cast<unsigned long long*>(smem + kStages * kStageBytes);
+  Stretch* stretch = reinterpret_cast<Stretch*>(list);
+  // once the row is through, the ring holds: the row's list, and places by index
+  unsigned long long* final_list = reinterpret_cast<unsigned long long*>(smem);
+  unsigned* index = reinterpret_cast<unsigned*>(smem + kList * 8);
+  unsigned* by = index + kList;
+  __shared__ StreamShared sh;
   cg::cluster_group cl = cg::this_cluster();
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int rank = C > 1 ? (int)cl.block_rank() : 0, row = blockIdx.x / C;
-  int phase = 0;
   auto sync_row = [&] {
     if (C > 1) cl.sync(); else __syncthreads();
   };
   auto peer = [&](auto* ptr, int r) { return C > 1 ? cl.map_shared_rank(ptr, r) : ptr; };
 
-  // ---- the slice.  Positions count from the 16-byte boundary at or before the row's first logit
-  // (`skip` of them lie before it), so that vectors are aligned whatever the row's address;
-  // position i of this CTA's slice is logit first + i.  Positions outside the row hold -inf.
-  const T* src = static_cast<const T*>(p.logits) + (int64_t)row * p.stride;
-  const int skip = (int)(reinterpret_cast<uintptr_t>(src) & 15) / (int)sizeof(T);
-  const int first = rank * p.per - skip;
-  const int count = max(0, min(p.per, p.vocab - first)), begin = max(0, -first);
-  const int padded = (count + N * 32 * kWarps - 1) / (N * 32 * kWarps) * (N * 32 * kWarps);
-  float best = -INFINITY;
-#pragma unroll 4
-  for (int i = t * N; i < padded; i += kThreads * N) {
-    uint4 r;
-    if (i >= begin && i + N <= count) {
-      r = __ldcs(reinterpret_cast<const uint4*>(src + first + i));
-    } else {  // the row's ends
-      r = make_uint4(Vec<T>::kPad, Vec<T>::kPad, Vec<T>::kPad, Vec<T>::kPad);
+  const Slice<T> sl(q, row, rank);
+  const int blocks = (sl.count + kBlock - 1) / kBlock;
+  auto pos_of = [&](int b, int v) { return b * kBlock + warp * kWarpPart + (v * 32 + lane) * N; };
+  // a thread copies and reads back its own vectors, so the ring needs no barrier
+  auto issue = [&](int b) {
+    if (b < blocks) {
 #pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (i + e >= begin && i + e < count) reinterpret_cast<T*>(&r)[e] = src[first + i + e];
+      for (int v = 0; v < kVec; ++v) {
+        const int i = pos_of(b, v);
+        uint4* d = ring + (b % kStages * kVec + v) * kST + t;
+        if (sl.whole(i)) tc::cp_async16(d, sl.at(i)); else *d = sl.edge(i);
+      }
     }
-    best = fmaxf(best, Vec<T>::top(r));
-    *reinterpret_cast<uint4*>(xs + i) = r;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  for (int b = 0; b < kStages; ++b) issue(b);
+  const Row r = row_of(q, row);
+  if (t < 128) sh.table[t] = q.table[t];
+  if (t < kBins) sh.count[t] = 0, sh.mass[t] = 0;
+  if (t == 0) {
+    sh.m_key = 0;
+    sh.n_list = sh.n_final = sh.bad = 0;
+    sh.rest = sh.best = sh.far = 0;
+    sh.pick[0] = 0x7fffffff;
+    sh.pick[1] = -1;
   }
-  if (t < 128) sh.table[t] = p.table[t];
-  for (int b = t; b < kBins; b += kThreads) sh.hist[b] = 0;
-  if (t == 0) sh.n_list = 0;
-
-  // reductions over the row; every thread of every CTA gets the same result
-  auto row_max = [&](float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    if (lane == 0) sh.red_f[0][warp] = v;
-    __syncthreads();
-    if (t == 0) {
-      float r = sh.red_f[0][0];
-      for (int w = 1; w < kWarps; ++w) r = fmaxf(r, sh.red_f[0][w]);
-      sh.slot[phase].f = r;
-    }
-    sync_row();
-    float r = -INFINITY;
-#pragma unroll
-    for (int c = 0; c < C; ++c) r = fmaxf(r, peer(&sh.slot[phase], c)->f);
-    phase ^= 1;
-    return r;
-  };
-  // op 0: sum, 1: min, 2: max of unsigned values
-  auto row_u = [&](unsigned (&v)[2], int op0, int op1) {
-    const int op[2] = {op0, op1};
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const unsigned r = op[k] == 0 ? __reduce_add_sync(0xffffffffu, v[k])
-                                    : op[k] == 1 ? __reduce_min_sync(0xffffffffu, v[k]) : __reduce_max_sync(0xffffffffu, v[k]);
-      if (lane == 0) sh.red_u[k][warp] = r;
-    }
-    __syncthreads();
-    if (t < 2) {
-      unsigned r = sh.red_u[t][0];
-      for (int w = 1; w < kWarps; ++w) {
-        const unsigned x = sh.red_u[t][w];
-        r = op[t] == 0 ? r + x : op[t] == 1 ? min(r, x) : max(r, x);
-      }
-      sh.slot[phase].u[t] = r;
-    }
-    sync_row();
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      unsigned r = peer(&sh.slot[phase], 0)->u[k];
-#pragma unroll
-      for (int c = 1; c < C; ++c) {
-        const unsigned x = peer(&sh.slot[phase], c)->u[k];
-        r = op[k] == 0 ? r + x : op[k] == 1 ? min(r, x) : max(r, x);
-      }
-      v[k] = r;
-    }
-    phase ^= 1;
-  };
-  auto row_sum2 = [&](F2 a, F2 b, unsigned long long (&out)[2]) {  // in units of 2^-43
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a = shfl_add(a, o), b = shfl_add(b, o);
-    if (lane == 0) sh.red_l[0][warp] = fix<43>(a), sh.red_l[1][warp] = fix<43>(b);
-    __syncthreads();
-    if (t < 2) {
-      unsigned long long r = 0;
-      for (int w = 0; w < kWarps; ++w) r += sh.red_l[t][w];
-      sh.slot[phase].d[t] = r;
-    }
-    sync_row();
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      unsigned long long r = 0;
-#pragma unroll
-      for (int c = 0; c < C; ++c) r += peer(&sh.slot[phase], c)->d[k];
-      out[k] = r;
-    }
-    phase ^= 1;
-  };
-  // f(position, logit) over this thread's elements of vectors whose largest is at least `from`: warp
-  // w has the contiguous segment of `seg` positions from w * seg on, lanes take vectors of it in
-  // turn.  NaN and -0 come as -inf and +0 (equal logits have equal keys).
-  const int seg = padded / kWarps;
-  auto each = [&](float from, auto&& f) {
-    for (int i = warp * seg + lane * N; i < (warp + 1) * seg; i += 32 * N) {
-      const uint4 r = *reinterpret_cast<const uint4*>(xs + i);
-      if (!(Vec<T>::top(r) >= from)) continue;
-      float v[N];
-      Vec<T>::get(r, v);
-#pragma unroll
-      for (int e = 0; e < N; ++e) f(i + e, v[e] == v[e] ? v[e] + 0.f : -INFINITY);
-    }
-  };
-
-  const float m = row_max(best);  // also: the slice, the table and the zeroed bins are visible
-  const float T_row = p.temperature ? p.temperature[row] : 1.f;
-  const int k_row = p.top_k ? p.top_k[row] : 0;
-  const float p_row = p.top_p ? p.top_p[row] : 1.f;
-  const float lo_row = p.min_p ? p.min_p[row] : 0.f;
-  float u_row = p.u[row];
-  u_row = u_row > 0.f ? u_row : 0.f;
-  const bool valid = m > -INFINITY && T_row >= 0.f && T_row <= FLT_MAX;
-  if (!valid || T_row == 0.f) {
-    unsigned v[2] = {0xffffffffu, 0};
-    if (valid)
-      each(m, [&](int i, float x) { v[0] = x == m && i < count ? min(v[0], (unsigned)(first + i)) : v[0]; });
-    row_u(v, 1, 0);
-    if (rank == 0 && t == 0) {
-      p.tokens[row] = valid ? (int)v[0] : -1;
-      if (p.probs) p.probs[row] = valid ? 1.f : 0.f;
-    }
-    sync_row();  // no CTA leaves while another reads its shared memory
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (!(r.T >= 0.f && r.T <= FLT_MAX)) {  // the same in every CTA of the row
+    if (rank == 0 && t == 0) put(q, row, -1, 0.f);
     return;
   }
-  // log2(e) / T as a pair: quotient, and the exact remainder's quotient
-  constexpr float kE = 1.44269502162933349609375f, kEl = 1.92596299e-8f;  // log2(e)
-  Scale sc;
-  sc.m = m;
-  sc.c_hi = kE / T_row;
-  sc.c_lo = isinf(sc.c_hi) ? 0.f : (fmaf(-sc.c_hi, T_row, kE) + kEl) / T_row;
-  sc.table = sh.table;
-  // a logit from which on t can be below r (rounding allowed for)
-  auto reach = [&](float r) { return isinf(sc.c_hi) || isinf(m) ? m : m - r / sc.c_hi * 1.00001f - fabsf(m) * 1e-6f; };
-
-  // ---- (tau, n): keys above tau are kept, and the n first of those equal to it
-  unsigned tau = key_of(-INFINITY), n_tau = 0;  // -inf itself is never drawn
-  bool use_k = k_row > 0 && k_row < p.vocab;
-  const bool use_p = p_row < 1.f;
-  const float p_pos = fmaxf(p_row, 0.f);
-  if (use_k || use_p) {
-    const bool had_k = use_k;
-    constexpr int kB = kBins / kThreads;  // thread t owns bins kB t .. of the falling logits
-    float bin_scale = 0.f;
-    int bin_k = 0, bin_end = 0;           // top-k's last bin; the last bin that the prefix can reach
-    unsigned above_k = 0, n_list = 0, cnt[kB], cum0 = 0;
-    unsigned long long mass = 0, tail = 0;  // of the row and of its logits past the range (top-p without top-k)
-    auto bin_of = [&](float x) {
-      const float b = t_of(sc, x) * bin_scale;
-      return b < kBins ? (int)b : kBins;
-    };
-    auto before_u = [&](unsigned v, unsigned* all) {  // sum over lower threads
-      unsigned inc = v;
+  __syncthreads();
+  // ---- the first blocks' maximum
+  float top = -INFINITY;
+  for (int b = 0; b < min(blocks, kStages); ++b) {
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
-      }
-      if (lane == 31) sh.red_u[0][warp] = inc;
-      __syncthreads();
-      unsigned b = inc - v, a = 0;
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) b += sh.red_u[0][w];
-        a += sh.red_u[0][w];
-      }
-      __syncthreads();
-      *all = a;
-      return b;
-    };
-    // sums over the bins of lower threads (bounds, loose enough for fp32 sums)
-    auto before_f = [&](float v, int slot, float* all) {
-      float inc = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
-      }
-      if (lane == 31) sh.red_f[slot][warp] = inc;
-      __syncthreads();
-      float b = inc - v, a = 0.f;
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) b += sh.red_f[slot][w];
-        a += sh.red_f[slot][w];
-      }
-      *all = a;
-      return b;
-    };
-    auto lo_of = [&](int bin) { return exp2f(-(bin + 1.001f) / bin_scale) * 0.999f; };
-    auto up_of = [&](int bin) { return exp2f(-(bin - 0.001f) / bin_scale) * 1.001f; };
-
-    for (int far = 0;; ++far) {  // t in [0, 20), then in [0, 40)
-      const float range = far ? kCut : kNear;
-      bin_scale = kBins / range;
-      F2 near = {0, 0};
-      float rest = 0.f;
-      const bool sum = use_p && !use_k && !far;
-      each(reach(sum ? kCut : range), [&](int, float x) {
-        const int b = bin_of(x);
-        if (b < kBins) {
-          atomicAdd(&sh.hist[b], 1u);
-          if (sum) near = add(near, weight(sc, x));
-        } else if (sum) {
-          const float tt = t_of(sc, x);
-          rest += tt <= kCut ? exp2f(-tt) : 0.f;
-        }
-      });
-      if (sum) {
-        unsigned long long s2[2];
-        row_sum2(near, F2{rest, 0.f}, s2);  // (and the row's histograms are complete)
-        mass = s2[0] + s2[1];
-        tail = s2[1];
-      } else {
-        sync_row();
-        tail = 0;
-      }
-      unsigned mine = 0, n_all;
-#pragma unroll
-      for (int b = 0; b < kB; ++b) {
-        cnt[b] = 0;
-#pragma unroll
-        for (int r = 0; r < C; ++r) cnt[b] += peer(sh.hist, r)[t * kB + b];
-        mine += cnt[b];
-      }
-      if (t < 4) sh.pick[t] = t < 2 ? -1 : kBins - 1;
-      cum0 = before_u(mine, &n_all);
-      unsigned cum = cum0;
-      bool found;
-      if (use_k) {  // the bin in which the count reaches k
-#pragma unroll
-        for (int b = 0; b < kB; ++b) {
-          if (cum < (unsigned)k_row && cum + cnt[b] >= (unsigned)k_row) sh.pick[0] = t * kB + b, sh.pick[1] = (int)cum;
-          cum += cnt[b];
-        }
-        __syncthreads();
-        bin_k = bin_end = sh.pick[0];
-        above_k = (unsigned)sh.pick[1];
-        found = bin_k >= 0;
-      } else {      // the first bin by which the goal is surely reached: by what lies before, or what is left
-        float lo_s = 0.f, up_s = 0.f, lo_all, up_all;
-#pragma unroll
-        for (int b = 0; b < kB; ++b) lo_s += cnt[b] * lo_of(t * kB + b), up_s += cnt[b] * up_of(t * kB + b);
-        float lo_run = before_f(lo_s, 0, &lo_all), up_run = before_f(up_s, 1, &up_all);
-        const float whole = (float)mass * 0x1p-43f, left = (float)tail * 0x1.001p-43f;
-        const float goal = p_pos * whole * 1.0001f, spare = (1.f - p_pos) * whole * 0.999f;
-        bool any = false;
-#pragma unroll
-        for (int b = 0; b < kB; ++b) {
-          lo_run += cnt[b] * lo_of(t * kB + b);
-          up_run += cnt[b] * up_of(t * kB + b);
-          if (cnt[b] > 0 && (lo_run >= goal || (up_all - up_run) + up_all * 1e-5f + left <= spare)) {
-            atomicMin(&sh.pick[2], t * kB + b);
-            any = true;
-          }
-        }
-        found = __syncthreads_or(any);
-        bin_end = sh.pick[2];
-      }
-      if (found || far) {
-        if (!found) {  // every weight above 0 counts
-          bin_end = kBins - 1;
-          use_k = false;
-        }
-        // logits in bins up to bin_end
-        cum = cum0;
-#pragma unroll
-        for (int b = 0; b < kB; ++b) {
-          cum += cnt[b];
-          if (t * kB + b == bin_end) sh.pick[3] = (int)cum;
-        }
-        __syncthreads();
-        n_list = (unsigned)sh.pick[3];
-        if (n_list <= kList || far) break;
-      }
-      // look further: zero the histogram once every CTA has read it
-      sync_row();
-      for (int b = t; b < kBins; b += kThreads) sh.hist[b] = 0;
-      __syncthreads();
-    }
-
-    if (n_list <= kList) {
-      // ---- the list, in the first CTA
-      unsigned long long* list = peer(sh.list, 0);
-      unsigned* n_at = peer(&sh.n_list, 0);
-      each(reach((bin_end + 1) / bin_scale), [&](int i, float x) {
-        if (bin_of(x) <= bin_end)
-          list[atomicAdd(n_at, 1u)] = (unsigned long long)~key_of(x) << 32 | (unsigned)(first + i);
-      });
-      sync_row();
-      if (rank != 0) return;  // nothing of the other CTAs' is read from here on
-      const int n = (int)n_list;
-      int n2 = 64;
-      while (n2 < n) n2 *= 2;
-      for (int i = n + t; i < n2; i += kThreads) sh.list[i] = ~0ull;
-      __syncthreads();
-      // bitonic sort by (falling logit, index)
-      if (n2 > 64 || warp == 0) {
-        for (int len = 2; len <= n2; len *= 2) {
-          for (int d = len / 2; d > 0; d /= 2) {
-            for (int i = t; i < n2 / 2; i += kThreads) {
-              const int a = 2 * i - (i & (d - 1)), b = a + d;
-              const unsigned long long va = sh.list[a], vb = sh.list[b];
-              if ((va > vb) == ((a & len) == 0)) sh.list[a] = vb, sh.list[b] = va;
-            }
-            if (n2 > 64) __syncthreads(); else __syncwarp();
-          }
-        }
-      }
-      __syncthreads();
-      // thread t has items [t per, (t + 1) per): weights and their running sum
-      const int per = max(1, n2 / kThreads), i0 = t * per;
-      constexpr int kPer = kList / kThreads;
-      unsigned long long w[kPer], mine = 0;
-      unsigned idx[kPer];
-      bool low[kPer];  // below min-p
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        w[e] = 0, idx[e] = 0, low[e] = false;
-        if (e < per && i0 + e < n) {
-          const unsigned long long it = sh.list[i0 + e];
-          const F2 f = weight(sc, of_key(~(unsigned)(it >> 32)));
-          w[e] = fix<52>(f);
-          low[e] = below(f, lo_row);
-          idx[e] = (unsigned)it;
-        }
-        mine += w[e];
-      }
-      auto scan_l = [&](unsigned long long v) {  // sum over lower threads
-        unsigned long long inc = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned long long x = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += x;
-        }
-        if (lane == 31) sh.red_l[0][warp] = inc;
-        __syncthreads();
-        unsigned long long b = inc - v;
-        for (int q = 0; q < warp; ++q) b += sh.red_l[0][q];
-        __syncthreads();
-        return b;
-      };
-      const unsigned long long before = scan_l(mine);
-      const int k_end = use_k ? min(n, k_row) : n;
-      unsigned long long goal = ~0ull;  // kept: what lies before is below it
-      if (use_p) {
-        int up = 9;  // the row's mass is in units of 2^-43
-        if (had_k) {  // that left by top-k is all in the list
-          unsigned long long run = before;
-#pragma unroll
-          for (int e = 0; e < kPer; ++e) {
-            run += w[e];
-            if (e < per && i0 + e == k_end - 1) sh.red_l[1][0] = run;
-          }
-          __syncthreads();
-          mass = sh.red_l[1][0];
-          up = 0;
-        } else if (mass < 1ull << 54) {
-          mass <<= up;
-          up = 0;
-        }
-        bool more;
-        goal = part_of(mass, p_pos, &more);
-        goal += more;
-        goal = goal >> (64 - up - 1) > 1 ? ~0ull : goal << up;  // (a prefix in the list is below 2^63)
-      }
-      // the kept prefix: its length and mass
-      unsigned long long run = before, kept_w = 0;
-      int kept_n = 0;
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        const int i = i0 + e;
-        const bool in = e < per && i < k_end && (i == 0 || run < goal) && !low[e] && w[e] > 0;
-        run += w[e];
-        if (in) ++kept_n, kept_w += w[e];
-      }
-      int n_kept = __reduce_add_sync(0xffffffffu, kept_n);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) kept_w += __shfl_xor_sync(0xffffffffu, kept_w, o);
-      if (lane == 0) sh.red_u[0][warp] = n_kept, sh.red_l[0][warp] = kept_w;
-#pragma unroll
-      for (int e = 0; e < kPer; ++e)
-        if (e < per && i0 + e < n) sh.index[i0 + e] = idx[e], sh.list[i0 + e] = w[e];
-      if (t == 0) sh.pick[0] = 0x7fffffff, sh.pick[1] = -1;
-      __syncthreads();
-      n_kept = 0;
-      kept_w = 0;
-      for (int q = 0; q < kWarps; ++q) n_kept += sh.red_u[0][q], kept_w += sh.red_l[0][q];
-      const unsigned long long target = part_of(kept_w, u_row);
-      // the lowest index at which the running sum by index exceeds the target, else the last one
-      // (packed with the item's place: below 2^20 and 2^11)
-      if (n_kept <= 128) {
-        if (t < n_kept) {
-          const unsigned me = sh.index[t];
-          unsigned long long s = 0;
-          for (int j = 0; j < n_kept; ++j) s += sh.index[j] <= me ? sh.list[j] : 0ull;
-          const int at = (int)(me << 11 | t);
-          if (s > target) atomicMin(&sh.pick[0], at);
-          atomicMax(&sh.pick[1], at);
-        }
-      } else {
-        int m2 = 256;
-        while (m2 < n_kept) m2 *= 2;
-        unsigned* by = reinterpret_cast<unsigned*>(xs);  // the slice is not read any more
-        for (int i = t; i < m2; i += kThreads) by[i] = i < n_kept ? sh.index[i] << 11 | i : 0xffffffffu;
-        __syncthreads();
-        for (int len = 2; len <= m2; len *= 2) {
-          for (int d = len / 2; d > 0; d /= 2) {
-            for (int i = t; i < m2 / 2; i += kThreads) {
-              const int a = 2 * i - (i & (d - 1)), b = a + d;
-              const unsigned va = by[a], vb = by[b];
-              if ((va > vb) == ((a & len) == 0)) by[a] = vb, by[b] = va;
-            }
-            __syncthreads();
-          }
-        }
-        const int q = max(1, m2 / kThreads), j0 = t * q;
-        unsigned long long s = 0;
-        for (int e = 0; e < q; ++e)
-          if (j0 + e < n_kept) s += sh.list[by[j0 + e] & 2047];
-        s = scan_l(s);
-        for (int e = 0; e < q; ++e) {
-          if (j0 + e >= n_kept) break;
-          s += sh.list[by[j0 + e] & 2047];
-          if (s > target) {
-            atomicMin(&sh.pick[0], (int)by[j0 + e]);
-            break;
-          }
-        }
-        if (t == 0) sh.pick[1] = (int)by[n_kept - 1];
-      }
-      __syncthreads();
-      if (t == 0) {
-        const int at = sh.pick[0] != 0x7fffffff ? sh.pick[0] : sh.pick[1];
-        p.tokens[row] = at >= 0 ? at >> 11 : -1;
-        if (p.probs) p.probs[row] = at >= 0 ? (float)((double)sh.list[at & 2047] / (double)kept_w) : 0.f;
-      }
-      return;
-    }
-
-    // ---- the list is too long (the histogram is that of [0, 40)): bisection
-    if (use_k) {
-      // smallest and largest key in top-k's bin, then the largest tau with count(key >= tau) >= k
-      unsigned v[2] = {0xffffffffu, 0u};
-      const float from = reach((bin_k + 1) / bin_scale);
-      each(from, [&](int, float x) {
-        if (bin_of(x) == bin_k) v[0] = min(v[0], key_of(x)), v[1] = max(v[1], key_of(x));
-      });
-      row_u(v, 1, 2);
-      unsigned lo = v[0], hi = v[1], above = above_k;
-      while (lo < hi) {
-        const unsigned mid = lo + (hi - lo + 1) / 2;
-        unsigned n[2] = {0, 0};
-        each(of_key(mid), [&](int, float x) { n[0] += bin_of(x) == bin_k && key_of(x) >= mid; });
-        row_u(n, 0, 0);
-        if (above_k + n[0] >= (unsigned)k_row) lo = mid; else hi = mid - 1, above = above_k + n[0];
-      }
-      n_tau = (unsigned)k_row - above;
-      tau = lo;
-    }
-    if (use_p) {
-      // bounds on the mass of every bin, cut at k: the bins in which the goal can be reached
-      float lo_m = 0.f, up_m = 0.f, lo_b[kB], up_b[kB];
-      unsigned cum = cum0;
-#pragma unroll
-      for (int b = 0; b < kB; ++b) {
-        const int bin = t * kB + b;
-        const unsigned kept = !use_k ? cnt[b] : cum >= (unsigned)k_row ? 0u : min(cnt[b], (unsigned)k_row - cum);
-        cum += cnt[b];
-        lo_b[b] = kept * lo_of(bin);
-        up_b[b] = kept * up_of(bin);
-        lo_m += lo_b[b], up_m += up_b[b];
-      }
-      float lo_all, up_all;
-      float lo_c = before_f(lo_m, 0, &lo_all), up_c = before_f(up_m, 1, &up_all);
-      __syncthreads();
-      if (t < 2) sh.pick[2 + t] = kBins - 1;
-      __syncthreads();
-      const float p_lo = p_pos * lo_all * 0.999f, p_up = p_pos * up_all * 1.001f;
-#pragma unroll
-      for (int b = 0; b < kB; ++b) {
-        lo_c += lo_b[b], up_c += up_b[b];
-        if (up_c >= p_lo) atomicMin(&sh.pick[2], t * kB + b);
-        if (lo_c >= p_up) atomicMin(&sh.pick[3], t * kB + b);
-      }
-      __syncthreads();
-      const int b0 = sh.pick[2], b1 = sh.pick[3];
-      // the mass left by top-k, and its part in the bins before b0
-      const unsigned tau_k = tau, n_k = n_tau;
-      const bool tie_in = n_k > 0;
-      const unsigned long long w_k = tie_in ? n_k * fix<43>(weight(sc, of_key(tau_k))) : 0ull;  // the ties' mass
-      F2 all = {0, 0}, head = {0, 0};
-      unsigned v[2] = {0xffffffffu, 0u};
-      each(fmaxf(reach(kCut), of_key(tau_k)), [&](int, float x) {
-        const unsigned key = key_of(x);
-        if (key < tau_k || (key == tau_k && n_k == 0)) return;
-        const int b = bin_of(x);
-        if (b >= b0 && b <= b1) v[0] = min(v[0], key), v[1] = max(v[1], key);
-        if (key > tau_k) {
-          const F2 w = weight(sc, x);
-          all = add(all, w);
-          if (b < b0) head = add(head, w);
-        }
-      });
-      unsigned long long sums[2];
-      row_sum2(all, head, sums);
-      row_u(v, 1, 2);
-      const int bin_tau = tie_in ? bin_of(of_key(tau_k)) : kBins;
-      const unsigned long long base = sums[1] + (bin_tau < b0 ? w_k : 0ull);
-      bool rem;
-      unsigned long long goal = part_of(sums[0] + w_k, p_pos, &rem);
-      goal += rem;
-      unsigned lo = v[0], hi = v[1];
-      if (lo <= hi) {
-        unsigned long long above = base;  // mass of the keys above hi
-        while (lo < hi) {
-          const unsigned mid = lo + (hi - lo + 1) / 2;
-          F2 s = {0, 0};
-          each(of_key(mid), [&](int, float x) {
-            const unsigned key = key_of(x);
-            if (key < mid || key <= tau_k) return;
-            const int b = bin_of(x);
-            if (b >= b0 && b <= b1) s = add(s, weight(sc, x));
-          });
-          unsigned long long r[2];
-          row_sum2(s, F2{0, 0}, r);
-          const unsigned long long f = base + r[0] + (tau_k >= mid && bin_tau >= b0 ? w_k : 0ull);
-          if (f >= goal) lo = mid; else hi = mid - 1, above = f;
-        }
-        // of the keys equal to tau: those before which less than the goal lies
-        if (t == 0) {
-          const F2 w = weight(sc, of_key(lo));
-          const double need = goal > above ? (double)(goal - above) * 0x1p-43 : 0.0;
-          const double more = w.h > 0.f ? ceil(need / ((double)w.h + (double)w.l)) : 1.0;
-          sh.pick[0] = (int)fmin(more, 2e9);
-        }
-        __syncthreads();
-        const unsigned more = (unsigned)sh.pick[0];
-        const unsigned n_p = more == 0 && goal == 0 && lo == key_of(m) ? 1u : more;  // the first always stays
-        n_tau = lo == tau_k && tie_in ? min(n_k, n_p) : n_p;
-        tau = lo;
-      }
-    }
+    for (int v = 0; v < kVec; ++v) top = fmaxf(top, Vec<T>::top(ring[(b * kVec + v) * kST + t]));
   }
-
-  // ---- ties at tau before each warp's segment
-  const bool ties = use_k || use_p;
-  unsigned my_ties = 0;
-  if (ties) {
-    each(of_key(tau), [&](int i, float x) { my_ties += key_of(x) == tau && i >= begin && i < count; });
-    my_ties = __reduce_add_sync(0xffffffffu, my_ties);
-  }
-  unsigned ties_before = 0;
-  if (ties) {
-    if (lane == 0) sh.wties[warp] = my_ties;
+  unsigned w_key = __reduce_max_sync(0xffffffffu, key_of(top + 0.f));
+  if (lane == 0) atomicMax(&sh.m_key, w_key);
+  sync_row();
+  float m = of_key(sh.m_key);  // this warp's maximum so far
+  for (int c = 0; c < C; ++c) m = fmaxf(m, of_key(*peer(&sh.m_key, c)));
+  Scale sc = scale_of(m, r.T, sh.table);  // (T == 0: not used)
+  // rows by list: a short prefix by right
+  const bool greedy = r.T == 0.f;
+  const bool by_list = !greedy && (r.use_k || r.use_p || r.lo > 0.f);
+  const bool sum = by_list && r.use_p && !r.use_k;
+  float floor_x = -INFINITY;  // the list takes logits from here on
+  if (by_list) {
+    const float from = reach(sc, kFar);
+    for (int b = 0; b < min(blocks, kStages); ++b) {
+#pragma unroll 1
+      for (int v = 0; v < kVec; ++v) {
+        const uint4 x4 = ring[(b * kVec + v) * kST + t];
+        if (!(Vec<T>::top(x4) >= from)) continue;
+        float x[N];
+        Vec<T>::get(x4, x);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const float tt = t_of(sc, clean(x[e]));
+          if (tt < kFar && x[e] > -INFINITY) atomicAdd(&sh.count[(int)(tt * (kLook / kFar))], 1u);
+        }
+      }
+    }
     sync_row();
-    if (t < C * kWarps) sh.all_ties[t] = peer(sh.wties, t / kWarps)[t % kWarps];
-    __syncthreads();
-    for (int w = 0; w < rank * kWarps + warp; ++w) ties_before += sh.all_ties[w];
-  }
-  // f(index, logit, kept weight) over this warp's segment in order, a vector per lane at a time
-  // (a weight has to reach min-p; the largest one does, or none)
-  const float from = fmaxf(fmaxf(reach(kCut), of_key(tau)), lo_row > 0.f && lo_row < 1.f ? reach(-log2f(lo_row) + 0.01f) : -INFINITY);
-  auto kept = [&](auto&& f) {
-    unsigned rank0 = ties_before;
-    const bool some = ties && ties_before < n_tau && ties_before + my_ties > n_tau;  // the n-th tie is here
-    const bool whole = ties && ties_before + my_ties <= n_tau;
-    for (int i0 = warp * seg; i0 < (warp + 1) * seg; i0 += 32 * N) {
-      const uint4 r = *reinterpret_cast<const uint4*>(xs + i0 + lane * N);
-      if (!__any_sync(0xffffffffu, Vec<T>::top(r) >= from)) continue;  // nothing kept here
-      float v[N];
-      Vec<T>::get(r, v);
+    if (warp == 0) {
+      // lane l: bins 2 l, 2 l + 1 of the row's first blocks.  The first bin by which, going by them,
+      // the list holds what the filter needs: k and half as many more, a p of the mass with a quarter
+      // of the rest, every t up to min-p's
+      unsigned a = 0, b = 0;
+      for (int c = 0; c < C; ++c) a += peer(sh.count, c)[2 * lane], b += peer(sh.count, c)[2 * lane + 1];
+      const float wa = a * exp2f(-(2 * lane + 0.5f) * (kFar / kLook)), wb = b * exp2f(-(2 * lane + 1.5f) * (kFar / kLook));
+      unsigned n = a + b;
+      float w = wa + wb;
 #pragma unroll
-      for (int e = 0; e < N; ++e) v[e] = v[e] == v[e] ? v[e] + 0.f : -INFINITY;
-      unsigned eq = 0, at = 0;
-      if (some) {
-#pragma unroll
-        for (int e = 0; e < N; ++e) eq += key_of(v[e]) == tau && i0 + lane * N + e >= begin && i0 + lane * N + e < count;
-        unsigned inc = eq;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned x = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += x;
-        }
-        at = rank0 + inc - eq;
-        rank0 += __shfl_sync(0xffffffffu, inc, 31);
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned x = __shfl_up_sync(0xffffffffu, n, o);
+        const float y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) n += x, w += y;
       }
-      F2 w[N];
+      const float whole = __shfl_sync(0xffffffffu, w, 31);
+      const float share = (float)min(blocks, kStages) / (float)max(blocks, 1);  // of the row seen
+      const float end = (2 * lane + 2) * (kFar / kLook);
+      bool enough = true;
+      if (r.use_k)
+        enough = n >= (1.5f * r.k + 64.f) * share;
+      else if (r.use_p)
+        enough = w >= (0.75f + 0.25f * r.p) * whole;
+      else
+        enough = end > -log2f(r.lo) + 0.5f;
+      const unsigned yes = __ballot_sync(0xffffffffu, enough), fits = __ballot_sync(0xffffffffu, n <= kAim * share);
+      const int pairs = min(yes ? __ffs(yes) : 32, max(1, ~fits ? __ffs(~fits) - 1 : 32));
+      if (lane == 0) sh.floor = m - pairs * 2 * (kFar / kLook) / sc.c_hi;
+    }
+    if (C > 1) cl.sync(); else __syncthreads();  // (the counts are read by every CTA)
+    floor_x = isinf(m) || isinf(sc.c_hi) ? m : sh.floor;
+    if (t < kLook) sh.count[t] = 0;
+  }
+
+  // ---- the row
+  float rest = 0.f;                                  // fp32 mass below the floor, relative to m
+  unsigned long long best = 0;                       // greedy: (key, ~index)
+  bool exact = false;                                // temperature alone: the second time
+stream:
+  for (int b = 0; b < blocks; ++b) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    uint4 x4[kVec];
+    float tops[kVec];
+    top = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) {
+      x4[v] = ring[(b % kStages * kVec + v) * kST + t];
+      tops[v] = Vec<T>::top(x4[v]);
+      top = fmaxf(top, tops[v]);
+    }
+    w_key = __reduce_max_sync(0xffffffffu, key_of(top + 0.f));
+    if (lane == 0 && w_key > *(volatile unsigned*)&sh.m_key) atomicMax(&sh.m_key, w_key);
+    issue(b + kStages);
+    const float m_new = fmaxf(of_key(w_key), of_key(__shfl_sync(0xffffffffu, *(volatile unsigned*)&sh.m_key, 0)));
+    if (m_new > m) {
+      sc.m = m_new;
+      rest *= exp2f(-t_of(sc, m));  // (0 at first: m = -inf)
+      m = m_new;
+    }
+    // 2^-t of a vector's logits, in fp32 (NaN and -inf give 0; m is finite): t with its low part, a
+    // tree of sums
+    auto fast = [&](const uint4& v4) {
+      float x[N];
+      Vec<T>::get(v4, x);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        const unsigned key = key_of(v[e]);
-        bool in = key > tau;
-        if (ties && key == tau) in = some ? at++ < n_tau : whole;
-        w[e] = F2{0.f, 0.f};
-        if (in) {
-          w[e] = weight(sc, v[e]);
-          if (below(w[e], lo_row)) w[e] = F2{0.f, 0.f};
+        const float d = fmaxf(x[e], -FLT_MAX) - m, a = d * sc.c_hi;
+        const float w = ex2(a), lo = fmaf(d, sc.c_hi, -a) + d * sc.c_lo;
+        x[e] = a >= -kCut ? fmaf(w, lo * 0.693147182f, w) : 0.f;
+      }
+#pragma unroll
+      for (int o = N / 2; o > 0; o /= 2) {
+#pragma unroll
+        for (int e = 0; e < o; ++e) x[e] += x[e + o];
+      }
+      return x[0];
+    };
+    const bool finite = m > -INFINITY && m < INFINITY && !isinf(sc.c_hi);
+    const float cut_x = reach(sc, kCut);  // vectors below weigh nothing
+    if (greedy) {
+#pragma unroll
+      for (int v = 0; v < kVec; ++v) {
+        if (!(tops[v] >= m)) continue;
+        float x[N];
+        Vec<T>::get(x4[v], x);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const unsigned long long c = (unsigned long long)key_of(clean(x[e])) << 32 | ~(unsigned)(sl.first + pos_of(b, v) + e);
+          if (clean(x[e]) > -INFINITY && c > best) best = c;
         }
       }
-      if (!f(i0, w)) break;
+    } else if (by_list) {
+#pragma unroll
+      for (int v = 0; v < kVec; ++v) {
+        if (tops[v] >= floor_x) {
+          float x[N];
+          Vec<T>::get(x4[v], x);
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            const float c = clean(x[e]);
+            if (c >= floor_x && c > -INFINITY) {
+              const unsigned at = atomicAdd(&sh.n_list, 1u);
+              if (at < kList) list[at] = (unsigned long long)~key_of(c) << 32 | (unsigned)(sl.first + pos_of(b, v) + e);
+            } else if (sum && finite) {
+              rest += ex2((c - m) * sc.c_hi);
+            }
+          }
+        } else if (sum && finite && tops[v] >= cut_x) {
+          rest += fast(x4[v]);
+        }
+      }
+    } else {
+      F2 s = {0.f, 0.f};
+      float far = 0.f;
+      const float near_x = exact || !finite ? cut_x : reach(sc, kNear);
+#pragma unroll 1
+      for (int v = 0; v < kVec; ++v) {
+        const uint4 y4 = v == 0 ? x4[0] : v == 1 ? x4[1] : v == 2 ? x4[2] : x4[3];
+        const float top_v = Vec<T>::top(y4);
+        if (!(top_v >= cut_x)) continue;
+        if (top_v >= near_x) {
+          float x[N];
+          Vec<T>::get(y4, x);
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            F2 w = weight(sc, clean(x[e]));
+            if (clean(x[e]) == -INFINITY) w = F2{0.f, 0.f};
+            s = add(s, w);
+          }
+        } else {
+          const float f = fast(y4);
+          far += f;
+          s = add(s, F2{f, 0.f});
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s = shfl_add(s, o), far += __shfl_xor_sync(0xffffffffu, far, o);
+      if (lane == 0) stretch[b * kSW + warp] = Stretch{s.h, s.l, far, m};
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (greedy) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+    if (lane == 0) atomicMax(&sh.best, best);
+    sync_row();
+    if (rank == 0 && t == 0) {
+      for (int c = 0; c < C; ++c) best = max(best, *peer(&sh.best, c));
+      put(q, row, best ? (int)~(unsigned)best : -1, best ? 1.f : 0.f);
+    }
+    if (C > 1) cl.sync();  // no CTA leaves while another reads its shared memory
+    return;
+  }
+
+  // ---- the row's maximum
+  sync_row();
+  float m_row = of_key(sh.m_key);
+  for (int c = 0; c < C; ++c) m_row = fmaxf(m_row, of_key(*peer(&sh.m_key, c)));
+  sc.m = m_row;
+  if (!(m_row > -INFINITY)) {
+    if (rank == 0 && t == 0) put(q, row, -1, 0.f);
+    if (C > 1) cl.sync();
+    return;
+  }
+
+  if (!by_list) {
+    // ---- temperature alone: running sums
+    const int n = blocks * kSW, per = (n + kST - 1) / kST;
+    unsigned long long mine = 0, my_far = 0;
+    for (int e = 0; e < per; ++e) {
+      const int i = t * per + e;
+      if (i >= n) break;
+      const Stretch& s = stretch[i];
+      if (s.ref > -INFINITY) {
+        const F2 f = weight(sc, s.ref);
+        mine += fix<43>(mul(F2{s.h, s.l}, f));
+        my_far += fix<43>(F2{s.far * f.h, 0.f});
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) my_far += __shfl_xor_sync(0xffffffffu, my_far, o);
+    if (lane == 0 && my_far) atomicAdd(&sh.far, my_far);
+    unsigned long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) sh.red_l[warp] = inc;
+    __syncthreads();
+    unsigned long long run = inc - mine, part = 0, total = 0, ahead = 0, far = sh.far;
+    for (int w = 0; w < kSW; ++w) {
+      if (w < warp) run += sh.red_l[w];
+      part += sh.red_l[w];
+    }
+    int last = 0;  // the row's last CTA with any mass
+    if (C > 1) {
+      if (t == 0) sh.part = part, sh.far_part = far;
+      cl.sync();
+      far = 0;
+      for (int c = 0; c < C; ++c) {
+        const unsigned long long x = *peer(&sh.part, c);
+        far += *peer(&sh.far_part, c);
+        if (c < rank) ahead += x;
+        if (x > 0) last = c;
+        total += x;
+      }
+      cl.sync();  // (the last that is read of the others)
+    } else {
+      total = part;
+    }
+    const unsigned long long target = part_of(total, r.u);
+    // the fp32 sums' error: of what lies ahead, and of the target
+    const unsigned long long slack = exact ? 0ull : part_of(far, 2.f * kFastError) + 1024;
+    run += ahead;
+    for (int e = 0; e < per; ++e) {  // this CTA's first stretch past the target, and its last with any mass
+      const int i = t * per + e;
+      if (i >= n) break;
+      const Stretch& s = stretch[i];
+      const unsigned long long x = s.ref > -INFINITY ? fix<43>(mul(F2{s.h, s.l}, weight(sc, s.ref))) : 0ull;
+      if (x > 0) {
+        if (run <= target && run + x > target) sh.pick[0] = i, sh.before = run;
+        atomicMax(&sh.pick[1], i);
+      }
+      run += x;
+    }
+    __syncthreads();
+    const bool mine_past = sh.pick[0] != 0x7fffffff;
+    const bool owner = mine_past || (rank == last && target >= total);  // u >= 1: the row's last kept one
+    if (owner && warp == 0) {
+      const int at = mine_past ? sh.pick[0] : sh.pick[1];
+      const int i1 = at / kSW * kBlock + at % kSW * kWarpPart;
+      const unsigned long long before = mine_past ? sh.before : 0ull;
+      auto weights = [&](int i0, F2 (&ws)[N]) {
+        const int i = i1 + i0 + lane * N;
+        const uint4 y4 = sl.whole(i) ? *reinterpret_cast<const uint4*>(sl.at(i)) : sl.edge(i);
+        float x[N];
+        Vec<T>::get(y4, x);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const float c = clean(x[e]);
+          ws[e] = c > -INFINITY ? weight(sc, c) : F2{0.f, 0.f};
+        }
+      };
+      int token, token2;
+      F2 w;
+      const unsigned long long goal = mine_past ? target : ~0ull;
+      walk<N>(kWarpPart, before, goal - (mine_past ? slack : 0), weights, &token, &w);
+      bool sure = token >= 0;
+      if (slack && mine_past) {  // the same token at both ends of the error, inside this stretch
+        walk<N>(kWarpPart, before, target + slack, weights, &token2, &w, &sure);
+        sure = sure && token2 == token && before + slack <= target;
+      }
+      if (q.probs) sure = sure && (float)far * kFastError <= (float)total * kProbError;
+      if (exact || sure) {
+        if (lane == 0) put(q, row, token >= 0 ? sl.first + i1 + token : -1, token >= 0 ? prob_of(w, total) : 0.f);
+      } else if (lane == 0) {
+        for (int c = 0; c < C; ++c) *peer(&sh.bad, c) = 1;  // stream the row again
+      }
+    }
+    if (exact) return;
+    sync_row();
+    if (!sh.bad) return;
+    exact = true;
+    __syncthreads();
+    if (t == 0) sh.pick[0] = 0x7fffffff, sh.pick[1] = -1, sh.far = 0;
+    m = m_row;  // every stretch by the row's maximum now
+    for (int b = 0; b < kStages; ++b) issue(b);
+    __syncthreads();
+    goto stream;
+  }
+
+  // ---- the row's list, in the first CTA (its ring is idle: its own part of the row is through)
+  {
+    sc.m = m_row;
+    rest *= m > -INFINITY ? exp2f(-t_of(sc, m)) : 0.f;
+    unsigned long long* dst = peer(final_list, 0);
+    unsigned* n_at = peer(&sh.n_final, 0);
+    const int n = (int)min(sh.n_list, (unsigned)kList);
+    bool full = sh.n_list > kList;
+    for (int i = t; i < n; i += kST) {
+      const unsigned at = C > 1 ? atomicAdd(n_at, 1u) : i;
+      if (at < kList) dst[at] = list[i]; else full = true;
+    }
+    if (C == 1 && t == 0) sh.n_final = n;
+    if (full) atomicOr(peer(&sh.bad, 0), 1u);
+    if (sum) {
+      F2 s = {rest, 0.f};
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s = shfl_add(s, o);
+      if (lane == 0) atomicAdd(peer(&sh.rest, 0), fix<43>(s));
+    }
+  }
+  sync_row();
+  if (rank != 0) return;
+  const int n_all = (int)sh.n_final;
+  if (sh.bad) {  // too many
+    if (t == 0) q.tokens[row] = kRetry;
+    return;
+  }
+  const float scale = kBins / fmaxf(t_of(sc, floor_x), 1e-30f);
+  auto bin_of = [&](float tt) { return min(kBins - 1, (int)fminf(tt * scale, kBins)); };
+  for (int i = t; i < n_all; i += kST) {
+    const float x = of_key(~(unsigned)(final_list[i] >> 32));
+    const int b = bin_of(t_of(sc, x));
+    atomicAdd(&sh.count[b], 1u);
+    if (sum) atomicAdd(&sh.mass[b], fix<52>(weight(sc, x)));
+  }
+  __syncthreads();
+  auto scan_l = [&](unsigned long long v, unsigned long long* all) {  // sum over lower threads
+    unsigned long long inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) sh.red_l[warp] = inc;
+    __syncthreads();
+    unsigned long long b = inc - v, a = 0;
+    for (int w = 0; w < kSW; ++w) {
+      if (w < warp) b += sh.red_l[w];
+      a += sh.red_l[w];
+    }
+    __syncthreads();
+    *all = a;
+    return b;
+  };
+  // thread t: bin t.  The last bin that the prefix reaches
+  unsigned long long all, goal = ~0ull;
+  const unsigned cum = (unsigned)scan_l(sh.count[t], &all) + sh.count[t];
+  bool here;
+  if (sum) {
+    if (sh.rest >= 1ull << 54) {  // a mass above 2048 largest weights
+      if (t == 0) q.tokens[row] = kRetry;
+      return;
+    }
+    unsigned long long whole;
+    const unsigned long long run = scan_l(sh.mass[t], &whole) + sh.mass[t];
+    bool more;
+    goal = part_of(whole + (sh.rest << 9), r.p, &more);
+    goal += more;
+    here = run >= goal;
+  } else if (r.use_k) {
+    here = cum >= (unsigned)r.k;
+  } else {  // min-p: t <= -log2(min_p), allowing for rounding
+    const float far = fmaxf(0.f, -log2f(r.lo)) + 0.01f;
+    here = (t + 1) / scale > far || (t == kBins - 1 && isinf(t_of(sc, floor_x))) || (t == kBins - 1 && floor_x == m_row && isinf(m_row));
+  }
+  if (here) atomicMin(&sh.pick[0], t);
+  __syncthreads();
+  const int bin_end = sh.pick[0];
+  if (bin_end == 0x7fffffff) {  // the prefix goes on past the list
+    if (t == 0) q.tokens[row] = kRetry;
+    return;
+  }
+  if (t == bin_end) sh.red_u[0] = cum;
+  if (t == 0) sh.n_list = 0;
+  __syncthreads();
+  const int n = (int)sh.red_u[0];
+  int n2 = 64;
+  while (n2 < n) n2 *= 2;
+  for (int i = t; i < n_all; i += kST) {
+    const unsigned long long it = final_list[i];
+    if (bin_of(t_of(sc, of_key(~(unsigned)(it >> 32)))) <= bin_end) list[atomicAdd(&sh.n_list, 1u)] = it;
+  }
+  for (int i = n + t; i < n2; i += kST) list[i] = ~0ull;
+  if (t == 0) sh.pick[0] = 0x7fffffff;
+  __syncthreads();
+  auto sort = [&](auto* v, int len_all) {  // ascending, bitonic; up to 64 by one warp
+    if (len_all > 64 || warp == 0) {
+      for (int len = 2; len <= len_all; len *= 2) {
+        for (int d = len / 2; d > 0; d /= 2) {
+          for (int i = t; i < len_all / 2; i += kST) {
+            const int a = 2 * i - (i & (d - 1)), b = a + d;
+            const auto va = v[a], vb = v[b];
+            if ((va > vb) == ((a & len) == 0)) v[a] = vb, v[b] = va;
+          }
+          if (len_all > 64) __syncthreads(); else __syncwarp();
+        }
+      }
+    }
+    __syncthreads();
+  };
+  sort(list, n2);  // by (falling logit, index)
+  // thread t has items [t per, (t + 1) per): weights (units of 2^-52) and their running sum
+  const int per = max(1, n2 / kST), i0 = t * per;
+  constexpr int kPer = kList / kST;
+  unsigned long long mine = 0;
+  unsigned low = 0;  // items below min-p
+#pragma unroll 1
+  for (int e = 0; e < per; ++e) {
+    const int i = i0 + e;
+    if (i >= n) break;
+    const unsigned long long it = list[i];
+    const F2 f = weight(sc, of_key(~(unsigned)(it >> 32)));
+    const unsigned long long w = fix<52>(f);
+    low |= (unsigned)below(f, r.lo) << e;
+    index[i] = (unsigned)it;
+    list[i] = w;
+    mine += w;
+  }
+  static_assert(kPer <= 32, "one bit per item");
+  const unsigned long long before = scan_l(mine, &all);
+  const int k_end = r.use_k ? min(n, r.k) : n;
+  if (r.use_k && r.use_p) {  // the goal is a part of the mass left by top-k
+    unsigned long long run = before;
+    for (int e = 0; e < per && i0 + e < k_end; ++e) {
+      run += list[i0 + e];
+      if (i0 + e == k_end - 1) sh.before = run;
+    }
+    __syncthreads();
+    bool more;
+    goal = part_of(sh.before, r.p, &more);
+    goal += more;
+  }
+  // the kept prefix: its length and mass
+  unsigned long long run = before, kept_w = 0;
+  int n_kept = 0;
+  for (int e = 0; e < per && i0 + e < k_end; ++e) {
+    const unsigned long long w = list[i0 + e];
+    if ((i0 + e == 0 || run < goal) && !(low >> e & 1) && w > 0) ++n_kept, kept_w += w;
+    run += w;
+  }
+  n_kept = __reduce_add_sync(0xffffffffu, n_kept);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) kept_w += __shfl_xor_sync(0xffffffffu, kept_w, o);
+  if (lane == 0) sh.red_u[warp] = n_kept, sh.red_l[warp] = kept_w;
+  __syncthreads();
+  n_kept = 0;
+  kept_w = 0;
+  for (int w = 0; w < kSW; ++w) n_kept += sh.red_u[w], kept_w += sh.red_l[w];
+  const unsigned long long target = part_of(kept_w, r.u);
+  // the lowest index at which the running sum by index exceeds the target, else the last one
+  // (packed with the item's place: below 2^20 and 2^11)
+  if (n_kept <= 128) {
+    if (t < n_kept) {
+      const unsigned me = index[t];
+      unsigned long long s = 0;
+      for (int j = 0; j < n_kept; ++j) s += index[j] <= me ? list[j] : 0ull;
+      const int at = (int)(me << 11 | t);
+      if (s > target) atomicMin(&sh.pick[0], at);
+      atomicMax(&sh.pick[1], at);
+    }
+  } else {
+    int m2 = 256;
+    while (m2 < n_kept) m2 *= 2;
+    for (int i = t; i < m2; i += kST) by[i] = i < n_kept ? index[i] << 11 | i : 0xffffffffu;
+    __syncthreads();
+    sort(by, m2);
+    const int c = m2 / kST, j0 = t * c;
+    unsigned long long s = 0;
+    for (int e = 0; e < c && j0 + e < n_kept; ++e) s += list[by[j0 + e] & 2047];
+    s = scan_l(s, &all);
+    for (int e = 0; e < c && j0 + e < n_kept; ++e) {
+      s += list[by[j0 + e] & 2047];
+      if (s > target) {
+        atomicMin(&sh.pick[0], (int)by[j0 + e]);
+        break;
+      }
+    }
+    if (t == 0) sh.pick[1] = (int)by[n_kept - 1];
+  }
+  __syncthreads();
+  if (t == 0) {
+    const int at = sh.pick[0] != 0x7fffffff ? sh.pick[0] : sh.pick[1];
+    put(q, row, at >= 0 ? at >> 11 : -1, at >= 0 ? (float)((double)list[at & 2047] / (double)kept_w) : 0.f);
+  }
+}
+
+// ------------------------------------------------------------------ select_kernel
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kC = 8;                        // CTAs of a row
+constexpr int kDigit = 10, kKeys = 1 << kDigit;
+constexpr int kSliceBytes = 184 * 1024;      // shared memory for a CTA's slice
+
+struct SelectShared {
+  float2 table[128];
+  unsigned count[kKeys];              // the slice's histogram of a round
+  unsigned long long mass[kKeys];
+  unsigned long long wsum[kWarps], all_sum[kC * kWarps];  // kept mass of each warp's segment
+  unsigned wties[kWarps], all_ties[kC * kWarps];          // logits equal to tau in it
+  unsigned long long red_l[kWarps], found_l;
+  unsigned todo[kWarps], m_key;
+  int found;
+};
+
+template <typename T>
+__device__ void select_row(const SampleParams& q, int row, T* xs, SelectShared& sh, cg::cluster_group& cl) {
+  constexpr int N = Vec<T>::N;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, rank = (int)cl.block_rank();
+  const Slice<T> sl(q, row, rank);
+  const int padded = (sl.count + N * 32 * kWarps - 1) / (N * 32 * kWarps) * (N * 32 * kWarps);
+  const int seg = padded / kWarps;  // warp w has positions w seg .. (w + 1) seg - 1, lanes take vectors in turn
+  if (t == 0) sh.m_key = 0;
+  __syncthreads();
+  float top = -INFINITY;
+  for (int i = t * N; i < padded; i += kThreads * N) {
+    const uint4 v = sl.whole(i) ? *reinterpret_cast<const uint4*>(sl.at(i)) : sl.edge(i);
+    top = fmaxf(top, Vec<T>::top(v));
+    *reinterpret_cast<uint4*>(xs + i) = v;
+  }
+  const unsigned w_key = __reduce_max_sync(0xffffffffu, key_of(top + 0.f));
+  if (lane == 0) atomicMax(&sh.m_key, w_key);
+  cl.sync();
+  unsigned m_key = 0;
+  for (int c = 0; c < kC; ++c) m_key = max(m_key, *cl.map_shared_rank(&sh.m_key, c));
+  const Row r = row_of(q, row);
+  const Scale sc = scale_of(of_key(m_key), r.T, sh.table);
+
+  auto each = [&](float from, auto&& f) {  // f(position, logit) over vectors whose largest is at least `from`
+    for (int i = warp * seg + lane * N; i < (warp + 1) * seg; i += 32 * N) {
+      const uint4 v4 = *reinterpret_cast<const uint4*>(xs + i);
+      if (!(Vec<T>::top(v4) >= from)) continue;
+      float v[N];
+      Vec<T>::get(v4, v);
+#pragma unroll
+      for (int e = 0; e < N; ++e) f(i + e, clean(v[e]));
     }
   };
-  F2 sum = {0, 0};
-  kept([&](int, F2 (&w)[N]) {
+
+  // ---- (tau, n_tau): keys above tau are kept, and the n_tau first of those equal to it
+  unsigned tau = key_of(-INFINITY), n_tau = 0;  // -inf itself is never drawn
+  bool use_k = r.use_k;
+  constexpr int kB = kKeys / kThreads;
+  // One border: the first key, falling, by which the count reaches k (by_mass: the mass reaches
+  // p of all).  Rounds over keys [lo, hi], 10 bits of them each; keys below tau_k do not take
+  // part and n_k of those equal to it do.  false: it is not reached.
+  auto border = [&](bool by_mass, unsigned tau_k, unsigned n_k, unsigned* key, unsigned long long* left) {
+    unsigned hi = m_key, lo = max(tau_k, key_of(by_mass ? fmaxf(reach(sc, kCut), -FLT_MAX) : -FLT_MAX));
+    unsigned long long goal = (unsigned)r.k, above = 0;
+    const unsigned long long w_k = by_mass && n_k > 0 ? n_k * fix<43>(weight(sc, of_key(tau_k))) : 0ull;
+    for (bool first = true;; first = false) {
+      const int bits = 32 - __clz(hi - lo), sh_r = max(0, bits - kDigit);
+      for (int b = t; b < kKeys; b += kThreads) sh.count[b] = 0, sh.mass[b] = 0;
+      if (t == 0) sh.found = -1;
+      __syncthreads();
+      each(of_key(lo), [&](int, float x) {
+        const unsigned kk = key_of(x);
+        if (kk < lo || kk > hi) return;
+        const int b = (int)((hi - kk) >> sh_r);
+        if (!by_mass) {
+          atomicAdd(&sh.count[b], 1u);
+        } else if (kk > tau_k || n_k == 0) {
+          atomicAdd(&sh.mass[b], fix<43>(weight(sc, x)));
+        }
+      });
+      if (by_mass && n_k > 0 && rank == 0 && t == 0 && tau_k >= lo && tau_k <= hi)
+        atomicAdd(&sh.mass[(hi - tau_k) >> sh_r], w_k);
+      cl.sync();
+      unsigned long long v[kB], mine = 0;
 #pragma unroll
-    for (int e = 0; e < N; ++e) sum = add(sum, w[e]);
-    return true;
-  });
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum = shfl_add(sum, o);
-  if (lane == 0) sh.wsum[warp] = fix<43>(sum);
-  sync_row();
-  if (t < C * kWarps) sh.all_sum[t] = peer(sh.wsum, t / kWarps)[t % kWarps];
-  __syncthreads();
-  // the first segment whose running sum exceeds the target (else the last with any mass): lane l
-  // has segments [l kS, (l + 1) kS)
-  constexpr int kS = (C * kWarps + 31) / 32;
-  unsigned long long seg_w[kS], inc = 0;
-#pragma unroll
-  for (int e = 0; e < kS; ++e) {
-    seg_w[e] = lane * kS + e < C * kWarps ? sh.all_sum[lane * kS + e] : 0ull;
-    inc += seg_w[e];
-  }
-  unsigned long long run = inc;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long x = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += x;
-  }
-  const unsigned long long total = __shfl_sync(0xffffffffu, inc, 31);
-  const unsigned long long target = part_of(total, u_row);
-  run = inc - run;
-  int mine_at = -1;  // this lane's first segment past the target, else its last with any mass
-  unsigned long long mine_before = 0;
-  bool past = false;
-#pragma unroll
-  for (int e = 0; e < kS; ++e) {
-    if (seg_w[e] > 0 && !past) mine_at = lane * kS + e, mine_before = run, past = run + seg_w[e] > target;
-    run += seg_w[e];
-  }
-  const unsigned hit_lanes = __ballot_sync(0xffffffffu, past), any_lanes = __ballot_sync(0xffffffffu, mine_at >= 0);
-  int owner = -1;
-  unsigned long long before = 0;
-  if (any_lanes) {
-    const int from_lane = hit_lanes ? __ffs(hit_lanes) - 1 : 31 - __clz(any_lanes);
-    owner = __shfl_sync(0xffffffffu, mine_at, from_lane);
-    before = __shfl_sync(0xffffffffu, mine_before, from_lane);
-  }
-  if (owner < 0 && rank == 0 && t == 0) {  // min-p above 1: nothing is left
-    p.tokens[row] = -1;
-    if (p.probs) p.probs[row] = 0.f;
-  }
-  if (owner == rank * kWarps + warp) {
-    int token = -1;  // so far: the last kept position seen
-    float wt = 0.f;
-    kept([&](int i0, F2 (&w)[N]) {
-      unsigned long long f[N], mine = 0;
-#pragma unroll
-      for (int e = 0; e < N; ++e) f[e] = fix<43>(w[e]), mine += f[e];
+      for (int b = 0; b < kB; ++b) {
+        v[b] = 0;
+        for (int c = 0; c < kC; ++c) {
+          const int at = t * kB + b;
+          v[b] += by_mass ? cl.map_shared_rank(sh.mass, c)[at] : cl.map_shared_rank(sh.count, c)[at];
+        }
+        mine += v[b];
+      }
       unsigned long long inc = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const unsigned long long x = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += x;
       }
-      // this lane's first position past the target, else its last kept one
-      unsigned long long cum = before + (inc - mine);
-      float my_w = 0.f;
-      int my = -1;
-      bool hit = false;
+      if (lane == 31) sh.red_l[warp] = inc;
+      __syncthreads();
+      unsigned long long run = above + inc - mine, all = 0;
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) run += sh.red_l[w];
+        all += sh.red_l[w];
+      }
+      if (first && by_mass) {
+        bool more;
+        goal = part_of(all, r.p, &more);
+        goal = max(goal + more, 1ull);  // the first always stays
+      }
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        cum += f[e];
-        if (f[e] > 0 && !hit) {
-          my = i0 + lane * N + e;
-          my_w = w[e].h;
-          hit = cum > target;
-        }
+      for (int b = 0; b < kB; ++b) {
+        if (run < goal && run + v[b] >= goal) sh.found = t * kB + b, sh.found_l = run;
+        run += v[b];
       }
-      const unsigned hits = __ballot_sync(0xffffffffu, hit), any = __ballot_sync(0xffffffffu, my >= 0);
-      if (any) {
-        const int from_lane = hits ? __ffs(hits) - 1 : 31 - __clz(any);
-        token = __shfl_sync(0xffffffffu, my, from_lane);
-        wt = __shfl_sync(0xffffffffu, my_w, from_lane);
+      cl.sync();  // every CTA has read the others' bins; its own find is visible to it
+      const int b = sh.found;
+      const unsigned long long found_l = sh.found_l;
+      __syncthreads();  // read before the next round resets it
+      if (b < 0) return false;
+      above = found_l;
+      hi -= (unsigned)b << sh_r;
+      lo = max(lo, hi - ((1u << sh_r) - 1));
+      if (sh_r == 0) {
+        *key = hi;
+        *left = goal - above;
+        return true;
       }
-      before += __shfl_sync(0xffffffffu, inc, 31);
-      return hits == 0;
-    });
-    if (lane == 0) {
-      p.tokens[row] = token >= 0 ? first + token : -1;
-      if (p.probs) p.probs[row] = token >= 0 ? wt / ((float)total * 0x1p-43f) : 0.f;
+    }
+  };
+  unsigned long long left;
+  if (use_k) {
+    if (border(false, 0, 0, &tau, &left))
+      n_tau = (unsigned)left;
+    else
+      use_k = false;  // fewer than k candidates: all stay
+  }
+  if (r.use_p) {
+    const unsigned n_k = n_tau;
+    unsigned key;
+    if (border(true, tau, n_k, &key, &left)) {
+      // of the keys equal to it: those before which less than the goal lies
+      const F2 w = weight(sc, of_key(key));
+      const double each_w = (double)w.h + (double)w.l;
+      const unsigned n = (unsigned)fmin(ceil((double)left * 0x1p-43 / each_w - 1e-9), 2e9);
+      n_tau = key == tau && n_k > 0 ? min(n_k, max(n, 1u)) : max(n, 1u);
+      tau = key;
     }
   }
-  sync_row();  // no CTA leaves while another reads its shared memory
+
+  // ---- ties at tau before each warp's segment
+  const bool ties = use_k || r.use_p;
+  unsigned my_ties = 0, ties_before = 0;
+  if (ties) {
+    each(of_key(tau), [&](int i, float x) { my_ties += key_of(x) == tau && i >= sl.begin && i < sl.count; });
+    my_ties = __reduce_add_sync(0xffffffffu, my_ties);
+    if (lane == 0) sh.wties[warp] = my_ties;
+    cl.sync();
+    if (t < kC * kWarps) sh.all_ties[t] = cl.map_shared_rank(sh.wties, t / kWarps)[t % kWarps];
+    __syncthreads();
+    for (int w = 0; w < rank * kWarps + warp; ++w) ties_before += sh.all_ties[w];
+  }
+  // the kept weights of positions i + lane N .. of this warp's segment (in order: `rank0` ties so far)
+  const float from = fmaxf(fmaxf(reach(sc, kCut), of_key(tau)), r.lo > 0.f && r.lo < 1.f ? reach(sc, -log2f(r.lo) + 0.01f) : -INFINITY);
+  const bool some = ties && ties_before < n_tau && ties_before + my_ties > n_tau;  // the n-th tie is here
+  const bool whole = ties && ties_before + my_ties <= n_tau;
+  auto kept = [&](int i, unsigned& rank0, F2 (&w)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) w[e] = F2{0.f, 0.f};
+    const uint4 v4 = *reinterpret_cast<const uint4*>(xs + i + lane * N);
+    if (!__any_sync(0xffffffffu, Vec<T>::top(v4) >= from)) return;  // nothing kept here
+    float v[N];
+    Vec<T>::get(v4, v);
+    unsigned eq = 0, at = 0;
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = clean(v[e]);
+    if (some) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) eq += key_of(v[e]) == tau && i + lane * N + e >= sl.begin && i + lane * N + e < sl.count;
+      unsigned inc = eq;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      at = rank0 + inc - eq;
+      rank0 += __shfl_sync(0xffffffffu, inc, 31);
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const unsigned kk = key_of(v[e]);
+      bool in = kk > tau;
+      if (ties && kk == tau) in = some ? at++ < n_tau : whole;
+      if (in) {
+        w[e] = weight(sc, v[e]);
+        if (below(w[e], r.lo)) w[e] = F2{0.f, 0.f};
+      }
+    }
+  };
+  F2 sum = {0, 0};
+  unsigned rank0 = ties_before;
+  for (int i = warp * seg; i < (warp + 1) * seg; i += 32 * N) {
+    F2 w[N];
+    kept(i, rank0, w);
+#pragma unroll
+    for (int e = 0; e < N; ++e) sum = add(sum, w[e]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum = shfl_add(sum, o);
+  if (lane == 0) sh.wsum[warp] = fix<43>(sum);
+  cl.sync();
+  if (t < kC * kWarps) sh.all_sum[t] = cl.map_shared_rank(sh.wsum, t / kWarps)[t % kWarps];
+  __syncthreads();
+  // the first segment whose running sum exceeds the target (else the last with any mass): lane l
+  // has segments [l kS, (l + 1) kS)
+  constexpr int kS = kC * kWarps / 32;
+  unsigned long long inc = 0;
+#pragma unroll
+  for (int e = 0; e < kS; ++e) inc += sh.all_sum[lane * kS + e];
+  unsigned long long run = inc;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  const unsigned long long total = __shfl_sync(0xffffffffu, inc, 31), target = part_of(total, r.u);
+  run = inc - run;
+  int mine_at = -1;  // this lane's first segment past the target, else its last with any mass
+  unsigned long long mine_before = 0;
+  bool past = false;
+#pragma unroll
+  for (int e = 0; e < kS; ++e) {
+    const unsigned long long x = sh.all_sum[lane * kS + e];
+    if (x > 0 && !past) mine_at = lane * kS + e, mine_before = run, past = run + x > target;
+    run += x;
+  }
+  const unsigned hits = __ballot_sync(0xffffffffu, past), any = __ballot_sync(0xffffffffu, mine_at >= 0);
+  int owner = -1;
+  unsigned long long before = 0;
+  if (any) {
+    const int from_lane = hits ? __ffs(hits) - 1 : 31 - __clz(any);
+    owner = __shfl_sync(0xffffffffu, mine_at, from_lane);
+    before = __shfl_sync(0xffffffffu, mine_before, from_lane);
+  }
+  if (owner < 0 && rank == 0 && t == 0) put(q, row, -1, 0.f);  // min-p above 1: nothing is left
+  if (owner == rank * kWarps + warp) {
+    int token;
+    F2 w;
+    rank0 = ties_before;
+    walk<N>(seg, before, target, [&](int i0, F2 (&ws)[N]) { kept(warp * seg + i0, rank0, ws); }, &token, &w);
+    if (lane == 0)
+      put(q, row, token >= 0 ? sl.first + warp * seg + token : -1, token >= 0 ? prob_of(w, total) : 0.f);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) select_kernel(const SampleParams q) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ SelectShared sh;
+  cg::cluster_group cl = cg::this_cluster();
+  tc::pdl_wait();
+  if (threadIdx.x < 128) sh.table[threadIdx.x] = q.table[threadIdx.x];
+  const int clusters = gridDim.x / kC, mine = blockIdx.x / kC;
+  const int t = threadIdx.x, warp = t >> 5;
+  // this cluster's rows are mine, mine + clusters, ..: kThreads of them looked at together.  Every
+  // CTA reads the same marks: a row's token is written only after barriers that follow the look.
+  for (int64_t i0 = 0; mine + i0 * clusters < q.rows; i0 += kThreads) {
+    const int64_t row = mine + (i0 + t) * clusters;
+    const unsigned left = __ballot_sync(0xffffffffu, row < q.rows && q.tokens[row] == kRetry);
+    if ((t & 31) == 0) sh.todo[warp] = left;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) {
+      for (unsigned m = sh.todo[w]; m; m &= m - 1) {
+        const int64_t at = mine + (i0 + w * 32 + __ffs(m) - 1) * clusters;
+        select_row<T>(q, (int)at, reinterpret_cast<T*>(smem), sh, cl);
+        cl.sync();  // the row's exchanges are over
+      }
+    }
+    __syncthreads();
+  }
 }
 
 struct Powers {  // 2^(j / 128) as pairs of floats
@@ -928,22 +1183,50 @@ struct Powers {  // 2^(j / 128) as pairs of floats
 };
 
 template <typename T, int C>
-cudaError_t launch(const SampleParams& p, cudaStream_t st) {
+cudaError_t launch_stream(SampleParams p, cudaStream_t st) {
   static std::atomic<unsigned long long> attr{0};
-  if (cudaError_t e = smem_attr_once(sample_kernel<T, C>, kSliceBytes, attr); e != cudaSuccess) return e;
-  constexpr int step = Vec<T>::N * kThreads;
+  if (cudaError_t e = smem_attr_once(stream_kernel<T, C>, kStreamSmem, attr); e != cudaSuccess) return e;
+  p.per = (p.vocab + 7 + C - 1) / C;  // (up to 7 positions before an unaligned row)
+  p.per = (p.per + 7) / 8 * 8;
   cudaLaunchConfig_t c = {};
   cudaLaunchAttribute a[1];
   a[0].id = cudaLaunchAttributeClusterDimension;
   a[0].val.clusterDim.x = C;
   a[0].val.clusterDim.y = a[0].val.clusterDim.z = 1;
   c.gridDim = dim3(p.rows * C);
+  c.blockDim = dim3(kST);
+  c.dynamicSmemBytes = kStreamSmem;
+  c.stream = st;
+  c.attrs = a;
+  c.numAttrs = C > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&c, stream_kernel<T, C>, p);
+}
+
+template <typename T>
+cudaError_t launch(SampleParams p, int sms, cudaStream_t st) {
+  // one CTA per row where rows fill the SMs; eight where they do not, and the row is long enough
+  const bool few = p.rows < sms && (int64_t)p.vocab * (int)sizeof(T) > 2 * kStageBytes;
+  cudaError_t e = few ? launch_stream<T, 8>(p, st) : launch_stream<T, 1>(p, st);
+  if (e != cudaSuccess) return e;
+  static std::atomic<unsigned long long> attr{0};
+  if (e = smem_attr_once(select_kernel<T>, kSliceBytes, attr); e != cudaSuccess) return e;
+  p.per = (p.vocab + 7 + kC - 1) / kC;
+  p.per = (p.per + 7) / 8 * 8;
+  constexpr int step = Vec<T>::N * kThreads;
+  cudaLaunchConfig_t c = {};
+  cudaLaunchAttribute a[2];
+  a[0].id = cudaLaunchAttributeClusterDimension;
+  a[0].val.clusterDim.x = kC;
+  a[0].val.clusterDim.y = a[0].val.clusterDim.z = 1;
+  a[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[1].val.programmaticStreamSerializationAllowed = 1;
+  c.gridDim = dim3(std::min(p.rows, std::max(1, 2 * sms / kC)) * kC);
   c.blockDim = dim3(kThreads);
   c.dynamicSmemBytes = (p.per + step - 1) / step * step * sizeof(T);
   c.stream = st;
   c.attrs = a;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, sample_kernel<T, C>, p);
+  c.numAttrs = 2;
+  return cudaLaunchKernelEx(&c, select_kernel<T>, p);
 }
 
 }  // namespace
@@ -964,10 +1247,10 @@ extern "C" int dflash_sample(const void* logits, int64_t row_stride, int32_t dty
   SampleParams p{logits, row_stride, rows, vocab, u, temperature, top_p, min_p, top_k, tokens, probs, 0, {}};
   static const Powers powers;
   memcpy(p.table, powers.table, sizeof p.table);
-  p.per = (vocab + 7 + kMaxC - 1) / kMaxC;  // (up to 7 positions before an unaligned row)
-  p.per = (p.per + 7) / 8 * 8;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == DFLASH_F32 ? launch<float, kMaxC>(p, st) : launch<__nv_bfloat16, kMaxC>(p, st);
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e == cudaSuccess) e = dtype == DFLASH_F32 ? launch<float>(p, sms, st) : launch<__nv_bfloat16>(p, sms, st);
   if (e != cudaSuccess) return call_error(DFLASH_ECUDA, "sample", e);
   return DFLASH_OK;
 }
