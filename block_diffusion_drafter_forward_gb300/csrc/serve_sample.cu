@@ -253,14 +253,13 @@ struct Slice {
 
 // Walks a stretch of a row in order for the first position whose running mass exceeds `target`
 // (else the last with any mass).  One warp; step(i, w) gives the kept weights w of positions
-// i + lane * N ..; `before`: the mass ahead of the stretch; *passed: whether the target was.
+// i + lane * N ..; `before`: the mass ahead of the stretch.
 template <int N, typename F>
 __device__ __forceinline__ void walk(int n, unsigned long long before, unsigned long long target, F&& step, int* token,
-                                     F2* weight_out, bool* passed = nullptr) {
+                                     F2* weight_out) {
   const int lane = threadIdx.x & 31;
   *token = -1;
   *weight_out = F2{0.f, 0.f};
-  if (passed) *passed = true;
   for (int i0 = 0; i0 < n; i0 += 32 * N) {
     F2 w[N];
     step(i0, w);
@@ -295,7 +294,6 @@ __device__ __forceinline__ void walk(int n, unsigned long long before, unsigned 
     if (hits) return;
     before += __shfl_sync(0xffffffffu, inc, 31);
   }
-  if (passed) *passed = false;
 }
 
 __device__ __forceinline__ float prob_of(F2 w, unsigned long long total) {  // total in units of 2^-43
@@ -310,8 +308,9 @@ __device__ __forceinline__ void put(const SampleParams& q, int row, int token, f
 constexpr int kST = 256, kSW = kST / 32;     // threads, warps
 constexpr int kStages = 3, kVec = 4;         // ring: blocks in flight; vectors of a thread in a block
 constexpr int kStageBytes = kST * kVec * 16; // 16 KB
-constexpr int kList = 2048;                  // logits that a list holds
-constexpr int kAim = 1536;                   // and that the floor may aim at
+constexpr int kList = 4096;                  // places that a list holds
+constexpr int kAim = 3072;                   // and that the floor may aim at
+constexpr int kSorted = 2048;                // logits of the sorted prefix
 constexpr int kBins = 256;                   // histogram of the list
 constexpr int kLook = 64;                    // bins of the look at the first blocks
 constexpr float kFar = 32.f;                 // their range of t, below the maximum found there
@@ -319,7 +318,9 @@ constexpr float kFar = 32.f;                 // their range of t, below the maxi
 // 2^-22; the correction's and the tree's roundings 5 2^-24), and the error a probability may carry
 constexpr float kNear = 12.f;
 constexpr float kFastError = 1.4e-6f, kProbError = 8e-8f;
-constexpr int kStreamSmem = kStages * kStageBytes + kList * 8;
+constexpr int kListBytes = kList * 4;         // = the sorted prefix: kSorted * 8
+static_assert(kListBytes == kSorted * 8 && kList * 8 + kSorted * 8 <= kStages * kStageBytes, "shared memory is used twice");
+constexpr int kStreamSmem = kStages * kStageBytes + kListBytes;
 
 struct Stretch {  // mass of a warp's part of a block, relative to ref; `far`: what of it came in fp32
   float h, l, far, ref;
@@ -341,12 +342,13 @@ __global__ void __launch_bounds__(kST, 3) stream_kernel(const SampleParams q) {
   constexpr int N = Vec<T>::N, kBlock = kST * kVec * N, kWarpPart = kVec * 32 * N;
   extern __shared__ __align__(16) uint8_t smem[];
   uint4* ring = reinterpret_cast<uint4*>(smem);
-  unsigned long long* list = reinterpret_cast<unsigned long long*>(smem + kStages * kStageBytes);
-  Stretch* stretch = reinterpret_cast<Stretch*>(list);
-  // once the row is through, the ring holds: the row's list, and places by index
+  unsigned* places = reinterpret_cast<unsigned*>(smem + kStages * kStageBytes);  // the list: vocabulary indices
+  Stretch* stretch = reinterpret_cast<Stretch*>(places);
+  unsigned long long* list = reinterpret_cast<unsigned long long*>(places);      // then: the sorted prefix
+  // once the row is through, the ring holds: the row's list as (~key, index), and places by index
   unsigned long long* final_list = reinterpret_cast<unsigned long long*>(smem);
   unsigned* index = reinterpret_cast<unsigned*>(smem + kList * 8);
-  unsigned* by = index + kList;
+  unsigned* by = index + kSorted;
   __shared__ StreamShared sh;
   cg::cluster_group cl = cg::this_cluster();
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -423,9 +425,10 @@ __global__ void __launch_bounds__(kST, 3) stream_kernel(const SampleParams q) {
     }
     sync_row();
     if (warp == 0) {
-      // lane l: bins 2 l, 2 l + 1 of the row's first blocks.  The first bin by which, going by them,
-      // the list holds what the filter needs: k and half as many more, a p of the mass with a quarter
-      // of the rest, every t up to min-p's
+      // lane l: bins 2 l, 2 l + 1 of the row's first blocks.  The first bins by which, going by them,
+      // the list holds what the filter needs: k and half as many more; all but 1 - p of the mass
+      // (the mass left out, as the blocks seen have it, against that seen alone: the few large
+      // weights of a row may lie anywhere) and some 192 logits; every t up to min-p's
       unsigned a = 0, b = 0;
       for (int c = 0; c < C; ++c) a += peer(sh.count, c)[2 * lane], b += peer(sh.count, c)[2 * lane + 1];
       const float wa = a * exp2f(-(2 * lane + 0.5f) * (kFar / kLook)), wb = b * exp2f(-(2 * lane + 1.5f) * (kFar / kLook));
@@ -444,7 +447,7 @@ __global__ void __launch_bounds__(kST, 3) stream_kernel(const SampleParams q) {
       if (r.use_k)
         enough = n >= (1.5f * r.k + 64.f) * share;
       else if (r.use_p)
-        enough = w >= (0.75f + 0.25f * r.p) * whole;
+        enough = (whole - w) * 1.3f <= (1.f - r.p) * whole * share && n >= 192.f * share;
       else
         enough = end > -log2f(r.lo) + 0.5f;
       const unsigned yes = __ballot_sync(0xffffffffu, enough), fits = __ballot_sync(0xffffffffu, n <= kAim * share);
@@ -524,7 +527,7 @@ stream:
             const float c = clean(x[e]);
             if (c >= floor_x && c > -INFINITY) {
               const unsigned at = atomicAdd(&sh.n_list, 1u);
-              if (at < kList) list[at] = (unsigned long long)~key_of(c) << 32 | (unsigned)(sl.first + pos_of(b, v) + e);
+              if (at < kList) places[at] = (unsigned)(sl.first + pos_of(b, v) + e);
             } else if (sum && finite) {
               rest += ex2((c - m) * sc.c_hi);
             }
@@ -651,35 +654,62 @@ stream:
     __syncthreads();
     const bool mine_past = sh.pick[0] != 0x7fffffff;
     const bool owner = mine_past || (rank == last && target >= total);  // u >= 1: the row's last kept one
-    if (owner && warp == 0) {
+    if (owner) {  // the whole CTA walks the stretch: thread t has its positions 4 t .. 4 t + 3 (N = 8) or 2 t, 2 t + 1
+      constexpr int kE = kWarpPart / kST;
       const int at = mine_past ? sh.pick[0] : sh.pick[1];
-      const int i1 = at / kSW * kBlock + at % kSW * kWarpPart;
-      const unsigned long long before = mine_past ? sh.before : 0ull;
-      auto weights = [&](int i0, F2 (&ws)[N]) {
-        const int i = i1 + i0 + lane * N;
-        const uint4 y4 = sl.whole(i) ? *reinterpret_cast<const uint4*>(sl.at(i)) : sl.edge(i);
-        float x[N];
-        Vec<T>::get(y4, x);
+      const int i0 = at / kSW * kBlock + at % kSW * kWarpPart + t * kE;
+      const unsigned long long before = mine_past ? sh.before : 0ull, goal = mine_past ? target : ~0ull;
+      F2 w[kE];
+      unsigned long long f[kE], sum_w = 0;
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const float c = clean(x[e]);
-          ws[e] = c > -INFINITY ? weight(sc, c) : F2{0.f, 0.f};
-        }
-      };
-      int token, token2;
-      F2 w;
-      const unsigned long long goal = mine_past ? target : ~0ull;
-      walk<N>(kWarpPart, before, goal - (mine_past ? slack : 0), weights, &token, &w);
-      bool sure = token >= 0;
-      if (slack && mine_past) {  // the same token at both ends of the error, inside this stretch
-        walk<N>(kWarpPart, before, target + slack, weights, &token2, &w, &sure);
-        sure = sure && token2 == token && before + slack <= target;
+      for (int e = 0; e < kE; ++e) {
+        const int i = i0 + e;
+        const float c = i >= sl.begin && i < sl.count ? clean(Elem<T>::to_f(*sl.at(i))) : -INFINITY;
+        w[e] = c > -INFINITY ? weight(sc, c) : F2{0.f, 0.f};
+        f[e] = fix<43>(w[e]);
+        sum_w += f[e];
       }
-      if (q.probs) sure = sure && (float)far * kFastError <= (float)total * kProbError;
-      if (exact || sure) {
-        if (lane == 0) put(q, row, token >= 0 ? sl.first + i1 + token : -1, token >= 0 ? prob_of(w, total) : 0.f);
-      } else if (lane == 0) {
-        for (int c = 0; c < C; ++c) *peer(&sh.bad, c) = 1;  // stream the row again
+      unsigned long long cum = sum_w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long x = __shfl_up_sync(0xffffffffu, cum, o);
+        if (lane >= o) cum += x;
+      }
+      if (t == 0) sh.pick[0] = 0x7fffffff, sh.pick[1] = -1;
+      __syncthreads();  // (and red_l has been read)
+      if (lane == 31) sh.red_l[warp] = cum;
+      __syncthreads();
+      cum = before + cum - sum_w;
+      for (int x = 0; x < warp; ++x) cum += sh.red_l[x];
+      // the first position past the target, else the last with any mass
+      int hit = -1, any = -1;
+      unsigned long long from[2] = {0, 0}, run2 = cum;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        if (f[e] > 0) {
+          any = i0 + e;
+          if (hit < 0 && run2 + f[e] > goal) hit = i0 + e, from[0] = run2, from[1] = run2 + f[e];
+        }
+        run2 += f[e];
+      }
+      if (hit >= 0) atomicMin(&sh.pick[0], hit);
+      if (any >= 0) atomicMax(&sh.pick[1], any);
+      __syncthreads();
+      const int token = sh.pick[0] != 0x7fffffff ? sh.pick[0] : sh.pick[1];
+      if (token >= i0 && token < i0 + kE) {
+        F2 tw = w[0];
+#pragma unroll
+        for (int e = 1; e < kE; ++e)
+          if (token == i0 + e) tw = w[e];
+        // sure: the fp32 sums' error moves neither border of the token past the target, nor the
+        // probability's last bit
+        bool sure = exact || !mine_past ||
+                    (token == hit && (from[0] == 0 || from[0] + slack <= target) && from[1] > target + slack);
+        if (q.probs && !exact) sure = sure && (float)far * kFastError <= (float)total * kProbError;
+        if (sure)
+          put(q, row, sl.first + token, prob_of(tw, total));
+        else
+          for (int c = 0; c < C; ++c) *peer(&sh.bad, c) = 1;  // stream the row again
       }
     }
     if (exact) return;
@@ -687,7 +717,7 @@ stream:
     if (!sh.bad) return;
     exact = true;
     __syncthreads();
-    if (t == 0) sh.pick[0] = 0x7fffffff, sh.pick[1] = -1, sh.far = 0;
+    if (t == 0) sh.pick[0] = 0x7fffffff, sh.pick[1] = -1, sh.far = 0, sh.bad = 0;
     m = m_row;  // every stretch by the row's maximum now
     for (int b = 0; b < kStages; ++b) issue(b);
     __syncthreads();
@@ -703,8 +733,11 @@ stream:
     const int n = (int)min(sh.n_list, (unsigned)kList);
     bool full = sh.n_list > kList;
     for (int i = t; i < n; i += kST) {
-      const unsigned at = C > 1 ? atomicAdd(n_at, 1u) : i;
-      if (at < kList) dst[at] = list[i]; else full = true;
+      const unsigned at = C > 1 ? atomicAdd(n_at, 1u) : i, place = places[i];
+      if (at < kList)
+        dst[at] = (unsigned long long)~key_of(clean(Elem<T>::to_f(sl.src[place]))) << 32 | place;
+      else
+        full = true;
     }
     if (C == 1 && t == 0) sh.n_final = n;
     if (full) atomicOr(peer(&sh.bad, 0), 1u);
@@ -728,7 +761,7 @@ stream:
     const float x = of_key(~(unsigned)(final_list[i] >> 32));
     const int b = bin_of(t_of(sc, x));
     atomicAdd(&sh.count[b], 1u);
-    if (sum) atomicAdd(&sh.mass[b], fix<52>(weight(sc, x)));
+    if (sum) atomicAdd(&sh.mass[b], fix<51>(weight(sc, x)));  // (4096 of them, and the rest, below 2^64)
   }
   __syncthreads();
   auto scan_l = [&](unsigned long long v, unsigned long long* all) {  // sum over lower threads
@@ -761,9 +794,10 @@ stream:
     unsigned long long whole;
     const unsigned long long run = scan_l(sh.mass[t], &whole) + sh.mass[t];
     bool more;
-    goal = part_of(whole + (sh.rest << 9), r.p, &more);
+    goal = part_of(whole + (sh.rest << 8), r.p, &more);
     goal += more;
     here = run >= goal;
+    goal = goal >> 63 ? ~0ull : goal << 1;  // in the sorted prefix's units
   } else if (r.use_k) {
     here = cum >= (unsigned)r.k;
   } else {  // min-p: t <= -log2(min_p), allowing for rounding
@@ -781,6 +815,10 @@ stream:
   if (t == 0) sh.n_list = 0;
   __syncthreads();
   const int n = (int)sh.red_u[0];
+  if (n > kSorted) {
+    if (t == 0) q.tokens[row] = kRetry;
+    return;
+  }
   int n2 = 64;
   while (n2 < n) n2 *= 2;
   for (int i = t; i < n_all; i += kST) {
@@ -808,7 +846,7 @@ stream:
   sort(list, n2);  // by (falling logit, index)
   // thread t has items [t per, (t + 1) per): weights (units of 2^-52) and their running sum
   const int per = max(1, n2 / kST), i0 = t * per;
-  constexpr int kPer = kList / kST;
+  constexpr int kPer = kSorted / kST;
   unsigned long long mine = 0;
   unsigned low = 0;  // items below min-p
 #pragma unroll 1
