@@ -20,9 +20,12 @@
 // 2^8 (P <= 2^8 stays exact in range, the normalised result is the same).
 //
 // Rounding: P is bf16 (the MMA's operand type), sums and O fp32, the normaliser sums the fp32 P.
-// Warp roles: 0-3 stream 0, 4-7 stream 1, 8 K pages, 9 MMA issue, 10 V pages, 11 zeroes the key
-// rows behind a sequence's end in its last V page (never-written rows may hold NaN, and 0 * NaN
-// would reach O; their scores are masked by select).
+// Warp roles: 0-3 stream 0, 4-7 stream 1, 8 K pages, 10 V pages, 9 and 11 MMA issue.  The V warp
+// also zeroes the key rows behind a sequence's end in its last page (never-written rows may hold
+// NaN, and 0 * NaN would reach O; their scores are masked by select).  Issuing an MMA blocks its
+// thread while the tensor pipe's queue is full, so with two tiles each stream has a warp of its own
+// (one that issued for both left the pipe idle between the streams: 614 against 4xx us for a prompt
+// of 8192); with one tile a single thread keeps the chunks in order over both streams.
 #include <float.h>
 
 #include <atomic>
@@ -222,6 +225,53 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// two fp32 in one register pair, and the packed operations on them (sm_100 and on)
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t r, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 64 columns of this lane's TMEM row, without the wait; ld_wait ties the registers to it
+__device__ __forceinline__ void ld64(uint32_t taddr, float (&v)[64]) {
+  __syncwarp();
+#define R8(i) "=f"(v[i]), "=f"(v[i + 1]), "=f"(v[i + 2]), "=f"(v[i + 3]), "=f"(v[i + 4]), "=f"(v[i + 5]), "=f"(v[i + 6]), "=f"(v[i + 7])
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
+      : R8(0), R8(8), R8(16), R8(24), R8(32), R8(40), R8(48), R8(56)
+      : "r"(taddr));
+#undef R8
+}
+__device__ __forceinline__ void ld_wait(float (&a)[64], float (&b)[64]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 64; ++i) asm volatile("" : "+f"(a[i]), "+f"(b[i]));
+}
+__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t (&v)[32]) {  // 32 columns, without the wait
+  __syncwarp();
+#define R8(i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::R8(0),
+      R8(8), R8(16), R8(24), "r"(taddr)
+      : "memory");
+#undef R8
+}
+__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -327,7 +377,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == 8 || warp == 10) {
       // ---- page producers: lane l copies page l of a chunk.  The page ids of the next chunk are
-      // fetched while the warp waits for a slot.
+      // fetched while the warp waits for a slot.  V of a chunk whose last page is part full (or that
+      // has no page) lands on v_raw; the V warp zeroes its rows behind the end when it has come,
+      // between its other work.
       const int kv = warp == 10;
       uint64_t* full = kv ? c.v_full : c.k_full;
       uint64_t* empty = kv ? c.v_empty : c.k_empty;
@@ -337,6 +389,28 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
       Seg q;
       int i = 0;
       bool stop = false;
+      uint32_t used = 0;                 // parity of each slot's v_raw
+      int tail_b = -1, tail_page = 0, tail_live = 0;  // the slot to zero in; its last page, rows to keep there
+      auto mend = [&] {                  // waits for it; false: gave up
+        if (tail_b < 0) return true;
+        if (!__all_sync(0xffffffffu, mbar_wait_ab(&c.v_raw[tail_b], (used >> tail_b) & 1, flags))) return false;
+        uint4* v = reinterpret_cast<uint4*>(sV + tail_b * C::kSlot + tail_page * C::kTile);
+        for (int e = lane; e < HD * 2; e += 32) {  // 16 bytes: 8 keys of one dim, (d / 8, key / 8, d % 8)
+          const int j0 = (e >> 3 & 1) * 8;
+          if (j0 >= tail_live) {
+            v[e] = make_uint4(0, 0, 0, 0);
+          } else if (j0 + 8 > tail_live) {
+            __nv_bfloat16* x = reinterpret_cast<__nv_bfloat16*>(v + e);
+            for (int k = tail_live - j0; k < 8; ++k) x[k] = __float2bfloat16(0.f);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c.v_full[tail_b]);
+        used ^= 1u << tail_b;
+        tail_b = -1;
+        return true;
+      };
       while (!stop && w.next(p, h, q)) {
         const int pages = (q.kv + kPage - 1) / kPage;
         auto fetch = [&](int ch) {
@@ -346,14 +420,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         int page = fetch(q.c_lo);
         for (int ch = q.c_lo; ch < q.c_hi; ++ch, ++i) {
           const int b = i % slots;
-          if (i >= slots && !mbar_wait_ab(&empty[b], (i / slots - 1) & 1, flags)) {
-            stop = true;
-            break;
+          if (i >= slots) {
+            const uint32_t par = (i / slots - 1) & 1;
+            // meanwhile the pending page (votes keep the warp together); the wait below is the bound
+            for (long long n = 0; tail_b >= 0 && n < kSpinLimit; ++n) {
+              if (__any_sync(0xffffffffu, flags[0] || mbar_test_wait(&empty[b], par))) break;
+              if (__any_sync(0xffffffffu, mbar_test_wait(&c.v_raw[tail_b], (used >> tail_b) & 1))) mend();
+            }
+            if (!mbar_wait_ab(&empty[b], par, flags)) {
+              stop = true;
+              break;
+            }
           }
           const int key = q.k0 + ch * kKeys;
           const int np = max(0, min(kPages, pages - key / kPage));
-          // V of a chunk whose last page is part full (or that has no page) goes by the zeroing warp
           const bool tail = kv && (np == 0 || key + np * kPage > q.kv);
+          if (tail && !mend()) {  // one at a time
+            stop = true;
+            break;
+          }
           uint64_t* bar = tail ? &c.v_raw[b] : &full[b];
           if (lane == 0) mbar_arrive_expect_tx(bar, np * C::kTile);
           __syncwarp();
@@ -366,50 +451,107 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
                                        ((int64_t)q.g * 2 + kv) * (kPage * HD);
             bulk_load(ring + b * C::kSlot + lane * C::kTile, src, C::kTile, bar);
           }
+          if (tail) {
+            tail_b = b;
+            tail_page = max(0, np - 1);
+            tail_live = np == 0 ? 0 : q.kv - key - tail_page * kPage;
+          }
           page = fetch(ch + 1);
         }
       }
-    } else if (warp == 9) {
-      // ---- MMA issue (lane 0): each stream alternates S and P V; whichever is ready goes out
-      if (lane == 0) {
-        constexpr uint32_t id_s = idesc_bf16(128, kKeys), id_o = idesc_bf16(128, HD);
+      if (!stop) mend();
+    } else if (lane == 0) {
+      // ---- MMA issue
+      constexpr uint32_t id_s = idesc_bf16(128, kKeys), id_o = idesc_bf16(128, HD);
+      // operand descriptors of the first tiles; the others are further on (16-byte units)
+      const uint64_t dQ = desc_noswz(sQ, 128, HD * 16), dK = desc_noswz(sK, 128, HD * 16), dV = desc_noswz(sV, 128, 256);
+      auto issue_s = [&](int x, int kb) {
+        const uint64_t q = dQ + (uint64_t)((NT == 2 ? x : 0) * (C::kQ / 16)), k = dK + (uint64_t)(kb * (C::kSlot / 16));
+#pragma unroll
+        for (int d = 0; d < HD / 16; ++d) mma_bf16(tmem + x * 128, q + d * 16, k + d * 16, id_s, d > 0 ? 1u : 0u);
+      };
+      auto issue_pv = [&](int x, int vb, int np, bool more) {  // 16 keys = 8 TMEM columns of P each
+        const uint64_t v = dV + (uint64_t)(vb * (C::kSlot / 16));
+        const uint32_t tS = tmem + x * 128, tO = tmem + 256 + x * 128;
+        if (np == kPages) {
+#pragma unroll
+          for (int k = 0; k < kPages; ++k) mma_bf16_tmem_a(tO, tS + k * 8, v + k * (C::kTile / 16), id_o, k > 0 || more ? 1u : 0u);
+        } else {
+          for (int k = 0; k < np; ++k) mma_bf16_tmem_a(tO, tS + k * 8, v + k * (C::kTile / 16), id_o, k > 0 || more ? 1u : 0u);
+        }
+      };
+      if (NT == 2) {
+        // one stream: S of a chunk, then its P V and the next S as soon as the softmax has written P
+        const int x = warp == 9 ? 0 : 1;
+        Walk w = walk;
+        Seg q;
+        int kc = 0, it = 0, act = 0;
+        auto wait = [&](uint64_t* bar, int phase) {
+          if (!mbar_wait_ab(bar, phase & 1, flags)) flags[0] = 1;  // after a timeout: commits only, no MMAs
+        };
+        auto s_of = [&](int kc) {
+          const int kb = kc % C::kNK;
+          wait(&c.k_full[kb], kc / C::kNK);
+          tc_fence_after();
+          if (!flags[0]) issue_s(x, kb);
+          mma_commit(&c.s_full[x]);
+          mma_commit(&c.k_empty[kb]);
+        };
+        while (w.next(p, h, q)) {
+          const int n = q.c_hi - q.c_lo;
+          if (!It<NT>::active(h, q, x)) {
+            // no row of this stream: it still follows every slot, so that its waits stay exact
+            for (int j = 0; j < n; ++j, ++kc) {
+              wait(&c.k_full[kc % C::kNK], kc / C::kNK);
+              mbar_arrive(&c.k_empty[kc % C::kNK]);
+              wait(&c.v_full[kc % C::kNV], kc / C::kNV);
+              mbar_arrive(&c.v_empty[kc % C::kNV]);
+            }
+            continue;
+          }
+          wait(&c.q_full[x], act);
+          s_of(kc);
+          for (int j = 0; j < n; ++j, ++kc, ++it) {
+            const int vb = kc % C::kNV;
+            const int np = max(1, min(kPages, (q.kv - q.k0 - (q.c_lo + j) * kKeys + kPage - 1) / kPage));
+            wait(&c.v_full[vb], kc / C::kNV);
+            if (j == 0 && act > 0) wait(&c.o_free[x], act - 1);
+            wait(&c.p_full[x], it);
+            tc_fence_after();
+            if (!flags[0]) issue_pv(x, vb, np, j > 0);
+            mma_commit(&c.o_done[x]);
+            mma_commit(&c.v_empty[vb]);
+            if (j + 1 < n) s_of(kc + 1);
+          }
+          ++act;
+        }
+      } else if (warp == 9) {
+        // both streams: each alternates S and P V; whichever is ready goes out
         It<NT> its[2];
         bool pv[2] = {false, false};
         its[0].start(p, h, walk, 0);
         its[1].start(p, h, walk, 1);
         long long idle = 0;
-        int s_out = 0;  // one tile: S of the segment issued so far
+        int s_out = 0;  // S of the segment issued so far
         // A wait by parity is exact only while the phase before the awaited one is known complete, so
-        // a stream may not run ahead of the other by a ring.  One tile: S and P V go out in chunk
-        // order over both streams.  Two tiles: stream 1, which can skip segments, keeps within a
-        // ring of stream 0, which works in all of them.
-        int s_next = 0, pv_next = 0;  // chunks whose S / P V is out (two tiles: stream 0's)
-        auto s_turn = [&](int x, int kc) { return NT == 1 ? kc == s_next : x == 0 || s_next > kc - C::kNK; };
-        auto pv_turn = [&](int x, int kc) { return NT == 1 ? kc == pv_next : x == 0 || pv_next > kc - C::kNV; };
+        // no stream may run ahead of the other by a ring: S and P V go out in chunk order over both.
+        int s_next = 0, pv_next = 0;  // chunks whose S / P V is out
         while (its[0].valid || its[1].valid) {
           bool did = false;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             It<NT>& a = its[x];
-            const uint32_t tS = tmem + x * 128, tO = tmem + 256 + x * 128;
             const bool give_up = flags[0];  // after a timeout: commits only, no MMAs
             if (a.valid && pv[x]) {
               const int kc = a.kc0 + a.j, vb = kc % C::kNV;
-              const int segs = NT == 2 ? a.act : a.seg;
-              if (give_up || (pv_turn(x, kc) && mbar_test_wait(&c.p_full[x], a.it & 1) &&
+              if (give_up || (kc == pv_next && mbar_test_wait(&c.p_full[x], a.it & 1) &&
                               mbar_test_wait(&c.v_full[vb], (kc / C::kNV) & 1) &&
-                              (!a.first(x) || segs == 0 || mbar_test_wait(&c.o_free[NT == 2 ? x : 0], (segs - 1) & 1)))) {
+                              (!a.first(x) || a.seg == 0 || mbar_test_wait(&c.o_free[0], (a.seg - 1) & 1)))) {
                 tc_fence_after();
-                if (!give_up) {
-                  const int np = max(1, a.pages());
-                  for (int k = 0; k < np; ++k)  // 16 keys = 8 TMEM columns of P each
-                    mma_bf16_tmem_a(tO, tS + k * 8, desc_noswz(sV + vb * C::kSlot + k * C::kTile, 128, 256), id_o,
-                                    (!a.first(x) || k > 0) ? 1u : 0u);
-                }
+                if (!give_up) issue_pv(x, vb, max(1, a.pages()), !a.first(x));
                 mma_commit(&c.o_done[x]);
                 mma_commit(&c.v_empty[vb]);
-                if (NT == 2 && x == 0 && !It<NT>::active(h, a.sg, 1)) mma_commit(&c.v_empty[vb]);
-                if (NT == 1 || x == 0) ++pv_next;
+                ++pv_next;
                 pv[x] = false;
                 a.step(p, h, x);
                 did = true;
@@ -417,25 +559,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
             }
             if (a.valid && !pv[x]) {
               const int kc = a.kc0 + a.j, kb = kc % C::kNK;
-              if (give_up || (s_turn(x, kc) && mbar_test_wait(&c.k_full[kb], (kc / C::kNK) & 1) &&
-                              (!a.first(x) || mbar_test_wait(&c.q_full[NT == 2 ? x : 0], (NT == 2 ? a.act : a.seg) & 1)))) {
+              if (give_up || (kc == s_next && mbar_test_wait(&c.k_full[kb], (kc / C::kNK) & 1) &&
+                              (!a.first(x) || mbar_test_wait(&c.q_full[0], a.seg & 1)))) {
                 tc_fence_after();
-                if (!give_up) {
-                  const uint8_t* q = sQ + (NT == 2 ? x : 0) * C::kQ;
-                  const uint8_t* k = sK + kb * C::kSlot;
-#pragma unroll
-                  for (int d = 0; d < HD / 16; ++d)
-                    mma_bf16(tS, desc_noswz(q + d * 256, 128, HD * 16), desc_noswz(k + d * 256, 128, HD * 16), id_s,
-                             d > 0 ? 1u : 0u);
-                }
+                if (!give_up) issue_s(x, kb);
                 mma_commit(&c.s_full[x]);
                 mma_commit(&c.k_empty[kb]);
-                if (NT == 2 && x == 0 && !It<NT>::active(h, a.sg, 1)) mma_commit(&c.k_empty[kb]);
-                if (NT == 1 && ++s_out == a.n) {  // both streams' S read the same queries
+                if (++s_out == a.n) {  // both streams' S read the same queries
                   mma_commit(&c.q_empty);
                   s_out = 0;
                 }
-                if (NT == 1 || x == 0) ++s_next;
+                ++s_next;
                 pv[x] = true;
                 did = true;
               }
@@ -445,43 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
           if (idle > kSpinLimit) flags[0] = 1;
         }
       }
-      __syncwarp();
-    } else {
-      // ---- zero the rows behind the sequence's end in its last V page (keys >= kv)
-      Walk w = walk;
-      Seg q;
-      int i = 0;
-      uint32_t used = 0;  // parity of each slot's v_raw
-      bool stop = false;
-      while (!stop && w.next(p, h, q)) {
-        const int pages = (q.kv + kPage - 1) / kPage;
-        const int n = q.c_hi - q.c_lo;
-        const int key = q.k0 + (q.c_hi - 1) * kKeys;  // only a unit's last chunk can reach past the end
-        const int np = max(0, min(kPages, pages - key / kPage));
-        i += n;
-        if (np > 0 && key + np * kPage <= q.kv) continue;
-        const int b = (i - 1) % C::kNV;
-        if (!mbar_wait_ab(&c.v_raw[b], (used >> b) & 1, flags)) {
-          stop = true;
-          break;
-        }
-        used ^= 1u << b;
-        const int lp = max(0, np - 1), live = np == 0 ? 0 : q.kv - key - lp * kPage;  // rows of the page to keep
-        uint4* v = reinterpret_cast<uint4*>(sV + b * C::kSlot + lp * C::kTile);
-        for (int e = lane; e < HD * 2; e += 32) {  // 16 bytes: 8 keys of one dim, (d / 8, key / 8, d % 8)
-          const int j0 = (e >> 3 & 1) * 8;
-          if (j0 >= live) {
-            v[e] = make_uint4(0, 0, 0, 0);
-          } else if (j0 + 8 > live) {
-            __nv_bfloat16* x = reinterpret_cast<__nv_bfloat16*>(v + e);
-            for (int k = live - j0; k < 8; ++k) x[k] = __float2bfloat16(0.f);
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c.v_full[b]);
-      }
     }
+    __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ---- softmax streams: thread = query row `row` of its tile
@@ -549,8 +648,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         if (warp_valid) {
           const int kb = q.k0 + (q.c_lo + j) * kKeys;
           float a[64], b[64];
-          tmem_ld64(tS, a);
-          tmem_ld64(tS + 64, b);
+          ld64(tS, a);
+          ld64(tS + 64, b);
+          ld_wait(a, b);
           if (__any_sync(0xffffffffu, kb < lo || kb + kKeys > hi)) {
             const unsigned span = hi > lo ? (unsigned)(hi - lo) : 0u;
 #pragma unroll
@@ -582,23 +682,31 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
             }
           }
           const float off = m_new == -INFINITY ? 0.f : -m_new;
-          float l0 = 0.f, l1 = 0.f;
+          const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), off2 = pair(off, off);
+          uint64_t l0 = 0, l1 = 0;  // two sums of pairs
           uint32_t pk[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const float u = ex2(fmaf(a[2 * e], p.scale_log2, off)), v = ex2(fmaf(a[2 * e + 1], p.scale_log2, off));
-            l0 += u, l1 += v;
+            float u, v;
+            unpair(fma2(pair(a[2 * e], a[2 * e + 1]), scale2, off2), u, v);
+            u = ex2(u), v = ex2(v);
+            if (e & 1) l0 = add2(l0, pair(u, v)); else l1 = add2(l1, pair(u, v));
             pk[e] = pack_bf16(u, v);
           }
-          tmem_st32u(tS, pk);
+          st32(tS, pk);
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const float u = ex2(fmaf(b[2 * e], p.scale_log2, off)), v = ex2(fmaf(b[2 * e + 1], p.scale_log2, off));
-            l0 += u, l1 += v;
+            float u, v;
+            unpair(fma2(pair(b[2 * e], b[2 * e + 1]), scale2, off2), u, v);
+            u = ex2(u), v = ex2(v);
+            if (e & 1) l0 = add2(l0, pair(u, v)); else l1 = add2(l1, pair(u, v));
             pk[e] = pack_bf16(u, v);
           }
-          tmem_st32u(tS + 32, pk);
-          l = l * alpha + (l0 + l1);
+          st32(tS + 32, pk);
+          st_wait();
+          float lu, lv;
+          unpair(add2(l0, l1), lu, lv);
+          l = l * alpha + (lu + lv);
           m = m_new;
         }
         tc_fence_before();
