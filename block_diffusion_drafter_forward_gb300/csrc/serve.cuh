@@ -12,6 +12,20 @@ namespace dflash {
 // Records `msg` (and the CUDA error's text) for dflash_last_error(NULL); returns `code`.
 int call_error(int code, const char* msg, cudaError_t e = cudaSuccess) noexcept;
 
+#ifdef __CUDACC__
+// 32 bytes: one store (a whole sector) where they are aligned, which the host knows (`wide`)
+__device__ __forceinline__ void put32(void* d, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(d)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(d)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+#endif
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // 0, or the status of pages that the kernels do not take.

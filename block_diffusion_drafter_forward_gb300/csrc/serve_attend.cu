@@ -127,7 +127,7 @@ extern "C" int dflash_attend(const dflash_kv_pages* kv, const void* q, int64_t q
     return call_error(DFLASH_EINVAL, "attend: rows below n_q_heads * head_dim, or q, out or a stride not whole 16 bytes");
   AttendParams p{q, out, lse, kv->pool, page_tables, kv_lens, row_starts, kv->status, q_stride, out_stride, kv->page_stride,
                  nb, n_rows, max_pages_per_seq, kv->num_pages, n_q_heads, kv->n_kv_heads, window, causal != 0,
-                 scale * 1.4426950408889634f};
+                 reinterpret_cast<uintptr_t>(out) % 32 == 0 && (out_stride * es) % 32 == 0, scale * 1.4426950408889634f};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (kv->dtype == DFLASH_BF16) {
     int sms = 0;

@@ -15,6 +15,7 @@ struct AttendParams {
   uint32_t* status;
   int64_t q_stride, out_stride, page_stride;  // elements
   int nb, n_rows, mpps, num_pages, nh, nkv, window, causal;
+  bool wide_out;     // rows of out start on 32 bytes
   float scale_log2;  // scale * log2(e): scores are exponents of 2
 };
 

@@ -45,6 +45,12 @@ constexpr int kThreads = 384;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtl = 2944;                      // barriers, plan, row exchange
 
+// The wait of tc_common.cuh with its first poll ahead of the abort flag: most waits find their phase
+// complete, and a shared-memory read costs hundreds of cycles while MMAs saturate its bandwidth.
+__device__ __forceinline__ bool wait_ab(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return mbar_try_wait(bar, parity) || mbar_wait_ab(bar, parity, abort);
+}
+
 // Slots of the index space a unit occupies beside its chunks: the cost of opening a segment
 // (queries, pipeline restart, output) in chunks.
 constexpr int kUnitCost = 3;
@@ -118,7 +124,7 @@ struct Walk {
 
 struct Ctl {
   uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6], v_raw[6];
-  uint64_t s_full[2], p_full[2], o_done[2], o_free[2], q_full[2], q_empty;
+  uint64_t s_full[2], p_half[2], p_full[2], o_done[2], o_free[2], q_full[2], q_empty;
   uint32_t tmem_slot;
   int flags[2];
   int s0, tile0, found;
@@ -356,6 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.s_full[i], 1);
+      mbar_init(&c.p_half[i], 128);
       mbar_init(&c.p_full[i], 128);
       mbar_init(&c.o_done[i], 1);
       mbar_init(&c.o_free[i], NT == 2 ? 128 : 256);
@@ -393,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
       int tail_b = -1, tail_page = 0, tail_live = 0;  // the slot to zero in; its last page, rows to keep there
       auto mend = [&] {                  // waits for it; false: gave up
         if (tail_b < 0) return true;
-        if (!__all_sync(0xffffffffu, mbar_wait_ab(&c.v_raw[tail_b], (used >> tail_b) & 1, flags))) return false;
+        if (!__all_sync(0xffffffffu, wait_ab(&c.v_raw[tail_b], (used >> tail_b) & 1, flags))) return false;
         uint4* v = reinterpret_cast<uint4*>(sV + tail_b * C::kSlot + tail_page * C::kTile);
         for (int e = lane; e < HD * 2; e += 32) {  // 16 bytes: 8 keys of one dim, (d / 8, key / 8, d % 8)
           const int j0 = (e >> 3 & 1) * 8;
@@ -427,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
               if (__any_sync(0xffffffffu, flags[0] || mbar_test_wait(&empty[b], par))) break;
               if (__any_sync(0xffffffffu, mbar_test_wait(&c.v_raw[tail_b], (used >> tail_b) & 1))) mend();
             }
-            if (!mbar_wait_ab(&empty[b], par, flags)) {
+            if (!wait_ab(&empty[b], par, flags)) {
               stop = true;
               break;
             }
@@ -470,14 +477,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
 #pragma unroll
         for (int d = 0; d < HD / 16; ++d) mma_bf16(tmem + x * 128, q + d * 16, k + d * 16, id_s, d > 0 ? 1u : 0u);
       };
-      auto issue_pv = [&](int x, int vb, int np, bool more) {  // 16 keys = 8 TMEM columns of P each
+      auto issue_pv = [&](int x, int vb, int k0, int k1, bool more) {  // pages k0 .. k1 - 1: 16 keys = 8 TMEM columns of P each
         const uint64_t v = dV + (uint64_t)(vb * (C::kSlot / 16));
         const uint32_t tS = tmem + x * 128, tO = tmem + 256 + x * 128;
-        if (np == kPages) {
+        if (k1 - k0 == kPages / 2) {
 #pragma unroll
-          for (int k = 0; k < kPages; ++k) mma_bf16_tmem_a(tO, tS + k * 8, v + k * (C::kTile / 16), id_o, k > 0 || more ? 1u : 0u);
+          for (int k = 0; k < kPages / 2; ++k)
+            mma_bf16_tmem_a(tO, tS + (k0 + k) * 8, v + (k0 + k) * (C::kTile / 16), id_o, k0 + k > 0 || more ? 1u : 0u);
         } else {
-          for (int k = 0; k < np; ++k) mma_bf16_tmem_a(tO, tS + k * 8, v + k * (C::kTile / 16), id_o, k > 0 || more ? 1u : 0u);
+          for (int k = k0; k < k1; ++k) mma_bf16_tmem_a(tO, tS + k * 8, v + k * (C::kTile / 16), id_o, k > 0 || more ? 1u : 0u);
         }
       };
       if (NT == 2) {
@@ -487,11 +495,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         Seg q;
         int kc = 0, it = 0, act = 0;
         auto wait = [&](uint64_t* bar, int phase) {
-          if (!mbar_wait_ab(bar, phase & 1, flags)) flags[0] = 1;  // after a timeout: commits only, no MMAs
+          if (!wait_ab(bar, phase & 1, flags)) flags[0] = 1;  // after a timeout: commits only, no MMAs
         };
-        auto s_of = [&](int kc) {
+        auto s_of = [&](int kc) {  // (its K has been waited for)
           const int kb = kc % C::kNK;
-          wait(&c.k_full[kb], kc / C::kNK);
           tc_fence_after();
           if (!flags[0]) issue_s(x, kb);
           mma_commit(&c.s_full[x]);
@@ -509,16 +516,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
             }
             continue;
           }
+          wait(&c.k_full[kc % C::kNK], kc / C::kNK);
           wait(&c.q_full[x], act);
           s_of(kc);
           for (int j = 0; j < n; ++j, ++kc, ++it) {
             const int vb = kc % C::kNV;
             const int np = max(1, min(kPages, (q.kv - q.k0 - (q.c_lo + j) * kKeys + kPage - 1) / kPage));
+            // what the softmax does not decide is waited for while it runs
+            if (j + 1 < n) wait(&c.k_full[(kc + 1) % C::kNK], (kc + 1) / C::kNK);
             wait(&c.v_full[vb], kc / C::kNV);
             if (j == 0 && act > 0) wait(&c.o_free[x], act - 1);
+            wait(&c.p_half[x], it);  // P of the first 64 keys, while the exponentials of the others run
+            tc_fence_after();
+            if (!flags[0]) issue_pv(x, vb, 0, min(np, kPages / 2), j > 0);
             wait(&c.p_full[x], it);
             tc_fence_after();
-            if (!flags[0]) issue_pv(x, vb, np, j > 0);
+            if (!flags[0]) issue_pv(x, vb, kPages / 2, np, true);
             mma_commit(&c.o_done[x]);
             mma_commit(&c.v_empty[vb]);
             if (j + 1 < n) s_of(kc + 1);
@@ -548,7 +561,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
                               mbar_test_wait(&c.v_full[vb], (kc / C::kNV) & 1) &&
                               (!a.first(x) || a.seg == 0 || mbar_test_wait(&c.o_free[0], (a.seg - 1) & 1)))) {
                 tc_fence_after();
-                if (!give_up) issue_pv(x, vb, max(1, a.pages()), !a.first(x));
+                if (!give_up) {
+                  const int np = max(1, a.pages());
+                  issue_pv(x, vb, 0, min(np, kPages / 2), !a.first(x));
+                  issue_pv(x, vb, kPages / 2, np, true);
+                }
                 mma_commit(&c.o_done[x]);
                 mma_commit(&c.v_empty[vb]);
                 ++pv_next;
@@ -638,11 +655,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
       int done = 0;
 #pragma unroll 1
       for (int j = NT == 2 ? 0 : x; j < n; j += NT == 2 ? 1 : 2, ++it, ++done) {
-        if (!mbar_wait_ab(&c.s_full[x], it & 1, flags)) flags[0] = 1;
+        if (!wait_ab(&c.s_full[x], it & 1, flags)) flags[0] = 1;
         tc_fence_after();
         const bool load_next = j == n - 1 && more && loads_after(q);
         if (load_next) {  // once every S that reads this segment's queries is done
-          if (NT == 1 && !mbar_wait_ab(&c.q_empty, seg & 1, flags)) flags[0] = 1;
+          if (NT == 1 && !wait_ab(&c.q_empty, seg & 1, flags)) flags[0] = 1;
           load_q(nq);
         }
         if (warp_valid) {
@@ -661,16 +678,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
           }
           float m0 = a[0], m1 = b[0], m2 = a[1], m3 = b[1];
 #pragma unroll
-          for (int e = 2; e < 64; e += 2) {
-            m0 = fmaxf(m0, a[e]), m1 = fmaxf(m1, b[e]);
-            m2 = fmaxf(m2, a[e + 1]), m3 = fmaxf(m3, b[e + 1]);
+          for (int e = 2; e < 62; e += 4) {
+            m0 = fmaxf(m0, fmaxf(a[e], a[e + 1])), m1 = fmaxf(m1, fmaxf(b[e], b[e + 1]));
+            m2 = fmaxf(m2, fmaxf(a[e + 2], a[e + 3])), m3 = fmaxf(m3, fmaxf(b[e + 2], b[e + 3]));
           }
+          m0 = fmaxf(m0, fmaxf(a[62], a[63])), m1 = fmaxf(m1, fmaxf(b[62], b[63]));
           const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * p.scale_log2;
           const bool grow = top > m + 8.f;  // (m = -inf: any finite score)
           const float m_new = grow ? top : m;
           const float alpha = grow && m != -INFINITY ? ex2(m - m_new) : 1.f;
           if (done > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-            if (!mbar_wait_ab(&c.o_done[x], (it - 1) & 1, flags)) flags[0] = 1;
+            if (!wait_ab(&c.o_done[x], (it - 1) & 1, flags)) flags[0] = 1;
             tc_fence_after();
 #pragma unroll 1
             for (int d = 0; d < HD; d += 32) {
@@ -694,6 +712,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
             pk[e] = pack_bf16(u, v);
           }
           st32(tS, pk);
+          if (NT == 2) {
+            st_wait();
+            tc_fence_before();
+            mbar_arrive(&c.p_half[x]);
+          }
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             float u, v;
@@ -710,6 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
           m = m_new;
         }
         tc_fence_before();
+        if (NT == 2 && !warp_valid) mbar_arrive(&c.p_half[x]);
         mbar_arrive(&c.p_full[x]);
         if (load_next) q_ready();
       }
@@ -719,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
       float w0 = 1.f, w1 = 0.f;  // weights of O 0 and O 1 in this row
       bool use1 = false;
       // this stream's O: its last P V done, hence every earlier one
-      if (done > 0 && !mbar_wait_ab(&c.o_done[x], (it - 1) & 1, flags)) flags[0] = 1;
+      if (done > 0 && !wait_ab(&c.o_done[x], (it - 1) & 1, flags)) flags[0] = 1;
       if (NT == 1) {  // and the other's, with its (m, l)
         c.ml[x][row] = make_float2(m, l);
         named_barrier(1 + (warp & 3), 64);
@@ -765,9 +789,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
           if (!valid) continue;
           if (whole) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4*>(dst + d + e) = make_uint4(pack_bf16(v[e], v[e + 1]), pack_bf16(v[e + 2], v[e + 3]),
-                                                                  pack_bf16(v[e + 4], v[e + 5]), pack_bf16(v[e + 6], v[e + 7]));
+            for (int e = 0; e < 32; e += 16) {
+              uint32_t w[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) w[k] = pack_bf16(v[e + 2 * k], v[e + 2 * k + 1]);
+              put32(dst + d + e, w, p.wide_out);
+            }
           } else {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)

@@ -163,17 +163,6 @@ template <typename T>
 __device__ __forceinline__ void copy16(T* d, const T* s) {
   *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>(s);
 }
-// 32 bytes; one store where they are aligned (the pages' base and stride decide, `wide`)
-__device__ __forceinline__ void put32(void* d, const uint32_t (&w)[8], bool wide) {
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-  } else {
-    static_cast<uint4*>(d)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    static_cast<uint4*>(d)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  }
-}
 __device__ __forceinline__ void put_keys(__nv_bfloat16* d, const uint32_t (&r)[8], bool wide) {  // dims x, x + 1 of 8 keys
   uint32_t w[8];
 #pragma unroll
