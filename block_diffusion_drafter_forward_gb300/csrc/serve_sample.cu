@@ -1,21 +1,22 @@
 // One token per row of logits by temperature, top-k, top-p and min-p (dflash_sample).
 //
 // In falling order of the logits every filter keeps a prefix, and the prefix is short in most
-// rows: so the row is read once, and only the logits near its maximum are held.
-//   stream_kernel: a CTA (or a cluster of 8, when rows are few) streams a row through a ring in
-//     shared memory, with the running maximum m.  Logits from a floor on, which a look at the row's
-//     first blocks sets, go to a list; top-p alone also sums the mass of the others.  At the end a
-//     histogram of the list (counts, masses) over t = (m - x) log2(e) / T says how far the prefix
-//     reaches; that part, usually a few dozen logits, is sorted, and its weights' running sums give
-//     the kept prefix and the token.  Rows without a short prefix by right (temperature alone)
-//     sum every warp's stretches of the row in index order, rescaled as m grows; the stretch that
-//     holds u * total is read again.  Vectors whose logits are all far below m (t > 12) go in fp32,
-//     with a bound on their error: where the token could depend on it, or the probability's last
-//     bit (flat rows; a few in a hundred others), the row is streamed once more with exact weights.
-//   select_kernel: rows whose prefix did not fit in the list (flat ones) have their slice in the
-//     shared memory of a cluster of 8 and find (tau, n) - the lowest kept logit, and how many of
-//     those equal to it stay - by histograms over the logits' order-preserving keys, 10 bits a
-//     round, with exact counts (top-k) and masses (top-p); then sum stretches as above.
+// rows: so the row is read once, and only the logits near its maximum are held.  A CTA (a cluster
+// of up to 8, when rows are few) streams a row through a ring in shared memory:
+//   - a look at the first blocks sets a floor; logits from it on go to a list, and top-p alone also
+//     sums the mass of the others.  A histogram of the list (counts, masses) over
+//     t = (m - x) log2(e) / T, m the largest logit, says how far the prefix reaches; that part,
+//     usually a few dozen logits, is sorted, and its weights' running sums give the kept prefix and
+//     the token.
+//   - rows without a short prefix by right (temperature alone) sum every warp's stretches of the
+//     row in index order, rescaled as m grows; the stretch that holds u * total is read again.
+//     Vectors whose logits are all far below m (t > 12) go in fp32, with a bound on their error:
+//     where the token could depend on it, or the probability's last bit (flat rows; a few in a
+//     hundred others), the row is streamed once more with exact weights.
+//   - rows whose prefix is longer than the list are streamed again (from L2, mostly): histograms
+//     over the logits' order-preserving keys, 10 bits a pass, with exact counts (top-k) and masses
+//     (top-p), find (tau, n): the lowest kept logit, and how many of those equal to it stay; then
+//     stretches of the kept weights are summed as above.
 // Bound by HBM: one read of the logits (the finishing phases of some CTAs overlap the streaming of
 // others; three CTAs per SM with 32 KB of copies in flight each).
 //
@@ -41,7 +42,6 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr float kCut = 40.f;                 // weights below 2^-40 are 0
-constexpr int kRetry = -2;                   // a row that stream_kernel leaves to select_kernel
 
 struct SampleParams {
   const void* logits;
@@ -51,7 +51,7 @@ struct SampleParams {
   const int32_t* top_k;
   int32_t* tokens;
   float* probs;
-  int per;  // positions of a CTA's slice (a multiple of 8)
+  int ctas, per;  // CTAs of a row; positions of a CTA's slice (a multiple of 8)
   float2 table[128];  // 2^(j / 128) as pairs
 };
 
@@ -205,6 +205,28 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// two fp32 in one register pair, and the packed operations on them (sm_100 and on)
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t r, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ float clean(float x) { return x == x ? x + 0.f : -INFINITY; }  // NaN: -inf, -0: +0
 
 struct Row {  // a row's settings
@@ -251,51 +273,6 @@ struct Slice {
   }
 };
 
-// Walks a stretch of a row in order for the first position whose running mass exceeds `target`
-// (else the last with any mass).  One warp; step(i, w) gives the kept weights w of positions
-// i + lane * N ..; `before`: the mass ahead of the stretch.
-template <int N, typename F>
-__device__ __forceinline__ void walk(int n, unsigned long long before, unsigned long long target, F&& step, int* token,
-                                     F2* weight_out) {
-  const int lane = threadIdx.x & 31;
-  *token = -1;
-  *weight_out = F2{0.f, 0.f};
-  for (int i0 = 0; i0 < n; i0 += 32 * N) {
-    F2 w[N];
-    step(i0, w);
-    unsigned long long f[N], mine = 0;
-#pragma unroll
-    for (int e = 0; e < N; ++e) f[e] = fix<43>(w[e]), mine += f[e];
-    unsigned long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long x = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += x;
-    }
-    unsigned long long cum = before + (inc - mine);
-    F2 my_w = {0.f, 0.f};
-    int my = -1;
-    bool hit = false;
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      cum += f[e];
-      if (f[e] > 0 && !hit) {
-        my = i0 + lane * N + e;
-        my_w = w[e];
-        hit = cum > target;
-      }
-    }
-    const unsigned hits = __ballot_sync(0xffffffffu, hit), any = __ballot_sync(0xffffffffu, my >= 0);
-    if (any) {
-      const int from = hits ? __ffs(hits) - 1 : 31 - __clz(any);
-      *token = __shfl_sync(0xffffffffu, my, from);
-      *weight_out = F2{__shfl_sync(0xffffffffu, my_w.h, from), __shfl_sync(0xffffffffu, my_w.l, from)};
-    }
-    if (hits) return;
-    before += __shfl_sync(0xffffffffu, inc, 31);
-  }
-}
-
 __device__ __forceinline__ float prob_of(F2 w, unsigned long long total) {  // total in units of 2^-43
   return (float)(((double)w.h + (double)w.l) / ((double)total * 0x1p-43));
 }
@@ -304,55 +281,72 @@ __device__ __forceinline__ void put(const SampleParams& q, int row, int token, f
   if (q.probs) q.probs[row] = prob;
 }
 
-// ------------------------------------------------------------------ stream_kernel
+// Keys that differ by one for neighbouring values of the type
+template <typename T>
+__device__ __forceinline__ unsigned digit_key(float x) {
+  return sizeof(T) == 2 ? key_of(x) >> 16 : key_of(x);
+}
+template <typename T>
+__device__ __forceinline__ float of_digit_key(unsigned k) {
+  if (sizeof(T) == 2) return __uint_as_float((k & 0x8000u ? k ^ 0x8000u : ~k & 0xffffu) << 16);
+  return of_key(k);
+}
+
 constexpr int kST = 256, kSW = kST / 32;     // threads, warps
 constexpr int kStages = 3, kVec = 4;         // ring: blocks in flight; vectors of a thread in a block
 constexpr int kStageBytes = kST * kVec * 16; // 16 KB
+constexpr int kMaxC = 8;                     // CTAs of a row
 constexpr int kList = 4096;                  // places that a list holds
 constexpr int kAim = 3072;                   // and that the floor may aim at
 constexpr int kSorted = 2048;                // logits of the sorted prefix
 constexpr int kBins = 256;                   // histogram of the list
-constexpr int kLook = 64;                    // bins of the look at the first blocks
-constexpr float kFar = 32.f;                 // their range of t, below the maximum found there
+constexpr int kLook = 64;                    // bins of the look at the first blocks,
+constexpr float kLookNear = 12.f, kLookFar = 32.f;  // and their ranges of t below the maximum found there
+constexpr int kDigit = 10, kKeys = 1 << kDigit;     // histograms over keys
 // Far masses in fp32: a bound on their relative error (x - m rounded: t 2^-25 ln 2 < 8.3e-7; ex2
 // 2^-22; the correction's and the tree's roundings 5 2^-24), and the error a probability may carry
 constexpr float kNear = 12.f;
 constexpr float kFastError = 1.4e-6f, kProbError = 8e-8f;
-constexpr int kListBytes = kList * 4;         // = the sorted prefix: kSorted * 8
-static_assert(kListBytes == kSorted * 8 && kList * 8 + kSorted * 8 <= kStages * kStageBytes, "shared memory is used twice");
-constexpr int kStreamSmem = kStages * kStageBytes + kListBytes;
+// Shared memory beside the ring, in turn: the list's places; a list's sorted prefix; the
+// stretches; the digits' histograms (the stretches are not needed yet)
+constexpr int kSideBytes = 16384;
+static_assert(kList * 4 == kSideBytes && kSorted * 8 == kSideBytes && kKeys * 16 == kSideBytes, "one size");
+static_assert(kList * 8 + kSorted * 8 <= kStages * kStageBytes, "the row's list, and places by index, fit in the ring");
+constexpr int kStreamSmem = kStages * kStageBytes + kSideBytes;
 
 struct Stretch {  // mass of a warp's part of a block, relative to ref; `far`: what of it came in fp32
   float h, l, far, ref;
 };
 
-struct StreamShared {
+struct Shared {
   float2 table[128];
   unsigned count[kBins];
   unsigned long long mass[kBins];
   unsigned long long red_l[kSW], rest, best, before, part, far, far_part;
-  unsigned red_u[kSW];
-  unsigned m_key, n_list, n_final, bad;
+  unsigned red_u[kSW], ties;
+  unsigned m_key, n_list, n_final, full, again;
   float floor;
   int pick[2];
 };
 
-template <typename T, int C>
-__global__ void __launch_bounds__(kST, 3) stream_kernel(const SampleParams q) {
+template <typename T>
+__global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
   constexpr int N = Vec<T>::N, kBlock = kST * kVec * N, kWarpPart = kVec * 32 * N;
   extern __shared__ __align__(16) uint8_t smem[];
   uint4* ring = reinterpret_cast<uint4*>(smem);
-  unsigned* places = reinterpret_cast<unsigned*>(smem + kStages * kStageBytes);  // the list: vocabulary indices
-  Stretch* stretch = reinterpret_cast<Stretch*>(places);
-  unsigned long long* list = reinterpret_cast<unsigned long long*>(places);      // then: the sorted prefix
+  uint8_t* side = smem + kStages * kStageBytes;
+  unsigned* places = reinterpret_cast<unsigned*>(side);                        // the list: vocabulary indices
+  unsigned long long* list = reinterpret_cast<unsigned long long*>(side);      // the sorted prefix
+  Stretch* stretch = reinterpret_cast<Stretch*>(side);
+  unsigned* digits = reinterpret_cast<unsigned*>(side);                        // counts, or masses in four parts
   // once the row is through, the ring holds: the row's list as (~key, index), and places by index
   unsigned long long* final_list = reinterpret_cast<unsigned long long*>(smem);
   unsigned* index = reinterpret_cast<unsigned*>(smem + kList * 8);
   unsigned* by = index + kSorted;
-  __shared__ StreamShared sh;
+  __shared__ Shared sh;
   cg::cluster_group cl = cg::this_cluster();
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const int rank = C > 1 ? (int)cl.block_rank() : 0, row = blockIdx.x / C;
+  const int C = q.ctas, rank = C > 1 ? (int)cl.block_rank() : 0, row = blockIdx.x / C;
   auto sync_row = [&] {
     if (C > 1) cl.sync(); else __syncthreads();
   };
@@ -373,14 +367,33 @@ __global__ void __launch_bounds__(kST, 3) stream_kernel(const SampleParams q) {
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  for (int b = 0; b < kStages; ++b) issue(b);
+  // f(block, its vectors, their largest logits) over the slice; the first blocks are on their way
+  auto stream = [&](auto&& f) {
+#pragma unroll 1
+    for (int b = 0; b < blocks; ++b) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      uint4 x4[kVec];
+      float tops[kVec];
+#pragma unroll
+      for (int v = 0; v < kVec; ++v) {
+        x4[v] = ring[(b % kStages * kVec + v) * kST + t];
+        tops[v] = Vec<T>::top(x4[v]);
+      }
+      f(b, x4, tops, [&] { issue(b + kStages); });
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  };
+  auto start = [&] {
+    for (int b = 0; b < kStages; ++b) issue(b);
+  };
+  start();
   const Row r = row_of(q, row);
   if (t < 128) sh.table[t] = q.table[t];
   if (t < kBins) sh.count[t] = 0, sh.mass[t] = 0;
   if (t == 0) {
     sh.m_key = 0;
-    sh.n_list = sh.n_final = sh.bad = 0;
-    sh.rest = sh.best = sh.far = 0;
+    sh.n_list = sh.n_final = sh.full = sh.again = 0;
+    sh.rest = sh.best = sh.far = sh.part = 0;
     sh.pick[0] = 0x7fffffff;
     sh.pick[1] = -1;
   }
@@ -391,13 +404,16 @@ __global__ void __launch_bounds__(kST, 3) stream_kernel(const SampleParams q) {
   }
   __syncthreads();
   // ---- the first blocks' maximum
+  const int seen = min(blocks, kStages);
   float top = -INFINITY;
-  for (int b = 0; b < min(blocks, kStages); ++b) {
+  for (int b = 0; b < seen; ++b) {
 #pragma unroll
     for (int v = 0; v < kVec; ++v) top = fmaxf(top, Vec<T>::top(ring[(b * kVec + v) * kST + t]));
   }
-  unsigned w_key = __reduce_max_sync(0xffffffffu, key_of(top + 0.f));
-  if (lane == 0) atomicMax(&sh.m_key, w_key);
+  {
+    const unsigned k = __reduce_max_sync(0xffffffffu, key_of(top + 0.f));
+    if (lane == 0) atomicMax(&sh.m_key, k);
+  }
   sync_row();
   float m = of_key(sh.m_key);  // this warp's maximum so far
   for (int c = 0; c < C; ++c) m = fmaxf(m, of_key(*peer(&sh.m_key, c)));
@@ -406,104 +422,122 @@ __global__ void __launch_bounds__(kST, 3) stream_kernel(const SampleParams q) {
   const bool greedy = r.T == 0.f;
   const bool by_list = !greedy && (r.use_k || r.use_p || r.lo > 0.f);
   const bool sum = by_list && r.use_p && !r.use_k;
+  // 2^-t of a vector's logits, in fp32 (NaN and -inf give 0; m is finite): t with its low part
+  auto fast = [&](const uint4& v4) {
+    float x[N];
+    Vec<T>::get(v4, x);
+    const uint64_t nm = pair(-m, -m), c = pair(sc.c_hi, sc.c_hi), nc = pair(-sc.c_hi, -sc.c_hi), cl2 = pair(sc.c_lo, sc.c_lo);
+    const uint64_t ln2 = pair(0.693147182f, 0.693147182f);
+    uint64_t s = 0;
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      const uint64_t d = add2(pair(fmaxf(x[e], -FLT_MAX), fmaxf(x[e + 1], -FLT_MAX)), nm);
+      const uint64_t tt = mul2(d, nc), lo = fma2(d, cl2, fma2(d, c, tt));
+      float t0, t1, w0, w1;
+      unpair(tt, t0, t1);
+      const uint64_t w = pair(ex2(-t0), ex2(-t1));
+      unpair(fma2(w, mul2(lo, ln2), w), w0, w1);
+      s = add2(s, pair(t0 <= kCut ? w0 : 0.f, t1 <= kCut ? w1 : 0.f));
+    }
+    float s0, s1;
+    unpair(s, s0, s1);
+    return s0 + s1;
+  };
   float floor_x = -INFINITY;  // the list takes logits from here on
   if (by_list) {
-    const float from = reach(sc, kFar);
-    for (int b = 0; b < min(blocks, kStages); ++b) {
+    const float share = (float)seen / (float)max(blocks, 1);  // of the row seen
+    for (int far = 0; far < 2; ++far) {
+      const float range = far ? kLookFar : kLookNear, step = range / kLook;
+      const float from = reach(sc, range), cut_x = reach(sc, kCut);
+      const bool beyond = sum && !far && m > -INFINITY && m < INFINITY && !isinf(sc.c_hi);
+      float rest = 0.f;  // top-p alone: the mass past the range
+      for (int b = 0; b < seen; ++b) {
 #pragma unroll 1
-      for (int v = 0; v < kVec; ++v) {
-        const uint4 x4 = ring[(b * kVec + v) * kST + t];
-        if (!(Vec<T>::top(x4) >= from)) continue;
-        float x[N];
-        Vec<T>::get(x4, x);
+        for (int v = 0; v < kVec; ++v) {
+          const uint4 x4 = ring[(b * kVec + v) * kST + t];
+          const float top = Vec<T>::top(x4);
+          if (!(top >= from)) {
+            if (beyond && top >= cut_x) rest += fast(x4);
+            continue;
+          }
+          float x[N];
+          Vec<T>::get(x4, x);
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const float tt = t_of(sc, clean(x[e]));
-          if (tt < kFar && x[e] > -INFINITY) atomicAdd(&sh.count[(int)(tt * (kLook / kFar))], 1u);
+          for (int e = 0; e < N; ++e) {
+            const float tt = t_of(sc, clean(x[e]));
+            if (tt < range && x[e] > -INFINITY)
+              atomicAdd(&sh.count[min(kLook - 1, (int)(tt / step))], 1u);
+            else if (beyond)
+              rest += ex2(-tt);
+          }
         }
       }
-    }
-    sync_row();
-    if (warp == 0) {
-      // lane l: bins 2 l, 2 l + 1 of the row's first blocks.  The first bins by which, going by them,
-      // the list holds what the filter needs: k and half as many more; all but 1 - p of the mass
-      // (the mass left out, as the blocks seen have it, against that seen alone: the few large
-      // weights of a row may lie anywhere) and some 192 logits; every t up to min-p's
-      unsigned a = 0, b = 0;
-      for (int c = 0; c < C; ++c) a += peer(sh.count, c)[2 * lane], b += peer(sh.count, c)[2 * lane + 1];
-      const float wa = a * exp2f(-(2 * lane + 0.5f) * (kFar / kLook)), wb = b * exp2f(-(2 * lane + 1.5f) * (kFar / kLook));
-      unsigned n = a + b;
-      float w = wa + wb;
+      if (beyond) {
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned x = __shfl_up_sync(0xffffffffu, n, o);
-        const float y = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) n += x, w += y;
+        for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
+        if (lane == 0) atomicAdd(&sh.part, fix<43>(F2{rest, 0.f}));
       }
-      const float whole = __shfl_sync(0xffffffffu, w, 31);
-      const float share = (float)min(blocks, kStages) / (float)max(blocks, 1);  // of the row seen
-      const float end = (2 * lane + 2) * (kFar / kLook);
-      bool enough = true;
-      if (r.use_k)
-        enough = n >= (1.5f * r.k + 64.f) * share;
-      else if (r.use_p)
-        enough = (whole - w) * 1.3f <= (1.f - r.p) * whole * share && n >= 192.f * share;
-      else
-        enough = end > -log2f(r.lo) + 0.5f;
-      const unsigned yes = __ballot_sync(0xffffffffu, enough), fits = __ballot_sync(0xffffffffu, n <= kAim * share);
-      const int pairs = min(yes ? __ffs(yes) : 32, max(1, ~fits ? __ffs(~fits) - 1 : 32));
-      if (lane == 0) sh.floor = m - pairs * 2 * (kFar / kLook) / sc.c_hi;
+      sync_row();
+      if (warp == 0) {
+        // lane l: bins 2 l, 2 l + 1 of the row's first blocks.  The first bins by which, going by them,
+        // the list holds what the filter needs: k and half as many more; all but 1 - p of the mass
+        // (the mass left out, as the blocks seen have it, against that seen alone: the few large
+        // weights of a row may lie anywhere) and some 192 logits; every t up to min-p's
+        unsigned a = 0, b = 0;
+        for (int c = 0; c < C; ++c) a += peer(sh.count, c)[2 * lane], b += peer(sh.count, c)[2 * lane + 1];
+        unsigned n = a + b;
+        float w = a * exp2f(-(2 * lane + 0.5f) * step) + b * exp2f(-(2 * lane + 1.5f) * step);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned x = __shfl_up_sync(0xffffffffu, n, o);
+          const float y = __shfl_up_sync(0xffffffffu, w, o);
+          if (lane >= o) n += x, w += y;
+        }
+        float whole = __shfl_sync(0xffffffffu, w, 31);
+        for (int c = 0; c < C; ++c) whole += (float)*peer(&sh.part, c) * 0x1p-43f;
+        const float end = (2 * lane + 2) * step;
+        bool enough = true;
+        if (r.use_k)
+          enough = n >= (1.5f * r.k + 64.f) * share;
+        else if (r.use_p)
+          enough = (whole - w) * 1.3f <= (1.f - r.p) * whole * share && n >= 192.f * share;
+        else
+          enough = end > -log2f(r.lo) + 0.5f;
+        const unsigned yes = __ballot_sync(0xffffffffu, enough), fits = __ballot_sync(0xffffffffu, n <= kAim * share);
+        const int need = yes ? __ffs(yes) : 33, room = max(1, ~fits ? __ffs(~fits) - 1 : 32);
+        if (lane == 0) {
+          sh.floor = m - min(min(need, room), 32) * 2 * step / sc.c_hi;
+          sh.pick[0] = need <= 32 || room < 32;
+        }
+      }
+      sync_row();  // (the counts have been read by every CTA)
+      const bool set = sh.pick[0] || far;  // the same in every CTA
+      floor_x = isinf(m) || isinf(sc.c_hi) ? m : sh.floor;
+      __syncthreads();
+      if (t < kLook) sh.count[t] = 0;
+      if (t == 0) sh.pick[0] = 0x7fffffff, sh.part = 0;
+      __syncthreads();
+      if (set) break;
     }
-    if (C > 1) cl.sync(); else __syncthreads();  // (the counts are read by every CTA)
-    floor_x = isinf(m) || isinf(sc.c_hi) ? m : sh.floor;
-    if (t < kLook) sh.count[t] = 0;
   }
 
   // ---- the row
   float rest = 0.f;                                  // fp32 mass below the floor, relative to m
   unsigned long long best = 0;                       // greedy: (key, ~index)
-  bool exact = false;                                // temperature alone: the second time
-stream:
-  for (int b = 0; b < blocks; ++b) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-    uint4 x4[kVec];
-    float tops[kVec];
-    top = -INFINITY;
+  stream([&](int b, uint4 (&x4)[kVec], float (&tops)[kVec], auto&& next) {
+    float top = tops[0];
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) {
-      x4[v] = ring[(b % kStages * kVec + v) * kST + t];
-      tops[v] = Vec<T>::top(x4[v]);
-      top = fmaxf(top, tops[v]);
-    }
-    w_key = __reduce_max_sync(0xffffffffu, key_of(top + 0.f));
-    if (lane == 0 && w_key > *(volatile unsigned*)&sh.m_key) atomicMax(&sh.m_key, w_key);
-    issue(b + kStages);
-    const float m_new = fmaxf(of_key(w_key), of_key(__shfl_sync(0xffffffffu, *(volatile unsigned*)&sh.m_key, 0)));
+    for (int v = 1; v < kVec; ++v) top = fmaxf(top, tops[v]);
+    const unsigned w_key = __reduce_max_sync(0xffffffffu, key_of(top + 0.f));
+    const unsigned s_key = *(volatile unsigned*)&sh.m_key;
+    if (lane == 0 && w_key > s_key) atomicMax(&sh.m_key, w_key);
+    next();
+    const float m_new = of_key(max(w_key, __shfl_sync(0xffffffffu, s_key, 0)));
     if (m_new > m) {
       sc.m = m_new;
       rest *= exp2f(-t_of(sc, m));  // (0 at first: m = -inf)
       m = m_new;
     }
-    // 2^-t of a vector's logits, in fp32 (NaN and -inf give 0; m is finite): t with its low part, a
-    // tree of sums
-    auto fast = [&](const uint4& v4) {
-      float x[N];
-      Vec<T>::get(v4, x);
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float d = fmaxf(x[e], -FLT_MAX) - m, a = d * sc.c_hi;
-        const float w = ex2(a), lo = fmaf(d, sc.c_hi, -a) + d * sc.c_lo;
-        x[e] = a >= -kCut ? fmaf(w, lo * 0.693147182f, w) : 0.f;
-      }
-#pragma unroll
-      for (int o = N / 2; o > 0; o /= 2) {
-#pragma unroll
-        for (int e = 0; e < o; ++e) x[e] += x[e + o];
-      }
-      return x[0];
-    };
-    const bool finite = m > -INFINITY && m < INFINITY && !isinf(sc.c_hi);
-    const float cut_x = reach(sc, kCut);  // vectors below weigh nothing
     if (greedy) {
 #pragma unroll
       for (int v = 0; v < kVec; ++v) {
@@ -516,7 +550,11 @@ stream:
           if (clean(x[e]) > -INFINITY && c > best) best = c;
         }
       }
-    } else if (by_list) {
+      return;
+    }
+    const bool finite = m > -INFINITY && m < INFINITY && !isinf(sc.c_hi);
+    const float cut_x = reach(sc, kCut);  // vectors below weigh nothing
+    if (by_list) {
 #pragma unroll
       for (int v = 0; v < kVec; ++v) {
         if (tops[v] >= floor_x) {
@@ -536,36 +574,36 @@ stream:
           rest += fast(x4[v]);
         }
       }
-    } else {
-      F2 s = {0.f, 0.f};
-      float far = 0.f;
-      const float near_x = exact || !finite ? cut_x : reach(sc, kNear);
+      return;
+    }
+    F2 s = {0.f, 0.f};
+    float far = 0.f;
+    const float near_x = finite ? reach(sc, kNear) : cut_x;
+#pragma unroll
+    for (int v = 0; v < kVec; ++v)
+      if (tops[v] >= cut_x && !(tops[v] >= near_x)) far += fast(x4[v]);
+    bool near = false;
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) near |= tops[v] >= near_x;
+    if (near) {
 #pragma unroll 1
       for (int v = 0; v < kVec; ++v) {
         const uint4 y4 = v == 0 ? x4[0] : v == 1 ? x4[1] : v == 2 ? x4[2] : x4[3];
-        const float top_v = Vec<T>::top(y4);
-        if (!(top_v >= cut_x)) continue;
-        if (top_v >= near_x) {
-          float x[N];
-          Vec<T>::get(y4, x);
+        if (!(Vec<T>::top(y4) >= near_x)) continue;
+        float x[N];
+        Vec<T>::get(y4, x);
 #pragma unroll
-          for (int e = 0; e < N; ++e) {
-            F2 w = weight(sc, clean(x[e]));
-            if (clean(x[e]) == -INFINITY) w = F2{0.f, 0.f};
-            s = add(s, w);
-          }
-        } else {
-          const float f = fast(y4);
-          far += f;
-          s = add(s, F2{f, 0.f});
+        for (int e = 0; e < N; ++e) {
+          const float c = clean(x[e]);
+          if (c > -INFINITY) s = add(s, weight(sc, c));
         }
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s = shfl_add(s, o), far += __shfl_xor_sync(0xffffffffu, far, o);
-      if (lane == 0) stretch[b * kSW + warp] = Stretch{s.h, s.l, far, m};
     }
-  }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
+    s = add(s, F2{far, 0.f});
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s = shfl_add(s, o), far += __shfl_xor_sync(0xffffffffu, far, o);
+    if (lane == 0) stretch[b * kSW + warp] = Stretch{s.h, s.l, far, m};
+  });
   if (greedy) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
@@ -589,182 +627,7 @@ stream:
     if (C > 1) cl.sync();
     return;
   }
-
-  if (!by_list) {
-    // ---- temperature alone: running sums
-    const int n = blocks * kSW, per = (n + kST - 1) / kST;
-    unsigned long long mine = 0, my_far = 0;
-    for (int e = 0; e < per; ++e) {
-      const int i = t * per + e;
-      if (i >= n) break;
-      const Stretch& s = stretch[i];
-      if (s.ref > -INFINITY) {
-        const F2 f = weight(sc, s.ref);
-        mine += fix<43>(mul(F2{s.h, s.l}, f));
-        my_far += fix<43>(F2{s.far * f.h, 0.f});
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) my_far += __shfl_xor_sync(0xffffffffu, my_far, o);
-    if (lane == 0 && my_far) atomicAdd(&sh.far, my_far);
-    unsigned long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long x = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += x;
-    }
-    if (lane == 31) sh.red_l[warp] = inc;
-    __syncthreads();
-    unsigned long long run = inc - mine, part = 0, total = 0, ahead = 0, far = sh.far;
-    for (int w = 0; w < kSW; ++w) {
-      if (w < warp) run += sh.red_l[w];
-      part += sh.red_l[w];
-    }
-    int last = 0;  // the row's last CTA with any mass
-    if (C > 1) {
-      if (t == 0) sh.part = part, sh.far_part = far;
-      cl.sync();
-      far = 0;
-      for (int c = 0; c < C; ++c) {
-        const unsigned long long x = *peer(&sh.part, c);
-        far += *peer(&sh.far_part, c);
-        if (c < rank) ahead += x;
-        if (x > 0) last = c;
-        total += x;
-      }
-      cl.sync();  // (the last that is read of the others)
-    } else {
-      total = part;
-    }
-    const unsigned long long target = part_of(total, r.u);
-    // the fp32 sums' error: of what lies ahead, and of the target
-    const unsigned long long slack = exact ? 0ull : part_of(far, 2.f * kFastError) + 1024;
-    run += ahead;
-    for (int e = 0; e < per; ++e) {  // this CTA's first stretch past the target, and its last with any mass
-      const int i = t * per + e;
-      if (i >= n) break;
-      const Stretch& s = stretch[i];
-      const unsigned long long x = s.ref > -INFINITY ? fix<43>(mul(F2{s.h, s.l}, weight(sc, s.ref))) : 0ull;
-      if (x > 0) {
-        if (run <= target && run + x > target) sh.pick[0] = i, sh.before = run;
-        atomicMax(&sh.pick[1], i);
-      }
-      run += x;
-    }
-    __syncthreads();
-    const bool mine_past = sh.pick[0] != 0x7fffffff;
-    const bool owner = mine_past || (rank == last && target >= total);  // u >= 1: the row's last kept one
-    if (owner) {  // the whole CTA walks the stretch: thread t has its positions 4 t .. 4 t + 3 (N = 8) or 2 t, 2 t + 1
-      constexpr int kE = kWarpPart / kST;
-      const int at = mine_past ? sh.pick[0] : sh.pick[1];
-      const int i0 = at / kSW * kBlock + at % kSW * kWarpPart + t * kE;
-      const unsigned long long before = mine_past ? sh.before : 0ull, goal = mine_past ? target : ~0ull;
-      F2 w[kE];
-      unsigned long long f[kE], sum_w = 0;
-#pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        const int i = i0 + e;
-        const float c = i >= sl.begin && i < sl.count ? clean(Elem<T>::to_f(*sl.at(i))) : -INFINITY;
-        w[e] = c > -INFINITY ? weight(sc, c) : F2{0.f, 0.f};
-        f[e] = fix<43>(w[e]);
-        sum_w += f[e];
-      }
-      unsigned long long cum = sum_w;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long x = __shfl_up_sync(0xffffffffu, cum, o);
-        if (lane >= o) cum += x;
-      }
-      if (t == 0) sh.pick[0] = 0x7fffffff, sh.pick[1] = -1;
-      __syncthreads();  // (and red_l has been read)
-      if (lane == 31) sh.red_l[warp] = cum;
-      __syncthreads();
-      cum = before + cum - sum_w;
-      for (int x = 0; x < warp; ++x) cum += sh.red_l[x];
-      // the first position past the target, else the last with any mass
-      int hit = -1, any = -1;
-      unsigned long long from[2] = {0, 0}, run2 = cum;
-#pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        if (f[e] > 0) {
-          any = i0 + e;
-          if (hit < 0 && run2 + f[e] > goal) hit = i0 + e, from[0] = run2, from[1] = run2 + f[e];
-        }
-        run2 += f[e];
-      }
-      if (hit >= 0) atomicMin(&sh.pick[0], hit);
-      if (any >= 0) atomicMax(&sh.pick[1], any);
-      __syncthreads();
-      const int token = sh.pick[0] != 0x7fffffff ? sh.pick[0] : sh.pick[1];
-      if (token >= i0 && token < i0 + kE) {
-        F2 tw = w[0];
-#pragma unroll
-        for (int e = 1; e < kE; ++e)
-          if (token == i0 + e) tw = w[e];
-        // sure: the fp32 sums' error moves neither border of the token past the target, nor the
-        // probability's last bit
-        bool sure = exact || !mine_past ||
-                    (token == hit && (from[0] == 0 || from[0] + slack <= target) && from[1] > target + slack);
-        if (q.probs && !exact) sure = sure && (float)far * kFastError <= (float)total * kProbError;
-        if (sure)
-          put(q, row, sl.first + token, prob_of(tw, total));
-        else
-          for (int c = 0; c < C; ++c) *peer(&sh.bad, c) = 1;  // stream the row again
-      }
-    }
-    if (exact) return;
-    sync_row();
-    if (!sh.bad) return;
-    exact = true;
-    __syncthreads();
-    if (t == 0) sh.pick[0] = 0x7fffffff, sh.pick[1] = -1, sh.far = 0, sh.bad = 0;
-    m = m_row;  // every stretch by the row's maximum now
-    for (int b = 0; b < kStages; ++b) issue(b);
-    __syncthreads();
-    goto stream;
-  }
-
-  // ---- the row's list, in the first CTA (its ring is idle: its own part of the row is through)
-  {
-    sc.m = m_row;
-    rest *= m > -INFINITY ? exp2f(-t_of(sc, m)) : 0.f;
-    unsigned long long* dst = peer(final_list, 0);
-    unsigned* n_at = peer(&sh.n_final, 0);
-    const int n = (int)min(sh.n_list, (unsigned)kList);
-    bool full = sh.n_list > kList;
-    for (int i = t; i < n; i += kST) {
-      const unsigned at = C > 1 ? atomicAdd(n_at, 1u) : i, place = places[i];
-      if (at < kList)
-        dst[at] = (unsigned long long)~key_of(clean(Elem<T>::to_f(sl.src[place]))) << 32 | place;
-      else
-        full = true;
-    }
-    if (C == 1 && t == 0) sh.n_final = n;
-    if (full) atomicOr(peer(&sh.bad, 0), 1u);
-    if (sum) {
-      F2 s = {rest, 0.f};
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s = shfl_add(s, o);
-      if (lane == 0) atomicAdd(peer(&sh.rest, 0), fix<43>(s));
-    }
-  }
-  sync_row();
-  if (rank != 0) return;
-  const int n_all = (int)sh.n_final;
-  if (sh.bad) {  // too many
-    if (t == 0) q.tokens[row] = kRetry;
-    return;
-  }
-  const float scale = kBins / fmaxf(t_of(sc, floor_x), 1e-30f);
-  auto bin_of = [&](float tt) { return min(kBins - 1, (int)fminf(tt * scale, kBins)); };
-  for (int i = t; i < n_all; i += kST) {
-    const float x = of_key(~(unsigned)(final_list[i] >> 32));
-    const int b = bin_of(t_of(sc, x));
-    atomicAdd(&sh.count[b], 1u);
-    if (sum) atomicAdd(&sh.mass[b], fix<51>(weight(sc, x)));  // (4096 of them, and the rest, below 2^64)
-  }
-  __syncthreads();
-  auto scan_l = [&](unsigned long long v, unsigned long long* all) {  // sum over lower threads
+  auto scan_l = [&](unsigned long long v, unsigned long long* all) {  // sum over lower threads of the CTA
     unsigned long long inc = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -782,430 +645,483 @@ stream:
     *all = a;
     return b;
   };
-  // thread t: bin t.  The last bin that the prefix reaches
-  unsigned long long all, goal = ~0ull;
-  const unsigned cum = (unsigned)scan_l(sh.count[t], &all) + sh.count[t];
-  bool here;
-  if (sum) {
-    if (sh.rest >= 1ull << 54) {  // a mass above 2048 largest weights
-      if (t == 0) q.tokens[row] = kRetry;
-      return;
+
+  // ---- the token from the row's list, in the first CTA; false: the prefix is not in it
+  auto from_list = [&]() -> bool {
+    const int n_all = (int)sh.n_final;
+    if (sh.full || sh.rest >= 1ull << 54) return false;  // too many, or a mass above 2048 largest weights
+    const float scale = kBins / fmaxf(t_of(sc, floor_x), 1e-30f);
+    auto bin_of = [&](float tt) { return min(kBins - 1, (int)fminf(tt * scale, kBins)); };
+    for (int i = t; i < n_all; i += kST) {
+      const float x = of_key(~(unsigned)(final_list[i] >> 32));
+      const int b = bin_of(t_of(sc, x));
+      atomicAdd(&sh.count[b], 1u);
+      if (sum) atomicAdd(&sh.mass[b], fix<51>(weight(sc, x)));  // (4096 of them, and the rest, below 2^64)
     }
-    unsigned long long whole;
-    const unsigned long long run = scan_l(sh.mass[t], &whole) + sh.mass[t];
-    bool more;
-    goal = part_of(whole + (sh.rest << 8), r.p, &more);
-    goal += more;
-    here = run >= goal;
-    goal = goal >> 63 ? ~0ull : goal << 1;  // in the sorted prefix's units
-  } else if (r.use_k) {
-    here = cum >= (unsigned)r.k;
-  } else {  // min-p: t <= -log2(min_p), allowing for rounding
-    const float far = fmaxf(0.f, -log2f(r.lo)) + 0.01f;
-    here = (t + 1) / scale > far || (t == kBins - 1 && isinf(t_of(sc, floor_x))) || (t == kBins - 1 && floor_x == m_row && isinf(m_row));
-  }
-  if (here) atomicMin(&sh.pick[0], t);
-  __syncthreads();
-  const int bin_end = sh.pick[0];
-  if (bin_end == 0x7fffffff) {  // the prefix goes on past the list
-    if (t == 0) q.tokens[row] = kRetry;
-    return;
-  }
-  if (t == bin_end) sh.red_u[0] = cum;
-  if (t == 0) sh.n_list = 0;
-  __syncthreads();
-  const int n = (int)sh.red_u[0];
-  if (n > kSorted) {
-    if (t == 0) q.tokens[row] = kRetry;
-    return;
-  }
-  int n2 = 64;
-  while (n2 < n) n2 *= 2;
-  for (int i = t; i < n_all; i += kST) {
-    const unsigned long long it = final_list[i];
-    if (bin_of(t_of(sc, of_key(~(unsigned)(it >> 32)))) <= bin_end) list[atomicAdd(&sh.n_list, 1u)] = it;
-  }
-  for (int i = n + t; i < n2; i += kST) list[i] = ~0ull;
-  if (t == 0) sh.pick[0] = 0x7fffffff;
-  __syncthreads();
-  auto sort = [&](auto* v, int len_all) {  // ascending, bitonic; up to 64 by one warp
-    if (len_all > 64 || warp == 0) {
-      for (int len = 2; len <= len_all; len *= 2) {
-        for (int d = len / 2; d > 0; d /= 2) {
-          for (int i = t; i < len_all / 2; i += kST) {
-            const int a = 2 * i - (i & (d - 1)), b = a + d;
-            const auto va = v[a], vb = v[b];
-            if ((va > vb) == ((a & len) == 0)) v[a] = vb, v[b] = va;
+    __syncthreads();
+    // thread t: bin t.  The last bin that the prefix reaches
+    unsigned long long all, goal = ~0ull;
+    const unsigned cum = (unsigned)scan_l(sh.count[t], &all) + sh.count[t];
+    bool here;
+    if (sum) {
+      unsigned long long whole;
+      const unsigned long long run = scan_l(sh.mass[t], &whole) + sh.mass[t];
+      bool more;
+      goal = part_of(whole + (sh.rest << 8), r.p, &more);
+      goal += more;
+      here = run >= goal;
+      goal = goal >> 63 ? ~0ull : goal << 1;  // in the sorted prefix's units
+    } else if (r.use_k) {
+      here = cum >= (unsigned)r.k;
+    } else {  // min-p: t <= -log2(min_p), allowing for rounding
+      const float far = fmaxf(0.f, -log2f(r.lo)) + 0.01f;
+      here = (t + 1) / scale > far || (t == kBins - 1 && isinf(t_of(sc, floor_x)));
+    }
+    if (here) atomicMin(&sh.pick[0], t);
+    if (t == 0) sh.n_list = 0;
+    __syncthreads();
+    const int bin_end = sh.pick[0];
+    if (bin_end == 0x7fffffff) return false;  // the prefix goes on past the list
+    if (t == bin_end) sh.red_u[0] = cum;
+    __syncthreads();
+    const int n = (int)sh.red_u[0];
+    if (n > kSorted) return false;
+    int n2 = 64;
+    while (n2 < n) n2 *= 2;
+    for (int i = t; i < n_all; i += kST) {
+      const unsigned long long it = final_list[i];
+      if (bin_of(t_of(sc, of_key(~(unsigned)(it >> 32)))) <= bin_end) list[atomicAdd(&sh.n_list, 1u)] = it;
+    }
+    for (int i = n + t; i < n2; i += kST) list[i] = ~0ull;
+    if (t == 0) sh.pick[0] = 0x7fffffff;
+    __syncthreads();
+    auto sort = [&](auto* v, int len_all) {  // ascending, bitonic; up to 64 by one warp
+      if (len_all > 64 || warp == 0) {
+        for (int len = 2; len <= len_all; len *= 2) {
+          for (int d = len / 2; d > 0; d /= 2) {
+            for (int i = t; i < len_all / 2; i += kST) {
+              const int a = 2 * i - (i & (d - 1)), b = a + d;
+              const auto va = v[a], vb = v[b];
+              if ((va > vb) == ((a & len) == 0)) v[a] = vb, v[b] = va;
+            }
+            if (len_all > 64) __syncthreads(); else __syncwarp();
           }
-          if (len_all > 64) __syncthreads(); else __syncwarp();
         }
       }
-    }
-    __syncthreads();
-  };
-  sort(list, n2);  // by (falling logit, index)
-  // thread t has items [t per, (t + 1) per): weights (units of 2^-52) and their running sum
-  const int per = max(1, n2 / kST), i0 = t * per;
-  constexpr int kPer = kSorted / kST;
-  unsigned long long mine = 0;
-  unsigned low = 0;  // items below min-p
+      __syncthreads();
+    };
+    sort(list, n2);  // by (falling logit, index)
+    // thread t has items [t per, (t + 1) per): weights (units of 2^-52) and their running sum
+    const int per = max(1, n2 / kST), i0 = t * per;
+    static_assert(kSorted / kST <= 32, "one bit per item");
+    unsigned long long mine = 0;
+    unsigned low = 0;  // items below min-p
 #pragma unroll 1
-  for (int e = 0; e < per; ++e) {
-    const int i = i0 + e;
-    if (i >= n) break;
-    const unsigned long long it = list[i];
-    const F2 f = weight(sc, of_key(~(unsigned)(it >> 32)));
-    const unsigned long long w = fix<52>(f);
-    low |= (unsigned)below(f, r.lo) << e;
-    index[i] = (unsigned)it;
-    list[i] = w;
-    mine += w;
-  }
-  static_assert(kPer <= 32, "one bit per item");
-  const unsigned long long before = scan_l(mine, &all);
-  const int k_end = r.use_k ? min(n, r.k) : n;
-  if (r.use_k && r.use_p) {  // the goal is a part of the mass left by top-k
-    unsigned long long run = before;
+    for (int e = 0; e < per; ++e) {
+      const int i = i0 + e;
+      if (i >= n) break;
+      const unsigned long long it = list[i];
+      const F2 f = weight(sc, of_key(~(unsigned)(it >> 32)));
+      const unsigned long long w = fix<52>(f);
+      low |= (unsigned)below(f, r.lo) << e;
+      index[i] = (unsigned)it;
+      list[i] = w;
+      mine += w;
+    }
+    const unsigned long long before = scan_l(mine, &all);
+    const int k_end = r.use_k ? min(n, r.k) : n;
+    if (r.use_k && r.use_p) {  // the goal is a part of the mass left by top-k
+      unsigned long long run = before;
+      for (int e = 0; e < per && i0 + e < k_end; ++e) {
+        run += list[i0 + e];
+        if (i0 + e == k_end - 1) sh.before = run;
+      }
+      __syncthreads();
+      bool more;
+      goal = part_of(sh.before, r.p, &more);
+      goal += more;
+    }
+    // the kept prefix: its length and mass
+    unsigned long long run = before, kept_w = 0;
+    int n_kept = 0;
     for (int e = 0; e < per && i0 + e < k_end; ++e) {
-      run += list[i0 + e];
-      if (i0 + e == k_end - 1) sh.before = run;
+      const unsigned long long w = list[i0 + e];
+      if ((i0 + e == 0 || run < goal) && !(low >> e & 1) && w > 0) ++n_kept, kept_w += w;
+      run += w;
     }
-    __syncthreads();
-    bool more;
-    goal = part_of(sh.before, r.p, &more);
-    goal += more;
-  }
-  // the kept prefix: its length and mass
-  unsigned long long run = before, kept_w = 0;
-  int n_kept = 0;
-  for (int e = 0; e < per && i0 + e < k_end; ++e) {
-    const unsigned long long w = list[i0 + e];
-    if ((i0 + e == 0 || run < goal) && !(low >> e & 1) && w > 0) ++n_kept, kept_w += w;
-    run += w;
-  }
-  n_kept = __reduce_add_sync(0xffffffffu, n_kept);
+    n_kept = __reduce_add_sync(0xffffffffu, n_kept);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) kept_w += __shfl_xor_sync(0xffffffffu, kept_w, o);
-  if (lane == 0) sh.red_u[warp] = n_kept, sh.red_l[warp] = kept_w;
-  __syncthreads();
-  n_kept = 0;
-  kept_w = 0;
-  for (int w = 0; w < kSW; ++w) n_kept += sh.red_u[w], kept_w += sh.red_l[w];
-  const unsigned long long target = part_of(kept_w, r.u);
-  // the lowest index at which the running sum by index exceeds the target, else the last one
-  // (packed with the item's place: below 2^20 and 2^11)
-  if (n_kept <= 128) {
-    if (t < n_kept) {
-      const unsigned me = index[t];
+    for (int o = 16; o > 0; o >>= 1) kept_w += __shfl_xor_sync(0xffffffffu, kept_w, o);
+    if (lane == 0) sh.red_u[warp] = n_kept, sh.red_l[warp] = kept_w;
+    __syncthreads();
+    n_kept = 0;
+    kept_w = 0;
+    for (int w = 0; w < kSW; ++w) n_kept += sh.red_u[w], kept_w += sh.red_l[w];
+    const unsigned long long target = part_of(kept_w, r.u);
+    // the lowest index at which the running sum by index exceeds the target, else the last one
+    // (packed with the item's place: below 2^20 and 2^11)
+    if (n_kept <= 128) {
+      if (t < n_kept) {
+        const unsigned me = index[t];
+        unsigned long long s = 0;
+        for (int j = 0; j < n_kept; ++j) s += index[j] <= me ? list[j] : 0ull;
+        const int at = (int)(me << 11 | t);
+        if (s > target) atomicMin(&sh.pick[0], at);
+        atomicMax(&sh.pick[1], at);
+      }
+    } else {
+      int m2 = 256;
+      while (m2 < n_kept) m2 *= 2;
+      for (int i = t; i < m2; i += kST) by[i] = i < n_kept ? index[i] << 11 | i : 0xffffffffu;
+      __syncthreads();
+      sort(by, m2);
+      const int c = m2 / kST, j0 = t * c;
       unsigned long long s = 0;
-      for (int j = 0; j < n_kept; ++j) s += index[j] <= me ? list[j] : 0ull;
-      const int at = (int)(me << 11 | t);
-      if (s > target) atomicMin(&sh.pick[0], at);
-      atomicMax(&sh.pick[1], at);
-    }
-  } else {
-    int m2 = 256;
-    while (m2 < n_kept) m2 *= 2;
-    for (int i = t; i < m2; i += kST) by[i] = i < n_kept ? index[i] << 11 | i : 0xffffffffu;
-    __syncthreads();
-    sort(by, m2);
-    const int c = m2 / kST, j0 = t * c;
-    unsigned long long s = 0;
-    for (int e = 0; e < c && j0 + e < n_kept; ++e) s += list[by[j0 + e] & 2047];
-    s = scan_l(s, &all);
-    for (int e = 0; e < c && j0 + e < n_kept; ++e) {
-      s += list[by[j0 + e] & 2047];
-      if (s > target) {
-        atomicMin(&sh.pick[0], (int)by[j0 + e]);
-        break;
+      for (int e = 0; e < c && j0 + e < n_kept; ++e) s += list[by[j0 + e] & 2047];
+      s = scan_l(s, &all);
+      for (int e = 0; e < c && j0 + e < n_kept; ++e) {
+        s += list[by[j0 + e] & 2047];
+        if (s > target) {
+          atomicMin(&sh.pick[0], (int)by[j0 + e]);
+          break;
+        }
       }
+      if (t == 0) sh.pick[1] = (int)by[n_kept - 1];
     }
-    if (t == 0) sh.pick[1] = (int)by[n_kept - 1];
-  }
-  __syncthreads();
-  if (t == 0) {
-    const int at = sh.pick[0] != 0x7fffffff ? sh.pick[0] : sh.pick[1];
-    put(q, row, at >= 0 ? at >> 11 : -1, at >= 0 ? (float)((double)list[at & 2047] / (double)kept_w) : 0.f);
-  }
-}
-
-// ------------------------------------------------------------------ select_kernel
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kC = 8;                        // CTAs of a row
-constexpr int kDigit = 10, kKeys = 1 << kDigit;
-constexpr int kSliceBytes = 184 * 1024;      // shared memory for a CTA's slice
-
-struct SelectShared {
-  float2 table[128];
-  unsigned count[kKeys];              // the slice's histogram of a round
-  unsigned long long mass[kKeys];
-  unsigned long long wsum[kWarps], all_sum[kC * kWarps];  // kept mass of each warp's segment
-  unsigned wties[kWarps], all_ties[kC * kWarps];          // logits equal to tau in it
-  unsigned long long red_l[kWarps], found_l;
-  unsigned todo[kWarps], m_key;
-  int found;
-};
-
-template <typename T>
-__device__ void select_row(const SampleParams& q, int row, T* xs, SelectShared& sh, cg::cluster_group& cl) {
-  constexpr int N = Vec<T>::N;
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, rank = (int)cl.block_rank();
-  const Slice<T> sl(q, row, rank);
-  const int padded = (sl.count + N * 32 * kWarps - 1) / (N * 32 * kWarps) * (N * 32 * kWarps);
-  const int seg = padded / kWarps;  // warp w has positions w seg .. (w + 1) seg - 1, lanes take vectors in turn
-  if (t == 0) sh.m_key = 0;
-  __syncthreads();
-  float top = -INFINITY;
-  for (int i = t * N; i < padded; i += kThreads * N) {
-    const uint4 v = sl.whole(i) ? *reinterpret_cast<const uint4*>(sl.at(i)) : sl.edge(i);
-    top = fmaxf(top, Vec<T>::top(v));
-    *reinterpret_cast<uint4*>(xs + i) = v;
-  }
-  const unsigned w_key = __reduce_max_sync(0xffffffffu, key_of(top + 0.f));
-  if (lane == 0) atomicMax(&sh.m_key, w_key);
-  cl.sync();
-  unsigned m_key = 0;
-  for (int c = 0; c < kC; ++c) m_key = max(m_key, *cl.map_shared_rank(&sh.m_key, c));
-  const Row r = row_of(q, row);
-  const Scale sc = scale_of(of_key(m_key), r.T, sh.table);
-
-  auto each = [&](float from, auto&& f) {  // f(position, logit) over vectors whose largest is at least `from`
-    for (int i = warp * seg + lane * N; i < (warp + 1) * seg; i += 32 * N) {
-      const uint4 v4 = *reinterpret_cast<const uint4*>(xs + i);
-      if (!(Vec<T>::top(v4) >= from)) continue;
-      float v[N];
-      Vec<T>::get(v4, v);
-#pragma unroll
-      for (int e = 0; e < N; ++e) f(i + e, clean(v[e]));
+    __syncthreads();
+    if (t == 0) {
+      const int at = sh.pick[0] != 0x7fffffff ? sh.pick[0] : sh.pick[1];
+      put(q, row, at >= 0 ? at >> 11 : -1, at >= 0 ? (float)((double)list[at & 2047] / (double)kept_w) : 0.f);
     }
+    return true;
   };
 
-  // ---- (tau, n_tau): keys above tau are kept, and the n_tau first of those equal to it
-  unsigned tau = key_of(-INFINITY), n_tau = 0;  // -inf itself is never drawn
-  bool use_k = r.use_k;
-  constexpr int kB = kKeys / kThreads;
-  // One border: the first key, falling, by which the count reaches k (by_mass: the mass reaches
-  // p of all).  Rounds over keys [lo, hi], 10 bits of them each; keys below tau_k do not take
-  // part and n_k of those equal to it do.  false: it is not reached.
-  auto border = [&](bool by_mass, unsigned tau_k, unsigned n_k, unsigned* key, unsigned long long* left) {
-    unsigned hi = m_key, lo = max(tau_k, key_of(by_mass ? fmaxf(reach(sc, kCut), -FLT_MAX) : -FLT_MAX));
-    unsigned long long goal = (unsigned)r.k, above = 0;
-    const unsigned long long w_k = by_mass && n_k > 0 ? n_k * fix<43>(weight(sc, of_key(tau_k))) : 0ull;
-    for (bool first = true;; first = false) {
-      const int bits = 32 - __clz(hi - lo), sh_r = max(0, bits - kDigit);
-      for (int b = t; b < kKeys; b += kThreads) sh.count[b] = 0, sh.mass[b] = 0;
-      if (t == 0) sh.found = -1;
-      __syncthreads();
-      each(of_key(lo), [&](int, float x) {
-        const unsigned kk = key_of(x);
-        if (kk < lo || kk > hi) return;
-        const int b = (int)((hi - kk) >> sh_r);
-        if (!by_mass) {
-          atomicAdd(&sh.count[b], 1u);
-        } else if (kk > tau_k || n_k == 0) {
-          atomicAdd(&sh.mass[b], fix<43>(weight(sc, x)));
-        }
-      });
-      if (by_mass && n_k > 0 && rank == 0 && t == 0 && tau_k >= lo && tau_k <= hi)
-        atomicAdd(&sh.mass[(hi - tau_k) >> sh_r], w_k);
-      cl.sync();
-      unsigned long long v[kB], mine = 0;
+  // (tau, n_tau): logits above tau are kept, and the n_tau first of those equal to it (by keys)
+  unsigned tau = digit_key<T>(-INFINITY), n_tau = 0;  // -inf itself is never drawn
+  bool ties = false, exact = false;
+  if (by_list) {
+    {  // gather the row's list in the first CTA (its ring is idle: its own part of the row is through)
+      rest *= m > -INFINITY ? exp2f(-t_of(sc, m)) : 0.f;
+      unsigned long long* dst = peer(final_list, 0);
+      unsigned* n_at = peer(&sh.n_final, 0);
+      const int n = (int)min(sh.n_list, (unsigned)kList);
+      bool full = sh.n_list > kList;
+      for (int i = t; i < n; i += kST) {
+        const unsigned at = C > 1 ? atomicAdd(n_at, 1u) : i, place = places[i];
+        if (at < kList)
+          dst[at] = (unsigned long long)~key_of(clean(Elem<T>::to_f(sl.src[place]))) << 32 | place;
+        else
+          full = true;
+      }
+      if (C == 1 && t == 0) sh.n_final = n;
+      if (full) atomicOr(peer(&sh.full, 0), 1u);
+      if (sum) {
+        F2 s = {rest, 0.f};
 #pragma unroll
-      for (int b = 0; b < kB; ++b) {
-        v[b] = 0;
-        for (int c = 0; c < kC; ++c) {
+        for (int o = 16; o > 0; o >>= 1) s = shfl_add(s, o);
+        if (lane == 0) atomicAdd(peer(&sh.rest, 0), fix<43>(s));
+      }
+    }
+    sync_row();
+    bool done = false;
+    if (rank == 0) {
+      done = from_list();
+      if (!done && t == 0)
+        for (int c = 0; c < C; ++c) *peer(&sh.again, c) = 1;
+    }
+    sync_row();
+    if (!sh.again) return;
+
+    // ---- by histograms over keys.  One border: the first key, falling, by which the count reaches
+    // k (by_mass: the mass reaches p of all).  Rounds over keys [lo, hi], kDigit bits of them each;
+    // keys below tau_k do not take part and n_k of those equal to it do.  false: it is not reached.
+    m = m_row;
+    auto border = [&](bool by_mass, unsigned tau_k, unsigned n_k, unsigned* key, unsigned long long* left) {
+      unsigned hi = digit_key<T>(m_row);
+      unsigned lo = max(tau_k, digit_key<T>(by_mass ? fmaxf(reach(sc, kCut), -FLT_MAX) : -FLT_MAX));
+      unsigned long long goal = (unsigned)r.k, above = 0;
+      const unsigned long long w_k = by_mass && n_k > 0 ? n_k * fix<43>(weight(sc, of_digit_key<T>(tau_k))) : 0ull;
+      for (bool first = true;; first = false) {
+        const int bits = 32 - __clz(hi - lo), shift = max(0, bits - kDigit);
+        for (int i = t; i < kKeys * 4; i += kST) digits[i] = 0;
+        if (t == 0) sh.pick[0] = -1;
+        start();
+        __syncthreads();
+        const float from = of_digit_key<T>(lo);
+        stream([&](int b, uint4 (&x4)[kVec], float (&tops)[kVec], auto&& next) {
+          next();
+#pragma unroll 1
+          for (int v = 0; v < kVec; ++v) {
+            const uint4 y4 = v == 0 ? x4[0] : v == 1 ? x4[1] : v == 2 ? x4[2] : x4[3];
+            if (!(Vec<T>::top(y4) >= from)) continue;
+            float x[N];
+            Vec<T>::get(y4, x);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+              const unsigned k = digit_key<T>(clean(x[e]));
+              if (k < lo || k > hi) continue;
+              unsigned* d = digits + ((hi - k) >> shift);
+              if (!by_mass) {
+                atomicAdd(d, 1u);
+              } else if (k > tau_k || n_k == 0) {
+                // four parts of 11 bits: 2^20 of them fit in a word
+                const unsigned long long w = fix<43>(weight(sc, clean(x[e])));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const unsigned part = (unsigned)(w >> 11 * i) & 2047u;
+                  if (part) atomicAdd(d + i * kKeys, part);
+                }
+              }
+            }
+          }
+        });
+        sync_row();
+        constexpr int kB = kKeys / kST;  // thread t: bins kB t ..
+        unsigned long long v[kB], mine = 0, all;
+#pragma unroll
+        for (int b = 0; b < kB; ++b) {
+          v[b] = 0;
           const int at = t * kB + b;
-          v[b] += by_mass ? cl.map_shared_rank(sh.mass, c)[at] : cl.map_shared_rank(sh.count, c)[at];
+          for (int c = 0; c < C; ++c) {
+            const unsigned* d = peer(digits, c) + at;
+            v[b] += by_mass ? (unsigned long long)d[0] + ((unsigned long long)d[kKeys] << 11) +
+                                  ((unsigned long long)d[2 * kKeys] << 22) + ((unsigned long long)d[3 * kKeys] << 33)
+                            : d[0];
+          }
+          if (by_mass && n_k > 0 && tau_k >= lo && tau_k <= hi && (int)((hi - tau_k) >> shift) == at) v[b] += w_k;
+          mine += v[b];
         }
-        mine += v[b];
-      }
-      unsigned long long inc = mine;
+        unsigned long long run = above + scan_l(mine, &all);
+        if (first && by_mass) {
+          bool more;
+          goal = part_of(all, r.p, &more);
+          goal = max(goal + more, 1ull);  // the first always stays
+        }
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
+        for (int b = 0; b < kB; ++b) {
+          if (run < goal && run + v[b] >= goal) sh.pick[0] = t * kB + b, sh.before = run;
+          run += v[b];
+        }
+        sync_row();  // every CTA has read the others' bins
+        const int b = sh.pick[0];
+        above = b < 0 ? above : sh.before;
+        __syncthreads();  // read before the next round resets it
+        if (b < 0) return false;
+        hi -= (unsigned)b << shift;
+        lo = max(lo, hi - ((1u << shift) - 1));
+        if (shift == 0) {
+          *key = hi;
+          *left = goal - above;
+          return true;
+        }
       }
-      if (lane == 31) sh.red_l[warp] = inc;
-      __syncthreads();
-      unsigned long long run = above + inc - mine, all = 0;
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) run += sh.red_l[w];
-        all += sh.red_l[w];
-      }
-      if (first && by_mass) {
-        bool more;
-        goal = part_of(all, r.p, &more);
-        goal = max(goal + more, 1ull);  // the first always stays
-      }
-#pragma unroll
-      for (int b = 0; b < kB; ++b) {
-        if (run < goal && run + v[b] >= goal) sh.found = t * kB + b, sh.found_l = run;
-        run += v[b];
-      }
-      cl.sync();  // every CTA has read the others' bins; its own find is visible to it
-      const int b = sh.found;
-      const unsigned long long found_l = sh.found_l;
-      __syncthreads();  // read before the next round resets it
-      if (b < 0) return false;
-      above = found_l;
-      hi -= (unsigned)b << sh_r;
-      lo = max(lo, hi - ((1u << sh_r) - 1));
-      if (sh_r == 0) {
-        *key = hi;
-        *left = goal - above;
-        return true;
-      }
-    }
-  };
-  unsigned long long left;
-  if (use_k) {
-    if (border(false, 0, 0, &tau, &left))
+    };
+    unsigned long long left;
+    if (r.use_k && border(false, 0, 0, &tau, &left)) {  // (else fewer than k candidates: all stay)
       n_tau = (unsigned)left;
-    else
-      use_k = false;  // fewer than k candidates: all stay
-  }
-  if (r.use_p) {
-    const unsigned n_k = n_tau;
-    unsigned key;
-    if (border(true, tau, n_k, &key, &left)) {
-      // of the keys equal to it: those before which less than the goal lies
-      const F2 w = weight(sc, of_key(key));
-      const double each_w = (double)w.h + (double)w.l;
-      const unsigned n = (unsigned)fmin(ceil((double)left * 0x1p-43 / each_w - 1e-9), 2e9);
-      n_tau = key == tau && n_k > 0 ? min(n_k, max(n, 1u)) : max(n, 1u);
-      tau = key;
+      ties = true;
     }
+    if (r.use_p) {
+      const unsigned n_k = n_tau;
+      unsigned key;
+      if (border(true, tau, n_k, &key, &left)) {
+        // of the keys equal to it: those before which less than the goal lies
+        const F2 w = weight(sc, of_digit_key<T>(key));
+        const unsigned n = max(1u, (unsigned)fmin(ceil((double)left * 0x1p-43 / ((double)w.h + (double)w.l) - 1e-9), 2e9));
+        n_tau = key == tau && n_k > 0 ? min(n_k, n) : n;
+        tau = key;
+        ties = true;
+      }
+    }
+    exact = true;
   }
 
-  // ---- ties at tau before each warp's segment
-  const bool ties = use_k || r.use_p;
-  unsigned my_ties = 0, ties_before = 0;
-  if (ties) {
-    each(of_key(tau), [&](int i, float x) { my_ties += key_of(x) == tau && i >= sl.begin && i < sl.count; });
-    my_ties = __reduce_add_sync(0xffffffffu, my_ties);
-    if (lane == 0) sh.wties[warp] = my_ties;
-    cl.sync();
-    if (t < kC * kWarps) sh.all_ties[t] = cl.map_shared_rank(sh.wties, t / kWarps)[t % kWarps];
-    __syncthreads();
-    for (int w = 0; w < rank * kWarps + warp; ++w) ties_before += sh.all_ties[w];
-  }
-  // the kept weights of positions i + lane N .. of this warp's segment (in order: `rank0` ties so far)
-  const float from = fmaxf(fmaxf(reach(sc, kCut), of_key(tau)), r.lo > 0.f && r.lo < 1.f ? reach(sc, -log2f(r.lo) + 0.01f) : -INFINITY);
-  const bool some = ties && ties_before < n_tau && ties_before + my_ties > n_tau;  // the n-th tie is here
-  const bool whole = ties && ties_before + my_ties <= n_tau;
-  auto kept = [&](int i, unsigned& rank0, F2 (&w)[N]) {
+  // ---- sums by stretch of what is kept (the first time, temperature alone: they are there)
+  for (bool summed = !by_list;; summed = false, exact = true) {
+    if (!summed) {
+      m = m_row;
+      const float from = fmaxf(fmaxf(reach(sc, kCut), of_digit_key<T>(tau)), r.lo > 0.f && r.lo < 1.f ? reach(sc, -log2f(r.lo) + 0.01f) : -INFINITY);
+      if (ties) {  // ties at tau ahead of each stretch
+        start();
+        stream([&](int b, uint4 (&x4)[kVec], float (&tops)[kVec], auto&& next) {
+          next();
+          unsigned n = 0;
 #pragma unroll
-    for (int e = 0; e < N; ++e) w[e] = F2{0.f, 0.f};
-    const uint4 v4 = *reinterpret_cast<const uint4*>(xs + i + lane * N);
-    if (!__any_sync(0xffffffffu, Vec<T>::top(v4) >= from)) return;  // nothing kept here
-    float v[N];
-    Vec<T>::get(v4, v);
-    unsigned eq = 0, at = 0;
+          for (int v = 0; v < kVec; ++v) {
+            if (!(tops[v] >= from)) continue;
+            float x[N];
+            Vec<T>::get(x4[v], x);
 #pragma unroll
-    for (int e = 0; e < N; ++e) v[e] = clean(v[e]);
-    if (some) {
-#pragma unroll
-      for (int e = 0; e < N; ++e) eq += key_of(v[e]) == tau && i + lane * N + e >= sl.begin && i + lane * N + e < sl.count;
-      unsigned inc = eq;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
+            for (int e = 0; e < N; ++e) n += x[e] > -INFINITY && digit_key<T>(clean(x[e])) == tau;
+          }
+          n = __reduce_add_sync(0xffffffffu, n);
+          if (lane == 0) stretch[b * kSW + warp].far = __uint_as_float(n);
+        });
+        __syncthreads();
+        const int n = blocks * kSW, per = (n + kST - 1) / kST;
+        unsigned long long mine = 0, part;
+        for (int i = t * per; i < min(n, (t + 1) * per); ++i) mine += __float_as_uint(stretch[i].far);
+        unsigned long long run = scan_l(mine, &part);
+        if (t == 0) sh.ties = (unsigned)part;
+        sync_row();
+        for (int c = 0; c < rank; ++c) run += *peer(&sh.ties, c);
+        for (int i = t * per; i < min(n, (t + 1) * per); ++i) {
+          const unsigned x = __float_as_uint(stretch[i].far);
+          stretch[i].far = __uint_as_float((unsigned)run);
+          run += x;
+        }
+        sync_row();  // (the counts have been read)
       }
-      at = rank0 + inc - eq;
-      rank0 += __shfl_sync(0xffffffffu, inc, 31);
+      start();
+      stream([&](int b, uint4 (&x4)[kVec], float (&tops)[kVec], auto&& next) {
+        next();
+        F2 s = {0.f, 0.f};
+        unsigned at = ties ? __float_as_uint(stretch[b * kSW + warp].far) : 0u;
+        const float ahead = __uint_as_float(at);
+#pragma unroll 1
+        for (int v = 0; v < kVec; ++v) {
+          const uint4 y4 = v == 0 ? x4[0] : v == 1 ? x4[1] : v == 2 ? x4[2] : x4[3];
+          const bool any = Vec<T>::top(y4) >= from;
+          if (!__any_sync(0xffffffffu, any)) continue;
+          float x[N];
+          Vec<T>::get(y4, x);
+          unsigned eq = 0, inc = 0;
+          if (ties) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) eq += x[e] > -INFINITY && digit_key<T>(clean(x[e])) == tau;
+            inc = eq;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const unsigned y = __shfl_up_sync(0xffffffffu, inc, o);
+              if (lane >= o) inc += y;
+            }
+          }
+          unsigned mine = at + inc - eq;
+          if (any) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+              const float c = clean(x[e]);
+              const unsigned k = digit_key<T>(c);
+              if (c > -INFINITY && (k > tau || (ties && k == tau && mine++ < n_tau))) {
+                const F2 w = weight(sc, c);
+                if (!below(w, r.lo)) s = add(s, w);
+              }
+            }
+          }
+          if (ties) at += __shfl_sync(0xffffffffu, inc, 31);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s = shfl_add(s, o);
+        if (lane == 0) stretch[b * kSW + warp] = Stretch{s.h, s.l, ahead, m_row};
+      });
+      __syncthreads();
+    }
+    // ---- the stretch that holds the target
+    const int n = blocks * kSW, per = (n + kST - 1) / kST;
+    auto mass_of = [&](int i) {
+      const Stretch s = stretch[i];
+      return s.ref > -INFINITY ? fix<43>(mul(F2{s.h, s.l}, weight(sc, s.ref))) : 0ull;
+    };
+    unsigned long long mine = 0, my_far = 0, part;
+    for (int i = t * per; i < min(n, (t + 1) * per); ++i) {
+      mine += mass_of(i);
+      if (!exact && stretch[i].ref > -INFINITY) my_far += fix<43>(F2{stretch[i].far * weight(sc, stretch[i].ref).h, 0.f});
     }
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const unsigned kk = key_of(v[e]);
-      bool in = kk > tau;
-      if (ties && kk == tau) in = some ? at++ < n_tau : whole;
-      if (in) {
-        w[e] = weight(sc, v[e]);
+    for (int o = 16; o > 0; o >>= 1) my_far += __shfl_xor_sync(0xffffffffu, my_far, o);
+    if (lane == 0 && my_far) atomicAdd(&sh.far, my_far);
+    if (t == 0) sh.pick[0] = 0x7fffffff, sh.pick[1] = -1;
+    unsigned long long run = scan_l(mine, &part), total = part, far = sh.far;
+    int last = 0;  // the row's last CTA with any mass
+    if (C > 1) {
+      if (t == 0) sh.part = part, sh.far_part = far;
+      cl.sync();
+      total = far = 0;
+      for (int c = 0; c < C; ++c) {
+        const unsigned long long x = *peer(&sh.part, c);
+        far += *peer(&sh.far_part, c);
+        if (c < rank) run += x;
+        if (x > 0) last = c;
+        total += x;
+      }
+    }
+    const unsigned long long target = part_of(total, r.u);
+    // the fp32 sums' error: of what lies ahead, and of the target
+    const unsigned long long slack = exact ? 0ull : part_of(far, 2.f * kFastError) + 1024;
+    for (int i = t * per; i < min(n, (t + 1) * per); ++i) {  // this CTA's first stretch past the target, and its last with any mass
+      const unsigned long long x = mass_of(i);
+      if (x > 0) {
+        if (run <= target && run + x > target) sh.pick[0] = i, sh.before = run;
+        atomicMax(&sh.pick[1], i);
+      }
+      run += x;
+    }
+    __syncthreads();
+    const bool mine_past = sh.pick[0] != 0x7fffffff;
+    if (total == 0) {  // min-p above 1: nothing is left
+      if (rank == 0 && t == 0) put(q, row, -1, 0.f);
+    } else if (mine_past || (rank == last && target >= total)) {  // (u >= 1: the row's last kept one)
+      // the whole CTA walks the stretch: thread t has its positions kE t .. kE t + kE - 1
+      constexpr int kE = kWarpPart / kST;
+      const int at = mine_past ? sh.pick[0] : sh.pick[1];
+      const int i0 = at / kSW * kBlock + at % kSW * kWarpPart + t * kE;
+      const unsigned long long before = mine_past ? sh.before : 0ull, goal = mine_past ? target : ~0ull;
+      float x[kE];
+      unsigned eq = 0;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        const int i = i0 + e;
+        x[e] = i >= sl.begin && i < sl.count ? clean(Elem<T>::to_f(*sl.at(i))) : -INFINITY;
+        eq += x[e] > -INFINITY && digit_key<T>(x[e]) == tau;
+      }
+      unsigned long long all;
+      unsigned tie = ties ? (unsigned)scan_l(eq, &all) + __float_as_uint(stretch[at].far) : 0u;
+      F2 w[kE];
+      unsigned long long f[kE], sum_w = 0;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        const unsigned k = digit_key<T>(x[e]);
+        w[e] = F2{0.f, 0.f};
+        if (x[e] > -INFINITY && (k > tau || (ties && k == tau && tie++ < n_tau))) w[e] = weight(sc, x[e]);
         if (below(w[e], r.lo)) w[e] = F2{0.f, 0.f};
+        f[e] = fix<43>(w[e]);
+        sum_w += f[e];
+      }
+      unsigned long long cum = before + scan_l(sum_w, &all);
+      if (t == 0) sh.pick[0] = 0x7fffffff, sh.pick[1] = -1;
+      __syncthreads();
+      // the first position past the target, else the last with any mass
+      int hit = -1, any = -1;
+      unsigned long long from = 0, to = 0;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        if (f[e] > 0) {
+          any = i0 + e;
+          if (hit < 0 && cum + f[e] > goal) hit = i0 + e, from = cum, to = cum + f[e];
+        }
+        cum += f[e];
+      }
+      if (hit >= 0) atomicMin(&sh.pick[0], hit);
+      if (any >= 0) atomicMax(&sh.pick[1], any);
+      __syncthreads();
+      const int token = sh.pick[0] != 0x7fffffff ? sh.pick[0] : sh.pick[1];
+      if (token >= i0 && token < i0 + kE) {
+        F2 tw = w[0];
+#pragma unroll
+        for (int e = 1; e < kE; ++e)
+          if (token == i0 + e) tw = w[e];
+        // sure: the fp32 sums' error moves neither border of the token past the target, nor the
+        // probability's last bit
+        bool sure = exact || !mine_past || (token == hit && (from == 0 || from + slack <= target) && to > target + slack);
+        if (q.probs && !exact) sure = sure && (float)far * kFastError <= (float)total * kProbError;
+        if (sure)
+          put(q, row, sl.first + token, prob_of(tw, total));
+        else
+          for (int c = 0; c < C; ++c) *peer(&sh.again, c) = 1;  // once more, exactly
       }
     }
-  };
-  F2 sum = {0, 0};
-  unsigned rank0 = ties_before;
-  for (int i = warp * seg; i < (warp + 1) * seg; i += 32 * N) {
-    F2 w[N];
-    kept(i, rank0, w);
-#pragma unroll
-    for (int e = 0; e < N; ++e) sum = add(sum, w[e]);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum = shfl_add(sum, o);
-  if (lane == 0) sh.wsum[warp] = fix<43>(sum);
-  cl.sync();
-  if (t < kC * kWarps) sh.all_sum[t] = cl.map_shared_rank(sh.wsum, t / kWarps)[t % kWarps];
-  __syncthreads();
-  // the first segment whose running sum exceeds the target (else the last with any mass): lane l
-  // has segments [l kS, (l + 1) kS)
-  constexpr int kS = kC * kWarps / 32;
-  unsigned long long inc = 0;
-#pragma unroll
-  for (int e = 0; e < kS; ++e) inc += sh.all_sum[lane * kS + e];
-  unsigned long long run = inc;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long x = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += x;
-  }
-  const unsigned long long total = __shfl_sync(0xffffffffu, inc, 31), target = part_of(total, r.u);
-  run = inc - run;
-  int mine_at = -1;  // this lane's first segment past the target, else its last with any mass
-  unsigned long long mine_before = 0;
-  bool past = false;
-#pragma unroll
-  for (int e = 0; e < kS; ++e) {
-    const unsigned long long x = sh.all_sum[lane * kS + e];
-    if (x > 0 && !past) mine_at = lane * kS + e, mine_before = run, past = run + x > target;
-    run += x;
-  }
-  const unsigned hits = __ballot_sync(0xffffffffu, past), any = __ballot_sync(0xffffffffu, mine_at >= 0);
-  int owner = -1;
-  unsigned long long before = 0;
-  if (any) {
-    const int from_lane = hits ? __ffs(hits) - 1 : 31 - __clz(any);
-    owner = __shfl_sync(0xffffffffu, mine_at, from_lane);
-    before = __shfl_sync(0xffffffffu, mine_before, from_lane);
-  }
-  if (owner < 0 && rank == 0 && t == 0) put(q, row, -1, 0.f);  // min-p above 1: nothing is left
-  if (owner == rank * kWarps + warp) {
-    int token;
-    F2 w;
-    rank0 = ties_before;
-    walk<N>(seg, before, target, [&](int i0, F2 (&ws)[N]) { kept(warp * seg + i0, rank0, ws); }, &token, &w);
-    if (lane == 0)
-      put(q, row, token >= 0 ? sl.first + warp * seg + token : -1, token >= 0 ? prob_of(w, total) : 0.f);
-  }
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) select_kernel(const SampleParams q) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ SelectShared sh;
-  cg::cluster_group cl = cg::this_cluster();
-  tc::pdl_wait();
-  if (threadIdx.x < 128) sh.table[threadIdx.x] = q.table[threadIdx.x];
-  const int clusters = gridDim.x / kC, mine = blockIdx.x / kC;
-  const int t = threadIdx.x, warp = t >> 5;
-  // this cluster's rows are mine, mine + clusters, ..: kThreads of them looked at together.  Every
-  // CTA reads the same marks: a row's token is written only after barriers that follow the look.
-  for (int64_t i0 = 0; mine + i0 * clusters < q.rows; i0 += kThreads) {
-    const int64_t row = mine + (i0 + t) * clusters;
-    const unsigned left = __ballot_sync(0xffffffffu, row < q.rows && q.tokens[row] == kRetry);
-    if ((t & 31) == 0) sh.todo[warp] = left;
-    __syncthreads();
-    for (int w = 0; w < kWarps; ++w) {
-      for (unsigned m = sh.todo[w]; m; m &= m - 1) {
-        const int64_t at = mine + (i0 + w * 32 + __ffs(m) - 1) * clusters;
-        select_row<T>(q, (int)at, reinterpret_cast<T*>(smem), sh, cl);
-        cl.sync();  // the row's exchanges are over
-      }
-    }
-    __syncthreads();
+    sync_row();
+    if (exact || !sh.again) return;
   }
 }
 
@@ -1220,51 +1136,28 @@ struct Powers {  // 2^(j / 128) as pairs of floats
   }
 };
 
-template <typename T, int C>
-cudaError_t launch_stream(SampleParams p, cudaStream_t st) {
+template <typename T>
+cudaError_t launch(SampleParams p, int sms, cudaStream_t st) {
   static std::atomic<unsigned long long> attr{0};
-  if (cudaError_t e = smem_attr_once(stream_kernel<T, C>, kStreamSmem, attr); e != cudaSuccess) return e;
-  p.per = (p.vocab + 7 + C - 1) / C;  // (up to 7 positions before an unaligned row)
+  if (cudaError_t e = smem_attr_once(sample_kernel<T>, kStreamSmem, attr); e != cudaSuccess) return e;
+  // as many CTAs per row (up to 8) as run together, three per SM, when the row is long enough to
+  // be worth the exchanges: 64 rows of 262144 fp32 take 7
+  const int64_t blocks = ((int64_t)p.vocab * (int)sizeof(T) + kStageBytes - 1) / kStageBytes;
+  p.ctas = (int)std::max<int64_t>(1, std::min<int64_t>({(int64_t)kMaxC, 3ll * sms / p.rows, blocks / 2}));
+  p.per = (p.vocab + 7 + p.ctas - 1) / p.ctas;  // (up to 7 positions before an unaligned row)
   p.per = (p.per + 7) / 8 * 8;
   cudaLaunchConfig_t c = {};
   cudaLaunchAttribute a[1];
   a[0].id = cudaLaunchAttributeClusterDimension;
-  a[0].val.clusterDim.x = C;
+  a[0].val.clusterDim.x = p.ctas;
   a[0].val.clusterDim.y = a[0].val.clusterDim.z = 1;
-  c.gridDim = dim3(p.rows * C);
+  c.gridDim = dim3(p.rows * p.ctas);
   c.blockDim = dim3(kST);
   c.dynamicSmemBytes = kStreamSmem;
   c.stream = st;
   c.attrs = a;
-  c.numAttrs = C > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&c, stream_kernel<T, C>, p);
-}
-
-template <typename T>
-cudaError_t launch(SampleParams p, int sms, cudaStream_t st) {
-  // one CTA per row where rows fill the SMs; eight where they do not, and the row is long enough
-  const bool few = p.rows < sms && (int64_t)p.vocab * (int)sizeof(T) > 2 * kStageBytes;
-  cudaError_t e = few ? launch_stream<T, 8>(p, st) : launch_stream<T, 1>(p, st);
-  if (e != cudaSuccess) return e;
-  static std::atomic<unsigned long long> attr{0};
-  if (e = smem_attr_once(select_kernel<T>, kSliceBytes, attr); e != cudaSuccess) return e;
-  p.per = (p.vocab + 7 + kC - 1) / kC;
-  p.per = (p.per + 7) / 8 * 8;
-  constexpr int step = Vec<T>::N * kThreads;
-  cudaLaunchConfig_t c = {};
-  cudaLaunchAttribute a[2];
-  a[0].id = cudaLaunchAttributeClusterDimension;
-  a[0].val.clusterDim.x = kC;
-  a[0].val.clusterDim.y = a[0].val.clusterDim.z = 1;
-  a[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a[1].val.programmaticStreamSerializationAllowed = 1;
-  c.gridDim = dim3(std::min(p.rows, std::max(1, 2 * sms / kC)) * kC);
-  c.blockDim = dim3(kThreads);
-  c.dynamicSmemBytes = (p.per + step - 1) / step * step * sizeof(T);
-  c.stream = st;
-  c.attrs = a;
-  c.numAttrs = 2;
-  return cudaLaunchKernelEx(&c, select_kernel<T>, p);
+  c.numAttrs = p.ctas > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&c, sample_kernel<T>, p);
 }
 
 }  // namespace
@@ -1282,7 +1175,7 @@ extern "C" int dflash_sample(const void* logits, int64_t row_stride, int32_t dty
   if (rows > (1 << 28) - 1) return call_error(DFLASH_ECAPACITY, "sample: too many rows for one call");
   if (rows == 0) return DFLASH_OK;
   if (!logits || !u || !tokens) return call_error(DFLASH_EINVAL, "sample: null pointer");
-  SampleParams p{logits, row_stride, rows, vocab, u, temperature, top_p, min_p, top_k, tokens, probs, 0, {}};
+  SampleParams p{logits, row_stride, rows, vocab, u, temperature, top_p, min_p, top_k, tokens, probs, 1, 0, {}};
   static const Powers powers;
   memcpy(p.table, powers.table, sizeof p.table);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
