@@ -301,7 +301,7 @@ constexpr int kAim = 3072;                   // and that the floor may aim at
 constexpr int kSorted = 2048;                // logits of the sorted prefix
 constexpr int kBins = 256;                   // histogram of the list
 constexpr int kLook = 64;                    // bins of the look at the first blocks,
-constexpr float kLookNear = 12.f, kLookFar = 32.f;  // and their ranges of t below the maximum found there
+constexpr float kLookFar = 32.f;             // and their range of t below the maximum found there
 constexpr int kDigit = 10, kKeys = 1 << kDigit;     // histograms over keys
 // Far masses in fp32: a bound on their relative error (x - m rounded: t 2^-25 ln 2 < 8.3e-7; ex2
 // 2^-22; the correction's and the tree's roundings 5 2^-24), and the error a probability may carry
@@ -444,87 +444,88 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     return s0 + s1;
   };
   float floor_x = -INFINITY;  // the list takes logits from here on
-  if (by_list) {
-    const float share = (float)seen / (float)max(blocks, 1);  // of the row seen
-    for (int far = 0; far < 2; ++far) {
-      const float range = far ? kLookFar : kLookNear, step = range / kLook;
-      const float from = reach(sc, range), cut_x = reach(sc, kCut);
-      const bool beyond = sum && !far && m > -INFINITY && m < INFINITY && !isinf(sc.c_hi);
-      float rest = 0.f;  // top-p alone: the mass past the range
-      for (int b = 0; b < seen; ++b) {
-#pragma unroll 1
-        for (int v = 0; v < kVec; ++v) {
-          const uint4 x4 = ring[(b * kVec + v) * kST + t];
-          const float top = Vec<T>::top(x4);
-          if (!(top >= from)) {
-            if (beyond && top >= cut_x) rest += fast(x4);
-            continue;
-          }
-          float x[N];
-          Vec<T>::get(x4, x);
-#pragma unroll
-          for (int e = 0; e < N; ++e) {
-            const float tt = t_of(sc, clean(x[e]));
-            if (tt < range && x[e] > -INFINITY)
-              atomicAdd(&sh.count[min(kLook - 1, (int)(tt / step))], 1u);
-            else if (beyond)
-              rest += ex2(-tt);
-          }
-        }
-      }
-      if (beyond) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
-        if (lane == 0) atomicAdd(&sh.part, fix<43>(F2{rest, 0.f}));
-      }
-      sync_row();
-      if (warp == 0) {
-        // lane l: bins 2 l, 2 l + 1 of the row's first blocks.  The first bins by which, going by them,
-        // the list holds what the filter needs: k and half as many more; all but 1 - p of the mass
-        // (the mass left out, as the blocks seen have it, against that seen alone: the few large
-        // weights of a row may lie anywhere) and some 192 logits; every t up to min-p's
-        unsigned a = 0, b = 0;
-        for (int c = 0; c < C; ++c) a += peer(sh.count, c)[2 * lane], b += peer(sh.count, c)[2 * lane + 1];
-        unsigned n = a + b;
-        float w = a * exp2f(-(2 * lane + 0.5f) * step) + b * exp2f(-(2 * lane + 1.5f) * step);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned x = __shfl_up_sync(0xffffffffu, n, o);
-          const float y = __shfl_up_sync(0xffffffffu, w, o);
-          if (lane >= o) n += x, w += y;
-        }
-        float whole = __shfl_sync(0xffffffffu, w, 31);
-        for (int c = 0; c < C; ++c) whole += (float)*peer(&sh.part, c) * 0x1p-43f;
-        const float end = (2 * lane + 2) * step;
-        bool enough = true;
-        if (r.use_k)
-          enough = n >= (1.5f * r.k + 64.f) * share;
-        else if (r.use_p)
-          enough = (whole - w) * 1.3f <= (1.f - r.p) * whole * share && n >= 192.f * share;
-        else
-          enough = end > -log2f(r.lo) + 0.5f;
-        const unsigned yes = __ballot_sync(0xffffffffu, enough), fits = __ballot_sync(0xffffffffu, n <= kAim * share);
-        const int need = yes ? __ffs(yes) : 33, room = max(1, ~fits ? __ffs(~fits) - 1 : 32);
-        if (lane == 0) {
-          sh.floor = m - min(min(need, room), 32) * 2 * step / sc.c_hi;
-          sh.pick[0] = need <= 32 || room < 32;
-        }
-      }
-      sync_row();  // (the counts have been read by every CTA)
-      const bool set = sh.pick[0] || far;  // the same in every CTA
-      floor_x = isinf(m) || isinf(sc.c_hi) ? m : sh.floor;
-      __syncthreads();
-      if (t < kLook) sh.count[t] = 0;
-      if (t == 0) sh.pick[0] = 0x7fffffff, sh.part = 0;
-      __syncthreads();
-      if (set) break;
+  const float share = (float)seen / (float)max(blocks, 1);  // of the row seen
+  // A floor by rank: the threads' largest logits in the blocks seen, of which the r-th is about the
+  // row's r / share-th (a thread seldom has two of them).  false: the list wants more than that tells
+  auto floor_by_rank = [&]() -> bool {
+    if (!r.use_k && !r.use_p) {  // min-p: every t up to its own (below the row's m, not this one's: more)
+      floor_x = isinf(m) || isinf(sc.c_hi) ? m : m - (fmaxf(0.f, -log2f(r.lo)) + 0.5f) / sc.c_hi;
+      return true;
     }
-  }
+    const float want = r.use_k ? 1.5f * r.k + 64.f : 320.f;
+    const int at = max(8, (int)ceilf(want * share / C));
+    if (at > kST / 2) return false;
+    unsigned* tops = places;
+    tops[t] = key_of(top + 0.f);
+    if (t == 0) sh.floor = -INFINITY;
+    __syncthreads();
+    int ahead = 0;
+    const unsigned mine = tops[t];
+    for (int i = 0; i < kST; ++i) ahead += tops[i] > mine || (tops[i] == mine && i < t);
+    if (ahead == at - 1) sh.floor = of_key(mine);
+    sync_row();
+    floor_x = sh.floor;
+    for (int c = 0; c < C; ++c) floor_x = fminf(floor_x, *peer(&sh.floor, c));
+    return true;
+  };
+  // A floor by a histogram of t in the blocks seen
+  auto floor_by_look = [&] {
+    const float step = kLookFar / kLook;
+    const float from = reach(sc, kLookFar);
+    for (int b = 0; b < seen; ++b) {
+#pragma unroll 1
+      for (int v = 0; v < kVec; ++v) {
+        const uint4 x4 = ring[(b * kVec + v) * kST + t];
+        if (!(Vec<T>::top(x4) >= from)) continue;
+        float x[N];
+        Vec<T>::get(x4, x);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const float tt = t_of(sc, clean(x[e]));
+          if (tt < kLookFar && x[e] > -INFINITY) atomicAdd(&sh.count[(int)(tt * (kLook / kLookFar))], 1u);
+        }
+      }
+    }
+    sync_row();
+    if (warp == 0) {
+      // lane l: bins 2 l, 2 l + 1 of the row's first blocks.  The first bins by which, going by them,
+      // the list holds what the filter needs: k and half as many more; all but 1 - p of the mass
+      // (the mass left out, as the blocks seen have it, against that seen alone: the few large
+      // weights of a row may lie anywhere) and some 192 logits
+      unsigned a = 0, b = 0;
+      for (int c = 0; c < C; ++c) a += peer(sh.count, c)[2 * lane], b += peer(sh.count, c)[2 * lane + 1];
+      unsigned n = a + b;
+      float w = a * exp2f(-(2 * lane + 0.5f) * step) + b * exp2f(-(2 * lane + 1.5f) * step);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned x = __shfl_up_sync(0xffffffffu, n, o);
+        const float y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) n += x, w += y;
+      }
+      const float whole = __shfl_sync(0xffffffffu, w, 31);
+      const bool enough = r.use_k ? n >= (1.5f * r.k + 64.f) * share
+                                  : !r.use_p || ((whole - w) * 1.3f <= (1.f - r.p) * whole * share && n >= 192.f * share);
+      const unsigned yes = __ballot_sync(0xffffffffu, enough), fits = __ballot_sync(0xffffffffu, n <= kAim * share);
+      const int pairs = min(yes ? __ffs(yes) : 32, max(1, ~fits ? __ffs(~fits) - 1 : 32));
+      if (lane == 0) sh.floor = isinf(m) || isinf(sc.c_hi) ? m : m - pairs * 2 * step / sc.c_hi;
+    }
+    sync_row();  // (the counts have been read by every CTA)
+    floor_x = sh.floor;
+    if (t < kLook) sh.count[t] = 0;
+    __syncthreads();
+  };
 
   // ---- the row
   float rest = 0.f;                                  // fp32 mass below the floor, relative to m
   unsigned long long best = 0;                       // greedy: (key, ~index)
-  stream([&](int b, uint4 (&x4)[kVec], float (&tops)[kVec], auto&& next) {
+  bool finite;                                       // m and log2(e) / T are: fp32 masses make sense
+  float cut_x, near_x;                               // vectors below weigh nothing; are far
+  auto bounds = [&] {
+    finite = m > -INFINITY && m < INFINITY && !isinf(sc.c_hi);
+    cut_x = reach(sc, kCut);
+    near_x = finite ? reach(sc, kNear) : cut_x;
+  };
+  auto first_pass = [&](int b, uint4 (&x4)[kVec], float (&tops)[kVec], auto&& next) {
     float top = tops[0];
 #pragma unroll
     for (int v = 1; v < kVec; ++v) top = fmaxf(top, tops[v]);
@@ -537,8 +538,10 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
       sc.m = m_new;
       rest *= exp2f(-t_of(sc, m));  // (0 at first: m = -inf)
       m = m_new;
+      bounds();
     }
     if (greedy) {
+      if (!(top >= m)) return;
 #pragma unroll
       for (int v = 0; v < kVec; ++v) {
         if (!(tops[v] >= m)) continue;
@@ -552,9 +555,8 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
       }
       return;
     }
-    const bool finite = m > -INFINITY && m < INFINITY && !isinf(sc.c_hi);
-    const float cut_x = reach(sc, kCut);  // vectors below weigh nothing
     if (by_list) {
+      if (!(top >= (sum ? fminf(floor_x, cut_x) : floor_x))) return;
 #pragma unroll
       for (int v = 0; v < kVec; ++v) {
         if (tops[v] >= floor_x) {
@@ -578,14 +580,10 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     }
     F2 s = {0.f, 0.f};
     float far = 0.f;
-    const float near_x = finite ? reach(sc, kNear) : cut_x;
 #pragma unroll
     for (int v = 0; v < kVec; ++v)
       if (tops[v] >= cut_x && !(tops[v] >= near_x)) far += fast(x4[v]);
-    bool near = false;
-#pragma unroll
-    for (int v = 0; v < kVec; ++v) near |= tops[v] >= near_x;
-    if (near) {
+    if (top >= near_x) {
 #pragma unroll 1
       for (int v = 0; v < kVec; ++v) {
         const uint4 y4 = v == 0 ? x4[0] : v == 1 ? x4[1] : v == 2 ? x4[2] : x4[3];
@@ -603,7 +601,13 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s = shfl_add(s, o), far += __shfl_xor_sync(0xffffffffu, far, o);
     if (lane == 0) stretch[b * kSW + warp] = Stretch{s.h, s.l, far, m};
-  });
+  };
+  bool looked = false;  // the floor is a look's
+  if (by_list && !floor_by_rank()) looked = true, floor_by_look();
+  __syncthreads();      // (the list takes the place of what the floor was found with)
+  rest = 0.f;
+  bounds();
+  stream(first_pass);
   if (greedy) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
@@ -800,37 +804,58 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
   unsigned tau = digit_key<T>(-INFINITY), n_tau = 0;  // -inf itself is never drawn
   bool ties = false, exact = false;
   if (by_list) {
-    {  // gather the row's list in the first CTA (its ring is idle: its own part of the row is through)
-      rest *= m > -INFINITY ? exp2f(-t_of(sc, m)) : 0.f;
-      unsigned long long* dst = peer(final_list, 0);
-      unsigned* n_at = peer(&sh.n_final, 0);
-      const int n = (int)min(sh.n_list, (unsigned)kList);
-      bool full = sh.n_list > kList;
-      for (int i = t; i < n; i += kST) {
-        const unsigned at = C > 1 ? atomicAdd(n_at, 1u) : i, place = places[i];
-        if (at < kList)
-          dst[at] = (unsigned long long)~key_of(clean(Elem<T>::to_f(sl.src[place]))) << 32 | place;
-        else
-          full = true;
-      }
-      if (C == 1 && t == 0) sh.n_final = n;
-      if (full) atomicOr(peer(&sh.full, 0), 1u);
-      if (sum) {
-        F2 s = {rest, 0.f};
+    for (;;) {
+      {  // gather the row's list in the first CTA (its ring is idle: its own part of the row is through)
+        rest *= m > -INFINITY ? exp2f(-t_of(sc, m)) : 0.f;
+        unsigned long long* dst = peer(final_list, 0);
+        unsigned* n_at = peer(&sh.n_final, 0);
+        const int n = (int)min(sh.n_list, (unsigned)kList);
+        bool full = sh.n_list > kList;
+        for (int i = t; i < n; i += kST) {
+          const unsigned at = C > 1 ? atomicAdd(n_at, 1u) : i, place = places[i];
+          if (at < kList)
+            dst[at] = (unsigned long long)~key_of(clean(Elem<T>::to_f(sl.src[place]))) << 32 | place;
+          else
+            full = true;
+        }
+        if (C == 1 && t == 0) sh.n_final = n;
+        if (full) atomicOr(peer(&sh.full, 0), 1u);
+        if (sum) {
+          F2 s = {rest, 0.f};
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s = shfl_add(s, o);
-        if (lane == 0) atomicAdd(peer(&sh.rest, 0), fix<43>(s));
+          for (int o = 16; o > 0; o >>= 1) s = shfl_add(s, o);
+          if (lane == 0) atomicAdd(peer(&sh.rest, 0), fix<43>(s));
+        }
       }
+      sync_row();
+      if (rank == 0) {
+        const bool done = from_list();
+        if (t == 0)
+          for (int c = 0; c < C; ++c) *peer(&sh.again, c) = !done;
+      }
+      sync_row();
+      if (!sh.again) return;
+      if (looked || (!r.use_k && !r.use_p)) break;
+      // once more with a floor that a look sets
+      looked = true;
+      m = m_row;
+      __syncthreads();
+      if (t < kBins) sh.count[t] = 0, sh.mass[t] = 0;
+      if (t == 0) {
+        sh.n_list = sh.n_final = sh.full = 0;
+        sh.rest = 0;
+        sh.pick[0] = 0x7fffffff;
+        sh.pick[1] = -1;
+      }
+      start();
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncthreads();
+      floor_by_look();
+      rest = 0.f;
+      bounds();
+      stream(first_pass);
+      sync_row();
     }
-    sync_row();
-    bool done = false;
-    if (rank == 0) {
-      done = from_list();
-      if (!done && t == 0)
-        for (int c = 0; c < C; ++c) *peer(&sh.again, c) = 1;
-    }
-    sync_row();
-    if (!sh.again) return;
 
     // ---- by histograms over keys.  One border: the first key, falling, by which the count reaches
     // k (by_mass: the mass reaches p of all).  Rounds over keys [lo, hi], kDigit bits of them each;
