@@ -314,8 +314,9 @@ static_assert(kList * 4 == kSideBytes && kSorted * 8 == kSideBytes && kKeys * 16
 static_assert(kList * 8 + kSorted * 8 <= kStages * kStageBytes, "the row's list, and places by index, fit in the ring");
 constexpr int kStreamSmem = kStages * kStageBytes + kSideBytes;
 
-struct Stretch {  // mass of a warp's part of a block, relative to ref; `far`: what of it came in fp32
-  float h, l, far, ref;
+struct Stretch {  // mass of a warp's part of a block (2^-43), relative to ref; `far`: what of it came in fp32
+  unsigned long long mass;
+  float far, ref;
 };
 
 struct Shared {
@@ -325,7 +326,7 @@ struct Shared {
   unsigned long long red_l[kSW], rest, best, before, part, far, far_part;
   unsigned red_u[kSW], ties;
   unsigned m_key, n_list, n_final, full, again;
-  float floor;
+  float floor, floors[kSW];
   int pick[2];
 };
 
@@ -357,12 +358,15 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
   auto pos_of = [&](int b, int v) { return b * kBlock + warp * kWarpPart + (v * 32 + lane) * N; };
   // a thread copies and reads back its own vectors, so the ring needs no barrier
   auto issue = [&](int b) {
-    if (b < blocks) {
+    uint4* d = ring + b % kStages * (kVec * kST) + t;
+    if (b * kBlock >= sl.begin && (b + 1) * kBlock <= sl.count) {
+      const T* src = sl.at(pos_of(b, 0));
 #pragma unroll
+      for (int v = 0; v < kVec; ++v) tc::cp_async16(d + v * kST, src + v * 32 * N);
+    } else if (b < blocks) {  // with the row's ends
       for (int v = 0; v < kVec; ++v) {
         const int i = pos_of(b, v);
-        uint4* d = ring + (b % kStages * kVec + v) * kST + t;
-        if (sl.whole(i)) tc::cp_async16(d, sl.at(i)); else *d = sl.edge(i);
+        if (sl.whole(i)) tc::cp_async16(d + v * kST, sl.at(i)); else d[v * kST] = sl.edge(i);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -422,16 +426,15 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
   const bool greedy = r.T == 0.f;
   const bool by_list = !greedy && (r.use_k || r.use_p || r.lo > 0.f);
   const bool sum = by_list && r.use_p && !r.use_k;
-  // 2^-t of a vector's logits, in fp32 (NaN and -inf give 0; m is finite): t with its low part
-  auto fast = [&](const uint4& v4) {
-    float x[N];
-    Vec<T>::get(v4, x);
+  // 2^-t of N logits, in fp32 (NaN and -inf fail the comparison with the cut; m is finite): t with
+  // its low part
+  auto fast_of = [&](const float (&x)[N]) {
     const uint64_t nm = pair(-m, -m), c = pair(sc.c_hi, sc.c_hi), nc = pair(-sc.c_hi, -sc.c_hi), cl2 = pair(sc.c_lo, sc.c_lo);
     const uint64_t ln2 = pair(0.693147182f, 0.693147182f);
     uint64_t s = 0;
 #pragma unroll
     for (int e = 0; e < N; e += 2) {
-      const uint64_t d = add2(pair(fmaxf(x[e], -FLT_MAX), fmaxf(x[e + 1], -FLT_MAX)), nm);
+      const uint64_t d = add2(pair(x[e], x[e + 1]), nm);
       const uint64_t tt = mul2(d, nc), lo = fma2(d, cl2, fma2(d, c, tt));
       float t0, t1, w0, w1;
       unpair(tt, t0, t1);
@@ -443,29 +446,38 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     unpair(s, s0, s1);
     return s0 + s1;
   };
+  auto fast = [&](const uint4& v4) {
+    float x[N];
+    Vec<T>::get(v4, x);
+    return fast_of(x);
+  };
   float floor_x = -INFINITY;  // the list takes logits from here on
   const float share = (float)seen / (float)max(blocks, 1);  // of the row seen
-  // A floor by rank: the threads' largest logits in the blocks seen, of which the r-th is about the
-  // row's r / share-th (a thread seldom has two of them).  false: the list wants more than that tells
+  // A floor by rank: of the threads' largest logits in the blocks seen, the r-th is about the row's
+  // r / share-th (a thread seldom has two of them).  false: the list wants more than that tells
   auto floor_by_rank = [&]() -> bool {
     if (!r.use_k && !r.use_p) {  // min-p: every t up to its own (below the row's m, not this one's: more)
       floor_x = isinf(m) || isinf(sc.c_hi) ? m : m - (fmaxf(0.f, -log2f(r.lo)) + 0.5f) / sc.c_hi;
       return true;
     }
     const float want = r.use_k ? 1.5f * r.k + 64.f : 320.f;
-    const int at = max(8, (int)ceilf(want * share / C));
-    if (at > kST / 2) return false;
-    unsigned* tops = places;
-    tops[t] = key_of(top + 0.f);
-    if (t == 0) sh.floor = -INFINITY;
-    __syncthreads();
+    const int at = max(1, (int)ceilf(want * share / (C * kSW)));  // per warp
+    if (at > 16) return false;
+    // each warp's at-th largest; their mean
+    const unsigned mine = key_of(top + 0.f);
     int ahead = 0;
-    const unsigned mine = tops[t];
-    for (int i = 0; i < kST; ++i) ahead += tops[i] > mine || (tops[i] == mine && i < t);
-    if (ahead == at - 1) sh.floor = of_key(mine);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const unsigned x = __shfl_sync(0xffffffffu, mine, i);
+      ahead += x > mine || (x == mine && i < lane);
+    }
+    if (ahead == at - 1) sh.floors[warp] = top;
     sync_row();
-    floor_x = sh.floor;
-    for (int c = 0; c < C; ++c) floor_x = fminf(floor_x, *peer(&sh.floor, c));
+    float mean = 0.f;
+    for (int c = 0; c < C; ++c)
+      for (int w = 0; w < kSW; ++w) mean += peer(sh.floors, c)[w];
+    floor_x = mean / (C * kSW);
+    if (!(floor_x < INFINITY)) floor_x = m;  // infinities among them
     return true;
   };
   // A floor by a histogram of t in the blocks seen
@@ -564,14 +576,13 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
           Vec<T>::get(x4[v], x);
 #pragma unroll
           for (int e = 0; e < N; ++e) {
-            const float c = clean(x[e]);
-            if (c >= floor_x && c > -INFINITY) {
+            if (x[e] >= floor_x && x[e] > -INFINITY) {
               const unsigned at = atomicAdd(&sh.n_list, 1u);
               if (at < kList) places[at] = (unsigned)(sl.first + pos_of(b, v) + e);
-            } else if (sum && finite) {
-              rest += ex2((c - m) * sc.c_hi);
+              x[e] = -INFINITY;
             }
           }
+          if (sum && finite) rest += fast_of(x);
         } else if (sum && finite && tops[v] >= cut_x) {
           rest += fast(x4[v]);
         }
@@ -581,26 +592,27 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     F2 s = {0.f, 0.f};
     float far = 0.f;
 #pragma unroll
-    for (int v = 0; v < kVec; ++v)
-      if (tops[v] >= cut_x && !(tops[v] >= near_x)) far += fast(x4[v]);
-    if (top >= near_x) {
+    for (int v = 0; v < kVec; ++v) {
+      if (!(tops[v] >= cut_x)) continue;
+      float x[N];
+      Vec<T>::get(x4[v], x);
+      if (tops[v] >= near_x) {
 #pragma unroll 1
-      for (int v = 0; v < kVec; ++v) {
-        const uint4 y4 = v == 0 ? x4[0] : v == 1 ? x4[1] : v == 2 ? x4[2] : x4[3];
-        if (!(Vec<T>::top(y4) >= near_x)) continue;
-        float x[N];
-        Vec<T>::get(y4, x);
+        for (int e = 0; e < N; ++e) {  // (by selects: a loop of one weight's size)
+          float c = x[0];
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const float c = clean(x[e]);
-          if (c > -INFINITY) s = add(s, weight(sc, c));
+          for (int k = 1; k < N; ++k) c = e == k ? x[k] : c;
+          if (c >= near_x && c > -INFINITY) s = add(s, weight(sc, c + 0.f));
         }
-      }
-    }
-    s = add(s, F2{far, 0.f});
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s = shfl_add(s, o), far += __shfl_xor_sync(0xffffffffu, far, o);
-    if (lane == 0) stretch[b * kSW + warp] = Stretch{s.h, s.l, far, m};
+        for (int e = 0; e < N; ++e) x[e] = x[e] >= near_x ? -INFINITY : x[e];
+      }
+      if (finite) far += fast_of(x);
+    }
+    unsigned long long mass = fix<43>(add(s, F2{far, 0.f}));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o), far += __shfl_xor_sync(0xffffffffu, far, o);
+    if (lane == 0) stretch[b * kSW + warp] = Stretch{mass, far, m};
   };
   bool looked = false;  // the floor is a look's
   if (by_list && !floor_by_rank()) looked = true, floor_by_look();
@@ -1035,9 +1047,10 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
           }
           if (ties) at += __shfl_sync(0xffffffffu, inc, 31);
         }
+        unsigned long long mass = fix<43>(s);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s = shfl_add(s, o);
-        if (lane == 0) stretch[b * kSW + warp] = Stretch{s.h, s.l, ahead, m_row};
+        for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
+        if (lane == 0) stretch[b * kSW + warp] = Stretch{mass, ahead, m_row};
       });
       __syncthreads();
     }
@@ -1045,7 +1058,10 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     const int n = blocks * kSW, per = (n + kST - 1) / kST;
     auto mass_of = [&](int i) {
       const Stretch s = stretch[i];
-      return s.ref > -INFINITY ? fix<43>(mul(F2{s.h, s.l}, weight(sc, s.ref))) : 0ull;
+      if (s.ref == m_row) return s.mass;
+      if (!(s.ref > -INFINITY)) return 0ull;
+      const float h = (float)s.mass, l = (float)(long long)(s.mass - (unsigned long long)h);
+      return fix<0>(mul(F2{h, l}, weight(sc, s.ref)));  // (in the same units)
     };
     unsigned long long mine = 0, my_far = 0, part;
     for (int i = t * per; i < min(n, (t + 1) * per); ++i) {
