@@ -264,6 +264,7 @@ struct Slice {
   }
   __device__ bool whole(int i) const { return i >= begin && i + Vec<T>::N <= count; }
   __device__ const T* at(int i) const { return src + (first + i); }
+  __device__ uint4 vector(int i) const { return whole(i) ? *reinterpret_cast<const uint4*>(at(i)) : edge(i); }
   __device__ uint4 edge(int i) const {  // a vector at the row's ends
     uint4 r = make_uint4(Vec<T>::kPad, Vec<T>::kPad, Vec<T>::kPad, Vec<T>::kPad);
 #pragma unroll
@@ -314,9 +315,10 @@ static_assert(kList * 4 == kSideBytes && kSorted * 8 == kSideBytes && kKeys * 16
 static_assert(kList * 8 + kSorted * 8 <= kStages * kStageBytes, "the row's list, and places by index, fit in the ring");
 constexpr int kStreamSmem = kStages * kStageBytes + kSideBytes;
 
-struct Stretch {  // mass of a warp's part of a block (2^-43), relative to ref; `far`: what of it came in fp32
+struct Stretch {  // mass of a warp's part of a block (2^-43), relative to ref
   unsigned long long mass;
-  float far, ref;
+  unsigned ties;  // logits equal to tau ahead of it
+  float ref;
 };
 
 struct Shared {
@@ -355,6 +357,9 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
 
   const Slice<T> sl(q, row, rank);
   const int blocks = (sl.count + kBlock - 1) / kBlock;
+  // behind the stretches: vectors near the maximum
+  unsigned* near_places = reinterpret_cast<unsigned*>(stretch + blocks * kSW);
+  const unsigned near_room = kSideBytes / 4 - blocks * kSW * 4;
   auto pos_of = [&](int b, int v) { return b * kBlock + warp * kWarpPart + (v * 32 + lane) * N; };
   // a thread copies and reads back its own vectors, so the ring needs no barrier
   auto issue = [&](int b) {
@@ -571,48 +576,30 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
       if (!(top >= (sum ? fminf(floor_x, cut_x) : floor_x))) return;
 #pragma unroll
       for (int v = 0; v < kVec; ++v) {
-        if (tops[v] >= floor_x) {
-          float x[N];
-          Vec<T>::get(x4[v], x);
-#pragma unroll
-          for (int e = 0; e < N; ++e) {
-            if (x[e] >= floor_x && x[e] > -INFINITY) {
-              const unsigned at = atomicAdd(&sh.n_list, 1u);
-              if (at < kList) places[at] = (unsigned)(sl.first + pos_of(b, v) + e);
-              x[e] = -INFINITY;
-            }
-          }
-          if (sum && finite) rest += fast_of(x);
+        if (tops[v] >= floor_x) {  // its logits are looked at when the row is through, by all lanes
+          const unsigned at = atomicAdd(&sh.n_list, 1u);
+          if (at < kList) places[at] = pos_of(b, v);
         } else if (sum && finite && tops[v] >= cut_x) {
           rest += fast(x4[v]);
         }
       }
       return;
     }
-    F2 s = {0.f, 0.f};
     float far = 0.f;
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
       if (!(tops[v] >= cut_x)) continue;
-      float x[N];
-      Vec<T>::get(x4[v], x);
-      if (tops[v] >= near_x) {
-#pragma unroll 1
-        for (int e = 0; e < N; ++e) {  // (by selects: a loop of one weight's size)
-          float c = x[0];
-#pragma unroll
-          for (int k = 1; k < N; ++k) c = e == k ? x[k] : c;
-          if (c >= near_x && c > -INFINITY) s = add(s, weight(sc, c + 0.f));
-        }
-#pragma unroll
-        for (int e = 0; e < N; ++e) x[e] = x[e] >= near_x ? -INFINITY : x[e];
+      if (tops[v] >= near_x) {  // exactly, when the row is through
+        const unsigned at = atomicAdd(&sh.n_list, 1u);
+        if (at < near_room) near_places[at] = pos_of(b, v);
+      } else {
+        far += fast(x4[v]);
       }
-      if (finite) far += fast_of(x);
     }
-    unsigned long long mass = fix<43>(add(s, F2{far, 0.f}));
+    unsigned long long mass = fix<43>(F2{far, 0.f});
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o), far += __shfl_xor_sync(0xffffffffu, far, o);
-    if (lane == 0) stretch[b * kSW + warp] = Stretch{mass, far, m};
+    for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
+    if (lane == 0) stretch[b * kSW + warp] = Stretch{mass, 0u, m};
   };
   bool looked = false;  // the floor is a look's
   if (by_list && !floor_by_rank()) looked = true, floor_by_look();
@@ -819,18 +806,44 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     for (;;) {
       {  // gather the row's list in the first CTA (its ring is idle: its own part of the row is through)
         rest *= m > -INFINITY ? exp2f(-t_of(sc, m)) : 0.f;
+        m = m_row;
+        bounds();
         unsigned long long* dst = peer(final_list, 0);
         unsigned* n_at = peer(&sh.n_final, 0);
         const int n = (int)min(sh.n_list, (unsigned)kList);
         bool full = sh.n_list > kList;
-        for (int i = t; i < n; i += kST) {
-          const unsigned at = C > 1 ? atomicAdd(n_at, 1u) : i, place = places[i];
-          if (at < kList)
-            dst[at] = (unsigned long long)~key_of(clean(Elem<T>::to_f(sl.src[place]))) << 32 | place;
-          else
-            full = true;
+        // (whole warps: a vector per lane, their hits counted together)
+        for (int i = t; i < (n + 31) / 32 * 32; i += kST) {
+          float x[N];
+          const int pos = i < n ? (int)places[i] : 0;
+          if (i < n) Vec<T>::get(sl.vector(pos), x);
+          int hits = 0;
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            if (i >= n) x[e] = -INFINITY;
+            hits += x[e] >= floor_x && x[e] > -INFINITY;
+          }
+          int inc = hits;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+          }
+          unsigned at = 0;
+          if (lane == 31) at = atomicAdd(n_at, (unsigned)inc);
+          at = __shfl_sync(0xffffffffu, at, 31) + inc - hits;
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            if (x[e] >= floor_x && x[e] > -INFINITY) {
+              if (at < kList)
+                dst[at++] = (unsigned long long)~key_of(x[e] + 0.f) << 32 | (unsigned)(sl.first + pos + e);
+              else
+                full = true;
+              x[e] = -INFINITY;
+            }
+          }
+          if (sum && finite) rest += fast_of(x);
         }
-        if (C == 1 && t == 0) sh.n_final = n;
         if (full) atomicOr(peer(&sh.full, 0), 1u);
         if (sum) {
           F2 s = {rest, 0.f};
@@ -992,19 +1005,19 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
             for (int e = 0; e < N; ++e) n += x[e] > -INFINITY && digit_key<T>(clean(x[e])) == tau;
           }
           n = __reduce_add_sync(0xffffffffu, n);
-          if (lane == 0) stretch[b * kSW + warp].far = __uint_as_float(n);
+          if (lane == 0) stretch[b * kSW + warp].ties = n;
         });
         __syncthreads();
         const int n = blocks * kSW, per = (n + kST - 1) / kST;
         unsigned long long mine = 0, part;
-        for (int i = t * per; i < min(n, (t + 1) * per); ++i) mine += __float_as_uint(stretch[i].far);
+        for (int i = t * per; i < min(n, (t + 1) * per); ++i) mine += stretch[i].ties;
         unsigned long long run = scan_l(mine, &part);
         if (t == 0) sh.ties = (unsigned)part;
         sync_row();
         for (int c = 0; c < rank; ++c) run += *peer(&sh.ties, c);
         for (int i = t * per; i < min(n, (t + 1) * per); ++i) {
-          const unsigned x = __float_as_uint(stretch[i].far);
-          stretch[i].far = __uint_as_float((unsigned)run);
+          const unsigned x = stretch[i].ties;
+          stretch[i].ties = (unsigned)run;
           run += x;
         }
         sync_row();  // (the counts have been read)
@@ -1013,8 +1026,8 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
       stream([&](int b, uint4 (&x4)[kVec], float (&tops)[kVec], auto&& next) {
         next();
         F2 s = {0.f, 0.f};
-        unsigned at = ties ? __float_as_uint(stretch[b * kSW + warp].far) : 0u;
-        const float ahead = __uint_as_float(at);
+        unsigned at = ties ? stretch[b * kSW + warp].ties : 0u;
+        const unsigned ahead = at;
 #pragma unroll 1
         for (int v = 0; v < kVec; ++v) {
           const uint4 y4 = v == 0 ? x4[0] : v == 1 ? x4[1] : v == 2 ? x4[2] : x4[3];
@@ -1056,18 +1069,33 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     }
     // ---- the stretch that holds the target
     const int n = blocks * kSW, per = (n + kST - 1) / kST;
-    auto mass_of = [&](int i) {
-      const Stretch s = stretch[i];
-      if (s.ref == m_row) return s.mass;
-      if (!(s.ref > -INFINITY)) return 0ull;
-      const float h = (float)s.mass, l = (float)(long long)(s.mass - (unsigned long long)h);
-      return fix<0>(mul(F2{h, l}, weight(sc, s.ref)));  // (in the same units)
-    };
     unsigned long long mine = 0, my_far = 0, part;
-    for (int i = t * per; i < min(n, (t + 1) * per); ++i) {
-      mine += mass_of(i);
-      if (!exact && stretch[i].ref > -INFINITY) my_far += fix<43>(F2{stretch[i].far * weight(sc, stretch[i].ref).h, 0.f});
+    if (!exact) {
+      // by the row's maximum now, and the near vectors exactly
+      for (int i = t; i < n; i += kST) {
+        Stretch& s = stretch[i];
+        if (s.ref != m_row) {
+          const float h = (float)s.mass, l = (float)(long long)(s.mass - (unsigned long long)h);
+          s.mass = s.ref > -INFINITY ? fix<0>(mul(F2{h, l}, weight(sc, s.ref))) : 0ull;  // (in the same units)
+        }
+        my_far += s.mass;
+      }
+      __syncthreads();
+      for (int i = t; i < (int)min(sh.n_list, near_room); i += kST) {
+        const int pos = near_places[i];
+        float x[N];
+        Vec<T>::get(sl.vector(pos), x);
+        F2 s = {0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (clean(x[e]) > -INFINITY) s = add(s, weight(sc, clean(x[e])));
+        atomicAdd(&stretch[pos / kBlock * kSW + pos % kBlock / kWarpPart].mass, fix<43>(s));
+      }
+      __syncthreads();
     }
+    for (int i = t * per; i < min(n, (t + 1) * per); ++i) mine += stretch[i].mass;
+    if (!exact && t == 0 && sh.n_list > near_room)  // near vectors were left out
+      for (int c = 0; c < C; ++c) *peer(&sh.again, c) = 1;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) my_far += __shfl_xor_sync(0xffffffffu, my_far, o);
     if (lane == 0 && my_far) atomicAdd(&sh.far, my_far);
@@ -1086,11 +1114,12 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
         total += x;
       }
     }
+    const bool whole = exact || !sh.again;
     const unsigned long long target = part_of(total, r.u);
     // the fp32 sums' error: of what lies ahead, and of the target
     const unsigned long long slack = exact ? 0ull : part_of(far, 2.f * kFastError) + 1024;
     for (int i = t * per; i < min(n, (t + 1) * per); ++i) {  // this CTA's first stretch past the target, and its last with any mass
-      const unsigned long long x = mass_of(i);
+      const unsigned long long x = stretch[i].mass;
       if (x > 0) {
         if (run <= target && run + x > target) sh.pick[0] = i, sh.before = run;
         atomicMax(&sh.pick[1], i);
@@ -1116,7 +1145,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
         eq += x[e] > -INFINITY && digit_key<T>(x[e]) == tau;
       }
       unsigned long long all;
-      unsigned tie = ties ? (unsigned)scan_l(eq, &all) + __float_as_uint(stretch[at].far) : 0u;
+      unsigned tie = ties ? (unsigned)scan_l(eq, &all) + stretch[at].ties : 0u;
       F2 w[kE];
       unsigned long long f[kE], sum_w = 0;
 #pragma unroll
@@ -1153,7 +1182,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
           if (token == i0 + e) tw = w[e];
         // sure: the fp32 sums' error moves neither border of the token past the target, nor the
         // probability's last bit
-        bool sure = exact || !mine_past || (token == hit && (from == 0 || from + slack <= target) && to > target + slack);
+        bool sure = exact || (whole && !mine_past) || (whole && token == hit && (from == 0 || from + slack <= target) && to > target + slack);
         if (q.probs && !exact) sure = sure && (float)far * kFastError <= (float)total * kProbError;
         if (sure)
           put(q, row, sl.first + token, prob_of(tw, total));
