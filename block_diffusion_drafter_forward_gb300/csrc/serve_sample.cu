@@ -659,20 +659,55 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
       const float x = of_key(~(unsigned)(final_list[i] >> 32));
       const int b = bin_of(t_of(sc, x));
       atomicAdd(&sh.count[b], 1u);
-      if (sum) atomicAdd(&sh.mass[b], fix<51>(weight(sc, x)));  // (4096 of them, and the rest, below 2^64)
+      if (r.use_p) atomicAdd(&sh.mass[b], fix<51>(weight(sc, x)));  // (4096 of them, and the rest, below 2^64)
     }
     __syncthreads();
     // thread t: bin t.  The last bin that the prefix reaches
     unsigned long long all, goal = ~0ull;
     const unsigned cum = (unsigned)scan_l(sh.count[t], &all) + sh.count[t];
+    unsigned long long whole = 0, run_m = 0;
+    if (r.use_p) run_m = scan_l(sh.mass[t], &whole) + sh.mass[t];
+    whole += sh.rest << 8;
+    bool goal_set = sum;
+    if (r.use_k && r.use_p) {
+      // the mass left by top-k: the bins before the one in which the count reaches k, and the largest
+      // of that one
+      if (cum >= (unsigned)r.k && cum - sh.count[t] < (unsigned)r.k) {
+        sh.pick[1] = t;
+        sh.red_u[1] = cum - sh.count[t];
+        sh.before = run_m - sh.mass[t];
+      }
+      if (t == 0) sh.n_list = 0;
+      __syncthreads();
+      const int bin_k = sh.pick[1];
+      if (bin_k < 0) return false;
+      const unsigned in_bin = sh.count[bin_k];
+      if (in_bin <= kST) {
+        for (int i = t; i < n_all; i += kST) {
+          const unsigned long long it = final_list[i];
+          if (bin_of(t_of(sc, of_key(~(unsigned)(it >> 32)))) == bin_k) list[atomicAdd(&sh.n_list, 1u)] = it;
+        }
+        __syncthreads();
+        unsigned long long w = 0;
+        if (t < in_bin) {
+          const unsigned long long it = list[t];
+          unsigned ahead = sh.red_u[1];
+          for (unsigned j = 0; j < in_bin; ++j) ahead += list[j] < it;
+          if (ahead < (unsigned)r.k) w = fix<51>(weight(sc, of_key(~(unsigned)(it >> 32))));
+        }
+        scan_l(w, &all);
+        whole = sh.before + all;
+        goal_set = true;
+      }
+      __syncthreads();
+      if (t == 0) sh.pick[1] = -1;
+    }
     bool here;
-    if (sum) {
-      unsigned long long whole;
-      const unsigned long long run = scan_l(sh.mass[t], &whole) + sh.mass[t];
+    if (goal_set) {
       bool more;
-      goal = part_of(whole + (sh.rest << 8), r.p, &more);
-      goal += more;
-      here = run >= goal;
+      goal = part_of(whole, r.p, &more);
+      goal = max(goal + more, 1ull);  // the first always stays
+      here = run_m >= goal;
       goal = goal >> 63 ? ~0ull : goal << 1;  // in the sorted prefix's units
     } else if (r.use_k) {
       here = cum >= (unsigned)r.k;
@@ -733,7 +768,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     }
     const unsigned long long before = scan_l(mine, &all);
     const int k_end = r.use_k ? min(n, r.k) : n;
-    if (r.use_k && r.use_p) {  // the goal is a part of the mass left by top-k
+    if (r.use_p && !goal_set) {  // the goal is a part of the mass left by top-k
       unsigned long long run = before;
       for (int e = 0; e < per && i0 + e < k_end; ++e) {
         run += list[i0 + e];
