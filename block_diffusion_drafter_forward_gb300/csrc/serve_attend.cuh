@@ -21,16 +21,16 @@ struct AttendParams {
 
 // Workspace of the tensor-core form: split units' partials.
 struct AttendWork {
-  float4* o;       // [2 sms][rows] unnormalised O, by part_at
+  float* o;        // [2 sms][rows][head_dim] unnormalised O
   float2* ml;      // [2 sms][rows] (maximum in log2 units, sum)
   int4* meta;      // [sms] the unit that starts in a CTA and ends in a later one: (CTAs, s, tile, g)
   int long_chunks; // many query tiles per sequence
 };
 
-// Dims 4 db .. of row r of partial slot `slot`: [slot][r / 4][db][r % 4], so that a merging block
-// reads 4 rows of a slot as one run and a row-per-thread writer stores 64 bytes per 4 rows.
-__device__ __forceinline__ float4* part_at(const AttendWork& w, int slot, int r, int db, int rows, int hd) {
-  return w.o + (((int64_t)slot * rows + (r & ~3)) * (hd / 4) + db * 4 + (r & 3));
+// Row r of partial slot `slot` (rows of fp32, as many as a unit of `rows` has): a warp merges a row,
+// a row-per-thread writer stores whole sectors.
+__device__ __forceinline__ float* part_row(const AttendWork& w, int slot, int r, int rows, int hd) {
+  return w.o + ((int64_t)slot * rows + r) * hd;
 }
 
 __device__ __forceinline__ float lse_of(float m, float l) {

@@ -144,6 +144,44 @@ __device__ __forceinline__ long long tile_slots(const AttendParams& p, const Sha
 // This CTA's walk.  `scratch`: nb long longs of shared memory.  All threads.
 __device__ Walk plan(const AttendParams& p, const Shape& h, Ctl& c, long long* scratch, bool wide, long long* W_out) {
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  if (p.nb <= 32 && !wide) {
+    // a lane per sequence, every warp for itself: no barrier (a step's first 3.5 us went by in the
+    // general form's)
+    int r0, n = 0, kv = 0, k0;
+    bool bad = false;
+    const bool has = lane < p.nb && seq_of(p, lane, &r0, &n, &kv, &bad);
+    if (bad && blockIdx.x == 0 && warp == 0 && p.status) atomicOr(p.status, DFLASH_DEV_BAD_CTX);
+    const int tiles = has ? (n + h.TT - 1) / h.TT : 0;
+    const long long mine = tile_slots(p, h, n, kv, 0, tiles, 1) * p.nkv;
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    const long long W = __shfl_sync(0xffffffffu, inc, 31);
+    const int G = (int)min((long long)gridDim.x, W), b = blockIdx.x;
+    Walk w;
+    w.lo = b < G ? (long long)b * W / G : 0;
+    w.hi = b < G ? (long long)(b + 1) * W / G : 0;
+    w.s = p.nb, w.tile = w.g = 0, w.pu = w.hi;
+    *W_out = W;
+    if (w.lo >= w.hi) return w;
+    const int s0 = __ffs(__ballot_sync(0xffffffffu, inc > w.lo)) - 1;  // the sequence that holds slot lo
+    long long at = __shfl_sync(0xffffffffu, inc - mine, s0);
+    const int n0 = __shfl_sync(0xffffffffu, n, s0), kv0 = __shfl_sync(0xffffffffu, kv, s0);
+    w.s = s0;
+    for (;;) {  // its tile: at most a few
+      const int slots = unit_chunks(p, h, n0, kv0, w.tile, &k0) + kUnitCost;
+      if (w.lo < at + (long long)slots * p.nkv) {
+        w.g = (int)((w.lo - at) / slots);
+        w.pu = at + (long long)w.g * slots;
+        return w;
+      }
+      at += (long long)slots * p.nkv;
+      ++w.tile;
+    }
+  }
   // slots of each sequence (all kv heads): a thread per sequence, or a warp where chunks are long
   for (int s = wide ? warp : t; s < p.nb; s += wide ? kWarps : kThreads) {
     int r0, n, kv;
@@ -345,6 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const Shape h = shape_of(p, NT);
 
+  pdl_wait();  // everything read here may come from the kernel before
   if (t == 0) wk.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
   long long W;
   const Walk walk = plan(p, h, c, reinterpret_cast<long long*>(sK), wk.long_chunks, &W);
@@ -797,8 +836,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              __stcg(part_at(wk, slot, prow, (d_lo + d + e) >> 2, NT * 128, HD), make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
+            for (int e = 0; e < 32; e += 8) {
+              uint32_t w[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(v[e + k]);
+              put32(part_row(wk, slot, prow, NT * 128, HD) + d_lo + d + e, w, true);
+            }
           }
         }
         if (valid && (NT == 2 || x == 0)) {
@@ -831,9 +874,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
 }
 
 // Merges the partials of the unit that starts in CTA b = blockIdx.x and ends in a later one, in
-// key order.  Threads: dims 4 db .. of rows in turn; blockIdx.y strides over the row groups.
+// key order.  A warp has a row (lane: HD / 32 dims); of a unit cut into more than 8 parts (few
+// sequences, long contexts) the block's 8 warps share a row's parts and meet in shared memory, so
+// that no warp waits for one batch of loads after another.
 template <int HD, int NT>
-__global__ void __launch_bounds__(128) attend_combine_kernel(const AttendParams p, const AttendWork wk) {
+__global__ void __launch_bounds__(256) attend_combine_kernel(const AttendParams p, const AttendWork wk) {
+  constexpr int kD = HD / 32;  // dims of a lane: 4 or 2
+  __shared__ float s_o[8][HD];
+  __shared__ float2 s_ml[8];
+  pdl_trigger();
   pdl_wait();
   const int4 meta = wk.meta[blockIdx.x];
   const int nsplit = meta.x;
@@ -843,43 +892,86 @@ __global__ void __launch_bounds__(128) attend_combine_kernel(const AttendParams 
   bool bad;
   seq_of(p, meta.y, &r0, &n, &kv, &bad);
   const int t0 = meta.z * h.TT, g = meta.w;
-  constexpr int kDb = HD / 4, kR = 128 / kDb;  // dim blocks of a row, rows of a block
-  const int t = threadIdx.x, rr = t % kR, db = t / kR;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tiles = min(NT, (n - t0 + h.T - 1) / h.T);  // query tiles with tokens
-  for (int row = blockIdx.y * kR + rr; row < tiles * 128; row += gridDim.y * kR) {
+  const bool shared = nsplit > 8;
+  const int rows = shared ? 1 : 8;                      // of the block at a time
+  for (int base = blockIdx.y * rows; base < tiles * 128; base += gridDim.y * rows) {
+    const int row = shared ? base : base + warp;
     const int x = row >> 7, tok = (row & 127) / h.group, head = (row & 127) - tok * h.group;
     const int tk = t0 + x * h.T + tok;
-    if (tok >= h.T || tk >= n) continue;
-    float M = -INFINITY, L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int q0 = 0; q0 < nsplit; q0 += 8) {
+    const bool valid = tok < h.T && tk < n;
+    if (!valid) continue;  // (shared: the whole block has the same row)
+    float M = -INFINITY, L = 0.f, acc[kD];
+#pragma unroll
+    for (int d = 0; d < kD; ++d) acc[d] = 0.f;
+    for (int q0 = shared ? warp : 0; q0 < nsplit; q0 += shared ? 64 : 8) {
       float2 ml[8];
-      float4 o[8];
+      float o[8][kD];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const int q = q0 + u, slot = 2 * (blockIdx.x + q) + (q == 0 ? 1 : 0);
-        const bool v = q < nsplit;
-        ml[u] = v ? __ldcg(wk.ml + (int64_t)slot * (NT * 128) + row) : make_float2(-INFINITY, 0.f);
-        o[u] = v ? __ldcg(part_at(wk, slot, row, db, NT * 128, HD)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const int q = q0 + u * (shared ? 8 : 1), slot = 2 * (blockIdx.x + q) + (q == 0 ? 1 : 0);
+        ml[u] = make_float2(-INFINITY, 0.f);
+        if (q < nsplit) {
+          ml[u] = __ldcg(wk.ml + (int64_t)slot * (NT * 128) + row);
+          const float* src = part_row(wk, slot, row, NT * 128, HD) + lane * kD;
+          if (kD == 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+            o[u][0] = v.x, o[u][1] = v.y, o[u][kD - 2] = v.z, o[u][kD - 1] = v.w;
+          } else {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+            o[u][0] = v.x, o[u][1] = v.y;
+          }
+        } else {
+#pragma unroll
+          for (int d = 0; d < kD; ++d) o[u][d] = 0.f;
+        }
       }
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const float Mn = fmaxf(M, ml[u].x), base = Mn == -INFINITY ? 0.f : Mn;
-        const float f = exp2f(M - base), fu = exp2f(ml[u].x - base);
-        acc.x = acc.x * f + o[u].x * fu;
-        acc.y = acc.y * f + o[u].y * fu;
-        acc.z = acc.z * f + o[u].z * fu;
-        acc.w = acc.w * f + o[u].w * fu;
+        const float Mn = fmaxf(M, ml[u].x), z = Mn == -INFINITY ? 0.f : Mn;
+        const float f = exp2f(M - z), fu = exp2f(ml[u].x - z);
+#pragma unroll
+        for (int d = 0; d < kD; ++d) acc[d] = acc[d] * f + o[u][d] * fu;
         L = L * f + ml[u].y * fu;
         M = Mn;
       }
     }
-    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-    const int64_t gr = r0 + tk;
-    const int gh = g * h.group + head;
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + gr * p.out_stride + (int64_t)gh * HD + db * 4;
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-    if (p.lse && db == 0) p.lse[gr * p.nh + gh] = lse_of(M, L);
+    if (shared) {
+#pragma unroll
+      for (int d = 0; d < kD; ++d) s_o[warp][lane * kD + d] = acc[d];
+      if (lane == 0) s_ml[warp] = make_float2(M, L);
+      __syncthreads();
+      if (warp == 0) {
+        float m2[8], z = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) z = fmaxf(z, s_ml[w].x);
+        M = z;
+        z = z == -INFINITY ? 0.f : z;
+        L = 0.f;
+#pragma unroll
+        for (int d = 0; d < kD; ++d) acc[d] = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          m2[w] = exp2f(s_ml[w].x - z);
+          L += s_ml[w].y * m2[w];
+#pragma unroll
+          for (int d = 0; d < kD; ++d) acc[d] += s_o[w][lane * kD + d] * m2[w];
+        }
+      }
+    }
+    if (!shared || warp == 0) {
+      const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+      const int64_t gr = r0 + tk;
+      const int gh = g * h.group + head;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + gr * p.out_stride + (int64_t)gh * HD + lane * kD;
+      if (kD == 4)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[kD - 2] * inv, acc[kD - 1] * inv));
+      else
+        *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
+      if (p.lse && lane == 0) p.lse[gr * p.nh + gh] = lse_of(M, L);
+    }
+    if (shared) __syncthreads();
   }
 }
 
@@ -887,17 +979,20 @@ template <int HD, int NT>
 cudaError_t launch(const AttendParams& p, const AttendWork& w, int sms, cudaStream_t st) {
   static std::atomic<unsigned long long> attr{0};
   if (cudaError_t e = smem_attr_once(attend_tc_kernel<HD, NT>, Cfg<HD, NT>::kSmem, attr); e != cudaSuccess) return e;
-  attend_tc_kernel<HD, NT><<<sms, kThreads, Cfg<HD, NT>::kSmem, st>>>(p, w);
-  if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
   cudaLaunchAttribute a[1];
   a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   a[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t c = {};
-  c.gridDim = dim3(sms, 8);
-  c.blockDim = dim3(128);
+  c.gridDim = dim3(sms);
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = Cfg<HD, NT>::kSmem;
   c.stream = st;
   c.attrs = a;
   c.numAttrs = 1;
+  if (cudaError_t e = cudaLaunchKernelEx(&c, attend_tc_kernel<HD, NT>, p, w); e != cudaSuccess) return e;
+  c.gridDim = dim3(sms, NT * 16);  // a unit's rows in one round
+  c.blockDim = dim3(256);
+  c.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&c, attend_combine_kernel<HD, NT>, p, w);
 }
 
@@ -910,7 +1005,7 @@ int64_t attend_tc_workspace(int head_dim, int sms) {
 
 cudaError_t launch_attend_tc(const AttendParams& p, int head_dim, int max_new, void* workspace, int sms, cudaStream_t st) {
   AttendWork w;
-  w.o = static_cast<float4*>(workspace);
+  w.o = static_cast<float*>(workspace);
   w.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + (int64_t)sms * 2 * 256 * head_dim * 4);
   w.meta = reinterpret_cast<int4*>(w.ml + (int64_t)sms * 2 * 256);
   const int T = 128 / (p.nh / p.nkv);

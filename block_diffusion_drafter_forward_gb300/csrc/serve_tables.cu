@@ -2,11 +2,13 @@
 //
 // extend_tables: two prefix sums over the sequences (pages needed, rows added), then one thread
 // per row finds its sequence by binary search.  Bound by latency: a step of 1024 rows moves 14 KB.
-// The scan is repeated by every CTA of the one cluster that runs it, so no CTA waits for another
-// before it maps its rows; the cluster barrier at the end lets the lengths and the stack position
-// be written in place of the inputs.
+// The scan is repeated by every CTA, so none waits for another before it maps its rows.  Lengths
+// or a stack position written in place of the inputs have to wait until every CTA has read them:
+// then the CTAs are one cluster (8 at most) with a barrier before the first CTA writes; else the
+// rows spread over as many CTAs as they fill (134 Ki rows: X against Y us in a cluster of 8).
 #include <cooperative_groups.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "launch_util.cuh"
@@ -25,6 +27,7 @@ struct TablesParams {
   int32_t *page_tables, *free_end, *kv_lens, *row_starts, *row_seq, *row_index, *slots;
   uint32_t* status;
   int nb, mpps, n_free, max_rows;
+  bool in_place;
 };
 
 __global__ void __launch_bounds__(kTabThreads) extend_tables_kernel(const TablesParams p) {
@@ -127,7 +130,7 @@ __global__ void __launch_bounds__(kTabThreads) extend_tables_kernel(const Tables
     p.row_index[i] = idx;
     p.slots[i] = slot;
   }
-  if (nctas > 1) cg::this_cluster().sync();  // every CTA has read the inputs
+  if (p.in_place) cg::this_cluster().sync();  // every CTA has read the inputs
   else __syncthreads();
   if (rank == 0) {
     for (int s = t; s <= p.nb; s += kTabThreads) {
@@ -146,18 +149,20 @@ struct AppendParams {
   int64_t page_bytes;
   const int32_t* slots;
   uint32_t* status;
-  int n, nkv, num_pages;
+  int n, nkv, num_pages, heads;
   bool wide;  // tiles start on 32 bytes
 };
 
-// A block takes kRows consecutive rows and kHeads heads; a warp one entry of one head at a time.
+// A block takes kRows consecutive rows and one head, or four where there are rows enough to fill
+// the SMs with fewer blocks (1024 rows of 4 heads: 8.2 us by fours, X by ones; 16.7 Ki rows of 8
+// heads: 28 us by fours, Y by ones); a warp one entry of one head at a time.
 // An entry is a run of eight rows whose slots fill one half page in order (the usual case: a
 // step's rows of a sequence follow one another), or a single row.  In the tile eight keys of a
 // half page lie side by side, so a run is written in whole sectors: K by lanes of 8 rows x 4
 // pieces (64 contiguous bytes read per row, 128 written), V transposed in registers (a lane
 // reads two dims of the eight rows and writes both dims' eight keys).  A single row writes V
 // element by element.  Bound by HBM, both ways once.
-constexpr int kRows = 16, kHeads = 4;
+constexpr int kRows = 16;
 
 template <typename T>
 __device__ __forceinline__ void copy16(T* d, const T* s) {
@@ -212,10 +217,10 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
     if (t == 0) s_n = __popc(m);
   }
   __syncthreads();
-  const int h = blockIdx.y * kHeads + (warp & (kHeads - 1));
+  const int h = blockIdx.y * p.heads + warp % p.heads;
   if (h >= p.nkv) return;
   constexpr int kPer = 16 / sizeof(T);  // dims of a 16-byte piece
-  for (int e = warp / kHeads; e < s_n; e += 8 / kHeads) {
+  for (int e = warp / p.heads; e < s_n; e += 8 / p.heads) {
     const int i = s_entry[e] & 63, slot = s_slot[7 + i];
     const int64_t row = r0 + i;
     T* tile = reinterpret_cast<T*>(p.pool + (slot / kPage) * p.page_bytes) + (int64_t)h * 2 * kPage * HD;
@@ -268,16 +273,21 @@ extern "C" int dflash_extend_tables(const int32_t* ctx_lens, const int32_t* new_
   if (nb > kTabMaxSeqs) return call_error(DFLASH_ECAPACITY, "extend_tables: nb above 16384");
   if (max_rows > 1 << 30) return call_error(DFLASH_ECAPACITY, "extend_tables: max_rows above 2^30");
   TablesParams p{ctx_lens, new_rows, free_pages, free_begin, page_tables, free_end, kv_lens, row_starts,
-                 row_seq,  row_index, slots, status, nb, max_pages_per_seq, n_free, max_rows};
+                 row_seq,  row_index, slots, status, nb, max_pages_per_seq, n_free, max_rows, false};
   const int smem = (3 * nb + 1) * (int)sizeof(int32_t);
   static std::atomic<unsigned long long> attr{0};
   if (cudaError_t e = smem_attr_once(extend_tables_kernel, (3 * kTabMaxSeqs + 1) * (int)sizeof(int32_t), attr); e != cudaSuccess)
     return call_error(DFLASH_ECUDA, "extend_tables", e);
   cudaLaunchConfig_t c = {};
   cudaLaunchAttribute a[1];
-  const int ctas = max_rows > 4096 ? 8 : 1;
+  auto overlap = [](const int32_t* a, int64_t n, const int32_t* b, int64_t m) { return a < b + m && b < a + n; };
+  p.in_place = free_end == free_begin || overlap(kv_lens, nb, ctx_lens, nb);
+  int sms = 0;
+  if (cudaError_t e = sm_count(&sms); e != cudaSuccess) return call_error(DFLASH_ECUDA, "extend_tables", e);
+  const int fill = std::max(1, (max_rows + kTabThreads - 1) / kTabThreads);
+  const int ctas = p.in_place ? (max_rows > 4096 ? 8 : 1) : std::min(fill, sms);
   a[0].id = cudaLaunchAttributeClusterDimension;
-  a[0].val.clusterDim.x = ctas;
+  a[0].val.clusterDim.x = p.in_place ? ctas : 1;
   a[0].val.clusterDim.y = a[0].val.clusterDim.z = 1;
   c.gridDim = dim3(ctas);
   c.blockDim = dim3(kTabThreads);
@@ -300,9 +310,13 @@ extern "C" int dflash_append_kv(const dflash_kv_pages* kv, const void* k, int64_
   if (k_stride < row || v_stride < row || (k_stride * es) % 16 || (v_stride * es) % 16 || !aligned16(k) || !aligned16(v))
     return call_error(DFLASH_EINVAL, "append_kv: rows below n_kv_heads * head_dim, or k, v or a stride not whole 16 bytes");
   AppendParams p{static_cast<const uint8_t*>(k), static_cast<const uint8_t*>(v), k_stride * es, v_stride * es,
-                 static_cast<uint8_t*>(kv->pool), kv->page_stride * es, slots, kv->status, n, kv->n_kv_heads, kv->num_pages,
+                 static_cast<uint8_t*>(kv->pool), kv->page_stride * es, slots, kv->status, n, kv->n_kv_heads, kv->num_pages, 4,
                  reinterpret_cast<uintptr_t>(kv->pool) % 32 == 0 && (kv->page_stride * es) % 32 == 0};
-  const dim3 grid((unsigned)((n + (int64_t)kRows - 1) / kRows), (unsigned)((kv->n_kv_heads + kHeads - 1) / kHeads));
+  int sms = 0;
+  if (cudaError_t e = sm_count(&sms); e != cudaSuccess) return call_error(DFLASH_ECUDA, "append_kv", e);
+  const int64_t groups = (n + (int64_t)kRows - 1) / kRows;
+  p.heads = groups * ((kv->n_kv_heads + 3) / 4) < 4 * sms ? 1 : 4;
+  const dim3 grid((unsigned)groups, (unsigned)((kv->n_kv_heads + p.heads - 1) / p.heads));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool f32 = kv->dtype == DFLASH_F32, w = kv->head_dim == 128;
   auto kern = f32 ? (w ? append_kernel<float, 128> : append_kernel<float, 64>)
