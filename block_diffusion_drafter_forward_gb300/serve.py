@@ -174,10 +174,15 @@ def extend_tables(ctx_lens: torch.Tensor, new_rows: torch.Tensor, page_tables: t
     page_tables [nb, max_pages_per_seq], extended in place; free_pages [n] a stack of page ids taken
     from position free_begin [1] on.  Sequences are served in order while pages and max_rows last.
     `out`: a RowPlan to write into; its kv_lens may be ctx_lens and its free_end free_begin."""
-    dev = _first(ctx_lens, "ctx_lens", 1).device
-    nb, max_rows = ctx_lens.shape[0], int(max_rows)
-    mpps = _first(page_tables, "page_tables", 2).shape[1]
-    n_free = _first(free_pages, "free_pages", 1).shape[0]
+    try:  # sizes first; _addresses holds every tensor to them
+        dev, nb = ctx_lens.device, ctx_lens.shape[0]
+        mpps, n_free = page_tables.shape[1], free_pages.shape[0]
+        ok = dev.type == "cuda"
+    except (AttributeError, IndexError):
+        ok = False
+    if not ok:
+        _first(ctx_lens, "ctx_lens", 1), _first(page_tables, "page_tables", 2), _first(free_pages, "free_pages", 1)
+    max_rows = int(max_rows)
     if max_rows < 0:
         raise ValueError("max_rows must be >= 0")
     one, seqs, rows = (1,), (nb,), (max_rows,)
@@ -206,22 +211,23 @@ class PagedKV:
     (`Drafter.kv_pages`), is a view of it."""
 
     def __init__(self, pool: torch.Tensor):
-        _first(pool, "pool", 4, (_BF16, _F32))
-        P, nkv, two, tile = pool.shape
-        if two != 2 or tile not in (1024, 2048):
+        try:
+            (P, nkv, two, tile), st = pool.shape, pool.stride()
+            dtype, dev = pool.dtype, pool.device
+            ok = dev.type == "cuda" and (dtype is _BF16 or dtype is _F32)
+        except (AttributeError, ValueError):
+            ok = False
+        if not ok:
+            _first(pool, "pool", 4, (_BF16, _F32))
+        if two != 2 or (tile != 1024 and tile != 2048):
             raise ValueError(f"pool: expected shape [pages, kv_heads, 2, 16 * 64 or 16 * 128], got {tuple(pool.shape)}")
-        st = pool.stride()
         if st[3] != 1 or st[2] != tile or (nkv > 1 and st[1] != 2 * tile):
             raise ValueError("pool: heads and tiles of a page must be contiguous")
         self.pool = pool
         self.head_dim = tile // 16
-        self._stride = st[0] if P > 1 else 2 * nkv * tile
-        k = L.dflash_kv_pages()
-        k.pool, k.page_stride = pool.data_ptr(), self._stride
-        k.status = _status_word(pool.device).data_ptr()
-        k.dtype = L.DFLASH_BF16 if pool.dtype is _BF16 else L.DFLASH_F32
-        k.n_kv_heads, k.head_dim, k.num_pages = nkv, self.head_dim, P
-        self._c = k
+        self._c = L.dflash_kv_pages(pool.data_ptr(), st[0] if P > 1 else 2 * nkv * tile, _status_word(dev).data_ptr(),
+                                    L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32, nkv, self.head_dim, P)
+        self._workspace = None  # bytes that a call of attend needs
 
     @classmethod
     def empty(cls, num_pages: int, n_kv_heads: int, head_dim: int, dtype: torch.dtype = _BF16, device="cuda") -> "PagedKV":
@@ -233,7 +239,11 @@ class PagedKV:
         of the pages.  Returns the pages' tensor."""
         pool = self.pool
         dev = pool.device
-        n = _first(slots, "slots", 1).shape[0]
+        try:
+            n = slots.shape[0]
+        except (AttributeError, IndexError):
+            _first(slots, "slots", 1)
+            raise
         a_s, = _addresses(dev, (slots, "slots", _I32, (n,)))
         shape = (n, pool.shape[1], self.head_dim)
         a_k, ks = _rows_of(k, "k", pool.dtype, shape, dev)
@@ -253,10 +263,13 @@ class PagedKV:
         pool = self.pool
         dev = pool.device
         hd = self.head_dim
-        n, nh = _first(q, "q", 3, (pool.dtype,)).shape[:2]
+        try:
+            (n, nh, _), (nb, mpps) = q.shape, page_tables.shape
+        except (AttributeError, ValueError):
+            _first(q, "q", 3, (pool.dtype,)), _first(page_tables, "page_tables", 2)
+            raise
         shape = (n, nh, hd)
         a_q, qs = _rows_of(q, "q", pool.dtype, shape, dev)
-        nb, mpps = _first(page_tables, "page_tables", 2).shape
         a_pt, a_kv, a_rs = _addresses(dev, (page_tables, "page_tables", _I32, (nb, mpps)), (kv_lens, "kv_lens", _I32, (nb,)),
                                       (row_starts, "row_starts", _I32, (nb + 1,)))
         a_lse = 0 if lse is None else _addresses(dev, (lse, "lse", _F32, (n, nh)))[0]
@@ -264,7 +277,9 @@ class PagedKV:
             if out is None:
                 out = torch.zeros(shape, dtype=pool.dtype, device=dev)
             a_out, os_ = _rows_of(out, "out", pool.dtype, shape, dev)
-            need = L.dflash_attend_workspace(self._c)
+            need = self._workspace
+            if need is None:
+                need = self._workspace = L.dflash_attend_workspace(self._c)
             ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
             L.dflash_attend(self._c, a_q, qs, a_pt, mpps, a_kv, a_rs, nb, n, int(max_new), nh,
                             1.0 / math.sqrt(hd) if scale is None else float(scale), int(window), 1 if causal else 0,
@@ -279,21 +294,27 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Te
     """One token per row of logits [rows, vocab] (bfloat16 or float32, any stride between rows) from
     uniform numbers u [rows] float32.  temperature, top_p, min_p float32 and top_k int32 [rows], each
     optional.  Returns tokens [rows] int32, or (tokens, probs) when `probs` [rows] float32 is given."""
-    dev = _first(logits, "logits", 2, (_BF16, _F32)).device
-    rows, V = logits.shape
-    st0, st1 = logits.stride()
+    try:
+        dev, dtype = logits.device, logits.dtype
+        (rows, V), (st0, st1) = logits.shape, logits.stride()
+        ok = dev.type == "cuda" and (dtype is _BF16 or dtype is _F32)
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        _first(logits, "logits", 2, (_BF16, _F32))
     if (V > 1 and st1 != 1) or (rows > 1 and st0 < V):
         raise ValueError(f"logits: a row must be contiguous and rows must not overlap, got strides {(st0, st1)}")
     col = (rows,)
-    a_u, = _addresses(dev, (u, "u", _F32, col))
-    a_temp, a_k, a_p, a_min, a_probs = [
-        0 if w[0] is None else _addresses(dev, w)[0]
-        for w in ((temperature, "temperature", _F32, col), (top_k, "top_k", _I32, col), (top_p, "top_p", _F32, col),
-                  (min_p, "min_p", _F32, col), (probs, "probs", _F32, col))]
+    given = [w for w in ((u, "u", _F32, col), (temperature, "temperature", _F32, col), (top_k, "top_k", _I32, col),
+                         (top_p, "top_p", _F32, col), (min_p, "min_p", _F32, col), (probs, "probs", _F32, col),
+                         (tokens, "tokens", _I32, col)) if w[0] is not None or w[1] == "u"]
+    at = dict(zip((w[1] for w in given), _addresses(dev, *given)))
     with _on(dev, stream) as st:
         if tokens is None:
             tokens = torch.empty(rows, dtype=_I32, device=dev)
-        a_t, = _addresses(dev, (tokens, "tokens", _I32, col))
-        L.dflash_sample(logits.data_ptr(), st0 if rows > 1 else V, L.DFLASH_BF16 if logits.dtype is _BF16 else L.DFLASH_F32,
-                        rows, V, a_u, a_temp, a_k, a_p, a_min, a_t, a_probs, st)
+            at["tokens"] = tokens.data_ptr()
+        get = at.get
+        L.dflash_sample(logits.data_ptr(), st0 if rows > 1 else V, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32, rows, V,
+                        at["u"], get("temperature", 0), get("top_k", 0), get("top_p", 0), get("min_p", 0), at["tokens"],
+                        get("probs", 0), st)
     return tokens if probs is None else (tokens, probs)
