@@ -435,6 +435,20 @@ bool make_tmap_bf16(CUtensorMap* map, const void* base, int64_t rows, int64_t co
   return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_heads_bf16(CUtensorMap* map, const void* base, int64_t rows, int heads, int head_dim, int64_t ld_elems,
+                          int box_heads, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)heads, (cuuint64_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)(head_dim * 2), (cuuint64_t)(ld_elems * 2)};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 int pick_tn(int M) {
   if (M <= 16) return 16;
   if (M <= 32) return 32;

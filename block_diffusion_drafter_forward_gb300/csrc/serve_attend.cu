@@ -117,6 +117,8 @@ extern "C" int dflash_attend(const dflash_kv_pages* kv, const void* q, int64_t q
   if (!(scale > 0.f) || !(scale <= FLT_MAX)) return call_error(DFLASH_EINVAL, "attend: scale must be positive and finite");
   if (n_rows == 0) return DFLASH_OK;
   if (!q || !out || !page_tables || !kv_lens || !row_starts) return call_error(DFLASH_EINVAL, "attend: null pointer");
+  if (kv->dtype == DFLASH_BF16 && q_stride % kv->head_dim)
+    return call_error(DFLASH_EINVAL, "attend: q_stride must be a multiple of head_dim (bf16)");
   const int64_t need = dflash_attend_workspace(kv);
   if (need < 0) return (int)need;
   if (workspace_bytes < need || (need > 0 && (!workspace || !aligned16(workspace))))

@@ -30,6 +30,7 @@
 
 #include <atomic>
 
+#include "gemm_tc.cuh"
 #include "launch_util.cuh"
 #include "serve_attend.cuh"
 #include "tc_common.cuh"
@@ -61,8 +62,8 @@ struct Cfg {
   static constexpr int kQ = 128 * HD * 2;              // a query tile
   static constexpr int kSlot = kPages * kTile;         // a chunk's K (or V)
   static constexpr int kNK = HD == 128 ? 3 : 6;        // K and V slots in flight
-  static constexpr int kNV = HD == 128 ? (NT == 2 ? 2 : 3) : 6;
-  static constexpr int kSmem = NT * kQ + (kNK + kNV) * kSlot + kCtl + 128;
+  static constexpr int kNV = HD == 128 ? 2 : 6;
+  static constexpr int kSmem = 2 * kQ + (kNK + kNV) * kSlot + kCtl;  // (queries: two tiles, or two segments' tile)
 };
 
 struct Seg {
@@ -124,7 +125,7 @@ struct Walk {
 
 struct Ctl {
   uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6], v_raw[6];
-  uint64_t s_full[2], p_half[2], p_full[2], o_done[2], o_free[2], q_full[2], q_empty;
+  uint64_t s_full[2], p_half[2], p_full[2], o_done[2], o_free[2], q_full[2];
   uint32_t tmem_slot;
   int flags[2];
   int s0, tile0, found;
@@ -371,12 +372,11 @@ struct It {
 };
 
 template <int HD, int NT>
-__global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendParams p, const AttendWork wk) {
+__global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendParams p, const AttendWork wk, const __grid_constant__ CUtensorMap q_map) {
   using C = Cfg<HD, NT>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  extern __shared__ __align__(1024) uint8_t smem[];  // (the queries' swizzle counts from 1 KB boundaries)
   uint8_t* sQ = smem;
-  uint8_t* sK = sQ + NT * C::kQ;
+  uint8_t* sK = sQ + 2 * C::kQ;
   uint8_t* sV = sK + C::kNK * C::kSlot;
   Ctl& c = *reinterpret_cast<Ctl*>(sV + C::kNV * C::kSlot);
   volatile int* flags = c.flags;
@@ -405,12 +405,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
       mbar_init(&c.p_full[i], 128);
       mbar_init(&c.o_done[i], 1);
       mbar_init(&c.o_free[i], NT == 2 ? 128 : 256);
-      mbar_init(&c.q_full[i], 128);
+      mbar_init(&c.q_full[i], 1);
     }
-    mbar_init(&c.q_empty, 1);
     flags[0] = 0;
     fence_barrier_init();
   }
+  // rows that no query fills stay finite
+  if (h.group * h.T < 128)
+    for (int i = t; i < 2 * C::kQ / 16; i += kThreads) reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();  // the plan's scratch is overwritten by copies
   if (warp == 0) tmem_alloc(&c.tmem_slot, 512);
   tc_fence_before();
@@ -418,6 +420,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
   tc_fence_after();
   const uint32_t tmem = c.tmem_slot;
   pdl_trigger();
+  // Queries of a segment into tile b (its second query tile's: two tiles, b = 1) by TMA: rows of 64
+  // dims in the 128-byte swizzle, (head, token) in the tile's row order.  One thread.  (Copied by the
+  // softmax threads, 16 bytes each, they queued for thousands of cycles behind the pages.)
+  auto load_q = [&](const Seg& q, int b) {
+    mbar_arrive_expect_tx(&c.q_full[b], h.group * h.T * HD * 2);
+    for (int d = 0; d < HD / 64; ++d)
+      tma_load_3d(sQ + b * C::kQ + d * (128 * 128), &q_map, &c.q_full[b], d * 64, q.g * h.group, q.r0 + q.t0 + (NT == 2 ? b * h.T : 0));
+  };
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
@@ -510,11 +520,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
       // ---- MMA issue
       constexpr uint32_t id_s = idesc_bf16(128, kKeys), id_o = idesc_bf16(128, HD);
       // operand descriptors of the first tiles; the others are further on (16-byte units)
-      const uint64_t dQ = desc_noswz(sQ, 128, HD * 16), dK = desc_noswz(sK, 128, HD * 16), dV = desc_noswz(sV, 128, 256);
-      auto issue_s = [&](int x, int kb) {
-        const uint64_t q = dQ + (uint64_t)((NT == 2 ? x : 0) * (C::kQ / 16)), k = dK + (uint64_t)(kb * (C::kSlot / 16));
+      const uint64_t dQ = desc_sw128(sQ), dK = desc_noswz(sK, 128, HD * 16), dV = desc_noswz(sV, 128, 256);
+      auto issue_s = [&](int x, int qb, int kb) {  // queries in tile qb
+        const uint64_t q = dQ + (uint64_t)(qb * (C::kQ / 16)), k = dK + (uint64_t)(kb * (C::kSlot / 16));
 #pragma unroll
-        for (int d = 0; d < HD / 16; ++d) mma_bf16(tmem + x * 128, q + d * 16, k + d * 16, id_s, d > 0 ? 1u : 0u);
+        for (int d = 0; d < HD / 16; ++d)  // (queries: 32 bytes on in a 64-dim half of 16 KB)
+          mma_bf16(tmem + x * 128, q + (d & 3) * 2 + (d >> 2) * 1024, k + d * 16, id_s, d > 0 ? 1u : 0u);
       };
       auto issue_pv = [&](int x, int vb, int k0, int k1, bool more) {  // pages k0 .. k1 - 1: 16 keys = 8 TMEM columns of P each
         const uint64_t v = dV + (uint64_t)(vb * (C::kSlot / 16));
@@ -539,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         auto s_of = [&](int kc) {  // (its K has been waited for)
           const int kb = kc % C::kNK;
           tc_fence_after();
-          if (!flags[0]) issue_s(x, kb);
+          if (!flags[0]) issue_s(x, x, kb);
           mma_commit(&c.s_full[x]);
           mma_commit(&c.k_empty[kb]);
         };
@@ -584,7 +595,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         its[0].start(p, h, walk, 0);
         its[1].start(p, h, walk, 1);
         long long idle = 0;
-        int s_out = 0;  // S of the segment issued so far
         // A wait by parity is exact only while the phase before the awaited one is known complete, so
         // no stream may run ahead of the other by a ring: S and P V go out in chunk order over both.
         int s_next = 0, pv_next = 0;  // chunks whose S / P V is out
@@ -616,15 +626,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
             if (a.valid && !pv[x]) {
               const int kc = a.kc0 + a.j, kb = kc % C::kNK;
               if (give_up || (kc == s_next && mbar_test_wait(&c.k_full[kb], (kc / C::kNK) & 1) &&
-                              (!a.first(x) || mbar_test_wait(&c.q_full[0], a.seg & 1)))) {
+                              (!a.first(x) || mbar_test_wait(&c.q_full[a.seg & 1], a.seg >> 1 & 1)))) {
                 tc_fence_after();
-                if (!give_up) issue_s(x, kb);
+                if (!give_up) issue_s(x, a.seg & 1, kb);
                 mma_commit(&c.s_full[x]);
                 mma_commit(&c.k_empty[kb]);
-                if (++s_out == a.n) {  // both streams' S read the same queries
-                  mma_commit(&c.q_empty);
-                  s_out = 0;
-                }
                 ++s_next;
                 pv[x] = true;
                 did = true;
@@ -644,40 +650,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + x * 128 + lane_off;
     const int tok = row / h.group, head = row - tok * h.group;
-    // queries of a segment's tile (16-byte pieces; a warp copies 8 rows x 64 bytes at a time: whole
-    // sectors of q, conflict-free rows of the operand layout)
-    auto load_q = [&](const Seg& q) {
-      const int tb = q.t0 + (NT == 2 ? x * h.T : 0);
-      uint8_t* dst = sQ + (NT == 2 ? x : 0) * C::kQ;
-#pragma unroll
-      for (int k = 0; k < HD / 8; ++k) {
-        const int idx = k * 4 + (warp & 3);
-        const int r = idx / (HD / 32) * 8 + (lane & 7), d8 = idx % (HD / 32) * 4 + (lane >> 3);
-        const int tk = r / h.group, hd = r - tk * h.group;
-        uint8_t* d = dst + ((r >> 3) * (HD / 8) + d8) * 128 + (r & 7) * 16;
-        if (tk < h.T && tb + tk < q.n)
-          cp_async16(d, static_cast<const __nv_bfloat16*>(p.q) + (int64_t)(q.r0 + tb + tk) * p.q_stride +
-                            ((int64_t)q.g * h.group + hd) * HD + d8 * 8);
-        else
-          *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);
-      }
-    };
-    auto q_ready = [&] {
-      cp_async_wait_all();
-      fence_proxy_async_smem();
-      mbar_arrive(&c.q_full[NT == 2 ? x : 0]);
-    };
-    // one tile: the stream that does a segment's last chunk loads the next one's queries
-    auto loads_after = [&](const Seg& q) { return NT == 2 || ((q.c_hi - q.c_lo - 1) & 1) == x; };
-
+    const bool loads = (t & 127) == 0 && (NT == 2 || x == 0);  // (one tile: stream 0's, a segment ahead)
     Walk w = walk;
     Seg q, nq;
     bool have = w.next(p, h, q);
     while (NT == 2 && have && !It<NT>::active(h, q, x)) have = w.next(p, h, q);
-    if (have && (NT == 2 || x == 0)) {
-      load_q(q);
-      q_ready();
-    }
+    if (have && loads) load_q(q, x);
     int it = 0, seg = 0;  // chunks and segments done by this stream
     while (have) {
       bool more = w.next(p, h, nq);
@@ -696,11 +674,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
       for (int j = NT == 2 ? 0 : x; j < n; j += NT == 2 ? 1 : 2, ++it, ++done) {
         if (!wait_ab(&c.s_full[x], it & 1, flags)) flags[0] = 1;
         tc_fence_after();
-        const bool load_next = j == n - 1 && more && loads_after(q);
-        if (load_next) {  // once every S that reads this segment's queries is done
-          if (NT == 1 && !wait_ab(&c.q_empty, seg & 1, flags)) flags[0] = 1;
-          load_q(nq);
-        }
+        // the next queries: two tiles, into the same tile once this segment's last S is done; one,
+        // into the other tile once this segment's first is (so every S of the segment before is)
+        if (loads && more && j == (NT == 2 ? n - 1 : 0)) load_q(nq, NT == 2 ? x : (seg + 1) & 1);
         if (warp_valid) {
           const int kb = q.k0 + (q.c_lo + j) * kKeys;
           float a[64], b[64];
@@ -774,7 +750,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         tc_fence_before();
         if (NT == 2 && !warp_valid) mbar_arrive(&c.p_half[x]);
         mbar_arrive(&c.p_full[x]);
-        if (load_next) q_ready();
       }
       // ---- the segment's rows
       const bool whole = q.c_lo == 0 && q.c_hi == q.nch;
@@ -989,7 +964,10 @@ cudaError_t launch(const AttendParams& p, const AttendWork& w, int sms, cudaStre
   c.stream = st;
   c.attrs = a;
   c.numAttrs = 1;
-  if (cudaError_t e = cudaLaunchKernelEx(&c, attend_tc_kernel<HD, NT>, p, w); e != cudaSuccess) return e;
+  CUtensorMap q_map;
+  const int group = p.nh / p.nkv;
+  if (!make_tmap_heads_bf16(&q_map, p.q, p.n_rows, p.nh, HD, p.q_stride, group, 128 / group)) return cudaErrorInvalidValue;
+  if (cudaError_t e = cudaLaunchKernelEx(&c, attend_tc_kernel<HD, NT>, p, w, q_map); e != cudaSuccess) return e;
   c.gridDim = dim3(sms, NT * 16);  // a unit's rows in one round
   c.blockDim = dim3(256);
   c.dynamicSmemBytes = 0;

@@ -375,7 +375,7 @@ int dflash_append_kv(const dflash_kv_pages* kv, const void* k, int64_t k_stride,
  * (p - j < window or window == 0):
  *   out = sum_j softmax_j(scale q . k_j) v_j,   lse = ln sum_j exp(scale q . k_j)   (fp32)
  * A row that sees no key gets out = 0 and lse = -inf.  Rows of q and out are `q_stride` and
- * `out_stride` elements apart (heads contiguous, whole 16 bytes); lse [n_rows, n_q_heads] or NULL.
+ * `out_stride` elements apart (heads contiguous, whole 16 bytes; q_stride a multiple of head_dim); lse [n_rows, n_q_heads] or NULL.
  * Rows of out and lse outside every sequence's range are left as they are.  row_starts never
  * falls and stays in [0, n_rows], kv_lens in [0, 16 * max_pages_per_seq]: a sequence that breaks
  * this is skipped (its rows are left as they are) and sets DFLASH_DEV_BAD_CTX.  A page id outside

@@ -53,10 +53,12 @@ def attend_args(**kw):
 @pytest.mark.parametrize("kw", [
     dict(q=None), dict(out=None), dict(page_tables=None), dict(kv_lens=None), dict(row_starts=None), dict(nb=0), dict(n_rows=-1),
     dict(max_new=-1), dict(mpps=0), dict(mpps=1 << 27), dict(nh=7), dict(nh=0), dict(nh=258), dict(window=-1), dict(scale=0.0),
-    dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(q_stride=1020), dict(q_stride=1026),
+    dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(q_stride=1020), dict(q_stride=1026), dict(dtype=1, q_stride=1032),
     dict(out_stride=1000), dict(q=4104), dict(out=4098)])
 def test_attend_refuses(lib, kw):
-    k = pages(dtype=0)
+    kw = dict(kw)
+    bf16 = kw.pop("dtype", 0) == 1  # (refused before the workspace is asked for, which needs a device)
+    k = pages(dtype=1 if bf16 else 0)
     assert lib.dflash_attend(ctypes.byref(k), *attend_args(**kw)) == -1
     assert b"attend" in lib.dflash_last_error(None)
 
