@@ -72,9 +72,6 @@ int pick_tn(int M);
 // Split-K ways for `tiles` output tiles of `nkb` k-blocks with tn-token tiles.
 int pick_splits(int tiles, int nkb, int num_sms, int tn);
 bool make_tmap_bf16(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld_elems, int box_rows);
-// Rows of `heads` heads (head_dim elements each, contiguous): boxes of 64 dims x box_heads x box_rows.
-bool make_tmap_heads_bf16(CUtensorMap* map, const void* base, int64_t rows, int heads, int head_dim, int64_t ld_elems,
-                          int box_heads, int box_rows);
 // D = W [N, K] x X [M, K]^T with the epilogue `epi`; nsplit K-splits (1 for EPI_LMHEAD).
 // w_fp8: W holds e4m3 codes and p.row_scale the per-row scales (EPI_LMHEAD, and the layer
 // projections EPI_QKV / EPI_RESID / EPI_GATEUP of the FP8 drafter lane).

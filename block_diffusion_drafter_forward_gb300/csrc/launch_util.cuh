@@ -1,6 +1,7 @@
 // Host-side launch helpers shared by the projection GEMM and attention launchers.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -34,5 +35,10 @@ inline cudaError_t sm_count(int* sms) {
   if (e == cudaSuccess && dev >= 0 && dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
   return e;
 }
+
+// Tensor map over rows of `heads` heads (head_dim bf16 each, contiguous): boxes of 64 dims x box_heads x
+// box_rows in the 128-byte swizzle.  In gemm_tc.cu, beside the other map.
+bool make_tmap_heads_bf16(CUtensorMap* map, const void* base, int64_t rows, int heads, int head_dim, int64_t ld_elems,
+                          int box_heads, int box_rows);
 
 }  // namespace dflash

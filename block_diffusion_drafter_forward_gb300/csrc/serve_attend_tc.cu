@@ -19,18 +19,25 @@
 // read from TMEM; O stays in TMEM and is rescaled only when a row's maximum grew by more than
 // 2^8 (P <= 2^8 stays exact in range, the normalised result is the same).
 //
+// Bound and measured (GB300, 32 query heads on 4 kv heads of 128): single tokens and short blocks by
+// HBM - 16 single tokens on 16-32 Ki rows (64 heads on 8) 243 us, 6.6 TB/s; 32 blocks of 16 on
+// 0.5-8 Ki rows 67 us, 4.1 TB/s (the first pages of every SM come late, and each segment ends with
+// its output).  Prompts by the chain of one chunk - softmax 1.5-2.3 kcycles, P V and S 1.2 and their
+// hand-overs - of which two streams fill 55 % of the tensor pipe: a prompt of 8192 516 us,
+// 1.07 PFLOP/s.  Shared memory is nearly full with the MMAs' operands: S reads Q and K at 128 B a
+// cycle.
+//
 // Rounding: P is bf16 (the MMA's operand type), sums and O fp32, the normaliser sums the fp32 P.
 // Warp roles: 0-3 stream 0, 4-7 stream 1, 8 K pages, 10 V pages, 9 and 11 MMA issue.  The V warp
 // also zeroes the key rows behind a sequence's end in its last page (never-written rows may hold
 // NaN, and 0 * NaN would reach O; their scores are masked by select).  Issuing an MMA blocks its
 // thread while the tensor pipe's queue is full, so with two tiles each stream has a warp of its own
-// (one that issued for both left the pipe idle between the streams: 614 against 4xx us for a prompt
+// (one that issued for both left the pipe idle between the streams: 614 against 564 us for a prompt
 // of 8192); with one tile a single thread keeps the chunks in order over both streams.
 #include <float.h>
 
 #include <atomic>
 
-#include "gemm_tc.cuh"
 #include "launch_util.cuh"
 #include "serve_attend.cuh"
 #include "tc_common.cuh"
@@ -45,6 +52,14 @@ constexpr int kPages = kKeys / kPage;           // 8
 constexpr int kThreads = 384;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtl = 2944;                      // barriers, plan, row exchange
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
 
 // The wait of tc_common.cuh with its first poll ahead of the abort flag: most waits find their phase
 // complete, and a shared-memory read costs hundreds of cycles while MMAs saturate its bandwidth.
@@ -987,7 +1002,11 @@ cudaError_t launch_attend_tc(const AttendParams& p, int head_dim, int max_new, v
   w.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + (int64_t)sms * 2 * 256 * head_dim * 4);
   w.meta = reinterpret_cast<int4*>(w.ml + (int64_t)sms * 2 * 256);
   const int T = 128 / (p.nh / p.nkv);
-  const bool two = max_new > T;  // chunks longer than one tile: two tiles share every K/V slot
+  // Chunks longer than one tile: two tiles share every K/V slot, where there are units enough for the
+  // SMs.  Measured (32 query heads on 4, one tile / two): 32 sequences x 17 tokens on 4096 rows
+  // 109 / 93 us, x 64 199 / 163 us, 8 x 256 on 2048 113 / 102 us, 64 x 20 on 500 62 / 49 us; with few
+  // units the split finer in queries wins: 4 x 32 on 8192 36 / 60 us, 1 x 32 on 30000 49 / 54 us.
+  const bool two = max_new > T && ((int64_t)p.n_rows + T - 1) / T * p.nkv * 2 >= sms;
   w.long_chunks = max_new > 4 * (two ? 2 * T : T);
   if (head_dim == 128) return two ? launch<128, 2>(p, w, sms, st) : launch<128, 1>(p, w, sms, st);
   return two ? launch<64, 2>(p, w, sms, st) : launch<64, 1>(p, w, sms, st);
