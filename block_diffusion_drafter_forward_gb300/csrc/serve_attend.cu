@@ -108,7 +108,7 @@ extern "C" int dflash_attend(const dflash_kv_pages* kv, const void* q, int64_t q
                              int64_t workspace_bytes, dflash_stream stream) {
   if (int rc = check_pages(kv)) return rc;
   if (nb < 1 || n_rows < 0 || max_new < 0) return call_error(DFLASH_EINVAL, "attend: nb >= 1, n_rows >= 0 and max_new >= 0");
-  if (nb > 16384) return call_error(DFLASH_ECAPACITY, "attend: nb above 16384");
+  if (nb > 16384 || n_rows > 1 << 30) return call_error(DFLASH_ECAPACITY, "attend: nb above 16384 or n_rows above 2^30");
   if (max_pages_per_seq < 1 || max_pages_per_seq >= 1 << 26)  // key indices stay below 2^30
     return call_error(DFLASH_EINVAL, "attend: max_pages_per_seq must be in [1, 2^26)");
   if (n_q_heads < 1 || n_q_heads % kv->n_kv_heads || n_q_heads / kv->n_kv_heads > 128)
@@ -117,16 +117,15 @@ extern "C" int dflash_attend(const dflash_kv_pages* kv, const void* q, int64_t q
   if (!(scale > 0.f) || !(scale <= FLT_MAX)) return call_error(DFLASH_EINVAL, "attend: scale must be positive and finite");
   if (n_rows == 0) return DFLASH_OK;
   if (!q || !out || !page_tables || !kv_lens || !row_starts) return call_error(DFLASH_EINVAL, "attend: null pointer");
-  if (kv->dtype == DFLASH_BF16 && q_stride % kv->head_dim)
-    return call_error(DFLASH_EINVAL, "attend: q_stride must be a multiple of head_dim (bf16)");
-  const int64_t need = dflash_attend_workspace(kv);
-  if (need < 0) return (int)need;
-  if (workspace_bytes < need || (need > 0 && (!workspace || !aligned16(workspace))))
-    return call_error(DFLASH_EINVAL, "attend: workspace below dflash_attend_workspace() bytes, or not 16-byte aligned");
   const int es = kv->dtype == DFLASH_F32 ? 4 : 2;
   const int64_t row = (int64_t)n_q_heads * kv->head_dim;
   if (q_stride < row || out_stride < row || (q_stride * es) % 16 || (out_stride * es) % 16 || !aligned16(q) || !aligned16(out))
     return call_error(DFLASH_EINVAL, "attend: rows below n_q_heads * head_dim, or q, out or a stride not whole 16 bytes");
+  const int64_t need = dflash_attend_workspace(kv);
+  if (need < 0) return (int)need;
+  if (workspace_bytes < need || (need > 0 && (!workspace || !aligned16(workspace))))
+    return call_error(DFLASH_EINVAL, "attend: workspace below dflash_attend_workspace() bytes, or not 16-byte aligned");
+  if (window >= 1 << 30) window = 0;  // longer than any sequence; positions less the window stay in 32 bits
   AttendParams p{q, out, lse, kv->pool, page_tables, kv_lens, row_starts, kv->status, q_stride, out_stride, kv->page_stride,
                  nb, n_rows, max_pages_per_seq, kv->num_pages, n_q_heads, kv->n_kv_heads, window, causal != 0,
                  reinterpret_cast<uintptr_t>(out) % 32 == 0 && (out_stride * es) % 32 == 0, scale * 1.4426950408889634f};

@@ -198,7 +198,8 @@ class Drafter:
         return L.dflash_kv_layout(self.handle)
 
     def kv_pages(self, layer: int) -> "PagedKV":
-        """One layer of the drafter's own pool as a PagedKV: a view, which keeps the drafter alive."""
+        """One layer of the drafter's own pool as a PagedKV: a view, which keeps the drafter alive (and
+        must not be used after its close())."""
         from .serve import PagedKV
         if not 0 <= layer < self.cfg.n_layers:
             raise ValueError(f"layer: expected one of {self.cfg.n_layers}, got {layer}")

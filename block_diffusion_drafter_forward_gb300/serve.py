@@ -6,7 +6,7 @@ dflash_attend and dflash_sample: include/dflash.h states what each computes and 
 Every call is asynchronous on `stream` (default: the current stream of the tensors' device), copies
 nothing to the host and keeps nothing for the next call.  Outputs and workspaces that a call
 allocates itself belong to that stream.  The kernels report bad page ids, lengths and full pools in
-one status word per device, read and cleared by `serve_status`."""
+one status word per device, read and cleared by `serve_status`.  Nothing here records gradients."""
 from __future__ import annotations
 
 import ctypes
@@ -19,6 +19,7 @@ import torch
 from . import _lib as L
 
 _I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
+_INT_MAX = 2 ** 31 - 1  # larger numbers would be cut to 32 bits on the way into the library
 _status: Dict[int, torch.Tensor] = {}  # device index -> its status word
 _status_lock = threading.Lock()
 
@@ -41,7 +42,8 @@ def _status_word(device: torch.device) -> torch.Tensor:
             if w is None:
                 if torch.cuda.is_current_stream_capturing():
                     raise RuntimeError("the first serving call of a device (or serve_status()) must come before a capture")
-                w = torch.zeros(1, dtype=_I32, device=device)
+                with torch.inference_mode(False):  # it outlives the caller's mode
+                    w = torch.zeros(1, dtype=_I32, device=device)
                 torch.cuda.current_stream(device).synchronize()  # zeroed for every stream
                 _status[device.index] = w
     return w
@@ -86,6 +88,12 @@ def _refuse(t, name: str, dtype: torch.dtype, shape: Tuple[int, ...], device: to
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     raise ValueError(f"{name}: must be contiguous")
+
+
+def _i32(n: int, name: str) -> int:
+    if n > _INT_MAX:
+        raise ValueError(f"{name}: {n} are too many for one call")
+    return n
 
 
 def _addresses(device: torch.device, *wanted) -> list:
@@ -183,8 +191,8 @@ def extend_tables(ctx_lens: torch.Tensor, new_rows: torch.Tensor, page_tables: t
     if not ok:
         _first(ctx_lens, "ctx_lens", 1), _first(page_tables, "page_tables", 2), _first(free_pages, "free_pages", 1)
     max_rows = int(max_rows)
-    if max_rows < 0:
-        raise ValueError("max_rows must be >= 0")
+    if not 0 <= max_rows <= _INT_MAX:
+        raise ValueError("max_rows must be in [0, 2^31)")
     one, seqs, rows = (1,), (nb,), (max_rows,)
     with _on(dev, stream) as st:
         if out is None:
@@ -249,7 +257,7 @@ class PagedKV:
         a_k, ks = _rows_of(k, "k", pool.dtype, shape, dev)
         a_v, vs = _rows_of(v, "v", pool.dtype, shape, dev)
         with _on(dev, stream) as st:
-            L.dflash_append_kv(self._c, a_k, ks, a_v, vs, a_s, n, st)
+            L.dflash_append_kv(self._c, a_k, ks, a_v, vs, a_s, _i32(n, "rows"), st)
         return pool
 
     def attend(self, q: torch.Tensor, page_tables: torch.Tensor, kv_lens: torch.Tensor, row_starts: torch.Tensor,
@@ -281,8 +289,8 @@ class PagedKV:
             if need is None:
                 need = self._workspace = L.dflash_attend_workspace(self._c)
             ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-            L.dflash_attend(self._c, a_q, qs, a_pt, mpps, a_kv, a_rs, nb, n, int(max_new), nh,
-                            1.0 / math.sqrt(hd) if scale is None else float(scale), int(window), 1 if causal else 0,
+            L.dflash_attend(self._c, a_q, qs, a_pt, mpps, a_kv, a_rs, nb, _i32(n, "rows"), min(int(max_new), _INT_MAX), nh,
+                            1.0 / math.sqrt(hd) if scale is None else float(scale), min(int(window), _INT_MAX), 1 if causal else 0,
                             a_out, os_, a_lse, ws.data_ptr() if need else 0, need, st)
         return out if lse is None else (out, lse)
 
@@ -314,7 +322,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Te
             tokens = torch.empty(rows, dtype=_I32, device=dev)
             at["tokens"] = tokens.data_ptr()
         get = at.get
-        L.dflash_sample(logits.data_ptr(), st0 if rows > 1 else V, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32, rows, V,
+        L.dflash_sample(logits.data_ptr(), st0 if rows > 1 else V, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32, _i32(rows, "rows"), V,
                         at["u"], get("temperature", 0), get("top_k", 0), get("top_p", 0), get("min_p", 0), at["tokens"],
                         get("probs", 0), st)
     return tokens if probs is None else (tokens, probs)

@@ -375,15 +375,16 @@ int dflash_append_kv(const dflash_kv_pages* kv, const void* k, int64_t k_stride,
  * (p - j < window or window == 0):
  *   out = sum_j softmax_j(scale q . k_j) v_j,   lse = ln sum_j exp(scale q . k_j)   (fp32)
  * A row that sees no key gets out = 0 and lse = -inf.  Rows of q and out are `q_stride` and
- * `out_stride` elements apart (heads contiguous, whole 16 bytes; q_stride a multiple of head_dim); lse [n_rows, n_q_heads] or NULL.
- * Rows of out and lse outside every sequence's range are left as they are.  row_starts never
+ * `out_stride` elements apart (heads contiguous, whole 16 bytes); lse [n_rows, n_q_heads] or NULL;
+ * out and lse overlap no input.  1 <= nb <= 16384 and n_rows <= 2^30 (ECAPACITY), max_pages_per_seq
+ * < 2^26.  Rows of out and lse outside every sequence's range are left as they are.  row_starts never
  * falls and stays in [0, n_rows], kv_lens in [0, 16 * max_pages_per_seq]: a sequence that breaks
  * this is skipped (its rows are left as they are) and sets DFLASH_DEV_BAD_CTX.  A page id outside
  * [0, num_pages) is read as page 0 and sets DFLASH_DEV_BAD_PAGE.  Page rows from kv_lens on are
- * not used, whatever they hold; a key that is masked for some rows only (by the causal mask or
- * the window) must hold finite values.  max_new is a host hint of the longest chunk (it picks the kernel,
- * any value gives the same results up to summation order).  n_q_heads is a multiple of
- * n_kv_heads, at most 128 times it.  `workspace` of dflash_attend_workspace() bytes (16-byte
+ * not used, whatever they hold; those below it must be finite where any row's mask hides them (a
+ * weight of zero times a NaN or infinite V is NaN).  max_new is a host hint of the longest chunk (it
+ * picks the kernel, any value gives the same results up to summation order).  n_q_heads is a
+ * multiple of n_kv_heads, at most 128 times it.  `workspace` of dflash_attend_workspace() bytes (16-byte
  * aligned) is scratch of this call: calls that may overlap on the GPU, replayed graphs among
  * them, need one each. */
 int dflash_attend(const dflash_kv_pages* kv, const void* q, int64_t q_stride, const int32_t* page_tables,

@@ -330,6 +330,87 @@ def test_attend_in_a_graph_and_on_a_stream():
         check_attend(out, lse, ref[i], slice(0, 49), 128)
 
 
+def test_attend_whatever_the_hint_and_the_row_stride():
+    """max_new picks the kernel and the way the work is found, not the result; a window past every
+    length is none; rows of q any whole 16 bytes apart."""
+    from block_diffusion_drafter_forward_gb300 import PagedKV
+    ctx, new = [40, 0, 900, 7, 130] * 8, [1, 300, 17, 0, 64] * 8
+    pool, table, lens, starts = cache(ctx, new, 2, 128, torch.bfloat16, 21)
+    n = starts[-1]
+    q = torch.randn(n, 16 * 128 + 8, device="cuda").to(torch.bfloat16).as_strided((n, 16, 128), (16 * 128 + 8, 128, 1))
+    ref = R.attend(q, pool, table, lens, starts, True, 0, 1 / math.sqrt(128))
+    kv = PagedKV(pool)
+    for hint, window in ((0, 0), (1, 2 ** 31 - 1), (17, 0), (65, 2 ** 30), (300, 2 ** 32), (2 ** 33, 0)):
+        out, lse = kv.attend(q, table, i32(lens), i32(starts), hint, window=window, lse=torch.empty(n, 16, device="cuda"))
+        check_attend(out, lse, ref, slice(0, n), 128)
+
+
+def test_attend_on_two_streams_at_once():
+    """Calls that overlap have their own workspaces, eager and replayed, and give what they give alone."""
+    from block_diffusion_drafter_forward_gb300 import PagedKV
+    cases = [([9000] * 6, [1, 2, 16, 1, 1, 9], 0), ([0, 500, 3000], [900, 40, 200], 100)]
+    calls, want = [], []
+    for i, (ctx, new, window) in enumerate(cases):
+        pool, table, lens, starts = cache(ctx, new, 4, 128, torch.bfloat16, 31 + i)
+        q = torch.randn(starts[-1], 32, 128, device="cuda").to(torch.bfloat16)
+        kv, args = PagedKV(pool), (q, table, i32(lens), i32(starts), max(new))
+        calls.append(lambda out, st=None, kv=kv, a=args, w=window: kv.attend(*a, window=w, out=out, stream=st))
+        want.append(calls[i](torch.zeros_like(q)).clone())
+    graphs, outs = [], [torch.zeros_like(w) for w in want]
+    for call, out in zip(calls, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(out)
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in calls]
+    for replay in (False, True):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for call, g, out, st in zip(calls, graphs, outs, streams):
+                if replay:
+                    with torch.cuda.stream(st):
+                        g.replay()
+                else:
+                    call(out, st)
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
+
+
+def test_pages_past_32_bits():
+    """Page offsets of more than 2^31 elements: rows appended there come back through attend."""
+    from block_diffusion_drafter_forward_gb300 import PagedKV
+    nkv, hd, stride = 1, 64, 2 ** 30 + 8
+    store = torch.empty(3 * stride, dtype=torch.bfloat16, device="cuda")
+    far = PagedKV(store.as_strided((3, nkv, 2, 16 * hd), (stride, 2 * 16 * hd, 16 * hd, 1)))
+    near = PagedKV.empty(3, nkv, hd)
+    k, v = (torch.randn(40, nkv, hd, device="cuda").to(torch.bfloat16) for _ in range(2))
+    slots = i32([(2 - i // 16) * 16 + i % 16 for i in range(40)])
+    q = torch.randn(5, 4, hd, device="cuda").to(torch.bfloat16)
+    got = []
+    for kv in (far, near):
+        kv.pool[0].zero_()
+        kv.append(k, v, slots)
+        got.append(kv.attend(q, i32([[2, 1, 0]]), i32([40]), i32([0, 5]), 5))
+    assert torch.equal(far.pool, near.pool) and torch.equal(got[0], got[1])
+
+
+def test_the_status_word_outlives_inference_mode():
+    from block_diffusion_drafter_forward_gb300 import PagedKV, _lib, serve
+    kept = dict(serve._status)
+    serve._status.clear()
+    try:
+        with torch.inference_mode():
+            kv = PagedKV(torch.zeros(2, 1, 2, 16 * 64, device="cuda"))
+            kv.append(torch.ones(1, 1, 64, device="cuda"), torch.ones(1, 1, 64, device="cuda"), i32([32]))
+        assert status() == _lib.DFLASH_DEV_BAD_PAGE and status() == 0
+    finally:
+        serve._status.clear()
+        serve._status.update(kept)
+
+
 # ------------------------------------------------------------------------------ sample
 def check_sample(x, u, tokens, probs, T, k, p, lo, rows=None):
     xs, us = x.double().cpu().numpy(), u.double().cpu().numpy()
@@ -424,6 +505,16 @@ def test_sample_rows_of_infinities_and_nan(dtype):
     check_sample(y[3:], u[3:5], tokens[3:], probs[3:], T[3:], None, None, None)
     lo = torch.full((5,), 1.5, device="cuda")     # above the largest weight
     assert sample(y, u[:5], min_p=lo).tolist() == [-1] * 5
+
+
+def test_sample_rows_past_32_bits():
+    from block_diffusion_drafter_forward_gb300 import sample
+    x = logits(3, 1000, torch.bfloat16, 7, "peaks")
+    far = torch.empty(2 * (2 ** 30 + 24) + 1000, dtype=torch.bfloat16, device="cuda").as_strided((3, 1000), (2 ** 30 + 24, 1))
+    far.copy_(x)
+    u = torch.rand(3, device="cuda")
+    a, b = (sample(t, u, probs=torch.empty(3, device="cuda")) for t in (x, far))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
 def test_sample_large_vocabulary_and_a_graph():

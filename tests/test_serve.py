@@ -53,7 +53,7 @@ def attend_args(**kw):
 @pytest.mark.parametrize("kw", [
     dict(q=None), dict(out=None), dict(page_tables=None), dict(kv_lens=None), dict(row_starts=None), dict(nb=0), dict(n_rows=-1),
     dict(max_new=-1), dict(mpps=0), dict(mpps=1 << 27), dict(nh=7), dict(nh=0), dict(nh=258), dict(window=-1), dict(scale=0.0),
-    dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(q_stride=1020), dict(q_stride=1026), dict(dtype=1, q_stride=1032),
+    dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(q_stride=1020), dict(q_stride=1026), dict(dtype=1, q_stride=1028), dict(dtype=1, out_stride=1028),
     dict(out_stride=1000), dict(q=4104), dict(out=4098)])
 def test_attend_refuses(lib, kw):
     kw = dict(kw)
