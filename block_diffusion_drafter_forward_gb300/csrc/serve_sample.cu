@@ -23,7 +23,8 @@
 // The token is a whole number that a sum's last bit can change, so weights are pairs of floats
 // (exp2 by a 128-entry table and a short polynomial on the compensated argument, about 2^-41)
 // and masses are compensated or whole numbers: in plain fp32 one row in a few hundred would
-// differ.  Only the mass past the list's range enters top-p's total in plain fp32 (a small part of it).
+// differ.  The mass past the list's range enters top-p's total with fp32 weights, and a bound on
+// their error: where a border of the prefix lies within it, the row goes by histograms, exactly.
 #include <cooperative_groups.h>
 #include <float.h>
 #include <string.h>
@@ -304,10 +305,16 @@ constexpr int kBins = 256;                   // histogram of the list
 constexpr int kLook = 64;                    // bins of the look at the first blocks,
 constexpr float kLookFar = 32.f;             // and their range of t below the maximum found there
 constexpr int kDigit = 10, kKeys = 1 << kDigit;     // histograms over keys
-// Far masses in fp32: a bound on their relative error (x - m rounded: t 2^-25 ln 2 < 8.3e-7; ex2
-// 2^-22; the correction's and the tree's roundings 5 2^-24), and the error a probability may carry
+// Far masses in fp32: a bound on their relative error up to t = 20 (x - m rounded: t 2^-24 ln 2 <
+// 8.3e-7; ex2 2^-22; the correction's and the tree's roundings 5 2^-24); what a logit further off can
+// add to it, in units of 2^-20 ((t - 20) 2^(20 - t) is at most 1 / (e ln 2): 0.531 2^-24 ln 2); and
+// the error a probability may carry
 constexpr float kNear = 12.f;
-constexpr float kFastError = 1.4e-6f, kProbError = 8e-8f;
+constexpr float kFastError = 1.4e-6f, kFastTail = 2.2e-8f, kProbError = 8e-8f;
+// The bound for a mass in units of 2^-43, of a row of `vocab` logits
+__device__ __forceinline__ unsigned long long far_error(unsigned long long far, int vocab) {
+  return part_of(far, kFastError) + part_of((unsigned long long)vocab << 23, kFastTail);
+}
 // Shared memory beside the ring, in turn: the list's places; a list's sorted prefix; the
 // stretches; the digits' histograms (the stretches are not needed yet)
 constexpr int kSideBytes = 16384;
@@ -533,7 +540,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
   };
 
   // ---- the row
-  float rest = 0.f;                                  // fp32 mass below the floor, relative to m
+  F2 rest = {0.f, 0.f};                              // mass below the floor (fp32 weights), relative to m
   unsigned long long best = 0;                       // greedy: (key, ~index)
   bool finite;                                       // m and log2(e) / T are: fp32 masses make sense
   float cut_x, near_x;                               // vectors below weigh nothing; are far
@@ -553,7 +560,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     const float m_new = of_key(max(w_key, __shfl_sync(0xffffffffu, s_key, 0)));
     if (m_new > m) {
       sc.m = m_new;
-      rest *= exp2f(-t_of(sc, m));  // (0 at first: m = -inf)
+      if (rest.h > 0.f) rest = mul(rest, weight(sc, m));
       m = m_new;
       bounds();
     }
@@ -580,7 +587,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
           const unsigned at = atomicAdd(&sh.n_list, 1u);
           if (at < kList) places[at] = pos_of(b, v);
         } else if (sum && finite && tops[v] >= cut_x) {
-          rest += fast(x4[v]);
+          rest = add(rest, F2{fast(x4[v]), 0.f});
         }
       }
       return;
@@ -604,7 +611,6 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
   bool looked = false;  // the floor is a look's
   if (by_list && !floor_by_rank()) looked = true, floor_by_look();
   __syncthreads();      // (the list takes the place of what the floor was found with)
-  rest = 0.f;
   bounds();
   stream(first_pass);
   if (greedy) {
@@ -649,10 +655,11 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     return b;
   };
 
-  // ---- the token from the row's list, in the first CTA; false: the prefix is not in it
-  auto from_list = [&]() -> bool {
+  // ---- the token from the row's list, in the first CTA
+  enum { kDone, kPast, kUnsure };  // kPast: the prefix is not in it; kUnsure: a border within the total's error
+  auto from_list = [&]() -> int {
     const int n_all = (int)sh.n_final;
-    if (sh.full || sh.rest >= 1ull << 54) return false;  // too many, or a mass above 2048 largest weights
+    if (sh.full || sh.rest >= 1ull << 54) return kPast;  // too many, or a mass above 2048 largest weights
     const float scale = kBins / fmaxf(t_of(sc, floor_x), 1e-30f);
     auto bin_of = [&](float tt) { return min(kBins - 1, (int)fminf(tt * scale, kBins)); };
     for (int i = t; i < n_all; i += kST) {
@@ -680,7 +687,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
       if (t == 0) sh.n_list = 0;
       __syncthreads();
       const int bin_k = sh.pick[1];
-      if (bin_k < 0) return false;
+      if (bin_k < 0) return kPast;
       const unsigned in_bin = sh.count[bin_k];
       if (in_bin <= kST) {
         for (int i = t; i < n_all; i += kST) {
@@ -719,11 +726,11 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     if (t == 0) sh.n_list = 0;
     __syncthreads();
     const int bin_end = sh.pick[0];
-    if (bin_end == 0x7fffffff) return false;  // the prefix goes on past the list
+    if (bin_end == 0x7fffffff) return kPast;  // the prefix goes on past the list
     if (t == bin_end) sh.red_u[0] = cum;
     __syncthreads();
     const int n = (int)sh.red_u[0];
-    if (n > kSorted) return false;
+    if (n > kSorted) return kPast;
     int n2 = 64;
     while (n2 < n) n2 *= 2;
     for (int i = t; i < n_all; i += kST) {
@@ -782,11 +789,16 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     // the kept prefix: its length and mass
     unsigned long long run = before, kept_w = 0;
     int n_kept = 0;
+    // the goal's error: the fp32 weights', and the roundings of the parts (2^-44 a warp)
+    const unsigned long long slack = sum && sh.rest ? (far_error(sh.rest, q.vocab) << 9) + (1ull << 15) : 0ull;
+    bool unsure = false;
     for (int e = 0; e < per && i0 + e < k_end; ++e) {
       const unsigned long long w = list[i0 + e];
       if ((i0 + e == 0 || run < goal) && !(low >> e & 1) && w > 0) ++n_kept, kept_w += w;
       run += w;
+      unsure |= slack && (run > goal ? run - goal : goal - run) <= slack;
     }
+    if (__syncthreads_or(unsure)) return kUnsure;
     n_kept = __reduce_add_sync(0xffffffffu, n_kept);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) kept_w += __shfl_xor_sync(0xffffffffu, kept_w, o);
@@ -831,7 +843,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
       const int at = sh.pick[0] != 0x7fffffff ? sh.pick[0] : sh.pick[1];
       put(q, row, at >= 0 ? at >> 11 : -1, at >= 0 ? (float)((double)list[at & 2047] / (double)kept_w) : 0.f);
     }
-    return true;
+    return kDone;
   };
 
   // (tau, n_tau): logits above tau are kept, and the n_tau first of those equal to it (by keys)
@@ -840,7 +852,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
   if (by_list) {
     for (;;) {
       {  // gather the row's list in the first CTA (its ring is idle: its own part of the row is through)
-        rest *= m > -INFINITY ? exp2f(-t_of(sc, m)) : 0.f;
+        if (rest.h > 0.f) rest = mul(rest, weight(sc, m));
         m = m_row;
         bounds();
         unsigned long long* dst = peer(final_list, 0);
@@ -877,11 +889,11 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
               x[e] = -INFINITY;
             }
           }
-          if (sum && finite) rest += fast_of(x);
+          if (sum && finite) rest = add(rest, F2{fast_of(x), 0.f});
         }
         if (full) atomicOr(peer(&sh.full, 0), 1u);
         if (sum) {
-          F2 s = {rest, 0.f};
+          F2 s = rest;
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) s = shfl_add(s, o);
           if (lane == 0) atomicAdd(peer(&sh.rest, 0), fix<43>(s));
@@ -889,13 +901,13 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
       }
       sync_row();
       if (rank == 0) {
-        const bool done = from_list();
+        const int what = from_list();
         if (t == 0)
-          for (int c = 0; c < C; ++c) *peer(&sh.again, c) = !done;
+          for (int c = 0; c < C; ++c) *peer(&sh.again, c) = (unsigned)what;
       }
       sync_row();
       if (!sh.again) return;
-      if (looked || (!r.use_k && !r.use_p)) break;
+      if (looked || sh.again == kUnsure || (!r.use_k && !r.use_p)) break;
       // once more with a floor that a look sets
       looked = true;
       m = m_row;
@@ -911,7 +923,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       __syncthreads();
       floor_by_look();
-      rest = 0.f;
+      rest = {0.f, 0.f};
       bounds();
       stream(first_pass);
       sync_row();
@@ -1152,7 +1164,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     const bool whole = exact || !sh.again;
     const unsigned long long target = part_of(total, r.u);
     // the fp32 sums' error: of what lies ahead, and of the target
-    const unsigned long long slack = exact ? 0ull : part_of(far, 2.f * kFastError) + 1024;
+    const unsigned long long far_off = far_error(far, q.vocab), slack = exact ? 0ull : 2 * far_off + 1024;
     for (int i = t * per; i < min(n, (t + 1) * per); ++i) {  // this CTA's first stretch past the target, and its last with any mass
       const unsigned long long x = stretch[i].mass;
       if (x > 0) {
@@ -1218,7 +1230,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
         // sure: the fp32 sums' error moves neither border of the token past the target, nor the
         // probability's last bit
         bool sure = exact || (whole && !mine_past) || (whole && token == hit && (from == 0 || from + slack <= target) && to > target + slack);
-        if (q.probs && !exact) sure = sure && (float)far * kFastError <= (float)total * kProbError;
+        if (q.probs && !exact) sure = sure && (float)far_off <= (float)total * kProbError;
         if (sure)
           put(q, row, sl.first + token, prob_of(tw, total));
         else
@@ -1280,6 +1292,7 @@ extern "C" int dflash_sample(const void* logits, int64_t row_stride, int32_t dty
   if (rows > (1 << 28) - 1) return call_error(DFLASH_ECAPACITY, "sample: too many rows for one call");
   if (rows == 0) return DFLASH_OK;
   if (!logits || !u || !tokens) return call_error(DFLASH_EINVAL, "sample: null pointer");
+  if (reinterpret_cast<uintptr_t>(logits) % (dtype == DFLASH_F32 ? 4 : 2)) return call_error(DFLASH_EINVAL, "sample: logits not whole elements");
   SampleParams p{logits, row_stride, rows, vocab, u, temperature, top_p, min_p, top_k, tokens, probs, 1, 0, {}};
   static const Powers powers;
   memcpy(p.table, powers.table, sizeof p.table);

@@ -412,7 +412,7 @@ int64_t dflash_attend_workspace(const dflash_kv_pages* kv);
  * drawn; +inf logits share the draw alone.  A row without a candidate, or whose temperature is
  * negative or not finite, gets token -1 and probability 0.  u outside [0, 1) or NaN is clamped.
  * Weights and sums carry about 40 bits, so the token is that of exact arithmetic unless u or p
- * falls within about 1e-12 of a border.
+ * falls within about 1e-11 of a border.
  *   tokens [rows] int32;  probs [rows] fp32 or NULL: kept weight of the token / their total.
  * 1 <= vocab <= 376000 (fp32) or 752000 (bf16) (EUNSUPPORTED above).  rows == 0 is a no-op. */
 int dflash_sample(const void* logits, int64_t row_stride, int32_t dtype, int32_t rows, int32_t vocab, const float* u,

@@ -507,6 +507,25 @@ def test_sample_rows_of_infinities_and_nan(dtype):
     assert sample(y, u[:5], min_p=lo).tolist() == [-1] * 5
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_sample_top_p_at_its_borders(dtype):
+    """p a rounding of fp32 away from the mass of a prefix, a tenth of the mass past it: whether the
+    next logit stays is decided by the 8th digit of the row's total."""
+    from block_diffusion_drafter_forward_gb300 import sample
+    rows, V = 256, 20000
+    g = torch.Generator(device="cuda").manual_seed(12)
+    x = (torch.randn(rows, V, generator=g, device="cuda") * 3).to(dtype)
+    p = []
+    for row in x.double().cpu().numpy():
+        w = np.exp(np.sort(row)[::-1] - row.max())
+        c = np.cumsum(np.where(w >= 2.0 ** -40, w, 0.0))
+        p.append(c[np.searchsorted(c, (0.85 + 0.1 * len(p) / rows) * c[-1])] / c[-1])
+    p = torch.tensor(p, device="cuda").float()
+    u, probs = torch.rand(rows, generator=g, device="cuda"), torch.empty(rows, device="cuda")
+    tokens, _ = sample(x, u, top_p=p, probs=probs)
+    check_sample(x, u, tokens, probs, None, None, p, None)
+
+
 def test_sample_rows_past_32_bits():
     from block_diffusion_drafter_forward_gb300 import sample
     x = logits(3, 1000, torch.bfloat16, 7, "peaks")

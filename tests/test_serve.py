@@ -99,7 +99,7 @@ def sample_args(**kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(logits=None), -1), (dict(u=None), -1), (dict(tokens=None), -1), (dict(dtype=2), -1), (dict(rows=-1), -1), (dict(vocab=0), -1),
-    (dict(stride=99), -1), (dict(vocab=752001, stride=752001), -5), (dict(vocab=376001, stride=376001, dtype=0), -5),
+    (dict(stride=99), -1), (dict(logits=4097), -1), (dict(logits=4098, dtype=0), -1), (dict(vocab=752001, stride=752001), -5), (dict(vocab=376001, stride=376001, dtype=0), -5),
     (dict(rows=1 << 28), -4), (dict(rows=0), 0)])
 def test_sample_refuses(lib, kw, code):
     assert lib.dflash_sample(*sample_args(**kw)) == code
