@@ -24,7 +24,8 @@
 // (exp2 by a 128-entry table and a short polynomial on the compensated argument, about 2^-41)
 // and masses are compensated or whole numbers: in plain fp32 one row in a few hundred would
 // differ.  The mass past the list's range enters top-p's total with fp32 weights, and a bound on
-// their error: where a border of the prefix lies within it, the row goes by histograms, exactly.
+// their error: where a border of the prefix lies within it (one row in a thousand), the row is
+// streamed once more with exact ones.
 #include <cooperative_groups.h>
 #include <float.h>
 #include <string.h>
@@ -540,7 +541,17 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
   };
 
   // ---- the row
-  F2 rest = {0.f, 0.f};                              // mass below the floor (fp32 weights), relative to m
+  F2 rest = {0.f, 0.f};                              // mass below the floor, relative to m
+  bool exact_rest = false;                           // of exact weights
+  auto slow = [&](const uint4& v4, float below_x) {  // exact mass of the logits below
+    float x[N];
+    Vec<T>::get(v4, x);
+    F2 s = {0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (x[e] < below_x && x[e] > -INFINITY) s = add(s, weight(sc, clean(x[e])));
+    return s;
+  };
   unsigned long long best = 0;                       // greedy: (key, ~index)
   bool finite;                                       // m and log2(e) / T are: fp32 masses make sense
   float cut_x, near_x;                               // vectors below weigh nothing; are far
@@ -581,6 +592,20 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     }
     if (by_list) {
       if (!(top >= (sum ? fminf(floor_x, cut_x) : floor_x))) return;
+      if (exact_rest) {
+#pragma unroll 1
+        for (int v = 0; v < kVec; ++v) {
+          const uint4 y4 = v == 0 ? x4[0] : v == 1 ? x4[1] : v == 2 ? x4[2] : x4[3];
+          const float y = Vec<T>::top(y4);
+          if (y >= floor_x) {
+            const unsigned at = atomicAdd(&sh.n_list, 1u);
+            if (at < kList) places[at] = pos_of(b, v);
+          } else if (finite && y >= cut_x) {
+            rest = add(rest, slow(y4, floor_x));
+          }
+        }
+        return;
+      }
 #pragma unroll
       for (int v = 0; v < kVec; ++v) {
         if (tops[v] >= floor_x) {  // its logits are looked at when the row is through, by all lanes
@@ -790,7 +815,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     unsigned long long run = before, kept_w = 0;
     int n_kept = 0;
     // the goal's error: the fp32 weights', and the roundings of the parts (2^-44 a warp)
-    const unsigned long long slack = sum && sh.rest ? (far_error(sh.rest, q.vocab) << 9) + (1ull << 15) : 0ull;
+    const unsigned long long slack = sum && sh.rest ? (exact_rest ? 0ull : far_error(sh.rest, q.vocab) << 9) + (1ull << 15) : 0ull;
     bool unsure = false;
     for (int e = 0; e < per && i0 + e < k_end; ++e) {
       const unsigned long long w = list[i0 + e];
@@ -889,7 +914,12 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
               x[e] = -INFINITY;
             }
           }
-          if (sum && finite) rest = add(rest, F2{fast_of(x), 0.f});
+          if (sum && finite) {
+            if (!exact_rest)
+              rest = add(rest, F2{fast_of(x), 0.f});
+            else if (i < n)
+              rest = add(rest, slow(sl.vector(pos), floor_x));
+          }
         }
         if (full) atomicOr(peer(&sh.full, 0), 1u);
         if (sum) {
@@ -907,9 +937,9 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
       }
       sync_row();
       if (!sh.again) return;
-      if (looked || sh.again == kUnsure || (!r.use_k && !r.use_p)) break;
-      // once more with a floor that a look sets
-      looked = true;
+      // once more, with exact weights or with a floor that a look sets
+      const bool unsure = sh.again == kUnsure;
+      if (unsure ? exact_rest : looked || (!r.use_k && !r.use_p)) break;
       m = m_row;
       __syncthreads();
       if (t < kBins) sh.count[t] = 0, sh.mass[t] = 0;
@@ -922,7 +952,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
       start();
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       __syncthreads();
-      floor_by_look();
+      if (unsure) exact_rest = true; else looked = true, floor_by_look();
       rest = {0.f, 0.f};
       bounds();
       stream(first_pass);
@@ -1163,8 +1193,9 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     }
     const bool whole = exact || !sh.again;
     const unsigned long long target = part_of(total, r.u);
-    // the fp32 sums' error: of what lies ahead, and of the target
-    const unsigned long long far_off = far_error(far, q.vocab), slack = exact ? 0ull : 2 * far_off + 1024;
+    // the fp32 sums' error, of what lies ahead (a) less u times the total's (a + b): at most
+    // (1 - u) |a| + u |b|, for a and b together at most far_off
+    const unsigned long long far_off = far_error(far, q.vocab), slack = exact ? 0ull : part_of(far_off, fmaxf(r.u, 1.f - r.u)) + 1024;
     for (int i = t * per; i < min(n, (t + 1) * per); ++i) {  // this CTA's first stretch past the target, and its last with any mass
       const unsigned long long x = stretch[i].mass;
       if (x > 0) {

@@ -526,6 +526,29 @@ def test_sample_top_p_at_its_borders(dtype):
     check_sample(x, u, tokens, probs, None, None, p, None)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_sample_u_at_its_borders(dtype):
+    """u a rounding of fp32 away from the mass ahead of a token, most of it small weights."""
+    from block_diffusion_drafter_forward_gb300 import sample
+    rows, V = 256, 20000
+    g = torch.Generator(device="cuda").manual_seed(13)
+    x = (torch.randn(rows, V, generator=g, device="cuda") * 2).to(dtype)
+    x[:, 777] = 9.0
+    u, rng = [], np.random.default_rng(5)
+    for row in x.double().cpu().numpy():
+        w = np.exp(row - row.max())
+        c = np.cumsum(np.where(w >= 2.0 ** -40, w, 0.0))
+        while True:  # (further than 1e-11 from the border, which the definition leaves open)
+            i = int(rng.integers(V))
+            v = float(np.float32(c[i] / c[-1]))
+            if abs(v * c[-1] - c[i]) > 1e-11 * c[-1] and 0 < v < 1:
+                break
+        u.append(v)
+    u, probs = torch.tensor(u, device="cuda"), torch.empty(rows, device="cuda")
+    tokens, _ = sample(x, u, probs=probs)
+    check_sample(x, u, tokens, probs, None, None, None, None)
+
+
 def test_sample_rows_past_32_bits():
     from block_diffusion_drafter_forward_gb300 import sample
     x = logits(3, 1000, torch.bfloat16, 7, "peaks")
