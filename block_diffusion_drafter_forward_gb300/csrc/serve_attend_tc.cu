@@ -21,11 +21,12 @@
 //
 // Bound and measured (GB300, 32 query heads on 4 kv heads of 128): single tokens and short blocks by
 // HBM - 16 single tokens on 16-32 Ki rows (64 heads on 8) 243 us, 6.6 TB/s; 32 blocks of 16 on
-// 0.5-8 Ki rows 67 us, 4.1 TB/s (the first pages of every SM come late, and each segment ends with
-// its output).  Prompts by the chain of one chunk - softmax 1.5-2.3 kcycles, P V and S 1.2 and their
-// hand-overs - of which two streams fill 55 % of the tensor pipe: a prompt of 8192 516 us,
-// 1.07 PFLOP/s.  Shared memory is nearly full with the MMAs' operands: S reads Q and K at 128 B a
-// cycle.
+// 0.5-8 Ki rows 65.5 us, 4.2 TB/s (60 us without its copies: the chunks' chain and the segments'
+// ends).  Prompts by the chain of one chunk - softmax 1.5-2.3 kcycles, P V and S 1.1 and their
+// hand-overs - of which two streams fill 56 % of the tensor pipe: a prompt of 8192 507 us,
+// 1.08 PFLOP/s (no single part holds it: without exponentials 2 % less, without maxima 8, without
+// copies 3; 64 keys at a time, S a half ahead of the softmax, 10 more - Q is then read twice as
+// often, and shared memory gives S its Q and K at 128 B a cycle).
 //
 // Rounding: P is bf16 (the MMA's operand type), sums and O fp32, the normaliser sums the fp32 P.
 // Warp roles: 0-3 stream 0, 4-7 stream 1, 8 K pages, 10 V pages, 9 and 11 MMA issue.  The V warp
@@ -37,6 +38,7 @@
 #include <float.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "launch_util.cuh"
 #include "serve_attend.cuh"
@@ -866,7 +868,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
 // Merges the partials of the unit that starts in CTA b = blockIdx.x and ends in a later one, in
 // key order.  A warp has a row (lane: HD / 32 dims); of a unit cut into more than 8 parts (few
 // sequences, long contexts) the block's 8 warps share a row's parts and meet in shared memory, so
-// that no warp waits for one batch of loads after another.
+// that no warp waits for one batch of loads after another.  Bound by issue and latency: two parts
+// taken as two instead of eight with six empty brought a prompt of 8192 from 516 to 507 us and 32
+// blocks of 16 from 67 to 65.5.
 template <int HD, int NT>
 __global__ void __launch_bounds__(256) attend_combine_kernel(const AttendParams p, const AttendWork wk) {
   constexpr int kD = HD / 32;  // dims of a lane: 4 or 2
@@ -895,12 +899,13 @@ __global__ void __launch_bounds__(256) attend_combine_kernel(const AttendParams 
     float M = -INFINITY, L = 0.f, acc[kD];
 #pragma unroll
     for (int d = 0; d < kD; ++d) acc[d] = 0.f;
-    for (int q0 = shared ? warp : 0; q0 < nsplit; q0 += shared ? 64 : 8) {
-      float2 ml[8];
-      float o[8][kD];
+    auto merge = [&](auto parts, int q0, int step) {  // parts q0, q0 + step, ...: all loads ahead of the sums
+      constexpr int N = decltype(parts)::value;
+      float2 ml[N];
+      float o[N][kD];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int q = q0 + u * (shared ? 8 : 1), slot = 2 * (blockIdx.x + q) + (q == 0 ? 1 : 0);
+      for (int u = 0; u < N; ++u) {
+        const int q = q0 + u * step, slot = 2 * (blockIdx.x + q) + (q == 0 ? 1 : 0);
         ml[u] = make_float2(-INFINITY, 0.f);
         if (q < nsplit) {
           ml[u] = __ldcg(wk.ml + (int64_t)slot * (NT * 128) + row);
@@ -918,7 +923,7 @@ __global__ void __launch_bounds__(256) attend_combine_kernel(const AttendParams 
         }
       }
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < N; ++u) {
         const float Mn = fmaxf(M, ml[u].x), z = Mn == -INFINITY ? 0.f : Mn;
         const float f = exp2f(M - z), fu = exp2f(ml[u].x - z);
 #pragma unroll
@@ -926,7 +931,11 @@ __global__ void __launch_bounds__(256) attend_combine_kernel(const AttendParams 
         L = L * f + ml[u].y * fu;
         M = Mn;
       }
-    }
+    };
+    if (nsplit == 2)  // most units
+      merge(std::integral_constant<int, 2>{}, 0, 1);
+    else
+      for (int q0 = shared ? warp : 0; q0 < nsplit; q0 += shared ? 64 : 8) merge(std::integral_constant<int, 8>{}, q0, shared ? 8 : 1);
     if (shared) {
 #pragma unroll
       for (int d = 0; d < kD; ++d) s_o[warp][lane * kD + d] = acc[d];
