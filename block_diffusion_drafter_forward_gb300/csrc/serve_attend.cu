@@ -129,6 +129,9 @@ extern "C" int dflash_attend(const dflash_kv_pages* kv, const void* q, int64_t q
   AttendParams p{q, out, lse, kv->pool, page_tables, kv_lens, row_starts, kv->status, q_stride, out_stride, kv->page_stride,
                  nb, n_rows, max_pages_per_seq, kv->num_pages, n_q_heads, kv->n_kv_heads, window, causal != 0,
                  reinterpret_cast<uintptr_t>(out) % 32 == 0 && (out_stride * es) % 32 == 0, scale * 1.4426950408889634f};
+  p.group = n_q_heads / kv->n_kv_heads;
+  p.tokens = 128 / p.group;
+  p.inv = (65536 + p.group - 1) / p.group;  // (exact: 127 (inv group - 65536) < 65536)
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (kv->dtype == DFLASH_BF16) {
     int sms = 0;

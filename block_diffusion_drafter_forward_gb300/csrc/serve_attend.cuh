@@ -17,13 +17,15 @@ struct AttendParams {
   int nb, n_rows, mpps, num_pages, nh, nkv, window, causal;
   bool wide_out;     // rows of out start on 32 bytes
   float scale_log2;  // scale * log2(e): scores are exponents of 2
+  int group, tokens; // query heads of a kv head; tokens of a tile of 128 rows
+  unsigned inv;      // row / group = row * inv >> 16 for rows below 128
 };
 
 // Workspace of the tensor-core form: split units' partials.
 struct AttendWork {
   float* o;        // [2 sms][rows][head_dim] unnormalised O
   float2* ml;      // [2 sms][rows] (maximum in log2 units, sum)
-  int4* meta;      // [sms] the unit that starts in a CTA and ends in a later one: (CTAs, s, tile, g)
+  int4* meta;      // [sms] the unit that starts in a CTA and ends in a later one: (CTAs, its first row, tokens, g)
   int long_chunks; // many query tiles per sequence
 };
 

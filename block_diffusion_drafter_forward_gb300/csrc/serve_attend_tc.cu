@@ -21,10 +21,10 @@
 //
 // Bound and measured (GB300, 32 query heads on 4 kv heads of 128): single tokens and short blocks by
 // HBM - 16 single tokens on 16-32 Ki rows (64 heads on 8) 243 us, 6.6 TB/s; 32 blocks of 16 on
-// 0.5-8 Ki rows 65.5 us, 4.2 TB/s (60 us without its copies: the chunks' chain and the segments'
+// 0.5-8 Ki rows 64 us, 4.3 TB/s (7 us less without its copies: the chunks' chain and the segments'
 // ends).  Prompts by the chain of one chunk - softmax 1.5-2.3 kcycles, P V and S 1.1 and their
-// hand-overs - of which two streams fill 56 % of the tensor pipe: a prompt of 8192 507 us,
-// 1.08 PFLOP/s (no single part holds it: without exponentials 2 % less, without maxima 8, without
+// hand-overs - of which two streams fill 57 % of the tensor pipe: a prompt of 8192 499 us,
+// 1.10 PFLOP/s (no single part holds it: without exponentials 2 % less, without maxima 8, without
 // copies 3; 64 keys at a time, S a half ahead of the softmax, 10 more - Q is then read twice as
 // often, and shared memory gives S its Q and K at 128 B a cycle).
 //
@@ -96,8 +96,8 @@ struct Shape {
 };
 __device__ __forceinline__ Shape shape_of(const AttendParams& p, int NT) {
   Shape h;
-  h.group = p.nh / p.nkv;
-  h.T = 128 / h.group;
+  h.group = p.group;
+  h.T = p.tokens;
   h.TT = h.T * NT;
   return h;
 }
@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
     const int x = warp >> 2, row = t & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + x * 128 + lane_off;
-    const int tok = row / h.group, head = row - tok * h.group;
+    const int tok = row / h.group, head = row - tok * h.group;  // (by p.inv the loop's registers fall worse: 519 us for 499)
     const bool loads = (t & 127) == 0 && (NT == 2 || x == 0);  // (one tile: stream 0's, a segment ahead)
     Walk w = walk;
     Seg q, nq;
@@ -847,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         const long long end = walk.hi - (q.c_hi - 1) + q.nch - 1;  // past its last slot: slot hi - 1 is chunk c_hi - 1
         const int G = (int)min((long long)gridDim.x, W);
         const int last = (int)((end * G + W - 1) / W) - 1;
-        wk.meta[blockIdx.x] = make_int4(last - (int)blockIdx.x + 1, q.s, q.tile, q.g);
+        wk.meta[blockIdx.x] = make_int4(last - (int)blockIdx.x + 1, q.r0 + q.t0, min(h.TT, q.n - q.t0), q.g);
       }
       tc_fence_before();
       mbar_arrive(&c.o_free[NT == 2 ? x : 0]);
@@ -869,8 +869,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
 // key order.  A warp has a row (lane: HD / 32 dims); of a unit cut into more than 8 parts (few
 // sequences, long contexts) the block's 8 warps share a row's parts and meet in shared memory, so
 // that no warp waits for one batch of loads after another.  Bound by issue and latency: two parts
-// taken as two instead of eight with six empty brought a prompt of 8192 from 516 to 507 us and 32
-// blocks of 16 from 67 to 65.5.
+// taken as two instead of eight with six empty, and no division or lookup of the unit, brought a prompt
+// of 8192 from 516 to 499 us and 32 blocks of 16 from 67 to 64.
 template <int HD, int NT>
 __global__ void __launch_bounds__(256) attend_combine_kernel(const AttendParams p, const AttendWork wk) {
   constexpr int kD = HD / 32;  // dims of a lane: 4 or 2
@@ -882,18 +882,15 @@ __global__ void __launch_bounds__(256) attend_combine_kernel(const AttendParams 
   const int nsplit = meta.x;
   if (nsplit == 0) return;
   const Shape h = shape_of(p, NT);
-  int r0, n, kv;
-  bool bad;
-  seq_of(p, meta.y, &r0, &n, &kv, &bad);
-  const int t0 = meta.z * h.TT, g = meta.w;
+  const int n = meta.z, g = meta.w;  // tokens of the unit
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tiles = min(NT, (n - t0 + h.T - 1) / h.T);  // query tiles with tokens
+  const int tiles = n > h.T ? 2 : 1;  // query tiles with tokens
   const bool shared = nsplit > 8;
   const int rows = shared ? 1 : 8;                      // of the block at a time
   for (int base = blockIdx.y * rows; base < tiles * 128; base += gridDim.y * rows) {
     const int row = shared ? base : base + warp;
-    const int x = row >> 7, tok = (row & 127) / h.group, head = (row & 127) - tok * h.group;
-    const int tk = t0 + x * h.T + tok;
+    const int x = row >> 7, tok = (row & 127) * p.inv >> 16, head = (row & 127) - tok * h.group;
+    const int tk = x * h.T + tok;
     const bool valid = tok < h.T && tk < n;
     if (!valid) continue;  // (shared: the whole block has the same row)
     float M = -INFINITY, L = 0.f, acc[kD];
@@ -961,7 +958,7 @@ __global__ void __launch_bounds__(256) attend_combine_kernel(const AttendParams 
     }
     if (!shared || warp == 0) {
       const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-      const int64_t gr = r0 + tk;
+      const int64_t gr = meta.y + tk;
       const int gh = g * h.group + head;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + gr * p.out_stride + (int64_t)gh * HD + lane * kD;
       if (kD == 4)
@@ -989,8 +986,7 @@ cudaError_t launch(const AttendParams& p, const AttendWork& w, int sms, cudaStre
   c.attrs = a;
   c.numAttrs = 1;
   CUtensorMap q_map;
-  const int group = p.nh / p.nkv;
-  if (!make_tmap_heads_bf16(&q_map, p.q, p.n_rows, p.nh, HD, p.q_stride, group, 128 / group)) return cudaErrorInvalidValue;
+  if (!make_tmap_heads_bf16(&q_map, p.q, p.n_rows, p.nh, HD, p.q_stride, p.group, p.tokens)) return cudaErrorInvalidValue;
   if (cudaError_t e = cudaLaunchKernelEx(&c, attend_tc_kernel<HD, NT>, p, w, q_map); e != cudaSuccess) return e;
   c.gridDim = dim3(sms, NT * 16);  // a unit's rows in one round
   c.blockDim = dim3(256);
@@ -1010,7 +1006,7 @@ cudaError_t launch_attend_tc(const AttendParams& p, int head_dim, int max_new, v
   w.o = static_cast<float*>(workspace);
   w.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + (int64_t)sms * 2 * 256 * head_dim * 4);
   w.meta = reinterpret_cast<int4*>(w.ml + (int64_t)sms * 2 * 256);
-  const int T = 128 / (p.nh / p.nkv);
+  const int T = p.tokens;
   // Chunks longer than one tile: two tiles share every K/V slot, where there are units enough for the
   // SMs.  Measured (32 query heads on 4, one tile / two): 32 sequences x 17 tokens on 4096 rows
   // 109 / 93 us, x 64 199 / 163 us, 8 x 256 on 2048 113 / 102 us, 64 x 20 on 500 62 / 49 us; with few
