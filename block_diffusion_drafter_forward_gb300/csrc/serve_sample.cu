@@ -303,7 +303,7 @@ constexpr int kStages = 3, kVec = 4;         // ring: blocks in flight; vectors 
 constexpr int kStageBytes = kST * kVec * 16; // 16 KB
 constexpr int kMaxC = 8;                     // CTAs of a row
 constexpr int kList = 4096;                  // places that a list holds
-constexpr int kAim = 3072;                   // and that the floor may aim at
+constexpr int kAim = 3000;                   // and that the floor may aim at
 constexpr int kSorted = 2048;                // logits of the sorted prefix
 constexpr int kBins = 256;                   // histogram of the list
 constexpr int kLook = 64;                    // bins of the look at the first blocks,
