@@ -468,7 +468,15 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     return fast_of(x);
   };
   float floor_x = -INFINITY;  // the list takes logits from here on
-  const float share = (float)seen / (float)max(blocks, 1);  // of the row seen
+  // The share of the row seen.  The last slice may have a block less than the others, and what the
+  // CTAs decide by it (which floor, hence which cluster barriers) has to be the same in all of them:
+  // it is counted over every slice, not over this CTA's.
+  int row_blocks = 0, row_seen = 0;
+  for (int c = 0; c < C; ++c) {
+    const int n = (max(0, min(q.per, q.vocab - (sl.first + (c - rank) * q.per))) + kBlock - 1) / kBlock;
+    row_blocks += n, row_seen += min(n, kStages);
+  }
+  const float share = (float)row_seen / (float)max(row_blocks, 1);
   // A floor by rank: of the threads' largest logits in the blocks seen, the r-th is about the row's
   // r / share-th (a thread seldom has two of them).  false: the list wants more than that tells
   auto floor_by_rank = [&]() -> bool {
@@ -515,7 +523,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
       }
     }
     sync_row();
-    if (warp == 0) {
+    if (rank == 0 && warp == 0) {
       // lane l: bins 2 l, 2 l + 1 of the row's first blocks.  The first bins by which, going by them,
       // the list holds what the filter needs: k and half as many more; all but 1 - p of the mass
       // (the mass left out, as the blocks seen have it, against that seen alone: the few large
@@ -538,7 +546,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
       if (lane == 0) sh.floor = isinf(m) || isinf(sc.c_hi) ? m : m - pairs * 2 * step / sc.c_hi;
     }
     sync_row();  // (the counts have been read by every CTA)
-    floor_x = sh.floor;
+    floor_x = *peer(&sh.floor, 0);  // one floor: from_list takes it for every slice's
     if (t < kLook) sh.count[t] = 0;
     __syncthreads();
   };

@@ -1,0 +1,66 @@
+"""Sampling of rows that several CTAs share, or that take the long ways through the kernel, against the
+plain 64-bit form (tests/serve_ref.py)."""
+import numpy as np
+import pytest
+import torch
+
+import serve_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+def body(rows, V, dtype, seed, scale, peaks):
+    """Rows of a Gaussian body, with `peaks` likely tokens at falling scores."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(rows, V, generator=g, device="cuda") * scale
+    if peaks:
+        at = torch.rand(rows, peaks, generator=g, device="cuda").argsort(1) * (V // peaks)
+        x.scatter_(1, at, 14.0 - 1.7 * torch.log1p(torch.arange(peaks, device="cuda").float()).expand(rows, peaks))
+    return x.to(dtype), torch.rand(rows, generator=g, device="cuda")
+
+
+def check(x, u, sets, take, probs=True):
+    """Draws all rows (they decide how many CTAs share one) with row r's settings sets[r % len(sets)] and
+    holds rows `take` to the plain form."""
+    from block_diffusion_drafter_forward_gb300 import sample
+    rows = x.shape[0]
+    col = [[sets[r % len(sets)][i] for r in range(rows)] for i in range(4)]
+    T, p, lo = (torch.tensor(col[i], dtype=torch.float32, device="cuda") for i in (0, 2, 3))
+    k = torch.tensor(col[1], dtype=torch.int32, device="cuda")
+    pr = torch.empty(rows, device="cuda") if probs else None
+    got = sample(x, u, T, k, p, lo, probs=pr)
+    tokens = (got[0] if probs else got).tolist()
+    for r in take:
+        T_, p_, lo_, u_ = (float(v[r]) for v in (T, p, lo, u))
+        want, wp = R.sample(x[r].double().cpu().numpy(), u_, T_, col[1][r], p_, lo_)
+        assert tokens[r] == want, (r, tokens[r], want, T_, col[1][r], p_, lo_, u_)
+        if probs:
+            assert abs(float(pr[r]) - wp) <= 2.0 ** -23 * wp + 1e-12, (r, float(pr[r]), wp)
+
+
+# (vocabulary, type, rows): CTAs of a row have unequal numbers of blocks, so that a share of the row
+# counted by each for itself sent some of them by one floor and the others by another
+UNEVEN = [(262144, torch.bfloat16, 1), (262144, torch.bfloat16, 16), (262144, torch.bfloat16, 100), (262144, torch.bfloat16, 200),
+          (262144, torch.float32, 16), (262144, torch.float32, 64), (131072, torch.bfloat16, 100), (131072, torch.float32, 20),
+          (163840, torch.bfloat16, 90), (102400, torch.float32, 90), (49152, torch.bfloat16, 200)]
+
+
+@pytest.mark.parametrize("V,dtype,rows", UNEVEN)
+def test_every_cta_of_a_row_goes_by_one_floor(V, dtype, rows):
+    k_sets = [(0.9, k, p, 0.0) for k, p in ((400, 1.0), (450, 0.9), (600, 1.0), (868, 1.0), (900, 0.95), (1000, 0.8), (1000, 1.0), (1095, 1.0),
+                                            (1300, 0.99), (1800, 1.0), (2000, 1.0), (2100, 0.9))]
+    p_sets = [(1.0, 0, 0.95, 0.0), (0.8, 0, 0.9, 0.0), (1.2, 0, 0.99, 0.0), (2.0, 0, 0.9, 0.0), (0.6, 0, 0.999, 0.0), (1.0, 0, 0.5, 0.01)]
+    for seed, (scale, peaks) in enumerate(((2.0, 48), (1.0, 0))):
+        x, u = body(rows, V, dtype, seed, scale, peaks)
+        for sets in (k_sets, p_sets):
+            if rows == 1:
+                for s in sets[::2]:
+                    check(x, u, [s], [0])
+            else:
+                check(x, u, sets, list(range(0, min(rows, len(sets)), 1 + seed)) + [rows - 1])
