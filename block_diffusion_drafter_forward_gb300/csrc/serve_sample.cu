@@ -572,9 +572,9 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     near_x = finite ? reach(sc, kNear) : cut_x;
   };
   auto first_pass = [&](int b, uint4 (&x4)[kVec], float (&tops)[kVec], auto&& next) {
-    float top = tops[0];
+    float top = -INFINITY;  // (a vector of NaN alone has a NaN for its largest, and NaN's key is above every number's)
 #pragma unroll
-    for (int v = 1; v < kVec; ++v) top = fmaxf(top, tops[v]);
+    for (int v = 0; v < kVec; ++v) top = fmaxf(top, tops[v]);
     const unsigned w_key = __reduce_max_sync(0xffffffffu, key_of(top + 0.f));
     const unsigned s_key = *(volatile unsigned*)&sh.m_key;
     if (lane == 0 && w_key > s_key) atomicMax(&sh.m_key, w_key);

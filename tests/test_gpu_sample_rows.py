@@ -64,3 +64,22 @@ def test_every_cta_of_a_row_goes_by_one_floor(V, dtype, rows):
                     check(x, u, [s], [0])
             else:
                 check(x, u, sets, list(range(0, min(rows, len(sets)), 1 + seed)) + [rows - 1])
+
+
+# (vocabulary, rows): one CTA of a row, two, and eight
+@pytest.mark.parametrize("V,rows", [(20000, 460), (40000, 8), (151936, 8)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_runs_of_nan_are_no_candidates(V, rows, dtype):
+    """NaN logits count as -inf, also where a thread meets nothing else; the largest logit in the run's
+    slice, ahead of it, behind it and elsewhere."""
+    sets = [(1.0, 0, 1.0, 0.0), (0.0, 0, 1.0, 0.0), (0.8, 50, 1.0, 0.0), (1.0, 0, 0.9, 0.0), (1.0, 0, 1.0, 0.05), (1.0, 700, 0.95, 0.01),
+            (1.5, 0, 0.99, 0.0), (3.0, 0, 0.9, 0.0)]
+    x, u = body(rows, V, dtype, V, 2.0, 16)
+    runs = [(V // 2, V), (V // 2, V // 2 + 5000), (0, V // 3), (V // 3, V - 3), (3, V - 1), (V - 4000, V - 500), (V // 2 - 2100, V // 2 + 2100), (8, 1500)]
+    for r in range(rows):
+        a, b = runs[r % len(runs)]
+        x[r, a:b] = float("nan")
+        x[r, (a - 1, min(b, V - 1))[r // 8 % 2]] = 16.0 if a else -1.0
+    for shift in (0, 1, 3) if rows == 8 else (0,):
+        take = range(16) if rows > 8 else range(8)
+        check(x, u, sets[shift:] + sets[:shift], take)
