@@ -78,8 +78,13 @@ __device__ __forceinline__ F2 mul(F2 a, F2 b) {
 }
 __device__ __forceinline__ bool below(F2 a, float b) { return a.h < b || (a.h == b && a.l < 0.f); }
 // Masses as whole numbers of 2^-B: sums and comparisons are exact and cost integer operations
-// (fp64 runs at 1/64 of the fp32 rate here).  B = 52 where at most 2048 weights are added, 43 for
-// a row's.
+// (fp64 runs at 1/64 of the fp32 rate here).  Equal logits round alike, so what a weight loses by
+// its rounding adds up over a row: B is chosen so that a row of 2^20 loses less than 1e-11 of its
+// mass (at least 1).  52 where at most 2048 weights are added in 64 bits (a sorted prefix, a stretch:
+// one rounding per lane of it), 59 where a row's are added one by one (keys); sums over a row then
+// have 128 bits.  43, in 64 bits over a row, is for masses rounded once per warp and for bounds.
+typedef unsigned __int128 u128;
+constexpr int kStretchUnit = 52, kKeyUnit = 59;
 template <int B>
 __device__ __forceinline__ unsigned long long fix(F2 a) {
   constexpr float k = (float)(1ull << B);
@@ -104,6 +109,20 @@ __device__ __forceinline__ unsigned long long part_of(unsigned long long a, floa
   }
   if (inexact) *inexact = rem != 0;
   return r;
+}
+__device__ __forceinline__ u128 part_of(u128 a, float f, bool* inexact = nullptr) {  // a below 2^104
+  if (inexact) *inexact = false;
+  if (!(f > 0.f)) return 0;
+  if (f >= 1.f) return a;
+  int e;
+  const u128 x = a * (unsigned long long)ldexpf(frexpf(f, &e), 24);  // f = m 2^(e - 24), e <= 0
+  const int sh = 24 - e;
+  const u128 r = sh < 128 ? x >> sh : 0;
+  if (inexact) *inexact = sh < 128 ? r << sh != x : x != 0;
+  return r;
+}
+__device__ __forceinline__ double to_double(u128 a) {
+  return (double)(unsigned long long)(a >> 64) * 0x1p64 + (double)(unsigned long long)a;
 }
 __device__ __forceinline__ F2 shfl_add(F2 a, int o) {
   F2 b = {__shfl_xor_sync(0xffffffffu, a.h, o), __shfl_xor_sync(0xffffffffu, a.l, o)};
@@ -279,8 +298,9 @@ struct Slice {
   }
 };
 
-__device__ __forceinline__ float prob_of(F2 w, unsigned long long total) {  // total in units of 2^-43
-  return (float)(((double)w.h + (double)w.l) / ((double)total * 0x1p-43));
+__device__ __forceinline__ float prob_of(F2 w, u128 total) {  // total in units of 2^-52
+  static_assert(kStretchUnit == 52, "the unit");
+  return (float)(((double)w.h + (double)w.l) / (to_double(total) * 0x1p-52));
 }
 __device__ __forceinline__ void put(const SampleParams& q, int row, int token, float prob) {
   q.tokens[row] = token;
@@ -308,7 +328,9 @@ constexpr int kSorted = 2048;                // logits of the sorted prefix
 constexpr int kBins = 256;                   // histogram of the list
 constexpr int kLook = 64;                    // bins of the look at the first blocks,
 constexpr float kLookFar = 32.f;             // and their range of t below the maximum found there
-constexpr int kDigit = 10, kKeys = 1 << kDigit;     // histograms over keys
+// Histograms over keys: bins of a round, and the words of a bin's mass, 12 bits of every weight each
+// (2^20 of them fit).  9 bits a round: two rounds for bf16's keys and four for fp32's, as by 10.
+constexpr int kDigit = 9, kKeys = 1 << kDigit, kParts = 5, kPartBits = 12;
 // Far masses in fp32: a bound on their relative error up to t = 20 (x - m rounded: t 2^-24 ln 2 <
 // 8.3e-7; ex2 2^-22; the correction's and the tree's roundings 5 2^-24); what a logit further off can
 // add to it, in units of 2^-20 ((t - 20) 2^(20 - t) is at most 1 / (e ln 2): 0.531 2^-24 ln 2); and
@@ -322,11 +344,12 @@ __device__ __forceinline__ unsigned long long far_error(unsigned long long far, 
 // Shared memory beside the ring, in turn: the list's places; a list's sorted prefix; the
 // stretches; the digits' histograms (the stretches are not needed yet)
 constexpr int kSideBytes = 16384;
-static_assert(kList * 4 == kSideBytes && kSorted * 8 == kSideBytes && kKeys * 16 == kSideBytes, "one size");
+static_assert(kList * 4 == kSideBytes && kSorted * 8 == kSideBytes && kKeys * kParts * 4 <= kSideBytes, "one size");
+static_assert(kKeyUnit < kParts * kPartBits, "a weight of 1 has its bits");
 static_assert(kList * 8 + kSorted * 8 <= kStages * kStageBytes, "the row's list, and places by index, fit in the ring");
 constexpr int kStreamSmem = kStages * kStageBytes + kSideBytes;
 
-struct Stretch {  // mass of a warp's part of a block (2^-43), relative to ref
+struct Stretch {  // mass of a warp's part of a block (2^-52: 1024 weights at most), relative to ref
   unsigned long long mass;
   unsigned ties;  // logits equal to tau ahead of it
   float ref;
@@ -336,7 +359,8 @@ struct Shared {
   float2 table[128];
   unsigned count[kBins];
   unsigned long long mass[kBins];
-  unsigned long long red_l[kSW], rest, best, before, part, far, far_part;
+  unsigned long long red_l[kSW], rest, best, before, far, far_part;
+  u128 part, above;
   unsigned red_u[kSW], ties;
   unsigned m_key, n_list, n_final, full, again;
   float floor, floors[kSW];
@@ -413,7 +437,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
   if (t == 0) {
     sh.m_key = 0;
     sh.n_list = sh.n_final = sh.full = sh.again = 0;
-    sh.rest = sh.best = sh.far = sh.part = 0;
+    sh.rest = sh.best = sh.far = 0;
     sh.pick[0] = 0x7fffffff;
     sh.pick[1] = -1;
   }
@@ -639,7 +663,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
         far += fast(x4[v]);
       }
     }
-    unsigned long long mass = fix<43>(F2{far, 0.f});
+    unsigned long long mass = fix<kStretchUnit>(F2{far, 0.f});
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
     if (lane == 0) stretch[b * kSW + warp] = Stretch{mass, 0u, m};
@@ -689,6 +713,14 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     __syncthreads();
     *all = a;
     return b;
+  };
+  auto scan_w = [&](u128 v, u128* all) {  // the same in 128 bits (256 values: each half's sum fits in 64)
+    constexpr int kHalf = 52;
+    unsigned long long a_lo, a_hi;
+    const unsigned long long lo = scan_l((unsigned long long)v & ((1ull << kHalf) - 1), &a_lo);
+    const unsigned long long hi = scan_l((unsigned long long)(v >> kHalf), &a_hi);
+    *all = ((u128)a_hi << kHalf) + a_lo;
+    return ((u128)hi << kHalf) + lo;
   };
 
   // ---- the token from the row's list, in the first CTA
@@ -974,14 +1006,15 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     // k (by_mass: the mass reaches p of all).  Rounds over keys [lo, hi], kDigit bits of them each;
     // keys below tau_k do not take part and n_k of those equal to it do.  false: it is not reached.
     m = m_row;
-    auto border = [&](bool by_mass, unsigned tau_k, unsigned n_k, unsigned* key, unsigned long long* left) {
+    auto border = [&](bool by_mass, unsigned tau_k, unsigned n_k, unsigned* key, u128* left) {
       unsigned hi = digit_key<T>(m_row);
       unsigned lo = max(tau_k, digit_key<T>(by_mass ? fmaxf(reach(sc, kCut), -FLT_MAX) : -FLT_MAX));
-      unsigned long long goal = (unsigned)r.k, above = 0;
-      const unsigned long long w_k = by_mass && n_k > 0 ? n_k * fix<43>(weight(sc, of_digit_key<T>(tau_k))) : 0ull;
+      u128 goal = (unsigned)r.k, above = 0;
+      const u128 w_k = by_mass && n_k > 0 ? (u128)n_k * fix<kKeyUnit>(weight(sc, of_digit_key<T>(tau_k))) : 0;
       for (bool first = true;; first = false) {
         const int bits = 32 - __clz(hi - lo), shift = max(0, bits - kDigit);
-        for (int i = t; i < kKeys * 4; i += kST) digits[i] = 0;
+        const bool by_count = !by_mass || shift == 0;  // (one key a bin: its mass is the count times its weight)
+        for (int i = t; i < kKeys * kParts; i += kST) digits[i] = 0;
         if (t == 0) sh.pick[0] = -1;
         start();
         __syncthreads();
@@ -999,14 +1032,14 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
               const unsigned k = digit_key<T>(clean(x[e]));
               if (k < lo || k > hi) continue;
               unsigned* d = digits + ((hi - k) >> shift);
-              if (!by_mass) {
+              if (by_mass && k == tau_k && n_k > 0) continue;  // (w_k has them)
+              if (by_count) {
                 atomicAdd(d, 1u);
-              } else if (k > tau_k || n_k == 0) {
-                // four parts of 11 bits: 2^20 of them fit in a word
-                const unsigned long long w = fix<43>(weight(sc, clean(x[e])));
+              } else {
+                const unsigned long long w = fix<kKeyUnit>(weight(sc, clean(x[e])));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const unsigned part = (unsigned)(w >> 11 * i) & 2047u;
+                for (int i = 0; i < kParts; ++i) {
+                  const unsigned part = (unsigned)(w >> kPartBits * i) & ((1u << kPartBits) - 1);
                   if (part) atomicAdd(d + i * kKeys, part);
                 }
               }
@@ -1015,34 +1048,33 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
         });
         sync_row();
         constexpr int kB = kKeys / kST;  // thread t: bins kB t ..
-        unsigned long long v[kB], mine = 0, all;
+        u128 v[kB], mine = 0, all;
 #pragma unroll
         for (int b = 0; b < kB; ++b) {
           v[b] = 0;
           const int at = t * kB + b;
           for (int c = 0; c < C; ++c) {
             const unsigned* d = peer(digits, c) + at;
-            v[b] += by_mass ? (unsigned long long)d[0] + ((unsigned long long)d[kKeys] << 11) +
-                                  ((unsigned long long)d[2 * kKeys] << 22) + ((unsigned long long)d[3 * kKeys] << 33)
-                            : d[0];
+            for (int i = 0; i < (by_count ? 1 : kParts); ++i) v[b] += (u128)d[i * kKeys] << kPartBits * i;
           }
+          if (by_mass && by_count && v[b] > 0) v[b] *= fix<kKeyUnit>(weight(sc, of_digit_key<T>(hi - at)));
           if (by_mass && n_k > 0 && tau_k >= lo && tau_k <= hi && (int)((hi - tau_k) >> shift) == at) v[b] += w_k;
           mine += v[b];
         }
-        unsigned long long run = above + scan_l(mine, &all);
+        u128 run = above + scan_w(mine, &all);
         if (first && by_mass) {
           bool more;
-          goal = part_of(all, r.p, &more);
-          goal = max(goal + more, 1ull);  // the first always stays
+          goal = part_of(all, r.p, &more) + more;
+          if (goal == 0) goal = 1;  // the first always stays
         }
 #pragma unroll
         for (int b = 0; b < kB; ++b) {
-          if (run < goal && run + v[b] >= goal) sh.pick[0] = t * kB + b, sh.before = run;
+          if (run < goal && run + v[b] >= goal) sh.pick[0] = t * kB + b, sh.above = run;
           run += v[b];
         }
         sync_row();  // every CTA has read the others' bins
         const int b = sh.pick[0];
-        above = b < 0 ? above : sh.before;
+        above = b < 0 ? above : sh.above;
         __syncthreads();  // read before the next round resets it
         if (b < 0) return false;
         hi -= (unsigned)b << shift;
@@ -1054,7 +1086,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
         }
       }
     };
-    unsigned long long left;
+    u128 left;
     if (r.use_k && border(false, 0, 0, &tau, &left)) {  // (else fewer than k candidates: all stay)
       n_tau = (unsigned)left;
       ties = true;
@@ -1063,9 +1095,13 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
       const unsigned n_k = n_tau;
       unsigned key;
       if (border(true, tau, n_k, &key, &left)) {
-        // of the keys equal to it: those before which less than the goal lies
-        const F2 w = weight(sc, of_digit_key<T>(key));
-        const unsigned n = max(1u, (unsigned)fmin(ceil((double)left * 0x1p-43 / ((double)w.h + (double)w.l) - 1e-9), 2e9));
+        // of the keys equal to it: those before which less than the goal lies (1 + the largest n of
+        // which the mass is below)
+        const unsigned long long w = fix<kKeyUnit>(weight(sc, of_digit_key<T>(key)));
+        unsigned n = 0;
+        for (unsigned bit = 1u << 20; bit > 0; bit >>= 1)
+          if ((u128)(n | bit) * w < left) n |= bit;
+        ++n;
         n_tau = key == tau && n_k > 0 ? min(n_k, n) : n;
         tau = key;
         ties = true;
@@ -1148,7 +1184,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
           }
           if (ties) at += __shfl_sync(0xffffffffu, inc, 31);
         }
-        unsigned long long mass = fix<43>(s);
+        unsigned long long mass = fix<kStretchUnit>(s);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
         if (lane == 0) stretch[b * kSW + warp] = Stretch{mass, ahead, m_row};
@@ -1157,7 +1193,8 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     }
     // ---- the stretch that holds the target
     const int n = blocks * kSW, per = (n + kST - 1) / kST;
-    unsigned long long mine = 0, my_far = 0, part;
+    u128 mine = 0, part;
+    unsigned long long my_far = 0;  // (2^-43)
     if (!exact) {
       // by the row's maximum now, and the near vectors exactly
       for (int i = t; i < n; i += kST) {
@@ -1166,7 +1203,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
           const float h = (float)s.mass, l = (float)(long long)(s.mass - (unsigned long long)h);
           s.mass = s.ref > -INFINITY ? fix<0>(mul(F2{h, l}, weight(sc, s.ref))) : 0ull;  // (in the same units)
         }
-        my_far += s.mass;
+        my_far += (s.mass >> (kStretchUnit - 43)) + 1;
       }
       __syncthreads();
       for (int i = t; i < (int)min(sh.n_list, near_room); i += kST) {
@@ -1177,7 +1214,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
 #pragma unroll
         for (int e = 0; e < N; ++e)
           if (clean(x[e]) > -INFINITY) s = add(s, weight(sc, clean(x[e])));
-        atomicAdd(&stretch[pos / kBlock * kSW + pos % kBlock / kWarpPart].mass, fix<43>(s));
+        atomicAdd(&stretch[pos / kBlock * kSW + pos % kBlock / kWarpPart].mass, fix<kStretchUnit>(s));
       }
       __syncthreads();
     }
@@ -1188,14 +1225,15 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     for (int o = 16; o > 0; o >>= 1) my_far += __shfl_xor_sync(0xffffffffu, my_far, o);
     if (lane == 0 && my_far) atomicAdd(&sh.far, my_far);
     if (t == 0) sh.pick[0] = 0x7fffffff, sh.pick[1] = -1;
-    unsigned long long run = scan_l(mine, &part), total = part, far = sh.far;
+    u128 run = scan_w(mine, &part), total = part;
+    unsigned long long far = sh.far;
     int last = 0;  // the row's last CTA with any mass
     if (C > 1) {
       if (t == 0) sh.part = part, sh.far_part = far;
       cl.sync();
       total = far = 0;
       for (int c = 0; c < C; ++c) {
-        const unsigned long long x = *peer(&sh.part, c);
+        const u128 x = *peer(&sh.part, c);
         far += *peer(&sh.far_part, c);
         if (c < rank) run += x;
         if (x > 0) last = c;
@@ -1203,14 +1241,21 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
       }
     }
     const bool whole = exact || !sh.again;
-    const unsigned long long target = part_of(total, r.u);
+    const u128 target = part_of(total, r.u);
     // the fp32 sums' error, of what lies ahead (a) less u times the total's (a + b): at most
-    // (1 - u) |a| + u |b|, for a and b together at most far_off
-    const unsigned long long far_off = far_error(far, q.vocab), slack = exact ? 0ull : part_of(far_off, fmaxf(r.u, 1.f - r.u)) + 1024;
+    // (1 - u) |a| + u |b|, for a and b together at most far_off; and the lanes' roundings.  (Saturated:
+    // it is compared with masses of a stretch)
+    const unsigned long long far_off = far_error(far, q.vocab);
+    const unsigned long long slack =
+        exact ? 0ull : (min(part_of(far_off, fmaxf(r.u, 1.f - r.u)), 1ull << 52) << (kStretchUnit - 43)) + (1 << 16);
     for (int i = t * per; i < min(n, (t + 1) * per); ++i) {  // this CTA's first stretch past the target, and its last with any mass
       const unsigned long long x = stretch[i].mass;
       if (x > 0) {
-        if (run <= target && run + x > target) sh.pick[0] = i, sh.before = run;
+        if (run <= target && run + x > target) {
+          sh.pick[0] = i;
+          sh.before = (unsigned long long)(target - run);  // of the target in this stretch
+          sh.ties = run == 0;                              // nothing lies ahead of it
+        }
         atomicMax(&sh.pick[1], i);
       }
       run += x;
@@ -1224,7 +1269,8 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
       constexpr int kE = kWarpPart / kST;
       const int at = mine_past ? sh.pick[0] : sh.pick[1];
       const int i0 = at / kSW * kBlock + at % kSW * kWarpPart + t * kE;
-      const unsigned long long before = mine_past ? sh.before : 0ull, goal = mine_past ? target : ~0ull;
+      const unsigned long long goal = mine_past ? sh.before : ~0ull;  // masses from the stretch's start
+      const bool at_start = mine_past && sh.ties;
       float x[kE];
       unsigned eq = 0;
 #pragma unroll
@@ -1243,10 +1289,10 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
         w[e] = F2{0.f, 0.f};
         if (x[e] > -INFINITY && (k > tau || (ties && k == tau && tie++ < n_tau))) w[e] = weight(sc, x[e]);
         if (below(w[e], r.lo)) w[e] = F2{0.f, 0.f};
-        f[e] = fix<43>(w[e]);
+        f[e] = fix<kStretchUnit>(w[e]);
         sum_w += f[e];
       }
-      unsigned long long cum = before + scan_l(sum_w, &all);
+      unsigned long long cum = scan_l(sum_w, &all);
       if (t == 0) sh.pick[0] = 0x7fffffff, sh.pick[1] = -1;
       __syncthreads();
       // the first position past the target, else the last with any mass
@@ -1271,8 +1317,8 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
           if (token == i0 + e) tw = w[e];
         // sure: the fp32 sums' error moves neither border of the token past the target, nor the
         // probability's last bit
-        bool sure = exact || (whole && !mine_past) || (whole && token == hit && (from == 0 || from + slack <= target) && to > target + slack);
-        if (q.probs && !exact) sure = sure && (float)far_off <= (float)total * kProbError;
+        bool sure = exact || (whole && !mine_past) || (whole && token == hit && ((at_start && from == 0) || from + slack <= goal) && to > goal + slack);
+        if (q.probs && !exact) sure = sure && (double)far_off * 0x1p9 <= to_double(total) * (double)kProbError;
         if (sure)
           put(q, row, sl.first + token, prob_of(tw, total));
         else

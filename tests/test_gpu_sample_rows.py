@@ -1,5 +1,8 @@
 """Sampling of rows that several CTAs share, or that take the long ways through the kernel, against the
 plain 64-bit form (tests/serve_ref.py)."""
+import math
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -83,3 +86,78 @@ def test_runs_of_nan_are_no_candidates(V, rows, dtype):
     for shift in (0, 1, 3) if rows == 8 else (0,):
         take = range(16) if rows > 8 else range(8)
         check(x, u, sets[shift:] + sets[:shift], take)
+
+
+def equal_tail(c, N, p, u):
+    """(kept tail, token, distances) of a row that holds 0 and then N logits c < 0, at T = 1, exactly: the
+    distances of p and u from the borders next to them, in parts of the row's mass."""
+    w = Fraction(float(np.exp(np.float64(c))))
+    total = 1 + N * w
+    n = N
+    dp = Fraction(1)
+    if p < 1:
+        at = (Fraction(p) * total - 1) / w
+        n = max(0, min(N, math.ceil(at)))
+        dp = abs(at - round(at)) * w / total
+    kept = 1 + n * w
+    at = (Fraction(u) * kept - 1) / w
+    token = 0 if at < 0 else 1 + min(n - 1, math.floor(at))
+    return n, token, float(dp), float(abs(at - round(at)) * w / kept)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("top_k", [0, 230000])
+def test_long_prefixes_at_their_borders(top_k, dtype):
+    """One likely token and a tail of equal ones, whose number kept the token at u near 1 tells: p 2e-11 to
+    4e-10 of the mass from a border (the definition leaves 1e-11 open), which the tail's common rounding
+    must not cross."""
+    V, rows = 262144, 64
+    N = top_k - 1 if top_k else V - 1
+    rng = np.random.default_rng(7)
+    x = torch.empty(rows, V)
+    ps, us, want = [], [], []
+    for r in range(rows):
+        c = -17.0 - 0.125 * (r % 16)
+        x[r] = c
+        x[r, 0] = 0.0
+        tail = float(N * np.exp(c) / (1 + N * np.exp(c)))
+        while True:
+            p = float(np.float32(1 - tail * rng.uniform(0.2, 0.9)))
+            if 2e-11 < equal_tail(c, N, p, 0.5)[2] < 4e-10:
+                break
+        u = 1.0
+        while True:
+            u = float(np.nextafter(np.float32(u), np.float32(0)))
+            n, token, _, du = equal_tail(c, N, p, u)
+            if du > 1e-9:
+                break
+        ps.append(p), us.append(u), want.append(token)
+    from block_diffusion_drafter_forward_gb300 import sample
+    k = torch.full((rows,), top_k, dtype=torch.int32, device="cuda") if top_k else None
+    got = sample(x.to(dtype).cuda(), torch.tensor(us, device="cuda"), None, k, torch.tensor(ps, device="cuda"))
+    assert got.tolist() == want
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows", [8, 230])
+def test_u_at_the_borders_of_a_flat_tail(rows, dtype):
+    """Temperature alone over the same rows: u 2e-11 to 4e-10 of the mass from a border."""
+    V = 262144
+    rng = np.random.default_rng(8)
+    x = torch.empty(rows, V, dtype=dtype, device="cuda")
+    us, want = [], []
+    for r in range(rows):
+        c = -14.0 - 0.0625 * (r % 32)
+        x[r] = c
+        x[r, 0] = 0.0
+        tail = float((V - 1) * np.exp(c) / (1 + (V - 1) * np.exp(c)))
+        while True:
+            u = float(np.float32(1 - tail * rng.uniform(0.01, 0.99)))
+            _, token, _, du = equal_tail(c, V - 1, 1.0, u)
+            if 2e-11 < du < 4e-10:
+                break
+        us.append(u), want.append(token)
+    from block_diffusion_drafter_forward_gb300 import sample
+    u = torch.tensor(us, device="cuda")
+    assert sample(x, u).tolist() == want
+    assert sample(x, u, probs=torch.empty(rows, device="cuda"))[0].tolist() == want
