@@ -79,7 +79,7 @@ EXPORTS = ("dflash_create", "dflash_destroy", "dflash_write_ctx_kv", "dflash_pro
            "dflash_profile_kinds", "dflash_profile_read", "dflash_gemm_bf16",
            "dflash_attention_check", "dflash_gemm_bf16_noalloc", "dflash_set_persistent", "dflash_persistent",
            "dflash_propose_ex", "dflash_write_ctx_kv_batch", "dflash_fp8_layer", "dflash_extend_tables",
-           "dflash_append_kv", "dflash_attend", "dflash_attend_workspace", "dflash_sample")
+           "dflash_append_kv", "dflash_attend", "dflash_attend_workspace", "dflash_sample", "dflash_take_status")
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -142,6 +142,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dflash_attend_workspace.restype = i64
     lib.dflash_sample.argtypes = [vp, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.dflash_sample.restype = c.c_int
+    lib.dflash_take_status.argtypes = [vp, vp, vp]
+    lib.dflash_take_status.restype = c.c_int
     lib.dflash_last_error.argtypes = [vp]
     lib.dflash_last_error.restype = c.c_char_p
     _lib = lib
@@ -295,6 +297,12 @@ def dflash_extend_tables(ctx_lens: int, new_rows: int, nb: int, page_tables: int
                          row_index: int, slots: int, max_rows: int, status: int = 0, stream: int = 0) -> None:
     rc = load().dflash_extend_tables(ctx_lens, new_rows, nb, page_tables, max_pages_per_seq, free_pages, n_free, free_begin,
                                      free_end, kv_lens, row_starts, row_seq, row_index, slots, max_rows, status, stream)
+    if rc:
+        _check(rc, None)
+
+
+def dflash_take_status(status: int, flags: int, stream: int = 0) -> None:
+    rc = load().dflash_take_status(status, flags, stream)
     if rc:
         _check(rc, None)
 

@@ -255,10 +255,19 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
   }
 }
 
+__global__ void take_status_kernel(uint32_t* status, uint32_t* flags) { *flags = atomicExch(status, 0u); }
+
 }  // namespace
 }  // namespace dflash
 
 using namespace dflash;
+
+extern "C" int dflash_take_status(uint32_t* status, uint32_t* flags, dflash_stream stream) {
+  if (!status || !flags) return call_error(DFLASH_EINVAL, "take_status: null pointer");
+  take_status_kernel<<<1, 1, 0, reinterpret_cast<cudaStream_t>(stream)>>>(status, flags);
+  if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return call_error(DFLASH_ECUDA, "take_status", e);
+  return DFLASH_OK;
+}
 
 extern "C" int dflash_extend_tables(const int32_t* ctx_lens, const int32_t* new_rows, int32_t nb,
                                     int32_t* page_tables, int32_t max_pages_per_seq, const int32_t* free_pages,

@@ -51,17 +51,15 @@ def _status_word(device: torch.device) -> torch.Tensor:
 
 def serve_status(device=None, stream: Optional[torch.cuda.Stream] = None) -> int:
     """Synchronise `stream` (default: the current one), read the device's DFLASH_DEV_* bits of the
-    serving calls since the last read, and clear them."""
+    serving calls since the last read, and clear them: at once, so that a call on another stream
+    meanwhile loses none of its own."""
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     if device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
-    with torch.cuda.stream(stream or torch.cuda.current_stream(device)):
-        w = _status_word(device)
-        bits = int(w.item())
-        if bits:
-            w.bitwise_and_(~bits)  # those read, no others
-            torch.cuda.current_stream(device).synchronize()
-    return bits
+    with _on(device, stream) as st:
+        flags = torch.empty(1, dtype=_I32, device=device)
+        L.dflash_take_status(_status_word(device).data_ptr(), flags.data_ptr(), st)
+        return int(flags.item())
 
 
 def _first(t, name: str, dim: int, dtypes=(_I32,)) -> torch.Tensor:

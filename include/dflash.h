@@ -320,8 +320,14 @@ int dflash_attention_check(dflash_handle* h, int32_t layer, const int32_t* ctx_l
  * `stream` (with the buffers' device current), allocate nothing, keep nothing between calls and
  * may be captured into CUDA graphs.  On an error status nothing was launched and
  * dflash_last_error(NULL) gives the message on this thread.  `status` pointers are one uint32
- * word on the device or NULL; the kernels OR DFLASH_DEV_* bits into it and never clear it.
+ * word on the device or NULL; the kernels OR DFLASH_DEV_* bits into it and never clear it
+ * (dflash_take_status does).
  * ------------------------------------------------------------------------------------- */
+
+/* Takes the bits of a status word: *flags (device) gets them and *status becomes 0, in one atomic
+ * operation, so that no bit that another stream's kernel sets meanwhile is lost.  Asynchronous on
+ * `stream`; kernels of other streams may use the word all along. */
+int dflash_take_status(uint32_t* status, uint32_t* flags, dflash_stream stream);
 
 /* Pages of one layer's K/V cache: the tile layout of dflash_kv_layout with a head's V tile
  * directly after its K tile, i.e. element offset page * page_stride + head * 32 * head_dim

@@ -178,3 +178,8 @@ def test_plain_append_and_rows_are_inverse():
     assert torch.equal(kk, k.double()) and torch.equal(vv, v.double())
     out, lse, _, _ = R.attend(k[:4].repeat_interleave(2, 1), pool, table[None], [20], [0, 4], True, 1, 1.0)
     assert torch.allclose(out, v[16:].double().repeat_interleave(2, 1))       # a window of one: each row its own value
+
+
+def test_take_status_refuses_null(lib):
+    assert lib.dflash_take_status(None, 4096, None) == -1 and lib.dflash_take_status(4096, None, None) == -1
+    assert b"take_status" in lib.dflash_last_error(None)
