@@ -79,7 +79,7 @@ EXPORTS = ("dflash_create", "dflash_destroy", "dflash_write_ctx_kv", "dflash_pro
            "dflash_profile_kinds", "dflash_profile_read", "dflash_gemm_bf16",
            "dflash_attention_check", "dflash_gemm_bf16_noalloc", "dflash_set_persistent", "dflash_persistent",
            "dflash_propose_ex", "dflash_write_ctx_kv_batch", "dflash_fp8_layer", "dflash_extend_tables",
-           "dflash_append_kv", "dflash_attend", "dflash_attend_workspace", "dflash_sample", "dflash_take_status")
+           "dflash_append_kv", "dflash_attend", "dflash_attend_workspace", "dflash_sample", "dflash_take_status", "dflash_extend_tables_ex")
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -133,6 +133,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     i64, kv = c.c_int64, c.POINTER(dflash_kv_pages)
     lib.dflash_extend_tables.argtypes = [vp, vp, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp]
     lib.dflash_extend_tables.restype = c.c_int
+    lib.dflash_extend_tables_ex.argtypes = [vp, vp, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp]
+    lib.dflash_extend_tables_ex.restype = c.c_int
     lib.dflash_append_kv.argtypes = [kv, vp, i64, vp, i64, vp, i32, vp]
     lib.dflash_append_kv.restype = c.c_int
     lib.dflash_attend.argtypes = [kv, vp, i64, vp, i32, vp, vp, i32, i32, i32, i32, c.c_float, i32, i32, vp, i64, vp, vp,
@@ -297,6 +299,17 @@ def dflash_extend_tables(ctx_lens: int, new_rows: int, nb: int, page_tables: int
                          row_index: int, slots: int, max_rows: int, status: int = 0, stream: int = 0) -> None:
     rc = load().dflash_extend_tables(ctx_lens, new_rows, nb, page_tables, max_pages_per_seq, free_pages, n_free, free_begin,
                                      free_end, kv_lens, row_starts, row_seq, row_index, slots, max_rows, status, stream)
+    if rc:
+        _check(rc, None)
+
+
+def dflash_extend_tables_ex(ctx_lens: int, new_rows: int, nb: int, page_tables: int, max_pages_per_seq: int, free_pages: int,
+                            n_free: int, free_begin: int, free_end: int, kv_lens: int, row_starts: int, row_seq: int,
+                            row_index: int, slots: int, max_rows: int, held_pages: int = 0, status: int = 0,
+                            stream: int = 0) -> None:
+    rc = load().dflash_extend_tables_ex(ctx_lens, new_rows, nb, page_tables, max_pages_per_seq, free_pages, n_free, free_begin,
+                                        free_end, kv_lens, row_starts, row_seq, row_index, slots, max_rows, held_pages, status,
+                                        stream)
     if rc:
         _check(rc, None)
 

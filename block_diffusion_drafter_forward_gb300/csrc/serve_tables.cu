@@ -3,8 +3,8 @@
 // extend_tables: two prefix sums over the sequences (pages needed, rows added), then one thread
 // per row finds its sequence by binary search.  Bound by latency: a step of 1024 rows moves 14 KB and
 // takes 5 us on the device.
-// The scan is repeated by every CTA, so none waits for another before it maps its rows.  Lengths
-// or a stack position written in place of the inputs have to wait until every CTA has read them:
+// The scan is repeated by every CTA, so none waits for another before it maps its rows.  Lengths,
+// pages held or a stack position written in place of the inputs have to wait until every CTA has read them:
 // then the CTAs are one cluster (8 at most) with a barrier before the first CTA writes; else the
 // rows spread over as many CTAs as they fill (134 Ki rows: 5.3 against 19.4 us in a cluster of 8).
 #include <cooperative_groups.h>
@@ -26,6 +26,7 @@ constexpr int kTabMaxSeqs = 16384;
 struct TablesParams {
   const int32_t *ctx_lens, *new_rows, *free_pages, *free_begin;
   int32_t *page_tables, *free_end, *kv_lens, *row_starts, *row_seq, *row_index, *slots;
+  int32_t* held;  // pages of each sequence, or NULL: those that its rows fill
   uint32_t* status;
   int nb, mpps, n_free, max_rows;
   bool in_place;
@@ -54,7 +55,13 @@ __global__ void __launch_bounds__(kTabThreads) extend_tables_kernel(const Tables
         n = 0;
         bad = true;
       } else {
-        need = (ctx + n + kPage - 1) / kPage - (ctx + kPage - 1) / kPage;
+        const int filled = (ctx + kPage - 1) / kPage, held = p.held ? p.held[s] : filled;
+        if (held < filled || held > p.mpps) {
+          n = 0;
+          bad = true;
+        } else {
+          need = max(0, (ctx + n + kPage - 1) / kPage - held);
+        }
       }
     }
     long long r = n, g = need;  // inclusive sums: warp, then across warps
@@ -116,7 +123,7 @@ __global__ void __launch_bounds__(kTabThreads) extend_tables_kernel(const Tables
       seq = lo;
       const int ctx = s_ctx[seq];
       idx = ctx + i - s_row[seq];
-      const int pg = idx / kPage, held = (ctx + kPage - 1) / kPage;
+      const int pg = idx / kPage, held = p.held ? p.held[seq] : (ctx + kPage - 1) / kPage;
       int32_t* entry = p.page_tables + (int64_t)seq * p.mpps + pg;
       int page;
       if (pg >= held) {  // a new page: entered in the table by its first row
@@ -136,7 +143,10 @@ __global__ void __launch_bounds__(kTabThreads) extend_tables_kernel(const Tables
   if (rank == 0) {
     for (int s = t; s <= p.nb; s += kTabThreads) {
       p.row_starts[s] = s_row[s];
-      if (s < p.nb) p.kv_lens[s] = s_ctx[s] + s_row[s + 1] - s_row[s];
+      if (s == p.nb) continue;
+      const int n = s_row[s + 1] - s_row[s];
+      if (p.held && n > 0) p.held[s] = max(p.held[s], (s_ctx[s] + n + kPage - 1) / kPage);
+      p.kv_lens[s] = s_ctx[s] + n;
     }
     if (t == 0) *p.free_end = (int)begin + granted_pages;
     if (p.status && (bad || no_room)) atomicOr(p.status, (bad ? DFLASH_DEV_BAD_CTX : 0u) | (no_room ? DFLASH_DEV_NO_ROOM : 0u));
@@ -274,6 +284,15 @@ extern "C" int dflash_extend_tables(const int32_t* ctx_lens, const int32_t* new_
                                     int32_t n_free, const int32_t* free_begin, int32_t* free_end, int32_t* kv_lens,
                                     int32_t* row_starts, int32_t* row_seq, int32_t* row_index, int32_t* slots,
                                     int32_t max_rows, uint32_t* status, dflash_stream stream) {
+  return dflash_extend_tables_ex(ctx_lens, new_rows, nb, page_tables, max_pages_per_seq, free_pages, n_free, free_begin,
+                                 free_end, kv_lens, row_starts, row_seq, row_index, slots, max_rows, nullptr, status, stream);
+}
+
+extern "C" int dflash_extend_tables_ex(const int32_t* ctx_lens, const int32_t* new_rows, int32_t nb,
+                                       int32_t* page_tables, int32_t max_pages_per_seq, const int32_t* free_pages,
+                                       int32_t n_free, const int32_t* free_begin, int32_t* free_end, int32_t* kv_lens,
+                                       int32_t* row_starts, int32_t* row_seq, int32_t* row_index, int32_t* slots,
+                                       int32_t max_rows, int32_t* held_pages, uint32_t* status, dflash_stream stream) {
   if (!ctx_lens || !new_rows || !page_tables || !free_pages || !free_begin || !free_end || !kv_lens || !row_starts ||
       !row_seq || !row_index || !slots)
     return call_error(DFLASH_EINVAL, "extend_tables: null pointer");
@@ -283,7 +302,7 @@ extern "C" int dflash_extend_tables(const int32_t* ctx_lens, const int32_t* new_
   if (nb > kTabMaxSeqs) return call_error(DFLASH_ECAPACITY, "extend_tables: nb above 16384");
   if (max_rows > 1 << 30) return call_error(DFLASH_ECAPACITY, "extend_tables: max_rows above 2^30");
   TablesParams p{ctx_lens, new_rows, free_pages, free_begin, page_tables, free_end, kv_lens, row_starts,
-                 row_seq,  row_index, slots, status, nb, max_pages_per_seq, n_free, max_rows, false};
+                 row_seq,  row_index, slots, held_pages, status, nb, max_pages_per_seq, n_free, max_rows, false};
   const int smem = (3 * nb + 1) * (int)sizeof(int32_t);
   static std::atomic<unsigned long long> attr{0};
   if (cudaError_t e = smem_attr_once(extend_tables_kernel, (3 * kTabMaxSeqs + 1) * (int)sizeof(int32_t), attr); e != cudaSuccess)
@@ -291,7 +310,7 @@ extern "C" int dflash_extend_tables(const int32_t* ctx_lens, const int32_t* new_
   cudaLaunchConfig_t c = {};
   cudaLaunchAttribute a[1];
   auto overlap = [](const int32_t* a, int64_t n, const int32_t* b, int64_t m) { return a < b + m && b < a + n; };
-  p.in_place = free_end == free_begin || overlap(kv_lens, nb, ctx_lens, nb);
+  p.in_place = held_pages || free_end == free_begin || overlap(kv_lens, nb, ctx_lens, nb);
   int sms = 0;
   if (cudaError_t e = sm_count(&sms); e != cudaSuccess) return call_error(DFLASH_ECUDA, "extend_tables", e);
   const int fill = std::max(1, (max_rows + kTabThreads - 1) / kTabThreads);

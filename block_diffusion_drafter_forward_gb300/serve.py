@@ -175,11 +175,16 @@ def _on(device: torch.device, stream: Optional[torch.cuda.Stream]):
 
 
 def extend_tables(ctx_lens: torch.Tensor, new_rows: torch.Tensor, page_tables: torch.Tensor, free_pages: torch.Tensor,
-                  free_begin: torch.Tensor, max_rows: int, out: Optional[RowPlan] = None, stream=None) -> RowPlan:
+                  free_begin: torch.Tensor, max_rows: int, out: Optional[RowPlan] = None, stream=None,
+                  held_pages: Optional[torch.Tensor] = None) -> RowPlan:
     """Pages for the new rows of a batch and every new row's place.  ctx_lens, new_rows [nb];
     page_tables [nb, max_pages_per_seq], extended in place; free_pages [n] a stack of page ids taken
     from position free_begin [1] on.  Sequences are served in order while pages and max_rows last.
-    `out`: a RowPlan to write into; its kv_lens may be ctx_lens and its free_end free_begin."""
+    `out`: a RowPlan to write into; its kv_lens may be ctx_lens and its free_end free_begin.
+    `held_pages` [nb]: pages that each sequence has in its table, brought up to date in place; for
+    sequences whose ctx_lens may go back (rejected rows), so that pages given for those rows are used
+    again.  Without it a sequence holds the pages that its ctx_lens rows fill, and entries behind them
+    are overwritten."""
     try:  # sizes first; _addresses holds every tensor to them
         dev, nb = ctx_lens.device, ctx_lens.shape[0]
         mpps, n_free = page_tables.shape[1], free_pages.shape[0]
@@ -204,9 +209,10 @@ def extend_tables(ctx_lens: torch.Tensor, new_rows: torch.Tensor, page_tables: t
             (free_begin, "free_begin", _I32, one), (free_end, "out.free_end", _I32, one),
             (kv_lens, "out.kv_lens", _I32, seqs), (row_starts, "out.row_starts", _I32, (nb + 1,)),
             (row_seq, "out.row_seq", _I32, rows), (row_index, "out.row_index", _I32, rows), (slots, "out.slots", _I32, rows))
+        a_held = 0 if held_pages is None else _addresses(dev, (held_pages, "held_pages", _I32, seqs))[0]
         # an empty tensor has no address, and the entry takes none that is null
-        L.dflash_extend_tables(a_ctx, a_new, nb, a_pt, mpps, a_free or a_pt, n_free, a_begin, a_end, a_kv, a_rs, a_seq or a_pt,
-                               a_idx or a_pt, a_slots or a_pt, max_rows, _status_word(dev).data_ptr(), st)
+        L.dflash_extend_tables_ex(a_ctx, a_new, nb, a_pt, mpps, a_free or a_pt, n_free, a_begin, a_end, a_kv, a_rs, a_seq or a_pt,
+                                  a_idx or a_pt, a_slots or a_pt, max_rows, a_held, _status_word(dev).data_ptr(), st)
     return out
 
 

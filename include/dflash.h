@@ -359,12 +359,28 @@ typedef struct {
  * Sequences are served in order: from the first whose pages or rows do not fit in n_free or
  * max_rows on, none gets rows (DFLASH_DEV_NO_ROOM).  A sequence with a negative length or more
  * than 16 * max_pages_per_seq rows gets none (DFLASH_DEV_BAD_CTX), the others are served.
- * 1 <= nb <= 16384 (ECAPACITY).  No other outputs may overlap inputs or each other. */
+ * 1 <= nb <= 16384 (ECAPACITY).  No other outputs may overlap inputs or each other.
+ * Here a sequence holds ceil(ctx_lens[s] / 16) pages.  One that goes back (rows of a verified block
+ * rejected: the next ctx_lens[s] is below the last kv_lens[s]) may hold more, whose table entries this
+ * call would overwrite with fresh pages: dflash_extend_tables_ex takes only what is missing.  Pages of a
+ * sequence that ends go back by the caller: k ids written to free_pages[*free_begin - k ..], *free_begin
+ * lowered by k. */
 int dflash_extend_tables(const int32_t* ctx_lens, const int32_t* new_rows, int32_t nb, int32_t* page_tables,
                          int32_t max_pages_per_seq, const int32_t* free_pages, int32_t n_free,
                          const int32_t* free_begin, int32_t* free_end, int32_t* kv_lens, int32_t* row_starts,
                          int32_t* row_seq, int32_t* row_index, int32_t* slots, int32_t max_rows, uint32_t* status,
                          dflash_stream stream);
+
+/* dflash_extend_tables with the pages held given: held_pages [nb] (NULL: as dflash_extend_tables), in and
+ * out, overlapping nothing else.  Sequence s has held_pages[s] pages, the first entries of its row of
+ * page_tables, and takes max(0, ceil((ctx + new) / 16) - held_pages[s]) more; held_pages[s] becomes what it
+ * has then.  A value outside [ceil(ctx_lens[s] / 16), max_pages_per_seq] gives the sequence no rows
+ * (DFLASH_DEV_BAD_CTX).  A caller starts with 0 for a new sequence and passes the array again at each step. */
+int dflash_extend_tables_ex(const int32_t* ctx_lens, const int32_t* new_rows, int32_t nb, int32_t* page_tables,
+                            int32_t max_pages_per_seq, const int32_t* free_pages, int32_t n_free,
+                            const int32_t* free_begin, int32_t* free_end, int32_t* kv_lens, int32_t* row_starts,
+                            int32_t* row_seq, int32_t* row_index, int32_t* slots, int32_t max_rows,
+                            int32_t* held_pages, uint32_t* status, dflash_stream stream);
 
 /* Copies K and V rows into the pages: row i of k and v [n, n_kv_heads, head_dim] (pages' dtype,
  * heads contiguous, `k_stride` / `v_stride` elements between rows) goes to slot slots[i].

@@ -183,3 +183,10 @@ def test_plain_append_and_rows_are_inverse():
 def test_take_status_refuses_null(lib):
     assert lib.dflash_take_status(None, 4096, None) == -1 and lib.dflash_take_status(4096, None, None) == -1
     assert b"take_status" in lib.dflash_last_error(None)
+
+
+@pytest.mark.parametrize("kw,code", [(dict(ctx=None), -1), (dict(slots=None), -1), (dict(nb=0), -1), (dict(nb=16385), -4), (dict(mpps=0), -1)])
+def test_tables_with_pages_held_refuse(lib, kw, code):
+    a = tables_args(**kw)
+    assert lib.dflash_extend_tables_ex(*a[:-2], 4096, *a[-2:]) == code
+    assert b"extend_tables" in lib.dflash_last_error(None)
