@@ -22,6 +22,14 @@ template <int HD>
 __global__ void __launch_bounds__(128) attend_simple_kernel(const AttendParams p) {
   __shared__ float s_q[4][HD];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && p.status) {  // every sequence is checked, also those that no row leads to
+    for (int s = threadIdx.x; s < p.nb; s += blockDim.x) {
+      int r0, n, kv;
+      bool bad;
+      seq_of(p, s, &r0, &n, &kv, &bad);
+      if (bad) atomicOr(p.status, DFLASH_DEV_BAD_CTX);
+    }
+  }
   const int64_t x = (int64_t)blockIdx.x * 4 + warp;
   const int i = (int)(x / p.nh), h = (int)(x % p.nh), g = h / (p.nh / p.nkv);
   if (i >= p.n_rows) return;
@@ -34,7 +42,6 @@ __global__ void __launch_bounds__(128) attend_simple_kernel(const AttendParams p
   int r0, n, kv;
   bool bad;
   const bool rows = seq_of(p, s, &r0, &n, &kv, &bad);
-  if (bad && p.status && lane == 0) atomicOr(p.status, DFLASH_DEV_BAD_CTX);
   if (!rows || i < r0 || i >= r0 + n) return;
   const float* q = static_cast<const float*>(p.q) + i * p.q_stride + h * HD;
 #pragma unroll

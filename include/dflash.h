@@ -401,7 +401,8 @@ int dflash_append_kv(const dflash_kv_pages* kv, const void* k, int64_t k_stride,
  * out and lse overlap no input.  1 <= nb <= 16384 and n_rows <= 2^30 (ECAPACITY), max_pages_per_seq
  * < 2^26.  Rows of out and lse outside every sequence's range are left as they are.  row_starts never
  * falls and stays in [0, n_rows], kv_lens in [0, 16 * max_pages_per_seq]: a sequence that breaks
- * this is skipped (its rows are left as they are) and sets DFLASH_DEV_BAD_CTX.  A page id outside
+ * this is skipped (its rows are left as they are) and sets DFLASH_DEV_BAD_CTX; sequences whose rows lie
+ * ahead of an earlier one's (row_starts that fell) may be skipped with it.  A page id outside
  * [0, num_pages) is read as page 0 and sets DFLASH_DEV_BAD_PAGE.  Page rows from kv_lens on are
  * not used, whatever they hold; those below it must be finite where any row's mask hides them (a
  * weight of zero times a NaN or infinite V is NaN).  max_new is a host hint of the longest chunk (it

@@ -188,3 +188,21 @@ def test_a_block_verified_twice_in_a_graph():
             keys[s], vals[s] = (torch.cat([old[s], fresh[at][:stay[s]]]) for old, fresh in ((keys, k), (vals, v)))
             lens[s] += stay[s]
     assert status() == 0 and int(pos) == int(held.sum()) <= nb * cap
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("kv_lens,starts", [
+    ([20, -1, 30], [0, 2, 2, 5]),          # a negative length, of a sequence without rows
+    ([20, 1000, 30], [0, 2, 2, 5]),        # and one past its table
+    ([20, 16, 30], [0, 2, 9, 9]),          # rows past q, of which the first five have a sequence of their own
+    ([20, 16, 30], [3, 5, 1, 3]),          # starts that fall: the second has none, the third has rows 1 and 2
+])
+def test_every_sequence_out_of_range_is_reported(kv_lens, starts, dtype):
+    from block_diffusion_drafter_forward_gb300 import PagedKV, _lib
+    status()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    kv = PagedKV(torch.randn(9, 1, 2, PAGE * 64, generator=g, device="cuda").to(dtype))
+    q = torch.randn(5, 2, 64, generator=g, device="cuda").to(dtype)
+    table = torch.arange(9, dtype=torch.int32, device="cuda").view(3, 3)
+    kv.attend(q, table, i32(kv_lens), i32(starts), 3)
+    assert status() == _lib.DFLASH_DEV_BAD_CTX
