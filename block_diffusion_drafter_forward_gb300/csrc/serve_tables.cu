@@ -132,7 +132,8 @@ __global__ void __launch_bounds__(kTabThreads) extend_tables_kernel(const Tables
       } else {
         page = *entry;
       }
-      slot = page >= 0 && page < (1 << 27) ? page * kPage + idx % kPage : -1;
+      if (page >= 0 && page < (1 << 27)) slot = page * kPage + idx % kPage;
+      else if (p.status) atomicOr(p.status, DFLASH_DEV_BAD_PAGE);
     }
     p.row_seq[i] = seq;
     p.row_index[i] = idx;

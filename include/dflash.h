@@ -358,7 +358,8 @@ typedef struct {
  *   free_end   [1]      *free_begin + pages taken (may be free_begin itself)
  * Sequences are served in order: from the first whose pages or rows do not fit in n_free or
  * max_rows on, none gets rows (DFLASH_DEV_NO_ROOM).  A sequence with a negative length or more
- * than 16 * max_pages_per_seq rows gets none (DFLASH_DEV_BAD_CTX), the others are served.
+ * than 16 * max_pages_per_seq rows gets none (DFLASH_DEV_BAD_CTX), the others are served.  A row whose
+ * page id is negative or at least 2^27 has slot -1 (DFLASH_DEV_BAD_PAGE).
  * 1 <= nb <= 16384 (ECAPACITY).  No other outputs may overlap inputs or each other.
  * Here a sequence holds ceil(ctx_lens[s] / 16) pages.  One that goes back (rows of a verified block
  * rejected: the next ctx_lens[s] is below the last kv_lens[s]) may hold more, whose table entries this

@@ -206,3 +206,17 @@ def test_every_sequence_out_of_range_is_reported(kv_lens, starts, dtype):
     table = torch.arange(9, dtype=torch.int32, device="cuda").view(3, 3)
     kv.attend(q, table, i32(kv_lens), i32(starts), 3)
     assert status() == _lib.DFLASH_DEV_BAD_CTX
+
+
+def test_rows_on_pages_that_are_none_are_reported():
+    """A table entry, or an id on the stack, that is no page: its rows have no slot, and a status bit says so."""
+    from block_diffusion_drafter_forward_gb300 import _lib, extend_tables
+    status()
+    for table, free, slots in (([[-7, -1], [3, -1]], [4, 5], [-1, -1, 3 * PAGE + 5, 3 * PAGE + 6]), ([[2 ** 27, 0], [3, 0]], [4, 5], [-1, -1, 53, 54]),
+                               ([[1, -1], [3, -1]], [-2, 5], [21, 22, 53, 54])):
+        t = i32(table)
+        plan = extend_tables(i32([5, 5]), i32([2, 2]), t, i32(free), i32([0]), 4)
+        assert plan.slots.tolist() == slots and plan.row_index.tolist() == [5, 6, 5, 6] and t.tolist() == table
+        assert status() == (_lib.DFLASH_DEV_BAD_PAGE if -1 in slots else 0)
+    plan = extend_tables(i32([15]), i32([2]), i32([[1, -1]]), i32([-2]), i32([0]), 2)
+    assert plan.slots.tolist() == [31, -1] and status() == _lib.DFLASH_DEV_BAD_PAGE
