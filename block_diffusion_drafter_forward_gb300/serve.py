@@ -94,6 +94,11 @@ def _i32(n: int, name: str) -> int:
     return n
 
 
+def _limit(n) -> int:
+    """A limit for the library: beyond 32 bits as good as the largest, below zero refused there."""
+    return max(-1, min(int(n), _INT_MAX))
+
+
 def _addresses(device: torch.device, *wanted) -> list:
     """The addresses of contiguous tensors on `device`, given as (tensor, name, dtype, shape); raises for
     the first that is something else.  (A loop of plain comparisons: the smallest calls cost little more.)"""
@@ -211,7 +216,8 @@ def extend_tables(ctx_lens: torch.Tensor, new_rows: torch.Tensor, page_tables: t
             (row_seq, "out.row_seq", _I32, rows), (row_index, "out.row_index", _I32, rows), (slots, "out.slots", _I32, rows))
         a_held = 0 if held_pages is None else _addresses(dev, (held_pages, "held_pages", _I32, seqs))[0]
         # an empty tensor has no address, and the entry takes none that is null
-        L.dflash_extend_tables_ex(a_ctx, a_new, nb, a_pt, mpps, a_free or a_pt, n_free, a_begin, a_end, a_kv, a_rs, a_seq or a_pt,
+        L.dflash_extend_tables_ex(a_ctx, a_new, _i32(nb, "sequences"), a_pt, _i32(mpps, "pages of a sequence"), a_free or a_pt,
+                                  _i32(n_free, "free pages"), a_begin, a_end, a_kv, a_rs, a_seq or a_pt,
                                   a_idx or a_pt, a_slots or a_pt, max_rows, a_held, _status_word(dev).data_ptr(), st)
     return out
 
@@ -293,8 +299,9 @@ class PagedKV:
             if need is None:
                 need = self._workspace = L.dflash_attend_workspace(self._c)
             ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-            L.dflash_attend(self._c, a_q, qs, a_pt, mpps, a_kv, a_rs, nb, _i32(n, "rows"), min(int(max_new), _INT_MAX), nh,
-                            1.0 / math.sqrt(hd) if scale is None else float(scale), min(int(window), _INT_MAX), 1 if causal else 0,
+            L.dflash_attend(self._c, a_q, qs, a_pt, _i32(mpps, "pages of a sequence"), a_kv, a_rs, _i32(nb, "sequences"),
+                            _i32(n, "rows"), _limit(max_new), nh,
+                            1.0 / math.sqrt(hd) if scale is None else float(scale), _limit(window), 1 if causal else 0,
                             a_out, os_, a_lse, ws.data_ptr() if need else 0, need, st)
         return out if lse is None else (out, lse)
 
@@ -326,7 +333,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Te
             tokens = torch.empty(rows, dtype=_I32, device=dev)
             at["tokens"] = tokens.data_ptr()
         get = at.get
-        L.dflash_sample(logits.data_ptr(), st0 if rows > 1 else V, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32, _i32(rows, "rows"), V,
-                        at["u"], get("temperature", 0), get("top_k", 0), get("top_p", 0), get("min_p", 0), at["tokens"],
+        L.dflash_sample(logits.data_ptr(), st0 if rows > 1 else V, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32, _i32(rows, "rows"),
+                        _i32(V, "logits of a row"), at["u"], get("temperature", 0), get("top_k", 0), get("top_p", 0), get("min_p", 0), at["tokens"],
                         get("probs", 0), st)
     return tokens if probs is None else (tokens, probs)

@@ -220,3 +220,15 @@ def test_rows_on_pages_that_are_none_are_reported():
         assert status() == (_lib.DFLASH_DEV_BAD_PAGE if -1 in slots else 0)
     plan = extend_tables(i32([15]), i32([2]), i32([[1, -1]]), i32([-2]), i32([0]), 2)
     assert plan.slots.tolist() == [31, -1] and status() == _lib.DFLASH_DEV_BAD_PAGE
+
+
+def test_sizes_and_hints_that_32_bits_would_cut_are_refused():
+    from block_diffusion_drafter_forward_gb300 import DflashError, PagedKV, sample
+    kv = PagedKV(torch.zeros(2, 1, 2, PAGE * 64, device="cuda"))
+    q, table = torch.zeros(1, 1, 64, device="cuda"), i32([[0, 1]])
+    for kw in (dict(window=-2 ** 32), dict(window=-2 ** 32 + 7), dict(max_new=-2 ** 32), dict(max_new=-1)):
+        with pytest.raises(DflashError, match="attend"):
+            kv.attend(q, table, i32([1]), i32([0, 1]), **{"max_new": 1, **kw})
+    long = torch.empty(1, 2 ** 32 + 5, dtype=torch.bfloat16, device="cuda")  # never read
+    with pytest.raises(ValueError, match="logits of a row: 4294967301 are too many"):
+        sample(long, torch.zeros(1, device="cuda"))

@@ -190,3 +190,12 @@ def test_tables_with_pages_held_refuse(lib, kw, code):
     a = tables_args(**kw)
     assert lib.dflash_extend_tables_ex(*a[:-2], 4096, *a[-2:]) == code
     assert b"extend_tables" in lib.dflash_last_error(None)
+
+
+def test_sizes_beyond_32_bits_are_refused_or_limited():
+    from block_diffusion_drafter_forward_gb300.serve import _i32, _limit
+    assert [_limit(n) for n in (5, 0, 2 ** 31 - 1, 2 ** 31, 2 ** 40)] == [5, 0] + [2 ** 31 - 1] * 3
+    assert [_limit(n) for n in (-1, -2 ** 31 - 1, -2 ** 32, -2 ** 32 + 7)] == [-1] * 4  # (cut to 32 bits: 0 and 7 among them)
+    assert _i32(2 ** 31 - 1, "rows") == 2 ** 31 - 1
+    with pytest.raises(ValueError, match="rows: 4294967301 are too many"):
+        _i32(2 ** 32 + 5, "rows")
