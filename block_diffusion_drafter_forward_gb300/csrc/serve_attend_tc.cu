@@ -1009,8 +1009,10 @@ cudaError_t launch_attend_tc(const AttendParams& p, int head_dim, int max_new, v
   const int T = p.tokens;
   // Chunks longer than one tile: two tiles share every K/V slot, where there are units enough for the
   // SMs.  Measured (32 query heads on 4, one tile / two): 32 sequences x 17 tokens on 4096 rows
-  // 109 / 93 us, x 64 199 / 163 us, 8 x 256 on 2048 113 / 102 us, 64 x 20 on 500 62 / 49 us; with few
-  // units the split finer in queries wins: 4 x 32 on 8192 36 / 60 us, 1 x 32 on 30000 49 / 54 us.
+  // 111 / 92 us, x 64 197 / 156 us, 8 x 256 on 2048 117 / 100 us, 64 x 20 on 500 66 / 51 us; with few
+  // units the split finer in queries wins: 4 x 32 on 8192 43 / 66 us, 1 x 32 on 30000 55 / 61 us.  The
+  // same way round with heads of 64, with 64 on 8 and under a window; 8 on 8 lose 4 of 51 us by it
+  // (8 x 256 on 2048).
   const bool two = max_new > T && ((int64_t)p.n_rows + T - 1) / T * p.nkv * 2 >= sms;
   w.long_chunks = max_new > 4 * (two ? 2 * T : T);
   if (head_dim == 128) return two ? launch<128, 2>(p, w, sms, st) : launch<128, 1>(p, w, sms, st);

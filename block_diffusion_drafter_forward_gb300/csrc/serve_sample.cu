@@ -14,14 +14,14 @@
 //     where the token could depend on it, or the probability's last bit (flat rows; a few in a
 //     thousand others), the row is streamed once more with exact weights.
 //   - rows whose prefix is longer than the list are streamed again (from L2, mostly): histograms
-//     over the logits' order-preserving keys, 10 bits a pass, with exact counts (top-k) and masses
+//     over the logits' order-preserving keys, 9 bits a pass, with exact counts (top-k) and masses
 //     (top-p), find (tau, n): the lowest kept logit, and how many of those equal to it stay; then
 //     stretches of the kept weights are summed as above.
 // Bound by HBM: one read of the logits (the finishing phases of some CTAs overlap the streaming of
 // others; three CTAs per SM with 32 KB of copies in flight each).  Measured, rows of 151936 bf16: 1024
-// rows greedy 53 us (5.9 TB/s), min-p 75, top-k 50 85, top-p 0.95 130, temperature alone 229, of
-// mixed settings 126 (210 where a row is streamed again: one call in six); flat ones (top-p 0.99 at
-// temperature 1.2: prefixes of many thousands) 2.3 ms; one row 21 us, of which most is latency.
+// rows greedy 53 us (5.9 TB/s), min-p 85, top-k 50 96, top-p 0.95 134, temperature alone 233, of
+// mixed settings 122 (210 where a row is streamed again: one call in six); flat ones (top-p 0.99 at
+// temperature 1.2: prefixes of many thousands) 2.06 ms; one row 23 us, of which most is latency.
 //
 // The token is a whole number that a sum's last bit can change, so weights are pairs of floats
 // (exp2 by a 128-entry table and a short polynomial on the compensated argument, about 2^-41)
