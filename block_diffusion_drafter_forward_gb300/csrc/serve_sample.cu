@@ -1310,6 +1310,10 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
       if (any >= 0) atomicMax(&sh.pick[1], any);
       __syncthreads();
       const int token = sh.pick[0] != 0x7fffffff ? sh.pick[0] : sh.pick[1];
+      // Nothing here counts: the fp32 sums, by the maximum as it was then, had weights in the stretch that
+      // are below 2^-40 by the row's.
+      if (token < 0 && t == 0)
+        for (int c = 0; c < C; ++c) *peer(&sh.again, c) = 1;
       if (token >= i0 && token < i0 + kE) {
         F2 tw = w[0];
 #pragma unroll

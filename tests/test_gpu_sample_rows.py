@@ -161,3 +161,32 @@ def test_u_at_the_borders_of_a_flat_tail(rows, dtype):
     u = torch.tensor(us, device="cuda")
     assert sample(x, u).tolist() == want
     assert sample(x, u, probs=torch.empty(rows, device="cuda"))[0].tolist() == want
+
+
+def late_maximum(V, dtype, a, b, mid=0):
+    """Rows whose maximum (1) comes late: against the maximum until then (0, at 5000) the body's weights are
+    above 2^-40, against the row's they are below and count as 0.  a, b: the two logits behind the maximum."""
+    x = torch.full((len(a), V), -27.0)
+    if mid:
+        x[:, 7:V - 4000:V // mid] = -12.0
+    x[:, 5000] = 0.0
+    at = [V - 2712, V - 1644, V - 644]
+    x[:, at[0]], x[:, at[1]], x[:, at[2]] = 1.0, torch.tensor(a).float(), torch.tensor(b).float()
+    return x.to(dtype).cuda(), at
+
+
+@pytest.mark.parametrize("rows", [8, 230])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_every_row_has_a_token_at_the_ends_of_u(rows, dtype):
+    """u = 0 and u = 1: the first and the last logit that counts, where whole stretches ahead and behind count
+    as 0 only since the row's maximum is known."""
+    from block_diffusion_drafter_forward_gb300 import sample
+    x, at = late_maximum(262144, dtype, [0.25] * rows, [-0.5] * rows)
+    for u, want in ((0.0, 5000), (1.0, at[2])):
+        tokens = torch.full((rows,), -7, dtype=torch.int32, device="cuda")
+        probs = torch.full((rows,), -7.0, device="cuda")
+        us = torch.full((rows,), u, device="cuda")
+        assert sample(x, us, tokens=tokens).tolist() == [want] * rows
+        tokens.fill_(-7)
+        sample(x, us, tokens=tokens, probs=probs)
+        assert tokens.tolist() == [want] * rows and bool((probs > 0).all())
