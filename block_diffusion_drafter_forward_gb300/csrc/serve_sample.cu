@@ -175,7 +175,7 @@ __device__ __forceinline__ F2 weight(const Scale& s, float x) {
   return {hh * sc, (lo - (hh - h)) * sc};
 }
 
-// 16 bytes of logits: their largest (NaN counts as nothing), and the values.
+// 16 bytes of logits: their largest and smallest (NaN counts as nothing), and the values.
 template <typename T>
 struct Vec;
 template <>
@@ -187,6 +187,12 @@ struct Vec<__nv_bfloat16> {
     const __nv_bfloat162 b = __hmax2(reinterpret_cast<const __nv_bfloat162&>(r.z), reinterpret_cast<const __nv_bfloat162&>(r.w));
     const __nv_bfloat162 m = __hmax2(a, b);
     return fmaxf(__low2float(m), __high2float(m));
+  }
+  __device__ static float low(const uint4& r) {
+    const __nv_bfloat162 a = __hmin2(reinterpret_cast<const __nv_bfloat162&>(r.x), reinterpret_cast<const __nv_bfloat162&>(r.y));
+    const __nv_bfloat162 b = __hmin2(reinterpret_cast<const __nv_bfloat162&>(r.z), reinterpret_cast<const __nv_bfloat162&>(r.w));
+    const __nv_bfloat162 m = __hmin2(a, b);
+    return fminf(__low2float(m), __high2float(m));
   }
   __device__ static void get(const uint4& r, float (&v)[8]) {
     const unsigned w[4] = {r.x, r.y, r.z, r.w};
@@ -203,6 +209,9 @@ struct Vec<float> {
   static constexpr unsigned kPad = 0xff800000u;
   __device__ static float top(const uint4& r) {
     return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+  }
+  __device__ static float low(const uint4& r) {
+    return fminf(fminf(__uint_as_float(r.x), __uint_as_float(r.y)), fminf(__uint_as_float(r.z), __uint_as_float(r.w)));
   }
   __device__ static void get(const uint4& r, float (&v)[4]) {
     v[0] = __uint_as_float(r.x), v[1] = __uint_as_float(r.y), v[2] = __uint_as_float(r.z), v[3] = __uint_as_float(r.w);
@@ -337,6 +346,9 @@ constexpr int kDigit = 9, kKeys = 1 << kDigit, kParts = 5, kPartBits = 12;
 // the error a probability may carry
 constexpr float kNear = 12.f;
 constexpr float kFastError = 1.4e-6f, kFastTail = 2.2e-8f, kProbError = 8e-8f;
+// Beside that bound: a far mass is taken against the largest logit met until then, so it may hold weights
+// that the row's maximum puts below 2^-40, where they count as 0: up to 2^-40 each.  (The probability's
+// last bit is not held to that: a row of a thousand such weights is 1e-9 off.)
 // The bound for a mass in units of 2^-43, of a row of `vocab` logits
 __device__ __forceinline__ unsigned long long far_error(unsigned long long far, int vocab) {
   return part_of(far, kFastError) + part_of((unsigned long long)vocab << 23, kFastTail);
@@ -351,7 +363,7 @@ constexpr int kStreamSmem = kStages * kStageBytes + kSideBytes;
 
 struct Stretch {  // mass of a warp's part of a block (2^-52: 1024 weights at most), relative to ref
   unsigned long long mass;
-  unsigned ties;  // logits equal to tau ahead of it
+  unsigned ties;  // logits equal to tau ahead of it; of fp32 sums: the key of the smallest logit summed
   float ref;
 };
 
@@ -362,7 +374,8 @@ struct Shared {
   unsigned long long red_l[kSW], rest, best, before, far, far_part;
   u128 part, above;
   unsigned red_u[kSW], ties;
-  unsigned m_key, n_list, n_final, full, again;
+  unsigned m_key, n_list, n_final, full, again, cut;
+  float m_look;
   float floor, floors[kSW];
   int pick[2];
 };
@@ -436,7 +449,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
   if (t < kBins) sh.count[t] = 0, sh.mass[t] = 0;
   if (t == 0) {
     sh.m_key = 0;
-    sh.n_list = sh.n_final = sh.full = sh.again = 0;
+    sh.n_list = sh.n_final = sh.full = sh.again = sh.cut = 0;
     sh.rest = sh.best = sh.far = 0;
     sh.pick[0] = 0x7fffffff;
     sh.pick[1] = -1;
@@ -461,6 +474,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
   sync_row();
   float m = of_key(sh.m_key);  // this warp's maximum so far
   for (int c = 0; c < C; ++c) m = fmaxf(m, of_key(*peer(&sh.m_key, c)));
+  if (t == 0) sh.m_look = m;
   Scale sc = scale_of(m, r.T, sh.table);  // (T == 0: not used)
   // rows by list: a short prefix by right
   const bool greedy = r.T == 0.f;
@@ -652,7 +666,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
       }
       return;
     }
-    float far = 0.f;
+    float far = 0.f, low = INFINITY;
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
       if (!(tops[v] >= cut_x)) continue;
@@ -661,12 +675,14 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
         if (at < near_room) near_places[at] = pos_of(b, v);
       } else {
         far += fast(x4[v]);
+        low = fminf(low, Vec<T>::low(x4[v]));
       }
     }
     unsigned long long mass = fix<kStretchUnit>(F2{far, 0.f});
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
-    if (lane == 0) stretch[b * kSW + warp] = Stretch{mass, 0u, m};
+    const unsigned low_key = __reduce_min_sync(0xffffffffu, key_of(low));
+    if (lane == 0) stretch[b * kSW + warp] = Stretch{mass, low_key, m};
   };
   bool looked = false;  // the floor is a look's
   if (by_list && !floor_by_rank()) looked = true, floor_by_look();
@@ -857,8 +873,10 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     // the kept prefix: its length and mass
     unsigned long long run = before, kept_w = 0;
     int n_kept = 0;
-    // the goal's error: the fp32 weights', and the roundings of the parts (2^-44 a warp)
-    const unsigned long long slack = sum && sh.rest ? (exact_rest ? 0ull : far_error(sh.rest, q.vocab) << 9) + (1ull << 15) : 0ull;
+    // the goal's error: the fp32 weights', those below the cut, and the roundings of the parts (2^-44 a warp)
+    unsigned long long slack = sum && sh.rest ? 1ull << 15 : 0ull;
+    if (slack && !exact_rest)
+      slack += (far_error(sh.rest, q.vocab) << 9) + (sh.m_look < m_row ? (unsigned long long)q.vocab << 12 : 0ull);
     bool unsure = false;
     for (int e = 0; e < per && i0 + e < k_end; ++e) {
       const unsigned long long w = list[i0 + e];
@@ -989,6 +1007,7 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
       if (t == 0) {
         sh.n_list = sh.n_final = sh.full = 0;
         sh.rest = 0;
+        sh.m_look = m_row;
         sh.pick[0] = 0x7fffffff;
         sh.pick[1] = -1;
       }
@@ -1195,11 +1214,13 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     const int n = blocks * kSW, per = (n + kST - 1) / kST;
     u128 mine = 0, part;
     unsigned long long my_far = 0;  // (2^-43)
+    unsigned my_cut = 0;            // logits of stretches that hold weights below the cut
     if (!exact) {
       // by the row's maximum now, and the near vectors exactly
       for (int i = t; i < n; i += kST) {
         Stretch& s = stretch[i];
         if (s.ref != m_row) {
+          if (t_of(sc, of_key(s.ties)) > kCut - 0.01f) my_cut += kWarpPart;
           const float h = (float)s.mass, l = (float)(long long)(s.mass - (unsigned long long)h);
           s.mass = s.ref > -INFINITY ? fix<0>(mul(F2{h, l}, weight(sc, s.ref))) : 0ull;  // (in the same units)
         }
@@ -1224,17 +1245,20 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) my_far += __shfl_xor_sync(0xffffffffu, my_far, o);
     if (lane == 0 && my_far) atomicAdd(&sh.far, my_far);
+    if (my_cut) atomicAdd(&sh.cut, my_cut);
     if (t == 0) sh.pick[0] = 0x7fffffff, sh.pick[1] = -1;
     u128 run = scan_w(mine, &part), total = part;
     unsigned long long far = sh.far;
+    unsigned cut = sh.cut;
     int last = 0;  // the row's last CTA with any mass
     if (C > 1) {
       if (t == 0) sh.part = part, sh.far_part = far;
       cl.sync();
-      total = far = 0;
+      total = far = cut = 0;
       for (int c = 0; c < C; ++c) {
         const u128 x = *peer(&sh.part, c);
         far += *peer(&sh.far_part, c);
+        cut += *peer(&sh.cut, c);
         if (c < rank) run += x;
         if (x > 0) last = c;
         total += x;
@@ -1243,11 +1267,12 @@ __global__ void __launch_bounds__(kST, 3) sample_kernel(const SampleParams q) {
     const bool whole = exact || !sh.again;
     const u128 target = part_of(total, r.u);
     // the fp32 sums' error, of what lies ahead (a) less u times the total's (a + b): at most
-    // (1 - u) |a| + u |b|, for a and b together at most far_off; and the lanes' roundings.  (Saturated:
-    // it is compared with masses of a stretch)
+    // (1 - u) |a| + u |b|, for a and b together at most far_off; the weights below the cut, and the lanes'
+    // roundings.  (Saturated: it is compared with masses of a stretch)
     const unsigned long long far_off = far_error(far, q.vocab);
     const unsigned long long slack =
-        exact ? 0ull : (min(part_of(far_off, fmaxf(r.u, 1.f - r.u)), 1ull << 52) << (kStretchUnit - 43)) + (1 << 16);
+        exact ? 0ull : (min(part_of(far_off, fmaxf(r.u, 1.f - r.u)), 1ull << 52) << (kStretchUnit - 43)) +
+                           ((unsigned long long)cut << (kStretchUnit - (int)kCut)) + (1 << 16);
     for (int i = t * per; i < min(n, (t + 1) * per); ++i) {  // this CTA's first stretch past the target, and its last with any mass
       const unsigned long long x = stretch[i].mass;
       if (x > 0) {

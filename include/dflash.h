@@ -425,7 +425,7 @@ int64_t dflash_attend_workspace(const dflash_kv_pages* kv);
  * DFLASH_BF16 or DFLASH_F32), drawn from the uniform numbers u [rows] in [0, 1).  temperature,
  * top_k, top_p, min_p: device arrays [rows] or NULL (1, off, off, off).  Row r with logits x_i,
  * largest m, T = temperature:
- *   w_i = exp((x_i - m) / T), taken as 0 where it is below 2^-40;
+ *   w_i = exp((x_i - m) / T), taken as 0 where it is below 2^-40 (within a part in 10^5 of that: either);
  *   top-k (k > 0): the k largest x stay, equal ones by lowest index;
  *   top-p (p < 1): in falling order (equal ones by index) those stay before which less than p of
  *     the mass left by top-k lies; the first always stays;

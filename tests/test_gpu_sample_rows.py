@@ -190,3 +190,41 @@ def test_every_row_has_a_token_at_the_ends_of_u(rows, dtype):
         tokens.fill_(-7)
         sample(x, us, tokens=tokens, probs=probs)
         assert tokens.tolist() == [want] * rows and bool((probs > 0).all())
+
+
+def near_border(rows, seed, other, of, step):
+    """Logits a > b > 0 (multiples of 1/128) and an fp32 fraction f of the row's mass 1 + e^-1 + e^(a-1) +
+    e^(b-1) + `other`, next to the border of(a, b) in direction `step` and so near that a body of
+    262144 e^-28, counted, would move the border past it."""
+    rng, out = np.random.default_rng(seed), []
+    while len(out) < rows:
+        b, a = sorted(rng.integers(1, 64, 2) / 128.0)
+        if a == b:
+            continue
+        total = 1 + math.exp(-1) + math.exp(a - 1) + math.exp(b - 1) + other
+        ahead = of(a, b)
+        f = np.float32(ahead / total)
+        if (float(f) * total - ahead) * step <= 0:
+            f = np.nextafter(f, np.float32(step > 0))
+        d = abs(float(f) * total - ahead)
+        body = 262144 * math.exp(-28.0) * (1 - float(f) if step > 0 else float(f))
+        if 1e-9 < d < 0.8 * body:
+            out.append((a, b, float(f)))
+    return [list(v) for v in zip(*out)]
+
+
+@pytest.mark.parametrize("rows", [8, 230])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_weights_below_the_cut_move_no_border(rows, dtype):
+    """The body of such a row, 1.8e-7 of the mass were it counted, moves neither u's border between a and b
+    (u lies just above it: b) nor p's behind a (p lies just below it: b goes)."""
+    from block_diffusion_drafter_forward_gb300 import sample
+    V, e = 262144, math.exp
+    a, b, u = near_border(rows, 2, 0.0, lambda a, b: e(-1) + 1 + e(a - 1), 1)
+    x, at = late_maximum(V, dtype, a, b)
+    assert sample(x, torch.tensor(u, device="cuda")).tolist() == [at[2]] * rows
+    mid = len(range(7, V - 4000, V // 1500))
+    a, b, p = near_border(rows, 3, mid * e(-13.0), lambda a, b: 1 + e(a - 1), -1)
+    x, at = late_maximum(V, dtype, a, b, 1500)
+    last = torch.full((rows,), 1 - 2.0 ** -24, device="cuda")
+    assert sample(x, last, top_p=torch.tensor(p, device="cuda")).tolist() == [at[1]] * rows
