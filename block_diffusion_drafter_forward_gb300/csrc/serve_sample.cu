@@ -19,8 +19,8 @@
 //     stretches of the kept weights are summed as above.
 // Bound by HBM: one read of the logits (the finishing phases of some CTAs overlap the streaming of
 // others; three CTAs per SM with 32 KB of copies in flight each).  Measured, rows of 151936 bf16: 1024
-// rows greedy 53 us (5.9 TB/s), min-p 85, top-k 50 96, top-p 0.95 134, temperature alone 233, of
-// mixed settings 123 (205 where a row is streamed again: one call in four); flat ones (top-p 0.99 at
+// rows greedy 54 us (5.8 TB/s), min-p 84, top-k 50 95, top-p 0.95 133, temperature alone 229, of
+// mixed settings 126 (205 where a row is streamed again: one call in four); flat ones (top-p 0.99 at
 // temperature 1.2: prefixes of many thousands) 2.06 ms; one row 23 us, of which most is latency.
 //
 // The token is a whole number that a sum's last bit can change, so weights are pairs of floats
