@@ -21,6 +21,7 @@ DFLASH_EDEVICE = -6
 DFLASH_F32 = 0
 DFLASH_BF16 = 1
 DFLASH_FP8E4M3_ROWSCALE = 2
+DFLASH_FP8E4M3_ROWEXP = 3
 
 DFLASH_DEV_BAD_PAGE = 0x1
 DFLASH_DEV_BAD_CTX = 0x2
@@ -28,6 +29,7 @@ DFLASH_DEV_BAD_TOKEN = 0x4
 DFLASH_DEV_TIMEOUT = 0x8
 DFLASH_DEV_BAD_WIDTH = 0x10
 DFLASH_DEV_NO_ROOM = 0x20
+DFLASH_DEV_BAD_TREE = 0x40
 
 STATUS_NAMES = {0: "OK", -1: "EINVAL", -2: "ENOMEM", -3: "ECUDA", -4: "ECAPACITY", -5: "EUNSUPPORTED",
                 -6: "EDEVICE"}
@@ -79,7 +81,9 @@ EXPORTS = ("dflash_create", "dflash_destroy", "dflash_write_ctx_kv", "dflash_pro
            "dflash_profile_kinds", "dflash_profile_read", "dflash_gemm_bf16",
            "dflash_attention_check", "dflash_gemm_bf16_noalloc", "dflash_set_persistent", "dflash_persistent",
            "dflash_propose_ex", "dflash_write_ctx_kv_batch", "dflash_fp8_layer", "dflash_extend_tables",
-           "dflash_append_kv", "dflash_attend", "dflash_attend_workspace", "dflash_sample", "dflash_take_status", "dflash_extend_tables_ex")
+           "dflash_append_kv", "dflash_attend", "dflash_attend_workspace", "dflash_sample", "dflash_take_status", "dflash_extend_tables_ex",
+           "dflash_attend_ex", "dflash_draft_tree", "dflash_keep_rows", "dflash_append_kv_quant", "dflash_read_kv_quant",
+           "dflash_rope_turns", "dflash_rotate")
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -146,6 +150,22 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dflash_sample.restype = c.c_int
     lib.dflash_take_status.argtypes = [vp, vp, vp]
     lib.dflash_take_status.restype = c.c_int
+    lib.dflash_attend_ex.argtypes = [kv, i32, vp, i64, vp, i32, vp, vp, i32, i32, i32, i32, c.c_float, i32, i32, vp, i32, vp, vp,
+                                     i64, vp, vp, i64, vp]
+    lib.dflash_attend_ex.restype = c.c_int
+    lib.dflash_draft_tree.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, vp, vp]
+    lib.dflash_draft_tree.restype = c.c_int
+    lib.dflash_keep_rows.argtypes = [kv, vp, i32, vp, i32, vp, i32, vp, vp]
+    lib.dflash_keep_rows.restype = c.c_int
+    lib.dflash_append_kv_quant.argtypes = [kv, i32, vp, i64, vp, i64, vp, i32, vp]
+    lib.dflash_append_kv_quant.restype = c.c_int
+    lib.dflash_read_kv_quant.argtypes = [kv, i32, vp, i32, vp, i64, vp, i64, vp]
+    lib.dflash_read_kv_quant.restype = c.c_int
+    lib.dflash_rope_turns.argtypes = [i32, c.c_double, c.c_double, i32, c.c_double, c.c_double, c.c_double, c.c_double, vp,
+                                      c.POINTER(c.c_float)]
+    lib.dflash_rope_turns.restype = c.c_int
+    lib.dflash_rotate.argtypes = [vp, i64, vp, i64, i32, vp, i64, vp, i64, i32, i32, i32, i32, i32, i32, i32, vp, vp, c.c_float, vp]
+    lib.dflash_rotate.restype = c.c_int
     lib.dflash_last_error.argtypes = [vp]
     lib.dflash_last_error.restype = c.c_char_p
     _lib = lib
@@ -349,5 +369,66 @@ def dflash_sample(logits: int, row_stride: int, dtype: int, rows: int, vocab: in
                   top_p: int, min_p: int, tokens: int, probs: int, stream: int = 0) -> None:
     rc = load().dflash_sample(logits, row_stride, dtype, rows, vocab, u, temperature, top_k, top_p, min_p, tokens, probs,
                               stream)
+    if rc:
+        _check(rc, None)
+
+
+def dflash_attend_ex(kv: dflash_kv_pages, q_dtype: int, q: int, q_stride: int, page_tables: int, max_pages_per_seq: int,
+                     kv_lens: int, row_starts: int, nb: int, n_rows: int, max_new: int, n_q_heads: int, scale: float,
+                     window: int, causal: int, masks: int, mask_words: int, positions: int, out: int, out_stride: int,
+                     lse: int, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    rc = load().dflash_attend_ex(ctypes.byref(kv), q_dtype, q, q_stride, page_tables, max_pages_per_seq, kv_lens, row_starts,
+                                 nb, n_rows, max_new, n_q_heads, scale, window, causal, masks or None, mask_words,
+                                 positions or None, out, out_stride, lse, workspace, workspace_bytes, stream)
+    if rc:
+        _check(rc, None)
+
+
+def dflash_draft_tree(parents: int, kv_lens: int, row_starts: int, nb: int, n_rows: int, max_nodes: int, positions: int,
+                      masks: int, status: int = 0, stream: int = 0) -> None:
+    rc = load().dflash_draft_tree(parents, kv_lens, row_starts, nb, n_rows, max_nodes, positions, masks, status, stream)
+    if rc:
+        _check(rc, None)
+
+
+def dflash_keep_rows(kv: dflash_kv_pages, page_tables: int, max_pages_per_seq: int, ctx_lens: int, nb: int, path: int,
+                     max_path: int, path_lens: int, stream: int = 0) -> None:
+    rc = load().dflash_keep_rows(ctypes.byref(kv), page_tables, max_pages_per_seq, ctx_lens, nb, path, max_path, path_lens, stream)
+    if rc:
+        _check(rc, None)
+
+
+def dflash_append_kv_quant(kv: dflash_kv_pages, src_dtype: int, k: int, k_stride: int, v: int, v_stride: int, slots: int, n: int,
+                           stream: int = 0) -> None:
+    rc = load().dflash_append_kv_quant(ctypes.byref(kv), src_dtype, k, k_stride, v, v_stride, slots, n, stream)
+    if rc:
+        _check(rc, None)
+
+
+def dflash_read_kv_quant(kv: dflash_kv_pages, dst_dtype: int, slots: int, n: int, k: int, k_stride: int, v: int, v_stride: int,
+                         stream: int = 0) -> None:
+    rc = load().dflash_read_kv_quant(ctypes.byref(kv), dst_dtype, slots, n, k, k_stride, v, v_stride, stream)
+    if rc:
+        _check(rc, None)
+
+
+def dflash_rope_turns(rotary_dim: int, theta: float, linear: float = 1.0, yarn: Optional[Tuple[float, float, float, float]] = None):
+    """(rotary_dim / 2 frequencies in 2^-64 turns per position, mscale); yarn: (factor, original length, beta
+    fast, beta slow)."""
+    if not 16 <= rotary_dim <= 512:
+        raise DflashError(DFLASH_EUNSUPPORTED, "rope_turns: rotary_dim must be a multiple of 16 up to 512")
+    turns, mscale = (ctypes.c_uint64 * (rotary_dim // 2))(), ctypes.c_float()
+    rc = load().dflash_rope_turns(rotary_dim, theta, linear, 0 if yarn is None else 1, *(yarn or (1.0, 1.0, 1.0, 1.0)), turns,
+                                  ctypes.byref(mscale))
+    if rc:
+        _check(rc, None)
+    return list(turns), mscale.value
+
+
+def dflash_rotate(q: int, q_stride: int, q_out: int, q_out_stride: int, q_heads: int, k: int, k_stride: int, k_out: int,
+                  k_out_stride: int, k_heads: int, dtype: int, rows: int, head_dim: int, rotary_dim: int, interleaved: int,
+                  inverse: int, positions: int, turns: int, mscale: float, stream: int = 0) -> None:
+    rc = load().dflash_rotate(q, q_stride, q_out, q_out_stride, q_heads, k, k_stride, k_out, k_out_stride, k_heads, dtype, rows,
+                              head_dim, rotary_dim, interleaved, inverse, positions, turns, mscale, stream)
     if rc:
         _check(rc, None)

@@ -19,6 +19,10 @@ struct AttendParams {
   float scale_log2;  // scale * log2(e): scores are exponents of 2
   int group, tokens; // query heads of a kv head; tokens of a tile of 128 rows
   unsigned inv;      // row / group = row * inv >> 16 for rows below 128
+  // trees: masks of a sequence's rows over its rows (words of 64 bits each), positions; or NULL
+  const unsigned long long* masks;
+  const int32_t* positions;
+  int words;
 };
 
 // Workspace of the tensor-core form: split units' partials.
@@ -40,9 +44,11 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 }
 
 // Sequence s: its rows [*r0, *r0 + *n), key rows *kv.  false: no rows, or out of range (*bad).
+template <bool kTree = false>
 __device__ __forceinline__ bool seq_of(const AttendParams& p, int s, int* r0, int* n, int* kv, bool* bad) {
   const int a = __ldg(p.row_starts + s), b = __ldg(p.row_starts + s + 1), k = __ldg(p.kv_lens + s);
-  *bad = a < 0 || b < a || b > p.n_rows || k < 0 || (long long)k > (long long)p.mpps * kPage;
+  *bad = a < 0 || b < a || b > p.n_rows || k < 0 || (long long)k > (long long)p.mpps * kPage ||
+         (kTree && b - a > 64 * p.words);
   *r0 = a;
   *n = b - a;
   *kv = k;

@@ -1,7 +1,8 @@
 """Serving operators around the drafter, over torch device tensors: page tables and row maps built
-on the device (`extend_tables`), K/V rows appended to a paged cache and attended over (`PagedKV`),
-and tokens drawn from logits (`sample`).  Thin calls of dflash_extend_tables, dflash_append_kv,
-dflash_attend and dflash_sample: include/dflash.h states what each computes and refuses.
+on the device (`extend_tables`), K/V rows appended to a paged cache and attended over (`PagedKV`; in
+8 bits: `QuantKV`), trees of drafted tokens (`draft_tree`, `attend(tree=)`, `keep`), rotary positions
+(`Rope`) and tokens drawn from logits (`sample`).  Thin calls of the C entries of the same names:
+include/dflash.h states what each computes and refuses.
 
 Every call is asynchronous on `stream` (default: the current stream of the tensors' device), copies
 nothing to the host and keeps nothing for the next call.  Outputs and workspaces that a call
@@ -18,7 +19,7 @@ import torch
 
 from . import _lib as L
 
-_I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
+_I32, _I64, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat16
 _INT_MAX = 2 ** 31 - 1  # larger numbers would be cut to 32 bits on the way into the library
 _status: Dict[int, torch.Tensor] = {}  # device index -> its status word
 _status_lock = threading.Lock()
@@ -32,6 +33,12 @@ class RowPlan(NamedTuple):
     row_index: torch.Tensor   # [max_rows] its row (and position) in the sequence, -1 past the total
     slots: torch.Tensor       # [max_rows] its slot in the cache, -1 past the total
     free_end: torch.Tensor    # [1] position in the stack of free pages after this step
+
+
+class TreePlan(NamedTuple):
+    """What `draft_tree` returns, for every layer's `attend` (device tensors)."""
+    positions: torch.Tensor  # [rows] int32 position of each node: its sequence's context and its depth
+    masks: torch.Tensor      # [rows, words] int64: bit j % 64 of word j // 64 is set for the node j itself and its ancestors
 
 
 def _status_word(device: torch.device) -> torch.Tensor:
@@ -222,6 +229,91 @@ def extend_tables(ctx_lens: torch.Tensor, new_rows: torch.Tensor, page_tables: t
     return out
 
 
+def draft_tree(parents: torch.Tensor, kv_lens: torch.Tensor, row_starts: torch.Tensor, max_nodes: int,
+               out: Optional[TreePlan] = None, stream=None) -> TreePlan:
+    """Positions and masks of drafted trees.  Rows row_starts[s] .. row_starts[s + 1] - 1 are the nodes of
+    sequence s, its last rows of kv_lens[s]; parents [rows] is the node of the same sequence that a node
+    follows (an earlier one), or -1 where it follows the context.  max_nodes: the largest tree, or a
+    bound (at most 512); it sets the masks' words."""
+    try:
+        dev, n, nb = parents.device, parents.shape[0], kv_lens.shape[0]
+        ok = dev.type == "cuda"
+    except (AttributeError, IndexError):
+        ok = False
+    if not ok:
+        _first(parents, "parents", 1), _first(kv_lens, "kv_lens", 1)
+    max_nodes = int(max_nodes)
+    if not 1 <= max_nodes <= 512:
+        raise ValueError("max_nodes must be in [1, 512]")
+    words = (max_nodes + 63) // 64
+    with _on(dev, stream) as st:
+        if out is None:
+            out = TreePlan(torch.empty(n, dtype=_I32, device=dev), torch.empty((n, words), dtype=_I64, device=dev))
+        positions, masks = out
+        a_par, a_kv, a_rs, a_pos, a_mask = _addresses(
+            dev, (parents, "parents", _I32, (n,)), (kv_lens, "kv_lens", _I32, (nb,)), (row_starts, "row_starts", _I32, (nb + 1,)),
+            (positions, "out.positions", _I32, (n,)), (masks, "out.masks", _I64, (n, words)))
+        L.dflash_draft_tree(a_par, a_kv, a_rs, _i32(nb, "sequences"), _i32(n, "rows"), max_nodes, a_pos, a_mask,
+                            _status_word(dev).data_ptr(), st)
+    return out
+
+
+class Rope:
+    """Rotary positions with a table of frequencies on `device`: theta^(-2j / rotary_dim), divided by
+    `linear`, or remapped by `yarn` = (factor, original length, beta fast, beta slow) as a drafter's
+    configuration does.  Pairs are the halves of the rotated dims, or neighbours (interleaved)."""
+
+    def __init__(self, rotary_dim: int, theta: float = 1e6, linear: float = 1.0,
+                 yarn: Optional[Tuple[float, float, float, float]] = None, interleaved: bool = False, device="cuda"):
+        turns, self.mscale = L.dflash_rope_turns(int(rotary_dim), float(theta), float(linear), None if yarn is None else tuple(map(float, yarn)))
+        self.rotary_dim, self.interleaved = int(rotary_dim), bool(interleaved)
+        device = torch.device(device)
+        if device.type == "cuda" and device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        with torch.inference_mode(False):
+            self.turns = torch.tensor(turns, dtype=_I64).to(device)  # (below 2^62)
+        if device.type == "cuda":  # there for every stream
+            torch.cuda.current_stream(device).synchronize()
+
+    def rotate(self, q: torch.Tensor, positions: torch.Tensor, k: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+               k_out: Optional[torch.Tensor] = None, inverse: bool = False, stream=None):
+        """q [rows, heads, head_dim] and k [rows, kv_heads, head_dim] (any stride between rows) at `positions`
+        [rows] int32, into `out` and `k_out` (new ones by default; an input itself: in place).  inverse: the
+        map's transpose, which takes gradients back.  Returns out, or (out, k_out) when k is given."""
+        try:
+            n, nh, hd = q.shape
+            dtype, dev = q.dtype, q.device
+            ok = dev.type == "cuda" and (dtype is _BF16 or dtype is _F32)
+        except (AttributeError, ValueError):
+            ok = False
+        if not ok:
+            _first(q, "q", 3, (_BF16, _F32))
+        if self.turns.device != dev:
+            raise ValueError(f"q: the table is on {self.turns.device}, got a tensor on {dev}")
+        a_q, qs = _rows_of(q, "q", dtype, (n, nh, hd), dev)
+        a_pos, = _addresses(dev, (positions, "positions", _I32, (n,)))
+        a_k = ks = a_ko = kos = nk = 0
+        if k is not None:
+            if not isinstance(k, torch.Tensor) or k.dim() != 3:
+                _first(k, "k", 3, (dtype,))
+            nk = k.shape[1]
+            a_k, ks = _rows_of(k, "k", dtype, (n, nk, hd), dev)
+        elif k_out is not None:
+            raise ValueError("k_out: given without k")
+        with _on(dev, stream) as st:
+            if out is None:
+                out = torch.empty((n, nh, hd), dtype=dtype, device=dev)
+            a_o, os_ = _rows_of(out, "out", dtype, (n, nh, hd), dev)
+            if k is not None:
+                if k_out is None:
+                    k_out = torch.empty((n, nk, hd), dtype=dtype, device=dev)
+                a_ko, kos = _rows_of(k_out, "k_out", dtype, (n, nk, hd), dev)
+            L.dflash_rotate(a_q, qs, a_o, os_, nh, a_k, ks, a_ko, kos, nk, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32,
+                            _i32(n, "rows"), hd, self.rotary_dim, int(self.interleaved), 1 if inverse else 0, a_pos,
+                            self.turns.data_ptr(), self.mscale, st)
+        return out if k is None else (out, k_out)
+
+
 class PagedKV:
     """K/V pages of one layer: a tensor [pages, kv_heads, 2, 16 * head_dim] (bfloat16 or float32,
     contiguous but for the stride between pages), whose last dimension is a tile in the layout of
@@ -243,6 +335,7 @@ class PagedKV:
             raise ValueError("pool: heads and tiles of a page must be contiguous")
         self.pool = pool
         self.head_dim = tile // 16
+        self._rows = (dtype,)
         self._c = L.dflash_kv_pages(pool.data_ptr(), st[0] if P > 1 else 2 * nkv * tile, _status_word(dev).data_ptr(),
                                     L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32, nkv, self.head_dim, P)
         self._workspace = None  # bytes that a call of attend needs
@@ -272,38 +365,146 @@ class PagedKV:
 
     def attend(self, q: torch.Tensor, page_tables: torch.Tensor, kv_lens: torch.Tensor, row_starts: torch.Tensor,
                max_new: int, causal: bool = True, window: int = 0, scale: Optional[float] = None,
-               out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, stream=None):
+               out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, stream=None,
+               tree: Optional[TreePlan] = None):
         """Attention of each sequence's newest rows over its pages.  q [rows, heads, head_dim]; rows
         row_starts[s] .. row_starts[s + 1] - 1 are the last rows of sequence s, which has kv_lens[s].
         max_new: the longest chunk, or an upper bound (it picks the kernel).  scale: 1 / sqrt(head_dim)
-        by default.  Returns out [rows, heads, head_dim] (a new one is zeroed, so that rows behind the
-        last sequence hold zeros), or (out, lse) when `lse` [rows, heads] float32 is given."""
-        pool = self.pool
-        dev = pool.device
+        by default.  tree: of `draft_tree` for these rows, whose nodes see the context and their own
+        ancestors (`causal` is not looked at then, and a window is at least the masks' bits).  Returns out
+        [rows, heads, head_dim] (a new one is zeroed, so that rows behind the last sequence hold zeros), or
+        (out, lse) when `lse` [rows, heads] float32 is given."""
+        dev = self.pool.device
         hd = self.head_dim
         try:
-            (n, nh, _), (nb, mpps) = q.shape, page_tables.shape
+            (n, nh, _), (nb, mpps), dtype = q.shape, page_tables.shape, q.dtype
         except (AttributeError, ValueError):
-            _first(q, "q", 3, (pool.dtype,)), _first(page_tables, "page_tables", 2)
+            _first(q, "q", 3, self._rows), _first(page_tables, "page_tables", 2)
             raise
+        if dtype not in self._rows:
+            _first(q, "q", 3, self._rows)
         shape = (n, nh, hd)
-        a_q, qs = _rows_of(q, "q", pool.dtype, shape, dev)
+        a_q, qs = _rows_of(q, "q", dtype, shape, dev)
         a_pt, a_kv, a_rs = _addresses(dev, (page_tables, "page_tables", _I32, (nb, mpps)), (kv_lens, "kv_lens", _I32, (nb,)),
                                       (row_starts, "row_starts", _I32, (nb + 1,)))
         a_lse = 0 if lse is None else _addresses(dev, (lse, "lse", _F32, (n, nh)))[0]
+        a_pos = a_mask = words = 0
+        if tree is not None:
+            positions, masks = tree
+            words = masks.shape[1] if isinstance(masks, torch.Tensor) and masks.dim() == 2 else 1
+            a_pos, a_mask = _addresses(dev, (positions, "tree.positions", _I32, (n,)), (masks, "tree.masks", _I64, (n, words)))
+            if not n:
+                a_pos = a_mask = words = 0
         with _on(dev, stream) as st:
             if out is None:
-                out = torch.zeros(shape, dtype=pool.dtype, device=dev)
-            a_out, os_ = _rows_of(out, "out", pool.dtype, shape, dev)
-            need = self._workspace
-            if need is None:
-                need = self._workspace = L.dflash_attend_workspace(self._c)
+                out = torch.zeros(shape, dtype=dtype, device=dev)
+            a_out, os_ = _rows_of(out, "out", dtype, shape, dev)
+            need = 0
+            if dtype is _BF16:
+                need = self._workspace
+                if need is None:
+                    need = self._workspace = L.dflash_attend_workspace(self._c)
             ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-            L.dflash_attend(self._c, a_q, qs, a_pt, _i32(mpps, "pages of a sequence"), a_kv, a_rs, _i32(nb, "sequences"),
-                            _i32(n, "rows"), _limit(max_new), nh,
-                            1.0 / math.sqrt(hd) if scale is None else float(scale), _limit(window), 1 if causal else 0,
-                            a_out, os_, a_lse, ws.data_ptr() if need else 0, need, st)
+            L.dflash_attend_ex(self._c, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32, a_q, qs, a_pt,
+                               _i32(mpps, "pages of a sequence"), a_kv, a_rs, _i32(nb, "sequences"), _i32(n, "rows"),
+                               _limit(max_new), nh, 1.0 / math.sqrt(hd) if scale is None else float(scale), _limit(window),
+                               1 if causal else 0, a_mask, words, a_pos, a_out, os_, a_lse, ws.data_ptr() if need else 0, need, st)
         return out if lse is None else (out, lse)
+
+    def keep(self, page_tables: torch.Tensor, ctx_lens: torch.Tensor, path: torch.Tensor, path_lens: torch.Tensor,
+             stream=None) -> torch.Tensor:
+        """The rows of an accepted branch moved to where the sequence goes on: row ctx_lens[s] + path[s, i] to row
+        ctx_lens[s] + i, i < path_lens[s].  path [nb, longest] rises within a sequence; its entries from
+        path_lens[s] on are not read.  Returns the pages' tensor."""
+        dev = self.pool.device
+        try:
+            (nb, mpps), (_, longest) = page_tables.shape, path.shape
+        except (AttributeError, ValueError):
+            _first(page_tables, "page_tables", 2), _first(path, "path", 2)
+            raise
+        a_pt, a_ctx, a_path, a_len = _addresses(
+            dev, (page_tables, "page_tables", _I32, (nb, mpps)), (ctx_lens, "ctx_lens", _I32, (nb,)),
+            (path, "path", _I32, (nb, longest)), (path_lens, "path_lens", _I32, (nb,)))
+        with _on(dev, stream) as st:
+            L.dflash_keep_rows(self._c, a_pt, _i32(mpps, "pages of a sequence"), a_ctx, _i32(nb, "sequences"), a_path,
+                               _i32(longest, "nodes of a path"), a_len, st)
+        return self.pool
+
+
+class QuantKV(PagedKV):
+    """The same in 8 bits: a uint8 tensor [pages, kv_heads, 32 * head_dim + 32] (contiguous but for the stride
+    between pages) of e4m3 codes with a power of two for every row and head.  Rows are quantised as `append`
+    writes them and are bf16 numbers from then on; `attend` takes bfloat16 or float32 queries."""
+
+    def __init__(self, pool: torch.Tensor):
+        try:
+            (P, nkv, size), st = pool.shape, pool.stride()
+            dev = pool.device
+            ok = dev.type == "cuda" and pool.dtype is torch.uint8
+        except (AttributeError, ValueError):
+            ok = False
+        if not ok:
+            _first(pool, "pool", 3, (torch.uint8,))
+        if size != 32 * 64 + 32 and size != 32 * 128 + 32:
+            raise ValueError(f"pool: expected shape [pages, kv_heads, 32 * 64 + 32 or 32 * 128 + 32], got {tuple(pool.shape)}")
+        if st[2] != 1 or (nkv > 1 and st[1] != size):
+            raise ValueError("pool: heads of a page must be contiguous")
+        self.pool = pool
+        self.head_dim = (size - 32) // 32
+        self._rows = (_BF16, _F32)
+        self._c = L.dflash_kv_pages(pool.data_ptr(), st[0] if P > 1 else nkv * size, _status_word(dev).data_ptr(),
+                                    L.DFLASH_FP8E4M3_ROWEXP, nkv, self.head_dim, P)
+        self._workspace = None
+
+    @classmethod
+    def empty(cls, num_pages: int, n_kv_heads: int, head_dim: int, device="cuda") -> "QuantKV":
+        """A cache of its own (pages uninitialised: rows are defined once appended)."""
+        return cls(torch.empty((num_pages, n_kv_heads, 32 * head_dim + 32), dtype=torch.uint8, device=device))
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> torch.Tensor:
+        """Rows k, v [n, kv_heads, head_dim] (bfloat16 or float32, any stride between rows), quantised, into slots [n]
+        (negative: skipped) of the pages.  Returns the pages' tensor."""
+        dev = self.pool.device
+        try:
+            n, dtype = slots.shape[0], k.dtype
+        except (AttributeError, IndexError):
+            _first(slots, "slots", 1), _first(k, "k", 3, self._rows)
+            raise
+        if dtype not in self._rows:
+            _first(k, "k", 3, self._rows)
+        a_s, = _addresses(dev, (slots, "slots", _I32, (n,)))
+        shape = (n, self.pool.shape[1], self.head_dim)
+        a_k, ks = _rows_of(k, "k", dtype, shape, dev)
+        a_v, vs = _rows_of(v, "v", dtype, shape, dev)
+        with _on(dev, stream) as st:
+            L.dflash_append_kv_quant(self._c, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32, a_k, ks, a_v, vs, a_s,
+                                     _i32(n, "rows"), st)
+        return self.pool
+
+    def read(self, slots: torch.Tensor, dtype: torch.dtype = _BF16, k: Optional[torch.Tensor] = None,
+             v: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """(k, v) [n, kv_heads, head_dim]: the rows in slots [n] as numbers (zeros where a slot is negative), exact
+        in either dtype.  k, v: tensors to write into."""
+        dev = self.pool.device
+        if dtype not in self._rows:
+            raise ValueError(f"dtype: expected {' or '.join(map(str, self._rows))}, got {dtype}")
+        try:
+            n = slots.shape[0]
+        except (AttributeError, IndexError):
+            _first(slots, "slots", 1)
+            raise
+        a_s, = _addresses(dev, (slots, "slots", _I32, (n,)))
+        shape = (n, self.pool.shape[1], self.head_dim)
+        with _on(dev, stream) as st:
+            if k is None:
+                k = torch.empty(shape, dtype=dtype, device=dev)
+            if v is None:
+                v = torch.empty(shape, dtype=dtype, device=dev)
+            a_k, ks = _rows_of(k, "k", dtype, shape, dev)
+            a_v, vs = _rows_of(v, "v", dtype, shape, dev)
+            L.dflash_read_kv_quant(self._c, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32, a_s, _i32(n, "rows"), a_k, ks,
+                                   a_v, vs, st)
+        return k, v
 
 
 def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Tensor] = None,

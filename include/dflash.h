@@ -55,8 +55,9 @@ typedef enum {
 typedef enum {
   DFLASH_F32 = 0,              /* fp32 weights, activations and K/V cache (CUDA-core path) */
   DFLASH_BF16 = 1,             /* bf16 weights, activations and K/V cache (tensor-core path) */
-  DFLASH_FP8E4M3_ROWSCALE = 2  /* lm_head_dtype / layer_weight_dtype: e4m3 codes + one fp32 scale
+  DFLASH_FP8E4M3_ROWSCALE = 2, /* lm_head_dtype / layer_weight_dtype: e4m3 codes + one fp32 scale
                                   per output row */
+  DFLASH_FP8E4M3_ROWEXP = 3    /* dflash_kv_pages: e4m3 codes + one power of two per row and head */
 } dflash_dtype;
 
 /* Device status bits (dflash_device_status). */
@@ -66,6 +67,7 @@ typedef enum {
 #define DFLASH_DEV_TIMEOUT 0x8u     /* a kernel's bounded wait gave up (its outputs are invalid) */
 #define DFLASH_DEV_BAD_WIDTH 0x10u  /* dflash_propose_ex: a block width outside [2, gamma] (clamped) */
 #define DFLASH_DEV_NO_ROOM 0x20u    /* dflash_extend_tables: free pages or row slots ran out */
+#define DFLASH_DEV_BAD_TREE 0x40u   /* a parent that is no earlier node, a path that does not rise, a tree past its masks */
 
 /* Drafter configuration.  Names follow the drafter config.json of the pages
  * (hidden_size, num_attention_heads, num_key_value_heads, head_dim, intermediate_size,
@@ -337,7 +339,7 @@ typedef struct {
   void* pool;            /* device base of page 0, 16-byte aligned */
   int64_t page_stride;   /* elements between pages: >= 32 * n_kv_heads * head_dim, whole 16 bytes */
   uint32_t* status;      /* device status word or NULL */
-  int32_t dtype;         /* DFLASH_BF16 or DFLASH_F32 */
+  int32_t dtype;         /* DFLASH_BF16, DFLASH_F32, or DFLASH_FP8E4M3_ROWEXP where a call says so */
   int32_t n_kv_heads;    /* 1..1024 */
   int32_t head_dim;      /* 64 or 128 */
   int32_t num_pages;
@@ -420,6 +422,100 @@ int dflash_attend(const dflash_kv_pages* kv, const void* q, int64_t q_stride, co
 /* Bytes of workspace that dflash_attend needs on the current device for these pages (its size
  * does not depend on the batch); negative: a dflash_status. */
 int64_t dflash_attend_workspace(const dflash_kv_pages* kv);
+
+/* ---- Trees of drafted tokens.  Sequence s verifies n_s = row_starts[s+1] - row_starts[s] nodes, its last
+ * rows in the cache, in an order where every node comes after its parent.  kv_lens[s] counts them. */
+
+/* Positions and masks of a batch of trees.  parents [n_rows]: of node i of a sequence, the node in the
+ * same sequence (0 <= parent < i) that it follows, or -1: it follows the context (any number may).
+ *   positions [n_rows]        kv_lens[s] - n_s + the node's depth (its number of ancestors)
+ *   masks     [n_rows][words] words = ceil(max_nodes / 64); bit j % 64 of word j / 64 is set iff node j is
+ *                             the node itself or one of its ancestors
+ * Rows outside every sequence get position -1 and empty masks.  1 <= nb <= 16384, n_rows <= 2^30
+ * (ECAPACITY), 1 <= max_nodes <= 512 (EUNSUPPORTED).  A parent outside [-1, i) counts as -1 and sets
+ * DFLASH_DEV_BAD_TREE; so does a sequence of more than max_nodes nodes, whose rows get position -1 and empty
+ * masks.  A sequence whose row_starts fall or leave [0, n_rows], or with kv_lens[s] < n_s, sets
+ * DFLASH_DEV_BAD_CTX; the first kind's rows may be left as they are, the other's get -1 and empty masks.
+ * Outputs overlap no input. */
+int dflash_draft_tree(const int32_t* parents, const int32_t* kv_lens, const int32_t* row_starts, int32_t nb,
+                      int32_t n_rows, int32_t max_nodes, int32_t* positions, uint64_t* masks, uint32_t* status,
+                      dflash_stream stream);
+
+/* dflash_attend with queries of a type of their own and with trees.
+ * q_dtype: the pages' dtype, or DFLASH_BF16 or DFLASH_F32 over pages of DFLASH_FP8E4M3_ROWEXP (out has the
+ * same).  masks, positions: of dflash_draft_tree, or NULL, NULL (then exactly dflash_attend's rule).  With
+ * them `causal` is not looked at: with c = kv_lens[s] - n_s, row i of a sequence sees key j < kv_lens[s]
+ *   j < c:   iff window == 0 or positions[i] - j < window,
+ *   j >= c:  iff bit j - c of its mask is set (the caller may set others than ancestors').
+ * mask_words: 1..8 words of a row of masks.  A window below 64 mask_words is refused (EUNSUPPORTED: it
+ * could hide ancestors); a sequence of more than 64 mask_words rows is skipped and sets
+ * DFLASH_DEV_BAD_CTX.  The rest, dflash_attend_workspace among it, is as there. */
+int dflash_attend_ex(const dflash_kv_pages* kv, int32_t q_dtype, const void* q, int64_t q_stride,
+                     const int32_t* page_tables, int32_t max_pages_per_seq, const int32_t* kv_lens,
+                     const int32_t* row_starts, int32_t nb, int32_t n_rows, int32_t max_new, int32_t n_q_heads,
+                     float scale, int32_t window, int32_t causal, const uint64_t* masks, int32_t mask_words,
+                     const int32_t* positions, void* out, int64_t out_stride, float* lse, void* workspace,
+                     int64_t workspace_bytes, dflash_stream stream);
+
+/* Moves the rows of an accepted branch to where the sequence goes on: K and V of row
+ * ctx_lens[s] + path[s][i] go to row ctx_lens[s] + i, for i < path_lens[s].  path [nb, max_path] rises
+ * within a sequence (path[s][i] < path[s][i+1], path[s][0] >= 0), as a branch of a tree does; entries from
+ * path_lens[s] on are not read.  Afterwards the sequence has ctx_lens[s] + path_lens[s] rows.  Works on pages
+ * of every dtype; with the positions of dflash_draft_tree the keys' rotary positions stay right, since a
+ * branch's nodes lie at consecutive depths.  A sequence whose path does not rise, or with path_lens[s]
+ * outside [0, max_path], is left as it is (DFLASH_DEV_BAD_TREE); so is one with ctx_lens[s] < 0 or rows past
+ * 16 * max_pages_per_seq (DFLASH_DEV_BAD_CTX).  A row whose page id (its own or its new place's) is outside
+ * [0, num_pages) is not moved (DFLASH_DEV_BAD_PAGE).  Sequences share none of the pages that they write.
+ * 1 <= nb <= 16384, 0 <= max_path <= 512. */
+int dflash_keep_rows(const dflash_kv_pages* kv, const int32_t* page_tables, int32_t max_pages_per_seq,
+                     const int32_t* ctx_lens, int32_t nb, const int32_t* path, int32_t max_path,
+                     const int32_t* path_lens, dflash_stream stream);
+
+/* ---- Pages in 8 bits (dflash_kv_pages with dtype DFLASH_FP8E4M3_ROWEXP).  A row of a head, K or V alike, is
+ * x = 2^(e - 127) c: hd e4m3 codes c and one byte e.  A page of a head is 32 hd + 32 bytes: K codes, V codes,
+ * the 16 bytes e of K's rows and the 16 of V's; heads of a page follow one another and page_stride counts
+ * bytes (>= n_kv_heads (32 hd + 32), whole 16).  Row j (0..15), dim d lie at
+ *   K: (d/64) 1024 + j 64 + (((d/16) % 4) ^ ((j/2) % 4)) 16 + d % 16
+ *   V: 16 hd + (d/32) 512 + (d%8) 64 + ((j/4) ^ ((d%8)/2)) 16 + ((d%32)/8) 4 + j % 4
+ *   e: 32 hd + j (K), 32 hd + 16 + j (V)
+ * A row is written with k = e - 127 the smallest integer for which its largest finite |x| <= 448 2^k, kept
+ * in [-118, 119], and c = x 2^-k rounded to nearest even (largest magnitude 448).  Infinities and NaN become
+ * NaN.  All values 2^k c are bf16 numbers.  Bytes e outside [9, 246] are none that the library writes. */
+
+/* dflash_append_kv into pages of DFLASH_FP8E4M3_ROWEXP: rows of src_dtype (DFLASH_BF16 or DFLASH_F32) are
+ * quantised as they are written.  Arguments as there; strides in elements of src_dtype. */
+int dflash_append_kv_quant(const dflash_kv_pages* kv, int32_t src_dtype, const void* k, int64_t k_stride,
+                           const void* v, int64_t v_stride, const int32_t* slots, int32_t n, dflash_stream stream);
+
+/* The rows in `slots` [n] of pages of DFLASH_FP8E4M3_ROWEXP, as numbers: k, v [n, n_kv_heads, head_dim] in
+ * dst_dtype (DFLASH_BF16 or DFLASH_F32, exact in both), rows k_stride and v_stride elements apart (whole 16
+ * bytes).  A row whose slot is negative, or >= 16 * num_pages (DFLASH_DEV_BAD_PAGE), gets zeros. */
+int dflash_read_kv_quant(const dflash_kv_pages* kv, int32_t dst_dtype, const int32_t* slots, int32_t n, void* k,
+                         int64_t k_stride, void* v, int64_t v_stride, dflash_stream stream);
+
+/* ---- Rotary positions. */
+
+/* Angles per position of rotary_dim / 2 pairs, on the HOST: turns[j] = inv_freq_j / (2 pi) as a fraction of
+ * 2^64 (a position times it, modulo 2^64, is its angle exactly), and *mscale, which multiplies the rotated
+ * values.  inv_freq_j = theta^(-2j / rotary_dim) / linear, or with yarn != 0 (linear must be 1) the remap
+ * of dflash_create's rope_yarn for a head of rotary_dim.  turns [rotary_dim / 2]. */
+int dflash_rope_turns(int32_t rotary_dim, double theta, double linear, int32_t yarn, double yarn_factor,
+                      double yarn_orig_max_pos, double yarn_beta_fast, double yarn_beta_slow, uint64_t* turns,
+                      float* mscale);
+
+/* Rotates the first rotary_dim dims of every head by its row's position: with pairs (x_j, x_{j + rotary_dim/2})
+ * (interleaved == 0) or (x_2j, x_{2j+1}), and the angle a = positions[row] 2 pi turns[j] / 2^64,
+ *   y_a = mscale (x_a cos a - x_b sin a),   y_b = mscale (x_b cos a + x_a sin a);
+ * the other dims are copied.  inverse != 0: by -a, which is the map's transpose (mscale as it is) and so the
+ * gradient's.  q [rows, q_heads, head_dim] and k [rows, k_heads, head_dim] (NULL with k_heads 0: none) of
+ * `dtype` (DFLASH_BF16, DFLASH_F32), heads contiguous, rows a stride of whole 16 bytes apart; an output may be
+ * its input with the same stride, and overlaps nothing else.  positions [rows] int32 of either sign; turns
+ * [rotary_dim / 2] on the device.  head_dim is a multiple of 16 up to 512 and rotary_dim a multiple of 16 up
+ * to head_dim (EUNSUPPORTED), 1 <= q_heads, q_heads + k_heads <= 4096, rows <= 2^30.  rows == 0 is a no-op. */
+int dflash_rotate(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, int32_t q_heads, const void* k,
+                  int64_t k_stride, void* k_out, int64_t k_out_stride, int32_t k_heads, int32_t dtype, int32_t rows,
+                  int32_t head_dim, int32_t rotary_dim, int32_t interleaved, int32_t inverse, const int32_t* positions,
+                  const uint64_t* turns, float mscale, dflash_stream stream);
 
 /* One token per row of logits [rows, vocab] (`row_stride` elements between rows; dtype
  * DFLASH_BF16 or DFLASH_F32), drawn from the uniform numbers u [rows] in [0, 1).  temperature,
