@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(128) attend_simple_kernel(const AttendParams p
 #pragma unroll
   for (int e = 0; e < HD / 32; ++e) s_q[warp][lane + 32 * e] = Elem<T>::to_f(q[lane + 32 * e]) * p.scale_log2;
   __syncwarp();
-  const int ctx = kv - n, pos = p.masks ? p.positions[i] : ctx + (i - r0);
+  const int ctx = kv - n, pos = p.masks ? max(ctx, p.positions[i]) : ctx + (i - r0);
   const unsigned long long* mask = p.masks ? p.masks + (int64_t)i * p.words : nullptr;
   const int k_end = p.causal && !mask ? min(kv, pos + 1) : kv;
   const int k_begin = p.window > 0 ? max(0, pos - p.window + 1) : 0;
@@ -189,7 +189,7 @@ extern "C" int dflash_attend_ex(const dflash_kv_pages* kv, int32_t q_dtype, cons
   p.positions = positions;
   p.words = mask_words;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (kv->dtype == DFLASH_BF16 && !masks) {
+  if (kv->dtype == DFLASH_BF16) {
     int sms = 0;
     cudaError_t e = sm_count(&sms);
     if (e == cudaSuccess) e = launch_attend_tc(p, kv->head_dim, max_new, workspace, sms, st);

@@ -101,16 +101,18 @@ __device__ __forceinline__ Shape shape_of(const AttendParams& p, int NT) {
   h.TT = h.T * NT;
   return h;
 }
+template <bool kTree>
 __device__ __forceinline__ int unit_chunks(const AttendParams& p, const Shape& h, int n, int kv, int tile, int* k0) {
   const int t0 = tile * h.TT, t1 = min(n, t0 + h.TT);
-  const int end = p.causal ? min(kv, max(0, kv - n + t1)) : kv;
-  int lo = p.window > 0 ? max(0, kv - n + t0 - p.window + 1) : 0;
+  const int end = !kTree && p.causal ? min(kv, max(0, kv - n + t1)) : kv;
+  int lo = p.window > 0 ? max(0, kv - n + (kTree ? 0 : t0) - p.window + 1) : 0;
   lo &= ~(kPage - 1);
   *k0 = lo;
   return max(1, (end - lo + kKeys - 1) / kKeys);  // a unit without keys still writes its zeros
 }
 
 // The segments of index range [lo, hi), from unit (s, tile, g) whose first slot is pu.
+template <bool kTree>
 struct Walk {
   long long lo, hi, pu;
   int s, tile, g;
@@ -118,12 +120,12 @@ struct Walk {
   __device__ bool next(const AttendParams& p, const Shape& h, Seg& q) {
     while (pu < hi && s < p.nb) {
       bool bad;
-      if (!seq_of(p, s, &q.r0, &q.n, &q.kv, &bad)) {
+      if (!seq_of<kTree>(p, s, &q.r0, &q.n, &q.kv, &bad)) {
         ++s;
         tile = g = 0;
         continue;
       }
-      q.nch = unit_chunks(p, h, q.n, q.kv, tile, &q.k0);
+      q.nch = unit_chunks<kTree>(p, h, q.n, q.kv, tile, &q.k0);
       q.s = s, q.tile = tile, q.g = g, q.t0 = tile * h.TT;
       const long long first = pu + kUnitCost;
       pu = first + q.nch;
@@ -152,25 +154,27 @@ struct Ctl {
 static_assert(sizeof(Ctl) <= kCtl, "control block overflows its slot");
 
 // Slots of tiles [a, b) of a sequence for one kv head, by this thread.
+template <bool kTree>
 __device__ __forceinline__ long long tile_slots(const AttendParams& p, const Shape& h, int n, int kv, int a, int b, int step) {
   long long r = 0;
   int k0;
-  for (int t = a; t < b; t += step) r += unit_chunks(p, h, n, kv, t, &k0) + kUnitCost;
+  for (int t = a; t < b; t += step) r += unit_chunks<kTree>(p, h, n, kv, t, &k0) + kUnitCost;
   return r;
 }
 
 // This CTA's walk.  `scratch`: nb long longs of shared memory.  All threads.
-__device__ Walk plan(const AttendParams& p, const Shape& h, Ctl& c, long long* scratch, bool wide, long long* W_out) {
+template <bool kTree>
+__device__ Walk<kTree> plan(const AttendParams& p, const Shape& h, Ctl& c, long long* scratch, bool wide, long long* W_out) {
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   if (p.nb <= 32 && !wide) {
     // a lane per sequence, every warp for itself: no barrier (a step's first 3.5 us went by in the
     // general form's)
     int r0, n = 0, kv = 0, k0;
     bool bad = false;
-    const bool has = lane < p.nb && seq_of(p, lane, &r0, &n, &kv, &bad);
+    const bool has = lane < p.nb && seq_of<kTree>(p, lane, &r0, &n, &kv, &bad);
     if (bad && blockIdx.x == 0 && warp == 0 && p.status) atomicOr(p.status, DFLASH_DEV_BAD_CTX);
     const int tiles = has ? (n + h.TT - 1) / h.TT : 0;
-    const long long mine = tile_slots(p, h, n, kv, 0, tiles, 1) * p.nkv;
+    const long long mine = tile_slots<kTree>(p, h, n, kv, 0, tiles, 1) * p.nkv;
     long long inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -179,7 +183,7 @@ __device__ Walk plan(const AttendParams& p, const Shape& h, Ctl& c, long long* s
     }
     const long long W = __shfl_sync(0xffffffffu, inc, 31);
     const int G = (int)min((long long)gridDim.x, W), b = blockIdx.x;
-    Walk w;
+    Walk<kTree> w;
     w.lo = b < G ? (long long)b * W / G : 0;
     w.hi = b < G ? (long long)(b + 1) * W / G : 0;
     w.s = p.nb, w.tile = w.g = 0, w.pu = w.hi;
@@ -190,7 +194,7 @@ __device__ Walk plan(const AttendParams& p, const Shape& h, Ctl& c, long long* s
     const int n0 = __shfl_sync(0xffffffffu, n, s0), kv0 = __shfl_sync(0xffffffffu, kv, s0);
     w.s = s0;
     for (;;) {  // its tile: at most a few
-      const int slots = unit_chunks(p, h, n0, kv0, w.tile, &k0) + kUnitCost;
+      const int slots = unit_chunks<kTree>(p, h, n0, kv0, w.tile, &k0) + kUnitCost;
       if (w.lo < at + (long long)slots * p.nkv) {
         w.g = (int)((w.lo - at) / slots);
         w.pu = at + (long long)w.g * slots;
@@ -205,9 +209,9 @@ __device__ Walk plan(const AttendParams& p, const Shape& h, Ctl& c, long long* s
     int r0, n, kv;
     bool bad;
     long long m = 0;
-    if (seq_of(p, s, &r0, &n, &kv, &bad)) {
+    if (seq_of<kTree>(p, s, &r0, &n, &kv, &bad)) {
       const int tiles = (n + h.TT - 1) / h.TT;
-      m = wide ? tile_slots(p, h, n, kv, lane, tiles, 32) : tile_slots(p, h, n, kv, 0, tiles, 1);
+      m = wide ? tile_slots<kTree>(p, h, n, kv, lane, tiles, 32) : tile_slots<kTree>(p, h, n, kv, 0, tiles, 1);
     } else if (bad && blockIdx.x == 0 && p.status && (!wide || lane == 0)) {
       atomicOr(p.status, DFLASH_DEV_BAD_CTX);
     }
@@ -243,7 +247,7 @@ __device__ Walk plan(const AttendParams& p, const Shape& h, Ctl& c, long long* s
   for (int s = s_lo; s < s_hi; ++s) mine += scratch[s];
   long long at = scan(mine, &W);
   const int G = (int)min((long long)gridDim.x, W), b = blockIdx.x;
-  Walk w;
+  Walk<kTree> w;
   w.lo = b < G ? (long long)b * W / G : 0;
   w.hi = b < G ? (long long)(b + 1) * W / G : 0;
   w.s = p.nb, w.tile = w.g = 0, w.pu = w.hi;
@@ -263,11 +267,11 @@ __device__ Walk plan(const AttendParams& p, const Shape& h, Ctl& c, long long* s
   long long base = c.base;
   int r0, n, kv, k0;
   bool bad;
-  seq_of(p, s0, &r0, &n, &kv, &bad);
+  seq_of<kTree>(p, s0, &r0, &n, &kv, &bad);
   const int tiles = (n + h.TT - 1) / h.TT;
   for (int b0 = 0; b0 < tiles; b0 += kThreads) {  // the tile that holds slot lo
     const int tile = b0 + t;
-    const long long v = tile < tiles ? (long long)(unit_chunks(p, h, n, kv, tile, &k0) + kUnitCost) * p.nkv : 0;
+    const long long v = tile < tiles ? (long long)(unit_chunks<kTree>(p, h, n, kv, tile, &k0) + kUnitCost) * p.nkv : 0;
     long long all;
     const long long x = base + scan(v, &all);
     if (v > 0 && x <= w.lo && w.lo < x + v) c.tile0 = tile, c.base = x, c.found = 1;
@@ -276,7 +280,7 @@ __device__ Walk plan(const AttendParams& p, const Shape& h, Ctl& c, long long* s
     if (c.found) break;
   }
   w.s = s0, w.tile = c.tile0;
-  const int slots = unit_chunks(p, h, n, kv, w.tile, &k0) + kUnitCost;
+  const int slots = unit_chunks<kTree>(p, h, n, kv, w.tile, &k0) + kUnitCost;
   w.g = (int)((w.lo - c.base) / slots);
   w.pu = c.base + (long long)w.g * slots;
   return w;
@@ -339,10 +343,21 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Which of 32 keys from `key` on a tree's row sees: context [lo, ctx), of the rows [ctx, kv) those with a bit in
+// its mask of n words.
+__device__ __forceinline__ uint32_t mask_bits(const uint32_t* mask, int n, int key, int lo, int ctx, int kv) {
+  const int at = key - ctx;  // bit of the mask that the first key has
+  auto word = [&](int w) { return w >= 0 && w < n ? __ldg(mask + w) : w < 0 ? 0xffffffffu : 0u; };  // (the context: ones)
+  uint32_t m = at <= -32 ? 0xffffffffu : __funnelshift_r(word(at >> 5), word((at >> 5) + 1), at & 31);
+  if (lo > key) m = lo - key >= 32 ? 0u : m & 0xffffffffu << (lo - key);
+  if (kv < key + 32) m = kv <= key ? 0u : m & 0xffffffffu >> (key + 32 - kv);
+  return m;
+}
+
 // The chunks of stream x, in order, as every role counts them.
-template <int NT>
+template <int NT, bool kTree>
 struct It {
-  Walk w;
+  Walk<kTree> w;
   Seg sg;
   int j, n;        // chunk within the segment, chunks of it
   int kc0;         // chunks of the segments before it
@@ -367,7 +382,7 @@ struct It {
     }
     return false;
   }
-  __device__ void start(const AttendParams& p, const Shape& h, const Walk& w0, int x) {
+  __device__ void start(const AttendParams& p, const Shape& h, const Walk<kTree>& w0, int x) {
     w = w0;
     kc0 = it = 0;
     seg = act = -1;
@@ -388,7 +403,7 @@ struct It {
   }
 };
 
-template <int HD, int NT>
+template <int HD, int NT, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendParams p, const AttendWork wk, const __grid_constant__ CUtensorMap q_map) {
   using C = Cfg<HD, NT>;
   extern __shared__ __align__(1024) uint8_t smem[];  // (the queries' swizzle counts from 1 KB boundaries)
@@ -403,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
   pdl_wait();  // everything read here may come from the kernel before
   if (t == 0) wk.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
   long long W;
-  const Walk walk = plan(p, h, c, reinterpret_cast<long long*>(sK), wk.long_chunks, &W);
+  const Walk<kTree> walk = plan<kTree>(p, h, c, reinterpret_cast<long long*>(sK), wk.long_chunks, &W);
   if (walk.lo >= walk.hi) {  // nothing for this CTA
     pdl_trigger();
     return;
@@ -458,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
       uint64_t* empty = kv ? c.v_empty : c.k_empty;
       uint8_t* ring = kv ? sV : sK;
       const int slots = kv ? C::kNV : C::kNK;
-      Walk w = walk;
+      Walk<kTree> w = walk;
       Seg q;
       int i = 0;
       bool stop = false;
@@ -558,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
       if (NT == 2) {
         // one stream: S of a chunk, then its P V and the next S as soon as the softmax has written P
         const int x = warp == 9 ? 0 : 1;
-        Walk w = walk;
+        Walk<kTree> w = walk;
         Seg q;
         int kc = 0, it = 0, act = 0;
         auto wait = [&](uint64_t* bar, int phase) {
@@ -573,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         };
         while (w.next(p, h, q)) {
           const int n = q.c_hi - q.c_lo;
-          if (!It<NT>::active(h, q, x)) {
+          if (!It<NT, kTree>::active(h, q, x)) {
             // no row of this stream: it still follows every slot, so that its waits stay exact
             for (int j = 0; j < n; ++j, ++kc) {
               wait(&c.k_full[kc % C::kNK], kc / C::kNK);
@@ -607,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         }
       } else if (warp == 9) {
         // both streams: each alternates S and P V; whichever is ready goes out
-        It<NT> its[2];
+        It<NT, kTree> its[2];
         bool pv[2] = {false, false};
         its[0].start(p, h, walk, 0);
         its[1].start(p, h, walk, 1);
@@ -619,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
           bool did = false;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            It<NT>& a = its[x];
+            It<NT, kTree>& a = its[x];
             const bool give_up = flags[0];  // after a timeout: commits only, no MMAs
             if (a.valid && pv[x]) {
               const int kc = a.kc0 + a.j, vb = kc % C::kNV;
@@ -668,23 +683,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
     const uint32_t tS = tmem + x * 128 + lane_off;
     const int tok = row / h.group, head = row - tok * h.group;  // (by p.inv the loop's registers fall worse: 519 us for 499)
     const bool loads = (t & 127) == 0 && (NT == 2 || x == 0);  // (one tile: stream 0's, a segment ahead)
-    Walk w = walk;
+    Walk<kTree> w = walk;
     Seg q, nq;
     bool have = w.next(p, h, q);
-    while (NT == 2 && have && !It<NT>::active(h, q, x)) have = w.next(p, h, q);
+    while (NT == 2 && have && !It<NT, kTree>::active(h, q, x)) have = w.next(p, h, q);
     if (have && loads) load_q(q, x);
     int it = 0, seg = 0;  // chunks and segments done by this stream
     while (have) {
       bool more = w.next(p, h, nq);
-      while (NT == 2 && more && !It<NT>::active(h, nq, x)) more = w.next(p, h, nq);
+      while (NT == 2 && more && !It<NT, kTree>::active(h, nq, x)) more = w.next(p, h, nq);
       const int n = q.c_hi - q.c_lo;
       const int tk = q.t0 + (NT == 2 ? x * h.T : 0) + tok;
       const bool valid = tok < h.T && tk < q.n;
       const bool warp_valid = __any_sync(0xffffffffu, valid);
       // keys [lo, hi) are seen by this row (rows without a token: anything, they are not written)
-      const int pos = q.kv - q.n + tk;
-      const int hi = !valid ? INT_MAX : p.causal ? min(q.kv, pos + 1) : q.kv;
+      // (trees: keys [lo, hi) of the context, and those of the sequence's own rows that the mask has)
+      const int pos = !kTree ? q.kv - q.n + tk : valid && p.window > 0 ? max(q.kv - q.n, __ldg(p.positions + q.r0 + tk)) : 0;
+      const int hi = !valid ? INT_MAX : kTree ? q.kv - q.n : p.causal ? min(q.kv, pos + 1) : q.kv;
       const int lo = valid && p.window > 0 ? max(0, pos - p.window + 1) : 0;
+      const uint32_t* mask = kTree ? reinterpret_cast<const uint32_t*>(p.masks + (int64_t)(q.r0 + (valid ? tk : 0)) * p.words) : nullptr;
       float m = -INFINITY, l = 0.f;
       int done = 0;
 #pragma unroll 1
@@ -700,7 +717,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
           ld64(tS, a);
           ld64(tS + 64, b);
           ld_wait(a, b);
-          if (__any_sync(0xffffffffu, kb < lo || kb + kKeys > hi)) {
+          if (kTree && __any_sync(0xffffffffu, kb < lo || kb + kKeys > hi)) {
+            uint32_t mk[4];  // bit e of word w: key kb + 32 w + e is seen
+#pragma unroll
+            for (int w = 0; w < 4; ++w) mk[w] = valid ? mask_bits(mask, 2 * p.words, kb + 32 * w, lo, q.kv - q.n, q.kv) : 0xffffffffu;
+#pragma unroll
+            for (int e = 0; e < 64; ++e) {
+              if (!(mk[e >> 5] >> (e & 31) & 1)) a[e] = -INFINITY;
+              if (!(mk[2 + (e >> 5)] >> (e & 31) & 1)) b[e] = -INFINITY;
+            }
+          }
+          if (!kTree && __any_sync(0xffffffffu, kb < lo || kb + kKeys > hi)) {
             const unsigned span = hi > lo ? (unsigned)(hi - lo) : 0u;
 #pragma unroll
             for (int e = 0; e < 64; ++e) {
@@ -971,10 +998,10 @@ __global__ void __launch_bounds__(256) attend_combine_kernel(const AttendParams 
   }
 }
 
-template <int HD, int NT>
+template <int HD, int NT, bool kTree>
 cudaError_t launch(const AttendParams& p, const AttendWork& w, int sms, cudaStream_t st) {
   static std::atomic<unsigned long long> attr{0};
-  if (cudaError_t e = smem_attr_once(attend_tc_kernel<HD, NT>, Cfg<HD, NT>::kSmem, attr); e != cudaSuccess) return e;
+  if (cudaError_t e = smem_attr_once(attend_tc_kernel<HD, NT, kTree>, Cfg<HD, NT>::kSmem, attr); e != cudaSuccess) return e;
   cudaLaunchAttribute a[1];
   a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   a[0].val.programmaticStreamSerializationAllowed = 1;
@@ -987,7 +1014,7 @@ cudaError_t launch(const AttendParams& p, const AttendWork& w, int sms, cudaStre
   c.numAttrs = 1;
   CUtensorMap q_map;
   if (!make_tmap_heads_bf16(&q_map, p.q, p.n_rows, p.nh, HD, p.q_stride, p.group, p.tokens)) return cudaErrorInvalidValue;
-  if (cudaError_t e = cudaLaunchKernelEx(&c, attend_tc_kernel<HD, NT>, p, w, q_map); e != cudaSuccess) return e;
+  if (cudaError_t e = cudaLaunchKernelEx(&c, attend_tc_kernel<HD, NT, kTree>, p, w, q_map); e != cudaSuccess) return e;
   c.gridDim = dim3(sms, NT * 16);  // a unit's rows in one round
   c.blockDim = dim3(256);
   c.dynamicSmemBytes = 0;
@@ -1015,8 +1042,12 @@ cudaError_t launch_attend_tc(const AttendParams& p, int head_dim, int max_new, v
   // (8 x 256 on 2048).
   const bool two = max_new > T && ((int64_t)p.n_rows + T - 1) / T * p.nkv * 2 >= sms;
   w.long_chunks = max_new > 4 * (two ? 2 * T : T);
-  if (head_dim == 128) return two ? launch<128, 2>(p, w, sms, st) : launch<128, 1>(p, w, sms, st);
-  return two ? launch<64, 2>(p, w, sms, st) : launch<64, 1>(p, w, sms, st);
+  if (p.masks) {
+    if (head_dim == 128) return two ? launch<128, 2, true>(p, w, sms, st) : launch<128, 1, true>(p, w, sms, st);
+    return two ? launch<64, 2, true>(p, w, sms, st) : launch<64, 1, true>(p, w, sms, st);
+  }
+  if (head_dim == 128) return two ? launch<128, 2, false>(p, w, sms, st) : launch<128, 1, false>(p, w, sms, st);
+  return two ? launch<64, 2, false>(p, w, sms, st) : launch<64, 1, false>(p, w, sms, st);
 }
 
 }  // namespace dflash

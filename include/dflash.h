@@ -445,7 +445,7 @@ int dflash_draft_tree(const int32_t* parents, const int32_t* kv_lens, const int3
  * q_dtype: the pages' dtype, or DFLASH_BF16 or DFLASH_F32 over pages of DFLASH_FP8E4M3_ROWEXP (out has the
  * same).  masks, positions: of dflash_draft_tree, or NULL, NULL (then exactly dflash_attend's rule).  With
  * them `causal` is not looked at: with c = kv_lens[s] - n_s, row i of a sequence sees key j < kv_lens[s]
- *   j < c:   iff window == 0 or positions[i] - j < window,
+ *   j < c:   iff window == 0 or max(c, positions[i]) - j < window,
  *   j >= c:  iff bit j - c of its mask is set (the caller may set others than ancestors').
  * mask_words: 1..8 words of a row of masks.  A window below 64 mask_words is refused (EUNSUPPORTED: it
  * could hide ancestors); a sequence of more than 64 mask_words rows is skipped and sets
