@@ -195,6 +195,12 @@ extern "C" int dflash_attend_ex(const dflash_kv_pages* kv, int32_t q_dtype, cons
     if (e == cudaSuccess) e = launch_attend_tc(p, kv->head_dim, max_new, workspace, sms, st);
     return e == cudaSuccess ? DFLASH_OK : call_error(DFLASH_ECUDA, "attend", e);
   }
+  if (!f32 && p.group <= 16 && (int64_t)max_new * p.group <= 16) {
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e == cudaSuccess) e = launch_attend8(p, kv->head_dim, max_new, workspace, sms, st);
+    return e == cudaSuccess ? DFLASH_OK : call_error(DFLASH_ECUDA, "attend", e);
+  }
   const int64_t blocks = ((int64_t)n_rows * n_q_heads + 3) / 4;
   if (blocks > 0x7fffffff) return call_error(DFLASH_ECAPACITY, "attend: too many rows for one call");
   auto kern = kv->head_dim == 128 ? (quant ? (f32 ? attend_simple_kernel<128, float, true> : attend_simple_kernel<128, __nv_bfloat16, true>)

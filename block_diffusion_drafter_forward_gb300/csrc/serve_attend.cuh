@@ -56,6 +56,12 @@ __device__ __forceinline__ bool seq_of(const AttendParams& p, int s, int* r0, in
 }
 
 int64_t attend_tc_workspace(int head_dim, int sms);
+// The workspace's parts; long_chunks: many query tiles per sequence.
+AttendWork attend_work(void* workspace, int head_dim, int sms, bool long_chunks);
+// Merges the partials of split units (rows of p.tokens tokens, 128 rows a slot).
+cudaError_t launch_attend_combine(const AttendParams& p, const AttendWork& w, int head_dim, int sms, cudaStream_t st);
+// Pages in 8 bits, bf16 queries, at most 16 query heads of a kv head: units of 16 rows.
+cudaError_t launch_attend8(const AttendParams& p, int head_dim, int max_new, void* workspace, int sms, cudaStream_t st);
 cudaError_t launch_attend_tc(const AttendParams& p, int head_dim, int max_new, void* workspace, int sms, cudaStream_t st);
 
 }  // namespace dflash

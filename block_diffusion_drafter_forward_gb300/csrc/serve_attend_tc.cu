@@ -41,18 +41,25 @@
 #include <type_traits>
 
 #include "launch_util.cuh"
-#include "serve_attend.cuh"
+#include "serve_attend_plan.cuh"
 #include "tc_common.cuh"
 
 namespace dflash {
 namespace {
 
 using namespace tc;
+using plan::PlanCtl;
+using plan::Seg;
+using plan::Shape;
+using plan::mask_bits;
+using plan::shape_of;
 
 constexpr int kKeys = 128;                      // keys per chunk
 constexpr int kPages = kKeys / kPage;           // 8
 constexpr int kThreads = 384;
-constexpr int kWarps = kThreads / 32;
+struct Geo {
+  static constexpr int kKeys = 128, kUnitCost = 3, kThreads = 384;
+};
 constexpr int kCtl = 2944;                      // barriers, plan, row exchange
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
@@ -69,10 +76,6 @@ __device__ __forceinline__ bool wait_ab(uint64_t* bar, uint32_t parity, volatile
   return mbar_try_wait(bar, parity) || mbar_wait_ab(bar, parity, abort);
 }
 
-// Slots of the index space a unit occupies beside its chunks: the cost of opening a segment
-// (queries, pipeline restart, output) in chunks.
-constexpr int kUnitCost = 3;
-
 template <int HD, int NT>
 struct Cfg {
   static constexpr int kTile = kPage * HD * 2;         // a page of one head: bytes of K (or V)
@@ -83,208 +86,15 @@ struct Cfg {
   static constexpr int kSmem = 2 * kQ + (kNK + kNV) * kSlot + kCtl;  // (queries: two tiles, or two segments' tile)
 };
 
-struct Seg {
-  int s, r0, n, kv;     // sequence, its first row, rows, key rows
-  int tile, g, t0;      // query tile, kv head, its first token
-  int k0, nch;          // first key (page aligned), chunks of the unit
-  int c_lo, c_hi;       // this CTA's chunks of it
-};
-
-// Tokens of a unit's tile and the chunks it visits.
-struct Shape {
-  int group, T, TT;     // query heads per kv head, tokens of a 128-row tile, of a unit
-};
-__device__ __forceinline__ Shape shape_of(const AttendParams& p, int NT) {
-  Shape h;
-  h.group = p.group;
-  h.T = p.tokens;
-  h.TT = h.T * NT;
-  return h;
-}
-template <bool kTree>
-__device__ __forceinline__ int unit_chunks(const AttendParams& p, const Shape& h, int n, int kv, int tile, int* k0) {
-  const int t0 = tile * h.TT, t1 = min(n, t0 + h.TT);
-  const int end = !kTree && p.causal ? min(kv, max(0, kv - n + t1)) : kv;
-  int lo = p.window > 0 ? max(0, kv - n + (kTree ? 0 : t0) - p.window + 1) : 0;
-  lo &= ~(kPage - 1);
-  *k0 = lo;
-  return max(1, (end - lo + kKeys - 1) / kKeys);  // a unit without keys still writes its zeros
-}
-
-// The segments of index range [lo, hi), from unit (s, tile, g) whose first slot is pu.
-template <bool kTree>
-struct Walk {
-  long long lo, hi, pu;
-  int s, tile, g;
-
-  __device__ bool next(const AttendParams& p, const Shape& h, Seg& q) {
-    while (pu < hi && s < p.nb) {
-      bool bad;
-      if (!seq_of<kTree>(p, s, &q.r0, &q.n, &q.kv, &bad)) {
-        ++s;
-        tile = g = 0;
-        continue;
-      }
-      q.nch = unit_chunks<kTree>(p, h, q.n, q.kv, tile, &q.k0);
-      q.s = s, q.tile = tile, q.g = g, q.t0 = tile * h.TT;
-      const long long first = pu + kUnitCost;
-      pu = first + q.nch;
-      if (++g == p.nkv) {
-        g = 0;
-        if (++tile * h.TT >= q.n) tile = 0, ++s;
-      }
-      if (hi <= first || lo >= pu) continue;  // only cost slots of it are in range
-      q.c_lo = (int)(lo > first ? lo - first : 0);
-      q.c_hi = (int)(hi < pu ? hi - first : q.nch);
-      return true;
-    }
-    return false;
-  }
-};
-
 struct Ctl {
   uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6], v_raw[6];
   uint64_t s_full[2], p_half[2], p_full[2], o_done[2], o_free[2], q_full[2];
   uint32_t tmem_slot;
   int flags[2];
-  int s0, tile0, found;
-  long long red[kWarps], W, base;
+  PlanCtl<Geo> plan;
   float2 ml[2][128];  // one tile: the streams' (m, l) of every row
 };
 static_assert(sizeof(Ctl) <= kCtl, "control block overflows its slot");
-
-// Slots of tiles [a, b) of a sequence for one kv head, by this thread.
-template <bool kTree>
-__device__ __forceinline__ long long tile_slots(const AttendParams& p, const Shape& h, int n, int kv, int a, int b, int step) {
-  long long r = 0;
-  int k0;
-  for (int t = a; t < b; t += step) r += unit_chunks<kTree>(p, h, n, kv, t, &k0) + kUnitCost;
-  return r;
-}
-
-// This CTA's walk.  `scratch`: nb long longs of shared memory.  All threads.
-template <bool kTree>
-__device__ Walk<kTree> plan(const AttendParams& p, const Shape& h, Ctl& c, long long* scratch, bool wide, long long* W_out) {
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  if (p.nb <= 32 && !wide) {
-    // a lane per sequence, every warp for itself: no barrier (a step's first 3.5 us went by in the
-    // general form's)
-    int r0, n = 0, kv = 0, k0;
-    bool bad = false;
-    const bool has = lane < p.nb && seq_of<kTree>(p, lane, &r0, &n, &kv, &bad);
-    if (bad && blockIdx.x == 0 && warp == 0 && p.status) atomicOr(p.status, DFLASH_DEV_BAD_CTX);
-    const int tiles = has ? (n + h.TT - 1) / h.TT : 0;
-    const long long mine = tile_slots<kTree>(p, h, n, kv, 0, tiles, 1) * p.nkv;
-    long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += x;
-    }
-    const long long W = __shfl_sync(0xffffffffu, inc, 31);
-    const int G = (int)min((long long)gridDim.x, W), b = blockIdx.x;
-    Walk<kTree> w;
-    w.lo = b < G ? (long long)b * W / G : 0;
-    w.hi = b < G ? (long long)(b + 1) * W / G : 0;
-    w.s = p.nb, w.tile = w.g = 0, w.pu = w.hi;
-    *W_out = W;
-    if (w.lo >= w.hi) return w;
-    const int s0 = __ffs(__ballot_sync(0xffffffffu, inc > w.lo)) - 1;  // the sequence that holds slot lo
-    long long at = __shfl_sync(0xffffffffu, inc - mine, s0);
-    const int n0 = __shfl_sync(0xffffffffu, n, s0), kv0 = __shfl_sync(0xffffffffu, kv, s0);
-    w.s = s0;
-    for (;;) {  // its tile: at most a few
-      const int slots = unit_chunks<kTree>(p, h, n0, kv0, w.tile, &k0) + kUnitCost;
-      if (w.lo < at + (long long)slots * p.nkv) {
-        w.g = (int)((w.lo - at) / slots);
-        w.pu = at + (long long)w.g * slots;
-        return w;
-      }
-      at += (long long)slots * p.nkv;
-      ++w.tile;
-    }
-  }
-  // slots of each sequence (all kv heads): a thread per sequence, or a warp where chunks are long
-  for (int s = wide ? warp : t; s < p.nb; s += wide ? kWarps : kThreads) {
-    int r0, n, kv;
-    bool bad;
-    long long m = 0;
-    if (seq_of<kTree>(p, s, &r0, &n, &kv, &bad)) {
-      const int tiles = (n + h.TT - 1) / h.TT;
-      m = wide ? tile_slots<kTree>(p, h, n, kv, lane, tiles, 32) : tile_slots<kTree>(p, h, n, kv, 0, tiles, 1);
-    } else if (bad && blockIdx.x == 0 && p.status && (!wide || lane == 0)) {
-      atomicOr(p.status, DFLASH_DEV_BAD_CTX);
-    }
-    if (wide) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
-    }
-    if (!wide || lane == 0) scratch[s] = m * p.nkv;
-  }
-  if (t == 0) c.found = 0;
-  __syncthreads();
-  // thread t sums sequences [t per, (t + 1) per)
-  const int per = (p.nb + kThreads - 1) / kThreads, s_lo = min(p.nb, t * per), s_hi = min(p.nb, s_lo + per);
-  auto scan = [&](long long v, long long* all) {  // exclusive sum over the threads before this one
-    long long inc = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += x;
-    }
-    if (lane == 31) c.red[warp] = inc;
-    __syncthreads();
-    long long b = inc - v, a = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) b += c.red[w];
-      a += c.red[w];
-    }
-    __syncthreads();
-    *all = a;
-    return b;
-  };
-  long long mine = 0, W;
-  for (int s = s_lo; s < s_hi; ++s) mine += scratch[s];
-  long long at = scan(mine, &W);
-  const int G = (int)min((long long)gridDim.x, W), b = blockIdx.x;
-  Walk<kTree> w;
-  w.lo = b < G ? (long long)b * W / G : 0;
-  w.hi = b < G ? (long long)(b + 1) * W / G : 0;
-  w.s = p.nb, w.tile = w.g = 0, w.pu = w.hi;
-  *W_out = W;
-  if (w.lo >= w.hi) return w;
-  if (at <= w.lo && w.lo < at + mine) {
-    for (int s = s_lo; s < s_hi; ++s) {
-      if (w.lo < at + scratch[s]) {
-        c.s0 = s, c.base = at;
-        break;
-      }
-      at += scratch[s];
-    }
-  }
-  __syncthreads();
-  const int s0 = c.s0;
-  long long base = c.base;
-  int r0, n, kv, k0;
-  bool bad;
-  seq_of<kTree>(p, s0, &r0, &n, &kv, &bad);
-  const int tiles = (n + h.TT - 1) / h.TT;
-  for (int b0 = 0; b0 < tiles; b0 += kThreads) {  // the tile that holds slot lo
-    const int tile = b0 + t;
-    const long long v = tile < tiles ? (long long)(unit_chunks<kTree>(p, h, n, kv, tile, &k0) + kUnitCost) * p.nkv : 0;
-    long long all;
-    const long long x = base + scan(v, &all);
-    if (v > 0 && x <= w.lo && w.lo < x + v) c.tile0 = tile, c.base = x, c.found = 1;
-    base += all;
-    __syncthreads();
-    if (c.found) break;
-  }
-  w.s = s0, w.tile = c.tile0;
-  const int slots = unit_chunks<kTree>(p, h, n, kv, w.tile, &k0) + kUnitCost;
-  w.g = (int)((w.lo - c.base) / slots);
-  w.pu = c.base + (long long)w.g * slots;
-  return w;
-}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -343,18 +153,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Which of 32 keys from `key` on a tree's row sees: context [lo, ctx), of the rows [ctx, kv) those with a bit in
-// its mask of n words.
-__device__ __forceinline__ uint32_t mask_bits(const uint32_t* mask, int n, int key, int lo, int ctx, int kv) {
-  const int at = key - ctx;  // bit of the mask that the first key has
-  auto word = [&](int w) { return w >= 0 && w < n ? __ldg(mask + w) : w < 0 ? 0xffffffffu : 0u; };  // (the context: ones)
-  uint32_t m = at <= -32 ? 0xffffffffu : __funnelshift_r(word(at >> 5), word((at >> 5) + 1), at & 31);
-  if (lo > key) m = lo - key >= 32 ? 0u : m & 0xffffffffu << (lo - key);
-  if (kv < key + 32) m = kv <= key ? 0u : m & 0xffffffffu >> (key + 32 - kv);
-  return m;
-}
-
 // The chunks of stream x, in order, as every role counts them.
+template <bool kTree> using Walk = plan::Walk<Geo, kTree>;
+
 template <int NT, bool kTree>
 struct It {
   Walk<kTree> w;
@@ -418,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
   pdl_wait();  // everything read here may come from the kernel before
   if (t == 0) wk.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
   long long W;
-  const Walk<kTree> walk = plan<kTree>(p, h, c, reinterpret_cast<long long*>(sK), wk.long_chunks, &W);
+  const Walk<kTree> walk = plan::make<Geo, kTree>(p, h, c.plan, reinterpret_cast<long long*>(sK), wk.long_chunks, &W);
   if (walk.lo >= walk.hi) {  // nothing for this CTA
     pdl_trigger();
     return;
@@ -998,6 +799,20 @@ __global__ void __launch_bounds__(256) attend_combine_kernel(const AttendParams 
   }
 }
 
+template <int HD, int NT>
+cudaError_t combine(const AttendParams& p, const AttendWork& w, int sms, cudaStream_t st) {
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(sms, NT * 16);  // a unit's rows in one round
+  c.blockDim = dim3(256);
+  c.stream = st;
+  c.attrs = a;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, attend_combine_kernel<HD, NT>, p, w);
+}
+
 template <int HD, int NT, bool kTree>
 cudaError_t launch(const AttendParams& p, const AttendWork& w, int sms, cudaStream_t st) {
   static std::atomic<unsigned long long> attr{0};
@@ -1015,10 +830,7 @@ cudaError_t launch(const AttendParams& p, const AttendWork& w, int sms, cudaStre
   CUtensorMap q_map;
   if (!make_tmap_heads_bf16(&q_map, p.q, p.n_rows, p.nh, HD, p.q_stride, p.group, p.tokens)) return cudaErrorInvalidValue;
   if (cudaError_t e = cudaLaunchKernelEx(&c, attend_tc_kernel<HD, NT, kTree>, p, w, q_map); e != cudaSuccess) return e;
-  c.gridDim = dim3(sms, NT * 16);  // a unit's rows in one round
-  c.blockDim = dim3(256);
-  c.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&c, attend_combine_kernel<HD, NT>, p, w);
+  return combine<HD, NT>(p, w, sms, st);
 }
 
 }  // namespace
@@ -1028,11 +840,21 @@ int64_t attend_tc_workspace(int head_dim, int sms) {
   return (int64_t)sms * (2 * 256 * (head_dim * 4 + 8) + 16);
 }
 
-cudaError_t launch_attend_tc(const AttendParams& p, int head_dim, int max_new, void* workspace, int sms, cudaStream_t st) {
+AttendWork attend_work(void* workspace, int head_dim, int sms, bool long_chunks) {
   AttendWork w;
   w.o = static_cast<float*>(workspace);
   w.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + (int64_t)sms * 2 * 256 * head_dim * 4);
   w.meta = reinterpret_cast<int4*>(w.ml + (int64_t)sms * 2 * 256);
+  w.long_chunks = long_chunks;
+  return w;
+}
+
+cudaError_t launch_attend_combine(const AttendParams& p, const AttendWork& w, int head_dim, int sms, cudaStream_t st) {
+  return head_dim == 128 ? combine<128, 1>(p, w, sms, st) : combine<64, 1>(p, w, sms, st);
+}
+
+cudaError_t launch_attend_tc(const AttendParams& p, int head_dim, int max_new, void* workspace, int sms, cudaStream_t st) {
+  AttendWork w = attend_work(workspace, head_dim, sms, false);
   const int T = p.tokens;
   // Chunks longer than one tile: two tiles share every K/V slot, where there are units enough for the
   // SMs.  Measured (32 query heads on 4, one tile / two): 32 sequences x 17 tokens on 4096 rows
