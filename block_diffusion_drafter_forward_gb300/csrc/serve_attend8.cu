@@ -10,12 +10,21 @@
 // tcgen05 has nothing to give here: its smallest tile is 128 rows, of which a single token fills 8 or 16, and
 // its operands would have to go through shared memory once more as 16 bits.
 //
-// An e4m3 code becomes a bf16 number by moving its bits: sign | exponent and mantissa << 4 is the code's value
-// times 2^-120 exactly, subnormals included (three instructions for two).  Nothing multiplies the
-// factor and the rows' powers of two into the codes: Q is scaled by 2^(110 - e) with the row's largest
-// magnitude below 2^(e+1), the scores by 2^ke per key, P by 2^(ve - r + 90) per key before it is rounded to bf16
-// (exact but for that rounding), and O is kept in units of 2^(r + 30), r the largest exponent ve of
-// the pages so far, or up to 20 below it.
+// S takes Q and the codes of K as f16 numbers, both exact: Q is scaled by 2^(14 - e) with the row's largest
+// magnitude in [2^e, 2^(e+1)) (its eight bits fit; exact down to 2^-31 of the largest, below that to
+// 2^-38 of it), a code is an f16 number (one conversion for two).
+// V is multiplied in bf16, since P needs more range than f16 has: a code becomes a bf16 number by moving its bits -
+// sign, exponent and mantissa << 4 is the code's value times 2^-120 exactly, subnormals included, three
+// instructions for two.  Nothing multiplies that factor and the rows' powers of two into the codes: the
+// scores are scaled by 2^ke per key, P by 2^(ve - r + 90) per key before it is rounded to bf16 (exact but for
+// that rounding), and O is kept in units of 2^(r + 30), r the largest exponent ve of the pages so far, or up to
+// 20 below it.
+//
+// Measured (GB300; 16 tokens on 16-32 Ki rows, 64 heads on 8): 149 us, of which copies alone take 135.  K in bf16 as
+// V: 163.  K in e4m3 products with Q as two e4m3 parts: 204.  7 warps: 163; two pages a step: 152.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
 #include <atomic>
 
 #include "launch_util.cuh"
@@ -30,7 +39,7 @@ using plan::PlanCtl;
 using plan::Seg;
 using plan::Shape;
 
-constexpr int kW = 8;  // warps with pages of their own
+constexpr int kW = 11;  // warps with pages of their own (12 with the producer's: 168 registers a thread)
 struct Geo {
   static constexpr int kKeys = 16 * kW, kUnitCost = 2, kThreads = 32 * (kW + 1);
 };
@@ -39,7 +48,7 @@ template <bool kTree> using Walk = plan::Walk<Geo, kTree>;
 template <int HD>
 struct Cfg {
   static constexpr int kBytes = 32 * HD + 32;                       // a page of one head
-  static constexpr int kStages = HD == 128 ? 5 : 10;
+  static constexpr int kStages = HD == 128 ? 4 : 8;
   static constexpr int kRing = kW * kStages * kBytes;
   static constexpr int kMerge = kW * 16 * 32 * 4;                  // 32 dims of every warp's O
 };
@@ -57,11 +66,22 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t& a, uint32_t& b) {
   // each byte with its sign in the byte above, moved up by 4: the sign, four zeros, exponent and mantissa
   asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(a) : "r"(w));
   asm("prmt.b32 %0, %1, 0, 0xb3a2;" : "=r"(b) : "r"(w));
-  a = a << 4 & 0x87f087f0u;
-  b = b << 4 & 0x87f087f0u;
+  asm("mad.lo.u32 %0, %0, 16, 0;" : "+r"(a));  // (a shift, off the pipe of the permutes)
+  asm("mad.lo.u32 %0, %0, 16, 0;" : "+r"(b));
+  a &= 0x87f087f0u;
+  b &= 0x87f087f0u;
 }
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// codes 0, 1 and 2, 3 of a word as pairs of f16
+__device__ __forceinline__ void halves(uint32_t w, uint32_t& a, uint32_t& b) {
+  asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;}" : "=r"(a), "=r"(b) : "r"(w));
+}
+__device__ __forceinline__ void mma_bf16w(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -175,16 +195,16 @@ __global__ void __launch_bounds__(Geo::kThreads, 1) attend8_kernel(const AttendP
           for (int k = 0; k < 4; ++k) top = max(top, max((&v[x][z].x)[k] & 0x7fffu, (&v[x][z].x)[k] >> 16 & 0x7fffu));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int e = max((int)(top >> 7) - 127, -16);  // (rows near zero: less is enough)
-      const float up = pow2i(110 - e);
-      // scores come out as 2^(110 - e - 120) q . code: e + 10 puts that right (in two factors: either may be large)
-      rowf[y] = p.scale_log2 * pow2i(min(e + 10, 127)) * (e + 10 > 127 ? pow2i(e + 10 - 127) : 1.f);
+      const int e = top == 0 ? 0 : max((int)(top >> 7) - 127, -112);
+      const float up = pow2i(14 - e);
+      rowf[y] = p.scale_log2 * pow2i(e - 14);
 #pragma unroll
       for (int x = 0; x < HD / 64; ++x)
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const uint32_t u = (&v[x][k >> 2].x)[k & 3];
-          a[x][k >> 1][(k & 1) * 2 + y] = pack_bf16(__uint_as_float(u << 16) * up, __uint_as_float(u & 0xffff0000u) * up);
+          const __half2 g = __floats2half2_rn(__uint_as_float(u << 16) * up, __uint_as_float(u & 0xffff0000u) * up);
+          a[x][k >> 1][(k & 1) * 2 + y] = *reinterpret_cast<const uint32_t*>(&g);
         }
       const int ctx = q.kv - q.n;
       pos[y] = !kTree ? ctx + tk[y] : valid[y] && p.window > 0 ? max(ctx, __ldg(p.positions + q.r0 + tk[y])) : 0;
@@ -203,50 +223,57 @@ __global__ void __launch_bounds__(Geo::kThreads, 1) attend8_kernel(const AttendP
     for (int lp = q.k0 / kPage + q.c_lo * kW + warp; lp < end; lp += kW, ++i) {
       const int b = i % C::kStages;
       if (!mbar_wait_ab(&c.full[warp][b], (i / C::kStages) & 1, flags)) break;
-      const uint8_t* tile = ring + (warp * C::kStages + b) * C::kBytes;
-      // ---- S: score s[x][..] of keys 4 j + 2 x, + 1 (column n of the product x is key 4 (n / 2) + 2 x + n % 2)
-      float s[2][4], s2[2][4];
+      uint8_t* tile = ring + (warp * C::kStages + b) * C::kBytes;
+      const int key0 = lp * kPage + 4 * j;
+      if ((lp + 1) * kPage > q.kv) {
+        // rows behind the sequence's end may hold anything: their V becomes zeros (K's scores are replaced below)
+        const int live = q.kv - key0;
+        const uint32_t dead = live <= 0 ? 0xffffffffu : live >= 4 ? 0u : 0xffffffffu << 8 * live;
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) s[x][k] = s2[x][k] = 0.f;
+        for (int d = 0; d < HD / 32; ++d) {
+          uint4* v = reinterpret_cast<uint4*>(tile + 16 * HD + d * 512 + r * 64 + ((j ^ (r >> 1)) * 16));
+          *v = make_uint4(v->x & ~dead, v->y & ~dead, v->z & ~dead, v->w & ~dead);
+        }
+        uint32_t* e = reinterpret_cast<uint32_t*>(tile + 32 * HD + 16 + 4 * j);
+        __syncwarp();
+        if (r == 0) *e = (*e & ~dead) | (0x09090909u & dead);
+        fence_proxy_async_smem();  // ahead of the copy that reuses the slot
+        __syncwarp();
+      }
+      // ---- S: score s[x][..] of keys 4 j + 2 x, + 1 (column n of product x is key 4 (n / 2) + 2 x + n % 2)
+      float s[2][4];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int key = 4 * (r >> 1) + 2 * x + (r & 1);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[x][k] = 0.f;
 #pragma unroll
         for (int y = 0; y < HD / 64; ++y) {
           const uint4 k = *reinterpret_cast<const uint4*>(tile + y * 1024 + key * 64 + ((j ^ (key >> 1 & 3)) * 16));
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
             uint32_t b0, b1;
-            widen((&k.x)[z], b0, b1);
-            mma16816(z & 1 ? s2[x] : s[x], a[y][z], b0, b1);
+            halves((&k.x)[z], b0, b1);
+            mma_f16(s[x], a[y][z], b0, b1);
           }
         }
       }
-      uint32_t ek = *reinterpret_cast<const uint32_t*>(tile + 32 * HD + 4 * j), ev = *reinterpret_cast<const uint32_t*>(tile + 32 * HD + 16 + 4 * j);
-      const int key0 = lp * kPage + 4 * j;
-      uint32_t dead = 0;  // bytes of the lane's keys behind the sequence's end: whatever they hold is not used
-      if ((lp + 1) * kPage > q.kv) {
-        dead = key0 >= q.kv ? 0xffffffffu : key0 + 4 > q.kv ? 0xffffffffu << 8 * (q.kv - key0) : 0u;
-        ev = (ev & ~dead) | (0x09090909u & dead);
-      }
+      const uint32_t ek = *reinterpret_cast<const uint32_t*>(tile + 32 * HD + 4 * j), ev = *reinterpret_cast<const uint32_t*>(tile + 32 * HD + 16 + 4 * j);
       float sc[2][4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float f = __uint_as_float((ek >> 8 * k & 255) << 23);  // 2^ke
+        const float f = __uint_as_float(k < 3 ? ek << (23 - 8 * k) & 0x7f800000u : ek >> 1 & 0x7f800000u);  // 2^ke
 #pragma unroll
-        for (int y = 0; y < 2; ++y) sc[y][k] = (s[k >> 1][2 * y + (k & 1)] + s2[k >> 1][2 * y + (k & 1)]) * f * rowf[y];
+        for (int y = 0; y < 2; ++y) sc[y][k] = s[k >> 1][2 * y + (k & 1)] * (f * rowf[y]);
       }
       if (lp * kPage < see_lo || (lp + 1) * kPage > see_hi) {
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          uint32_t bits;
+          uint32_t bits = 0;
           if (kTree) {
             const uint32_t* mask = reinterpret_cast<const uint32_t*>(p.masks + (int64_t)(q.r0 + (valid[y] ? tk[y] : 0)) * p.words);
-            bits = valid[y] ? plan::mask_bits(mask, 2 * p.words, key0, lo[y], q.kv - q.n, q.kv) : 0u;
+            if (valid[y]) bits = plan::mask_bits(mask, 2 * p.words, key0, lo[y], q.kv - q.n, q.kv);
           } else {
-            bits = 0;
 #pragma unroll
             for (int k = 0; k < 4; ++k) bits |= key0 + k >= lo[y] && key0 + k < min(hi[y], q.kv) ? 1u << k : 0u;
           }
@@ -255,7 +282,7 @@ __global__ void __launch_bounds__(Geo::kThreads, 1) attend8_kernel(const AttendP
             if (!(bits >> k & 1)) sc[y][k] = -INFINITY;
         }
       }
-      // ---- softmax: the reference moves only when the maximum grew by more than 2^8
+      // ---- softmax: the references move only when a maximum grew by more than 2^8, or an exponent of V by 20
       bool grow = false;
       float alpha[2];
 #pragma unroll
@@ -270,41 +297,37 @@ __global__ void __launch_bounds__(Geo::kThreads, 1) attend8_kernel(const AttendP
       }
       uint32_t most = __vmaxu4(ev, ev >> 16);
       most = max(most & 255, most >> 8 & 255);
-      const int top_e = (int)__reduce_max_sync(0xffffffffu, most) - 127;
-      float drop = 1.f;
-      if (top_e > ref + 20) {
-        drop = ref == -1000 ? 0.f : ref - top_e < -126 ? 0.f : pow2i(ref - top_e);
-        ref = top_e;
-        grow = true;
-      }
-      if (__any_sync(0xffffffffu, grow)) {
+      if (__any_sync(0xffffffffu, grow || (int)most - 127 > ref + 20)) {
+        const int top_e = (int)__reduce_max_sync(0xffffffffu, most) - 127;
+        float drop = 1.f;
+        if (top_e > ref + 20) {
+          drop = ref - top_e < -126 ? 0.f : pow2i(ref - top_e);
+          ref = top_e;
+        }
         l[0] *= alpha[0], l[1] *= alpha[1];
         const float f0 = alpha[0] * drop, f1 = alpha[1] * drop;
 #pragma unroll
         for (int d = 0; d < HD / 8; ++d) o[d][0] *= f0, o[d][1] *= f0, o[d][2] *= f1, o[d][3] *= f1;
       }
-      uint32_t pa[4];
-      float pv[2][4];
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const float off = m[y] == -INFINITY ? 0.f : m[y];
-        float z = 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          pv[y][k] = ex2(sc[y][k] - off);
-          z += pv[y][k];
+          sc[y][k] = ex2(sc[y][k] - off);
+          l[y] += sc[y][k];
         }
-        l[y] += z;
       }
+      uint32_t pa[4];
+      {
+        float f[4];  // 2^(ve - ref + 90)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float f = pow2i(max((int)(ev >> 8 * k & 255) - 37 - ref, -126));  // 2^(ve - ref + 90)
-        pv[0][k] *= f, pv[1][k] *= f;
+        for (int k = 0; k < 4; ++k) f[k] = __int_as_float(max((k < 3 ? (int)(ev << (23 - 8 * k) & 0x7f800000u) : (int)(ev >> 1 & 0x7f800000u)) + (90 - ref) * (1 << 23), 1 << 23));
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) pa[2 * x + y] = pack_bf16(sc[y][2 * x] * f[2 * x], sc[y][2 * x + 1] * f[2 * x + 1]);
       }
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) pa[2 * x + y] = pack_bf16(pv[y][2 * x], pv[y][2 * x + 1]);
       // ---- O += P V
 #pragma unroll
       for (int d = 0; d < HD / 32; ++d) {
@@ -312,8 +335,8 @@ __global__ void __launch_bounds__(Geo::kThreads, 1) attend8_kernel(const AttendP
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
           uint32_t b0, b1;
-          widen((&v.x)[z] & ~dead, b0, b1);
-          mma16816(o[4 * d + z], pa, b0, b1);
+          widen((&v.x)[z], b0, b1);
+          mma_bf16w(o[4 * d + z], pa, b0, b1);
         }
       }
       __syncwarp();
@@ -357,21 +380,22 @@ __global__ void __launch_bounds__(Geo::kThreads, 1) attend8_kernel(const AttendP
         *reinterpret_cast<float2*>(dst + (r + 8) * 32) = make_float2(o[4 * d + z][2] * f[1] * 0x1p30f * unit, o[4 * d + z][3] * f[1] * 0x1p30f * unit);
       }
       named_barrier(1, 32 * kW);
-      // thread t: row t / 16, two dims
-      const int row = t >> 4, x = (t & 15) * 2, tok = row * p.inv >> 16, head = row - tok * h.group, token = q.t0 + tok;
-      float2 sum = make_float2(0.f, 0.f);
+      for (int e = t; e < 256; e += 32 * kW) {  // row e / 16, two dims
+        const int row = e >> 4, x = (e & 15) * 2, tok = row * p.inv >> 16, head = row - tok * h.group, token = q.t0 + tok;
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int u = 0; u < kW; ++u) {
-        const float2 v = *reinterpret_cast<const float2*>(merge + u * 512 + row * 32 + x);
-        sum.x += v.x, sum.y += v.y;
-      }
-      if (tok < h.T && token < q.n && !flags[0]) {
-        const int dim = 32 * d + x;
-        if (whole) {
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + (int64_t)(q.r0 + token) * p.out_stride + (int64_t)(q.g * h.group + head) * HD + dim;
-          *reinterpret_cast<uint32_t*>(dst) = pack_bf16(sum.x, sum.y);
-        } else {
-          *reinterpret_cast<float2*>(part_row(wk, 2 * blockIdx.x + (q.c_lo == 0 ? 1 : 0), row, 128, HD) + dim) = sum;
+        for (int u = 0; u < kW; ++u) {
+          const float2 v = *reinterpret_cast<const float2*>(merge + u * 512 + row * 32 + x);
+          sum.x += v.x, sum.y += v.y;
+        }
+        if (tok < h.T && token < q.n && !flags[0]) {
+          const int dim = 32 * d + x;
+          if (whole) {
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + (int64_t)(q.r0 + token) * p.out_stride + (int64_t)(q.g * h.group + head) * HD + dim;
+            *reinterpret_cast<uint32_t*>(dst) = pack_bf16(sum.x, sum.y);
+          } else {
+            *reinterpret_cast<float2*>(part_row(wk, 2 * blockIdx.x + (q.c_lo == 0 ? 1 : 0), row, 128, HD) + dim) = sum;
+          }
         }
       }
       named_barrier(1, 32 * kW);
