@@ -25,7 +25,7 @@ __device__ __forceinline__ float code_value(uint8_t c) {
 // CUDA-core form: one warp per (row, query head), online softmax over pages of 16 keys.  Lane l
 // takes key l % 16 and one half of the dims of q . k, and dims l, l + 32, ... of the output.
 // Pages in 8 bits (kQuant) give the numbers that they stand for.
-template <int HD, typename T, bool kQuant>
+template <int HD, bool kQuant>
 __global__ void __launch_bounds__(128) attend_simple_kernel(const AttendParams p) {
   __shared__ float s_q[4][HD];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -50,9 +50,9 @@ __global__ void __launch_bounds__(128) attend_simple_kernel(const AttendParams p
   bool bad;
   const bool rows = p.masks ? seq_of<true>(p, s, &r0, &n, &kv, &bad) : seq_of(p, s, &r0, &n, &kv, &bad);
   if (!rows || i < r0 || i >= r0 + n) return;
-  const T* q = static_cast<const T*>(p.q) + i * p.q_stride + h * HD;
+  const float* q = static_cast<const float*>(p.q) + i * p.q_stride + h * HD;
 #pragma unroll
-  for (int e = 0; e < HD / 32; ++e) s_q[warp][lane + 32 * e] = Elem<T>::to_f(q[lane + 32 * e]) * p.scale_log2;
+  for (int e = 0; e < HD / 32; ++e) s_q[warp][lane + 32 * e] = q[lane + 32 * e] * p.scale_log2;
   __syncwarp();
   const int ctx = kv - n, pos = p.masks ? max(ctx, p.positions[i]) : ctx + (i - r0);
   const unsigned long long* mask = p.masks ? p.masks + (int64_t)i * p.words : nullptr;
@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(128) attend_simple_kernel(const AttendParams p
   const int half = lane >> 4, j = lane & 15;
   for (int lp = k_begin / kPage; lp * kPage < k_end; ++lp) {
     const int page = page_id(p, s, lp);
-    const T* tile = static_cast<const T*>(p.pool) + page * p.page_stride + (int64_t)g * 2 * kPage * HD;
+    const float* tile = static_cast<const float*>(p.pool) + page * p.page_stride + (int64_t)g * 2 * kPage * HD;
     const uint8_t* codes = static_cast<const uint8_t*>(p.pool) + page * p.page_stride + (int64_t)g * (32 * HD + 32);
     float sc = 0.f;
 #pragma unroll
@@ -75,9 +75,9 @@ __global__ void __launch_bounds__(128) attend_simple_kernel(const AttendParams p
 #pragma unroll
         for (int e = 0; e < 8; ++e) sc = fmaf(s_q[warp][d8 * 8 + e], code_value(k[e]), sc);
       } else {
-        const T* k = tile + k_in_tile(j, d8 * 8, HD);
+        const float* k = tile + k_in_tile(j, d8 * 8, HD);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sc = fmaf(s_q[warp][d8 * 8 + e], Elem<T>::to_f(k[e]), sc);
+        for (int e = 0; e < 8; ++e) sc = fmaf(s_q[warp][d8 * 8 + e], k[e], sc);
       }
     }
     sc += __shfl_xor_sync(0xffffffffu, sc, 16);
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(128) attend_simple_kernel(const AttendParams p
     m = m_new;
 #pragma unroll
     for (int e = 0; e < HD / 32; ++e) acc[e] *= alpha;
-    const T* v = tile + kPage * HD;
+    const float* v = tile + kPage * HD;
     const unsigned seen = __ballot_sync(0xffffffffu, see);
     for (int jj = max(0, k_begin - lp * kPage); jj < min(kPage, k_end - lp * kPage); ++jj) {  // seen keys only
       if (mask && !(seen >> jj & 1)) continue;
@@ -110,14 +110,14 @@ __global__ void __launch_bounds__(128) attend_simple_kernel(const AttendParams p
         for (int e = 0; e < HD / 32; ++e) acc[e] = fmaf(w, code_value(codes[16 * HD + v8_in_tile(jj, lane + 32 * e)]) * f, acc[e]);
       } else {
 #pragma unroll
-        for (int e = 0; e < HD / 32; ++e) acc[e] = fmaf(w, Elem<T>::to_f(v[v_in_tile(jj, lane + 32 * e, HD)]), acc[e]);
+        for (int e = 0; e < HD / 32; ++e) acc[e] = fmaf(w, v[v_in_tile(jj, lane + 32 * e, HD)], acc[e]);
       }
     }
   }
-  T* out = static_cast<T*>(p.out) + i * p.out_stride + h * HD;
+  float* out = static_cast<float*>(p.out) + i * p.out_stride + h * HD;
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
 #pragma unroll
-  for (int e = 0; e < HD / 32; ++e) out[lane + 32 * e] = Elem<T>::from_f(acc[e] * inv);
+  for (int e = 0; e < HD / 32; ++e) out[lane + 32 * e] = acc[e] * inv;
   if (p.lse && lane == 0) p.lse[(int64_t)i * p.nh + h] = lse_of(m, l);
 }
 
@@ -188,25 +188,19 @@ extern "C" int dflash_attend_ex(const dflash_kv_pages* kv, int32_t q_dtype, cons
   p.masks = reinterpret_cast<const unsigned long long*>(masks);
   p.positions = positions;
   p.words = mask_words;
+  p.quant = quant;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (kv->dtype == DFLASH_BF16) {
+  if (!f32) {
     int sms = 0;
     cudaError_t e = sm_count(&sms);
-    if (e == cudaSuccess) e = launch_attend_tc(p, kv->head_dim, max_new, workspace, sms, st);
-    return e == cudaSuccess ? DFLASH_OK : call_error(DFLASH_ECUDA, "attend", e);
-  }
-  if (!f32 && p.group <= 16 && (int64_t)max_new * p.group <= 16) {
-    int sms = 0;
-    cudaError_t e = sm_count(&sms);
-    if (e == cudaSuccess) e = launch_attend8(p, kv->head_dim, max_new, workspace, sms, st);
+    if (e == cudaSuccess && quant && (int64_t)max_new * p.group <= 16) e = launch_attend8(p, kv->head_dim, max_new, workspace, sms, st);
+    else if (e == cudaSuccess) e = launch_attend_tc(p, kv->head_dim, max_new, workspace, sms, st);
     return e == cudaSuccess ? DFLASH_OK : call_error(DFLASH_ECUDA, "attend", e);
   }
   const int64_t blocks = ((int64_t)n_rows * n_q_heads + 3) / 4;
   if (blocks > 0x7fffffff) return call_error(DFLASH_ECAPACITY, "attend: too many rows for one call");
-  auto kern = kv->head_dim == 128 ? (quant ? (f32 ? attend_simple_kernel<128, float, true> : attend_simple_kernel<128, __nv_bfloat16, true>)
-                                           : f32 ? attend_simple_kernel<128, float, false> : attend_simple_kernel<128, __nv_bfloat16, false>)
-                                  : (quant ? (f32 ? attend_simple_kernel<64, float, true> : attend_simple_kernel<64, __nv_bfloat16, true>)
-                                           : f32 ? attend_simple_kernel<64, float, false> : attend_simple_kernel<64, __nv_bfloat16, false>);
+  auto kern = kv->head_dim == 128 ? (quant ? attend_simple_kernel<128, true> : attend_simple_kernel<128, false>)
+                                  : (quant ? attend_simple_kernel<64, true> : attend_simple_kernel<64, false>);
   kern<<<(unsigned)blocks, 128, 0, st>>>(p);
   if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return call_error(DFLASH_ECUDA, "attend", e);
   return DFLASH_OK;

@@ -23,6 +23,7 @@ struct AttendParams {
   const unsigned long long* masks;
   const int32_t* positions;
   int words;
+  bool quant;        // pages in 8 bits
 };
 
 // Workspace of the tensor-core form: split units' partials.

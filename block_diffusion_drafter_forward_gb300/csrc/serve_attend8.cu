@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(Geo::kThreads, 1) attend8_kernel(const AttendP
     const int pages = (q.kv + kPage - 1) / kPage, end = min(pages, q.k0 / kPage + q.c_hi * kW);
     for (int lp = q.k0 / kPage + q.c_lo * kW + warp; lp < end; lp += kW, ++i) {
       const int b = i % C::kStages;
-      if (!mbar_wait_ab(&c.full[warp][b], (i / C::kStages) & 1, flags)) break;
+      if (!__all_sync(0xffffffffu, mbar_wait_ab(&c.full[warp][b], (i / C::kStages) & 1, flags))) break;  // (the lanes together)
       uint8_t* tile = ring + (warp * C::kStages + b) * C::kBytes;
       const int key0 = lp * kPage + 4 * j;
       if ((lp + 1) * kPage > q.kv) {

@@ -56,11 +56,10 @@ using plan::shape_of;
 
 constexpr int kKeys = 128;                      // keys per chunk
 constexpr int kPages = kKeys / kPage;           // 8
-constexpr int kThreads = 384;
+template <bool kQuant>
 struct Geo {
-  static constexpr int kKeys = 128, kUnitCost = 3, kThreads = 384;
+  static constexpr int kKeys = 128, kUnitCost = 3, kThreads = kQuant ? 512 : 384;
 };
-constexpr int kCtl = 2944;                      // barriers, plan, row exchange
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
   asm volatile(
@@ -76,25 +75,33 @@ __device__ __forceinline__ bool wait_ab(uint64_t* bar, uint32_t parity, volatile
   return mbar_try_wait(bar, parity) || mbar_wait_ab(bar, parity, abort);
 }
 
-template <int HD, int NT>
+template <int HD, int NT, bool kQuant>
 struct Cfg {
   static constexpr int kTile = kPage * HD * 2;         // a page of one head: bytes of K (or V)
   static constexpr int kQ = 128 * HD * 2;              // a query tile
   static constexpr int kSlot = kPages * kTile;         // a chunk's K (or V)
-  static constexpr int kNK = HD == 128 ? 3 : 6;        // K and V slots in flight
-  static constexpr int kNV = HD == 128 ? 2 : 6;
-  static constexpr int kSmem = 2 * kQ + (kNK + kNV) * kSlot + kCtl;  // (queries: two tiles, or two segments' tile)
+  static constexpr int kQTiles = kQuant && NT == 1 ? 1 : 2;  // queries: two tiles, or two segments' tile (8 bits: one segment's)
+  static constexpr int kNK = kQuant ? (HD == 128 ? 2 : 3) : HD == 128 ? 3 : 6;  // K and V slots in flight
+  static constexpr int kNV = kQuant ? (HD == 128 ? 2 : 3) : HD == 128 ? 2 : 6;
+  // 8 bits: halves of a chunk as they are in the pages
+  static constexpr int kCodes = 32 * HD + 32;          // a page of one head
+  static constexpr int kNS = !kQuant ? 1 : HD == 64 ? 6 : NT == 1 ? 4 : 2;
+  static constexpr int kHalf = kQuant ? kPages / 2 * kCodes : 0;
+  static constexpr int kCtl = kQuant ? 2560 : 2944;    // barriers, plan, row exchange
+  static constexpr int kSmem = kQTiles * kQ + (kNK + kNV) * kSlot + kNS * kHalf + kCtl;
+  static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
 
+template <class C, class G>
 struct Ctl {
-  uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6], v_raw[6];
-  uint64_t s_full[2], p_half[2], p_full[2], o_done[2], o_free[2], q_full[2];
+  uint64_t k_full[C::kNK], k_empty[C::kNK], v_full[C::kNV], v_empty[C::kNV], v_raw[C::kNV];
+  uint64_t st_full[C::kNS], st_empty[C::kNS];
+  uint64_t s_full[2], p_half[2], p_full[2], o_done[2], o_free[2], q_full[2], q_empty;
   uint32_t tmem_slot;
   int flags[2];
-  PlanCtl<Geo> plan;
+  PlanCtl<G> plan;
   float2 ml[2][128];  // one tile: the streams' (m, l) of every row
 };
-static_assert(sizeof(Ctl) <= kCtl, "control block overflows its slot");
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -154,11 +161,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // The chunks of stream x, in order, as every role counts them.
-template <bool kTree> using Walk = plan::Walk<Geo, kTree>;
-
-template <int NT, bool kTree>
+template <int NT, class Walk>
 struct It {
-  Walk<kTree> w;
+  Walk w;
   Seg sg;
   int j, n;        // chunk within the segment, chunks of it
   int kc0;         // chunks of the segments before it
@@ -183,7 +188,7 @@ struct It {
     }
     return false;
   }
-  __device__ void start(const AttendParams& p, const Shape& h, const Walk<kTree>& w0, int x) {
+  __device__ void start(const AttendParams& p, const Shape& h, const Walk& w0, int x) {
     w = w0;
     kc0 = it = 0;
     seg = act = -1;
@@ -204,14 +209,182 @@ struct It {
   }
 };
 
-template <int HD, int NT, bool kTree>
-__global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendParams p, const AttendWork wk, const __grid_constant__ CUtensorMap q_map) {
-  using C = Cfg<HD, NT>;
+// ---- Pages in 8 bits.  A chunk comes as two halves of four pages (K and V codes and their exponents, one copy a
+// page), and four warps write its values as bf16 into the K and V slots, in the layout that pages of
+// bf16 have.
+
+// A warp's wait: its lanes go on, or give up, together.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, wait_ab(bar, parity, abort));
+}
+
+// Warp 8: lane l copies page l of a half.
+template <class C, class Walk, class Ctl>
+__device__ __forceinline__ void load_codes(const AttendParams& p, const Shape& h, const Walk& walk, uint8_t* stage, Ctl& c, int lane) {
+  volatile int* flags = c.flags;
+  Walk w = walk;
+  Seg q;
+  int i = 0;  // halves so far
+  while (w.next(p, h, q)) {
+    const int pages = (q.kv + kPage - 1) / kPage;
+    const int first = q.k0 / kPage + q.c_lo * kPages, end = min(pages, q.k0 / kPage + q.c_hi * kPages);
+    const int32_t* table = p.page_tables + (int64_t)q.s * p.mpps;
+    auto fetch = [&](int lp) { return lane < kPages / 2 && lp < end ? __ldg(table + lp) : 0; };
+    int page = fetch(first + lane);
+    for (int lp = first; lp < end; lp += kPages / 2, ++i) {
+      const int b = i % C::kNS, n = min(kPages / 2, end - lp);
+      if (i >= C::kNS && !warp_wait(&c.st_empty[b], (i / C::kNS - 1) & 1, flags)) return;
+      if (lane == 0) mbar_arrive_expect_tx(&c.st_full[b], n * C::kCodes);
+      __syncwarp();
+      if (lane < n) {
+        if (page < 0 || page >= p.num_pages) {
+          if (p.status) atomicOr(p.status, DFLASH_DEV_BAD_PAGE);
+          page = 0;
+        }
+        bulk_load(stage + b * C::kHalf + lane * C::kCodes, static_cast<const uint8_t*>(p.pool) + page * p.page_stride + (int64_t)q.g * C::kCodes,
+                  C::kCodes, &c.st_full[b]);
+      }
+      page = fetch(lp + kPages / 2 + lane);
+    }
+  }
+}
+
+// Codes 0, 1 and 2, 3 of a word as pairs of bf16, times 2^-120: sign, exponent and mantissa << 4.
+__device__ __forceinline__ uint2 widen(uint32_t w) {
+  uint32_t a, b;  // each byte with its sign in the byte above, moved up by 4
+  asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(a) : "r"(w));
+  asm("prmt.b32 %0, %1, 0, 0xb3a2;" : "=r"(b) : "r"(w));
+  asm("mad.lo.u32 %0, %0, 16, 0;" : "+r"(a));  // (a shift, off the pipe of the permutes)
+  asm("mad.lo.u32 %0, %0, 16, 0;" : "+r"(b));
+  return make_uint2(a & 0x87f087f0u, b & 0x87f087f0u);
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+  return a;
+}
+
+// Warps 12 - 15 (`sub` 0 - 3): the values of a half.  K: a lane has 16 dims of a row, V: eight rows of four dims;
+// eight lanes write 128 bytes in a row, and read as many from different banks.  A row's factor
+// 2^(e - 127 + 120) is a bf16 number up to e = 134; beyond (values from 2^15 on) it goes in two steps.
+template <int HD, class C, class Walk, class Ctl>
+__device__ __forceinline__ void widen_codes(const AttendParams& p, const Shape& h, const Walk& walk, const uint8_t* stage, uint8_t* sK, uint8_t* sV,
+                                            Ctl& c, int sub, int lane) {
+  volatile int* flags = c.flags;
+  Walk w = walk;
+  Seg q;
+  int i = 0, kc = 0;  // halves copied, chunks so far
+  while (w.next(p, h, q)) {
+    const int pages = (q.kv + kPage - 1) / kPage;
+    for (int ch = q.c_lo; ch < q.c_hi; ++ch, ++kc) {
+      const int lp0 = q.k0 / kPage + ch * kPages, kb = kc % C::kNK, vb = kc % C::kNV;
+      uint8_t *kd = sK + kb * C::kSlot, *vd = sV + vb * C::kSlot;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        const int lp = lp0 + half * (kPages / 2), n = max(0, min(kPages / 2, pages - lp)), b = i % C::kNS;
+        const uint8_t* src = stage + b * C::kHalf;
+        if (n > 0 && !warp_wait(&c.st_full[b], (i / C::kNS) & 1, flags)) return;
+        if (half == 0 && kc >= C::kNK && !warp_wait(&c.k_empty[kb], (kc / C::kNK - 1) & 1, flags)) return;
+        // K: lane (row % 8, row / 8, dims 16 x of a pair)
+        const int j = lane & 15;
+        for (int e = sub; e < n * (HD / 32); e += 4) {
+          const int pg = e / (HD / 32), x = e % (HD / 32) * 2 + (lane >> 4);  // page, 16 dims
+          const uint8_t* tile = src + pg * C::kCodes;
+          const uint4 v = *reinterpret_cast<const uint4*>(tile + (x >> 2) * 1024 + j * 64 + (((x & 3) ^ (j >> 1 & 3)) * 16));
+          const uint32_t ex = tile[32 * HD + j];
+          uint32_t f = min(ex + 120, 254u) << 7;
+          f |= f << 16;
+          uint2 y[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            y[k] = widen((&v.x)[k]);
+            y[k].x = mul2(y[k].x, f), y[k].y = mul2(y[k].y, f);
+          }
+          if (__any_sync(0xffffffffu, ex > 134)) {
+            const uint32_t up = (max(ex, 134u) - 134 + 127) << 7, g = up | up << 16;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k].x = mul2(y[k].x, g), y[k].y = mul2(y[k].y, g);
+          }
+          uint8_t* dst = kd + (half * (kPages / 2) + pg) * C::kTile + ((j >> 3) * (HD / 8) + 2 * x) * 128 + (j & 7) * 16;
+          *reinterpret_cast<uint4*>(dst) = make_uint4(y[0].x, y[0].y, y[1].x, y[1].y);
+          *reinterpret_cast<uint4*>(dst + 128) = make_uint4(y[2].x, y[2].y, y[3].x, y[3].y);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c.k_full[kb]);
+        if (half == 0 && kc >= C::kNV && !warp_wait(&c.v_empty[vb], (kc / C::kNV - 1) & 1, flags)) return;
+        // V: lane (dim % 8, rows 8 r .., dims 32 g + dim % 8 + 8 k).  Rows behind the sequence's end become zeros
+        // (they may hold anything, and zero times NaN would reach O); a unit without keys has a page of them.
+        const int m = lane & 7, r = lane >> 3 & 1;
+        const int nv = half == 0 ? max(n, 1) : n;
+        for (int e = sub; e < nv * (HD / 64); e += 4) {
+          const int pg = e / (HD / 64), g = e % (HD / 64) * 2 + (lane >> 4);
+          const uint8_t* tile = src + pg * C::kCodes;
+          const int live = n == 0 ? 0 : q.kv - (lp + pg) * kPage - 8 * r;  // rows of the eight that are
+          uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+          uint2 ex = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+          if (live > 0) {
+            lo = *reinterpret_cast<const uint4*>(tile + 16 * HD + g * 512 + m * 64 + ((2 * r) ^ (m >> 1)) * 16);
+            hi = *reinterpret_cast<const uint4*>(tile + 16 * HD + g * 512 + m * 64 + ((2 * r + 1) ^ (m >> 1)) * 16);
+            ex = *reinterpret_cast<const uint2*>(tile + 32 * HD + 16 + 8 * r);
+          }
+          if (live < 8 && live > 0) {
+            const uint32_t dl = live >= 4 ? 0u : 0xffffffffu << 8 * live, dh = live <= 4 ? 0xffffffffu : 0xffffffffu << 8 * (live - 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) (&lo.x)[k] &= ~dl, (&hi.x)[k] &= ~dh;
+            ex.x = (ex.x & ~dl) | (0x7f7f7f7fu & dl), ex.y = (ex.y & ~dh) | (0x7f7f7f7fu & dh);
+          }
+          uint32_t f[4];  // factors of two rows
+          const uint32_t top = max(__vmaxu4(ex.x, ex.y) >> 24, max(__vmaxu4(ex.x, ex.y) >> 16 & 255, max(__vmaxu4(ex.x, ex.y) >> 8 & 255, __vmaxu4(ex.x, ex.y) & 255)));
+          auto factors = [&](int add, uint32_t least) {  // 2^(max(e, least) + add - 127), at most 2^127
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t z = (k < 2 ? ex.x : ex.y) >> 16 * (k & 1);
+              f[k] = min(max(z & 255, least) + add, 254u) << 7 | min(max(z >> 8 & 255, least) + add, 254u) << 23;
+            }
+          };
+          factors(120, 0);
+          uint32_t y[4][4];  // [dim][pair of rows]
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint2 a = widen((&lo.x)[k]), z = widen((&hi.x)[k]);
+            y[k][0] = mul2(a.x, f[0]), y[k][1] = mul2(a.y, f[1]), y[k][2] = mul2(z.x, f[2]), y[k][3] = mul2(z.y, f[3]);
+          }
+          if (__any_sync(0xffffffffu, top > 134)) {
+            factors(-7, 134);  // 2^(max(e, 134) - 134)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) y[k][u] = mul2(y[k][u], f[u]);
+          }
+          uint8_t* dst = vd + (half * (kPages / 2) + pg) * C::kTile + m * 16;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(dst + ((g * 4 + k) * 2 + r) * 128) = make_uint4(y[k][0], y[k][1], y[k][2], y[k][3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&c.v_full[vb]);
+          if (n > 0) mbar_arrive(&c.st_empty[b]);
+        }
+        if (n > 0) ++i;
+      }
+    }
+  }
+}
+
+template <int HD, int NT, bool kTree, bool kQuant>
+__global__ void __launch_bounds__(Geo<kQuant>::kThreads, 1) attend_tc_kernel(const AttendParams p, const AttendWork wk, const __grid_constant__ CUtensorMap q_map) {
+  using C = Cfg<HD, NT, kQuant>;
+  using Walk = plan::Walk<Geo<kQuant>, kTree>;
+  constexpr int kThreads = Geo<kQuant>::kThreads;
+  static_assert(sizeof(Ctl<C, Geo<kQuant>>) <= C::kCtl, "control block overflows its slot");
   extern __shared__ __align__(1024) uint8_t smem[];  // (the queries' swizzle counts from 1 KB boundaries)
   uint8_t* sQ = smem;
-  uint8_t* sK = sQ + 2 * C::kQ;
+  uint8_t* sK = sQ + C::kQTiles * C::kQ;
   uint8_t* sV = sK + C::kNK * C::kSlot;
-  Ctl& c = *reinterpret_cast<Ctl*>(sV + C::kNV * C::kSlot);
+  uint8_t* sS = sV + C::kNV * C::kSlot;  // 8 bits: halves of chunks
+  auto& c = *reinterpret_cast<Ctl<C, Geo<kQuant>>*>(sS + (kQuant ? C::kNS * C::kHalf : 0));
   volatile int* flags = c.flags;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const Shape h = shape_of(p, NT);
@@ -219,19 +392,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
   pdl_wait();  // everything read here may come from the kernel before
   if (t == 0) wk.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
   long long W;
-  const Walk<kTree> walk = plan::make<Geo, kTree>(p, h, c.plan, reinterpret_cast<long long*>(sK), wk.long_chunks, &W);
+  const Walk walk = plan::make<Geo<kQuant>, kTree>(p, h, c.plan, reinterpret_cast<long long*>(sK), wk.long_chunks, &W);
   if (walk.lo >= walk.hi) {  // nothing for this CTA
     pdl_trigger();
     return;
   }
   if (t == 0) {
-    for (int i = 0; i < 6; ++i) {
-      mbar_init(&c.k_full[i], 1);
+    for (int i = 0; i < C::kNK; ++i) {
+      mbar_init(&c.k_full[i], kQuant ? 8 : 1);  // (8 bits: four warps, twice)
       mbar_init(&c.k_empty[i], NT);
-      mbar_init(&c.v_full[i], 1);
+    }
+    for (int i = 0; i < C::kNV; ++i) {
+      mbar_init(&c.v_full[i], kQuant ? 8 : 1);
       mbar_init(&c.v_empty[i], NT);
       mbar_init(&c.v_raw[i], 1);
     }
+    for (int i = 0; i < C::kNS; ++i) {
+      mbar_init(&c.st_full[i], 1);
+      mbar_init(&c.st_empty[i], 4);
+    }
+    mbar_init(&c.q_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.s_full[i], 1);
       mbar_init(&c.p_half[i], 128);
@@ -245,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
   }
   // rows that no query fills stay finite
   if (h.group * h.T < 128)
-    for (int i = t; i < 2 * C::kQ / 16; i += kThreads) reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = t; i < C::kQTiles * C::kQ / 16; i += kThreads) reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();  // the plan's scratch is overwritten by copies
   if (warp == 0) tmem_alloc(&c.tmem_slot, 512);
   tc_fence_before();
@@ -263,8 +443,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
   };
 
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    if (warp == 8 || warp == 10) {
+    if (kQuant)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");  // (of 128 at launch: 8 warps with 192, 8 with 64)
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if constexpr (kQuant) {
+      if (warp == 8) {
+        load_codes<C>(p, h, walk, sS, c, lane);
+      } else if (warp >= 12) {
+        widen_codes<HD, C>(p, h, walk, sS, sK, sV, c, warp - 12, lane);
+      } else if (NT == 1 && warp == 10 && lane == 0) {
+        // queries of one segment at a time: once the last S of the one before is done
+        Walk w = walk;
+        Seg q;
+        for (int i = 0; w.next(p, h, q); ++i) {
+          if (i > 0 && !wait_ab(&c.q_empty, (i - 1) & 1, flags)) break;
+          load_q(q, 0);
+        }
+      }
+    }
+    if (!kQuant && (warp == 8 || warp == 10)) {
       // ---- page producers: lane l copies page l of a chunk.  The page ids of the next chunk are
       // fetched while the warp waits for a slot.  V of a chunk whose last page is part full (or that
       // has no page) lands on v_raw; the V warp zeroes its rows behind the end when it has come,
@@ -274,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
       uint64_t* empty = kv ? c.v_empty : c.k_empty;
       uint8_t* ring = kv ? sV : sK;
       const int slots = kv ? C::kNV : C::kNK;
-      Walk<kTree> w = walk;
+      Walk w = walk;
       Seg q;
       int i = 0;
       bool stop = false;
@@ -349,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         }
       }
       if (!stop) mend();
-    } else if (lane == 0) {
+    } else if (lane == 0 && (!kQuant || warp == 9 || warp == 11)) {
       // ---- MMA issue
       constexpr uint32_t id_s = idesc_bf16(128, kKeys), id_o = idesc_bf16(128, HD);
       // operand descriptors of the first tiles; the others are further on (16-byte units)
@@ -374,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
       if (NT == 2) {
         // one stream: S of a chunk, then its P V and the next S as soon as the softmax has written P
         const int x = warp == 9 ? 0 : 1;
-        Walk<kTree> w = walk;
+        Walk w = walk;
         Seg q;
         int kc = 0, it = 0, act = 0;
         auto wait = [&](uint64_t* bar, int phase) {
@@ -389,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         };
         while (w.next(p, h, q)) {
           const int n = q.c_hi - q.c_lo;
-          if (!It<NT, kTree>::active(h, q, x)) {
+          if (!It<NT, Walk>::active(h, q, x)) {
             // no row of this stream: it still follows every slot, so that its waits stay exact
             for (int j = 0; j < n; ++j, ++kc) {
               wait(&c.k_full[kc % C::kNK], kc / C::kNK);
@@ -423,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         }
       } else if (warp == 9) {
         // both streams: each alternates S and P V; whichever is ready goes out
-        It<NT, kTree> its[2];
+        It<NT, Walk> its[2];
         bool pv[2] = {false, false};
         its[0].start(p, h, walk, 0);
         its[1].start(p, h, walk, 1);
@@ -435,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
           bool did = false;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            It<NT, kTree>& a = its[x];
+            It<NT, Walk>& a = its[x];
             const bool give_up = flags[0];  // after a timeout: commits only, no MMAs
             if (a.valid && pv[x]) {
               const int kc = a.kc0 + a.j, vb = kc % C::kNV;
@@ -459,11 +657,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
             if (a.valid && !pv[x]) {
               const int kc = a.kc0 + a.j, kb = kc % C::kNK;
               if (give_up || (kc == s_next && mbar_test_wait(&c.k_full[kb], (kc / C::kNK) & 1) &&
-                              (!a.first(x) || mbar_test_wait(&c.q_full[a.seg & 1], a.seg >> 1 & 1)))) {
+                              (!a.first(x) || (kQuant ? mbar_test_wait(&c.q_full[0], a.seg & 1) : mbar_test_wait(&c.q_full[a.seg & 1], a.seg >> 1 & 1))))) {
                 tc_fence_after();
-                if (!give_up) issue_s(x, a.seg & 1, kb);
+                if (!give_up) issue_s(x, kQuant ? 0 : a.seg & 1, kb);
                 mma_commit(&c.s_full[x]);
                 mma_commit(&c.k_empty[kb]);
+                if (kQuant && a.j + 1 == a.n) mma_commit(&c.q_empty);  // (S goes in chunk order: the segment's last)
                 ++s_next;
                 pv[x] = true;
                 did = true;
@@ -477,22 +676,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
     }
     __syncwarp();
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    if (kQuant)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ---- softmax streams: thread = query row `row` of its tile
     const int x = warp >> 2, row = t & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + x * 128 + lane_off;
     const int tok = row / h.group, head = row - tok * h.group;  // (by p.inv the loop's registers fall worse: 519 us for 499)
-    const bool loads = (t & 127) == 0 && (NT == 2 || x == 0);  // (one tile: stream 0's, a segment ahead)
-    Walk<kTree> w = walk;
+    const bool loads = (t & 127) == 0 && (NT == 2 || (x == 0 && !kQuant));  // (one tile: stream 0's, a segment ahead)
+    Walk w = walk;
     Seg q, nq;
     bool have = w.next(p, h, q);
-    while (NT == 2 && have && !It<NT, kTree>::active(h, q, x)) have = w.next(p, h, q);
+    while (NT == 2 && have && !It<NT, Walk>::active(h, q, x)) have = w.next(p, h, q);
     if (have && loads) load_q(q, x);
     int it = 0, seg = 0;  // chunks and segments done by this stream
     while (have) {
       bool more = w.next(p, h, nq);
-      while (NT == 2 && more && !It<NT, kTree>::active(h, nq, x)) more = w.next(p, h, nq);
+      while (NT == 2 && more && !It<NT, Walk>::active(h, nq, x)) more = w.next(p, h, nq);
       const int n = q.c_hi - q.c_lo;
       const int tk = q.t0 + (NT == 2 ? x * h.T : 0) + tok;
       const bool valid = tok < h.T && tk < q.n;
@@ -813,24 +1015,30 @@ cudaError_t combine(const AttendParams& p, const AttendWork& w, int sms, cudaStr
   return cudaLaunchKernelEx(&c, attend_combine_kernel<HD, NT>, p, w);
 }
 
-template <int HD, int NT, bool kTree>
+template <int HD, int NT, bool kTree, bool kQuant>
 cudaError_t launch(const AttendParams& p, const AttendWork& w, int sms, cudaStream_t st) {
   static std::atomic<unsigned long long> attr{0};
-  if (cudaError_t e = smem_attr_once(attend_tc_kernel<HD, NT, kTree>, Cfg<HD, NT>::kSmem, attr); e != cudaSuccess) return e;
+  if (cudaError_t e = smem_attr_once(attend_tc_kernel<HD, NT, kTree, kQuant>, Cfg<HD, NT, kQuant>::kSmem, attr); e != cudaSuccess) return e;
   cudaLaunchAttribute a[1];
   a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   a[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(sms);
-  c.blockDim = dim3(kThreads);
-  c.dynamicSmemBytes = Cfg<HD, NT>::kSmem;
+  c.blockDim = dim3(Geo<kQuant>::kThreads);
+  c.dynamicSmemBytes = Cfg<HD, NT, kQuant>::kSmem;
   c.stream = st;
   c.attrs = a;
   c.numAttrs = 1;
   CUtensorMap q_map;
   if (!make_tmap_heads_bf16(&q_map, p.q, p.n_rows, p.nh, HD, p.q_stride, p.group, p.tokens)) return cudaErrorInvalidValue;
-  if (cudaError_t e = cudaLaunchKernelEx(&c, attend_tc_kernel<HD, NT, kTree>, p, w, q_map); e != cudaSuccess) return e;
+  if (cudaError_t e = cudaLaunchKernelEx(&c, attend_tc_kernel<HD, NT, kTree, kQuant>, p, w, q_map); e != cudaSuccess) return e;
   return combine<HD, NT>(p, w, sms, st);
+}
+
+template <bool kTree, bool kQuant>
+cudaError_t launch_form(const AttendParams& p, const AttendWork& w, int head_dim, bool two, int sms, cudaStream_t st) {
+  if (head_dim == 128) return two ? launch<128, 2, kTree, kQuant>(p, w, sms, st) : launch<128, 1, kTree, kQuant>(p, w, sms, st);
+  return two ? launch<64, 2, kTree, kQuant>(p, w, sms, st) : launch<64, 1, kTree, kQuant>(p, w, sms, st);
 }
 
 }  // namespace
@@ -864,12 +1072,8 @@ cudaError_t launch_attend_tc(const AttendParams& p, int head_dim, int max_new, v
   // (8 x 256 on 2048).
   const bool two = max_new > T && ((int64_t)p.n_rows + T - 1) / T * p.nkv * 2 >= sms;
   w.long_chunks = max_new > 4 * (two ? 2 * T : T);
-  if (p.masks) {
-    if (head_dim == 128) return two ? launch<128, 2, true>(p, w, sms, st) : launch<128, 1, true>(p, w, sms, st);
-    return two ? launch<64, 2, true>(p, w, sms, st) : launch<64, 1, true>(p, w, sms, st);
-  }
-  if (head_dim == 128) return two ? launch<128, 2, false>(p, w, sms, st) : launch<128, 1, false>(p, w, sms, st);
-  return two ? launch<64, 2, false>(p, w, sms, st) : launch<64, 1, false>(p, w, sms, st);
+  if (p.quant) return p.masks ? launch_form<true, true>(p, w, head_dim, two, sms, st) : launch_form<false, true>(p, w, head_dim, two, sms, st);
+  return p.masks ? launch_form<true, false>(p, w, head_dim, two, sms, st) : launch_form<false, false>(p, w, head_dim, two, sms, st);
 }
 
 }  // namespace dflash
