@@ -87,7 +87,7 @@ struct Cfg {
   static constexpr int kCodes = 32 * HD + 32;          // a page of one head
   static constexpr int kNS = !kQuant ? 1 : HD == 64 ? 6 : NT == 1 ? 4 : 2;
   static constexpr int kHalf = kQuant ? kPages / 2 * kCodes : 0;
-  static constexpr int kCtl = kQuant ? 2560 : 2944;    // barriers, plan, row exchange
+  static constexpr int kCtl = kQuant && HD == 128 ? 2560 : 2944;    // barriers, plan, row exchange
   static constexpr int kSmem = kQTiles * kQ + (kNK + kNV) * kSlot + kNS * kHalf + kCtl;
   static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
@@ -96,6 +96,7 @@ template <class C, class G>
 struct Ctl {
   uint64_t k_full[C::kNK], k_empty[C::kNK], v_full[C::kNV], v_empty[C::kNV], v_raw[C::kNV];
   uint64_t st_full[C::kNS], st_empty[C::kNS];
+  int2 half[C::kNS];  // pages of the half, rows of the sequence from its first on
   uint64_t s_full[2], p_half[2], p_full[2], o_done[2], o_free[2], q_full[2], q_empty;
   uint32_t tmem_slot;
   int flags[2];
@@ -211,14 +212,16 @@ struct It {
 
 // ---- Pages in 8 bits.  A chunk comes as two halves of four pages (K and V codes and their exponents, one copy a
 // page), and four warps write its values as bf16 into the K and V slots, in the layout that pages of
-// bf16 have.
+// bf16 have: two for K, which is wanted first, and two for V.
 
 // A warp's wait: its lanes go on, or give up, together.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xffffffffu, wait_ab(bar, parity, abort));
 }
 
-// Warp 8: lane l copies page l of a half.
+// Warp 8: lane l copies page l of a half.  Every half of every chunk has its turn, those without pages too; what the
+// widening warps have to know of it lies beside its barrier, so that they need no walk of their own (its
+// registers would spill, and local memory has next to no L1 beside 227 KB of shared memory).
 template <class C, class Walk, class Ctl>
 __device__ __forceinline__ void load_codes(const AttendParams& p, const Shape& h, const Walk& walk, uint8_t* stage, Ctl& c, int lane) {
   volatile int* flags = c.flags;
@@ -227,14 +230,17 @@ __device__ __forceinline__ void load_codes(const AttendParams& p, const Shape& h
   int i = 0;  // halves so far
   while (w.next(p, h, q)) {
     const int pages = (q.kv + kPage - 1) / kPage;
-    const int first = q.k0 / kPage + q.c_lo * kPages, end = min(pages, q.k0 / kPage + q.c_hi * kPages);
+    const int first = q.k0 / kPage + q.c_lo * kPages, end = q.k0 / kPage + q.c_hi * kPages;
     const int32_t* table = p.page_tables + (int64_t)q.s * p.mpps;
-    auto fetch = [&](int lp) { return lane < kPages / 2 && lp < end ? __ldg(table + lp) : 0; };
+    auto fetch = [&](int lp) { return lane < kPages / 2 && lp < min(end, pages) ? __ldg(table + lp) : 0; };
     int page = fetch(first + lane);
     for (int lp = first; lp < end; lp += kPages / 2, ++i) {
-      const int b = i % C::kNS, n = min(kPages / 2, end - lp);
+      const int b = i % C::kNS, n = max(0, min(kPages / 2, pages - lp));
       if (i >= C::kNS && !warp_wait(&c.st_empty[b], (i / C::kNS - 1) & 1, flags)) return;
-      if (lane == 0) mbar_arrive_expect_tx(&c.st_full[b], n * C::kCodes);
+      if (lane == 0) {
+        c.half[b] = make_int2(n, q.kv - lp * kPage);  // pages, rows from its first on
+        mbar_arrive_expect_tx(&c.st_full[b], n * C::kCodes);
+      }
       __syncwarp();
       if (lane < n) {
         if (page < 0 || page >= p.num_pages) {
@@ -246,6 +252,12 @@ __device__ __forceinline__ void load_codes(const AttendParams& p, const Shape& h
       }
       page = fetch(lp + kPages / 2 + lane);
     }
+  }
+  const int b = i % C::kNS;
+  if (i >= C::kNS && !warp_wait(&c.st_empty[b], (i / C::kNS - 1) & 1, flags)) return;
+  if (lane == 0) {
+    c.half[b] = make_int2(-1, 0);  // no more
+    mbar_arrive(&c.st_full[b]);
   }
 }
 
@@ -263,112 +275,97 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   return a;
 }
 
-// Warps 12 - 15 (`sub` 0 - 3): the values of a half.  K: a lane has 16 dims of a row, V: eight rows of four dims;
-// eight lanes write 128 bytes in a row, and read as many from different banks.  A row's factor
-// 2^(e - 127 + 120) is a bf16 number up to e = 134; beyond (values from 2^15 on) it goes in two steps.
-template <int HD, class C, class Walk, class Ctl>
-__device__ __forceinline__ void widen_codes(const AttendParams& p, const Shape& h, const Walk& walk, const uint8_t* stage, uint8_t* sK, uint8_t* sV,
-                                            Ctl& c, int sub, int lane) {
-  volatile int* flags = c.flags;
-  Walk w = walk;
-  Seg q;
-  int i = 0, kc = 0;  // halves copied, chunks so far
-  while (w.next(p, h, q)) {
-    const int pages = (q.kv + kPage - 1) / kPage;
-    for (int ch = q.c_lo; ch < q.c_hi; ++ch, ++kc) {
-      const int lp0 = q.k0 / kPage + ch * kPages, kb = kc % C::kNK, vb = kc % C::kNV;
-      uint8_t *kd = sK + kb * C::kSlot, *vd = sV + vb * C::kSlot;
+// One warp's pages (pg and pg + 2) of a half, of whose rows `rows` are the sequence's.  K: a lane has dims 16 x .. of row j,
+// for two x at a time.  V: rows 8 r .. of dims 32 g + m + 8 k; rows from `rows` on become zeros (they may hold
+// anything, and zero times NaN would reach O).  Eight lanes write 128 bytes in a row, and read as many from
+// different banks.  A row's factor 2^(e - 127 + 120) is a bf16 number up to e = 134; rows beyond (values from
+// 2^15 on, kFar) go in two steps.  A loop, not unrolled: the roles' code together is more than the instruction
+// caches hold (both pages unrolled: 3.6 us a chunk for 2.3).
+template <int HD, class C, bool kV, bool kFar>
+__device__ __forceinline__ void widen_pages(const uint8_t* half, uint8_t* dst, int pg, int n, int rows, int lane) {
+  const int j = lane & 15, m = lane & 7, r = lane >> 3 & 1, up = lane >> 4;
+  const uint8_t* src = half + pg * C::kCodes + (kV ? 16 * HD + up * 512 + m * 64 : j * 64);
+  const int u0 = kV ? (2 * r) ^ (m >> 1) : up ^ (j >> 1 & 3);  // the first unit of 16 bytes; the other differs in bit 0 (V), 1 (K)
+  const uint8_t* ex = half + pg * C::kCodes + 32 * HD + (kV ? 16 + 8 * r : j);
+  dst += pg * C::kTile + (kV ? m * 16 + r * 128 + up * 1024 : r * (HD * 16) + m * 16 + up * 256);
+  for (; pg < n; pg += 2, src += 2 * C::kCodes, ex += 2 * C::kCodes, dst += 2 * C::kTile) {
+    uint32_t e0, e1;
+    if (kV) {
+      const uint2 e = *reinterpret_cast<const uint2*>(ex);
+      e0 = e.x, e1 = e.y;
+    } else {
+      e0 = e1 = *ex * 0x01010101u;
+    }
+    uint32_t d0 = 0, d1 = 0;
+    if (kV && (pg + 1) * kPage > rows) {
+      const int live = rows - pg * kPage - 8 * r;  // rows of the eight that are
+      d0 = live <= 0 ? 0xffffffffu : live >= 4 ? 0u : 0xffffffffu << 8 * live;
+      d1 = live <= 4 ? 0xffffffffu : live >= 8 ? 0u : 0xffffffffu << 8 * (live - 4);
+      e0 = (e0 & ~d0) | (0x7f7f7f7fu & d0), e1 = (e1 & ~d1) | (0x7f7f7f7fu & d1);
+    }
+    uint32_t f[4], g[4];  // factors of two rows
+#pragma unroll
+    for (int k = 0; k < (kV ? 4 : 1); ++k) {
+      const uint32_t z = __byte_perm(k < 2 ? e0 : e1, 0, k & 1 ? 0x4342 : 0x4140);  // their exponent bytes, one to a half
+      f[k] = (kFar ? __vminu2(z + 0x00780078u, 0x00fe00feu) : z + 0x00780078u) << 7;
+      g[k] = kFar ? (__vmaxu2(z, 0x00860086u) - 0x00070007u) << 7 : 0;  // 2^(e - 134), at least 1
+    }
+    auto turn = [&](uint32_t a, int k) { return kFar ? mul2(mul2(a, f[k]), g[k]) : mul2(a, f[k]); };
 #pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        const int lp = lp0 + half * (kPages / 2), n = max(0, min(kPages / 2, pages - lp)), b = i % C::kNS;
-        const uint8_t* src = stage + b * C::kHalf;
-        if (n > 0 && !warp_wait(&c.st_full[b], (i / C::kNS) & 1, flags)) return;
-        if (half == 0 && kc >= C::kNK && !warp_wait(&c.k_empty[kb], (kc / C::kNK - 1) & 1, flags)) return;
-        // K: lane (row % 8, row / 8, dims 16 x of a pair)
-        const int j = lane & 15;
-        for (int e = sub; e < n * (HD / 32); e += 4) {
-          const int pg = e / (HD / 32), x = e % (HD / 32) * 2 + (lane >> 4);  // page, 16 dims
-          const uint8_t* tile = src + pg * C::kCodes;
-          const uint4 v = *reinterpret_cast<const uint4*>(tile + (x >> 2) * 1024 + j * 64 + (((x & 3) ^ (j >> 1 & 3)) * 16));
-          const uint32_t ex = tile[32 * HD + j];
-          uint32_t f = min(ex + 120, 254u) << 7;
-          f |= f << 16;
-          uint2 y[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            y[k] = widen((&v.x)[k]);
-            y[k].x = mul2(y[k].x, f), y[k].y = mul2(y[k].y, f);
-          }
-          if (__any_sync(0xffffffffu, ex > 134)) {
-            const uint32_t up = (max(ex, 134u) - 134 + 127) << 7, g = up | up << 16;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) y[k].x = mul2(y[k].x, g), y[k].y = mul2(y[k].y, g);
-          }
-          uint8_t* dst = kd + (half * (kPages / 2) + pg) * C::kTile + ((j >> 3) * (HD / 8) + 2 * x) * 128 + (j & 7) * 16;
-          *reinterpret_cast<uint4*>(dst) = make_uint4(y[0].x, y[0].y, y[1].x, y[1].y);
-          *reinterpret_cast<uint4*>(dst + 128) = make_uint4(y[2].x, y[2].y, y[3].x, y[3].y);
+    for (int e = 0; e < HD / 64; ++e) {
+      const uint8_t* s = src + e * 1024;
+      uint4 lo = *reinterpret_cast<const uint4*>(s + u0 * 16), hi = *reinterpret_cast<const uint4*>(s + (u0 ^ (kV ? 1 : 2)) * 16);
+      uint8_t* d = dst + e * (kV ? 2048 : 1024);
+      if (kV) {
+        if (d0 | d1) {
+          lo = make_uint4(lo.x & ~d0, lo.y & ~d0, lo.z & ~d0, lo.w & ~d0);
+          hi = make_uint4(hi.x & ~d1, hi.y & ~d1, hi.z & ~d1, hi.w & ~d1);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c.k_full[kb]);
-        if (half == 0 && kc >= C::kNV && !warp_wait(&c.v_empty[vb], (kc / C::kNV - 1) & 1, flags)) return;
-        // V: lane (dim % 8, rows 8 r .., dims 32 g + dim % 8 + 8 k).  Rows behind the sequence's end become zeros
-        // (they may hold anything, and zero times NaN would reach O); a unit without keys has a page of them.
-        const int m = lane & 7, r = lane >> 3 & 1;
-        const int nv = half == 0 ? max(n, 1) : n;
-        for (int e = sub; e < nv * (HD / 64); e += 4) {
-          const int pg = e / (HD / 64), g = e % (HD / 64) * 2 + (lane >> 4);
-          const uint8_t* tile = src + pg * C::kCodes;
-          const int live = n == 0 ? 0 : q.kv - (lp + pg) * kPage - 8 * r;  // rows of the eight that are
-          uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-          uint2 ex = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-          if (live > 0) {
-            lo = *reinterpret_cast<const uint4*>(tile + 16 * HD + g * 512 + m * 64 + ((2 * r) ^ (m >> 1)) * 16);
-            hi = *reinterpret_cast<const uint4*>(tile + 16 * HD + g * 512 + m * 64 + ((2 * r + 1) ^ (m >> 1)) * 16);
-            ex = *reinterpret_cast<const uint2*>(tile + 32 * HD + 16 + 8 * r);
-          }
-          if (live < 8 && live > 0) {
-            const uint32_t dl = live >= 4 ? 0u : 0xffffffffu << 8 * live, dh = live <= 4 ? 0xffffffffu : 0xffffffffu << 8 * (live - 4);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) (&lo.x)[k] &= ~dl, (&hi.x)[k] &= ~dh;
-            ex.x = (ex.x & ~dl) | (0x7f7f7f7fu & dl), ex.y = (ex.y & ~dh) | (0x7f7f7f7fu & dh);
-          }
-          uint32_t f[4];  // factors of two rows
-          const uint32_t top = max(__vmaxu4(ex.x, ex.y) >> 24, max(__vmaxu4(ex.x, ex.y) >> 16 & 255, max(__vmaxu4(ex.x, ex.y) >> 8 & 255, __vmaxu4(ex.x, ex.y) & 255)));
-          auto factors = [&](int add, uint32_t least) {  // 2^(max(e, least) + add - 127), at most 2^127
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t z = (k < 2 ? ex.x : ex.y) >> 16 * (k & 1);
-              f[k] = min(max(z & 255, least) + add, 254u) << 7 | min(max(z >> 8 & 255, least) + add, 254u) << 23;
-            }
-          };
-          factors(120, 0);
-          uint32_t y[4][4];  // [dim][pair of rows]
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint2 a = widen((&lo.x)[k]), z = widen((&hi.x)[k]);
-            y[k][0] = mul2(a.x, f[0]), y[k][1] = mul2(a.y, f[1]), y[k][2] = mul2(z.x, f[2]), y[k][3] = mul2(z.y, f[3]);
-          }
-          if (__any_sync(0xffffffffu, top > 134)) {
-            factors(-7, 134);  // 2^(max(e, 134) - 134)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-              for (int u = 0; u < 4; ++u) y[k][u] = mul2(y[k][u], f[u]);
-          }
-          uint8_t* dst = vd + (half * (kPages / 2) + pg) * C::kTile + m * 16;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint4*>(dst + ((g * 4 + k) * 2 + r) * 128) = make_uint4(y[k][0], y[k][1], y[k][2], y[k][3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&c.v_full[vb]);
-          if (n > 0) mbar_arrive(&c.st_empty[b]);
-        }
-        if (n > 0) ++i;
+        auto put = [&](uint32_t a, uint32_t b, int k) {
+          const uint2 x = widen(a), y = widen(b);
+          *reinterpret_cast<uint4*>(d + k * 256) = make_uint4(turn(x.x, 0), turn(x.y, 1), turn(y.x, 2), turn(y.y, 3));
+        };
+        put(lo.x, hi.x, 0), put(lo.y, hi.y, 1), put(lo.z, hi.z, 2), put(lo.w, hi.w, 3);
+      } else {
+        auto put = [&](uint32_t a, uint32_t b, int at) {
+          const uint2 x = widen(a), y = widen(b);
+          *reinterpret_cast<uint4*>(d + at) = make_uint4(turn(x.x, 0), turn(x.y, 0), turn(y.x, 0), turn(y.y, 0));
+        };
+        put(lo.x, lo.y, 0), put(lo.z, lo.w, 128), put(hi.x, hi.y, 512), put(hi.z, hi.w, 640);
       }
+    }
+  }
+}
+
+// Warps 12 and 13 (`sub` 0, 1): K of the halves, every second page each; 14 and 15 (2, 3): V.
+template <int HD, class C, bool kV, class Ctl>
+__device__ __forceinline__ void widen_codes(const uint8_t* stage, uint8_t* slots, Ctl& c, int sub, int lane) {
+  volatile int* flags = c.flags;
+  constexpr int kN = kV ? C::kNV : C::kNK;
+  uint64_t *full = kV ? c.v_full : c.k_full, *empty = kV ? c.v_empty : c.k_empty;
+#pragma unroll 1
+  for (int i = 0;; ++i) {
+    const int b = i % C::kNS, kc = i >> 1, half = i & 1, slot = kc % kN;
+    if (!warp_wait(&c.st_full[b], (i / C::kNS) & 1, flags)) return;
+    const int n = c.half[b].x, rows = c.half[b].y;
+    if (n < 0) return;
+    if (half == 0 && kc >= kN && !warp_wait(&empty[slot], (kc / kN - 1) & 1, flags)) return;
+    uint8_t* dst = slots + slot * C::kSlot + half * (kPages / 2) * C::kTile;
+    const uint8_t* src = stage + b * C::kHalf;
+    const int pg = sub & 1, mine = pg + (lane >> 4) * 2;  // a lane looks at a row of one of the two pages
+    const bool far = mine < n && src[mine * C::kCodes + 32 * HD + (kV ? 16 : 0) + (lane & 15)] > 134;
+    if (__any_sync(0xffffffffu, far))
+      widen_pages<HD, C, kV, true>(src, dst, pg, n, rows, lane);
+    else
+      widen_pages<HD, C, kV, false>(src, dst, pg, n, rows, lane);
+    if (kV && half == 0 && n == 0 && (sub & 1) == 0) {  // a unit without keys: a page of zeros
+      for (int e = lane; e < C::kTile / 16; e += 32) reinterpret_cast<uint4*>(dst)[e] = make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&full[slot]);
+      mbar_arrive(&c.st_empty[b]);  // (not before what was read has been used)
     }
   }
 }
@@ -399,11 +396,11 @@ __global__ void __launch_bounds__(Geo<kQuant>::kThreads, 1) attend_tc_kernel(con
   }
   if (t == 0) {
     for (int i = 0; i < C::kNK; ++i) {
-      mbar_init(&c.k_full[i], kQuant ? 8 : 1);  // (8 bits: four warps, twice)
+      mbar_init(&c.k_full[i], kQuant ? 4 : 1);  // (8 bits: two warps, two halves)
       mbar_init(&c.k_empty[i], NT);
     }
     for (int i = 0; i < C::kNV; ++i) {
-      mbar_init(&c.v_full[i], kQuant ? 8 : 1);
+      mbar_init(&c.v_full[i], kQuant ? 4 : 1);
       mbar_init(&c.v_empty[i], NT);
       mbar_init(&c.v_raw[i], 1);
     }
@@ -451,7 +448,7 @@ __global__ void __launch_bounds__(Geo<kQuant>::kThreads, 1) attend_tc_kernel(con
       if (warp == 8) {
         load_codes<C>(p, h, walk, sS, c, lane);
       } else if (warp >= 12) {
-        widen_codes<HD, C>(p, h, walk, sS, sK, sV, c, warp - 12, lane);
+        warp < 14 ? widen_codes<HD, C, false>(sS, sK, c, warp - 12, lane) : widen_codes<HD, C, true>(sS, sV, c, warp - 12, lane);
       } else if (NT == 1 && warp == 10 && lane == 0) {
         // queries of one segment at a time: once the last S of the one before is done
         Walk w = walk;
