@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(Geo<kQuant>::kThreads, 1) attend_tc_kernel(con
       mbar_init(&c.st_full[i], 1);
       mbar_init(&c.st_empty[i], 4);
     }
-    mbar_init(&c.q_empty, 1);
+    mbar_init(&c.q_empty, 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.s_full[i], 1);
       mbar_init(&c.p_half[i], 128);
@@ -616,6 +616,54 @@ __global__ void __launch_bounds__(Geo<kQuant>::kThreads, 1) attend_tc_kernel(con
           }
           ++act;
         }
+      } else if constexpr (kQuant) {
+        // One tile, a warp a stream: chunks j of its parity.  A wait by parity is exact only while the phase before is
+        // known complete and the next one is not.  The next one needs this warp (S, P V or q_empty).  The one
+        // before: q_full of a segment says that every S before it is done, hence every K loaded (K and V come in
+        // order); K of a chunk says that V kNV chunks earlier is in its slot (its half had to be free); O is
+        // counted by the stream's own segments.
+        static_assert(NT == 2 || C::kNS == 2 * C::kNV, "K of a chunk tells of V kNV chunks earlier");
+        const int x = warp == 9 ? 0 : 1;
+        Walk w = walk;
+        Seg q;
+        int it = 0, act = 0, kc0 = 0;  // chunks and segments of this stream; chunks of the segments before
+        auto wait = [&](uint64_t* bar, int phase) {
+          if (!wait_ab(bar, phase & 1, flags)) flags[0] = 1;  // after a timeout: commits only, no MMAs
+        };
+        for (int seg = 0; w.next(p, h, q); ++seg) {
+          const int n = q.c_hi - q.c_lo;
+          wait(&c.q_full[0], seg);
+          auto s_of = [&](int j) {
+            const int kc = kc0 + j, kb = kc % C::kNK;
+            wait(&c.k_full[kb], kc / C::kNK);
+            tc_fence_after();
+            if (!flags[0]) issue_s(x, 0, kb);
+            mma_commit(&c.s_full[x]);
+            mma_commit(&c.k_empty[kb]);
+            if (j + 2 >= n) mma_commit(&c.q_empty);  // this stream's last
+          };
+          if (x < n)
+            s_of(x);
+          else
+            mbar_arrive(&c.q_empty);
+          for (int j = x; j < n; j += 2, ++it) {
+            const int kc = kc0 + j, vb = kc % C::kNV;
+            const int np = max(1, min(kPages, (q.kv - q.k0 - (q.c_lo + j) * kKeys + kPage - 1) / kPage));
+            wait(&c.v_full[vb], kc / C::kNV);
+            if (j == x && act > 0) wait(&c.o_free[x], act - 1);
+            wait(&c.p_half[x], it);
+            tc_fence_after();
+            if (!flags[0]) issue_pv(x, vb, 0, min(np, kPages / 2), j > x);
+            wait(&c.p_full[x], it);
+            tc_fence_after();
+            if (!flags[0]) issue_pv(x, vb, kPages / 2, np, true);
+            mma_commit(&c.o_done[x]);
+            mma_commit(&c.v_empty[vb]);
+            if (j + 2 < n) s_of(j + 2);
+          }
+          if (x < n) ++act;
+          kc0 += n;
+        }
       } else if (warp == 9) {
         // both streams: each alternates S and P V; whichever is ready goes out
         It<NT, Walk> its[2];
@@ -654,12 +702,11 @@ __global__ void __launch_bounds__(Geo<kQuant>::kThreads, 1) attend_tc_kernel(con
             if (a.valid && !pv[x]) {
               const int kc = a.kc0 + a.j, kb = kc % C::kNK;
               if (give_up || (kc == s_next && mbar_test_wait(&c.k_full[kb], (kc / C::kNK) & 1) &&
-                              (!a.first(x) || (kQuant ? mbar_test_wait(&c.q_full[0], a.seg & 1) : mbar_test_wait(&c.q_full[a.seg & 1], a.seg >> 1 & 1))))) {
+                              (!a.first(x) || mbar_test_wait(&c.q_full[a.seg & 1], a.seg >> 1 & 1)))) {
                 tc_fence_after();
-                if (!give_up) issue_s(x, kQuant ? 0 : a.seg & 1, kb);
+                if (!give_up) issue_s(x, a.seg & 1, kb);
                 mma_commit(&c.s_full[x]);
                 mma_commit(&c.k_empty[kb]);
-                if (kQuant && a.j + 1 == a.n) mma_commit(&c.q_empty);  // (S goes in chunk order: the segment's last)
                 ++s_next;
                 pv[x] = true;
                 did = true;
@@ -771,7 +818,7 @@ __global__ void __launch_bounds__(Geo<kQuant>::kThreads, 1) attend_tc_kernel(con
             pk[e] = pack_bf16(u, v);
           }
           st32(tS, pk);
-          if (NT == 2) {
+          if (NT == 2 || kQuant) {
             st_wait();
             tc_fence_before();
             mbar_arrive(&c.p_half[x]);
@@ -792,7 +839,7 @@ __global__ void __launch_bounds__(Geo<kQuant>::kThreads, 1) attend_tc_kernel(con
           m = m_new;
         }
         tc_fence_before();
-        if (NT == 2 && !warp_valid) mbar_arrive(&c.p_half[x]);
+        if ((NT == 2 || kQuant) && !warp_valid) mbar_arrive(&c.p_half[x]);
         mbar_arrive(&c.p_full[x]);
       }
       // ---- the segment's rows
@@ -878,6 +925,7 @@ __global__ void __launch_bounds__(Geo<kQuant>::kThreads, 1) attend_tc_kernel(con
       }
       tc_fence_before();
       mbar_arrive(&c.o_free[NT == 2 ? x : 0]);
+      if (NT == 1 && kQuant && n > 1) mbar_arrive(&c.o_free[1]);  // (each stream's warp counts the segments that it works in)
       q = nq;
       have = more;
       ++seg;
