@@ -32,6 +32,7 @@ struct AttendWork {
   float2* ml;      // [2 sms][rows] (maximum in log2 units, sum)
   int4* meta;      // [sms] the unit that starts in a CTA and ends in a later one: (CTAs, its first row, tokens, g)
   int long_chunks; // many query tiles per sequence
+  int spread;      // merge: rows before parts where that waits less
 };
 
 // Row r of partial slot `slot` (rows of fp32, as many as a unit of `rows` has): a warp merges a row,

@@ -960,7 +960,9 @@ __global__ void __launch_bounds__(256) attend_combine_kernel(const AttendParams 
   const int n = meta.z, g = meta.w;  // tokens of the unit
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tiles = n > h.T ? 2 : 1;  // query tiles with tokens
-  const bool shared = nsplit > 8;
+  // (where the caller's form allows: by the rounds of loads that either way waits for)
+  const int filled = min(n, h.T) * h.group;  // rows of a query tile
+  const bool shared = nsplit > 8 && !(wk.spread && (filled * tiles + gridDim.y - 1) / gridDim.y * ((nsplit + 63) / 64) >= (nsplit + 7) / 8);
   const int rows = shared ? 1 : 8;                      // of the block at a time
   for (int base = blockIdx.y * rows; base < tiles * 128; base += gridDim.y * rows) {
     const int row = shared ? base : base + warp;
@@ -1099,6 +1101,7 @@ AttendWork attend_work(void* workspace, int head_dim, int sms, bool long_chunks)
   w.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + (int64_t)sms * 2 * 256 * head_dim * 4);
   w.meta = reinterpret_cast<int4*>(w.ml + (int64_t)sms * 2 * 256);
   w.long_chunks = long_chunks;
+  w.spread = 0;
   return w;
 }
 
@@ -1117,6 +1120,7 @@ cudaError_t launch_attend_tc(const AttendParams& p, int head_dim, int max_new, v
   // (8 x 256 on 2048).
   const bool two = max_new > T && ((int64_t)p.n_rows + T - 1) / T * p.nkv * 2 >= sms;
   w.long_chunks = max_new > 4 * (two ? 2 * T : T);
+  w.spread = p.masks || p.quant;
   if (p.quant) return p.masks ? launch_form<true, true>(p, w, head_dim, two, sms, st) : launch_form<false, true>(p, w, head_dim, two, sms, st);
   return p.masks ? launch_form<true, false>(p, w, head_dim, two, sms, st) : launch_form<false, false>(p, w, head_dim, two, sms, st);
 }

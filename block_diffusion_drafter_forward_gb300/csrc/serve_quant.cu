@@ -68,15 +68,20 @@ __device__ __forceinline__ void find_entries(Entries& e, const QuantParams& p, i
   __syncthreads();
 }
 
-// Eight dims of a row as fp32, infinities as NaN.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
+// Eight dims of a row as they are loaded, and as fp32.
+template <typename T> struct Raw { uint4 w[sizeof(T) / 2]; };
+template <typename T>
+__device__ __forceinline__ void load8(const uint8_t* p, Raw<T>& x) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float((&w.x)[i] << 16), x[2 * i + 1] = __uint_as_float((&w.x)[i] & 0xffff0000u);
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) x.w[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
 }
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+__device__ __forceinline__ void open8(const Raw<__nv_bfloat16>& r, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float((&r.w[0].x)[i] << 16), x[2 * i + 1] = __uint_as_float((&r.w[0].x)[i] & 0xffff0000u);
+}
+__device__ __forceinline__ void open8(const Raw<float>& r, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = __uint_as_float((&r.w[i >> 2].x)[i & 3]);
 }
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {  // (bf16 numbers: no rounding)
   uint4 w;
@@ -89,9 +94,11 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 
-// Codes of a row held eight dims a lane by kLanes neighbouring lanes; *e: its exponent byte.
-template <int kLanes>
-__device__ __forceinline__ uint2 encode(const float (&x)[8], int* e) {
+// Codes of a row held eight dims a lane by kLanes neighbouring lanes (infinities as NaN); *e: its exponent byte.
+template <int kLanes, typename T>
+__device__ __forceinline__ uint2 encode(const Raw<T>& raw, int* e) {
+  float x[8];
+  open8(raw, x);
   uint32_t top = 0;  // largest finite magnitude, by its bits
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -147,18 +154,20 @@ __global__ void __launch_bounds__(256) append_quant_kernel(const QuantParams p) 
     uint8_t* tile = p.pool + (int64_t)(slot / kPage) * p.page_bytes + (int64_t)h * (32 * HD + 32);
     const uint8_t* src[2] = {p.k + row * p.ks, p.v + row * p.vs};
     const int64_t at = ((int64_t)h * HD + d) * sizeof(T);
-    auto fetch = [&](int side, int r, float (&x)[8]) {
+    auto fetch = [&](int side, int r, Raw<T>& x) {
       if (on) {
-        load8(reinterpret_cast<const T*>(src[side] + r * (side ? p.vs : p.ks) + at), x);
+        load8(src[side] + r * (side ? p.vs : p.ks) + at, x);
       } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = 0.f;
+        for (int k = 0; k < (int)sizeof(T) / 2; ++k) x.w[k] = make_uint4(0, 0, 0, 0);
       }
     };
     if (en & 64) {
-      float x[4][8];
+      Raw<T> x[4], y[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) fetch(0, 2 * r + half, x[r]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) fetch(1, 4 * half + r, y[r]);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         int ex;
@@ -167,13 +176,11 @@ __global__ void __launch_bounds__(256) append_quant_kernel(const QuantParams p) 
         if (on) *reinterpret_cast<uint2*>(tile + k8_in_tile(jr, d)) = c;
         if (on && d == 0) tile[32 * HD + jr] = (uint8_t)ex;
       }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) fetch(1, 4 * half + r, x[r]);
       uint32_t lo[4], hi[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         int ex;
-        const uint2 c = encode<kPieces>(x[r], &ex);
+        const uint2 c = encode<kPieces>(y[r], &ex);
         lo[r] = c.x, hi[r] = c.y;
         if (on && d == 0) tile[32 * HD + 16 + j + 4 * half + r] = (uint8_t)ex;
       }
@@ -186,7 +193,7 @@ __global__ void __launch_bounds__(256) append_quant_kernel(const QuantParams p) 
         *reinterpret_cast<uint32_t*>(tile + 16 * HD + v8_in_tile(j + 4 * half, d + 4 + r)) = hi[r];
       }
     } else {  // K by the lower lanes, V by the upper ones
-      float x[8];
+      Raw<T> x;
       fetch(half, 0, x);
       int ex;
       const uint2 c = encode<kPieces>(x, &ex);
@@ -298,7 +305,7 @@ int run(const char* name, const dflash_kv_pages* kv, int32_t dtype, QuantParams&
   if (cudaError_t e = sm_count(&sms); e != cudaSuccess) return call_error(DFLASH_ECUDA, name, e);
   const int64_t blocks = (p.n + (int64_t)kRows - 1) / kRows;
   const int groups = (p.nkv + 128 / kv->head_dim - 1) / (128 / kv->head_dim);
-  const dim3 grid((unsigned)blocks, (unsigned)std::min<int64_t>(groups, std::max<int64_t>(1, 8 * sms / blocks)));
+  const dim3 grid((unsigned)blocks, (unsigned)std::min<int64_t>(groups, std::max<int64_t>(1, 32 * sms / blocks)));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == DFLASH_F32)
     kv->head_dim == 128 ? launch<float, 128>(p, read, grid, st) : launch<float, 64>(p, read, grid, st);

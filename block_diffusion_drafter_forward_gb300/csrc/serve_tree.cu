@@ -88,13 +88,15 @@ struct KeepParams {
   int nb, nkv, mpps, num_pages, max_path, hd;
 };
 
-// A warp has one (sequence, head) and takes the path's rows in order, kBatch at a time: all loads of a
-// batch ahead of its stores.  Since the path rises, row i of it is read at or behind i, and no
-// row is written before it has been read; a lane reads and writes the same dims, so that its own
-// program order is enough.  Bound by latency (a batch is one round trip).
+// A warp has one (sequence, head) and takes the rows in order of their new places, a half page (eight rows, or what
+// of them the path fills) at a time: all loads of a half page ahead of its stores.  Since the path rises, row i of it
+// is read at or behind i, and no row is written before it has been read; a lane reads and writes the same dims,
+// so that its own program order is enough.  V of a whole half page is stored eight rows of a dim at once:
+// row by row every element is a sector of its own.  Bound by latency (a half page is one round trip) and by V's
+// gathered elements.
 template <int ES>  // bytes of an element: 4, 2, or 1 (codes, with their exponents)
 __global__ void __launch_bounds__(128) keep_kernel(const KeepParams p) {
-  constexpr int kBatch = 8;
+  using V = typename std::conditional<ES == 4, uint32_t, typename std::conditional<ES == 2, uint16_t, uint8_t>::type>::type;
   const int lane = threadIdx.x & 31;
   const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int s = (int)(unit / p.nkv), h = (int)(unit % p.nkv);
@@ -119,38 +121,40 @@ __global__ void __launch_bounds__(128) keep_kernel(const KeepParams p) {
     return;
   }
   const int32_t* table = p.page_tables + (int64_t)s * p.mpps;
-  const int hd = p.hd;
-  for (int i0 = 0; i0 < n; i0 += kBatch) {
-    // lane l < kBatch: the batch's row l
-    const int i = i0 + lane;
+  const int hd = p.hd, pieces = hd * ES / 16;  // K of a row: pieces of 16 bytes, at most 32
+  for (int b0 = ctx & ~7; b0 < ctx + n; b0 += 8) {
+    // lane l < 8: the row that goes to b0 + l
+    const int i = b0 + lane - ctx;
+    const bool row = lane < 8 && i >= 0 && i < n;
     uint8_t *from = nullptr, *to = nullptr;
-    int jf = 0, jt = 0;
-    bool move = false;
-    if (lane < kBatch && i < n) {
-      const int a = ctx + path[i], b = ctx + i;
-      if (a != b) {
-        const int pa = table[a / kPage], pb = table[b / kPage];
-        move = pa >= 0 && pa < p.num_pages && pb >= 0 && pb < p.num_pages;
-        if (!move && p.status) atomicOr(p.status, DFLASH_DEV_BAD_PAGE);
-        if (move) {
-          from = p.pool + pa * p.page_bytes + h * p.head_bytes;
-          to = p.pool + pb * p.page_bytes + h * p.head_bytes;
-        }
-        jf = a % kPage, jt = b % kPage;
+    int jf = 0;
+    bool there = false, move = false;
+    if (row) {
+      const int a = ctx + path[i], b = b0 + lane;
+      const int pa = table[a / kPage], pb = table[b / kPage];
+      there = pa >= 0 && pa < p.num_pages && pb >= 0 && pb < p.num_pages;
+      move = there && a != b;
+      if (!there && a != b && p.status) atomicOr(p.status, DFLASH_DEV_BAD_PAGE);
+      if (there) {
+        from = p.pool + pa * p.page_bytes + h * p.head_bytes;
+        to = p.pool + pb * p.page_bytes + h * p.head_bytes;
       }
+      jf = a % kPage;
     }
     const unsigned moving = __ballot_sync(0xffffffffu, move);
     if (!moving) continue;
-    using V = typename std::conditional<ES == 4, uint32_t, typename std::conditional<ES == 2, uint16_t, uint8_t>::type>::type;
-    uint4 k[kBatch];
-    V v[kBatch][4];
-    uint8_t e[kBatch];
-    const int pieces = hd * ES / 16;  // of K, 16 bytes each: at most 32
+    const bool whole = __ballot_sync(0xffffffffu, there) == 0xffu;  // (rows that stay are then stored as they were)
+    const unsigned take = whole ? 0xffu : moving;
+    uint8_t* dst = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), __ffs(moving) - 1));
+    const int j0 = b0 % kPage;
+    uint4 k[8];
+    V v[8][4];
+    uint8_t e[8];
 #pragma unroll
-    for (int r = 0; r < kBatch; ++r) {
+    for (int r = 0; r < 8; ++r) {
       const uint8_t* f = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(from), r));
       const int j = __shfl_sync(0xffffffffu, jf, r);
-      if (!(moving >> r & 1)) continue;
+      if (!(take >> r & 1)) continue;
       if (lane < pieces)
         k[r] = *reinterpret_cast<const uint4*>(f + (ES == 1 ? k8_in_tile(j, lane * 16) : k_in_tile(j, lane * (16 / ES), hd) * ES));
 #pragma unroll
@@ -161,18 +165,39 @@ __global__ void __launch_bounds__(128) keep_kernel(const KeepParams p) {
       if (ES == 1 && lane < 2) e[r] = f[32 * hd + 16 * lane + j];
     }
 #pragma unroll
-    for (int r = 0; r < kBatch; ++r) {
-      uint8_t* f = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), r));
-      const int j = __shfl_sync(0xffffffffu, jt, r);
-      if (!(moving >> r & 1)) continue;
+    for (int r = 0; r < 8; ++r) {
+      if (!(take >> r & 1)) continue;
+      const int j = j0 + r;
       if (lane < pieces)
-        *reinterpret_cast<uint4*>(f + (ES == 1 ? k8_in_tile(j, lane * 16) : k_in_tile(j, lane * (16 / ES), hd) * ES)) = k[r];
+        *reinterpret_cast<uint4*>(dst + (ES == 1 ? k8_in_tile(j, lane * 16) : k_in_tile(j, lane * (16 / ES), hd) * ES)) = k[r];
+      if (!whole) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int d = lane + 32 * x;
+          if (d < hd) reinterpret_cast<V*>(dst + 16 * hd * ES)[ES == 1 ? v8_in_tile(j, d) : v_in_tile(j, d, hd)] = v[r][x];
+        }
+      }
+      if (ES == 1 && lane < 2) dst[32 * hd + 16 * lane + j] = e[r];
+    }
+    if (whole) {
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const int d = lane + 32 * x;
-        if (d < hd) reinterpret_cast<V*>(f + 16 * hd * ES)[ES == 1 ? v8_in_tile(j, d) : v_in_tile(j, d, hd)] = v[r][x];
+        if (d >= hd) continue;
+        if (ES == 1) {
+#pragma unroll
+          for (int z = 0; z < 8; z += 4)
+            *reinterpret_cast<uint32_t*>(dst + 16 * hd + v8_in_tile(j0 + z, d)) = v[z][x] | (uint32_t)v[z + 1][x] << 8 | (uint32_t)v[z + 2][x] << 16 | (uint32_t)v[z + 3][x] << 24;
+        } else {
+          uint4* out = reinterpret_cast<uint4*>(dst + (16 * hd + v_in_tile(j0, d, hd)) * ES);
+          if (ES == 2) {
+            out[0] = make_uint4(v[0][x] | (uint32_t)v[1][x] << 16, v[2][x] | (uint32_t)v[3][x] << 16, v[4][x] | (uint32_t)v[5][x] << 16, v[6][x] | (uint32_t)v[7][x] << 16);
+          } else {
+            out[0] = make_uint4(v[0][x], v[1][x], v[2][x], v[3][x]);
+            out[1] = make_uint4(v[4][x], v[5][x], v[6][x], v[7][x]);
+          }
+        }
       }
-      if (ES == 1 && lane < 2) f[32 * hd + 16 * lane + j] = e[r];
     }
   }
 }
