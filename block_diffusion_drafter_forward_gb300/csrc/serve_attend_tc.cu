@@ -56,11 +56,9 @@ using plan::shape_of;
 
 constexpr int kKeys = 128;                      // keys per chunk
 constexpr int kPages = kKeys / kPage;           // 8
-template <bool kTree, bool kQuant>
+template <bool kQuant>
 struct Geo {
-  static constexpr bool kWide = kTree || kQuant;       // two threads a query row
-  static constexpr int kSoft = kWide ? 16 : 8;         // softmax warps
-  static constexpr int kKeys = 128, kUnitCost = 3, kThreads = 32 * (kSoft + (kQuant ? 8 : 4));
+  static constexpr int kKeys = 128, kUnitCost = 3, kThreads = kQuant ? 512 : 384;
 };
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
@@ -372,254 +370,18 @@ __device__ __forceinline__ void widen_codes(const uint8_t* stage, uint8_t* slots
   }
 }
 
-__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&v)[16]) {  // 16 columns, without the wait
-  __syncwarp();
-#define R8(i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::R8(0),
-      R8(8), "r"(taddr)
-      : "memory");
-#undef R8
-}
-__device__ __forceinline__ void ld_row(uint32_t taddr, float (&v)[32]) { tmem_ld32(taddr, v); }
-__device__ __forceinline__ void ld_row(uint32_t taddr, float (&v)[16]) { tmem_ld16(taddr, v); }
-
-// Softmax with two threads a query row, for the forms with trees or pages in 8 bits: warps 8 x + 4 f + w are stream x,
-// keys [64 f, + 64) of a chunk, rows [32 w, + 32).  Half the work per thread is half the way from S to P, which is
-// what a chunk waits for; S is read twice, 32 columns at a time in loops, so that registers suffice for so many warps
-// and the code for the instruction caches.  The two threads of a row meet in shared memory over its maximum
-// (each chunk) and its sum (each segment); O is rescaled and written by halves of its dims.  P of keys 64 f + 32 i ..
-// goes back over S columns that this thread has read: 16 columns from 64 f + 16 i on.
-template <int HD, int NT, bool kTree, bool kQuant, class C, class Walk, class Ctl, class LoadQ>
-__device__ __forceinline__ void wide_softmax(const AttendParams& p, const AttendWork& wk, const Shape& h, const Walk& walk, long long W, Ctl& c,
-                                             uint32_t tmem, const LoadQ& load_q) {
-  volatile int* flags = c.flags;
-  float(*mx)[2][128] = reinterpret_cast<float(*)[2][128]>(c.ml);  // [stream][half][row]
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const int x = warp >> 3, f = warp >> 2 & 1, w4 = warp & 3, row = w4 * 32 + lane;
-  const uint32_t lane_off = (uint32_t)(w4 * 32) << 16;
-  const uint32_t tS = tmem + x * 128 + f * 64 + lane_off;
-  const int pair_bar = 1 + x * 4 + w4, quad_bar = 9 + w4;
-  const int tok = row / h.group, head = row - tok * h.group;
-  const bool loads = (warp & 7) == 0 && lane == 0 && (NT == 2 || (x == 0 && !kQuant));
-  Walk w = walk;
-  Seg q, nq;
-  bool have = w.next(p, h, q);
-  while (NT == 2 && have && !It<NT, Walk>::active(h, q, x)) have = w.next(p, h, q);
-  if (have && loads) load_q(q, x);
-  int it = 0, seg = 0;  // chunks and segments done by this stream
-  while (have) {
-    bool more = w.next(p, h, nq);
-    while (NT == 2 && more && !It<NT, Walk>::active(h, nq, x)) more = w.next(p, h, nq);
-    const int n = q.c_hi - q.c_lo;
-    const int tk = q.t0 + (NT == 2 ? x * h.T : 0) + tok;
-    const bool valid = tok < h.T && tk < q.n;
-    const bool warp_valid = __any_sync(0xffffffffu, valid);
-    // keys [lo, hi) are seen by this row (rows without a token: anything, they are not written); trees: of the
-    // context, and those of the sequence's own rows that the mask has
-    const int ctx = q.kv - q.n;
-    const int pos = !kTree ? ctx + tk : valid && p.window > 0 ? max(ctx, __ldg(p.positions + q.r0 + tk)) : 0;
-    const int hi = !valid ? INT_MAX : kTree ? ctx : p.causal ? min(q.kv, pos + 1) : q.kv;
-    const int lo = valid && p.window > 0 ? max(0, pos - p.window + 1) : 0;
-    const uint32_t* mask = kTree ? reinterpret_cast<const uint32_t*>(p.masks + (int64_t)(q.r0 + (valid ? tk : 0)) * p.words) : nullptr;
-    float m = -INFINITY, l = 0.f;
-    int done = 0;
-#pragma unroll 1
-    for (int j = NT == 2 ? 0 : x; j < n; j += NT == 2 ? 1 : 2, ++it, ++done) {
-      if (!wait_ab(&c.s_full[x], it & 1, flags)) flags[0] = 1;
-      tc_fence_after();
-      // the next queries: two tiles, into the same tile once this segment's last S is done; one,
-      // into the other tile once this segment's first is (so every S of the segment before is)
-      if (loads && more && j == (NT == 2 ? n - 1 : 0)) load_q(nq, NT == 2 ? x : (seg + 1) & 1);
-      if (warp_valid) {
-        const int kb = q.k0 + (q.c_lo + j) * kKeys, key0 = kb + f * 64;
-        const bool edge = __any_sync(0xffffffffu, kb < lo || kb + kKeys > hi);
-        auto see = [&](int key) {  // of 32 keys from `key` on
-          if (kTree) return valid ? mask_bits(mask, 2 * p.words, key, lo, ctx, q.kv) : 0xffffffffu;
-          uint32_t b = 0xffffffffu;
-          if (lo > key) b = lo - key >= 32 ? 0u : b << (lo - key);
-          if (hi < key + 32) b = hi <= key ? 0u : b & 0xffffffffu >> (key + 32 - hi);
-          return b;
-        };
-        float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll 1
-        for (int i = 0; i < 64; i += 32) {
-          float v[32];
-          tmem_ld32(tS + i, v);
-          if (edge) {
-            const uint32_t b = see(key0 + i);
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(b >> e & 1)) v[e] = -INFINITY;
-          }
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) m0 = fmaxf(m0, fmaxf(v[e], v[e + 1])), m1 = fmaxf(m1, fmaxf(v[e + 2], v[e + 3]));
-        }
-        // (the other half reads it ahead of its arrivals below, and those come ahead of the next S)
-        mx[x][f][row] = fmaxf(m0, m1);
-        named_barrier(pair_bar, 64);
-        const float top = fmaxf(fmaxf(m0, m1), mx[x][f ^ 1][row]) * p.scale_log2;
-        const bool grow = top > m + 8.f;  // (m = -inf: any finite score)
-        const float m_new = grow ? top : m;
-        const float alpha = grow && m != -INFINITY ? ex2(m - m_new) : 1.f;
-        if (done > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          if (!wait_ab(&c.o_done[x], (it - 1) & 1, flags)) flags[0] = 1;
-          tc_fence_after();
-#pragma unroll 1
-          for (int d = f * (HD / 2); d < (f + 1) * (HD / 2); d += 32) {
-            float v[32];
-            tmem_ld32(tmem + 256 + x * 128 + lane_off + d, v);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] *= alpha;
-            tmem_st32(tmem + 256 + x * 128 + lane_off + d, v);
-          }
-        }
-        if (f == 1) {  // its half of O is ready for the first keys' P V
-          tc_fence_before();
-          mbar_arrive(&c.p_half[x]);
-        }
-        const float off = m_new == -INFINITY ? 0.f : -m_new;
-        const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), off2 = pair(off, off);
-        uint64_t l0 = 0, l1 = 0;  // two sums of pairs
-#pragma unroll 1
-        for (int i = 0; i < 64; i += 32) {
-          float v[32];
-          tmem_ld32(tS + i, v);
-          if (edge) {
-            const uint32_t b = see(key0 + i);
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(b >> e & 1)) v[e] = -INFINITY;
-          }
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float u, z;
-            unpair(fma2(pair(v[2 * e], v[2 * e + 1]), scale2, off2), u, z);
-            u = ex2(u), z = ex2(z);
-            if (e & 1) l0 = add2(l0, pair(u, z)); else l1 = add2(l1, pair(u, z));
-            pk[e] = pack_bf16(u, z);
-          }
-          st16(tS + i / 2, pk);
-        }
-        st_wait();
-        float lu, lv;
-        unpair(add2(l0, l1), lu, lv);
-        l = l * alpha + (lu + lv);
-        m = m_new;
-      } else if (f == 1) {
-        mbar_arrive(&c.p_half[x]);
-      }
-      tc_fence_before();
-      mbar_arrive(f == 0 ? &c.p_half[x] : &c.p_full[x]);
-    }
-    // ---- the segment's rows
-    const bool whole = q.c_lo == 0 && q.c_hi == q.nch;
-    const int slot = 2 * blockIdx.x + (q.c_lo == 0 ? 1 : 0);  // partials: the unit's start, or a later part
-    float w0 = 1.f, w1 = 0.f;  // weights of O 0 and O 1 in this row
-    bool use1 = false;
-    // this stream's O: its last P V done, hence every earlier one
-    if (done > 0 && !wait_ab(&c.o_done[x], (it - 1) & 1, flags)) flags[0] = 1;
-    mx[x][f][row] = l;
-    named_barrier(pair_bar, 64);
-    l = mx[x][0][row] + mx[x][1][row];
-    if (NT == 1) {  // and the other stream's, with its (m, l)
-      named_barrier(quad_bar, 128);
-      if (f == 0) mx[x][0][row] = m, mx[x][1][row] = l;
-      named_barrier(quad_bar, 128);
-      const float om = mx[x ^ 1][0][row], ol = mx[x ^ 1][1][row];
-      named_barrier(quad_bar, 128);  // read before the next segment's write
-      const float M = fmaxf(m, om), base = M == -INFINITY ? 0.f : M;
-      const float a = ex2(m - base), b = ex2(om - base);
-      l = x == 0 ? l * a + ol * b : ol * b + l * a;
-      m = M;
-      w0 = x == 0 ? a : b;
-      w1 = x == 0 ? b : a;
-      use1 = n > 1;
-    } else {
-      named_barrier(pair_bar, 64);
-    }
-    tc_fence_after();
-    if (__all_sync(0xffffffffu, !flags[0]) && warp_valid) {
-      // one tile: a quarter of the dims of both streams' O; two: a half of the row's own
-      constexpr int kD = NT == 2 ? HD / 2 : HD / 4, kStep = kD < 32 ? kD : 32;
-      const int d_lo = (NT == 2 ? f : 2 * x + f) * kD;
-      const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;
-      const int64_t gr = q.r0 + tk;
-      const int gh = q.g * h.group + head;
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + gr * p.out_stride + (int64_t)gh * HD + d_lo;
-      const int prow = (NT == 2 ? x * 128 : 0) + row;
-      w0 *= inv, w1 *= inv;
-#pragma unroll 1
-      for (int d = 0; d < kD; d += kStep) {
-        float v[kStep];
-        ld_row(tmem + 256 + (NT == 2 ? x * 128 : 0) + lane_off + d_lo + d, v);
-#pragma unroll
-        for (int e = 0; e < kStep; ++e) v[e] *= w0;
-        if (NT == 1 && use1) {
-          float v1[kStep];
-          ld_row(tmem + 384 + lane_off + d_lo + d, v1);
-#pragma unroll
-          for (int e = 0; e < kStep; ++e) v[e] = fmaf(v1[e], w1, v[e]);
-        }
-        if (!valid) continue;
-        if (whole) {
-#pragma unroll
-          for (int e = 0; e < kStep; e += 16) {
-            uint32_t o[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) o[k] = pack_bf16(v[e + 2 * k], v[e + 2 * k + 1]);
-            put32(dst + d + e, o, p.wide_out);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < kStep; e += 8) {
-            uint32_t o[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(v[e + k]);
-            put32(part_row(wk, slot, prow, NT * 128, HD) + d_lo + d + e, o, true);
-          }
-        }
-      }
-      if (valid && f == 0 && (NT == 2 || x == 0)) {
-        if (!whole)
-          __stcg(wk.ml + (int64_t)slot * (NT * 128) + prow, make_float2(m, l));
-        else if (p.lse)
-          p.lse[gr * p.nh + gh] = lse_of(m, l);
-      }
-    }
-    if (t == 0 && q.c_lo == 0 && !whole) {  // the unit starts here and goes on in the next CTAs
-      const long long end = walk.hi - (q.c_hi - 1) + q.nch - 1;  // past its last slot: slot hi - 1 is chunk c_hi - 1
-      const int ctas = (int)min((long long)gridDim.x, W);
-      const int last = (int)((end * ctas + W - 1) / W) - 1;
-      wk.meta[blockIdx.x] = make_int4(last - (int)blockIdx.x + 1, q.r0 + q.t0, min(h.TT, q.n - q.t0), q.g);
-    }
-    tc_fence_before();
-    mbar_arrive(&c.o_free[NT == 2 ? x : 0]);
-    if (NT == 1 && kQuant && n > 1) mbar_arrive(&c.o_free[1]);  // (each stream's warp counts the segments that it works in)
-    q = nq;
-    have = more;
-    ++seg;
-  }
-  if (flags[0]) {
-    if (t == 0 && p.status) atomicOr(p.status, DFLASH_DEV_TIMEOUT);
-    for (int k = 0; k < 2000; ++k) __nanosleep(1000);  // copies still in flight land first
-  }
-}
-
 template <int HD, int NT, bool kTree, bool kQuant>
-__global__ void __launch_bounds__(Geo<kTree, kQuant>::kThreads, 1) attend_tc_kernel(const AttendParams p, const AttendWork wk, const __grid_constant__ CUtensorMap q_map) {
+__global__ void __launch_bounds__(Geo<kQuant>::kThreads, 1) attend_tc_kernel(const AttendParams p, const AttendWork wk, const __grid_constant__ CUtensorMap q_map) {
   using C = Cfg<HD, NT, kQuant>;
-  using Walk = plan::Walk<Geo<kTree, kQuant>, kTree>;
-  constexpr int kThreads = Geo<kTree, kQuant>::kThreads, kSoft = Geo<kTree, kQuant>::kSoft;
-  constexpr bool kWide = Geo<kTree, kQuant>::kWide;
-  static_assert(sizeof(Ctl<C, Geo<kTree, kQuant>>) <= C::kCtl, "control block overflows its slot");
+  using Walk = plan::Walk<Geo<kQuant>, kTree>;
+  constexpr int kThreads = Geo<kQuant>::kThreads;
+  static_assert(sizeof(Ctl<C, Geo<kQuant>>) <= C::kCtl, "control block overflows its slot");
   extern __shared__ __align__(1024) uint8_t smem[];  // (the queries' swizzle counts from 1 KB boundaries)
   uint8_t* sQ = smem;
   uint8_t* sK = sQ + C::kQTiles * C::kQ;
   uint8_t* sV = sK + C::kNK * C::kSlot;
   uint8_t* sS = sV + C::kNV * C::kSlot;  // 8 bits: halves of chunks
-  auto& c = *reinterpret_cast<Ctl<C, Geo<kTree, kQuant>>*>(sS + (kQuant ? C::kNS * C::kHalf : 0));
+  auto& c = *reinterpret_cast<Ctl<C, Geo<kQuant>>*>(sS + (kQuant ? C::kNS * C::kHalf : 0));
   volatile int* flags = c.flags;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const Shape h = shape_of(p, NT);
@@ -627,7 +389,7 @@ __global__ void __launch_bounds__(Geo<kTree, kQuant>::kThreads, 1) attend_tc_ker
   pdl_wait();  // everything read here may come from the kernel before
   if (t == 0) wk.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
   long long W;
-  const Walk walk = plan::make<Geo<kTree, kQuant>, kTree>(p, h, c.plan, reinterpret_cast<long long*>(sK), wk.long_chunks, &W);
+  const Walk walk = plan::make<Geo<kQuant>, kTree>(p, h, c.plan, reinterpret_cast<long long*>(sK), wk.long_chunks, &W);
   if (walk.lo >= walk.hi) {  // nothing for this CTA
     pdl_trigger();
     return;
@@ -649,10 +411,10 @@ __global__ void __launch_bounds__(Geo<kTree, kQuant>::kThreads, 1) attend_tc_ker
     mbar_init(&c.q_empty, 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.s_full[i], 1);
-      mbar_init(&c.p_half[i], kWide ? 256 : 128);
+      mbar_init(&c.p_half[i], 128);
       mbar_init(&c.p_full[i], 128);
       mbar_init(&c.o_done[i], 1);
-      mbar_init(&c.o_free[i], (NT == 2 ? 128 : 256) * (kWide ? 2 : 1));
+      mbar_init(&c.o_free[i], NT == 2 ? 128 : 256);
       mbar_init(&c.q_full[i], 1);
     }
     flags[0] = 0;
@@ -677,21 +439,17 @@ __global__ void __launch_bounds__(Geo<kTree, kQuant>::kThreads, 1) attend_tc_ker
       tma_load_3d(sQ + b * C::kQ + d * (128 * 128), &q_map, &c.q_full[b], d * 64, q.g * h.group, q.r0 + q.t0 + (NT == 2 ? b * h.T : 0));
   };
 
-  const int role = warp - kSoft;
-  if (role >= 0) {
-    // (what a block has at launch is what its warps have together: 80 a thread of 24 warps, 96 of 20, 168 of 12)
+  if (warp >= 8) {
     if (kQuant)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
-    else if (kWide)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");  // (of 128 at launch: 8 warps with 192, 8 with 64)
     else
       asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if constexpr (kQuant) {
-      if (role == 0) {
+      if (warp == 8) {
         load_codes<C>(p, h, walk, sS, c, lane);
-      } else if (role >= 4) {
-        role < 6 ? widen_codes<HD, C, false>(sS, sK, c, role - 4, lane) : widen_codes<HD, C, true>(sS, sV, c, role - 4, lane);
-      } else if (NT == 1 && role == 2 && lane == 0) {
+      } else if (warp >= 12) {
+        warp < 14 ? widen_codes<HD, C, false>(sS, sK, c, warp - 12, lane) : widen_codes<HD, C, true>(sS, sV, c, warp - 12, lane);
+      } else if (NT == 1 && warp == 10 && lane == 0) {
         // queries of one segment at a time: once the last S of the one before is done
         Walk w = walk;
         Seg q;
@@ -701,12 +459,12 @@ __global__ void __launch_bounds__(Geo<kTree, kQuant>::kThreads, 1) attend_tc_ker
         }
       }
     }
-    if (!kQuant && (role == 0 || role == 2)) {
+    if (!kQuant && (warp == 8 || warp == 10)) {
       // ---- page producers: lane l copies page l of a chunk.  The page ids of the next chunk are
       // fetched while the warp waits for a slot.  V of a chunk whose last page is part full (or that
       // has no page) lands on v_raw; the V warp zeroes its rows behind the end when it has come,
       // between its other work.
-      const int kv = role == 2;
+      const int kv = warp == 10;
       uint64_t* full = kv ? c.v_full : c.k_full;
       uint64_t* empty = kv ? c.v_empty : c.k_empty;
       uint8_t* ring = kv ? sV : sK;
@@ -786,7 +544,7 @@ __global__ void __launch_bounds__(Geo<kTree, kQuant>::kThreads, 1) attend_tc_ker
         }
       }
       if (!stop) mend();
-    } else if (lane == 0 && (!kQuant || role == 1 || role == 3)) {
+    } else if (lane == 0 && (!kQuant || warp == 9 || warp == 11)) {
       // ---- MMA issue
       constexpr uint32_t id_s = idesc_bf16(128, kKeys), id_o = idesc_bf16(128, HD);
       // operand descriptors of the first tiles; the others are further on (16-byte units)
@@ -803,15 +561,14 @@ __global__ void __launch_bounds__(Geo<kTree, kQuant>::kThreads, 1) attend_tc_ker
         if (k1 - k0 == kPages / 2) {
 #pragma unroll
           for (int k = 0; k < kPages / 2; ++k)
-            mma_bf16_tmem_a(tO, tS + (k0 + k) * 8 + (kWide && k0 > 0 ? 32 : 0), v + (k0 + k) * (C::kTile / 16), id_o, k0 + k > 0 || more ? 1u : 0u);
+            mma_bf16_tmem_a(tO, tS + (k0 + k) * 8, v + (k0 + k) * (C::kTile / 16), id_o, k0 + k > 0 || more ? 1u : 0u);
         } else {
-          for (int k = k0; k < k1; ++k)
-            mma_bf16_tmem_a(tO, tS + k * 8 + (kWide && k0 > 0 ? 32 : 0), v + k * (C::kTile / 16), id_o, k > 0 || more ? 1u : 0u);
+          for (int k = k0; k < k1; ++k) mma_bf16_tmem_a(tO, tS + k * 8, v + k * (C::kTile / 16), id_o, k > 0 || more ? 1u : 0u);
         }
       };
       if (NT == 2) {
         // one stream: S of a chunk, then its P V and the next S as soon as the softmax has written P
-        const int x = role == 1 ? 0 : 1;
+        const int x = warp == 9 ? 0 : 1;
         Walk w = walk;
         Seg q;
         int kc = 0, it = 0, act = 0;
@@ -866,7 +623,7 @@ __global__ void __launch_bounds__(Geo<kTree, kQuant>::kThreads, 1) attend_tc_ker
         // order); K of a chunk says that V kNV chunks earlier is in its slot (its half had to be free); O is
         // counted by the stream's own segments.
         static_assert(NT == 2 || C::kNS == 2 * C::kNV, "K of a chunk tells of V kNV chunks earlier");
-        const int x = role == 1 ? 0 : 1;
+        const int x = warp == 9 ? 0 : 1;
         Walk w = walk;
         Seg q;
         int it = 0, act = 0, kc0 = 0;  // chunks and segments of this stream; chunks of the segments before
@@ -907,7 +664,7 @@ __global__ void __launch_bounds__(Geo<kTree, kQuant>::kThreads, 1) attend_tc_ker
           if (x < n) ++act;
           kc0 += n;
         }
-      } else if (role == 1) {
+      } else if (warp == 9) {
         // both streams: each alternates S and P V; whichever is ready goes out
         It<NT, Walk> its[2];
         bool pv[2] = {false, false};
@@ -925,7 +682,7 @@ __global__ void __launch_bounds__(Geo<kTree, kQuant>::kThreads, 1) attend_tc_ker
             const bool give_up = flags[0];  // after a timeout: commits only, no MMAs
             if (a.valid && pv[x]) {
               const int kc = a.kc0 + a.j, vb = kc % C::kNV;
-              if (give_up || (kc == pv_next && mbar_test_wait(&c.p_full[x], a.it & 1) && (!kWide || mbar_test_wait(&c.p_half[x], a.it & 1)) &&
+              if (give_up || (kc == pv_next && mbar_test_wait(&c.p_full[x], a.it & 1) &&
                               mbar_test_wait(&c.v_full[vb], (kc / C::kNV) & 1) &&
                               (!a.first(x) || a.seg == 0 || mbar_test_wait(&c.o_free[0], (a.seg - 1) & 1)))) {
                 tc_fence_after();
@@ -962,20 +719,17 @@ __global__ void __launch_bounds__(Geo<kTree, kQuant>::kThreads, 1) attend_tc_ker
       }
     }
     __syncwarp();
-  } else if constexpr (kWide) {
-    if (kQuant)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    else
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    wide_softmax<HD, NT, kTree, kQuant, C>(p, wk, h, walk, W, c, tmem, load_q);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    if (kQuant)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ---- softmax streams: thread = query row `row` of its tile
     const int x = warp >> 2, row = t & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + x * 128 + lane_off;
     const int tok = row / h.group, head = row - tok * h.group;  // (by p.inv the loop's registers fall worse: 519 us for 499)
-    const bool loads = (t & 127) == 0 && (NT == 2 || x == 0);  // (one tile: stream 0's, a segment ahead)
+    const bool loads = (t & 127) == 0 && (NT == 2 || (x == 0 && !kQuant));  // (one tile: stream 0's, a segment ahead)
     Walk w = walk;
     Seg q, nq;
     bool have = w.next(p, h, q);
@@ -990,9 +744,11 @@ __global__ void __launch_bounds__(Geo<kTree, kQuant>::kThreads, 1) attend_tc_ker
       const bool valid = tok < h.T && tk < q.n;
       const bool warp_valid = __any_sync(0xffffffffu, valid);
       // keys [lo, hi) are seen by this row (rows without a token: anything, they are not written)
-      const int pos = q.kv - q.n + tk;
-      const int hi = !valid ? INT_MAX : p.causal ? min(q.kv, pos + 1) : q.kv;
+      // (trees: keys [lo, hi) of the context, and those of the sequence's own rows that the mask has)
+      const int pos = !kTree ? q.kv - q.n + tk : valid && p.window > 0 ? max(q.kv - q.n, __ldg(p.positions + q.r0 + tk)) : 0;
+      const int hi = !valid ? INT_MAX : kTree ? q.kv - q.n : p.causal ? min(q.kv, pos + 1) : q.kv;
       const int lo = valid && p.window > 0 ? max(0, pos - p.window + 1) : 0;
+      const uint32_t* mask = kTree ? reinterpret_cast<const uint32_t*>(p.masks + (int64_t)(q.r0 + (valid ? tk : 0)) * p.words) : nullptr;
       float m = -INFINITY, l = 0.f;
       int done = 0;
 #pragma unroll 1
@@ -1008,7 +764,17 @@ __global__ void __launch_bounds__(Geo<kTree, kQuant>::kThreads, 1) attend_tc_ker
           ld64(tS, a);
           ld64(tS + 64, b);
           ld_wait(a, b);
-          if (__any_sync(0xffffffffu, kb < lo || kb + kKeys > hi)) {
+          if (kTree && __any_sync(0xffffffffu, kb < lo || kb + kKeys > hi)) {
+            uint32_t mk[4];  // bit e of word w: key kb + 32 w + e is seen
+#pragma unroll
+            for (int w = 0; w < 4; ++w) mk[w] = valid ? mask_bits(mask, 2 * p.words, kb + 32 * w, lo, q.kv - q.n, q.kv) : 0xffffffffu;
+#pragma unroll
+            for (int e = 0; e < 64; ++e) {
+              if (!(mk[e >> 5] >> (e & 31) & 1)) a[e] = -INFINITY;
+              if (!(mk[2 + (e >> 5)] >> (e & 31) & 1)) b[e] = -INFINITY;
+            }
+          }
+          if (!kTree && __any_sync(0xffffffffu, kb < lo || kb + kKeys > hi)) {
             const unsigned span = hi > lo ? (unsigned)(hi - lo) : 0u;
 #pragma unroll
             for (int e = 0; e < 64; ++e) {
@@ -1052,7 +818,7 @@ __global__ void __launch_bounds__(Geo<kTree, kQuant>::kThreads, 1) attend_tc_ker
             pk[e] = pack_bf16(u, v);
           }
           st32(tS, pk);
-          if (NT == 2) {
+          if (NT == 2 || kQuant) {
             st_wait();
             tc_fence_before();
             mbar_arrive(&c.p_half[x]);
@@ -1073,7 +839,7 @@ __global__ void __launch_bounds__(Geo<kTree, kQuant>::kThreads, 1) attend_tc_ker
           m = m_new;
         }
         tc_fence_before();
-        if (NT == 2 && !warp_valid) mbar_arrive(&c.p_half[x]);
+        if ((NT == 2 || kQuant) && !warp_valid) mbar_arrive(&c.p_half[x]);
         mbar_arrive(&c.p_full[x]);
       }
       // ---- the segment's rows
@@ -1159,6 +925,7 @@ __global__ void __launch_bounds__(Geo<kTree, kQuant>::kThreads, 1) attend_tc_ker
       }
       tc_fence_before();
       mbar_arrive(&c.o_free[NT == 2 ? x : 0]);
+      if (NT == 1 && kQuant && n > 1) mbar_arrive(&c.o_free[1]);  // (each stream's warp counts the segments that it works in)
       q = nq;
       have = more;
       ++seg;
@@ -1304,7 +1071,7 @@ cudaError_t launch(const AttendParams& p, const AttendWork& w, int sms, cudaStre
   a[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(sms);
-  c.blockDim = dim3(Geo<kTree, kQuant>::kThreads);
+  c.blockDim = dim3(Geo<kQuant>::kThreads);
   c.dynamicSmemBytes = Cfg<HD, NT, kQuant>::kSmem;
   c.stream = st;
   c.attrs = a;
