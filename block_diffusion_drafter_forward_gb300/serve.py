@@ -132,6 +132,8 @@ def _rows_of(t, name: str, dtype: torch.dtype, shape: Tuple[int, ...], device: t
     if not ok:
         _refuse(t, name, dtype, shape, device)
     rows, heads, dim = shape
+    if t.is_contiguous():
+        return t.data_ptr(), heads * dim
     s0, s1, s2 = t.stride()
     if s2 == 1 and s1 == dim and (s0 >= heads * dim or rows <= 1):
         return t.data_ptr(), (s0 if rows > 1 else heads * dim)
@@ -253,8 +255,10 @@ def draft_tree(parents: torch.Tensor, kv_lens: torch.Tensor, row_starts: torch.T
         a_par, a_kv, a_rs, a_pos, a_mask = _addresses(
             dev, (parents, "parents", _I32, (n,)), (kv_lens, "kv_lens", _I32, (nb,)), (row_starts, "row_starts", _I32, (nb + 1,)),
             (positions, "out.positions", _I32, (n,)), (masks, "out.masks", _I64, (n, words)))
-        L.dflash_draft_tree(a_par, a_kv, a_rs, _i32(nb, "sequences"), _i32(n, "rows"), max_nodes, a_pos, a_mask,
-                            _status_word(dev).data_ptr(), st)
+        rc = L.load().dflash_draft_tree(a_par, a_kv, a_rs, _i32(nb, "sequences"), _i32(n, "rows"), max_nodes, a_pos, a_mask,
+                                        _status_word(dev).data_ptr(), st)
+        if rc:
+            L._check(rc, None)
     return out
 
 
@@ -272,6 +276,7 @@ class Rope:
             device = torch.device("cuda", torch.cuda.current_device())
         with torch.inference_mode(False):
             self.turns = torch.tensor(turns, dtype=_I64).to(device)  # (below 2^62)
+        self._device, self._a_turns = self.turns.device, self.turns.data_ptr()
         if device.type == "cuda":  # there for every stream
             torch.cuda.current_stream(device).synchronize()
 
@@ -288,8 +293,8 @@ class Rope:
             ok = False
         if not ok:
             _first(q, "q", 3, (_BF16, _F32))
-        if self.turns.device != dev:
-            raise ValueError(f"q: the table is on {self.turns.device}, got a tensor on {dev}")
+        if self._device != dev:
+            raise ValueError(f"q: the table is on {self._device}, got a tensor on {dev}")
         a_q, qs = _rows_of(q, "q", dtype, (n, nh, hd), dev)
         a_pos, = _addresses(dev, (positions, "positions", _I32, (n,)))
         a_k = ks = a_ko = kos = nk = 0
@@ -308,9 +313,11 @@ class Rope:
                 if k_out is None:
                     k_out = torch.empty((n, nk, hd), dtype=dtype, device=dev)
                 a_ko, kos = _rows_of(k_out, "k_out", dtype, (n, nk, hd), dev)
-            L.dflash_rotate(a_q, qs, a_o, os_, nh, a_k, ks, a_ko, kos, nk, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32,
-                            _i32(n, "rows"), hd, self.rotary_dim, int(self.interleaved), 1 if inverse else 0, a_pos,
-                            self.turns.data_ptr(), self.mscale, st)
+            rc = L.load().dflash_rotate(a_q, qs, a_o, os_, nh, a_k, ks, a_ko, kos, nk, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32,
+                                        _i32(n, "rows"), hd, self.rotary_dim, self.interleaved, inverse, a_pos, self._a_turns,
+                                        self.mscale, st)
+            if rc:
+                L._check(rc, None)
         return out if k is None else (out, k_out)
 
 
@@ -338,6 +345,7 @@ class PagedKV:
         self._rows = (dtype,)
         self._c = L.dflash_kv_pages(pool.data_ptr(), st[0] if P > 1 else 2 * nkv * tile, _status_word(dev).data_ptr(),
                                     L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32, nkv, self.head_dim, P)
+        self._ref = ctypes.byref(self._c)
         self._workspace = None  # bytes that a call of attend needs
 
     @classmethod
@@ -385,9 +393,12 @@ class PagedKV:
             _first(q, "q", 3, self._rows)
         shape = (n, nh, hd)
         a_q, qs = _rows_of(q, "q", dtype, shape, dev)
-        a_pt, a_kv, a_rs = _addresses(dev, (page_tables, "page_tables", _I32, (nb, mpps)), (kv_lens, "kv_lens", _I32, (nb,)),
-                                      (row_starts, "row_starts", _I32, (nb + 1,)))
-        a_lse = 0 if lse is None else _addresses(dev, (lse, "lse", _F32, (n, nh)))[0]
+        lens = ((page_tables, "page_tables", _I32, (nb, mpps)), (kv_lens, "kv_lens", _I32, (nb,)), (row_starts, "row_starts", _I32, (nb + 1,)))
+        if lse is None:
+            a_lse = 0
+            a_pt, a_kv, a_rs = _addresses(dev, *lens)
+        else:
+            a_pt, a_kv, a_rs, a_lse = _addresses(dev, *lens, (lse, "lse", _F32, (n, nh)))
         a_pos = a_mask = words = 0
         if tree is not None:
             positions, masks = tree
@@ -405,10 +416,13 @@ class PagedKV:
                 if need is None:
                     need = self._workspace = L.dflash_attend_workspace(self._c)
             ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-            L.dflash_attend_ex(self._c, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32, a_q, qs, a_pt,
-                               _i32(mpps, "pages of a sequence"), a_kv, a_rs, _i32(nb, "sequences"), _i32(n, "rows"),
-                               _limit(max_new), nh, 1.0 / math.sqrt(hd) if scale is None else float(scale), _limit(window),
-                               1 if causal else 0, a_mask, words, a_pos, a_out, os_, a_lse, ws.data_ptr() if need else 0, need, st)
+            rc = L.load().dflash_attend_ex(
+                self._ref, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32, a_q, qs, a_pt, _i32(mpps, "pages of a sequence"),
+                a_kv, a_rs, _i32(nb, "sequences"), _i32(n, "rows"), _limit(max_new), nh,
+                1.0 / math.sqrt(hd) if scale is None else float(scale), _limit(window), 1 if causal else 0, a_mask or None, words,
+                a_pos or None, a_out, os_, a_lse, ws.data_ptr() if need else 0, need, st)
+            if rc:
+                L._check(rc, None)
         return out if lse is None else (out, lse)
 
     def keep(self, page_tables: torch.Tensor, ctx_lens: torch.Tensor, path: torch.Tensor, path_lens: torch.Tensor,
@@ -426,8 +440,10 @@ class PagedKV:
             dev, (page_tables, "page_tables", _I32, (nb, mpps)), (ctx_lens, "ctx_lens", _I32, (nb,)),
             (path, "path", _I32, (nb, longest)), (path_lens, "path_lens", _I32, (nb,)))
         with _on(dev, stream) as st:
-            L.dflash_keep_rows(self._c, a_pt, _i32(mpps, "pages of a sequence"), a_ctx, _i32(nb, "sequences"), a_path,
-                               _i32(longest, "nodes of a path"), a_len, st)
+            rc = L.load().dflash_keep_rows(self._ref, a_pt, _i32(mpps, "pages of a sequence"), a_ctx, _i32(nb, "sequences"), a_path,
+                                           _i32(longest, "nodes of a path"), a_len, st)
+            if rc:
+                L._check(rc, None)
         return self.pool
 
 
@@ -454,6 +470,7 @@ class QuantKV(PagedKV):
         self._rows = (_BF16, _F32)
         self._c = L.dflash_kv_pages(pool.data_ptr(), st[0] if P > 1 else nkv * size, _status_word(dev).data_ptr(),
                                     L.DFLASH_FP8E4M3_ROWEXP, nkv, self.head_dim, P)
+        self._ref = ctypes.byref(self._c)
         self._workspace = None
 
     @classmethod
@@ -477,8 +494,10 @@ class QuantKV(PagedKV):
         a_k, ks = _rows_of(k, "k", dtype, shape, dev)
         a_v, vs = _rows_of(v, "v", dtype, shape, dev)
         with _on(dev, stream) as st:
-            L.dflash_append_kv_quant(self._c, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32, a_k, ks, a_v, vs, a_s,
-                                     _i32(n, "rows"), st)
+            rc = L.load().dflash_append_kv_quant(self._ref, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32, a_k, ks, a_v, vs, a_s,
+                                                 _i32(n, "rows"), st)
+            if rc:
+                L._check(rc, None)
         return self.pool
 
     def read(self, slots: torch.Tensor, dtype: torch.dtype = _BF16, k: Optional[torch.Tensor] = None,
@@ -502,8 +521,10 @@ class QuantKV(PagedKV):
                 v = torch.empty(shape, dtype=dtype, device=dev)
             a_k, ks = _rows_of(k, "k", dtype, shape, dev)
             a_v, vs = _rows_of(v, "v", dtype, shape, dev)
-            L.dflash_read_kv_quant(self._c, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32, a_s, _i32(n, "rows"), a_k, ks,
-                                   a_v, vs, st)
+            rc = L.load().dflash_read_kv_quant(self._ref, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32, a_s, _i32(n, "rows"),
+                                               a_k, ks, a_v, vs, st)
+            if rc:
+                L._check(rc, None)
         return k, v
 
 
