@@ -109,7 +109,8 @@ def _limit(n) -> int:
 def _addresses(device: torch.device, *wanted) -> list:
     """The addresses of contiguous tensors on `device`, given as (tensor, name, dtype, shape); raises for
     the first that is something else.  (A loop of plain comparisons: the smallest calls cost little more.)"""
-    i = device.index if device.type == "cuda" else -1  # get_device() of a host tensor is -1
+    i = device.index
+    i = -1 if i is None else i  # get_device() of a host tensor is -1
     out = []
     for t, name, dtype, shape in wanted:
         try:
@@ -124,7 +125,8 @@ def _addresses(device: torch.device, *wanted) -> list:
 
 def _rows_of(t, name: str, dtype: torch.dtype, shape: Tuple[int, ...], device: torch.device) -> Tuple[int, int]:
     """(address, elements between rows) of a [rows, heads, dim] tensor whose heads are contiguous."""
-    i = device.index if device.type == "cuda" else -1
+    i = device.index
+    i = -1 if i is None else i
     try:
         ok = t.dtype is dtype and t.get_device() == i and t.shape == shape
     except AttributeError:
@@ -143,7 +145,8 @@ def _rows_of(t, name: str, dtype: torch.dtype, shape: Tuple[int, ...], device: t
     return t.data_ptr(), (s0 if rows > 1 else heads * dim)
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+_device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 class _On:
@@ -183,8 +186,8 @@ class _Here:
 
 def _on(device: torch.device, stream: Optional[torch.cuda.Stream]):
     i = device.index
-    if stream is None and torch.cuda.current_device() == i:
-        return _Here(_raw_stream(i) if _raw_stream else torch.cuda.current_stream(device).cuda_stream)
+    if stream is None and _device_now() == i:
+        return _Here(_raw_stream(i))
     return _On(device, stream)
 
 
@@ -248,17 +251,20 @@ def draft_tree(parents: torch.Tensor, kv_lens: torch.Tensor, row_starts: torch.T
     if not 1 <= max_nodes <= 512:
         raise ValueError("max_nodes must be in [1, 512]")
     words = (max_nodes + 63) // 64
-    with _on(dev, stream) as st:
-        if out is None:
-            out = TreePlan(torch.empty(n, dtype=_I32, device=dev), torch.empty((n, words), dtype=_I64, device=dev))
-        positions, masks = out
-        a_par, a_kv, a_rs, a_pos, a_mask = _addresses(
-            dev, (parents, "parents", _I32, (n,)), (kv_lens, "kv_lens", _I32, (nb,)), (row_starts, "row_starts", _I32, (nb + 1,)),
-            (positions, "out.positions", _I32, (n,)), (masks, "out.masks", _I64, (n, words)))
-        rc = L.load().dflash_draft_tree(a_par, a_kv, a_rs, _i32(nb, "sequences"), _i32(n, "rows"), max_nodes, a_pos, a_mask,
-                                        _status_word(dev).data_ptr(), st)
-        if rc:
-            L._check(rc, None)
+    if stream is not None or _device_now() != dev.index:
+        with _On(dev, stream):
+            return draft_tree(parents, kv_lens, row_starts, max_nodes, out)
+    st = _raw_stream(dev.index)
+    if out is None:
+        out = TreePlan(torch.empty(n, dtype=_I32, device=dev), torch.empty((n, words), dtype=_I64, device=dev))
+    positions, masks = out
+    a_par, a_kv, a_rs, a_pos, a_mask = _addresses(
+        dev, (parents, "parents", _I32, (n,)), (kv_lens, "kv_lens", _I32, (nb,)), (row_starts, "row_starts", _I32, (nb + 1,)),
+        (positions, "out.positions", _I32, (n,)), (masks, "out.masks", _I64, (n, words)))
+    rc = L.load().dflash_draft_tree(a_par, a_kv, a_rs, _i32(nb, "sequences"), _i32(n, "rows"), max_nodes, a_pos, a_mask,
+                                    _status_word(dev).data_ptr(), st)
+    if rc:
+        L._check(rc, None)
     return out
 
 
@@ -305,19 +311,22 @@ class Rope:
             a_k, ks = _rows_of(k, "k", dtype, (n, nk, hd), dev)
         elif k_out is not None:
             raise ValueError("k_out: given without k")
-        with _on(dev, stream) as st:
-            if out is None:
-                out = torch.empty((n, nh, hd), dtype=dtype, device=dev)
-            a_o, os_ = _rows_of(out, "out", dtype, (n, nh, hd), dev)
-            if k is not None:
-                if k_out is None:
-                    k_out = torch.empty((n, nk, hd), dtype=dtype, device=dev)
-                a_ko, kos = _rows_of(k_out, "k_out", dtype, (n, nk, hd), dev)
-            rc = L.load().dflash_rotate(a_q, qs, a_o, os_, nh, a_k, ks, a_ko, kos, nk, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32,
-                                        _i32(n, "rows"), hd, self.rotary_dim, self.interleaved, inverse, a_pos, self._a_turns,
-                                        self.mscale, st)
-            if rc:
-                L._check(rc, None)
+        if stream is not None or _device_now() != dev.index:
+            with _On(dev, stream):
+                return self.rotate(q, positions, k, out, k_out, inverse)
+        st = _raw_stream(dev.index)
+        if out is None:
+            out = torch.empty((n, nh, hd), dtype=dtype, device=dev)
+        a_o, os_ = _rows_of(out, "out", dtype, (n, nh, hd), dev)
+        if k is not None:
+            if k_out is None:
+                k_out = torch.empty((n, nk, hd), dtype=dtype, device=dev)
+            a_ko, kos = _rows_of(k_out, "k_out", dtype, (n, nk, hd), dev)
+        rc = L.load().dflash_rotate(a_q, qs, a_o, os_, nh, a_k, ks, a_ko, kos, nk, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32,
+                                    _i32(n, "rows"), hd, self.rotary_dim, self.interleaved, inverse, a_pos, self._a_turns,
+                                    self.mscale, st)
+        if rc:
+            L._check(rc, None)
         return out if k is None else (out, k_out)
 
 
@@ -406,23 +415,26 @@ class PagedKV:
             a_pos, a_mask = _addresses(dev, (positions, "tree.positions", _I32, (n,)), (masks, "tree.masks", _I64, (n, words)))
             if not n:
                 a_pos = a_mask = words = 0
-        with _on(dev, stream) as st:
-            if out is None:
-                out = torch.zeros(shape, dtype=dtype, device=dev)
-            a_out, os_ = _rows_of(out, "out", dtype, shape, dev)
-            need = 0
-            if dtype is _BF16:
-                need = self._workspace
-                if need is None:
-                    need = self._workspace = L.dflash_attend_workspace(self._c)
-            ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-            rc = L.load().dflash_attend_ex(
-                self._ref, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32, a_q, qs, a_pt, _i32(mpps, "pages of a sequence"),
-                a_kv, a_rs, _i32(nb, "sequences"), _i32(n, "rows"), _limit(max_new), nh,
-                1.0 / math.sqrt(hd) if scale is None else float(scale), _limit(window), 1 if causal else 0, a_mask or None, words,
-                a_pos or None, a_out, os_, a_lse, ws.data_ptr() if need else 0, need, st)
-            if rc:
-                L._check(rc, None)
+        if stream is not None or _device_now() != dev.index:
+            with _On(dev, stream):
+                return self.attend(q, page_tables, kv_lens, row_starts, max_new, causal, window, scale, out, lse, tree=tree)
+        st = _raw_stream(dev.index)
+        if out is None:
+            out = torch.zeros(shape, dtype=dtype, device=dev)
+        a_out, os_ = _rows_of(out, "out", dtype, shape, dev)
+        need = 0
+        if dtype is _BF16:
+            need = self._workspace
+            if need is None:
+                need = self._workspace = L.dflash_attend_workspace(self._c)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        rc = L.load().dflash_attend_ex(
+            self._ref, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32, a_q, qs, a_pt, _i32(mpps, "pages of a sequence"),
+            a_kv, a_rs, _i32(nb, "sequences"), _i32(n, "rows"), _limit(max_new), nh,
+            1.0 / math.sqrt(hd) if scale is None else float(scale), _limit(window), 1 if causal else 0, a_mask or None, words,
+            a_pos or None, a_out, os_, a_lse, ws.data_ptr() if need else 0, need, st)
+        if rc:
+            L._check(rc, None)
         return out if lse is None else (out, lse)
 
     def keep(self, page_tables: torch.Tensor, ctx_lens: torch.Tensor, path: torch.Tensor, path_lens: torch.Tensor,
@@ -439,11 +451,14 @@ class PagedKV:
         a_pt, a_ctx, a_path, a_len = _addresses(
             dev, (page_tables, "page_tables", _I32, (nb, mpps)), (ctx_lens, "ctx_lens", _I32, (nb,)),
             (path, "path", _I32, (nb, longest)), (path_lens, "path_lens", _I32, (nb,)))
-        with _on(dev, stream) as st:
-            rc = L.load().dflash_keep_rows(self._ref, a_pt, _i32(mpps, "pages of a sequence"), a_ctx, _i32(nb, "sequences"), a_path,
-                                           _i32(longest, "nodes of a path"), a_len, st)
-            if rc:
-                L._check(rc, None)
+        if stream is not None or _device_now() != dev.index:
+            with _On(dev, stream):
+                return self.keep(page_tables, ctx_lens, path, path_lens)
+        st = _raw_stream(dev.index)
+        rc = L.load().dflash_keep_rows(self._ref, a_pt, _i32(mpps, "pages of a sequence"), a_ctx, _i32(nb, "sequences"), a_path,
+                                       _i32(longest, "nodes of a path"), a_len, st)
+        if rc:
+            L._check(rc, None)
         return self.pool
 
 
@@ -493,11 +508,14 @@ class QuantKV(PagedKV):
         shape = (n, self.pool.shape[1], self.head_dim)
         a_k, ks = _rows_of(k, "k", dtype, shape, dev)
         a_v, vs = _rows_of(v, "v", dtype, shape, dev)
-        with _on(dev, stream) as st:
-            rc = L.load().dflash_append_kv_quant(self._ref, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32, a_k, ks, a_v, vs, a_s,
-                                                 _i32(n, "rows"), st)
-            if rc:
-                L._check(rc, None)
+        if stream is not None or _device_now() != dev.index:
+            with _On(dev, stream):
+                return self.append(k, v, slots)
+        st = _raw_stream(dev.index)
+        rc = L.load().dflash_append_kv_quant(self._ref, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32, a_k, ks, a_v, vs, a_s,
+                                             _i32(n, "rows"), st)
+        if rc:
+            L._check(rc, None)
         return self.pool
 
     def read(self, slots: torch.Tensor, dtype: torch.dtype = _BF16, k: Optional[torch.Tensor] = None,
@@ -514,17 +532,20 @@ class QuantKV(PagedKV):
             raise
         a_s, = _addresses(dev, (slots, "slots", _I32, (n,)))
         shape = (n, self.pool.shape[1], self.head_dim)
-        with _on(dev, stream) as st:
-            if k is None:
-                k = torch.empty(shape, dtype=dtype, device=dev)
-            if v is None:
-                v = torch.empty(shape, dtype=dtype, device=dev)
-            a_k, ks = _rows_of(k, "k", dtype, shape, dev)
-            a_v, vs = _rows_of(v, "v", dtype, shape, dev)
-            rc = L.load().dflash_read_kv_quant(self._ref, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32, a_s, _i32(n, "rows"),
-                                               a_k, ks, a_v, vs, st)
-            if rc:
-                L._check(rc, None)
+        if stream is not None or _device_now() != dev.index:
+            with _On(dev, stream):
+                return self.read(slots, dtype, k, v)
+        st = _raw_stream(dev.index)
+        if k is None:
+            k = torch.empty(shape, dtype=dtype, device=dev)
+        if v is None:
+            v = torch.empty(shape, dtype=dtype, device=dev)
+        a_k, ks = _rows_of(k, "k", dtype, shape, dev)
+        a_v, vs = _rows_of(v, "v", dtype, shape, dev)
+        rc = L.load().dflash_read_kv_quant(self._ref, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32, a_s, _i32(n, "rows"),
+                                           a_k, ks, a_v, vs, st)
+        if rc:
+            L._check(rc, None)
         return k, v
 
 
