@@ -22,7 +22,7 @@
 namespace dflash {
 namespace {
 
-constexpr int kRows = 16;
+constexpr int kRows = 16, kWarps = 8;
 
 struct QuantParams {
   const uint8_t *k, *v;  // rows (append) ...
@@ -35,37 +35,33 @@ struct QuantParams {
   int n, nkv, num_pages;
 };
 
-// Entries of the block's rows in s_entry (row, | 64: a run), rows without a place in s_none.
+// What a warp finds out by itself of the block's rows (every warp alike, without a barrier: with one, seven warps of
+// eight waited for the first at 30 % of HBM).  Lane l holds the slot of row r0 - 7 + l - the rows here, and seven on
+// either side that a run may reach - and the l-th entry: its row, | 64 for a run.
 struct Entries {
-  int slot[kRows + 14], entry[kRows], none[kRows], n, n_none;
+  int slot, entry, n;
+  unsigned none;  // rows without a place, a bit each
 };
-__device__ __forceinline__ void find_entries(Entries& e, const QuantParams& p, int r0) {
-  const int t = threadIdx.x;
-  if (t < kRows + 14) {  // the rows here, and seven on either side that a run may reach
-    const int r = r0 - 7 + t;
-    e.slot[t] = r >= 0 && r < p.n ? p.slots[r] : -1;
-  }
-  __syncthreads();
-  if (t < 32) {
-    bool take = false, run = false, none = false;
-    if (t < kRows && r0 + t < p.n) {
-      const int slot = e.slot[7 + t];
-      none = slot < 0 || slot / kPage >= p.num_pages;
-      if (none) {
-        if (slot >= 0 && p.status && blockIdx.y == 0) atomicOr(p.status, DFLASH_DEV_BAD_PAGE);
-      } else {
-        const int o = slot & 7, first = 7 + t - o;  // a row's run is decided alike in every block that sees it
-        run = true;
-        for (int k = 0; k < 8; ++k) run = run && e.slot[first + k] == slot - o + k;
-        take = !run || o == 0;  // a run belongs to the block of its first row
-      }
-    }
-    const unsigned m = __ballot_sync(0xffffffffu, take), z = __ballot_sync(0xffffffffu, none), below = (1u << t) - 1;
-    if (take) e.entry[__popc(m & below)] = t | (run ? 64 : 0);
-    if (none) e.none[__popc(z & below)] = t;
-    if (t == 0) e.n = __popc(m), e.n_none = __popc(z);
-  }
-  __syncthreads();
+__device__ __forceinline__ Entries find_entries(const QuantParams& p, int r0) {
+  Entries e;
+  const int lane = threadIdx.x & 31, r = r0 - 7 + lane;
+  e.slot = lane < kRows + 14 && r >= 0 && r < p.n ? p.slots[r] : -1;
+  const bool good = e.slot >= 0 && e.slot / kPage < p.num_pages;
+  if (threadIdx.x < 32 && blockIdx.y == 0 && p.status && lane >= 7 && lane < 7 + kRows && e.slot >= 0 && !good)
+    atomicOr(p.status, DFLASH_DEV_BAD_PAGE);
+  const int before = __shfl_up_sync(0xffffffffu, e.slot, 1);
+  const unsigned next = __ballot_sync(0xffffffffu, lane > 0 && good && before >= 0 && e.slot == before + 1);  // one behind the row before
+  const unsigned first = __ballot_sync(0xffffffffu, good && (e.slot & 7) == 0);
+  const int o = e.slot & 7, s = lane - o;  // a row's run is decided alike in every block that sees it
+  const bool run = good && s >= 0 && (first >> s & 1) && (next >> s >> 1 & 0x7f) == 0x7f;
+  const bool here = lane >= 7 && lane < 7 + kRows && r < p.n;
+  const unsigned take = __ballot_sync(0xffffffffu, here && good && (!run || o == 0));  // a run belongs to the block of its first row
+  const unsigned runs = __ballot_sync(0xffffffffu, run);
+  e.none = __ballot_sync(0xffffffffu, here && !good) >> 7;
+  e.n = __popc(take);
+  const int at = (int)__fns(take, 0, lane + 1);  // (-1: no such entry)
+  e.entry = at < 0 ? 0 : (at - 7) | (runs >> at & 1 ? 64 : 0);
+  return e;
 }
 
 // Eight dims of a row as they are loaded, and as fp32.
@@ -94,31 +90,36 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 
-// Codes of a row held eight dims a lane by kLanes neighbouring lanes (infinities as NaN); *e: its exponent byte.
+// Codes of a row held eight dims a lane by kLanes neighbouring lanes; *e: its exponent byte.  NaN become NaN by the
+// conversion and are no maximum; rows with infinities (a maximum of infinity) are looked at once more.
 template <int kLanes, typename T>
 __device__ __forceinline__ uint2 encode(const Raw<T>& raw, int* e) {
   float x[8];
   open8(raw, x);
-  uint32_t top = 0;  // largest finite magnitude, by its bits
+  float m = fmaxf(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))),
+                  fmaxf(fmaxf(fabsf(x[4]), fabsf(x[5])), fmaxf(fabsf(x[6]), fabsf(x[7]))));
+  m = m == m ? m : 0.f;  // (all of them NaN)
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t b = __float_as_uint(x[i]) & 0x7fffffffu;
-    if (b < 0x7f800000u) top = max(top, b);
+  for (int o = kLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (__any_sync(0xffffffffu, m == INFINITY)) {
+    m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (fabsf(x[i]) == INFINITY) x[i] = __uint_as_float(0x7fc00000u);
+      m = fmaxf(m, fabsf(x[i]));
+    }
+    m = m == m ? m : 0.f;
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   }
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const uint32_t top = __float_as_uint(m);
   // max = 1.m 2^(E - 127) <= 448 2^k = 1.75 2^(k + 8)
   const int k = min(max((int)(top >> 23) - 135 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0), -118), 119);
   *e = k + 127;
   const float f = pow2i(-k);
   uint32_t c[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float a = x[2 * i] * f, b = x[2 * i + 1] * f;
-    if ((__float_as_uint(x[2 * i]) & 0x7f800000u) == 0x7f800000u) a = __uint_as_float(0x7fc00000u);
-    if ((__float_as_uint(x[2 * i + 1]) & 0x7f800000u) == 0x7f800000u) b = __uint_as_float(0x7fc00000u);
-    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-  }
+  for (int i = 0; i < 4; ++i) c[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * f, x[2 * i + 1] * f), __NV_SATFINITE, __NV_E4M3);
   return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 __device__ __forceinline__ void decode4(uint32_t w, float f, float* x) {
@@ -138,18 +139,36 @@ __device__ __forceinline__ void transpose4(uint32_t (&w)[4]) {
   w[2] = __byte_perm(c, d, 0x5410), w[3] = __byte_perm(c, d, 0x7632);
 }
 
+// The units (entry, heads) of a warp: every kWarps-th, entries first.
+struct Units {
+  int entry, head, de, dh, n;
+  __device__ __forceinline__ Units(int warp, int n) : entry(warp % max(n, 1)), head(warp / max(n, 1)), de(kWarps % max(n, 1)), dh(kWarps / max(n, 1)), n(n) {}
+  __device__ __forceinline__ void next() {
+    entry += de, head += dh;
+    if (entry >= n) entry -= n, ++head;
+  }
+};
+// Bytes of a half page's rows (j = 0 or 8) in a tile, d a multiple of 8: K of row j + 2 r + half, and V of rows j + 4 half .. + 3
+// of dim d + x.  (k8_in_tile and v8_in_tile with what is known of j and d.)
+__device__ __forceinline__ int k_of_run(int j, int half, int r, int d) {
+  return (d >> 6) * 1024 + (d & 8) + (j + half) * 64 + r * 128 + (((d >> 4 & 3) ^ r) * 16);
+}
+__device__ __forceinline__ int v_of_run(int j, int half, int d, int x) {
+  return (d >> 5) * 512 + (d >> 3 & 3) * 4 + x * 64 + (((j >> 2) + half) ^ (x >> 1)) * 16;
+}
+
 template <typename T, int HD>
-__global__ void __launch_bounds__(256) append_quant_kernel(const QuantParams p) {
-  __shared__ Entries e;
+__global__ void __launch_bounds__(32 * kWarps) append_quant_kernel(const QuantParams p) {
   constexpr int kPieces = HD / 8, kHeads = 16 / kPieces;  // lanes of a row; heads of a warp
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r0 = blockIdx.x * kRows;
-  find_entries(e, p, r0);
+  const Entries e = find_entries(p, r0);
   const int half = lane >> 4, sub = (lane & 15) / kPieces, d = lane % kPieces * 8;
-  const int groups = (p.nkv + kHeads - 1) / kHeads, per = gridDim.y;
-  for (int u = warp; u < e.n * ((groups - (int)blockIdx.y + per - 1) / per); u += 8) {
-    const int en = e.entry[u % e.n], h = (blockIdx.y + u / e.n * per) * kHeads + sub;
+  const int groups = (p.nkv + kHeads - 1) / kHeads, per = gridDim.y, mine = (groups - (int)blockIdx.y + per - 1) / per;
+  if (e.n == 0) return;
+  for (Units u(warp, e.n); u.head < mine; u.next()) {
+    const int en = __shfl_sync(0xffffffffu, e.entry, u.entry), h = (blockIdx.y + u.head * per) * kHeads + sub;
     const bool on = h < p.nkv;  // (lanes past the last head follow its neighbours' shuffles)
-    const int i = en & 63, slot = e.slot[7 + i], j = slot % kPage;
+    const int i = en & 63, slot = __shfl_sync(0xffffffffu, e.slot, 7 + i), j = slot % kPage;
     const int64_t row = r0 + i;
     uint8_t* tile = p.pool + (int64_t)(slot / kPage) * p.page_bytes + (int64_t)h * (32 * HD + 32);
     const uint8_t* src[2] = {p.k + row * p.ks, p.v + row * p.vs};
@@ -172,9 +191,8 @@ __global__ void __launch_bounds__(256) append_quant_kernel(const QuantParams p) 
       for (int r = 0; r < 4; ++r) {
         int ex;
         const uint2 c = encode<kPieces>(x[r], &ex);
-        const int jr = j + 2 * r + half;
-        if (on) *reinterpret_cast<uint2*>(tile + k8_in_tile(jr, d)) = c;
-        if (on && d == 0) tile[32 * HD + jr] = (uint8_t)ex;
+        if (on) *reinterpret_cast<uint2*>(tile + k_of_run(j, half, r, d)) = c;
+        if (on && d == 0) tile[32 * HD + j + 2 * r + half] = (uint8_t)ex;
       }
       uint32_t lo[4], hi[4];
 #pragma unroll
@@ -189,8 +207,8 @@ __global__ void __launch_bounds__(256) append_quant_kernel(const QuantParams p) 
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         if (!on) continue;
-        *reinterpret_cast<uint32_t*>(tile + 16 * HD + v8_in_tile(j + 4 * half, d + r)) = lo[r];
-        *reinterpret_cast<uint32_t*>(tile + 16 * HD + v8_in_tile(j + 4 * half, d + 4 + r)) = hi[r];
+        *reinterpret_cast<uint32_t*>(tile + 16 * HD + v_of_run(j, half, d, r)) = lo[r];
+        *reinterpret_cast<uint32_t*>(tile + 16 * HD + v_of_run(j, half, d, 4 + r)) = hi[r];
       }
     } else {  // K by the lower lanes, V by the upper ones
       Raw<T> x;
@@ -210,21 +228,20 @@ __global__ void __launch_bounds__(256) append_quant_kernel(const QuantParams p) 
 }
 
 template <typename T, int HD>
-__global__ void __launch_bounds__(256) read_quant_kernel(const QuantParams p) {
-  __shared__ Entries e;
+__global__ void __launch_bounds__(32 * kWarps) read_quant_kernel(const QuantParams p) {
   constexpr int kPieces = HD / 8, kHeads = 16 / kPieces;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r0 = blockIdx.x * kRows;
-  find_entries(e, p, r0);
+  const Entries e = find_entries(p, r0);
   const int half = lane >> 4, sub = (lane & 15) / kPieces, d = lane % kPieces * 8;
   const int groups = (p.nkv + kHeads - 1) / kHeads, per = gridDim.y, mine = (groups - (int)blockIdx.y + per - 1) / per;
   auto put = [&](int side, int64_t row, int h, const float (&x)[8]) {
     uint8_t* dst = (side ? p.vo + row * p.vs : p.ko + row * p.ks) + ((int64_t)h * HD + d) * sizeof(T);
     store8(reinterpret_cast<T*>(dst), x);
   };
-  for (int u = warp; u < e.n * mine; u += 8) {
-    const int en = e.entry[u % e.n], h = (blockIdx.y + u / e.n * per) * kHeads + sub;
+  for (Units u(warp, e.n); e.n > 0 && u.head < mine; u.next()) {
+    const int en = __shfl_sync(0xffffffffu, e.entry, u.entry), h = (blockIdx.y + u.head * per) * kHeads + sub;
+    const int i = en & 63, slot = __shfl_sync(0xffffffffu, e.slot, 7 + i), j = slot % kPage;
     if (h >= p.nkv) continue;
-    const int i = en & 63, slot = e.slot[7 + i], j = slot % kPage;
     const int64_t row = r0 + i;
     const uint8_t* tile = p.pool + (int64_t)(slot / kPage) * p.page_bytes + (int64_t)h * (32 * HD + 32);
     float x[8];
@@ -233,9 +250,9 @@ __global__ void __launch_bounds__(256) read_quant_kernel(const QuantParams p) {
       uint32_t lo[4], hi[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        c[r] = *reinterpret_cast<const uint2*>(tile + k8_in_tile(j + 2 * r + half, d));
-        lo[r] = *reinterpret_cast<const uint32_t*>(tile + 16 * HD + v8_in_tile(j + 4 * half, d + r));
-        hi[r] = *reinterpret_cast<const uint32_t*>(tile + 16 * HD + v8_in_tile(j + 4 * half, d + 4 + r));
+        c[r] = *reinterpret_cast<const uint2*>(tile + k_of_run(j, half, r, d));
+        lo[r] = *reinterpret_cast<const uint32_t*>(tile + 16 * HD + v_of_run(j, half, d, r));
+        hi[r] = *reinterpret_cast<const uint32_t*>(tile + 16 * HD + v_of_run(j, half, d, 4 + r));
       }
       const uint2 ek = *reinterpret_cast<const uint2*>(tile + 32 * HD + j), ev = *reinterpret_cast<const uint2*>(tile + 32 * HD + 16 + j);
       auto scale = [&](const uint2& b, int r) { return pow2i((int)((r < 4 ? b.x : b.y) >> 8 * (r & 3) & 255) - 127); };
@@ -267,18 +284,19 @@ __global__ void __launch_bounds__(256) read_quant_kernel(const QuantParams p) {
       put(half, row, h, x);
     }
   }
-#pragma unroll
-  for (int u = warp; u < e.n_none * mine; u += 8) {  // rows without a place: zeros
-    const int h = (blockIdx.y + u / e.n_none * per) * kHeads + sub;
+  for (unsigned none = e.none; none; none &= none - 1) {  // rows without a place: zeros
     const float x[8] = {};
-    if (h < p.nkv) put(half, r0 + e.none[u % e.n_none], h, x);
+    for (int u = warp; u < mine; u += kWarps) {
+      const int h = (blockIdx.y + u * per) * kHeads + sub;
+      if (h < p.nkv) put(half, r0 + __ffs(none) - 1, h, x);
+    }
   }
 }
 
 template <typename T, int HD>
 void launch(const QuantParams& p, bool read, dim3 grid, cudaStream_t st) {
-  if (read) read_quant_kernel<T, HD><<<grid, 256, 0, st>>>(p);
-  else append_quant_kernel<T, HD><<<grid, 256, 0, st>>>(p);
+  if (read) read_quant_kernel<T, HD><<<grid, 32 * kWarps, 0, st>>>(p);
+  else append_quant_kernel<T, HD><<<grid, 32 * kWarps, 0, st>>>(p);
 }
 
 int run(const char* name, const dflash_kv_pages* kv, int32_t dtype, QuantParams& p, int64_t ks, int64_t vs, bool read, dflash_stream stream) {
@@ -305,7 +323,7 @@ int run(const char* name, const dflash_kv_pages* kv, int32_t dtype, QuantParams&
   if (cudaError_t e = sm_count(&sms); e != cudaSuccess) return call_error(DFLASH_ECUDA, name, e);
   const int64_t blocks = (p.n + (int64_t)kRows - 1) / kRows;
   const int groups = (p.nkv + 128 / kv->head_dim - 1) / (128 / kv->head_dim);
-  const dim3 grid((unsigned)blocks, (unsigned)std::min<int64_t>(groups, std::max<int64_t>(1, 32 * sms / blocks)));
+  const dim3 grid((unsigned)blocks, (unsigned)std::min<int64_t>(groups, std::max<int64_t>(1, 16 * sms / blocks)));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == DFLASH_F32)
     kv->head_dim == 128 ? launch<float, 128>(p, read, grid, st) : launch<float, 64>(p, read, grid, st);

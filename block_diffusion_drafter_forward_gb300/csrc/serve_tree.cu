@@ -10,13 +10,12 @@ namespace dflash {
 namespace {
 
 constexpr int kMaxNodes = 512, kMaxWords = kMaxNodes / 64;
-constexpr int kTreeThreads = kMaxNodes;
 
-// A block per sequence, a thread per node.  Ancestors by pointer jumping: with A_i the node and the
-// ancestors seen so far and J_i the first one not seen, A_i |= A_{J_i} and J_i = J_{J_i} double
-// them, so log2(depth) rounds do.  Bound by latency (a round is one pass through shared memory).
-// Blocks from nb on empty the rows outside the sequences.
-__global__ void __launch_bounds__(kTreeThreads) draft_tree_kernel(const int32_t* parents, const int32_t* kv_lens,
+// A block per sequence, a thread per node (64 for every word of the masks).  Ancestors by pointer jumping: with A_i the
+// node and the ancestors seen so far and J_i the first one not seen, A_i |= A_{J_i} and J_i = J_{J_i} double
+// them, so log2(depth) rounds do.  Bound by latency: a round is one pass through shared memory and two
+// barriers.  Blocks from nb on empty the rows outside the sequences.
+__global__ void __launch_bounds__(kMaxNodes) draft_tree_kernel(const int32_t* parents, const int32_t* kv_lens,
                                                                   const int32_t* row_starts, int nb, int n_rows, int words,
                                                                   int32_t* positions, unsigned long long* masks,
                                                                   uint32_t* status) {
@@ -29,8 +28,8 @@ __global__ void __launch_bounds__(kTreeThreads) draft_tree_kernel(const int32_t*
   };
   if (s >= nb) {
     const int lo = min(max(row_starts[0], 0), n_rows), hi = min(max(row_starts[nb], lo), n_rows);
-    const int64_t n = (int64_t)lo + (n_rows - hi), step = (int64_t)(gridDim.x - nb) * kTreeThreads;
-    for (int64_t i = (int64_t)(s - nb) * kTreeThreads + t; i < n; i += step) clear(i < lo ? i : hi + (i - lo));
+    const int64_t n = (int64_t)lo + (n_rows - hi), step = (int64_t)(gridDim.x - nb) * blockDim.x;
+    for (int64_t i = (int64_t)(s - nb) * blockDim.x + t; i < n; i += step) clear(i < lo ? i : hi + (i - lo));
     return;
   }
   const int r0 = row_starts[s], r1 = row_starts[s + 1], kv = kv_lens[s];
@@ -39,7 +38,7 @@ __global__ void __launch_bounds__(kTreeThreads) draft_tree_kernel(const int32_t*
   const bool bad = out || kv < n, wide = !out && n > 64 * words;
   if (bad || wide) {
     if (t == 0 && status) atomicOr(status, (bad ? DFLASH_DEV_BAD_CTX : 0u) | (wide ? DFLASH_DEV_BAD_TREE : 0u));
-    for (int i = t; i < n; i += kTreeThreads) clear(r0 + i);
+    for (int i = t; i < n; i += blockDim.x) clear(r0 + i);
     return;
   }
   unsigned long long anc[kMaxWords];
@@ -215,8 +214,9 @@ extern "C" int dflash_draft_tree(const int32_t* parents, const int32_t* kv_lens,
   if (max_nodes < 1 || max_nodes > kMaxNodes) return call_error(DFLASH_EUNSUPPORTED, "draft_tree: max_nodes must be in [1, 512]");
   if (n_rows == 0) return DFLASH_OK;
   if (!parents || !kv_lens || !row_starts || !positions || !masks) return call_error(DFLASH_EINVAL, "draft_tree: null pointer");
-  const int rest = (int)std::min<int64_t>(64, ((int64_t)n_rows + kTreeThreads - 1) / kTreeThreads);
-  draft_tree_kernel<<<nb + rest, kTreeThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+  const int threads = (max_nodes + 63) / 64 * 64;  // as many as the masks have bits
+  const int rest = (int)std::min<int64_t>(64, ((int64_t)n_rows + threads - 1) / threads);
+  draft_tree_kernel<<<nb + rest, threads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
       parents, kv_lens, row_starts, nb, n_rows, (max_nodes + 63) / 64, positions, reinterpret_cast<unsigned long long*>(masks), status);
   if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return call_error(DFLASH_ECUDA, "draft_tree", e);
   return DFLASH_OK;
