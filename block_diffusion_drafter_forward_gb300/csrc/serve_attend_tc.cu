@@ -28,8 +28,19 @@
 // copies 3; 64 keys at a time, S a half ahead of the softmax, 10 more - Q is then read twice as
 // often, and shared memory gives S its Q and K at 128 B a cycle).
 //
+// Trees (kTree): the sequence's own rows are seen by a mask per row, the context by the window; the units' chunks
+// go to the sequence's end.  32 trees of 33-64 nodes on 0.5-8 Ki rows 155 us (34 % of the tensor pipe: part-full
+// tiles, and a unit of 33-48 nodes has one stream at work); one of 32 nodes on 4096 rows 19 us, latency.
+//
+// Pages in 8 bits (kQuant): see below.  32 blocks of 16 as above 86 us, a prompt of 8192 575 us.  With one tile a chunk
+// takes a CTA 1.87 us; without the widening 1.35, without its stores 1.51, K or V alone 1.6, with one of four
+// softmax warps at work 1.77: the 64 KB that are written to shared memory, beside the 96 KB that the MMAs read of
+// it, and the instruction caches hold it (its loops unrolled: 2.5 us; codes read ahead of the step before: 2.05;
+// two threads a query row in loops of 32 columns: 1.82, but with two tiles 680 us for the prompt).
+//
 // Rounding: P is bf16 (the MMA's operand type), sums and O fp32, the normaliser sums the fp32 P.
-// Warp roles: 0-3 stream 0, 4-7 stream 1, 8 K pages, 10 V pages, 9 and 11 MMA issue.  The V warp
+// Warp roles: 0-3 stream 0, 4-7 stream 1, 8 K pages, 10 V pages, 9 and 11 MMA issue (8 bits: 8 pages, 10 the next
+// segment's queries, 12-15 widening).  The V warp
 // also zeroes the key rows behind a sequence's end in its last page (never-written rows may hold
 // NaN, and 0 * NaN would reach O; their scores are masked by select).  Issuing an MMA blocks its
 // thread while the tensor pipe's queue is full, so with two tiles each stream has a warp of its own
