@@ -57,7 +57,8 @@ __global__ void __launch_bounds__(128) attend_simple_kernel(const AttendParams p
   const int ctx = kv - n, pos = p.masks ? max(ctx, p.positions[i]) : ctx + (i - r0);
   const unsigned long long* mask = p.masks ? p.masks + (int64_t)i * p.words : nullptr;
   const int k_end = p.causal && !mask ? min(kv, pos + 1) : kv;
-  const int k_begin = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+  const int first = pos - p.window + 1;  // (of the context: a tree's own rows go by the mask alone)
+  const int k_begin = p.window > 0 ? max(0, mask ? min(ctx, first) : first) : 0;
   float m = -INFINITY, l = 0.f, acc[HD / 32];
 #pragma unroll
   for (int e = 0; e < HD / 32; ++e) acc[e] = 0.f;

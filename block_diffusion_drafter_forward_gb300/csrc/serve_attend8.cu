@@ -4,7 +4,7 @@
 //
 // A unit is (sequence, tile of 16 / group tokens, kv head); its query rows are the 16 rows of an m16n8k16
 // matrix product.  Chunks of keys are spread over the CTAs as in the other form (serve_attend_plan.cuh).
-// In a CTA each of the 8 warps has its own ring of pages (K, V and exponents of 16 rows: one bulk copy)
+// In a CTA each of 11 warps has its own ring of pages (K, V and exponents of 16 rows: one bulk copy)
 // and its own running maximum, sum and O, so that no warp waits for another before the segment ends:
 //   S[16, 16 keys] = Q K^T, softmax over the lane's four keys of two rows, O += P V.
 // tcgen05 has nothing to give here: its smallest tile is 128 rows, of which a single token fills 8 or 16, and
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(Geo::kThreads, 1) attend8_kernel(const AttendP
       const int ctx = q.kv - q.n;
       pos[y] = !kTree ? ctx + tk[y] : valid[y] && p.window > 0 ? max(ctx, __ldg(p.positions + q.r0 + tk[y])) : 0;
       hi[y] = !valid[y] ? INT_MAX : kTree ? ctx : p.causal ? min(q.kv, pos[y] + 1) : q.kv;
-      lo[y] = valid[y] && p.window > 0 ? max(0, pos[y] - p.window + 1) : 0;
+      lo[y] = valid[y] && p.window > 0 ? max(0, kTree ? min(ctx, pos[y] - p.window + 1) : pos[y] - p.window + 1) : 0;
     }
     const int see_lo = __reduce_max_sync(0xffffffffu, max(lo[0], lo[1]));                       // pages within are seen whole
     const int see_hi = min(q.kv, __reduce_min_sync(0xffffffffu, min(hi[0], hi[1])));

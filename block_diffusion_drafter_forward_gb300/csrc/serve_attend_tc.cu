@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(Geo<kQuant>::kThreads, 1) attend_tc_kernel(con
       // (trees: keys [lo, hi) of the context, and those of the sequence's own rows that the mask has)
       const int pos = !kTree ? q.kv - q.n + tk : valid && p.window > 0 ? max(q.kv - q.n, __ldg(p.positions + q.r0 + tk)) : 0;
       const int hi = !valid ? INT_MAX : kTree ? q.kv - q.n : p.causal ? min(q.kv, pos + 1) : q.kv;
-      const int lo = valid && p.window > 0 ? max(0, pos - p.window + 1) : 0;
+      const int lo = valid && p.window > 0 ? max(0, kTree ? min(q.kv - q.n, pos - p.window + 1) : pos - p.window + 1) : 0;
       const uint32_t* mask = kTree ? reinterpret_cast<const uint32_t*>(p.masks + (int64_t)(q.r0 + (valid ? tk : 0)) * p.words) : nullptr;
       float m = -INFINITY, l = 0.f;
       int done = 0;

@@ -258,6 +258,34 @@ def test_attend_masks_of_the_callers_own(dtype):
     assert status() == _lib.DFLASH_DEV_BAD_CTX and bool((out[:65] == 7).all()) and not bool((out[65:] == 7).any())
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32", "e4m3"])
+def test_attend_trees_with_positions_of_the_callers_own(kind):
+    """Positions far behind and far before the sequence: the window hides context by them, own rows go by the mask."""
+    from block_diffusion_drafter_forward_gb300 import PagedKV, TreePlan
+    status()
+    for n, ctx in ((2, 200), (40, 200)):
+        if kind == "e4m3":
+            kv, table, lens, starts = cache8([ctx], [n], 1, 128, n)
+            rows = V.rows8(kv.pool, table[0], ctx + n)
+        else:
+            pool, table, lens, starts = cache([ctx], [n], 1, 128, BF if kind == "bf16" else F32, n)
+            kv, rows = PagedKV(pool), R.rows_of(pool, table[0], ctx + n)
+        pos = [(5, ctx + 3, ctx + 70, ctx + 100000, 2 ** 31 - 1, -7)[i % 6] for i in range(n)]
+        see = [[(i * 7 + j) % 3 > 0 for j in range(n)] for i in range(n)]
+        plan = TreePlan(i32(pos), torch.tensor(V.words(see, 1), dtype=torch.int64, device="cuda"))
+        q = torch.randn(n, 8, 128, device="cuda").to(F32 if kind == "f32" else BF)
+        out, lse = kv.attend(q, table, i32(lens), i32(starts), n, window=64, tree=plan, lse=torch.empty(n, 8, device="cuda"))
+        K, Vv = (x.cuda().repeat_interleave(8, 1) for x in rows)
+        hide = torch.tensor([[max(ctx, p) - j >= 64 for j in range(ctx)] + [not x for x in see[i]] for i, p in enumerate(pos)], device="cuda")
+        sc = torch.einsum("ihd,jhd->hij", q.double(), K) / math.sqrt(128)
+        dots = torch.einsum("ihd,jhd->hij", q.double().abs(), K.abs()).amax(2).t() / math.sqrt(128)
+        sc = sc.masked_fill(hide, -math.inf)
+        l = torch.logsumexp(sc, 2)
+        p = torch.exp(sc - torch.where(l > -math.inf, l, 0.0)[..., None])
+        check_attend(out, lse, (torch.einsum("hij,jhd->ihd", p, Vv), l.t(), torch.einsum("hij,jhd->ihd", p, Vv.abs()), dots), slice(0, n), 128)
+    assert status() == 0
+
+
 def test_attend_trees_refuses():
     from block_diffusion_drafter_forward_gb300 import DflashError, PagedKV, QuantKV, TreePlan
     kv = PagedKV(torch.zeros(2, 1, 2, PAGE * 64, device="cuda"))

@@ -63,6 +63,13 @@ def test_pages_in_8_bits_are_checked(lib, kw, code):
     assert lib.dflash_attend_workspace(k) == code
 
 
+def test_attend_over_8_bits_without_the_queries_type(lib):
+    import test_serve
+    assert lib.dflash_attend(ctypes.byref(pages8()), *test_serve.attend_args(n_rows=0)) == 0
+    assert lib.dflash_attend(ctypes.byref(pages8()), *test_serve.attend_args(q=None)) == -1
+    assert lib.dflash_attend(ctypes.byref(pages8()), *test_serve.attend_args(q_stride=1028)) == -1
+
+
 def test_calls_for_other_pages_refuse_those_in_8_bits(lib):
     k = ctypes.byref(pages8())
     assert lib.dflash_append_kv(k, 4096, 256, 4096, 256, 4096, 1, None) == -1
