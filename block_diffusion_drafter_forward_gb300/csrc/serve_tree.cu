@@ -92,8 +92,9 @@ struct KeepParams {
 // of them the path fills) at a time: all loads of a half page ahead of its stores.  Since the path rises, row i of it
 // is read at or behind i, and no row is written before it has been read; a lane reads and writes the same dims,
 // so that its own program order is enough.  V of a whole half page is stored eight rows of a dim at once:
-// row by row every element is a sector of its own (256 trees, 8 heads of 128: 18.5 us, row by row 25).  Bound by
-// latency (a half page is one round trip; one tree 5.5 us) and by V's gathered elements.
+// row by row every element is a sector of its own (256 trees, 8 heads of 128: 18.1 us, row by row 25).  Bound by
+// latency (a half page is one round trip; one tree 4.7 us) and by V's gathered elements.  (K and halves of V in warps
+// of their own: one tree 4.3 us, but 256 trees 22.8.)
 template <int ES>  // bytes of an element: 4, 2, or 1 (codes, with their exponents)
 __global__ void __launch_bounds__(128) keep_kernel(const KeepParams p) {
   using V = typename std::conditional<ES == 4, uint32_t, typename std::conditional<ES == 2, uint16_t, uint8_t>::type>::type;
@@ -122,15 +123,14 @@ __global__ void __launch_bounds__(128) keep_kernel(const KeepParams p) {
   }
   const int32_t* table = p.page_tables + (int64_t)s * p.mpps;
   const int hd = p.hd, pieces = hd * ES / 16;  // K of a row: pieces of 16 bytes, at most 32
-  for (int b0 = ctx & ~7; b0 < ctx + n; b0 += 8) {
-    // lane l < 8: the row that goes to b0 + l
-    const int i = b0 + lane - ctx;
-    const bool row = lane < 8 && i >= 0 && i < n;
+  for (int b1 = ctx & ~7; b1 < ctx + n; b1 += 32) {
+    // lane l: the row that goes to b1 + l (four half pages' places are looked up at once: 5.0 -> 4.7 us for a tree)
+    const int i = b1 + lane - ctx;
     uint8_t *from = nullptr, *to = nullptr;
     int jf = 0;
     bool there = false, move = false;
-    if (row) {
-      const int a = ctx + path[i], b = b0 + lane;
+    if (i >= 0 && i < n) {
+      const int a = ctx + path[i], b = b1 + lane;
       const int pa = table[a / kPage], pb = table[b / kPage];
       there = pa >= 0 && pa < p.num_pages && pb >= 0 && pb < p.num_pages;
       move = there && a != b;
@@ -141,60 +141,64 @@ __global__ void __launch_bounds__(128) keep_kernel(const KeepParams p) {
       }
       jf = a % kPage;
     }
-    const unsigned moving = __ballot_sync(0xffffffffu, move);
-    if (!moving) continue;
-    const bool whole = __ballot_sync(0xffffffffu, there) == 0xffu;  // (rows that stay are then stored as they were)
-    const unsigned take = whole ? 0xffu : moving;
-    uint8_t* dst = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), __ffs(moving) - 1));
-    const int j0 = b0 % kPage;
-    uint4 k[8];
-    V v[8][4];
-    uint8_t e[8];
+    const unsigned movers = __ballot_sync(0xffffffffu, move), placed = __ballot_sync(0xffffffffu, there);
+#pragma unroll 1
+    for (int g = 0; g < 32; g += 8) {
+      const unsigned moving = movers >> g & 0xff;
+      if (!moving) continue;
+      const bool whole = (placed >> g & 0xff) == 0xffu;  // (rows that stay are then stored as they were)
+      const unsigned take = whole ? 0xffu : moving;
+      uint8_t* dst = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), g + __ffs(moving) - 1));
+      const int j0 = (b1 + g) % kPage;
+      uint4 k[8];
+      V v[8][4];
+      uint8_t e[8];
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const uint8_t* f = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(from), r));
-      const int j = __shfl_sync(0xffffffffu, jf, r);
-      if (!(take >> r & 1)) continue;
-      if (lane < pieces)
-        k[r] = *reinterpret_cast<const uint4*>(f + (ES == 1 ? k8_in_tile(j, lane * 16) : k_in_tile(j, lane * (16 / ES), hd) * ES));
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int d = lane + 32 * x;
-        if (d < hd) v[r][x] = reinterpret_cast<const V*>(f + 16 * hd * ES)[ES == 1 ? v8_in_tile(j, d) : v_in_tile(j, d, hd)];
-      }
-      if (ES == 1 && lane < 2) e[r] = f[32 * hd + 16 * lane + j];
-    }
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      if (!(take >> r & 1)) continue;
-      const int j = j0 + r;
-      if (lane < pieces)
-        *reinterpret_cast<uint4*>(dst + (ES == 1 ? k8_in_tile(j, lane * 16) : k_in_tile(j, lane * (16 / ES), hd) * ES)) = k[r];
-      if (!whole) {
+      for (int r = 0; r < 8; ++r) {
+        const uint8_t* f = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(from), g + r));
+        const int j = __shfl_sync(0xffffffffu, jf, g + r);
+        if (!(take >> r & 1)) continue;
+        if (lane < pieces)
+          k[r] = *reinterpret_cast<const uint4*>(f + (ES == 1 ? k8_in_tile(j, lane * 16) : k_in_tile(j, lane * (16 / ES), hd) * ES));
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const int d = lane + 32 * x;
-          if (d < hd) reinterpret_cast<V*>(dst + 16 * hd * ES)[ES == 1 ? v8_in_tile(j, d) : v_in_tile(j, d, hd)] = v[r][x];
+          if (d < hd) v[r][x] = reinterpret_cast<const V*>(f + 16 * hd * ES)[ES == 1 ? v8_in_tile(j, d) : v_in_tile(j, d, hd)];
         }
+        if (ES == 1 && lane < 2) e[r] = f[32 * hd + 16 * lane + j];
       }
-      if (ES == 1 && lane < 2) dst[32 * hd + 16 * lane + j] = e[r];
-    }
-    if (whole) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int d = lane + 32 * x;
-        if (d >= hd) continue;
-        if (ES == 1) {
+      for (int r = 0; r < 8; ++r) {
+        if (!(take >> r & 1)) continue;
+        const int j = j0 + r;
+        if (lane < pieces)
+          *reinterpret_cast<uint4*>(dst + (ES == 1 ? k8_in_tile(j, lane * 16) : k_in_tile(j, lane * (16 / ES), hd) * ES)) = k[r];
+        if (!whole) {
 #pragma unroll
-          for (int z = 0; z < 8; z += 4)
-            *reinterpret_cast<uint32_t*>(dst + 16 * hd + v8_in_tile(j0 + z, d)) = v[z][x] | (uint32_t)v[z + 1][x] << 8 | (uint32_t)v[z + 2][x] << 16 | (uint32_t)v[z + 3][x] << 24;
-        } else {
-          uint4* out = reinterpret_cast<uint4*>(dst + (16 * hd + v_in_tile(j0, d, hd)) * ES);
-          if (ES == 2) {
-            out[0] = make_uint4(v[0][x] | (uint32_t)v[1][x] << 16, v[2][x] | (uint32_t)v[3][x] << 16, v[4][x] | (uint32_t)v[5][x] << 16, v[6][x] | (uint32_t)v[7][x] << 16);
+          for (int x = 0; x < 4; ++x) {
+            const int d = lane + 32 * x;
+            if (d < hd) reinterpret_cast<V*>(dst + 16 * hd * ES)[ES == 1 ? v8_in_tile(j, d) : v_in_tile(j, d, hd)] = v[r][x];
+          }
+        }
+        if (ES == 1 && lane < 2) dst[32 * hd + 16 * lane + j] = e[r];
+      }
+      if (whole) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int d = lane + 32 * x;
+          if (d >= hd) continue;
+          if (ES == 1) {
+#pragma unroll
+            for (int z = 0; z < 8; z += 4)
+              *reinterpret_cast<uint32_t*>(dst + 16 * hd + v8_in_tile(j0 + z, d)) = v[z][x] | (uint32_t)v[z + 1][x] << 8 | (uint32_t)v[z + 2][x] << 16 | (uint32_t)v[z + 3][x] << 24;
           } else {
-            out[0] = make_uint4(v[0][x], v[1][x], v[2][x], v[3][x]);
-            out[1] = make_uint4(v[4][x], v[5][x], v[6][x], v[7][x]);
+            uint4* out = reinterpret_cast<uint4*>(dst + (16 * hd + v_in_tile(j0, d, hd)) * ES);
+            if (ES == 2) {
+              out[0] = make_uint4(v[0][x] | (uint32_t)v[1][x] << 16, v[2][x] | (uint32_t)v[3][x] << 16, v[4][x] | (uint32_t)v[5][x] << 16, v[6][x] | (uint32_t)v[7][x] << 16);
+            } else {
+              out[0] = make_uint4(v[0][x], v[1][x], v[2][x], v[3][x]);
+              out[1] = make_uint4(v[4][x], v[5][x], v[6][x], v[7][x]);
+            }
           }
         }
       }
