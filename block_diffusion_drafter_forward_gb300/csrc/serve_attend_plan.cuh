@@ -4,6 +4,12 @@
 // one-CTA-per-SM grid takes slots [b W / n, (b + 1) W / n) of it, sized on the device from the
 // lengths.  G: a form's geometry - keys of a chunk, slots a unit occupies beside its chunks (the cost of
 // opening a segment: queries, pipeline restart, output), threads of a CTA.
+//
+// Trees in units of two tiles: a chunk takes a CTA 2.3 us, or 1.55 where the unit's second tile has no token (33 to 48
+// nodes of 8 heads to a K/V head have one such unit of two), so that chunks occupy three slots or two, and belong to
+// the CTA that has their first: 32 trees of 33 nodes 155 -> 137 us, of 48 158 -> 145, of 64 (all two tiles) 161 as
+// before.  (Slots of 5 and 3: 163 for trees of mixed sizes, of 4 and 3 152, of 3 and 2 154.  Without trees a chunk is
+// one slot: a cut elsewhere would round results differently from before.)
 #pragma once
 
 #include "serve_attend.cuh"
@@ -39,6 +45,25 @@ __device__ __forceinline__ int unit_chunks(const AttendParams& p, const Shape& h
   return max(1, (end - lo + G::kKeys - 1) / G::kKeys);  // a unit without keys still writes its zeros
 }
 
+// Slots of a chunk of a unit, and of a unit beside its chunks.
+constexpr int kTwo = 3, kOne = 2;
+template <bool kTree>
+__device__ __forceinline__ int chunk_slots(const Shape& h, int n, int tile) {
+  return !kTree || h.TT == h.T ? 1 : tile * h.TT + h.T < n ? kTwo : kOne;
+}
+template <class G, bool kTree>
+__device__ __forceinline__ int cost_slots(const Shape& h) { return G::kUnitCost * (!kTree || h.TT == h.T ? 1 : kTwo); }
+template <class G, bool kTree>
+__device__ __forceinline__ int unit_slots(const AttendParams& p, const Shape& h, int n, int kv, int tile) {
+  int k0;
+  return unit_chunks<G, kTree>(p, h, n, kv, tile, &k0) * chunk_slots<kTree>(h, n, tile) + cost_slots<G, kTree>(h);
+}
+// CTAs that the W slots are cut for: each has the first slot of a chunk wherever a unit goes on on both its sides.
+template <bool kTree>
+__device__ __forceinline__ int ctas_of(const Shape& h, long long W) {
+  return (int)min((long long)gridDim.x, !kTree || h.TT == h.T ? W : W / kTwo);
+}
+
 // The segments of index range [lo, hi), from unit (s, tile, g) whose first slot is pu.
 template <class G, bool kTree>
 struct Walk {
@@ -55,15 +80,18 @@ struct Walk {
       }
       q.nch = unit_chunks<G, kTree>(p, h, q.n, q.kv, tile, &q.k0);
       q.s = s, q.tile = tile, q.g = g, q.t0 = tile * h.TT;
-      const long long first = pu + G::kUnitCost;
-      pu = first + q.nch;
+      const int w = chunk_slots<kTree>(h, q.n, tile);
+      const long long first = pu + cost_slots<G, kTree>(h);
+      pu = first + (long long)q.nch * w;
       if (++g == p.nkv) {
         g = 0;
         if (++tile * h.TT >= q.n) tile = 0, ++s;
       }
       if (hi <= first || lo >= pu) continue;  // only cost slots of it are in range
-      q.c_lo = (int)(lo > first ? lo - first : 0);
-      q.c_hi = (int)(hi < pu ? hi - first : q.nch);
+      auto chunks = [&](int slots) { return w == 1 ? slots : w == kOne ? (slots + kOne - 1) / kOne : (slots + kTwo - 1) / kTwo; };
+      q.c_lo = lo > first ? chunks((int)(lo - first)) : 0;
+      q.c_hi = hi < pu ? chunks((int)(hi - first)) : q.nch;
+      if (kTree && q.c_lo >= q.c_hi) continue;  // only later slots of a chunk
       return true;
     }
     return false;
@@ -80,8 +108,7 @@ struct PlanCtl {
 template <class G, bool kTree>
 __device__ __forceinline__ long long tile_slots(const AttendParams& p, const Shape& h, int n, int kv, int a, int b, int step) {
   long long r = 0;
-  int k0;
-  for (int t = a; t < b; t += step) r += unit_chunks<G, kTree>(p, h, n, kv, t, &k0) + G::kUnitCost;
+  for (int t = a; t < b; t += step) r += unit_slots<G, kTree>(p, h, n, kv, t);
   return r;
 }
 
@@ -92,7 +119,7 @@ __device__ Walk<G, kTree> make(const AttendParams& p, const Shape& h, PlanCtl<G>
   if (p.nb <= 32 && !wide) {
     // a lane per sequence, every warp for itself: no barrier (a step's first 3.5 us went by in the
     // general form's)
-    int r0, n = 0, kv = 0, k0;
+    int r0, n = 0, kv = 0;
     bool bad = false;
     const bool has = lane < p.nb && seq_of<kTree>(p, lane, &r0, &n, &kv, &bad);
     if (bad && blockIdx.x == 0 && warp == 0 && p.status) atomicOr(p.status, DFLASH_DEV_BAD_CTX);
@@ -105,7 +132,7 @@ __device__ Walk<G, kTree> make(const AttendParams& p, const Shape& h, PlanCtl<G>
       if (lane >= o) inc += x;
     }
     const long long W = __shfl_sync(0xffffffffu, inc, 31);
-    const int ctas = (int)min((long long)gridDim.x, W), b = blockIdx.x;
+    const int ctas = ctas_of<kTree>(h, W), b = blockIdx.x;
     Walk<G, kTree> w;
     w.lo = b < ctas ? (long long)b * W / ctas : 0;
     w.hi = b < ctas ? (long long)(b + 1) * W / ctas : 0;
@@ -117,7 +144,7 @@ __device__ Walk<G, kTree> make(const AttendParams& p, const Shape& h, PlanCtl<G>
     const int n0 = __shfl_sync(0xffffffffu, n, s0), kv0 = __shfl_sync(0xffffffffu, kv, s0);
     w.s = s0;
     for (;;) {  // its tile: at most a few
-      const int slots = unit_chunks<G, kTree>(p, h, n0, kv0, w.tile, &k0) + G::kUnitCost;
+      const int slots = unit_slots<G, kTree>(p, h, n0, kv0, w.tile);
       if (w.lo < at + (long long)slots * p.nkv) {
         w.g = (int)((w.lo - at) / slots);
         w.pu = at + (long long)w.g * slots;
@@ -169,7 +196,7 @@ __device__ Walk<G, kTree> make(const AttendParams& p, const Shape& h, PlanCtl<G>
   long long mine = 0, W;
   for (int s = s_lo; s < s_hi; ++s) mine += scratch[s];
   long long at = scan(mine, &W);
-  const int ctas = (int)min((long long)gridDim.x, W), b = blockIdx.x;
+  const int ctas = ctas_of<kTree>(h, W), b = blockIdx.x;
   Walk<G, kTree> w;
   w.lo = b < ctas ? (long long)b * W / ctas : 0;
   w.hi = b < ctas ? (long long)(b + 1) * W / ctas : 0;
@@ -188,13 +215,13 @@ __device__ Walk<G, kTree> make(const AttendParams& p, const Shape& h, PlanCtl<G>
   __syncthreads();
   const int s0 = c.s0;
   long long base = c.base;
-  int r0, n, kv, k0;
+  int r0, n, kv;
   bool bad;
   seq_of<kTree>(p, s0, &r0, &n, &kv, &bad);
   const int tiles = (n + h.TT - 1) / h.TT;
   for (int b0 = 0; b0 < tiles; b0 += G::kThreads) {  // the tile that holds slot lo
     const int tile = b0 + t;
-    const long long v = tile < tiles ? (long long)(unit_chunks<G, kTree>(p, h, n, kv, tile, &k0) + G::kUnitCost) * p.nkv : 0;
+    const long long v = tile < tiles ? (long long)unit_slots<G, kTree>(p, h, n, kv, tile) * p.nkv : 0;
     long long all;
     const long long x = base + scan(v, &all);
     if (v > 0 && x <= w.lo && w.lo < x + v) c.tile0 = tile, c.base = x, c.found = 1;
@@ -203,7 +230,7 @@ __device__ Walk<G, kTree> make(const AttendParams& p, const Shape& h, PlanCtl<G>
     if (c.found) break;
   }
   w.s = s0, w.tile = c.tile0;
-  const int slots = unit_chunks<G, kTree>(p, h, n, kv, w.tile, &k0) + G::kUnitCost;
+  const int slots = unit_slots<G, kTree>(p, h, n, kv, w.tile);
   w.g = (int)((w.lo - c.base) / slots);
   w.pu = c.base + (long long)w.g * slots;
   return w;

@@ -441,6 +441,11 @@ __global__ void __launch_bounds__(Geo<kQuant>::kThreads, 1) attend_tc_kernel(con
   tc_fence_after();
   const uint32_t tmem = c.tmem_slot;
   pdl_trigger();
+  // A unit that starts here and goes on in the next CTAs; end: behind the first slot of its last chunk.
+  auto goes_on = [&](const Seg& q, long long end) {
+    const int G = plan::ctas_of<kTree>(h, W), last = (int)((end * G + W - 1) / W) - 1;
+    wk.meta[blockIdx.x] = make_int4(last - (int)blockIdx.x + 1, q.r0 + q.t0, min(h.TT, q.n - q.t0), q.g);
+  };
   // Queries of a segment into tile b (its second query tile's: two tiles, b = 1) by TMA: rows of 64
   // dims in the 128-byte swizzle, (head, token) in the tile's row order.  One thread.  (Copied by the
   // softmax threads, 16 bytes each, they queued for thousands of cycles behind the pages.)
@@ -595,6 +600,8 @@ __global__ void __launch_bounds__(Geo<kQuant>::kThreads, 1) attend_tc_kernel(con
         };
         while (w.next(p, h, q)) {
           const int n = q.c_hi - q.c_lo;
+          // (here, where the walk is at hand: what the softmax warps keep beside their loop costs 3 % of a tree's time)
+          if (kTree && x == 0 && q.c_lo == 0 && q.c_hi < q.nch) goes_on(q, w.pu - plan::chunk_slots<kTree>(h, q.n, q.tile) + 1);
           if (!It<NT, Walk>::active(h, q, x)) {
             // no row of this stream: it still follows every slot, so that its waits stay exact
             for (int j = 0; j < n; ++j, ++kc) {
@@ -928,11 +935,8 @@ __global__ void __launch_bounds__(Geo<kQuant>::kThreads, 1) attend_tc_kernel(con
             p.lse[gr * p.nh + gh] = lse_of(m, l);
         }
       }
-      if (t == 0 && q.c_lo == 0 && !whole) {  // the unit starts here and goes on in the next CTAs
-        const long long end = walk.hi - (q.c_hi - 1) + q.nch - 1;  // past its last slot: slot hi - 1 is chunk c_hi - 1
-        const int G = (int)min((long long)gridDim.x, W);
-        const int last = (int)((end * G + W - 1) / W) - 1;
-        wk.meta[blockIdx.x] = make_int4(last - (int)blockIdx.x + 1, q.r0 + q.t0, min(h.TT, q.n - q.t0), q.g);
+      if (!(kTree && NT == 2) && t == 0 && q.c_lo == 0 && !whole) {
+        goes_on(q, walk.hi + q.nch - q.c_hi);  // (slot hi - 1: chunk c_hi - 1)
       }
       tc_fence_before();
       mbar_arrive(&c.o_free[NT == 2 ? x : 0]);

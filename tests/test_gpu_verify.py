@@ -505,6 +505,28 @@ ATTEND8 = [
 ]
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("trees", [24, 40])
+def test_attend_many_trees(trees, kind):
+    """Units of one and of two tiles, cut anywhere: trees of 1 to 100 nodes on contexts of up to 3000 rows."""
+    from block_diffusion_drafter_forward_gb300 import PagedKV
+    status()
+    r = random.Random(trees)
+    new = [r.choice([1, 16, 17, 32, 33, 47, 48, 49, 64, 100]) for _ in range(trees)]
+    ctx = [r.randint(0, 3000) for _ in range(trees)]
+    if kind == "e4m3":
+        kv, table, lens, starts = cache8(ctx, new, 3, 128, trees)
+        rows = lambda s, m: V.rows8(kv.pool, table[s], m)
+    else:
+        pool, table, lens, starts = cache(ctx, new, 3, 128, BF, trees)
+        kv, rows = PagedKV(pool), V.rows16(pool, table)
+    parents, plan = plan_of(new, lens, starts, trees)
+    q = (torch.randn(starts[-1], 24, 128, generator=torch.Generator(device="cuda").manual_seed(trees), device="cuda") * 1.5).to(BF)
+    out, lse = kv.attend(q, table, i32(lens), i32(starts), 100, tree=plan, lse=torch.empty(starts[-1], 24, device="cuda"))
+    check_attend(out, lse, V.attend(q, rows, lens, starts, 1 / math.sqrt(128), parents=parents), slice(0, starts[-1]), 128)
+    assert status() == 0
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("case", range(len(ATTEND8)))
 def test_attend_in_8_bits(case, dtype):
