@@ -20,7 +20,10 @@
 // that rounding), and O is kept in units of 2^(r + 30), r the largest exponent ve of the pages so far, or up to
 // 20 below it.
 //
-// Measured (GB300; 16 tokens on 16-32 Ki rows, 64 heads on 8): 151 us, 5.3 TB/s, of which copies alone take 135; a further
+// Codes of NaN: K's conversion keeps them and a row's scores tell; V's moved bits do not, so that the largest are kept
+// and looked at (147 us without).
+//
+// Measured (GB300; 16 tokens on 16-32 Ki rows, 64 heads on 8): 152 us, 5.3 TB/s, of which copies alone take 135; a further
 // 128 keys of every CTA take 0.84 us, 88 % of the copy rate, and 13 us are start, split and merge.  K in bf16 as V: 163 us.
 // K in e4m3 products with Q as two e4m3 parts: 204 us.  7 warps: 163 us; two pages a step: 152 us.  One token on 4096 rows
 // 11.9 us: latency.  What bounds it is issue (1.8 instructions a cycle of 4, the ALU pipe at half its rate) beside HBM.
@@ -55,24 +58,15 @@ struct Cfg {
   static constexpr int kMerge = kW * 16 * 32 * 4;                  // 32 dims of every warp's O
 };
 
-template <int HD>
+template <int HD, bool kTree>
 struct Ctl {
   uint64_t full[kW][Cfg<HD>::kStages], empty[kW][Cfg<HD>::kStages];
-  int flags[2];
+  int flags[2];  // a wait gave up; a NaN was met in V
+  Walk<kTree> walk;
   PlanCtl<Geo> plan;
   float2 ml[kW][16];
 };
 
-// codes 0, 1 and 2, 3 of a word as pairs of bf16, times 2^-120
-__device__ __forceinline__ void widen(uint32_t w, uint32_t& a, uint32_t& b) {
-  // each byte with its sign in the byte above, moved up by 4: the sign, four zeros, exponent and mantissa
-  asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(a) : "r"(w));
-  asm("prmt.b32 %0, %1, 0, 0xb3a2;" : "=r"(b) : "r"(w));
-  asm("mad.lo.u32 %0, %0, 16, 0;" : "+r"(a));  // (a shift, off the pipe of the permutes)
-  asm("mad.lo.u32 %0, %0, 16, 0;" : "+r"(b));
-  a &= 0x87f087f0u;
-  b &= 0x87f087f0u;
-}
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -102,13 +96,33 @@ __device__ __forceinline__ float quad_max(float x) {
   return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
 }
 
+// NaN in V, which the scores do not show, given to the rows that see one, for all of a CTA's segments when they are done.  The
+// 11 warps (eight of them have something to do); a thread has the row and dims that it wrote.
+template <int HD, bool kTree>
+__device__ __noinline__ void spread_nan8(const AttendParams& p, const AttendWork& wk, Walk<kTree> w) {
+  const int t = threadIdx.x, row = t >> 4, x = (t & 15) * 2;
+  if (row >= 16) return;
+  Shape h;
+  h.group = p.group, h.T = h.TT = p.tokens;
+  const int tok = row * p.inv >> 16, head = row - tok * h.group;
+  Seg q;
+  while (w.next(p, h, q)) {
+    const int token = q.t0 + tok;
+    const bool whole = q.c_lo == 0 && q.c_hi == q.nch;
+    plan::spread_nan<HD, kTree>(
+        p, q, q.k0 + q.c_lo * Geo::kKeys, min(q.kv, q.k0 + q.c_hi * Geo::kKeys), tok < h.T && token < q.n ? token : -1, x, 2, 32,
+        whole ? static_cast<__nv_bfloat16*>(p.out) + (int64_t)(q.r0 + token) * p.out_stride + (int64_t)(q.g * h.group + head) * HD : nullptr,
+        part_row(wk, 2 * blockIdx.x + (q.c_lo == 0 ? 1 : 0), row, 128, HD), nullptr, nullptr);
+  }
+}
+
 template <int HD, bool kTree>
 __global__ void __launch_bounds__(Geo::kThreads, 1) attend8_kernel(const AttendParams p, const AttendWork wk) {
   using C = Cfg<HD>;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* ring = smem;
   float* merge = reinterpret_cast<float*>(smem + C::kRing);  // [warp][16][32]
-  Ctl<HD>& c = *reinterpret_cast<Ctl<HD>*>(smem + C::kRing + C::kMerge);
+  Ctl<HD, kTree>& c = *reinterpret_cast<Ctl<HD, kTree>*>(smem + C::kRing + C::kMerge);
   volatile int* flags = c.flags;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   Shape h;
@@ -127,7 +141,7 @@ __global__ void __launch_bounds__(Geo::kThreads, 1) attend8_kernel(const AttendP
     }
     fence_barrier_init();
   }
-  if (t == 0) flags[0] = 0;
+  if (t == 0) flags[0] = flags[1] = 0, c.walk = walk;
   fence_proxy_async_smem();  // the plan's scratch is overwritten by copies
   __syncthreads();
 
@@ -221,6 +235,7 @@ __global__ void __launch_bounds__(Geo::kThreads, 1) attend8_kernel(const AttendP
 #pragma unroll
     for (int d = 0; d < HD / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
     int ref = -1000;  // r of the comment above; none yet
+    uint32_t met = 0;  // V's largest magnitudes
 
     const int pages = (q.kv + kPage - 1) / kPage, end = min(pages, q.k0 / kPage + q.c_hi * kW);
     for (int lp = q.k0 / kPage + q.c_lo * kW + warp; lp < end; lp += kW, ++i) {
@@ -337,9 +352,8 @@ __global__ void __launch_bounds__(Geo::kThreads, 1) attend8_kernel(const AttendP
         const uint4 v = *reinterpret_cast<const uint4*>(tile + 16 * HD + d * 512 + r * 64 + ((j ^ (r >> 1)) * 16));
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
-          uint32_t b0, b1;
-          widen((&v.x)[z], b0, b1);
-          mma_bf16w(o[4 * d + z], pa, b0, b1);
+          const uint2 w = plan::widen((&v.x)[z], met);
+          mma_bf16w(o[4 * d + z], pa, w.x, w.y);
         }
       }
       __syncwarp();
@@ -347,6 +361,7 @@ __global__ void __launch_bounds__(Geo::kThreads, 1) attend8_kernel(const AttendP
     }
 
     // ---- the warps' states meet: M, L of every row, then O by 32 dims at a time
+    if (plan::is_nan(met)) flags[1] = 1;
     const bool whole = q.c_lo == 0 && q.c_hi == q.nch;
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
@@ -410,12 +425,14 @@ __global__ void __launch_bounds__(Geo::kThreads, 1) attend8_kernel(const AttendP
       wk.meta[blockIdx.x] = make_int4(last - (int)blockIdx.x + 1, q.r0 + q.t0, min(h.TT, q.n - q.t0), q.g);
     }
   }
+  named_barrier(1, 32 * kW);
+  if (flags[1] && !flags[0]) spread_nan8<HD, kTree>(AttendParams(p), AttendWork(wk), c.walk);
   if (t == 0 && flags[0] && p.status) atomicOr(p.status, DFLASH_DEV_TIMEOUT);
 }
 
 template <int HD, bool kTree>
 cudaError_t launch(const AttendParams& p, const AttendWork& w, int sms, cudaStream_t st) {
-  constexpr int kSmem = Cfg<HD>::kRing + Cfg<HD>::kMerge + (int)sizeof(Ctl<HD>);
+  constexpr int kSmem = Cfg<HD>::kRing + Cfg<HD>::kMerge + (int)sizeof(Ctl<HD, kTree>);
   static_assert(kSmem <= 232448, "shared memory of a CTA");
   static_assert(Cfg<HD>::kRing >= 16384 * 8, "the plan's scratch");
   static std::atomic<unsigned long long> attr{0};

@@ -12,6 +12,8 @@
 // one slot: a cut elsewhere would round results differently from before.)
 #pragma once
 
+#include <cuda_bf16.h>
+
 #include "serve_attend.cuh"
 
 namespace dflash {
@@ -245,6 +247,72 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t* mask, int n, int k
   if (lo > key) m = lo - key >= 32 ? 0u : m & 0xffffffffu << (lo - key);
   if (kv < key + 32) m = kv <= key ? 0u : m & 0xffffffffu >> (key + 32 - kv);
   return m;
+}
+
+// ---- Pages in 8 bits.
+
+// Codes 0, 1 and 2, 3 of a word as pairs of bf16, times 2^-120: sign, exponent and mantissa << 4.  NaN (seven ones) becomes
+// 480, which no number's code does: `met` keeps the largest magnitudes, by one instruction a pair beside the
+// permutes' pipe, for is_nan() and spread_nan() below.  (By sums and masks of the codes: 158 us for 152, see serve_attend8.cu.)
+__device__ __forceinline__ uint2 widen(uint32_t w, uint32_t& met) {
+  uint32_t a, b;  // each byte with its sign in the byte above, moved up by 4
+  asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(a) : "r"(w));
+  asm("prmt.b32 %0, %1, 0, 0xb3a2;" : "=r"(b) : "r"(w));
+  asm("mad.lo.u32 %0, %0, 16, 0;" : "+r"(a));  // (a shift, off the pipe of the permutes)
+  asm("mad.lo.u32 %0, %0, 16, 0;" : "+r"(b));
+  a &= 0x87f087f0u, b &= 0x87f087f0u;
+  asm("max.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(met) : "r"(a));
+  asm("max.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(met) : "r"(b));
+  return make_uint2(a, b);
+}
+__device__ __forceinline__ bool is_nan(uint32_t met) { return (met & 0x7fffu) == 0x7f0u || (met >> 16 & 0x7fffu) == 0x7f0u; }
+
+// Is one of 16 codes NaN's, of either sign?
+__device__ __forceinline__ bool nan_codes(const uint4& w) {
+  auto flip = [](uint32_t x) { return (x + 0x01010101u) ^ x; };  // bit 7 of a byte changes where the seven below are ones
+  return (flip(w.x) | flip(w.y) | flip(w.z) | flip(w.w)) & 0x80808080u;
+}
+
+// Where is_nan() has met one, a warp goes through keys [lo, hi) of its unit once more, and rows that see a NaN get it; the
+// others keep what they have.  A lane has token `tk` of the sequence (-1: none) and of its output the dims [d, d + run) of
+// every `step` from d_lo on, at `out` or, of a part, `part`; lse, or a part's (m, l), or NULL.  Every lane comes to the
+// votes, with a token or not.
+template <int HD, bool kTree>
+__device__ __forceinline__ void spread_nan(const AttendParams& p, const Seg& q, int lo, int hi, int tk, int d_lo, int run, int step,
+                                           __nv_bfloat16* out, float* part, float* lse, float2* ml) {
+  const int lane = threadIdx.x & 31, ctx = q.kv - q.n;
+  const int pos = !kTree ? ctx + tk : tk >= 0 && p.window > 0 ? max(ctx, __ldg(p.positions + q.r0 + tk)) : 0;
+  const int from = p.window > 0 ? max(0, kTree ? min(ctx, pos - p.window + 1) : pos - p.window + 1) : 0;
+  const int to = p.causal ? min(q.kv, pos + 1) : q.kv;
+  const uint32_t* mask = kTree ? reinterpret_cast<const uint32_t*>(p.masks + (int64_t)(q.r0 + max(tk, 0)) * p.words) : nullptr;
+  const int32_t* table = p.page_tables + (int64_t)q.s * p.mpps;
+#pragma unroll 1
+  for (int lp = lo / kPage; lp * kPage < hi; ++lp) {
+    const int id = __ldg(table + lp), page = id < 0 || id >= p.num_pages ? 0 : id;  // (reported by the copy)
+    const uint8_t* tile = static_cast<const uint8_t*>(p.pool) + page * p.page_stride + (int64_t)q.g * (32 * HD + 32);
+    bool any = false;
+#pragma unroll 1
+    for (int u = lane; u < 2 * HD; u += 32) any |= nan_codes(reinterpret_cast<const uint4*>(tile)[u]);
+    if (!__any_sync(0xffffffffu, any)) continue;
+#pragma unroll 1
+    for (int j = 0; tk >= 0 && j < kPage; ++j) {
+      const int key = lp * kPage + j;
+      if (!(kTree ? mask_bits(mask, 2 * p.words, key, from, ctx, q.kv) & 1 : key >= from && key < to)) continue;
+      bool all = false;
+#pragma unroll 1
+      for (int d = 0; d < HD; d += 16) all |= nan_codes(*reinterpret_cast<const uint4*>(tile + k8_in_tile(j, d)));
+#pragma unroll 1
+      for (int a = d_lo; a < HD; a += step)
+#pragma unroll 1
+        for (int d = a; d < a + run; ++d) {
+          if (!all && (tile[16 * HD + v8_in_tile(j, d)] & 127) != 127) continue;
+          if (out) out[d] = __ushort_as_bfloat16(0x7fff); else part[d] = NAN;
+        }
+      if (all && lse) *lse = NAN;
+      if (all && ml) ml->y = NAN;
+    }
+    __syncwarp();
+  }
 }
 
 }  // namespace plan

@@ -32,11 +32,13 @@
 // go to the sequence's end.  32 trees of 33-64 nodes on 0.5-8 Ki rows 155 us (34 % of the tensor pipe: part-full
 // tiles, and a unit of 33-48 nodes has one stream at work); one of 32 nodes on 4096 rows 19 us, latency.
 //
-// Pages in 8 bits (kQuant): see below.  32 blocks of 16 as above 86 us, a prompt of 8192 575 us.  With one tile a chunk
+// Pages in 8 bits (kQuant): see below.  32 blocks of 16 as above 90 us, a prompt of 8192 599 us; 86 and 580 without the
+// search for NaN in the widened values, as which the following was measured.  With one tile a chunk
 // takes a CTA 1.87 us; without the widening 1.35, without its stores 1.51, K or V alone 1.6, with one of four
 // softmax warps at work 1.77: the 64 KB that are written to shared memory, beside the 96 KB that the MMAs read of
 // it, and the instruction caches hold it (its loops unrolled: 2.5 us; codes read ahead of the step before: 2.05;
-// two threads a query row in loops of 32 columns: 1.82, but with two tiles 680 us for the prompt).
+// two threads a query row in loops of 32 columns: 1.82, but with two tiles 680 us for the prompt).  The search in a
+// warp of its own beside the widening ones, which then waits for the stages too: 99 and 670 us.
 //
 // Rounding: P is bf16 (the MMA's operand type), sums and O fp32, the normaliser sums the fp32 P.
 // Warp roles: 0-3 stream 0, 4-7 stream 1, 8 K pages, 10 V pages, 9 and 11 MMA issue (8 bits: 8 pages, 10 the next
@@ -103,14 +105,15 @@ struct Cfg {
   static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
 
-template <class C, class G>
+template <class C, class G, class Walk>
 struct Ctl {
   uint64_t k_full[C::kNK], k_empty[C::kNK], v_full[C::kNV], v_empty[C::kNV], v_raw[C::kNV];
   uint64_t st_full[C::kNS], st_empty[C::kNS];
   int2 half[C::kNS];  // pages of the half, rows of the sequence from its first on
   uint64_t s_full[2], p_half[2], p_full[2], o_done[2], o_free[2], q_full[2], q_empty;
   uint32_t tmem_slot;
-  int flags[2];
+  int flags[2];  // a wait gave up; a NaN was met in pages of 8 bits
+  Walk walk;     // (8 bits: this CTA's, for those)
   PlanCtl<G> plan;
   float2 ml[2][128];  // one tile: the streams' (m, l) of every row
 };
@@ -272,15 +275,6 @@ __device__ __forceinline__ void load_codes(const AttendParams& p, const Shape& h
   }
 }
 
-// Codes 0, 1 and 2, 3 of a word as pairs of bf16, times 2^-120: sign, exponent and mantissa << 4.
-__device__ __forceinline__ uint2 widen(uint32_t w) {
-  uint32_t a, b;  // each byte with its sign in the byte above, moved up by 4
-  asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(a) : "r"(w));
-  asm("prmt.b32 %0, %1, 0, 0xb3a2;" : "=r"(b) : "r"(w));
-  asm("mad.lo.u32 %0, %0, 16, 0;" : "+r"(a));  // (a shift, off the pipe of the permutes)
-  asm("mad.lo.u32 %0, %0, 16, 0;" : "+r"(b));
-  return make_uint2(a & 0x87f087f0u, b & 0x87f087f0u);
-}
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
   return a;
@@ -289,15 +283,17 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
 // One warp's pages (pg and pg + 2) of a half, of whose rows `rows` are the sequence's.  K: a lane has dims 16 x .. of row j,
 // for two x at a time.  V: rows 8 r .. of dims 32 g + m + 8 k; rows from `rows` on become zeros (they may hold
 // anything, and zero times NaN would reach O).  Eight lanes write 128 bytes in a row, and read as many from
-// different banks.  A row's factor 2^(e - 127 + 120) is a bf16 number up to e = 134; rows beyond (values from
-// 2^15 on, kFar) go in two steps.  A loop, not unrolled: the roles' code together is more than the instruction
-// caches hold (both pages unrolled: 3.6 us a chunk for 2.3).
-template <int HD, class C, bool kV, bool kFar>
-__device__ __forceinline__ void widen_pages(const uint8_t* half, uint8_t* dst, int pg, int n, int rows, int lane) {
+// different banks.  Two products a pair, by 2^120 and the row's power (their product is a bf16 number for rows below
+// 2^15 alone; a second instance that took one product there was slower by its code: 97 us for 91).  A loop, not unrolled: the
+// roles' code together is more than the instruction caches hold (both pages unrolled: 3.6 us a chunk for 2.3; the two
+// steps of a page: 107 us for 90).  Not 0: one of the sequence's rows has a NaN in dims of this lane's.
+template <int HD, class C, bool kV>
+__device__ __forceinline__ uint32_t widen_pages(const uint8_t* half, uint8_t* dst, int pg, int n, int rows, int lane) {
   const int j = lane & 15, m = lane & 7, r = lane >> 3 & 1, up = lane >> 4;
   const uint8_t* src = half + pg * C::kCodes + (kV ? 16 * HD + up * 512 + m * 64 : j * 64);
   const int u0 = kV ? (2 * r) ^ (m >> 1) : up ^ (j >> 1 & 3);  // the first unit of 16 bytes; the other differs in bit 0 (V), 1 (K)
   const uint8_t* ex = half + pg * C::kCodes + 32 * HD + (kV ? 16 + 8 * r : j);
+  uint32_t nan = 0;
   dst += pg * C::kTile + (kV ? m * 16 + r * 128 + up * 1024 : r * (HD * 16) + m * 16 + up * 256);
   for (; pg < n; pg += 2, src += 2 * C::kCodes, ex += 2 * C::kCodes, dst += 2 * C::kTile) {
     uint32_t e0, e1;
@@ -314,14 +310,11 @@ __device__ __forceinline__ void widen_pages(const uint8_t* half, uint8_t* dst, i
       d1 = live <= 4 ? 0xffffffffu : live >= 8 ? 0u : 0xffffffffu << 8 * (live - 4);
       e0 = (e0 & ~d0) | (0x7f7f7f7fu & d0), e1 = (e1 & ~d1) | (0x7f7f7f7fu & d1);
     }
-    uint32_t f[4], g[4];  // factors of two rows
+    uint32_t f[4];  // powers of two rows
 #pragma unroll
-    for (int k = 0; k < (kV ? 4 : 1); ++k) {
-      const uint32_t z = __byte_perm(k < 2 ? e0 : e1, 0, k & 1 ? 0x4342 : 0x4140);  // their exponent bytes, one to a half
-      f[k] = (kFar ? __vminu2(z + 0x00780078u, 0x00fe00feu) : z + 0x00780078u) << 7;
-      g[k] = kFar ? (__vmaxu2(z, 0x00860086u) - 0x00070007u) << 7 : 0;  // 2^(e - 134), at least 1
-    }
-    auto turn = [&](uint32_t a, int k) { return kFar ? mul2(mul2(a, f[k]), g[k]) : mul2(a, f[k]); };
+    for (int k = 0; k < (kV ? 4 : 1); ++k) f[k] = __byte_perm(k < 2 ? e0 : e1, 0, k & 1 ? 0x4342 : 0x4140) << 7;  // (an exponent byte to a half)
+    uint32_t met = 0;
+    auto turn = [&](uint32_t a, int k) { return mul2(mul2(a, 0x7b807b80u), f[k]); };
 #pragma unroll 1
     for (int e = 0; e < HD / 64; ++e) {
       const uint8_t* s = src + e * 1024;
@@ -333,19 +326,21 @@ __device__ __forceinline__ void widen_pages(const uint8_t* half, uint8_t* dst, i
           hi = make_uint4(hi.x & ~d1, hi.y & ~d1, hi.z & ~d1, hi.w & ~d1);
         }
         auto put = [&](uint32_t a, uint32_t b, int k) {
-          const uint2 x = widen(a), y = widen(b);
+          const uint2 x = plan::widen(a, met), y = plan::widen(b, met);
           *reinterpret_cast<uint4*>(d + k * 256) = make_uint4(turn(x.x, 0), turn(x.y, 1), turn(y.x, 2), turn(y.y, 3));
         };
         put(lo.x, hi.x, 0), put(lo.y, hi.y, 1), put(lo.z, hi.z, 2), put(lo.w, hi.w, 3);
       } else {
         auto put = [&](uint32_t a, uint32_t b, int at) {
-          const uint2 x = widen(a), y = widen(b);
+          const uint2 x = plan::widen(a, met), y = plan::widen(b, met);
           *reinterpret_cast<uint4*>(d + at) = make_uint4(turn(x.x, 0), turn(x.y, 0), turn(y.x, 0), turn(y.y, 0));
         };
         put(lo.x, lo.y, 0), put(lo.z, lo.w, 128), put(hi.x, hi.y, 512), put(hi.z, hi.w, 640);
       }
     }
+    if (kV || pg * kPage + j < rows) nan |= plan::is_nan(met);  // (V behind the end: zeros by now)
   }
+  return nan;
 }
 
 // Warps 12 and 13 (`sub` 0, 1): K of the halves, every second page each; 14 and 15 (2, 3): V.
@@ -363,12 +358,7 @@ __device__ __forceinline__ void widen_codes(const uint8_t* stage, uint8_t* slots
     if (half == 0 && kc >= kN && !warp_wait(&empty[slot], (kc / kN - 1) & 1, flags)) return;
     uint8_t* dst = slots + slot * C::kSlot + half * (kPages / 2) * C::kTile;
     const uint8_t* src = stage + b * C::kHalf;
-    const int pg = sub & 1, mine = pg + (lane >> 4) * 2;  // a lane looks at a row of one of the two pages
-    const bool far = mine < n && src[mine * C::kCodes + 32 * HD + (kV ? 16 : 0) + (lane & 15)] > 134;
-    if (__any_sync(0xffffffffu, far))
-      widen_pages<HD, C, kV, true>(src, dst, pg, n, rows, lane);
-    else
-      widen_pages<HD, C, kV, false>(src, dst, pg, n, rows, lane);
+    if (widen_pages<HD, C, kV>(src, dst, sub & 1, n, rows, lane)) flags[1] = 1;
     if (kV && half == 0 && n == 0 && (sub & 1) == 0) {  // a unit without keys: a page of zeros
       for (int e = lane; e < C::kTile / 16; e += 32) reinterpret_cast<uint4*>(dst)[e] = make_uint4(0, 0, 0, 0);
     }
@@ -381,18 +371,38 @@ __device__ __forceinline__ void widen_codes(const uint8_t* stage, uint8_t* slots
   }
 }
 
+// NaN in K or V, given to the rows that see one, for all of a CTA's segments when they are done (beside each segment's end its
+// code cost the softmax loops: a prompt of 8192 20 us).  The softmax warps; a thread has the row and dims that it wrote.
+template <int HD, int NT, bool kTree, class Walk>
+__device__ __noinline__ void spread_nan_tc(const AttendParams& p, const AttendWork& wk, Walk w) {
+  constexpr int kD = NT == 2 ? HD : HD / 2;
+  const int x = threadIdx.x >> 7, row = threadIdx.x & 127, prow = (NT == 2 ? x * 128 : 0) + row;
+  const Shape h = shape_of(p, NT);
+  const int tok = row / h.group, head = row - tok * h.group;
+  Seg q;
+  while (w.next(p, h, q)) {
+    const int tk = q.t0 + (NT == 2 ? x * h.T : 0) + tok, gh = q.g * h.group + head, slot = 2 * blockIdx.x + (q.c_lo == 0 ? 1 : 0);
+    const int64_t gr = q.r0 + tk;
+    const bool whole = q.c_lo == 0 && q.c_hi == q.nch, first = NT == 2 || x == 0;
+    plan::spread_nan<HD, kTree>(p, q, q.k0 + q.c_lo * kKeys, min(q.kv, q.k0 + q.c_hi * kKeys), tok < h.T && tk < q.n ? tk : -1,
+                                NT == 2 ? 0 : x * kD, kD, HD, whole ? static_cast<__nv_bfloat16*>(p.out) + gr * p.out_stride + (int64_t)gh * HD : nullptr,
+                                part_row(wk, slot, prow, NT * 128, HD), first && whole && p.lse ? p.lse + gr * p.nh + gh : nullptr,
+                                first && !whole ? wk.ml + (int64_t)slot * (NT * 128) + prow : nullptr);
+  }
+}
+
 template <int HD, int NT, bool kTree, bool kQuant>
 __global__ void __launch_bounds__(Geo<kQuant>::kThreads, 1) attend_tc_kernel(const AttendParams p, const AttendWork wk, const __grid_constant__ CUtensorMap q_map) {
   using C = Cfg<HD, NT, kQuant>;
   using Walk = plan::Walk<Geo<kQuant>, kTree>;
   constexpr int kThreads = Geo<kQuant>::kThreads;
-  static_assert(sizeof(Ctl<C, Geo<kQuant>>) <= C::kCtl, "control block overflows its slot");
+  static_assert(sizeof(Ctl<C, Geo<kQuant>, Walk>) <= C::kCtl, "control block overflows its slot");
   extern __shared__ __align__(1024) uint8_t smem[];  // (the queries' swizzle counts from 1 KB boundaries)
   uint8_t* sQ = smem;
   uint8_t* sK = sQ + C::kQTiles * C::kQ;
   uint8_t* sV = sK + C::kNK * C::kSlot;
   uint8_t* sS = sV + C::kNV * C::kSlot;  // 8 bits: halves of chunks
-  auto& c = *reinterpret_cast<Ctl<C, Geo<kQuant>>*>(sS + (kQuant ? C::kNS * C::kHalf : 0));
+  auto& c = *reinterpret_cast<Ctl<C, Geo<kQuant>, Walk>*>(sS + (kQuant ? C::kNS * C::kHalf : 0));
   volatile int* flags = c.flags;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const Shape h = shape_of(p, NT);
@@ -428,7 +438,8 @@ __global__ void __launch_bounds__(Geo<kQuant>::kThreads, 1) attend_tc_kernel(con
       mbar_init(&c.o_free[i], NT == 2 ? 128 : 256);
       mbar_init(&c.q_full[i], 1);
     }
-    flags[0] = 0;
+    flags[0] = flags[1] = 0;
+    if (kQuant) c.walk = walk;
     fence_barrier_init();
   }
   // rows that no query fills stay finite
@@ -953,6 +964,9 @@ __global__ void __launch_bounds__(Geo<kQuant>::kThreads, 1) attend_tc_kernel(con
   tc_fence_before();
   __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, 512);
+  if constexpr (kQuant) {
+    if (warp < 8 && flags[1] && !flags[0]) spread_nan_tc<HD, NT, kTree>(AttendParams(p), AttendWork(wk), c.walk);
+  }
 }
 
 // Merges the partials of the unit that starts in CTA b = blockIdx.x and ends in a later one, in

@@ -481,7 +481,8 @@ int dflash_keep_rows(const dflash_kv_pages* kv, const int32_t* page_tables, int3
  * A row is written with k = e - 127 the smallest integer for which its largest finite |x| <= 448 2^k, kept
  * in [-118, 119], and c = x 2^-k rounded to nearest even (largest magnitude 448).  Infinities and NaN become
  * NaN.  All values 2^k c are bf16 numbers.  Bytes e outside [9, 246] are none that the library writes.
- * dflash_attend over such pages takes bf16 queries (dflash_attend_ex either). */
+ * dflash_attend over such pages takes bf16 queries (dflash_attend_ex either), and a NaN in them reaches the
+ * rows that see its key and no others: all of a row from K, the dim that it stands in from V. */
 
 /* dflash_append_kv into pages of DFLASH_FP8E4M3_ROWEXP: rows of src_dtype (DFLASH_BF16 or DFLASH_F32) are
  * quantised as they are written.  Arguments as there; strides in elements of src_dtype. */

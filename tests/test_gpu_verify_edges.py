@@ -1,0 +1,100 @@
+"""Calls at the edges of trees, kept rows, rotary positions and pages in 8 bits: NaN that a cache holds, sizes past its
+tables, tables of the caller's own."""
+import math
+
+import pytest
+import torch
+
+import verify_ref as V
+from test_gpu_serve import check_attend
+from test_gpu_verify import cache8, i32, plan_of, status
+
+pytestmark = pytest.mark.gpu
+PAGE = 16
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+# ------------------------------------------------------------------------------ NaN in pages of 8 bits
+def sees(lens, starts, causal, window, parents):
+    """[rows, longest] truth values: which keys of its sequence a row sees."""
+    out = torch.zeros(starts[-1], max(lens), dtype=torch.bool)
+    for s, kv in enumerate(lens):
+        n = starts[s + 1] - starts[s]
+        ctx = kv - n
+        own = V.tree(parents[starts[s]:starts[s + 1]]) if parents else None
+        for i in range(n):
+            pos = ctx + (own[0][i] if parents else i)
+            row = out[starts[s] + i]
+            row[:kv] = True
+            if window:
+                row[:max(0, pos - window + 1)] = False
+            if parents:
+                row[ctx:kv] = torch.tensor(own[1][i])
+            elif causal:
+                row[pos + 1:] = False
+    return out
+
+
+NANS = [
+    # ctx, new, nh, nkv, hd, window, causal, trees
+    ([37], [1], 8, 1, 128, 0, True, False), ([3000, 100], [1, 1], 32, 4, 128, 0, True, False), ([500, 90], [2, 2], 16, 2, 64, 40, True, False),
+    ([600, 17], [16, 5], 16, 2, 128, 0, True, False), ([2000, 0], [16, 40], 32, 4, 64, 100, True, False), ([300, 50], [16, 9], 8, 1, 128, 0, False, False),
+    ([700, 200, 0, 40] * 10, [17, 64, 20, 33] * 10, 32, 4, 128, 0, True, False), ([400, 900] * 12, [40, 30] * 12, 16, 4, 64, 64, True, False),
+    ([0], [1500], 16, 2, 128, 0, True, False), ([100, 30], [2, 1], 8, 1, 128, 0, True, True), ([2500, 60], [32, 7], 16, 2, 128, 0, True, True),
+    ([700, 200, 0, 40] * 8, [33, 64, 20, 50] * 8, 32, 4, 128, 128, True, True), ([300] * 24, [40, 17] * 12, 16, 4, 64, 0, True, True),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("case", range(len(NANS)))
+def test_nan_in_8_bits_reaches_the_rows_that_see_it(case, dtype):
+    """NaN in K (the whole row of the output) and in V (its dim), of the context and of rows that others hide: every row that
+    sees one has it, and the others have the numbers that they would have had."""
+    status()
+    ctx, new, nh, nkv, hd, window, causal, trees = NANS[case]
+    kv, table, lens, starts = cache8(ctx, new, nkv, hd, case)
+    parents, plan = plan_of(new, lens, starts, case, max(64, max(new))) if trees else (None, None)
+    n = starts[-1]
+    g = torch.Generator(device="cuda").manual_seed(case)
+    q = torch.randn(n, nh, hd, generator=g, device="cuda").to(dtype)
+    # of every second sequence: in V a context row and three of its last ones, by either sign's code, and in K its last row
+    pool, bad_k, bad_v = kv.pool, {}, {}
+    for s in range(0, len(lens), 2):
+        L = lens[s]
+        at = {j for j in (L * 2 // 3, L - 1, L - new[s] // 2 - 1, L - new[s]) if 0 <= j < L}
+        for x, j in enumerate(sorted(at)):
+            page, h, d = int(table[s, j // PAGE]), (x + s) % nkv, (7 * x + 31 * s + 5) % hd
+            pool[page, h, 16 * hd + V.v8(j % PAGE, d)] = 127 if x % 2 else 255
+            bad_v.setdefault((s, h), []).append((j, d))
+        if s % 4 == 0 and case % 3:
+            j, h = L - 1, (s // 4) % nkv
+            pool[int(table[s, j // PAGE]), h, V.k8(j % PAGE, (3 * s + 11) % hd)] = 255 if s % 8 else 127
+            bad_k.setdefault((s, h), []).append(j)
+    rows = lambda s, m: [x.nan_to_num() for x in V.rows8(pool, table[s], m)]
+    scale = 1 / math.sqrt(hd)
+    out, lse, spread, dots = V.attend(q, rows, lens, starts, scale, causal, window, parents)
+    see = sees(lens, starts, causal, window, parents).cuda()
+    group = nh // nkv
+    for (s, h), at in bad_v.items():
+        for j, d in at:
+            r = starts[s] + see[starts[s]:starts[s + 1], j].nonzero()[:, 0]
+            out[r[:, None], torch.arange(h * group, h * group + group, device="cuda")[None], d] = math.nan
+    for (s, h), at in bad_k.items():
+        for j in at:
+            r = (starts[s] + see[starts[s]:starts[s + 1], j].nonzero()[:, 0])[:, None]
+            heads = torch.arange(h * group, h * group + group, device="cuda")[None]
+            out[r, heads], lse[r, heads] = math.nan, math.nan
+    assert bool(torch.isnan(out).any()) and not bool(torch.isnan(out).all())
+    got, got_lse = kv.attend(q, table, i32(lens), i32(starts), max(new), causal=causal, window=window, tree=plan,
+                             lse=torch.empty(n, nh, device="cuda"))
+    assert torch.equal(torch.isnan(got), torch.isnan(out)) and torch.equal(torch.isnan(got_lse), torch.isnan(lse))
+    gone, whole = torch.isnan(out), torch.isnan(lse)
+    check_attend(got.masked_fill(gone, 0), got_lse.masked_fill(whole, 0),
+                 (out.masked_fill(gone, 0), lse.masked_fill(whole, 0), spread, dots), slice(0, n), hd)
+    assert status() == 0
