@@ -112,15 +112,16 @@ __global__ void __launch_bounds__(128) keep_kernel(const KeepParams p) {
     for (int i = lane; i < n; i += 32) {
       const int x = path[i];
       if (x < 0 || (i > 0 && path[i - 1] >= x)) bad |= DFLASH_DEV_BAD_TREE;
-      if (ctx < 0 || (int64_t)ctx + x >= cap) bad |= DFLASH_DEV_BAD_CTX;
+      if ((int64_t)ctx + x >= cap) bad |= DFLASH_DEV_BAD_CTX;
     }
-    if (ctx < 0) bad |= DFLASH_DEV_BAD_CTX;
+    if (ctx < 0 || ctx > cap - n) bad |= DFLASH_DEV_BAD_CTX;  // (also where no row moves: the rows below stay within the table's)
   }
   bad = __reduce_or_sync(0xffffffffu, bad);
   if (bad) {
     if (lane == 0 && p.status) atomicOr(p.status, bad & DFLASH_DEV_BAD_TREE ? DFLASH_DEV_BAD_TREE : DFLASH_DEV_BAD_CTX);
     return;
   }
+  if (n == 0) return;
   const int32_t* table = p.page_tables + (int64_t)s * p.mpps;
   const int hd = p.hd, pieces = hd * ES / 16;  // K of a row: pieces of 16 bytes, at most 32
   for (int b1 = ctx & ~7; b1 < ctx + n; b1 += 32) {

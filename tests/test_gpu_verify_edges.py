@@ -98,3 +98,21 @@ def test_nan_in_8_bits_reaches_the_rows_that_see_it(case, dtype):
     check_attend(got.masked_fill(gone, 0), got_lse.masked_fill(whole, 0),
                  (out.masked_fill(gone, 0), lse.masked_fill(whole, 0), spread, dots), slice(0, n), hd)
     assert status() == 0
+
+
+# ------------------------------------------------------------------------------ kept rows
+@pytest.mark.parametrize("kind", ["bf16", "f32", "e4m3"])
+def test_keep_reports_contexts_past_the_table(kind):
+    """Also where no row is kept, up to the largest numbers: the pages stay as they are, and the call ends."""
+    from block_diffusion_drafter_forward_gb300 import PagedKV, QuantKV, _lib
+    status()
+    kv = QuantKV.empty(8, 3, 64) if kind == "e4m3" else PagedKV.empty(8, 3, 64, BF if kind == "bf16" else F32)
+    kv.pool.random_(0, 100)
+    before = kv.pool.clone()
+    table, path = i32([[0, 1, 2]]), i32([[0, 2]])
+    for ctx, n, want in ((48, 0, 0), (47, 0, 0), (0, 0, 0), (46, 1, 0), (49, 0, _lib.DFLASH_DEV_BAD_CTX), (61, 0, _lib.DFLASH_DEV_BAD_CTX),
+                         (1000, 0, _lib.DFLASH_DEV_BAD_CTX), (-1, 0, _lib.DFLASH_DEV_BAD_CTX), (47, 2, _lib.DFLASH_DEV_BAD_CTX),
+                         (48, 1, _lib.DFLASH_DEV_BAD_CTX), (2 ** 31 - 31, 0, _lib.DFLASH_DEV_BAD_CTX), (2 ** 31 - 1, 0, _lib.DFLASH_DEV_BAD_CTX),
+                         (2 ** 31 - 1, 2, _lib.DFLASH_DEV_BAD_CTX), (-2 ** 31, 1, _lib.DFLASH_DEV_BAD_CTX)):
+        kv.keep(table, i32([ctx]), path, i32([n]))
+        assert status() == want and torch.equal(kv.pool, before), (ctx, n)
