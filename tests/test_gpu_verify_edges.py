@@ -116,3 +116,23 @@ def test_keep_reports_contexts_past_the_table(kind):
                          (2 ** 31 - 1, 2, _lib.DFLASH_DEV_BAD_CTX), (-2 ** 31, 1, _lib.DFLASH_DEV_BAD_CTX)):
         kv.keep(table, i32([ctx]), path, i32([n]))
         assert status() == want and torch.equal(kv.pool, before), (ctx, n)
+
+
+# ------------------------------------------------------------------------------ rotary positions
+@pytest.mark.parametrize("inter", [False, True])
+def test_sines_and_cosines_in_32_bits(inter):
+    """Of (1, 0) a rotation leaves (cos, sin) without another rounding: what is left of the angle, at most an eighth of a turn,
+    in fp32 half turns below 1/4 (2^-27, pi of which are 0.4 2^-24), its cut at 2^-32 turns (0.03 2^-24) and the last place that
+    sine and cosine may be off by (2^-24 below 1)."""
+    from block_diffusion_drafter_forward_gb300 import Rope
+    for theta, far in ((1e4, 2 ** 31 - 1), (1e6, 100000), (10.0, 2 ** 31 - 1)):
+        rope = Rope(128, theta, interleaved=inter)
+        pos = torch.randint(-far, far, (3000,), generator=torch.Generator().manual_seed(int(theta)))
+        pos[:9] = torch.tensor([0, 1, -1, 2 ** 31 - 1, -2 ** 31, 2, 3, 4, 5])
+        x = torch.zeros(3000, 1, 128, device="cuda")
+        x[..., 0::2] = 1.0 if inter else 0.0
+        x[..., :64] += 0.0 if inter else 1.0
+        for inverse in (False, True):
+            want, _ = V.rotate(x.double(), pos, rope.turns.tolist(), 1.0, inter, inverse)
+            got = rope.rotate(x, i32(pos.tolist()), inverse=inverse)
+            assert float((got.double() - want).abs().max()) <= 1.43 * 2.0 ** -24
