@@ -271,7 +271,9 @@ def draft_tree(parents: torch.Tensor, kv_lens: torch.Tensor, row_starts: torch.T
 class Rope:
     """Rotary positions with a table of frequencies on `device`: theta^(-2j / rotary_dim), divided by
     `linear`, or remapped by `yarn` = (factor, original length, beta fast, beta slow) as a drafter's
-    configuration does.  Pairs are the halves of the rotated dims, or neighbours (interleaved)."""
+    configuration does.  Pairs are the halves of the rotated dims, or neighbours (interleaved).  `turns`
+    [rotary_dim / 2] int64 holds the frequencies in 2^-64 turns per position; a model with others gives
+    the attribute a tensor of its own, and `mscale` the factor of its rotated values."""
 
     def __init__(self, rotary_dim: int, theta: float = 1e6, linear: float = 1.0,
                  yarn: Optional[Tuple[float, float, float, float]] = None, interleaved: bool = False, device="cuda"):
@@ -282,7 +284,6 @@ class Rope:
             device = torch.device("cuda", torch.cuda.current_device())
         with torch.inference_mode(False):
             self.turns = torch.tensor(turns, dtype=_I64).to(device)  # (below 2^62)
-        self._device, self._a_turns = self.turns.device, self.turns.data_ptr()
         if device.type == "cuda":  # there for every stream
             torch.cuda.current_stream(device).synchronize()
 
@@ -299,10 +300,11 @@ class Rope:
             ok = False
         if not ok:
             _first(q, "q", 3, (_BF16, _F32))
-        if self._device != dev:
-            raise ValueError(f"q: the table is on {self._device}, got a tensor on {dev}")
+        turns = self.turns
+        if isinstance(turns, torch.Tensor) and turns.device != dev:
+            raise ValueError(f"q: the table is on {turns.device}, got a tensor on {dev}")
         a_q, qs = _rows_of(q, "q", dtype, (n, nh, hd), dev)
-        a_pos, = _addresses(dev, (positions, "positions", _I32, (n,)))
+        a_pos, a_turns = _addresses(dev, (positions, "positions", _I32, (n,)), (turns, "turns", _I64, (self.rotary_dim // 2,)))
         a_k = ks = a_ko = kos = nk = 0
         if k is not None:
             if not isinstance(k, torch.Tensor) or k.dim() != 3:
@@ -323,7 +325,7 @@ class Rope:
                 k_out = torch.empty((n, nk, hd), dtype=dtype, device=dev)
             a_ko, kos = _rows_of(k_out, "k_out", dtype, (n, nk, hd), dev)
         rc = L.load().dflash_rotate(a_q, qs, a_o, os_, nh, a_k, ks, a_ko, kos, nk, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32,
-                                    _i32(n, "rows"), hd, self.rotary_dim, self.interleaved, inverse, a_pos, self._a_turns,
+                                    _i32(n, "rows"), hd, self.rotary_dim, self.interleaved, inverse, a_pos, a_turns,
                                     self.mscale, st)
         if rc:
             L._check(rc, None)

@@ -136,3 +136,24 @@ def test_sines_and_cosines_in_32_bits(inter):
             want, _ = V.rotate(x.double(), pos, rope.turns.tolist(), 1.0, inter, inverse)
             got = rope.rotate(x, i32(pos.tolist()), inverse=inverse)
             assert float((got.double() - want).abs().max()) <= 1.43 * 2.0 ** -24
+
+
+def test_rotate_with_a_table_of_the_callers_own():
+    from block_diffusion_drafter_forward_gb300 import Rope
+    rope = Rope(64, 1e4)
+    q, pos = torch.randn(50, 2, 64, device="cuda"), torch.arange(50, dtype=torch.int32, device="cuda") * 1000
+    table = [(j * 0x123456789ABCDEF + 2 ** 40) % 2 ** 62 for j in range(32)]
+    for scale in (1.0, 1.5):
+        table.reverse()
+        rope.turns, rope.mscale = torch.tensor(table, dtype=torch.int64, device="cuda"), scale
+        torch.empty(32, dtype=torch.int64, device="cuda").fill_(0)  # takes the place of the table before, if that is free
+        want, size = V.rotate(q.double(), pos.cpu(), table, scale, False)
+        # sine and cosine to 1.43 2^-24, the scale, two products and their sum to 2^-24 each, the result
+        assert bool(((rope.rotate(q, pos).double() - want).abs() <= 5 * 2.0 ** -24 * size).all())
+    for bad in (rope.turns[:31], rope.turns.int(), torch.zeros(64, dtype=torch.int64, device="cuda")[::2], rope.turns.cpu()):
+        rope.turns = bad
+        with pytest.raises(ValueError):
+            rope.rotate(q, pos)
+    rope.turns = table
+    with pytest.raises(TypeError, match="turns"):
+        rope.rotate(q, pos)
