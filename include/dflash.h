@@ -433,9 +433,11 @@ int64_t dflash_attend_workspace(const dflash_kv_pages* kv);
  *                             the node itself or one of its ancestors
  * Rows outside every sequence get position -1 and empty masks.  1 <= nb <= 16384, n_rows <= 2^30
  * (ECAPACITY), 1 <= max_nodes <= 512 (EUNSUPPORTED).  A parent outside [-1, i) counts as -1 and sets
- * DFLASH_DEV_BAD_TREE; so does a sequence of more than max_nodes nodes, whose rows get position -1 and empty
- * masks.  A sequence whose row_starts fall or leave [0, n_rows], or with kv_lens[s] < n_s, sets
- * DFLASH_DEV_BAD_CTX; the first kind's rows may be left as they are, the other's get -1 and empty masks.
+ * DFLASH_DEV_BAD_TREE; so does a sequence of more nodes than the masks have bits (64 words), whose rows get
+ * position -1 and empty masks.  A sequence whose row_starts fall or leave [0, n_rows], or with
+ * kv_lens[s] < n_s, sets DFLASH_DEV_BAD_CTX; the first kind's rows may be left as they are, the other's get -1
+ * and empty masks.  Where row_starts falls, rows ahead of row_starts[0] or from row_starts[nb] on may be
+ * emptied, whosever they are.
  * Outputs overlap no input. */
 int dflash_draft_tree(const int32_t* parents, const int32_t* kv_lens, const int32_t* row_starts, int32_t nb,
                       int32_t n_rows, int32_t max_nodes, int32_t* positions, uint64_t* masks, uint32_t* status,
