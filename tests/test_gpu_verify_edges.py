@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import verify_ref as V
-from test_gpu_serve import check_attend
+from test_gpu_serve import cache, check_attend
 from test_gpu_verify import cache8, i32, plan_of, status
 
 pytestmark = pytest.mark.gpu
@@ -157,3 +157,30 @@ def test_rotate_with_a_table_of_the_callers_own():
     rope.turns = table
     with pytest.raises(TypeError, match="turns"):
         rope.rotate(q, pos)
+
+
+# ------------------------------------------------------------------------------ chains
+@pytest.mark.parametrize("kind", ["bf16", "f32", "e4m3"])
+def test_a_chain_against_the_causal_form_in_64_bits(kind):
+    """A tree that is one chain, by any hint: within the roundings of a causal chunk, lse included (a key hidden or seen beside
+    the right ones is off by more)."""
+    from block_diffusion_drafter_forward_gb300 import PagedKV, draft_tree
+    status()
+    ctx, new = [333, 20, 1000, 0], [16, 1, 64, 130]
+    if kind == "e4m3":
+        kv, table, lens, starts = cache8(ctx, new, 2, 128, 5)
+        rows = lambda s, m: V.rows8(kv.pool, table[s], m)
+    else:
+        pool, table, lens, starts = cache(ctx, new, 2, 128, BF if kind == "bf16" else F32, 5)
+        kv, rows = PagedKV(pool), V.rows16(pool, table)
+    plan = draft_tree(i32([p for n in new for p in [-1] + list(range(n - 1))]), i32(lens), i32(starts), 300)
+    n = starts[-1]
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for dtype in ((BF, F32) if kind == "e4m3" else (kv.pool.dtype,)):
+        q = torch.randn(n, 16, 128, generator=g, device="cuda").to(dtype)
+        ref = V.attend(q, rows, lens, starts, 1 / math.sqrt(128))
+        for hint in (0, 64, 500):
+            for tree in (plan, None):
+                out, lse = kv.attend(q, table, i32(lens), i32(starts), hint, tree=tree, lse=torch.empty(n, 16, device="cuda"))
+                check_attend(out, lse, ref, slice(0, n), 128)
+    assert status() == 0
