@@ -497,7 +497,7 @@ class QuantKV(PagedKV):
 
     def append(self, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> torch.Tensor:
         """Rows k, v [n, kv_heads, head_dim] (bfloat16 or float32, any stride between rows), quantised, into slots [n]
-        (negative: skipped) of the pages.  Returns the pages' tensor."""
+        (negative: skipped; one named twice holds nothing meaningful) of the pages.  Returns the pages' tensor."""
         dev = self.pool.device
         try:
             n, dtype = slots.shape[0], k.dtype

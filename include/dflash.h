@@ -487,7 +487,9 @@ int dflash_keep_rows(const dflash_kv_pages* kv, const int32_t* page_tables, int3
  * rows that see its key and no others: all of a row from K, the dim that it stands in from V. */
 
 /* dflash_append_kv into pages of DFLASH_FP8E4M3_ROWEXP: rows of src_dtype (DFLASH_BF16 or DFLASH_F32) are
- * quantised as they are written.  Arguments as there; strides in elements of src_dtype. */
+ * quantised as they are written.  Arguments as there; strides in elements of src_dtype.  Two rows aimed at
+ * one slot leave nothing meaningful in it (codes of one may stand under the other's power of two, which is
+ * neither's number); every other slot is as it should be. */
 int dflash_append_kv_quant(const dflash_kv_pages* kv, int32_t src_dtype, const void* k, int64_t k_stride,
                            const void* v, int64_t v_stride, const int32_t* slots, int32_t n, dflash_stream stream);
 

@@ -100,6 +100,25 @@ def test_nan_in_8_bits_reaches_the_rows_that_see_it(case, dtype):
     assert status() == 0
 
 
+def test_a_slot_named_twice_in_8_bits_spoils_no_other():
+    """Singles and runs of eight aimed at one slot: what that slot holds is open, the others' bytes are not."""
+    from block_diffusion_drafter_forward_gb300 import QuantKV
+    status()
+    g = torch.Generator().manual_seed(1)
+    slots = list(range(40)) + [5, 5, 39, -1, 47] + list(range(16, 24))
+    twice = {5, 39} | set(range(16, 24))
+    k, v = torch.randn(2, len(slots), 2, 64, generator=g)
+    kv = QuantKV(torch.zeros(3, 2, 32 * 64 + 32, dtype=torch.uint8, device="cuda"))
+    kv.append(k.cuda(), v.cuda(), i32(slots))
+    got = kv.read(i32(list(range(48))), dtype=F32)
+    for x, y in zip(got, (k, v)):
+        for j in range(48):
+            if j not in twice:
+                want = V.quantise(y[slots.index(j)])[0] if j in slots else torch.zeros(2, 64).double()
+                assert torch.equal(x[j].cpu().double(), want), j
+    assert status() == 0
+
+
 # ------------------------------------------------------------------------------ kept rows
 @pytest.mark.parametrize("kind", ["bf16", "f32", "e4m3"])
 def test_keep_reports_contexts_past_the_table(kind):
