@@ -194,7 +194,7 @@ extern "C" int dflash_attend_ex(const dflash_kv_pages* kv, int32_t q_dtype, cons
   if (!f32) {
     int sms = 0;
     cudaError_t e = sm_count(&sms);
-    if (e == cudaSuccess && quant && p.group <= 16 && (int64_t)max_new * p.group <= 16) e = launch_attend8(p, kv->head_dim, max_new, workspace, sms, st);
+    if (e == cudaSuccess && quant && p.group <= 16 && (int64_t)max_new * p.group <= 16) e = launch_attend8(p, kv->head_dim, workspace, sms, st);
     else if (e == cudaSuccess) e = launch_attend_tc(p, kv->head_dim, max_new, workspace, sms, st);
     return e == cudaSuccess ? DFLASH_OK : call_error(DFLASH_ECUDA, "attend", e);
   }

@@ -41,6 +41,16 @@ __device__ __forceinline__ float* part_row(const AttendWork& w, int slot, int r,
   return w.o + ((int64_t)slot * rows + r) * hd;
 }
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 __device__ __forceinline__ float lse_of(float m, float l) {
   return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
@@ -63,7 +73,7 @@ AttendWork attend_work(void* workspace, int head_dim, int sms, bool long_chunks)
 // Merges the partials of split units (rows of p.tokens tokens, 128 rows a slot).
 cudaError_t launch_attend_combine(const AttendParams& p, const AttendWork& w, int head_dim, int sms, cudaStream_t st);
 // Pages in 8 bits, bf16 queries, at most 16 query heads of a kv head: units of 16 rows.
-cudaError_t launch_attend8(const AttendParams& p, int head_dim, int max_new, void* workspace, int sms, cudaStream_t st);
+cudaError_t launch_attend8(const AttendParams& p, int head_dim, void* workspace, int sms, cudaStream_t st);
 cudaError_t launch_attend_tc(const AttendParams& p, int head_dim, int max_new, void* workspace, int sms, cudaStream_t st);
 
 }  // namespace dflash

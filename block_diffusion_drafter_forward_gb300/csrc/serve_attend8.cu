@@ -82,15 +82,6 @@ __device__ __forceinline__ void mma_bf16w(float (&d)[4], const uint32_t (&a)[4],
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 __device__ __forceinline__ float quad_max(float x) {
   x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
   return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
@@ -453,10 +444,12 @@ cudaError_t launch(const AttendParams& p, const AttendWork& w, int sms, cudaStre
 
 }  // namespace
 
-cudaError_t launch_attend8(const AttendParams& p0, int head_dim, int max_new, void* workspace, int sms, cudaStream_t st) {
+cudaError_t launch_attend8(const AttendParams& p0, int head_dim, void* workspace, int sms, cudaStream_t st) {
   AttendParams p = p0;
   p.tokens = 16 / p.group;
-  const AttendWork w = attend_work(workspace, head_dim, sms, max_new > 4 * p.tokens);
+  // By the hint no sequence has a second tile; by the rows some may (a hint too low is legal), and then a warp looks at each
+  // sequence of the plan instead of a lane.
+  const AttendWork w = attend_work(workspace, head_dim, sms, p.n_rows > (int64_t)4 * p.tokens * p.nb);
   if (p.masks) return head_dim == 128 ? launch<128, true>(p, w, sms, st) : launch<64, true>(p, w, sms, st);
   return head_dim == 128 ? launch<128, false>(p, w, sms, st) : launch<64, false>(p, w, sms, st);
 }

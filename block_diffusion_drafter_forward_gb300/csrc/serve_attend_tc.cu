@@ -118,11 +118,6 @@ struct Ctl {
   float2 ml[2][128];  // one tile: the streams' (m, l) of every row
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // two fp32 in one register pair, and the packed operations on them (sm_100 and on)
 __device__ __forceinline__ uint64_t pair(float a, float b) {
   uint64_t r;
@@ -170,10 +165,6 @@ __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t (&v)[32]) { 
 #undef R8
 }
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 
 // The chunks of stream x, in order, as every role counts them.
 template <int NT, class Walk>
