@@ -203,3 +203,60 @@ def test_a_chain_against_the_causal_form_in_64_bits(kind):
                 out, lse = kv.attend(q, table, i32(lens), i32(starts), hint, tree=tree, lse=torch.empty(n, 16, device="cuda"))
                 check_attend(out, lse, ref, slice(0, n), 128)
     assert status() == 0
+
+
+# ------------------------------------------------------------------------------ the C entries by their names
+def test_entries_by_their_names_are_the_calls():
+    """Each entry called with addresses does what the tensor call of it does, to the last bit."""
+    import block_diffusion_drafter_forward_gb300 as D
+    status()
+    g = torch.Generator(device="cuda").manual_seed(7)
+    nb, nodes, nh, nkv, hd, ctx = 3, 5, 16, 2, 128, (30, 0, 77)
+    parents = i32([-1, 0, 0, 1, -1] * nb)
+    lens, starts, table = i32([c + nodes for c in ctx]), i32([0, 5, 10, 15]), torch.arange(18, dtype=torch.int32, device="cuda").view(3, 6)
+    plan = D.draft_tree(parents, lens, starts, nodes)
+    pos, masks = torch.empty_like(plan.positions), torch.empty_like(plan.masks)
+    D.dflash_draft_tree(parents.data_ptr(), lens.data_ptr(), starts.data_ptr(), nb, 15, nodes, pos.data_ptr(), masks.data_ptr())
+    assert torch.equal(pos, plan.positions) and torch.equal(masks, plan.masks)
+
+    rope = D.Rope(64, 1e4)
+    q, k = torch.randn(15, nh, hd, generator=g, device="cuda").to(BF), torch.randn(15, nkv, hd, generator=g, device="cuda").to(BF)
+    want = rope.rotate(q, pos, k=k, inverse=True)
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    D.dflash_rotate(q.data_ptr(), nh * hd, qo.data_ptr(), nh * hd, nh, k.data_ptr(), nkv * hd, ko.data_ptr(), nkv * hd, nkv, 1, 15, hd, 64, 0, 1,
+                    pos.data_ptr(), rope.turns.data_ptr(), rope.mscale)
+    assert torch.equal(qo, want[0]) and torch.equal(ko, want[1])
+
+    L = int(lens.sum())
+    rows = torch.randn(2, L, nkv, hd, generator=g, device="cuda").to(BF)
+    slots = i32([s * 96 + j for s, n in enumerate(lens.tolist()) for j in range(n)])
+    a, b = D.QuantKV(torch.zeros(18, nkv, 32 * hd + 32, dtype=torch.uint8, device="cuda")), D.QuantKV(torch.zeros(18, nkv, 32 * hd + 32, dtype=torch.uint8, device="cuda"))
+    a.append(*rows, slots)
+    D.dflash_append_kv_quant(b._c, 1, rows[0].data_ptr(), nkv * hd, rows[1].data_ptr(), nkv * hd, slots.data_ptr(), L)
+    assert torch.equal(a.pool, b.pool) and bool(a.pool.any())
+    back = torch.empty(2, L, nkv, hd, device="cuda")
+    D.dflash_read_kv_quant(b._c, 0, slots.data_ptr(), L, back[0].data_ptr(), nkv * hd, back[1].data_ptr(), nkv * hd)
+    for x, y in zip(a.read(slots, dtype=F32), back):
+        assert torch.equal(x, y)
+
+    c = D.PagedKV(torch.zeros(18, nkv, 2, 16 * hd, dtype=BF, device="cuda"))
+    c.append(*rows, slots)
+    for kv in (a, c):
+        need = D.dflash_attend_workspace(kv._c)
+        ws, scale = torch.empty(need, dtype=torch.uint8, device="cuda"), 1 / math.sqrt(hd)
+        for tree in (plan, None):
+            out, lse = torch.zeros(15, nh, hd, dtype=BF, device="cuda"), torch.empty(15, nh, device="cuda")
+            D.dflash_attend_ex(kv._c, 1, q.data_ptr(), nh * hd, table.data_ptr(), 6, lens.data_ptr(), starts.data_ptr(), nb, 15, nodes, nh, scale, 0, 1,
+                               masks.data_ptr() if tree else 0, 1 if tree else 0, pos.data_ptr() if tree else 0, out.data_ptr(), nh * hd,
+                               lse.data_ptr(), ws.data_ptr(), need)
+            y, l = kv.attend(q, table, lens, starts, nodes, tree=tree, lse=torch.empty(15, nh, device="cuda"))
+            assert torch.equal(out, y) and torch.equal(lse, l) and bool(y.any())
+        D.dflash_attend(kv._c, q.data_ptr(), nh * hd, table.data_ptr(), 6, lens.data_ptr(), starts.data_ptr(), nb, 15, nodes, nh, scale, 0, 1,
+                        out.zero_().data_ptr(), nh * hd, lse.data_ptr(), ws.data_ptr(), need)
+        assert torch.equal(out, y) and torch.equal(lse, l)
+        path, n_path, at = i32([[0, 1, 3], [0, 2, 9], [4, 9, 9]]), i32([3, 2, 1]), i32(list(ctx))
+        twin = type(kv)(kv.pool.clone())
+        kv.keep(table, at, path, n_path)
+        D.dflash_keep_rows(twin._c, table.data_ptr(), 6, at.data_ptr(), nb, path.data_ptr(), 3, n_path.data_ptr())
+        assert torch.equal(kv.pool, twin.pool)
+    assert status() == 0
