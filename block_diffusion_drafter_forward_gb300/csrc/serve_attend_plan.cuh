@@ -8,8 +8,10 @@
 // Trees in units of two tiles: a chunk takes a CTA 2.3 us, or 1.55 where the unit's second tile has no token (33 to 48
 // nodes of 8 heads to a K/V head have one such unit of two), so that chunks occupy three slots or two, and belong to
 // the CTA that has their first: 32 trees of 33 nodes 155 -> 137 us, of 48 158 -> 145, of 64 (all two tiles) 161 as
-// before.  (Slots of 5 and 3: 163 for trees of mixed sizes, of 4 and 3 152, of 3 and 2 154.  Without trees a chunk is
-// one slot: a cut elsewhere would round results differently from before.)
+// before.  (Slots of 5 and 3: 163 for trees of mixed sizes; of 4 and 3 1 to 2 us less than of 3 and 2 there, 3 to 4 more
+// for 33 to 40 nodes, whose units gain most.  Over 8-bit pages a chunk with one tile takes nearly as long as one with
+// two, and these slots cost: 32 x 33 nodes 215 us where 32 x 64 take 187.  Without trees a chunk is one slot: a cut
+// elsewhere would round results differently from before.)
 #pragma once
 
 #include <cuda_bf16.h>

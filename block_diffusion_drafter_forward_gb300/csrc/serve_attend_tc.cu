@@ -32,8 +32,8 @@
 // go to the sequence's end.  32 trees of 33-64 nodes on 0.5-8 Ki rows 155 us (34 % of the tensor pipe: part-full
 // tiles, and a unit of 33-48 nodes has one stream at work); one of 32 nodes on 4096 rows 19 us, latency.
 //
-// Pages in 8 bits (kQuant): see below.  32 blocks of 16 as above 90 us, a prompt of 8192 599 us; 86 and 580 without the
-// search for NaN in the widened values, as which the following was measured.  With one tile a chunk
+// Pages in 8 bits (kQuant): see below.  32 blocks of 16 as above 85 us, 4 of 32 on 8 Ki rows 48, 32 of 64 on 4 Ki rows 177,
+// a prompt of 8192 600 us; before the widening looked for NaN 86, 45, 164 and 580, and as such measured: with one tile a chunk
 // takes a CTA 1.87 us; without the widening 1.35, without its stores 1.51, K or V alone 1.6, with one of four
 // softmax warps at work 1.77: the 64 KB that are written to shared memory, beside the 96 KB that the MMAs read of
 // it, and the instruction caches hold it (its loops unrolled: 2.5 us; codes read ahead of the step before: 2.05;
@@ -90,6 +90,7 @@ __device__ __forceinline__ bool wait_ab(uint64_t* bar, uint32_t parity, volatile
 
 template <int HD, int NT, bool kQuant>
 struct Cfg {
+  static constexpr int kTiles = NT;                    // query tiles of a unit
   static constexpr int kTile = kPage * HD * 2;         // a page of one head: bytes of K (or V)
   static constexpr int kQ = 128 * HD * 2;              // a query tile
   static constexpr int kSlot = kPages * kTile;         // a chunk's K (or V)
@@ -306,27 +307,35 @@ __device__ __forceinline__ uint32_t widen_pages(const uint8_t* half, uint8_t* ds
     for (int k = 0; k < (kV ? 4 : 1); ++k) f[k] = __byte_perm(k < 2 ? e0 : e1, 0, k & 1 ? 0x4342 : 0x4140) << 7;  // (an exponent byte to a half)
     uint32_t met = 0;
     auto turn = [&](uint32_t a, int k) { return mul2(mul2(a, 0x7b807b80u), f[k]); };
+    auto put_k = [&](uint8_t* d, uint32_t a, uint32_t b) {
+      const uint2 x = plan::widen(a, met), y = plan::widen(b, met);
+      *reinterpret_cast<uint4*>(d) = make_uint4(turn(x.x, 0), turn(x.y, 0), turn(y.x, 0), turn(y.y, 0));
+    };
+    if constexpr (!kV && C::kTiles == 1) {  // half a step at a time (32 blocks of 16 90 -> 85 us; with two tiles a prompt of 8192 603 -> 614)
 #pragma unroll 1
-    for (int e = 0; e < HD / 64; ++e) {
-      const uint8_t* s = src + e * 1024;
-      uint4 lo = *reinterpret_cast<const uint4*>(s + u0 * 16), hi = *reinterpret_cast<const uint4*>(s + (u0 ^ (kV ? 1 : 2)) * 16);
-      uint8_t* d = dst + e * (kV ? 2048 : 1024);
-      if (kV) {
-        if (d0 | d1) {
-          lo = make_uint4(lo.x & ~d0, lo.y & ~d0, lo.z & ~d0, lo.w & ~d0);
-          hi = make_uint4(hi.x & ~d1, hi.y & ~d1, hi.z & ~d1, hi.w & ~d1);
+      for (int e = 0; e < HD / 32; ++e) {
+        const uint4 w = *reinterpret_cast<const uint4*>(src + (e >> 1) * 1024 + (u0 ^ (e & 1) * 2) * 16);
+        put_k(dst + e * 512, w.x, w.y), put_k(dst + e * 512 + 128, w.z, w.w);
+      }
+    } else {
+#pragma unroll 1
+      for (int e = 0; e < HD / 64; ++e) {
+        const uint8_t* s = src + e * 1024;
+        uint4 lo = *reinterpret_cast<const uint4*>(s + u0 * 16), hi = *reinterpret_cast<const uint4*>(s + (u0 ^ (kV ? 1 : 2)) * 16);
+        uint8_t* d = dst + e * (kV ? 2048 : 1024);
+        if (kV) {
+          if (d0 | d1) {
+            lo = make_uint4(lo.x & ~d0, lo.y & ~d0, lo.z & ~d0, lo.w & ~d0);
+            hi = make_uint4(hi.x & ~d1, hi.y & ~d1, hi.z & ~d1, hi.w & ~d1);
+          }
+          auto put = [&](uint32_t a, uint32_t b, int k) {
+            const uint2 x = plan::widen(a, met), y = plan::widen(b, met);
+            *reinterpret_cast<uint4*>(d + k * 256) = make_uint4(turn(x.x, 0), turn(x.y, 1), turn(y.x, 2), turn(y.y, 3));
+          };
+          put(lo.x, hi.x, 0), put(lo.y, hi.y, 1), put(lo.z, hi.z, 2), put(lo.w, hi.w, 3);
+        } else {
+          put_k(d, lo.x, lo.y), put_k(d + 128, lo.z, lo.w), put_k(d + 512, hi.x, hi.y), put_k(d + 640, hi.z, hi.w);
         }
-        auto put = [&](uint32_t a, uint32_t b, int k) {
-          const uint2 x = plan::widen(a, met), y = plan::widen(b, met);
-          *reinterpret_cast<uint4*>(d + k * 256) = make_uint4(turn(x.x, 0), turn(x.y, 1), turn(y.x, 2), turn(y.y, 3));
-        };
-        put(lo.x, hi.x, 0), put(lo.y, hi.y, 1), put(lo.z, hi.z, 2), put(lo.w, hi.w, 3);
-      } else {
-        auto put = [&](uint32_t a, uint32_t b, int at) {
-          const uint2 x = plan::widen(a, met), y = plan::widen(b, met);
-          *reinterpret_cast<uint4*>(d + at) = make_uint4(turn(x.x, 0), turn(x.y, 0), turn(y.x, 0), turn(y.y, 0));
-        };
-        put(lo.x, lo.y, 0), put(lo.z, lo.w, 128), put(hi.x, hi.y, 512), put(hi.z, hi.w, 640);
       }
     }
     if (kV || pg * kPage + j < rows) nan |= plan::is_nan(met);  // (V behind the end: zeros by now)
@@ -1137,7 +1146,8 @@ cudaError_t launch_attend_tc(const AttendParams& p, int head_dim, int max_new, v
   // 111 / 92 us, x 64 197 / 156 us, 8 x 256 on 2048 117 / 100 us, 64 x 20 on 500 66 / 51 us; with few
   // units the split finer in queries wins: 4 x 32 on 8192 43 / 66 us, 1 x 32 on 30000 55 / 61 us.  The
   // same way round with heads of 64, with 64 on 8 and under a window; 8 on 8 lose 4 of 51 us by it
-  // (8 x 256 on 2048).
+  // (8 x 256 on 2048).  Trees: 32 x 17 on 4096 104 / 81 us, 32 x 64 189 / 150, 8 x 256 on 2048 114 / 97, and
+  // over 8-bit pages 179 / 98, 340 / 187, 207 / 119; 8-bit chunks 32 x 17 165 / 94, 32 x 64 306 / 176.
   const bool two = max_new > T && ((int64_t)p.n_rows + T - 1) / T * p.nkv * 2 >= sms;
   w.long_chunks = max_new > 4 * (two ? 2 * T : T);
   w.spread = p.masks || p.quant;
