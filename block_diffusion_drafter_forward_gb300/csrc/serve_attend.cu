@@ -193,8 +193,8 @@ extern "C" int dflash_attend_ex(const dflash_kv_pages* kv, int32_t q_dtype, cons
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (!f32) {
     // 8 bits: units of 16 rows where a chunk fits one, tiles of 128 above.  Measured (32 sequences on 4352 rows, 8 heads to a
-    // K/V head): 2 tokens 43 us by 16 rows, 87 by tiles; 3 and 4, two units of 16 rows, would still be 72 and 73 for 87;
-    // 8 tokens 130 for 91.  With 16 heads 1 token 64 for 140 (16 Ki rows).
+    // K/V head): 2 tokens 43 us by 16 rows, 83 by tiles; 3 and 4, two units of 16 rows, would still be 72 and 73 for 84;
+    // 8 tokens 130 for 86.  With 16 heads 1 token 64 for 137 (16 on 16 Ki rows), 2, two units, 111 for 138.
     int sms = 0;
     cudaError_t e = sm_count(&sms);
     if (e == cudaSuccess && quant && p.group <= 16 && (int64_t)max_new * p.group <= 16) e = launch_attend8(p, kv->head_dim, workspace, sms, st);

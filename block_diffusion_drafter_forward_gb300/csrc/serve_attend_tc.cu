@@ -1146,8 +1146,8 @@ cudaError_t launch_attend_tc(const AttendParams& p, int head_dim, int max_new, v
   // 111 / 92 us, x 64 197 / 156 us, 8 x 256 on 2048 117 / 100 us, 64 x 20 on 500 66 / 51 us; with few
   // units the split finer in queries wins: 4 x 32 on 8192 43 / 66 us, 1 x 32 on 30000 55 / 61 us.  The
   // same way round with heads of 64, with 64 on 8 and under a window; 8 on 8 lose 4 of 51 us by it
-  // (8 x 256 on 2048).  Trees: 32 x 17 on 4096 104 / 81 us, 32 x 64 189 / 150, 8 x 256 on 2048 114 / 97, and
-  // over 8-bit pages 179 / 98, 340 / 187, 207 / 119; 8-bit chunks 32 x 17 165 / 94, 32 x 64 306 / 176.
+  // (8 x 256 on 2048).  Trees: 32 x 17 on 4096 104 / 81 us, 32 x 64 188 / 150, 8 x 256 on 2048 115 / 97, and
+  // over 8-bit pages 164 / 98, 310 / 187, 193 / 119; 8-bit chunks 32 x 17 151 / 94, 32 x 64 284 / 177, 8 x 256 169 / 105.
   const bool two = max_new > T && ((int64_t)p.n_rows + T - 1) / T * p.nkv * 2 >= sms;
   w.long_chunks = max_new > 4 * (two ? 2 * T : T);
   w.spread = p.masks || p.quant;
