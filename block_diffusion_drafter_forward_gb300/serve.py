@@ -287,6 +287,17 @@ class Rope:
         if device.type == "cuda":  # there for every stream
             torch.cuda.current_stream(device).synchronize()
 
+    @property
+    def turns(self) -> torch.Tensor:
+        return self._turns
+
+    @turns.setter
+    def turns(self, t: torch.Tensor) -> None:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"turns: expected a torch.Tensor, got {type(t).__name__}")
+        _addresses(t.device, (t, "turns", _I64, (self.rotary_dim // 2,)))
+        self._turns, self._device = t, t.device
+
     def rotate(self, q: torch.Tensor, positions: torch.Tensor, k: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                k_out: Optional[torch.Tensor] = None, inverse: bool = False, stream=None):
         """q [rows, heads, head_dim] and k [rows, kv_heads, head_dim] (any stride between rows) at `positions`
@@ -300,11 +311,13 @@ class Rope:
             ok = False
         if not ok:
             _first(q, "q", 3, (_BF16, _F32))
-        turns = self.turns
-        if isinstance(turns, torch.Tensor) and turns.device != dev:
-            raise ValueError(f"q: the table is on {turns.device}, got a tensor on {dev}")
+        turns = self._turns
+        if self._device != dev:
+            raise ValueError(f"q: the table is on {self._device}, got a tensor on {dev}")
+        if turns.shape != (self.rotary_dim // 2,):  # (checked as it was given; changed since)
+            _refuse(turns, "turns", _I64, (self.rotary_dim // 2,), dev)
         a_q, qs = _rows_of(q, "q", dtype, (n, nh, hd), dev)
-        a_pos, a_turns = _addresses(dev, (positions, "positions", _I32, (n,)), (turns, "turns", _I64, (self.rotary_dim // 2,)))
+        a_pos, = _addresses(dev, (positions, "positions", _I32, (n,)))
         a_k = ks = a_ko = kos = nk = 0
         if k is not None:
             if not isinstance(k, torch.Tensor) or k.dim() != 3:
@@ -325,7 +338,7 @@ class Rope:
                 k_out = torch.empty((n, nk, hd), dtype=dtype, device=dev)
             a_ko, kos = _rows_of(k_out, "k_out", dtype, (n, nk, hd), dev)
         rc = L.load().dflash_rotate(a_q, qs, a_o, os_, nh, a_k, ks, a_ko, kos, nk, L.DFLASH_BF16 if dtype is _BF16 else L.DFLASH_F32,
-                                    _i32(n, "rows"), hd, self.rotary_dim, self.interleaved, inverse, a_pos, a_turns,
+                                    _i32(n, "rows"), hd, self.rotary_dim, self.interleaved, inverse, a_pos, turns.data_ptr(),
                                     self.mscale, st)
         if rc:
             L._check(rc, None)

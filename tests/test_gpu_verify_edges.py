@@ -169,12 +169,19 @@ def test_rotate_with_a_table_of_the_callers_own():
         want, size = V.rotate(q.double(), pos.cpu(), table, scale, False)
         # sine and cosine to 1.43 2^-24, the scale, two products and their sum to 2^-24 each, the result
         assert bool(((rope.rotate(q, pos).double() - want).abs() <= 5 * 2.0 ** -24 * size).all())
-    for bad in (rope.turns[:31], rope.turns.int(), torch.zeros(64, dtype=torch.int64, device="cuda")[::2], rope.turns.cpu()):
-        rope.turns = bad
-        with pytest.raises(ValueError):
-            rope.rotate(q, pos)
-    rope.turns = table
+    kept = rope.turns
+    for bad in (kept[:31], kept.int(), torch.zeros(64, dtype=torch.int64, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="turns"):
+            rope.turns = bad
     with pytest.raises(TypeError, match="turns"):
+        rope.turns = table
+    assert rope.turns is kept
+    rope.turns = kept.cpu()
+    with pytest.raises(ValueError, match="the table is on cpu"):
+        rope.rotate(q, pos)
+    rope.turns = kept.clone()
+    rope.turns.resize_(31)
+    with pytest.raises(ValueError, match="turns"):
         rope.rotate(q, pos)
 
 
