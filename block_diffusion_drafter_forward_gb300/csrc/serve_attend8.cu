@@ -447,9 +447,9 @@ cudaError_t launch(const AttendParams& p, const AttendWork& w, int sms, cudaStre
 cudaError_t launch_attend8(const AttendParams& p0, int head_dim, void* workspace, int sms, cudaStream_t st) {
   AttendParams p = p0;
   p.tokens = 16 / p.group;
-  // By the hint no sequence has a second tile; by the rows some may (a hint too low is legal), and then a warp looks at each
-  // sequence of the plan instead of a lane.
-  const AttendWork w = attend_work(workspace, head_dim, sms, p.n_rows > (int64_t)4 * p.tokens * p.nb);
+  // By the hint no sequence has a second tile.  Where by the rows some have many (a hint too low is legal) a warp looks at each
+  // sequence of the plan instead of a lane; single tokens in a batch of as many idle rows lose 2 of 25 us by it.
+  const AttendWork w = attend_work(workspace, head_dim, sms, p.n_rows > (int64_t)32 * p.tokens * p.nb);
   if (p.masks) return head_dim == 128 ? launch<128, true>(p, w, sms, st) : launch<64, true>(p, w, sms, st);
   return head_dim == 128 ? launch<128, false>(p, w, sms, st) : launch<64, false>(p, w, sms, st);
 }

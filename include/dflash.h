@@ -466,8 +466,8 @@ int dflash_attend_ex(const dflash_kv_pages* kv, int32_t q_dtype, const void* q, 
  * of every dtype; with the positions of dflash_draft_tree the keys' rotary positions stay right, since a
  * branch's nodes lie at consecutive depths.  A sequence whose path does not rise, or with path_lens[s]
  * outside [0, max_path], is left as it is (DFLASH_DEV_BAD_TREE); so is one with ctx_lens[s] < 0 or rows past
- * 16 * max_pages_per_seq, with path_lens[s] == 0 too (DFLASH_DEV_BAD_CTX).  A row whose page id (its own or its new place's) is outside
- * [0, num_pages) is not moved (DFLASH_DEV_BAD_PAGE).  Sequences share none of the pages that they write.
+ * 16 * max_pages_per_seq, with path_lens[s] == 0 too (DFLASH_DEV_BAD_CTX).  A row whose page id (its own or
+ * its new place's) is outside [0, num_pages) is not moved (DFLASH_DEV_BAD_PAGE).  Sequences share none of the pages that they write.
  * 1 <= nb <= 16384, 0 <= max_path <= 512. */
 int dflash_keep_rows(const dflash_kv_pages* kv, const int32_t* page_tables, int32_t max_pages_per_seq,
                      const int32_t* ctx_lens, int32_t nb, const int32_t* path, int32_t max_path,

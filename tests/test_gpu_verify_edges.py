@@ -267,3 +267,27 @@ def test_entries_by_their_names_are_the_calls():
         D.dflash_keep_rows(twin._c, table.data_ptr(), 6, at.data_ptr(), nb, path.data_ptr(), 3, n_path.data_ptr())
         assert torch.equal(kv.pool, twin.pool)
     assert status() == 0
+
+
+# ------------------------------------------------------------------------------ hints
+@pytest.mark.parametrize("nb", [1, 40])
+def test_single_token_form_with_chunks_of_many_tiles(nb):
+    """A hint of one token for sequences of which some have hundreds: the units of 16 rows all the same, with a NaN among the
+    keys of one too."""
+    status()
+    new = ([700] if nb == 1 else [600] + [1, 2] * 10 + [900] + [1] * 18)
+    ctx = [(37 * i) % 300 for i in range(len(new))]
+    kv, table, lens, starts = cache8(ctx, new, 2, 64, nb)
+    n = starts[-1]
+    q = torch.randn(n, 16, 64, generator=torch.Generator(device="cuda").manual_seed(nb), device="cuda").to(BF)
+    ref = V.attend(q, lambda s, m: V.rows8(kv.pool, table[s], m), lens, starts, 1 / 8)
+    rows = i32(lens), i32(starts)
+    out, lse = kv.attend(q, table, *rows, 1, lse=torch.empty(n, 16, device="cuda"))
+    check_attend(out, lse, ref, slice(0, n), 64)
+    j, d = lens[0] - 300, 33                                     # rows 400 on of the first sequence see it, by the first K/V head
+    kv.pool[int(table[0, j // PAGE]), 0, 16 * 64 + V.v8(j % PAGE, d)] = 127
+    got, again = kv.attend(q, table, *rows, 1, lse=torch.empty(n, 16, device="cuda"))
+    gone = torch.zeros_like(got, dtype=torch.bool)
+    gone[new[0] - 300:new[0], :8, d] = True
+    assert torch.equal(torch.isnan(got), gone) and torch.equal(got[~gone], out[~gone]) and torch.equal(again, lse)
+    assert status() == 0
