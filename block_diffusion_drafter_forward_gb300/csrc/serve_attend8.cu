@@ -46,7 +46,7 @@ using plan::Shape;
 
 constexpr int kW = 11;  // warps with pages of their own (12 with the producer's: 168 registers a thread)
 struct Geo {
-  static constexpr int kKeys = 16 * kW, kUnitCost = 2, kThreads = 32 * (kW + 1);
+  static constexpr int kKeys = 16 * kW, kUnitCost = 2, kTwo = 1, kOne = 1, kThreads = 32 * (kW + 1);
 };
 template <bool kTree> using Walk = plan::Walk<Geo, kTree>;
 

@@ -3,15 +3,15 @@
 // The chunks of all units, in (sequence, tile, head) order, form one index space; CTA b of a
 // one-CTA-per-SM grid takes slots [b W / n, (b + 1) W / n) of it, sized on the device from the
 // lengths.  G: a form's geometry - keys of a chunk, slots a unit occupies beside its chunks (the cost of
-// opening a segment: queries, pipeline restart, output), threads of a CTA.
+// opening a segment: queries, pipeline restart, output), slots of a chunk with two tiles and with one, threads of a CTA.
 //
 // Trees in units of two tiles: a chunk takes a CTA 2.3 us, or 1.55 where the unit's second tile has no token (33 to 48
 // nodes of 8 heads to a K/V head have one such unit of two), so that chunks occupy three slots or two, and belong to
 // the CTA that has their first: 32 trees of 33 nodes 155 -> 137 us, of 48 158 -> 145, of 64 (all two tiles) 161 as
 // before.  (Slots of 5 and 3: 163 for trees of mixed sizes; of 4 and 3 1 to 2 us less than of 3 and 2 there, 3 to 4 more
 // for 33 to 40 nodes, whose units gain most.  Over 8-bit pages a chunk with one tile takes nearly as long as one with
-// two, and these slots cost: 32 x 33 nodes 215 us where 32 x 64 take 187.  Without trees a chunk is one slot: a cut
-// elsewhere would round results differently from before.)
+// two, and every chunk is one slot: by 3 and 2 32 trees of 33 nodes took 213 us for 191, of 64 186 for 181, of mixed
+// sizes 305 for 296.  So it is without trees, where a cut elsewhere would round results differently from before.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -50,22 +50,21 @@ __device__ __forceinline__ int unit_chunks(const AttendParams& p, const Shape& h
 }
 
 // Slots of a chunk of a unit, and of a unit beside its chunks.
-constexpr int kTwo = 3, kOne = 2;
-template <bool kTree>
+template <class G, bool kTree>
 __device__ __forceinline__ int chunk_slots(const Shape& h, int n, int tile) {
-  return !kTree || h.TT == h.T ? 1 : tile * h.TT + h.T < n ? kTwo : kOne;
+  return !kTree || h.TT == h.T ? 1 : tile * h.TT + h.T < n ? G::kTwo : G::kOne;
 }
 template <class G, bool kTree>
-__device__ __forceinline__ int cost_slots(const Shape& h) { return G::kUnitCost * (!kTree || h.TT == h.T ? 1 : kTwo); }
+__device__ __forceinline__ int cost_slots(const Shape& h) { return G::kUnitCost * (!kTree || h.TT == h.T ? 1 : G::kTwo); }
 template <class G, bool kTree>
 __device__ __forceinline__ int unit_slots(const AttendParams& p, const Shape& h, int n, int kv, int tile) {
   int k0;
-  return unit_chunks<G, kTree>(p, h, n, kv, tile, &k0) * chunk_slots<kTree>(h, n, tile) + cost_slots<G, kTree>(h);
+  return unit_chunks<G, kTree>(p, h, n, kv, tile, &k0) * chunk_slots<G, kTree>(h, n, tile) + cost_slots<G, kTree>(h);
 }
 // CTAs that the W slots are cut for: each has the first slot of a chunk wherever a unit goes on on both its sides.
-template <bool kTree>
+template <class G, bool kTree>
 __device__ __forceinline__ int ctas_of(const Shape& h, long long W) {
-  return (int)min((long long)gridDim.x, !kTree || h.TT == h.T ? W : W / kTwo);
+  return (int)min((long long)gridDim.x, !kTree || h.TT == h.T ? W : W / G::kTwo);
 }
 
 // The segments of index range [lo, hi), from unit (s, tile, g) whose first slot is pu.
@@ -84,7 +83,7 @@ struct Walk {
       }
       q.nch = unit_chunks<G, kTree>(p, h, q.n, q.kv, tile, &q.k0);
       q.s = s, q.tile = tile, q.g = g, q.t0 = tile * h.TT;
-      const int w = chunk_slots<kTree>(h, q.n, tile);
+      const int w = chunk_slots<G, kTree>(h, q.n, tile);
       const long long first = pu + cost_slots<G, kTree>(h);
       pu = first + (long long)q.nch * w;
       if (++g == p.nkv) {
@@ -92,7 +91,7 @@ struct Walk {
         if (++tile * h.TT >= q.n) tile = 0, ++s;
       }
       if (hi <= first || lo >= pu) continue;  // only cost slots of it are in range
-      auto chunks = [&](int slots) { return w == 1 ? slots : w == kOne ? (slots + kOne - 1) / kOne : (slots + kTwo - 1) / kTwo; };
+      auto chunks = [&](int slots) { return w == 1 ? slots : w == G::kOne ? (slots + G::kOne - 1) / G::kOne : (slots + G::kTwo - 1) / G::kTwo; };
       q.c_lo = lo > first ? chunks((int)(lo - first)) : 0;
       q.c_hi = hi < pu ? chunks((int)(hi - first)) : q.nch;
       if (kTree && q.c_lo >= q.c_hi) continue;  // only later slots of a chunk
@@ -136,7 +135,7 @@ __device__ Walk<G, kTree> make(const AttendParams& p, const Shape& h, PlanCtl<G>
       if (lane >= o) inc += x;
     }
     const long long W = __shfl_sync(0xffffffffu, inc, 31);
-    const int ctas = ctas_of<kTree>(h, W), b = blockIdx.x;
+    const int ctas = ctas_of<G, kTree>(h, W), b = blockIdx.x;
     Walk<G, kTree> w;
     w.lo = b < ctas ? (long long)b * W / ctas : 0;
     w.hi = b < ctas ? (long long)(b + 1) * W / ctas : 0;
@@ -200,7 +199,7 @@ __device__ Walk<G, kTree> make(const AttendParams& p, const Shape& h, PlanCtl<G>
   long long mine = 0, W;
   for (int s = s_lo; s < s_hi; ++s) mine += scratch[s];
   long long at = scan(mine, &W);
-  const int ctas = ctas_of<kTree>(h, W), b = blockIdx.x;
+  const int ctas = ctas_of<G, kTree>(h, W), b = blockIdx.x;
   Walk<G, kTree> w;
   w.lo = b < ctas ? (long long)b * W / ctas : 0;
   w.hi = b < ctas ? (long long)(b + 1) * W / ctas : 0;

@@ -71,7 +71,7 @@ constexpr int kKeys = 128;                      // keys per chunk
 constexpr int kPages = kKeys / kPage;           // 8
 template <bool kQuant>
 struct Geo {
-  static constexpr int kKeys = 128, kUnitCost = 3, kThreads = kQuant ? 512 : 384;
+  static constexpr int kKeys = 128, kUnitCost = 3, kTwo = kQuant ? 1 : 3, kOne = kQuant ? 1 : 2, kThreads = kQuant ? 512 : 384;
 };
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(Geo<kQuant>::kThreads, 1) attend_tc_kernel(con
   pdl_trigger();
   // A unit that starts here and goes on in the next CTAs; end: behind the first slot of its last chunk.
   auto goes_on = [&](const Seg& q, long long end) {
-    const int G = plan::ctas_of<kTree>(h, W), last = (int)((end * G + W - 1) / W) - 1;
+    const int G = plan::ctas_of<Geo<kQuant>, kTree>(h, W), last = (int)((end * G + W - 1) / W) - 1;
     wk.meta[blockIdx.x] = make_int4(last - (int)blockIdx.x + 1, q.r0 + q.t0, min(h.TT, q.n - q.t0), q.g);
   };
   // Queries of a segment into tile b (its second query tile's: two tiles, b = 1) by TMA: rows of 64
@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(Geo<kQuant>::kThreads, 1) attend_tc_kernel(con
         while (w.next(p, h, q)) {
           const int n = q.c_hi - q.c_lo;
           // (here, where the walk is at hand: what the softmax warps keep beside their loop costs 3 % of a tree's time)
-          if (kTree && x == 0 && q.c_lo == 0 && q.c_hi < q.nch) goes_on(q, w.pu - plan::chunk_slots<kTree>(h, q.n, q.tile) + 1);
+          if (kTree && x == 0 && q.c_lo == 0 && q.c_hi < q.nch) goes_on(q, w.pu - plan::chunk_slots<Geo<kQuant>, kTree>(h, q.n, q.tile) + 1);
           if (!It<NT, Walk>::active(h, q, x)) {
             // no row of this stream: it still follows every slot, so that its waits stay exact
             for (int j = 0; j < n; ++j, ++kc) {
@@ -1147,7 +1147,7 @@ cudaError_t launch_attend_tc(const AttendParams& p, int head_dim, int max_new, v
   // units the split finer in queries wins: 4 x 32 on 8192 43 / 66 us, 1 x 32 on 30000 55 / 61 us.  The
   // same way round with heads of 64, with 64 on 8 and under a window; 8 on 8 lose 4 of 51 us by it
   // (8 x 256 on 2048).  Trees: 32 x 17 on 4096 104 / 81 us, 32 x 64 188 / 150, 8 x 256 on 2048 115 / 97, and
-  // over 8-bit pages 164 / 98, 310 / 187, 193 / 119; 8-bit chunks 32 x 17 151 / 94, 32 x 64 284 / 177, 8 x 256 169 / 105.
+  // over 8-bit pages 164 / 96, 309 / 182, 193 / 115; 8-bit chunks 32 x 17 151 / 94, 32 x 64 284 / 177, 8 x 256 169 / 105.
   const bool two = max_new > T && ((int64_t)p.n_rows + T - 1) / T * p.nkv * 2 >= sms;
   w.long_chunks = max_new > 4 * (two ? 2 * T : T);
   w.spread = p.masks || p.quant;
