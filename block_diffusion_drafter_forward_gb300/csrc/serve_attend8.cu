@@ -26,7 +26,7 @@
 // Measured (GB300; 16 tokens on 16-32 Ki rows, 64 heads on 8): 152 us, 5.3 TB/s, of which copies alone take 135; a further
 // 128 keys of every CTA take 0.84 us, 88 % of the copy rate, and 13 us are start, split and merge.  K in bf16 as V: 163 us.
 // K in e4m3 products with Q as two e4m3 parts: 204 us.  7 warps: 163 us; two pages a step: 152 us.  One token on 4096 rows
-// 11.9 us: latency.  What bounds it is issue (1.8 instructions a cycle of 4, the ALU pipe at half its rate) beside HBM.
+// 12.2 us: latency.  What bounds it is issue (1.8 instructions a cycle of 4, the ALU pipe at half its rate) beside HBM.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
